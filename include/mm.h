@@ -363,6 +363,131 @@ int mm_moe_backward(const void* x, const void* Wr,
                     void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Around the experts' products   (the pages' block of [L13] §3 step 2 and its
+ * dispatch of steps 4-5, as separate operators with gradients, for a program
+ * that runs the products itself: adapters, a share of the experts, its own
+ * grouped GEMM)
+ *
+ * MM_DTYPE_BF16 and MM_DTYPE_F32; every sum and statistic in fp32, in a fixed
+ * order (deterministic), one rounding per output element.  Any width: rows
+ * whose byte length is a multiple of 16 move in 16-byte vectors.  None of
+ * these calls waits on the device (no watchdog), and none reads or writes the
+ * 256-byte header of a workspace.
+ * ---------------------------------------------------------------------- */
+
+/* Norms before and after a block, its gate and its residual scale, in one
+ * pass over the rows:
+ *   p = f * rho_f * post_w,  rho_f = 1 / sqrt(mean_h f^2 + eps)    (post_w NULL: p = f)
+ *   r = residual_scale * x + gate * p                              (gate NULL: 1)
+ *   n = r * rho_r * pre_w,   rho_r = 1 / sqrt(mean_h r^2 + eps)    (pre_w NULL: no n)
+ * x, f, r, n [T, H]; post_w, pre_w [H]; gate [H], or [T, H] with
+ * gate_per_token != 0; all of dtype.  n is the norm of r as stored (rounded),
+ * which is what the next sub-layer and the backward pass see.  rstd_post /
+ * rstd_pre [T] fp32 (nullable) receive rho_f / rho_r for the backward.
+ * f NULL: a plain norm, r = x is not written (r, post_w, gate NULL,
+ * residual_scale 1, pre_w given).
+ * r may be x and n may be f (the same address: an update in place); no other
+ * output may overlap an input.  T = 0 enqueues nothing.
+ * Limits: 1 <= H <= MM_NORM_MAX_H; eps finite and > 0; residual_scale finite. */
+#define MM_NORM_MAX_H 16384
+
+int mm_block_norm(const void* x, const void* f, const void* post_w, const void* gate,
+                  int gate_per_token, const void* pre_w, float residual_scale, float eps,
+                  int64_t T, int H, int dtype, void* r, void* n, float* rstd_post, float* rstd_pre,
+                  void* stream);
+
+/* Its gradient for dn = dL/dn and dr = dL/dr (the residual path's; NULL: zero),
+ * given r, f and the forward's rstd:
+ *   D  = dr + rho_r pre_w dn - r rho_r^3 mean_h(r pre_w dn)
+ *   dx = residual_scale D;  q = gate D
+ *   df = rho_f post_w q - f rho_f^3 mean_h(f post_w q)             (post_w NULL: q)
+ *   d_post_w = sum_t q f rho_f,  d_pre_w = sum_t dn r rho_r        (fp32 [H])
+ *   d_gate = D p: summed over the tokens (fp32 [H]), or per token (dtype [T, H])
+ * dn, r, rstd_pre, d_pre_w go with pre_w; rstd_post, d_post_w with post_w; f
+ * is needed with post_w or gate; df NULL: the plain norm (f NULL above).
+ * Every gradient is overwritten; no output may overlap an input.  T = 0 zeroes
+ * the sums. */
+size_t mm_block_norm_backward_workspace_bytes(int64_t T, int H, int dtype);
+
+int mm_block_norm_backward(const void* dn, const void* dr, const void* r, const void* f,
+                           const void* post_w, const void* gate, int gate_per_token,
+                           const void* pre_w, const float* rstd_post, const float* rstd_pre,
+                           float residual_scale, int64_t T, int H, int dtype, void* dx, void* df,
+                           float* d_post_w, void* d_gate, float* d_pre_w, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Tokens sorted by expert: the assignments (t, s) in the order expert, token,
+ * slot; each expert's group starts on a multiple of `align` rows.
+ *   offsets [E+1]  first row of each group (offsets[E]: the end of the last)
+ *   counts  [E]    assignments per expert
+ *   pos     [T, k] row of each assignment; -1 where topk_idx is outside
+ *                  [0, E) (dropped: another rank's expert, or over capacity)
+ *   perm    [rows] assignment t*k + s of each row; -1 in padding and behind
+ *   xs      [rows, H]  xs[pos[t,s]] = x[t]; zeros in a group's padding; rows
+ *                  from offsets[E] on are left as they were
+ * rows = mm_moe_permuted_rows(T, E, k, align) (-1: outside the limits), the
+ * most that any routing can need.  An expert may appear twice in a token.
+ * Limits: E <= MM_MAX_EXPERTS, k <= MM_MAX_TOPK (k > E is allowed), align <=
+ * MM_PERMUTE_MAX_ALIGN, T*k <= 2^30.  T = 0 zeroes offsets and counts. */
+#define MM_PERMUTE_MAX_ALIGN 1024
+
+int64_t mm_moe_permuted_rows(int64_t T, int E, int k, int align);
+size_t mm_moe_permute_workspace_bytes(int64_t T, int E, int k);
+
+int mm_moe_permute(const void* x, const int32_t* topk_idx, int64_t T, int H, int E, int k,
+                   int align, int dtype, void* xs, int32_t* offsets, int32_t* counts,
+                   int32_t* perm, int32_t* pos, void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+/* And back: y[t] = sum_s topk_w[t,s] ys[pos[t,s]] (fp32, slot order, rounded
+ * once; topk_w NULL: weights of 1, which is the gradient of the permute).  A
+ * pos outside [0, rows) adds nothing; a token with none gets zeros. */
+int mm_moe_unpermute(const void* ys, const int32_t* pos, const float* topk_w, int64_t T, int H,
+                     int k, int64_t rows, int dtype, void* y, void* stream);
+
+/* Gradient of the weighted combine:
+ *   dys[pos[t,s]] = topk_w[t,s] dy[t],  dw[t,s] = <dy[t], ys[pos[t,s]]>
+ * dys: zeros in a group's padding, rows from offsets[E] on left as they were;
+ * dw (fp32 [T, k], nullable; needs ys and topk_w): 0 for a dropped assignment.
+ * topk_w NULL: dys[pos[t,s]] = dy[t] (the permute of dy by a known order). */
+int mm_moe_unpermute_backward(const void* dy, const void* ys, const int32_t* pos,
+                              const float* topk_w, const int32_t* offsets, const int32_t* counts,
+                              int64_t T, int H, int E, int k, int64_t rows, int dtype, void* dys,
+                              float* dw, void* stream);
+
+/* Activations kept in 8 bits.  A row of C values is cut into groups of 32
+ * columns (the last one may be short); with amax over the group's finite
+ * values, e is the least integer >= -126 with amax <= 448 * 2^e, and
+ *   codes [R, C]            e4m3 of x * 2^-e, round to nearest even
+ *   exps  [R, ceil(C/32)]   e + 127 (one byte; 2^(exps - 127) is the scale)
+ * so that a value of a group is off by at most max(2^-4 |x|, 2^-10 * 2^e).
+ * An infinity or a NaN becomes a NaN code and leaves its group's scale alone.
+ * Unpacking multiplies back: exact in fp32 and, above its subnormals, in bf16,
+ * but for |x| > 1.9375 * 2^127, whose code stands for 2^128: an infinity there.
+ * Limits: C <= MM_CHECKPOINT_MAX_COLS, R*C <= 2^40.  R = 0 enqueues nothing. */
+#define MM_CHECKPOINT_MAX_COLS (1 << 20)
+
+int mm_checkpoint_pack(const void* x, int64_t R, int64_t C, int dtype, void* codes, uint8_t* exps,
+                       void* stream);
+int mm_checkpoint_unpack(const void* codes, const uint8_t* exps, int64_t R, int64_t C, int dtype,
+                         void* x, void* stream);
+
+/* The SwiGLU activation of rows gu [R, 2I] (g in columns [0, I), u in
+ * [I, 2I)): h = SiLU(g) u in dtype, and (codes / exps, both or neither) its
+ * checkpoint: g and u packed as above, each half with its own groups (codes
+ * [R, 2I], exps [R, 2 ceil(I/32)]).  n_rows (device int32, nullable): rows
+ * from *n_rows on are left alone (the offsets[E] of a permute).  2I <=
+ * MM_CHECKPOINT_MAX_COLS. */
+int mm_swiglu_act(const void* gu, int64_t R, int I, int dtype, const int32_t* n_rows, void* h,
+                  void* codes, uint8_t* exps, void* stream);
+
+/* Its backward from the checkpoint's values g, u: with sg = sigmoid(g),
+ *   dgu [R, 2I] = [ dh u sg (1 + g (1 - sg)) | dh g sg ],  h [R, I] = g sg u
+ * (h nullable: the operand of the down weights' gradient). */
+int mm_swiglu_act_backward(const void* codes, const uint8_t* exps, const void* dh, int64_t R, int I,
+                           int dtype, const int32_t* n_rows, void* dgu, void* h, void* stream);
+
+/* ------------------------------------------------------------------------
  * Status
  * ---------------------------------------------------------------------- */
 /* Synchronises `stream`, reads and clears the device status word kept at
@@ -392,7 +517,10 @@ typedef enum {
   MM_KERNEL_BWD_DGRAD = 8,  /* backward: dh = dy Wd and dx = dG Wg + dU Wu GEMMs */
   MM_KERNEL_BWD_SWIGLU = 9, /* backward: gate/up recomputed, SwiGLU derivative */
   MM_KERNEL_BWD_WGRAD = 10, /* backward: weight-gradient GEMMs                */
-  MM_KERNEL_BWD_ROUTER = 11 /* backward: dispatch, router gradient, dx combine */
+  MM_KERNEL_BWD_ROUTER = 11, /* backward: dispatch, router gradient, dx combine */
+  MM_KERNEL_NORM = 12,      /* block norm, forward and backward             */
+  MM_KERNEL_PERMUTE = 13,   /* tokens sorted by expert and back             */
+  MM_KERNEL_CHECKPOINT = 14 /* 8-bit checkpoints and the SwiGLU activation  */
 } mm_kernel_id;
 
 /* Number of kernels this library has enqueued since it was loaded. */

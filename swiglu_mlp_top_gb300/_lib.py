@@ -18,6 +18,10 @@ MM_DTYPE_F32, MM_DTYPE_BF16 = 0, 1
 MM_MAX_EXPERTS = 64
 MM_MAX_TOPK = 8
 MM_NOALLOC_SCRATCH_BYTES = 16 << 20
+MM_NORM_MAX_H = 16384
+MM_PERMUTE_MAX_ALIGN = 1024
+MM_CHECKPOINT_MAX_COLS = 1 << 20
+MM_CHECKPOINT_GROUP = 32
 
 _vp, _i32, _i64, _f32, _sz = C.c_void_p, C.c_int, C.c_int64, C.c_float, C.c_size_t
 _pp = C.POINTER(C.c_void_p)
@@ -70,6 +74,22 @@ SIGNATURES = {
     "mm_moe_backward": (_i32, [_vp, _vp, _pp, _pp, _pp, _i64, _i32, _i32, _i32, _i32, _f32, _i32,
                                _vp, _vp, _vp, _vp, _vp, _f32, _f32, _f32, _vp, _vp, _pp, _pp, _pp,
                                _vp, _vp, _sz, _vp]),
+    "mm_block_norm": (_i32, [_vp, _vp, _vp, _vp, _i32, _vp, _f32, _f32, _i64, _i32, _i32, _vp,
+                             _vp, _vp, _vp, _vp]),
+    "mm_block_norm_backward_workspace_bytes": (_sz, [_i64, _i32, _i32]),
+    "mm_block_norm_backward": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _f32,
+                                      _i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "mm_moe_permuted_rows": (_i64, [_i64, _i32, _i32, _i32]),
+    "mm_moe_permute_workspace_bytes": (_sz, [_i64, _i32, _i32]),
+    "mm_moe_permute": (_i32, [_vp, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
+                              _vp, _vp, _sz, _vp]),
+    "mm_moe_unpermute": (_i32, [_vp, _vp, _vp, _i64, _i32, _i32, _i64, _i32, _vp, _vp]),
+    "mm_moe_unpermute_backward": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32,
+                                         _i64, _i32, _vp, _vp, _vp]),
+    "mm_checkpoint_pack": (_i32, [_vp, _i64, _i64, _i32, _vp, _vp, _vp]),
+    "mm_checkpoint_unpack": (_i32, [_vp, _vp, _i64, _i64, _i32, _vp, _vp]),
+    "mm_swiglu_act": (_i32, [_vp, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp]),
+    "mm_swiglu_act_backward": (_i32, [_vp, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _vp]),
     "mm_check_status": (_i32, [_vp, _vp]),
     "mm_watchdog_selftest": (_i32, [_vp, _sz, C.c_uint32, _vp]),
     "mm_launch_count": (C.c_uint64, []),
@@ -78,6 +98,7 @@ SIGNATURES = {
 }
 MM_KERNEL_ROUTER, MM_KERNEL_DISPATCH, MM_KERNEL_GATEUP, MM_KERNEL_DOWN, MM_KERNEL_DECODE = 1, 3, 4, 5, 7
 MM_KERNEL_BWD_DGRAD, MM_KERNEL_BWD_SWIGLU, MM_KERNEL_BWD_WGRAD, MM_KERNEL_BWD_ROUTER = 8, 9, 10, 11
+MM_KERNEL_NORM, MM_KERNEL_PERMUTE, MM_KERNEL_CHECKPOINT = 12, 13, 14
 
 _lib = None
 

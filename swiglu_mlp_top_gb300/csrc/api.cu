@@ -2,6 +2,7 @@
 // Every entry point only enqueues work on the caller's stream.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -927,13 +928,222 @@ int mm_moe_backward(const void* x, const void* Wr, const void* const* Wg, const 
   return MM_OK;
 }
 
+// ------------------------------------------------ around the experts' products
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// Non-null and 16-byte aligned.
+static bool present16(const void* p) { return p != nullptr && aligned16(p); }
+
+int mm_block_norm(const void* x, const void* f, const void* post_w, const void* gate,
+                  int gate_per_token, const void* pre_w, float residual_scale, float eps, int64_t T,
+                  int H, int dtype, void* r, void* n, float* rstd_post, float* rstd_pre,
+                  void* stream) {
+  if (!valid_dtype(dtype) || T < 0 || H < 1) return MM_ERR_INVALID_ARG;
+  if (H > MM_NORM_MAX_H) return MM_ERR_UNSUPPORTED;
+  if (!(eps > 0.f) || !std::isfinite(eps) || !std::isfinite(residual_scale)) return MM_ERR_INVALID_ARG;
+  if (T == 0) return MM_OK;
+  if (!present16(x)) return MM_ERR_INVALID_ARG;
+  if (f != nullptr ? !present16(r) : (r || post_w || gate || residual_scale != 1.f || !pre_w))
+    return MM_ERR_INVALID_ARG;
+  if ((pre_w != nullptr) != (n != nullptr)) return MM_ERR_INVALID_ARG;
+  if ((rstd_post && !post_w) || (rstd_pre && !pre_w)) return MM_ERR_INVALID_ARG;
+  for (const void* q : {f, post_w, gate, pre_w, static_cast<const void*>(n)})
+    if (!aligned16(q)) return MM_ERR_INVALID_ARG;
+  if (!aligned4(rstd_post) || !aligned4(rstd_pre)) return MM_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const BlockNormFwd a{x, f, post_w, gate, pre_w, r, n, rstd_post, rstd_pre, T, H,
+                       gate_per_token != 0, residual_scale, eps};
+  cudaError_t e = counted_launch(MM_KERNEL_NORM, st, [&] { return launch_block_norm(dtype, a, st); });
+  return e == cudaSuccess ? MM_OK : cuda_fail(e, "block norm");
+}
+
+size_t mm_block_norm_backward_workspace_bytes(int64_t T, int H, int dtype) {
+  if (!valid_dtype(dtype) || T < 0 || H < 1 || H > MM_NORM_MAX_H) return 0;
+  return sizeof(WsHeader) + align_up(block_norm_bwd_bytes(T, H, dtype));
+}
+
+int mm_block_norm_backward(const void* dn, const void* dr, const void* r, const void* f,
+                           const void* post_w, const void* gate, int gate_per_token,
+                           const void* pre_w, const float* rstd_post, const float* rstd_pre,
+                           float residual_scale, int64_t T, int H, int dtype, void* dx, void* df,
+                           float* d_post_w, void* d_gate, float* d_pre_w, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  if (!valid_dtype(dtype) || T < 0 || H < 1) return MM_ERR_INVALID_ARG;
+  if (H > MM_NORM_MAX_H) return MM_ERR_UNSUPPORTED;
+  if (!std::isfinite(residual_scale)) return MM_ERR_INVALID_ARG;
+  // what each part needs, and nothing that has no use
+  if ((post_w != nullptr) != (d_post_w != nullptr) || (pre_w != nullptr) != (d_pre_w != nullptr))
+    return MM_ERR_INVALID_ARG;
+  const bool token_gate = gate != nullptr && gate_per_token != 0;
+  if (gate == nullptr && d_gate != nullptr) return MM_ERR_INVALID_ARG;
+  if (T > 0) {
+    if (!present16(dx) || (gate != nullptr && d_gate == nullptr)) return MM_ERR_INVALID_ARG;
+    if (df == nullptr && (post_w || gate || residual_scale != 1.f)) return MM_ERR_INVALID_ARG;
+    if ((post_w || gate) && !f) return MM_ERR_INVALID_ARG;
+    if (pre_w ? (!dn || !r || !rstd_pre) : (dn != nullptr || !dr)) return MM_ERR_INVALID_ARG;
+    if (post_w && !rstd_post) return MM_ERR_INVALID_ARG;
+  } else if (gate != nullptr && !token_gate && d_gate == nullptr) {
+    return MM_ERR_INVALID_ARG;
+  }
+  for (const void* q : {dn, dr, r, f, post_w, gate, pre_w, static_cast<const void*>(df),
+                        static_cast<const void*>(d_gate), static_cast<const void*>(d_post_w),
+                        static_cast<const void*>(d_pre_w)})
+    if (!aligned16(q)) return MM_ERR_INVALID_ARG;
+  if (!aligned4(rstd_post) || !aligned4(rstd_pre)) return MM_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < mm_block_norm_backward_workspace_bytes(T, H, dtype))
+    return MM_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  BlockNormBwd a{dn, dr, r, f, post_w, gate, pre_w, rstd_post, rstd_pre, dx, df, d_post_w, d_gate,
+                 d_pre_w, f32_at(workspace, sizeof(WsHeader)), T, H, token_gate, residual_scale};
+  cudaError_t e = cudaSuccess;
+  if (T > 0) {
+    e = counted_launch(MM_KERNEL_NORM, st, [&] { return launch_block_norm_bwd_rows(dtype, a, st); });
+    if (e != cudaSuccess) return cuda_fail(e, "block norm backward");
+  }
+  if (pre_w || post_w || (gate && !token_gate)) {
+    e = counted_launch(MM_KERNEL_NORM, st, [&] { return launch_block_norm_bwd_cols(dtype, a, st); });
+    if (e != cudaSuccess) return cuda_fail(e, "block norm backward sums");
+  }
+  return MM_OK;
+}
+
+int64_t mm_moe_permuted_rows(int64_t T, int E, int k, int align) {
+  if (T < 0 || E < 1 || E > MM_MAX_EXPERTS || k < 1 || k > MM_MAX_TOPK || align < 1 ||
+      align > MM_PERMUTE_MAX_ALIGN || T > (int64_t{1} << 30) / k)
+    return -1;
+  return T * k + std::min<int64_t>(E, T * k) * (align - 1);
+}
+
+size_t mm_moe_permute_workspace_bytes(int64_t T, int E, int k) {
+  if (mm_moe_permuted_rows(T, E, k, 1) < 0) return 0;
+  return sizeof(WsHeader) + align_up(permute_bytes(T, E, k));
+}
+
+int mm_moe_permute(const void* x, const int32_t* topk_idx, int64_t T, int H, int E, int k,
+                   int align, int dtype, void* xs, int32_t* offsets, int32_t* counts,
+                   int32_t* perm, int32_t* pos, void* workspace, size_t workspace_bytes,
+                   void* stream) {
+  if (!valid_dtype(dtype) || T < 0 || H < 1 || E < 1 || k < 1 || align < 1) return MM_ERR_INVALID_ARG;
+  const int64_t rows = mm_moe_permuted_rows(T, E, k, align);
+  if (rows < 0) return MM_ERR_UNSUPPORTED;
+  if (!offsets || !counts || !aligned4(offsets) || !aligned4(counts)) return MM_ERR_INVALID_ARG;
+  if (T > 0 && (!present16(x) || !present16(xs) || !topk_idx || !perm || !pos ||
+                !aligned4(topk_idx) || !aligned4(perm) || !aligned4(pos)))
+    return MM_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < mm_moe_permute_workspace_bytes(T, E, k))
+    return MM_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const PermuteArgs a{x, topk_idx, xs, offsets, counts, perm, pos, ws_at(workspace, sizeof(WsHeader)),
+                      T, rows, H, E, k, align};
+  cudaError_t e = counted_launch(MM_KERNEL_PERMUTE, st, [&] { return launch_permute_sort(a, st); });
+  if (e != cudaSuccess) return cuda_fail(e, "permute sort");
+  if (T == 0) return MM_OK;
+  e = counted_launch(MM_KERNEL_PERMUTE, st, [&] { return launch_permute_copy(dtype, a, st); });
+  return e == cudaSuccess ? MM_OK : cuda_fail(e, "permute copy");
+}
+
+int mm_moe_unpermute(const void* ys, const int32_t* pos, const float* topk_w, int64_t T, int H,
+                     int k, int64_t rows, int dtype, void* y, void* stream) {
+  if (!valid_dtype(dtype) || T < 0 || H < 1 || k < 1 || rows < 0) return MM_ERR_INVALID_ARG;
+  if (k > MM_MAX_TOPK || T > (int64_t{1} << 30) / k) return MM_ERR_UNSUPPORTED;
+  if (T == 0) return MM_OK;
+  if (!present16(y) || !pos || !aligned4(pos) || !aligned4(topk_w) || !aligned16(ys) ||
+      (rows > 0 && !ys))
+    return MM_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const UnpermuteArgs a{ys, pos, topk_w, y, T, rows, H, k};
+  cudaError_t e = counted_launch(MM_KERNEL_PERMUTE, st, [&] { return launch_unpermute(dtype, a, st); });
+  return e == cudaSuccess ? MM_OK : cuda_fail(e, "unpermute");
+}
+
+int mm_moe_unpermute_backward(const void* dy, const void* ys, const int32_t* pos,
+                              const float* topk_w, const int32_t* offsets, const int32_t* counts,
+                              int64_t T, int H, int E, int k, int64_t rows, int dtype, void* dys,
+                              float* dw, void* stream) {
+  if (!valid_dtype(dtype) || T < 0 || H < 1 || E < 1 || k < 1 || rows < 0) return MM_ERR_INVALID_ARG;
+  if (E > MM_MAX_EXPERTS || k > MM_MAX_TOPK || T > (int64_t{1} << 30) / k) return MM_ERR_UNSUPPORTED;
+  if (T == 0) return MM_OK;
+  if (!present16(dy) || !pos || !offsets || !counts || !aligned4(pos) || !aligned4(topk_w) ||
+      !aligned4(offsets) || !aligned4(counts) || !aligned4(dw) || !aligned16(ys) || !aligned16(dys))
+    return MM_ERR_INVALID_ARG;
+  if (rows > 0 && (!dys || (dw && !ys))) return MM_ERR_INVALID_ARG;
+  if (dw != nullptr && topk_w == nullptr) return MM_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const UnpermuteBwdArgs a{dy, ys, pos, topk_w, offsets, counts, dys, dw, T, rows, H, E, k};
+  cudaError_t e =
+      counted_launch(MM_KERNEL_PERMUTE, st, [&] { return launch_unpermute_bwd(dtype, a, st); });
+  return e == cudaSuccess ? MM_OK : cuda_fail(e, "unpermute backward");
+}
+
+// Rows and columns of an 8-bit checkpoint: any extents whose groups can be counted.
+static bool checkpoint_extent_ok(int64_t R, int64_t C) {
+  return C <= MM_CHECKPOINT_MAX_COLS && R <= (int64_t{1} << 40) / C;
+}
+
+static int checkpoint_impl(bool pack, const void* x, void* x_out, void* codes, uint8_t* exps,
+                           int64_t R, int64_t C, int dtype, void* stream) {
+  if (!valid_dtype(dtype) || R < 0 || C < 1) return MM_ERR_INVALID_ARG;
+  if (!checkpoint_extent_ok(R, C)) return MM_ERR_UNSUPPORTED;
+  if (R == 0) return MM_OK;
+  if (!present16(pack ? x : x_out) || !present16(codes) || !present16(exps)) return MM_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const CheckpointArgs a{x, x_out, static_cast<uint8_t*>(codes), exps, R, C};
+  cudaError_t e =
+      counted_launch(MM_KERNEL_CHECKPOINT, st, [&] { return launch_checkpoint(dtype, pack, a, st); });
+  return e == cudaSuccess ? MM_OK : cuda_fail(e, pack ? "checkpoint pack" : "checkpoint unpack");
+}
+
+int mm_checkpoint_pack(const void* x, int64_t R, int64_t C, int dtype, void* codes, uint8_t* exps,
+                       void* stream) {
+  return checkpoint_impl(true, x, nullptr, codes, exps, R, C, dtype, stream);
+}
+
+int mm_checkpoint_unpack(const void* codes, const uint8_t* exps, int64_t R, int64_t C, int dtype,
+                         void* x, void* stream) {
+  return checkpoint_impl(false, nullptr, x, const_cast<void*>(codes), const_cast<uint8_t*>(exps), R,
+                         C, dtype, stream);
+}
+
+int mm_swiglu_act(const void* gu, int64_t R, int I, int dtype, const int32_t* n_rows, void* h,
+                  void* codes, uint8_t* exps, void* stream) {
+  if (!valid_dtype(dtype) || R < 0 || I < 1) return MM_ERR_INVALID_ARG;
+  if (!checkpoint_extent_ok(R, 2 * static_cast<int64_t>(I))) return MM_ERR_UNSUPPORTED;
+  if (R == 0) return MM_OK;
+  if (!present16(gu) || !present16(h) || !aligned4(n_rows) || (codes != nullptr) != (exps != nullptr) ||
+      !aligned16(codes) || !aligned16(exps))
+    return MM_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const SwigluActArgs a{gu, nullptr, h, nullptr, static_cast<uint8_t*>(codes), exps, n_rows, R, I};
+  cudaError_t e =
+      counted_launch(MM_KERNEL_CHECKPOINT, st, [&] { return launch_swiglu_act(dtype, false, a, st); });
+  return e == cudaSuccess ? MM_OK : cuda_fail(e, "swiglu act");
+}
+
+int mm_swiglu_act_backward(const void* codes, const uint8_t* exps, const void* dh, int64_t R, int I,
+                           int dtype, const int32_t* n_rows, void* dgu, void* h, void* stream) {
+  if (!valid_dtype(dtype) || R < 0 || I < 1) return MM_ERR_INVALID_ARG;
+  if (!checkpoint_extent_ok(R, 2 * static_cast<int64_t>(I))) return MM_ERR_UNSUPPORTED;
+  if (R == 0) return MM_OK;
+  if (!present16(codes) || !present16(exps) || !present16(dh) || !present16(dgu) || !aligned16(h) ||
+      !aligned4(n_rows))
+    return MM_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const SwigluActArgs a{nullptr, dh, h, dgu, static_cast<uint8_t*>(const_cast<void*>(codes)),
+                        const_cast<uint8_t*>(exps), n_rows, R, I};
+  cudaError_t e =
+      counted_launch(MM_KERNEL_CHECKPOINT, st, [&] { return launch_swiglu_act(dtype, true, a, st); });
+  return e == cudaSuccess ? MM_OK : cuda_fail(e, "swiglu act backward");
+}
+
 uint64_t mm_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }
 
 int mm_profile_start(int kernel_id, int max_launches) {
   switch (kernel_id) {
     case MM_KERNEL_ROUTER: case MM_KERNEL_DISPATCH: case MM_KERNEL_GATEUP: case MM_KERNEL_DOWN:
     case MM_KERNEL_DECODE: case MM_KERNEL_BWD_DGRAD: case MM_KERNEL_BWD_SWIGLU:
-    case MM_KERNEL_BWD_WGRAD: case MM_KERNEL_BWD_ROUTER: break;
+    case MM_KERNEL_BWD_WGRAD: case MM_KERNEL_BWD_ROUTER: case MM_KERNEL_NORM:
+    case MM_KERNEL_PERMUTE: case MM_KERNEL_CHECKPOINT: break;
     default: return MM_ERR_INVALID_ARG;
   }
   if (max_launches < 1 || max_launches > 100000) return MM_ERR_INVALID_ARG;

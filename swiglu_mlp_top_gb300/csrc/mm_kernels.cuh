@@ -362,6 +362,111 @@ cudaError_t launch_router_bwd(const void* x, const void* Wr, int64_t T, int H, i
 cudaError_t launch_router_bwd_reduce(const float* dwr_part, const float* dbias_part, int nblk,
                                      int E, int H, float* dWr, float* d_bias, cudaStream_t st);
 
+// ------------------------------------------------ around the experts' products
+// Norms before and after a block with its gate and residual scale
+// (block_norm.cu); the pointers as mm_block_norm's.
+struct BlockNormFwd {
+  const void* x;
+  const void* f;              // the block's output, or null: r = x, nothing but n is written
+  const void* post_w;         // [H] or null
+  const void* gate;           // [H], or [T, H] with gate_per_token, or null
+  const void* pre_w;          // [H] or null
+  void* r;
+  void* n;
+  float* rstd_post;           // [T] or null
+  float* rstd_pre;            // [T] or null
+  int64_t T;
+  int H;
+  int gate_per_token;
+  float residual_scale, eps;
+};
+struct BlockNormBwd {
+  const void* dn;             // null without pre_w
+  const void* dr;             // null: zero
+  const void* r;
+  const void* f;
+  const void* post_w;
+  const void* gate;
+  const void* pre_w;
+  const float* rstd_post;
+  const float* rstd_pre;
+  void* dx;
+  void* df;                   // null: no branch
+  float* d_post_w;
+  void* d_gate;               // fp32 [H], or x's dtype [T, H] with gate_per_token
+  float* d_pre_w;
+  float* partial;             // workspace, block_norm_bwd_bytes()
+  int64_t T;
+  int H;
+  int gate_per_token;
+  float residual_scale;
+};
+size_t block_norm_bwd_bytes(int64_t T, int H, int dtype);
+cudaError_t launch_block_norm(int dtype, const BlockNormFwd& a, cudaStream_t st);
+cudaError_t launch_block_norm_bwd_rows(int dtype, const BlockNormBwd& a, cudaStream_t st);
+cudaError_t launch_block_norm_bwd_cols(int dtype, const BlockNormBwd& a, cudaStream_t st);
+
+// Tokens sorted by expert and back (permute.cu).
+struct PermuteArgs {
+  const void* x;
+  const int32_t* topk_idx;    // [T*k]; outside [0, E): dropped
+  void* xs;                   // [rows, H]
+  int32_t* offsets;           // [E + 1]
+  int32_t* counts;            // [E]
+  int32_t* perm;              // [rows] row -> assignment, -1
+  int32_t* pos;               // [T*k] assignment -> row, -1
+  void* scratch;              // permute_bytes()
+  int64_t T, rows;
+  int H, E, k, align;
+};
+struct UnpermuteArgs {
+  const void* ys;             // [rows, H]
+  const int32_t* pos;
+  const float* w;             // [T*k] or null (1)
+  void* y;
+  int64_t T, rows;
+  int H, k;
+};
+struct UnpermuteBwdArgs {
+  const void* dy;
+  const void* ys;             // null without dw
+  const int32_t* pos;
+  const float* w;             // null: 1
+  const int32_t* offsets;
+  const int32_t* counts;
+  void* dys;
+  float* dw;                  // [T*k] or null
+  int64_t T, rows;
+  int H, E, k;
+};
+size_t permute_bytes(int64_t T, int E, int k);
+cudaError_t launch_permute_sort(const PermuteArgs& a, cudaStream_t st);
+cudaError_t launch_permute_copy(int dtype, const PermuteArgs& a, cudaStream_t st);
+cudaError_t launch_unpermute(int dtype, const UnpermuteArgs& a, cudaStream_t st);
+cudaError_t launch_unpermute_bwd(int dtype, const UnpermuteBwdArgs& a, cudaStream_t st);
+
+// Activations in 8 bits (checkpoint.cu).
+struct CheckpointArgs {
+  const void* x;              // pack: [R, C]
+  void* x_out;                // unpack: [R, C]
+  uint8_t* codes;             // [R, C]
+  uint8_t* exps;              // [R, ceil(C / 32)]
+  int64_t R, C;
+};
+struct SwigluActArgs {
+  const void* gu;             // forward: [R, 2I]
+  const void* dh;             // backward: [R, I]
+  void* h;                    // [R, I]; backward: null or as the forward's
+  void* dgu;                  // backward: [R, 2I]
+  uint8_t* codes;             // [R, 2I], or null (forward only)
+  uint8_t* exps;              // [R, 2 ceil(I / 32)]
+  const int32_t* n_rows;      // device: rows from here on are left alone; null: R
+  int64_t R;
+  int I;
+};
+cudaError_t launch_checkpoint(int dtype, bool pack, const CheckpointArgs& a, cudaStream_t st);
+cudaError_t launch_swiglu_act(int dtype, bool backward, const SwigluActArgs& a, cudaStream_t st);
+
 // Workspace of the path that `path` (AUTO: the automatic choice) resolves to
 // for a dense call of this shape; 0 when that path does not take it.
 size_t dense_workspace_for_path(int64_t T, int H, int I, int dtype, int path);

@@ -1,0 +1,195 @@
+"""Tokens sorted by expert and back against the 64-bit forms of
+block_reference: indices and copied rows exactly; a combine of k weighted rows
+is k products and k - 1 sums (2 k roundings on the terms' magnitudes), a dot
+product of H terms H + 1."""
+import pytest
+import torch
+
+import block_reference as ref
+import swiglu_mlp_top_gb300 as mm
+from block_reference import U, U32, close
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def route(T, E, k, how="skewed", seed=0):
+    gen = torch.Generator().manual_seed(100 * T + 10 * E + k + seed)
+    if how == "one":                                   # every token to one expert, and the same slot twice
+        idx = torch.full((T, k), E - 1)
+    elif how == "dropped":
+        idx = torch.randint(-1, E + 1, (T, k), generator=gen)      # -1 and E: outside
+    elif how == "nothing":
+        idx = torch.full((T, k), -1)
+    else:
+        logits = torch.randn(T, E, generator=gen)
+        logits[:, 0] += 1.5
+        idx = torch.stack([torch.multinomial(torch.softmax(row, 0), k, replacement=k > E, generator=gen) for row in logits]) \
+            if T else torch.zeros(0, k)
+    return idx.to(torch.int32), torch.rand(T, k, generator=gen) + 0.05, gen
+
+
+def check(T, H, E, k, align, dtype, how="skewed"):
+    idx, w, gen = route(T, E, k, how)
+    x = torch.randn(T, H, generator=gen).to(dtype)
+    R = mm.moe_permuted_rows(T, E, k, align)
+    mark = torch.full((R, H), 7.0, dtype=dtype, device="cuda")
+    xs, plan = mm.moe_permute(x.cuda(), idx.cuda(), E, align=align, out=mark)
+    want = ref.sort_plan(idx, E, align, R)
+    for key in want:
+        assert torch.equal(plan[key].cpu(), want[key]), key
+    end = int(want["offsets"][-1])
+    rows = torch.full((R, H), 7.0, dtype=dtype)
+    rows[:end] = 0
+    at = want["perm"][:end] >= 0
+    rows[:end][at] = x[(want["perm"][:end][at] // k).long()]
+    assert torch.equal(xs.cpu(), rows)
+
+    # and back
+    u, pos = U[dtype], want["pos"]
+    ys = torch.randn(R, H, generator=gen).to(dtype)
+    y = mm.moe_unpermute(ys.cuda(), plan, w.cuda())
+    terms = ref.gathered(ys, pos) * w.double()[..., None]
+    total = terms.sum(1)
+    close(y, total, u * total.abs() + (u + 1) * 2 * k * U32 * terms.abs().sum(1), "y")
+    dx = mm.moe_permute_backward(ys.cuda(), plan)
+    terms = ref.gathered(ys, pos)
+    total = terms.sum(1)
+    close(dx, total, u * total.abs() + (u + 1) * k * U32 * terms.abs().sum(1), "dx")
+
+    # gradient of the combine
+    dy = torch.randn(T, H, generator=gen).to(dtype)
+    mark = torch.full((R, H), 7.0, dtype=dtype, device="cuda")
+    dys, dw = mm.moe_unpermute_backward(dy.cuda(), ys.cuda(), plan, w.cuda(), out=mark)
+    rows = torch.full((R, H), 7.0, dtype=torch.float64)
+    rows[:end] = 0
+    a = want["perm"][:end][at].long()
+    rows[:end][at] = dy.double()[a // k] * w.double().reshape(-1)[a][:, None]
+    bound = (u + (u + 1) * U32) * rows.abs()
+    bound[end:] = 0
+    close(dys, rows, bound, "dys")
+    terms = ref.gathered(ys, pos) * dy.double()[:, None, :]
+    close(dw, terms.sum(2), (H + 1) * U32 * terms.abs().sum(2), "dw")
+    again, none = mm.moe_unpermute_backward(dy.cuda(), None, plan, None, out=torch.full_like(mark, 7.0))
+    want_rows = torch.full((R, H), 7.0, dtype=dtype)
+    want_rows[:end] = 0
+    want_rows[:end][at] = dy[a // k]
+    assert none is None and torch.equal(again.cpu(), want_rows)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,H,E,k,align", [
+    (1, 768, 8, 2, 1), (1, 8, 1, 1, 1), (2, 1, 2, 2, 3), (16, 768, 8, 2, 64), (33, 72, 4, 1, 16), (100, 7, 8, 8, 1),
+    (65, 1001, 64, 6, 5), (257, 256, 64, 8, 128), (1000, 96, 3, 2, 1), (2049, 40, 8, 2, 64), (700, 2432, 5, 3, 7),
+    (40, 10, 2, 5, 4), (5000, 64, 16, 4, 1), (20001, 8, 64, 2, 1024)])
+def test_sort_and_back(T, H, E, k, align, dtype):
+    check(T, H, E, k, align, dtype)
+
+
+@pytest.mark.parametrize("how", ["one", "dropped", "nothing"])
+@pytest.mark.parametrize("T,H,E,k,align", [(1, 64, 4, 2, 1), (50, 768, 8, 2, 64), (3000, 24, 8, 3, 16), (333, 9, 64, 8, 1)])
+def test_uneven_routing(T, H, E, k, align, how):
+    check(T, H, E, k, align, BF, how)
+
+
+def test_no_tokens():
+    x, idx = torch.empty(0, 64, dtype=BF, device="cuda"), torch.empty(0, 2, dtype=torch.int32, device="cuda")
+    xs, plan = mm.moe_permute(x, idx, 4, align=16)
+    assert xs.shape == (0, 64) and not plan["offsets"].any() and not plan["counts"].any()
+    y = mm.moe_unpermute(xs, plan, torch.empty(0, 2, device="cuda"))
+    dys, dw = mm.moe_unpermute_backward(y, xs, plan, torch.empty(0, 2, device="cuda"))
+    assert y.shape == (0, 64) and dys.shape == (0, 64) and dw.shape == (0, 2)
+
+
+def test_rows_outside_the_tensor_are_left_out():
+    """A pos that no plan holds adds nothing instead of being read."""
+    ys = torch.ones(4, 64, dtype=BF, device="cuda")
+    plan = {"pos": torch.tensor([[0, 4], [-7, 2 ** 30], [3, 3]], dtype=torch.int32, device="cuda")}
+    y = mm.moe_unpermute(ys, plan, torch.ones(3, 2, device="cuda"))
+    assert y[:, 0].tolist() == [1.0, 0.0, 2.0]
+
+
+@pytest.mark.parametrize("E,k", [(8, 2), (4, 1), (64, 8)])
+def test_route_then_sort(E, k):
+    """moe_route's indices, sorted: its expert counts are the groups' sizes."""
+    gen = torch.Generator(device="cuda").manual_seed(E)
+    x = torch.randn(600, 256, generator=gen, device="cuda").to(BF)
+    Wr = (0.02 * torch.randn(E, 256, generator=gen, device="cuda")).to(BF)
+    idx, w, aux, counts = mm.moe_route(x, Wr, k, 0.01)
+    xs, plan = mm.moe_permute(x, idx, E)
+    assert torch.equal(plan["counts"], counts) and int(plan["offsets"][-1]) == 600 * k
+    y = mm.moe_unpermute(xs, plan, w)                  # the weights of a token add up to one
+    close(y, x.double().cpu(), (2 ** -8 + 2 ** -20) * x.double().cpu().abs(), "identity")
+
+
+def test_gradient_against_differences():
+    """y is linear in ys and in w: the difference quotient of the fp32 combine
+    is exact but for 2 k roundings on the terms, over the step."""
+    idx, w, gen = route(50, 8, 2)
+    xs, plan = mm.moe_permute(torch.randn(50, 96, generator=gen).cuda(), idx.cuda(), 8, align=4,
+                              out=torch.zeros(mm.moe_permuted_rows(50, 8, 2, 4), 96, device="cuda"))
+    w, dy = w.cuda(), torch.randn(50, 96, generator=gen).cuda()
+    dys, dw = mm.moe_unpermute_backward(dy, xs, plan, w, out=torch.zeros_like(xs))
+    loss = lambda a, b: (mm.moe_unpermute(a, plan, b).double() * dy).sum().item()  # noqa: E731
+    terms = (ref.gathered(xs, plan["pos"].cpu()) * w.double().cpu()[..., None] * dy.double().cpu()[:, None]).abs().sum().item()
+    va, vb = torch.randn(xs.shape, generator=gen).cuda(), torch.randn(w.shape, generator=gen).cuda()
+    for a, b, want in ((va, 0 * w, (dys.double() * va).sum().item()), (0 * xs, vb, (dw.double() * vb).sum().item())):
+        slope = (loss(xs + a / 2, w + b / 2) - loss(xs - a / 2, w - b / 2))
+        assert abs(slope - want) <= 40 * U32 * (terms + abs(want)) * 4, (slope, want)
+
+
+def test_side_stream_and_graph():
+    idx, w, gen = route(900, 8, 2)
+    x, idx, w = torch.randn(900, 768, generator=gen).to(BF).cuda(), idx.cuda(), w.cuda()
+    out = torch.zeros(mm.moe_permuted_rows(900, 8, 2, 64), 768, dtype=BF, device="cuda")
+
+    def both(stream=None, out=None, ws=None):
+        xs, plan = mm.moe_permute(x, idx, 8, align=64, out=out, workspace=ws, stream=stream)
+        return xs, mm.moe_unpermute(xs, plan, w, stream=stream), plan
+
+    xs, y, plan = both(out=out.clone())
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    o2 = out.clone()
+    torch.cuda.synchronize()
+    xs2, y2, plan2 = both(side, o2)
+    side.synchronize()
+    assert torch.equal(xs, xs2) and torch.equal(y, y2) and all(torch.equal(plan[k], plan2[k]) for k in plan)
+    ws = mm.new_workspace(mm.moe_permute_workspace_bytes(900, 8, 2))
+    graph, o3 = torch.cuda.CUDAGraph(), out.clone()
+    with torch.cuda.graph(graph):
+        xs3, y3, plan3 = both(out=o3, ws=ws)
+    for _ in range(2):
+        idx.copy_((idx + 3) % 8)
+        o3.zero_()
+        graph.replay()
+        xs, y, plan = both(out=out.clone())
+        torch.cuda.synchronize()
+        assert torch.equal(xs, xs3) and torch.equal(y, y3) and all(torch.equal(plan[k], plan3[k]) for k in plan)
+
+
+def test_refusals():
+    x, idx = torch.zeros(4, 64, dtype=BF, device="cuda"), torch.zeros(4, 2, dtype=torch.int32, device="cuda")
+    for bad in (idx.long(), idx[:3], idx[:, 0]):
+        with pytest.raises(ValueError):
+            mm.moe_permute(x, bad, 4)
+    for E, align in ((65, 1), (0, 1), (4, 0), (4, 1025)):
+        with pytest.raises(mm._lib.MMError):
+            mm.moe_permute(x, idx, E, align=align)
+    with pytest.raises(mm._lib.MMError):
+        mm.moe_permute(x, torch.zeros(4, 9, dtype=torch.int32, device="cuda"), 16)
+    with pytest.raises(ValueError):
+        mm.moe_permute(x, idx, 4, out=torch.zeros(9, 64, dtype=BF, device="cuda"))
+    xs, plan = mm.moe_permute(x, idx, 4)
+    w = torch.ones(4, 2, device="cuda")
+    with pytest.raises(ValueError):
+        mm.moe_unpermute(xs, plan, w.to(BF))
+    with pytest.raises(ValueError):
+        mm.moe_unpermute(xs, plan, None)
+    with pytest.raises(ValueError):
+        mm.moe_unpermute_backward(x, None, plan, w)
+    with pytest.raises(ValueError):
+        mm.moe_unpermute_backward(x, xs[:3], plan, w)
+    with pytest.raises(ValueError):
+        mm.moe_unpermute(xs.float(), plan, w, out=torch.zeros(4, 64, dtype=BF, device="cuda"))
