@@ -3,197 +3,746 @@
 //   p = f rho_f w_post,  rho_f = 1 / sqrt(mean_h f^2 + eps)     (w_post absent: p = f)
 //   r = round(s x + g p)                                        (g absent: 1)
 //   n = r rho_r w_pre,   rho_r of the rounded r
-// One block per row, fp32 sums in a fixed order.
+//
+// Both directions read every input and write every output once, so DRAM
+// bounds them.  A row is held in the registers of one group of `tpr` threads
+// (a multiple of a warp; V elements per load, NV loads per array), a block
+// holds several groups, and the loads of a row are all in flight together.
+// Sums run in fp32 in a fixed order: lane, warp tree, the group's warps.
 #include <cstring>
 
 #include "mm_kernels.cuh"
 
 namespace mm {
 
-constexpr int kBnThreads = 256;
+// V consecutive elements as loaded (one access), and as fp32.
+template <typename T, int V> struct Pack;
+template <> struct Pack<__nv_bfloat16, 8> {
+  typedef uint4 Raw;
+  static __device__ __forceinline__ float get(const Raw& r, int j) {
+    const uint32_t w = j < 2 ? r.x : j < 4 ? r.y : j < 6 ? r.z : r.w;
+    return __uint_as_float((j & 1) ? (w & 0xffff0000u) : (w << 16));
+  }
+  static __device__ __forceinline__ Raw put(const float (&v)[8]) {
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                      pack_bf16x2(v[6], v[7]));
+  }
+};
+template <> struct Pack<__nv_bfloat16, 1> {
+  typedef __nv_bfloat16 Raw;
+  static __device__ __forceinline__ float get(const Raw& r, int) { return __bfloat162float(r); }
+  static __device__ __forceinline__ Raw put(const float (&v)[1]) { return __float2bfloat16_rn(v[0]); }
+};
+template <> struct Pack<float, 4> {
+  typedef float4 Raw;
+  static __device__ __forceinline__ float get(const Raw& r, int j) {
+    return j == 0 ? r.x : j == 1 ? r.y : j == 2 ? r.z : r.w;
+  }
+  static __device__ __forceinline__ Raw put(const float (&v)[4]) {
+    return make_float4(v[0], v[1], v[2], v[3]);
+  }
+};
+template <> struct Pack<float, 1> {
+  typedef float Raw;
+  static __device__ __forceinline__ float get(const Raw& r, int) { return r; }
+  static __device__ __forceinline__ Raw put(const float (&v)[1]) { return v[0]; }
+};
 
-__device__ __forceinline__ float bn_load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float bn_load(const float* p) { return *p; }
-__device__ __forceinline__ void bn_store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void bn_store(float* p, float v) { *p = v; }
-template <typename T> __device__ __forceinline__ float bn_round(float v);
-template <> __device__ __forceinline__ float bn_round<float>(float v) { return v; }
-template <> __device__ __forceinline__ float bn_round<__nv_bfloat16>(float v) {
-  return __bfloat162float(__float2bfloat16_rn(v));
+// Vector c of a row that starts at element `base` of p.
+template <typename T, int V>
+__device__ __forceinline__ typename Pack<T, V>::Raw row_load(const void* p, int64_t base, int c) {
+  return reinterpret_cast<const typename Pack<T, V>::Raw*>(static_cast<const T*>(p) + base)[c];
+}
+template <typename T, int V>
+__device__ __forceinline__ void row_store(void* p, int64_t base, int c, const float (&v)[V]) {
+  reinterpret_cast<typename Pack<T, V>::Raw*>(static_cast<T*>(p) + base)[c] = Pack<T, V>::put(v);
 }
 
-// Sum over the block, the same value and order in every thread.
-__device__ __forceinline__ float bn_block_sum(float v, float* red) {
+// Sums of N values over a group of tpr threads, the same in all of them.
+// `red` holds 2 x N floats per warp of the block; the caller flips `turn`
+// between calls, so that a call's slots are not overwritten while a slower
+// warp of the group still reads them (every warp passes this call's barrier
+// before any writes the slots of the call after next).
+template <int N>
+__device__ __forceinline__ void group_sum(float (&v)[N], float* red, int turn, int group, int tpr) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float s = 0.f;
+  for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-  for (int w = 0; w < kBnThreads / 32; ++w) s += red[w];
-  return s;
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  if (tpr == 32) return;
+  const int warps = tpr >> 5, w0 = group * warps, total = blockDim.x >> 5;
+  float* slot = red + turn * (N * total);
+  if ((threadIdx.x & 31) == 0)
+#pragma unroll
+    for (int i = 0; i < N; ++i) slot[(threadIdx.x >> 5) * N + i] = v[i];
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float s = 0.f;
+    for (int w = 0; w < warps; ++w) s += slot[(w0 + w) * N + i];
+    v[i] = s;
+  }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kBnThreads) block_norm_kernel(const BlockNormFwd a) {
+__device__ __forceinline__ float inv_rms_of(float ss, int H, float eps) {
+  return 1.0f / sqrtf(ss / static_cast<float>(H) + eps);
+}
+
+// ------------------------------------------------------------------ forward
+constexpr int kBnFwdThreads = 512;      // most threads of a block (one group of them: H = 16384)
+
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(kBnFwdThreads) block_norm_kernel(const BlockNormFwd a, int tpr) {
+  using P = Pack<T, V>;
   pdl_enter();
-  __shared__ float red[kBnThreads / 32];
-  extern __shared__ float row[];           // r of the row, fp32
-  const int H = a.H;
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const T* x = static_cast<const T*>(a.x) + t * H;
-    const T* f = a.f ? static_cast<const T*>(a.f) + t * H : nullptr;
-    const T* gate = a.gate ? static_cast<const T*>(a.gate) + (a.gate_per_token ? t * H : 0) : nullptr;
-    float rho_f = 1.f;
+  __shared__ float red[2 * kBnFwdThreads / 32];
+  const int group = threadIdx.x / tpr, c0 = threadIdx.x - group * tpr, nv = a.H / V;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x / tpr) + group;
+  if (t >= a.T) return;                       // whole groups: their barriers are their own
+  const int64_t base = t * a.H, gbase = a.gate_per_token ? base : 0;
+  typename P::Raw x[NV], f[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = c0 + i * tpr;
+    if (c < nv) x[i] = row_load<T, V>(a.x, base, c);
+  }
+  if (a.f) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = c0 + i * tpr;
+      if (c < nv) f[i] = row_load<T, V>(a.f, base, c);
+    }
+    float rho[1] = {1.f};
     if (a.post_w) {
-      float ss = 0.f;
-      for (int h = threadIdx.x; h < H; h += kBnThreads) {
-        const float v = bn_load(f + h);
-        ss = fmaf(v, v, ss);
-      }
-      rho_f = 1.0f / sqrtf(bn_block_sum(ss, red) / static_cast<float>(H) + a.eps);
-      if (threadIdx.x == 0 && a.rstd_post) a.rstd_post[t] = rho_f;
+      rho[0] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (c0 + i * tpr < nv)
+#pragma unroll
+          for (int j = 0; j < V; ++j) rho[0] = fmaf(P::get(f[i], j), P::get(f[i], j), rho[0]);
+      group_sum(rho, red, 0, group, tpr);
+      rho[0] = inv_rms_of(rho[0], a.H, a.eps);
+      if (c0 == 0 && a.rstd_post) a.rstd_post[t] = rho[0];
     }
-    float ss = 0.f;
-    for (int h = threadIdx.x; h < H; h += kBnThreads) {
-      float v = bn_load(x + h);
-      if (f) {
-        float p = bn_load(f + h);
-        if (a.post_w) p = p * rho_f * bn_load(static_cast<const T*>(a.post_w) + h);
-        if (gate) p *= bn_load(gate + h);
-        v = bn_round<T>(fmaf(a.residual_scale, v, p));
-        bn_store(static_cast<T*>(a.r) + t * H + h, v);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = c0 + i * tpr;
+      if (c < nv) {
+        float v[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = P::get(f[i], j);
+        if (a.post_w) {
+          const auto w = row_load<T, V>(a.post_w, 0, c);
+#pragma unroll
+          for (int j = 0; j < V; ++j) v[j] = v[j] * rho[0] * P::get(w, j);
+        }
+        if (a.gate) {
+          const auto g = row_load<T, V>(a.gate, gbase, c);
+#pragma unroll
+          for (int j = 0; j < V; ++j) v[j] *= P::get(g, j);
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = fmaf(a.residual_scale, P::get(x[i], j), v[j]);
+        x[i] = P::put(v);                     // r as stored
+        row_store<T, V>(a.r, base, c, v);
       }
-      row[h] = v;
-      ss = fmaf(v, v, ss);
     }
-    if (a.pre_w) {
-      const float rho_r = 1.0f / sqrtf(bn_block_sum(ss, red) / static_cast<float>(H) + a.eps);
-      if (threadIdx.x == 0 && a.rstd_pre) a.rstd_pre[t] = rho_r;
-      for (int h = threadIdx.x; h < H; h += kBnThreads)
-        bn_store(static_cast<T*>(a.n) + t * H + h,
-                 row[h] * rho_r * bn_load(static_cast<const T*>(a.pre_w) + h));
+  }
+  if (a.pre_w == nullptr) return;
+  float rho[1] = {0.f};
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (c0 + i * tpr < nv)
+#pragma unroll
+      for (int j = 0; j < V; ++j) rho[0] = fmaf(P::get(x[i], j), P::get(x[i], j), rho[0]);
+  group_sum(rho, red, 1, group, tpr);
+  rho[0] = inv_rms_of(rho[0], a.H, a.eps);
+  if (c0 == 0 && a.rstd_pre) a.rstd_pre[t] = rho[0];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = c0 + i * tpr;
+    if (c < nv) {
+      const auto w = row_load<T, V>(a.pre_w, 0, c);
+      float v[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] = P::get(x[i], j) * rho[0] * P::get(w, j);
+      row_store<T, V>(a.n, base, c, v);
     }
   }
 }
 
-// D = dr + rho_r (w_pre dn) - r rho_r^3 c_r,  c_r = mean_h(r w_pre dn)
-template <typename T>
-__device__ __forceinline__ float bn_grad_r(const BlockNormBwd& a, int64_t t, int h, float rho_r,
-                                           float c_r) {
-  const int64_t i = t * a.H + h;
-  float d = a.dr ? bn_load(static_cast<const T*>(a.dr) + i) : 0.f;
-  if (a.pre_w) {
-    const float v = bn_load(static_cast<const T*>(a.dn) + i) * bn_load(static_cast<const T*>(a.pre_w) + h);
-    d += rho_r * (v - bn_load(static_cast<const T*>(a.r) + i) * (rho_r * rho_r * c_r));
-  }
+// ----------------------------------------------------------------- backward
+// With v = w_pre dn, e = dr + rho_r v, D = e - r rho_r^3 c_r and q = g D, the
+// two row means are linear in three sums that one pass over the row gives:
+//   c_r = S1 / H,  S1 = sum r v
+//   c_f = (S2 - rho_r^3 c_r S3) / H,  S2 = sum (f w_post g) e,
+//                                     S3 = sum (f w_post g) r
+// so a row costs one reduction.  A channel gate's two column sums are one,
+//   M = sum_t D f rho_f:  d_post_w = g M,  d_gate = w_post M
+// (a token gate has only d_post_w = sum_t g D f rho_f), so a thread keeps two
+// sums per column of its own over all rows of its group; the groups of a block
+// are added through shared memory, the blocks by a second kernel.  Products
+// and sums run on pairs (fma.rn.f32x2): with plain fp32 instructions the issue
+// slots, not DRAM, set the time (1654 instructions a row of 768 columns).
+constexpr int kBnBwdThreads = 512;      // 128 registers a thread
+constexpr int kBnSums = 2;              // d_pre_w, M
+constexpr size_t kBnMostSmem = 224 * 1024;   // dynamic, of 227 KB a block may have
+
+__device__ __forceinline__ u64 fmul2(u64 a, u64 b) {
+  u64 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+__device__ __forceinline__ u64 pair2(float lo, float hi) {
+  return (static_cast<u64>(__float_as_uint(hi)) << 32) | __float_as_uint(lo);
+}
+__device__ __forceinline__ float lo2(u64 v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float hi2(u64 v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+
+// A thread's unit m of a row: V consecutive elements, or (V = 1) two single
+// columns tpr apart.  Columns behind the row read as zeros.
+template <typename T, int V>
+struct Unit {
+  static constexpr int kPairs = V / 2;
+  static constexpr bool kAsync = true;        // 16-byte cp.async
+  typedef typename Pack<T, V>::Raw Raw;
+  static __device__ __forceinline__ void copy(uint32_t slot, const void* p, int64_t base, int m, int c0, int tpr,
+                                              int nv) {
+    if (c0 + m * tpr < nv)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot),
+                   "l"(reinterpret_cast<const Raw*>(static_cast<const T*>(p) + base) + c0 + m * tpr)
+                   : "memory");
+  }
+  static __device__ __forceinline__ Raw zero() { return Raw{}; }
+  static __device__ __forceinline__ Raw load(const void* p, int64_t base, int m, int c0, int tpr, int nv) {
+    const int c = c0 + m * tpr;
+    return c < nv ? row_load<T, V>(p, base, c) : zero();
+  }
+  static __device__ __forceinline__ u64 get(const Raw& r, int k) {
+    return pair2(Pack<T, V>::get(r, 2 * k), Pack<T, V>::get(r, 2 * k + 1));
+  }
+  static __device__ __forceinline__ void store(void* p, int64_t base, int m, int c0, int tpr, int nv,
+                                               const u64 (&v)[kPairs]) {
+    const int c = c0 + m * tpr;
+    if (c >= nv) return;
+    float o[V];
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) {
+      o[2 * k] = lo2(v[k]);
+      o[2 * k + 1] = hi2(v[k]);
+    }
+    row_store<T, V>(p, base, c, o);
+  }
+  // fp32 values by column in shared memory (16-byte aligned, kept for every unit)
+  static __device__ __forceinline__ void cols(const float* s, int m, int c0, int tpr, u64 (&v)[kPairs]) {
+    const ulonglong2* q = reinterpret_cast<const ulonglong2*>(s + (c0 + m * tpr) * V);
+#pragma unroll
+    for (int k = 0; k < kPairs / 2; ++k) {
+      const ulonglong2 w = q[k];
+      v[2 * k] = w.x;
+      v[2 * k + 1] = w.y;
+    }
+  }
+  static __device__ __forceinline__ void keep(float* s, int m, int c0, int tpr, int nv, const u64 (&v)[kPairs]) {
+    if (c0 + m * tpr >= nv) return;
+    ulonglong2* q = reinterpret_cast<ulonglong2*>(s + (c0 + m * tpr) * V);
+#pragma unroll
+    for (int k = 0; k < kPairs / 2; ++k) q[k] = make_ulonglong2(v[2 * k], v[2 * k + 1]);
+  }
+};
+template <typename T>
+struct Unit<T, 1> {
+  static constexpr int kPairs = 1;
+  static constexpr bool kAsync = false;       // cp.async of 4 bytes is slower than plain loads
+  struct __align__(2 * sizeof(T)) Raw {
+    T a, b;
+  };
+  static __device__ __forceinline__ void copy(uint32_t, const void*, int64_t, int, int, int, int) {}
+  static __device__ __forceinline__ Raw zero() { return Raw{T(0.f), T(0.f)}; }
+  static __device__ __forceinline__ Raw load(const void* p, int64_t base, int m, int c0, int tpr, int nv) {
+    const T* row = static_cast<const T*>(p) + base;
+    const int c = c0 + 2 * m * tpr;
+    return Raw{c < nv ? row[c] : T(0.f), c + tpr < nv ? row[c + tpr] : T(0.f)};
+  }
+  static __device__ __forceinline__ u64 get(const Raw& r, int) {
+    return pair2(static_cast<float>(r.a), static_cast<float>(r.b));
+  }
+  static __device__ __forceinline__ void store(void* p, int64_t base, int m, int c0, int tpr, int nv,
+                                               const u64 (&v)[1]) {
+    const int c = c0 + 2 * m * tpr;
+    const float a[1] = {lo2(v[0])}, b[1] = {hi2(v[0])};
+    if (c < nv) row_store<T, 1>(p, base, c, a);
+    if (c + tpr < nv) row_store<T, 1>(p, base, c + tpr, b);
+  }
+  static __device__ __forceinline__ void cols(const float* s, int m, int c0, int tpr, u64 (&v)[1]) {
+    const int c = c0 + 2 * m * tpr;
+    v[0] = pair2(s[c], s[c + tpr]);
+  }
+  static __device__ __forceinline__ void keep(float* s, int m, int c0, int tpr, int nv, const u64 (&v)[1]) {
+    const int c = c0 + 2 * m * tpr;
+    if (c < nv) s[c] = lo2(v[0]);
+    if (c + tpr < nv) s[c + tpr] = hi2(v[0]);
+  }
+};
 
 template <typename T>
-__global__ void __launch_bounds__(kBnThreads) block_norm_bwd_rows_kernel(const BlockNormBwd a) {
+__device__ __forceinline__ float bn_param(const void* w, int h) {
+  return w ? static_cast<float>(static_cast<const T*>(w)[h]) : 1.f;
+}
+
+// NU units a thread.  The next row's inputs are copied to shared memory with
+// cp.async while this one is worked on (`stages` 2; 1 where two do not fit):
+// each thread copies and reads its own slots only, so the ring needs no
+// barrier, and its registers hold only sums and D.  Without it a group's
+// loads, reduction and stores follow one another and DRAM idles between them
+// (T = 16384, H = 768, bf16: 41 us, with it 32 us,
+// of 22 us that its bytes take at the measured copy rate).  bf16 rows of odd width
+// (2-byte accesses, which cp.async does not move) load into registers.
+// Dynamic shared memory: w_pre and w_post g by column (`span` floats each: the
+// columns of every unit, zeros behind the row), then the ring
+// [stages][inputs][NU][threads], in whose place [groups][kBnSums][span] stands
+// at the end.
+enum BnInput { kInR, kInDn, kInDr, kInF, kInGate, kBnInputs };
+
+template <typename T, int V, int NU, bool kTokenGate>
+__global__ void __launch_bounds__(kBnBwdThreads, 1)
+block_norm_bwd_kernel(const BlockNormBwd a, int tpr, int span, int stages) {
+  using U = Unit<T, V>;
+  typedef typename U::Raw Raw;
+  constexpr int NP = U::kPairs;
+  extern __shared__ __align__(16) float bn_smem[];
+  __shared__ float red[2 * 3 * kBnBwdThreads / 32];
+  float* w_pre = bn_smem;
+  float* w_mid = bn_smem + span;
+  float* behind = bn_smem + 2 * span;
+  const int group = threadIdx.x / tpr, c0 = threadIdx.x - group * tpr, nv = a.H / V;
+  const int groups = blockDim.x / tpr;
+  constexpr int kIn = kTokenGate ? kBnInputs : kBnInputs - 1;
+  const void* src[kBnInputs] = {a.pre_w ? a.r : nullptr, a.pre_w ? a.dn : nullptr, a.dr, a.f,
+                                kTokenGate ? a.gate : nullptr};
+  // the thread's slots, a warp's side by side: stage, input i, unit m, lane
+  constexpr int kStageBytes = kIn * NU * 32 * static_cast<int>(sizeof(Raw));
+  unsigned char* ring = reinterpret_cast<unsigned char*>(behind) + (threadIdx.x >> 5) * (stages * kStageBytes) +
+                        (threadIdx.x & 31) * sizeof(Raw);
+  auto at = [](int i, int m) { return (i * NU + m) * 32 * static_cast<int>(sizeof(Raw)); };
+  Raw reg[U::kAsync ? 1 : kIn][U::kAsync ? 1 : NU];
+  auto fetch = [&](int64_t t, int stage) {
+    if (t < a.T)
+#pragma unroll
+      for (int i = 0; i < kIn; ++i)
+        if (src[i])
+#pragma unroll
+          for (int m = 0; m < NU; ++m) {
+            if constexpr (U::kAsync)
+              U::copy(smem_u32(ring + stage * kStageBytes) + at(i, m), src[i], t * a.H, m, c0, tpr, nv);
+            else
+              reg[i][m] = U::load(src[i], t * a.H, m, c0, tpr, nv);
+          }
+    if constexpr (U::kAsync) asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if constexpr (U::kAsync) {                  // what no copy will fill stays zero
+    for (int st = 0; st < stages; ++st)
+#pragma unroll
+      for (int i = 0; i < kIn; ++i)
+#pragma unroll
+        for (int m = 0; m < NU; ++m) *reinterpret_cast<Raw*>(ring + st * kStageBytes + at(i, m)) = U::zero();
+  } else {
+#pragma unroll
+    for (int i = 0; i < kIn; ++i)
+#pragma unroll
+      for (int m = 0; m < NU; ++m) reg[i][m] = U::zero();
+  }
+  auto value = [&](const unsigned char* here, int i, int m) -> Raw {
+    if constexpr (U::kAsync) return *reinterpret_cast<const Raw*>(here + at(i, m));
+    else return reg[i][m];
+  };
   pdl_enter();
-  __shared__ float red[kBnThreads / 32];
-  const int H = a.H;
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const T* gate = a.gate ? static_cast<const T*>(a.gate) + (a.gate_per_token ? t * H : 0) : nullptr;
-    float rho_r = 0.f, c_r = 0.f;
-    if (a.pre_w) {
-      rho_r = a.rstd_pre[t];
-      float s = 0.f;
-      for (int h = threadIdx.x; h < H; h += kBnThreads)
-        s = fmaf(bn_load(static_cast<const T*>(a.r) + t * H + h) * bn_load(static_cast<const T*>(a.pre_w) + h),
-                 bn_load(static_cast<const T*>(a.dn) + t * H + h), s);
-      c_r = bn_block_sum(s, red) / static_cast<float>(H);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * groups + group;
+  float next_r = 0.f, next_f = 1.f;
+  auto fetch_rstd = [&](int64_t row) {
+    if (row >= a.T) return;
+    if (a.pre_w) next_r = a.rstd_pre[row];
+    if (a.post_w) next_f = a.rstd_post[row];
+  };
+  if (U::kAsync && stages == 2) fetch(t, 0);
+  fetch_rstd(t);
+  for (int h = threadIdx.x; h < span; h += blockDim.x) {
+    w_pre[h] = h < a.H && a.pre_w ? bn_param<T>(a.pre_w, h) : 0.f;
+    w_mid[h] = h < a.H ? bn_param<T>(a.post_w, h) * bn_param<T>(kTokenGate ? nullptr : a.gate, h) : 0.f;
+  }
+  __syncthreads();
+  u64 s_pre[NU][NP], s_mid[NU][NP];
+#pragma unroll
+  for (int m = 0; m < NU; ++m)
+#pragma unroll
+    for (int k = 0; k < NP; ++k) s_pre[m][k] = s_mid[m][k] = 0;
+  const float inv_h = 1.0f / static_cast<float>(a.H);
+  const u64 scale2 = pair2(a.residual_scale, a.residual_scale);
+  int turn = 0, stage = 0;
+  for (; t < a.T; t += step) {
+    const int64_t base = t * a.H;
+    const float rho_r = next_r, rho_f = next_f;
+    if (U::kAsync && stages == 2) {
+      fetch(t + step, stage ^ 1);
+      fetch_rstd(t + step);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      fetch(t, 0);
+      fetch_rstd(t + step);
+      if constexpr (U::kAsync) asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
-    if (threadIdx.x == 0) a.partial[t] = c_r;
-    float rho_f = 1.f, c_f = 0.f;
-    if (a.post_w) {
-      rho_f = a.rstd_post[t];
-      float s = 0.f;
-      for (int h = threadIdx.x; h < H; h += kBnThreads) {
-        float q = bn_grad_r<T>(a, t, h, rho_r, c_r);
-        if (gate) q *= bn_load(gate + h);
-        s = fmaf(bn_load(static_cast<const T*>(a.f) + t * H + h) * bn_load(static_cast<const T*>(a.post_w) + h), q, s);
+    const unsigned char* here = ring + stage * kStageBytes;
+    const u64 rho_r2 = pair2(rho_r, rho_r), rho_f2 = pair2(rho_f, rho_f);
+    u64 s1 = 0, s2 = 0, s3 = 0;
+    u64 e[NU][NP];
+#pragma unroll
+    for (int m = 0; m < NU; ++m) {
+      u64 wp[NP], wm[NP];
+      U::cols(w_pre, m, c0, tpr, wp);
+      U::cols(w_mid, m, c0, tpr, wm);
+      const Raw r = value(here, kInR, m), dn = value(here, kInDn, m), dr = value(here, kInDr, m);
+      const Raw f = value(here, kInF, m), g = kTokenGate ? value(here, kInGate, m) : U::zero();
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        const u64 rk = U::get(r, k), nk = U::get(dn, k);
+        const u64 v = fmul2(nk, wp[k]);
+        s_pre[m][k] = ffma2(nk, fmul2(rk, rho_r2), s_pre[m][k]);
+        s1 = ffma2(rk, v, s1);
+        e[m][k] = ffma2(rho_r2, v, U::get(dr, k));
+        u64 fw = fmul2(U::get(f, k), wm[k]);
+        if constexpr (kTokenGate) fw = fmul2(fw, U::get(g, k));
+        s2 = ffma2(fw, e[m][k], s2);
+        s3 = ffma2(fw, rk, s3);
       }
-      c_f = bn_block_sum(s, red) / static_cast<float>(H);
     }
-    for (int h = threadIdx.x; h < H; h += kBnThreads) {
-      const int64_t i = t * H + h;
-      const float d = bn_grad_r<T>(a, t, h, rho_r, c_r);
-      bn_store(static_cast<T*>(a.dx) + i, a.residual_scale * d);
+    float s[3] = {hsum2(s1), hsum2(s2), hsum2(s3)};
+    group_sum(s, red, turn, group, tpr);
+    turn ^= 1;
+    const float k_r = rho_r * rho_r * (s[0] * inv_h) * rho_r;               // rho_r^3 c_r
+    const float k_f = a.post_w ? rho_f * rho_f * ((s[1] - k_r * s[2]) * inv_h) : 0.f;  // rho_f^2 c_f
+    const u64 k_r2 = pair2(-k_r, -k_r), k_f2 = pair2(-k_f, -k_f);
+#pragma unroll
+    for (int m = 0; m < NU; ++m) {
+      u64 wm[NP], o[NP];
+      U::cols(w_mid, m, c0, tpr, wm);
+      const Raw r = value(here, kInR, m);
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        e[m][k] = ffma2(U::get(r, k), k_r2, e[m][k]);                       // D
+        o[k] = fmul2(scale2, e[m][k]);
+      }
+      U::store(a.dx, base, m, c0, tpr, nv, o);
       if (a.df == nullptr) continue;
-      const float f = a.f ? bn_load(static_cast<const T*>(a.f) + i) : 0.f;
-      const float w = a.post_w ? bn_load(static_cast<const T*>(a.post_w) + h) : 1.f;
-      const float q = gate ? d * bn_load(gate + h) : d;
-      if (gate && a.gate_per_token) bn_store(static_cast<T*>(a.d_gate) + i, d * (f * rho_f * w));
-      bn_store(static_cast<T*>(a.df) + i, a.post_w ? rho_f * (w * q - f * (rho_f * rho_f * c_f)) : q);
+      const Raw f = value(here, kInF, m), g = kTokenGate ? value(here, kInGate, m) : U::zero();
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        const u64 fk = U::get(f, k), u = fmul2(fk, rho_f2);
+        if constexpr (kTokenGate) {
+          o[k] = fmul2(fmul2(e[m][k], u), wm[k]);                           // wm is w_post here
+          e[m][k] = fmul2(e[m][k], U::get(g, k));
+        }
+        s_mid[m][k] = ffma2(e[m][k], u, s_mid[m][k]);
+        e[m][k] = fmul2(rho_f2, ffma2(fk, k_f2, fmul2(wm[k], e[m][k])));
+      }
+      if constexpr (kTokenGate) U::store(a.d_gate, base, m, c0, tpr, nv, o);
+      U::store(a.df, base, m, c0, tpr, nv, e[m]);
+    }
+    if (U::kAsync && stages == 2) stage ^= 1;
+  }
+  // the block's column sums: each group's side by side, then added in order
+  if constexpr (U::kAsync) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+  float* mine = behind + group * kBnSums * span;
+#pragma unroll
+  for (int m = 0; m < NU; ++m) {
+    U::keep(mine, m, c0, tpr, nv, s_pre[m]);
+    U::keep(mine + span, m, c0, tpr, nv, s_mid[m]);
+  }
+  __syncthreads();
+  float* part = a.partial + static_cast<int64_t>(blockIdx.x) * kBnSums * a.H;
+  for (int h = threadIdx.x; h < a.H; h += blockDim.x)
+#pragma unroll
+    for (int q = 0; q < kBnSums; ++q) {
+      float sum = 0.f;
+      for (int gi = 0; gi < groups; ++gi) sum += behind[(gi * kBnSums + q) * span + h];
+      part[q * a.H + h] = sum;
+    }
+}
+
+// Rows too wide for a block's registers: the block walks the row twice (the
+// second time from L2), and keeps its column sums in shared memory, each
+// column owned by one thread.
+template <typename T, int V>
+__global__ void __launch_bounds__(kBnFwdThreads, 1) block_norm_bwd_wide_kernel(const BlockNormBwd a) {
+  using P = Pack<T, V>;
+  pdl_enter();
+  __shared__ float red[2 * 3 * kBnFwdThreads / 32];
+  extern __shared__ __align__(16) float bn_smem[];   // [2][H]
+  float* cols = bn_smem;
+  const int nv = a.H / V;
+  const bool token_gate = a.gate != nullptr && a.gate_per_token;
+  for (int c = threadIdx.x; c < nv; c += kBnFwdThreads)
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+      for (int q = 0; q < kBnSums; ++q) cols[q * a.H + c * V + j] = 0.f;
+  int turn = 0;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const int64_t base = t * a.H, gbase = a.gate_per_token ? base : 0;
+    const float rho_r = a.pre_w ? a.rstd_pre[t] : 0.f;
+    const float rho_f = a.post_w ? a.rstd_post[t] : 1.f;
+    float s[3] = {0.f, 0.f, 0.f};
+    float k_r = 0.f, k_f = 0.f;
+    for (int pass = 0; pass < 2; ++pass) {
+      for (int c = threadIdx.x; c < nv; c += kBnFwdThreads) {
+        float d[V], f[V], w[V], g[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          d[j] = f[j] = 0.f;
+          w[j] = g[j] = 1.f;
+        }
+        if (a.dr) {
+          const auto x = row_load<T, V>(a.dr, base, c);
+#pragma unroll
+          for (int j = 0; j < V; ++j) d[j] = P::get(x, j);
+        }
+        if (a.f) {
+          const auto x = row_load<T, V>(a.f, base, c);
+#pragma unroll
+          for (int j = 0; j < V; ++j) f[j] = P::get(x, j);
+        }
+        if (a.post_w) {
+          const auto x = row_load<T, V>(a.post_w, 0, c);
+#pragma unroll
+          for (int j = 0; j < V; ++j) w[j] = P::get(x, j);
+        }
+        if (a.gate) {
+          const auto x = row_load<T, V>(a.gate, gbase, c);
+#pragma unroll
+          for (int j = 0; j < V; ++j) g[j] = P::get(x, j);
+        }
+        if (a.pre_w) {
+          const auto xr = row_load<T, V>(a.r, base, c);
+          const auto xd = row_load<T, V>(a.dn, base, c);
+          const auto xw = row_load<T, V>(a.pre_w, 0, c);
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            const float r = P::get(xr, j), dn = P::get(xd, j), v = dn * P::get(xw, j);
+            if (pass == 0) {
+              s[0] = fmaf(r, v, s[0]);
+              s[2] = fmaf(f[j] * w[j] * g[j], r, s[2]);
+              d[j] = fmaf(rho_r, v, d[j]);
+            } else {
+              d[j] = fmaf(rho_r, fmaf(-r, k_r, v), d[j]);
+              cols[c * V + j] = fmaf(dn, r * rho_r, cols[c * V + j]);
+            }
+          }
+        }
+        if (pass == 0) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) s[1] = fmaf(f[j] * w[j] * g[j], d[j], s[1]);
+          continue;
+        }
+        float o[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) o[j] = a.residual_scale * d[j];
+        row_store<T, V>(a.dx, base, c, o);
+        if (a.df == nullptr) continue;
+#pragma unroll
+        for (int j = 0; j < V; ++j) o[j] = d[j] * (f[j] * rho_f * w[j]);
+        if (token_gate) row_store<T, V>(a.d_gate, base, c, o);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const int h = c * V + j;
+          const float q = d[j] * g[j];
+          cols[a.H + h] = fmaf(token_gate ? q : d[j], f[j] * rho_f, cols[a.H + h]);
+          d[j] = a.post_w ? rho_f * fmaf(-f[j], k_f, w[j] * q) : q;
+        }
+        row_store<T, V>(a.df, base, c, d);
+      }
+      if (pass == 0) {
+        group_sum(s, red, turn, 0, kBnFwdThreads);
+        turn ^= 1;
+        const float inv_h = 1.0f / static_cast<float>(a.H);
+        k_r = rho_r * rho_r * (s[0] * inv_h);
+        k_f = rho_f * rho_f * ((s[1] - rho_r * k_r * s[2]) * inv_h);
+      }
+    }
+  }
+  float* part = a.partial + static_cast<int64_t>(blockIdx.x) * kBnSums * a.H;
+  for (int c = threadIdx.x; c < nv; c += kBnFwdThreads)
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+      for (int q = 0; q < kBnSums; ++q) part[q * a.H + c * V + j] = cols[q * a.H + c * V + j];
+}
+
+// Sums over the blocks' partials: 32 columns x 32 slices of the blocks per
+// block of threads (five loads a thread, all in flight; 8 slices took 6 us at
+// H = 768), slices added in order; grid.y: 0 d_pre_w, 1 what follows from M.
+constexpr int kBnSlices = 32;
+template <typename T>
+__global__ void __launch_bounds__(32 * kBnSlices)
+block_norm_bwd_sum_kernel(const BlockNormBwd a, int nblk) {
+  pdl_enter();
+  __shared__ float red[kBnSlices][32];
+  const int h = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5, q = blockIdx.y;
+  float* d_gate = a.gate && !a.gate_per_token ? static_cast<float*>(a.d_gate) : nullptr;
+  if (q == 0 ? a.d_pre_w == nullptr : (a.d_post_w == nullptr && d_gate == nullptr)) return;
+  float s = 0.f;
+  if (h < a.H)
+#pragma unroll 8
+    for (int b = slice; b < nblk; b += kBnSlices)
+      s += a.partial[(static_cast<int64_t>(b) * kBnSums + q) * a.H + h];
+  red[slice][threadIdx.x & 31] = s;
+  __syncthreads();
+  if (slice == 0 && h < a.H) {
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kBnSlices; ++i) s += red[i][threadIdx.x];
+    if (q == 0) {
+      a.d_pre_w[h] = s;
+    } else {
+      if (a.d_post_w) a.d_post_w[h] = d_gate ? s * bn_param<T>(a.gate, h) : s;
+      if (d_gate) d_gate[h] = a.post_w ? s * bn_param<T>(a.post_w, h) : s;
     }
   }
 }
 
-// Column sums over the tokens: one thread per column.
-template <typename T>
-__global__ void __launch_bounds__(kBnThreads) block_norm_bwd_cols_kernel(const BlockNormBwd a) {
-  pdl_enter();
-  const int h = blockIdx.x * kBnThreads + threadIdx.x;
-  if (h >= a.H) return;
-  const float w = a.post_w ? bn_load(static_cast<const T*>(a.post_w) + h) : 1.f;
-  float s_pre = 0.f, s_post = 0.f, s_gate = 0.f;
-  for (int64_t t = 0; t < a.T; ++t) {
-    const int64_t i = t * a.H + h;
-    const float rho_r = a.pre_w ? a.rstd_pre[t] : 0.f;
-    if (a.pre_w)
-      s_pre += bn_load(static_cast<const T*>(a.dn) + i) * (bn_load(static_cast<const T*>(a.r) + i) * rho_r);
-    if (a.post_w == nullptr && (a.gate == nullptr || a.gate_per_token)) continue;
-    const float d = bn_grad_r<T>(a, t, h, rho_r, a.partial[t]);
-    const float u = bn_load(static_cast<const T*>(a.f) + i) * (a.post_w ? a.rstd_post[t] : 1.f);
-    const float g = a.gate ? bn_load(static_cast<const T*>(a.gate) + (a.gate_per_token ? i : h)) : 1.f;
-    s_post += d * g * u;
-    s_gate += d * (u * w);
+// ----------------------------------------------------------------- launches
+static inline int bn_vec(int dtype, int H) {
+  const int v = dtype == kDtypeBF16 ? 8 : 4;
+  return H % v == 0 ? v : 1;
+}
+// Threads of a row's group with NV vectors each.
+static inline int bn_tpr(int nv, int NV) { return (nv + 32 * NV - 1) / (32 * NV) * 32; }
+
+// Backward: a thread takes up to 24 elements of bf16 (three 16-byte vectors
+// of each input) and 16 of fp32 or of an unaligned width, as its registers
+// allow; the fewest idle lanes decide between the unit counts, more units a
+// thread where that is equal (fewer warps to add up).  A row that needs more
+// than a block's threads so is `wide`.
+template <int V> struct BnUnits;
+template <> struct BnUnits<8> { static constexpr int kMost = 3, kSome = 2, kFew = 1; };
+template <> struct BnUnits<4> { static constexpr int kMost = 4, kSome = 2, kFew = 1; };
+template <> struct BnUnits<1> { static constexpr int kMost = 4, kSome = 2, kFew = 1; };
+
+struct BnBwdShape {
+  int V, NU, tpr, groups, grid, span;
+  bool wide;
+};
+template <int V>
+static BnBwdShape bn_bwd_shape_v(int64_t T, int H) {
+  using N = BnUnits<V>;
+  constexpr int width = V == 1 ? 2 : V;       // elements of a unit
+  BnBwdShape s{V, 0, 0, 1, 1, 0, false};
+  for (int NU : {N::kMost, N::kSome, N::kFew}) {
+    const int tpr = (H + 32 * NU * width - 1) / (32 * NU * width) * 32;
+    if (tpr > kBnBwdThreads) continue;
+    if (s.NU == 0 || NU * tpr < s.NU * s.tpr) {
+      s.NU = NU;
+      s.tpr = tpr;
+    }
   }
-  if (a.pre_w) a.d_pre_w[h] = s_pre;
-  if (a.post_w) a.d_post_w[h] = s_post;
-  if (a.gate && !a.gate_per_token) static_cast<float*>(a.d_gate)[h] = s_gate;
+  const int64_t sms = num_sms();
+  if (s.NU == 0) {
+    s.wide = true;
+    s.tpr = kBnFwdThreads;
+    s.grid = static_cast<int>(T < sms ? (T > 0 ? T : 1) : sms);
+    return s;
+  }
+  s.span = s.NU * s.tpr * width;
+  s.groups = kBnBwdThreads / s.tpr;
+  const int64_t want = (T + s.groups - 1) / s.groups;
+  s.grid = static_cast<int>(want < sms ? (want > 0 ? want : 1) : sms);
+  return s;
+}
+static BnBwdShape bn_bwd_shape(int64_t T, int H, int dtype) {
+  const int v = bn_vec(dtype, H);
+  return v == 8 ? bn_bwd_shape_v<8>(T, H) : v == 4 ? bn_bwd_shape_v<4>(T, H) : bn_bwd_shape_v<1>(T, H);
 }
 
 size_t block_norm_bwd_bytes(int64_t T, int H, int dtype) {
-  (void)H;
-  (void)dtype;
-  return 4 * static_cast<size_t>(T);
+  return 4 * static_cast<size_t>(bn_bwd_shape(T, H, dtype).grid) * kBnSums * H;
 }
 
-static dim3 bn_row_grid(int64_t T) {
-  const int64_t most = static_cast<int64_t>(num_sms()) * 8;
-  return dim3(static_cast<unsigned>(T < most ? (T > 0 ? T : 1) : most));
+template <typename T, int V, int NV>
+static cudaError_t bn_fwd_launch(const BlockNormFwd& a, int tpr, cudaStream_t st) {
+  const int groups = tpr >= 256 ? 1 : 256 / tpr;
+  const int64_t blocks = (a.T + groups - 1) / groups;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  return launch_dependent_kernel(block_norm_kernel<T, V, NV>, dim3(static_cast<unsigned>(blocks)),
+                                 dim3(groups * tpr), 0, st, a, tpr);
+}
+
+template <typename T, int V>
+static cudaError_t bn_fwd_pick(const BlockNormFwd& a, cudaStream_t st) {
+  // up to 32 elements a thread; fewer, where a warp holds the row with fewer
+  const int nv = a.H / V;
+  constexpr int kMost = 32 / V;
+  constexpr int kSome = kMost * 3 / 4, kHalf = kMost / 2, kFew = kMost / 4;
+  if (nv <= 32 * kFew) return bn_fwd_launch<T, V, kFew>(a, 32, st);
+  const int options[3] = {kMost, kSome, kHalf};
+  int best = kMost;
+  for (int NV : options)
+    if (NV * bn_tpr(nv, NV) < best * bn_tpr(nv, best) && bn_tpr(nv, NV) <= kBnFwdThreads) best = NV;
+  if (best == kMost) return bn_fwd_launch<T, V, kMost>(a, bn_tpr(nv, kMost), st);
+  if (best == kSome) return bn_fwd_launch<T, V, kSome>(a, bn_tpr(nv, kSome), st);
+  return bn_fwd_launch<T, V, kHalf>(a, bn_tpr(nv, kHalf), st);
 }
 
 cudaError_t launch_block_norm(int dtype, const BlockNormFwd& a, cudaStream_t st) {
-  const size_t smem = 4 * static_cast<size_t>(a.H);
-  auto run = [&](auto kern) {
+  if (dtype == kDtypeBF16)
+    return a.H % 8 == 0 ? bn_fwd_pick<__nv_bfloat16, 8>(a, st) : bn_fwd_pick<__nv_bfloat16, 1>(a, st);
+  return a.H % 4 == 0 ? bn_fwd_pick<float, 4>(a, st) : bn_fwd_pick<float, 1>(a, st);
+}
+
+template <typename T, int V, int NU>
+static cudaError_t bn_bwd_launch(const BlockNormBwd& a, const BnBwdShape& s, cudaStream_t st) {
+  using U = Unit<T, V>;
+  const bool token_gate = a.gate != nullptr && a.gate_per_token;
+  auto kern = token_gate ? block_norm_bwd_kernel<T, V, NU, true> : block_norm_bwd_kernel<T, V, NU, false>;
+  const size_t threads = static_cast<size_t>(s.groups) * s.tpr;
+  const size_t cols = 2 * sizeof(float) * s.span, sums = kBnSums * sizeof(float) * s.span * s.groups;
+  const size_t stage = U::kAsync ? (kBnInputs - !token_gate) * NU * threads * sizeof(typename U::Raw) : 0;
+  const int stages = cols + 2 * stage <= kBnMostSmem ? 2 : 1;
+  const size_t smem = cols + (stages * stage > sums ? stages * stage : sums);
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent_kernel(kern, dim3(s.grid), dim3(static_cast<unsigned>(threads)), smem, st, a,
+                                 s.tpr, s.span, stages);
+}
+
+template <typename T, int V>
+static cudaError_t bn_bwd_pick(const BlockNormBwd& a, const BnBwdShape& s, cudaStream_t st) {
+  if (s.wide) {
+    auto kern = block_norm_bwd_wide_kernel<T, V>;
+    const size_t smem = sizeof(float) * kBnSums * a.H;
     cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent_kernel(kern, bn_row_grid(a.T), dim3(kBnThreads), smem, st, a);
-  };
-  return dtype == kDtypeBF16 ? run(block_norm_kernel<__nv_bfloat16>) : run(block_norm_kernel<float>);
+    return launch_dependent_kernel(kern, dim3(s.grid), dim3(kBnFwdThreads), smem, st, a);
+  }
+  using N = BnUnits<V>;
+  if (s.NU == N::kMost) return bn_bwd_launch<T, V, N::kMost>(a, s, st);
+  if (s.NU == N::kSome) return bn_bwd_launch<T, V, N::kSome>(a, s, st);
+  return bn_bwd_launch<T, V, N::kFew>(a, s, st);
 }
 
 cudaError_t launch_block_norm_bwd_rows(int dtype, const BlockNormBwd& a, cudaStream_t st) {
-  auto run = [&](auto kern) {
-    return launch_dependent_kernel(kern, bn_row_grid(a.T), dim3(kBnThreads), 0, st, a);
-  };
-  return dtype == kDtypeBF16 ? run(block_norm_bwd_rows_kernel<__nv_bfloat16>)
-                             : run(block_norm_bwd_rows_kernel<float>);
+  const BnBwdShape s = bn_bwd_shape(a.T, a.H, dtype);
+  if (dtype == kDtypeBF16)
+    return s.V == 8 ? bn_bwd_pick<__nv_bfloat16, 8>(a, s, st) : bn_bwd_pick<__nv_bfloat16, 1>(a, s, st);
+  return s.V == 4 ? bn_bwd_pick<float, 4>(a, s, st) : bn_bwd_pick<float, 1>(a, s, st);
 }
 
 cudaError_t launch_block_norm_bwd_cols(int dtype, const BlockNormBwd& a, cudaStream_t st) {
-  const dim3 grid((a.H + kBnThreads - 1) / kBnThreads);
+  const int nblk = a.T > 0 ? bn_bwd_shape(a.T, a.H, dtype).grid : 0;
   auto run = [&](auto kern) {
-    return launch_dependent_kernel(kern, grid, dim3(kBnThreads), 0, st, a);
+    return launch_dependent_kernel(kern, dim3((a.H + 31) / 32, kBnSums), dim3(32 * kBnSlices), 0, st, a, nblk);
   };
-  return dtype == kDtypeBF16 ? run(block_norm_bwd_cols_kernel<__nv_bfloat16>)
-                             : run(block_norm_bwd_cols_kernel<float>);
+  return dtype == kDtypeBF16 ? run(block_norm_bwd_sum_kernel<__nv_bfloat16>)
+                             : run(block_norm_bwd_sum_kernel<float>);
 }
 
 }  // namespace mm
