@@ -1036,11 +1036,13 @@ int mm_moe_permute(const void* x, const int32_t* topk_idx, int64_t T, int H, int
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const PermuteArgs a{x, topk_idx, xs, offsets, counts, perm, pos, ws_at(workspace, sizeof(WsHeader)),
                       T, rows, H, E, k, align};
-  cudaError_t e = counted_launch(MM_KERNEL_PERMUTE, st, [&] { return launch_permute_sort(a, st); });
-  if (e != cudaSuccess) return cuda_fail(e, "permute sort");
-  if (T == 0) return MM_OK;
-  e = counted_launch(MM_KERNEL_PERMUTE, st, [&] { return launch_permute_copy(dtype, a, st); });
-  return e == cudaSuccess ? MM_OK : cuda_fail(e, "permute copy");
+  cudaError_t e;
+  if (permute_launches(T, k) > 1) {
+    e = counted_launch(MM_KERNEL_PERMUTE, st, [&] { return launch_permute_count(a, st); });
+    if (e != cudaSuccess) return cuda_fail(e, "permute count");
+  }
+  e = counted_launch(MM_KERNEL_PERMUTE, st, [&] { return launch_permute(dtype, a, st); });
+  return e == cudaSuccess ? MM_OK : cuda_fail(e, "permute");
 }
 
 int mm_moe_unpermute(const void* ys, const int32_t* pos, const float* topk_w, int64_t T, int H,

@@ -440,8 +440,9 @@ struct UnpermuteBwdArgs {
   int H, E, k;
 };
 size_t permute_bytes(int64_t T, int E, int k);
-cudaError_t launch_permute_sort(const PermuteArgs& a, cudaStream_t st);
-cudaError_t launch_permute_copy(int dtype, const PermuteArgs& a, cudaStream_t st);
+int permute_launches(int64_t T, int k);           // 2: the counts first, 1: in one kernel
+cudaError_t launch_permute_count(const PermuteArgs& a, cudaStream_t st);
+cudaError_t launch_permute(int dtype, const PermuteArgs& a, cudaStream_t st);
 cudaError_t launch_unpermute(int dtype, const UnpermuteArgs& a, cudaStream_t st);
 cudaError_t launch_unpermute_bwd(int dtype, const UnpermuteBwdArgs& a, cudaStream_t st);
 

@@ -2,167 +2,409 @@
 // gradient (include/mm.h, mm_moe_permute).  Assignment a = t*k + s goes to
 // row pos[a] = offset[e] + (number of assignments to e before a), where
 // group e starts at offset[e], a multiple of `align`; an expert index
-// outside [0, E) drops the assignment (pos -1).
+// outside [0, E) drops the assignment (pos -1).  Each kernel reads a token's
+// row once and is bound by the row traffic; the indices are small beside it.
 #include "mm_kernels.cuh"
+#include "pack.cuh"
 
 namespace mm {
 
-constexpr int kPmThreads = 256;
+constexpr int kPmThreads = 512;         // sort and copy: two blocks an SM
+constexpr int kPmWarps = kPmThreads / 32;
+constexpr int kPmRowThreads = 256;      // combine and its gradient
 
-__device__ __forceinline__ float pm_load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float pm_load(const float* p) { return *p; }
-__device__ __forceinline__ void pm_store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void pm_store(float* p, float v) { *p = v; }
-
-// One block: counts, offsets, then the ranks 32 assignments at a time.
-__global__ void __launch_bounds__(kPmThreads) permute_sort_kernel(const PermuteArgs a) {
-  pdl_enter();
-  __shared__ int cnt[MM_MAX_EXPERTS], run[MM_MAX_EXPERTS];
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int64_t na = a.T * a.k;
-  for (int e = tid; e < a.E; e += kPmThreads) cnt[e] = 0;
-  __syncthreads();
-  for (int64_t i = tid; i < na; i += kPmThreads) {
-    const int e = a.topk_idx[i];
-    if (e >= 0 && e < a.E) atomicAdd(&cnt[e], 1);
-  }
-  __syncthreads();
-  if (tid == 0) {
-    int off = 0;
-    for (int e = 0; e < a.E; ++e) {
-      a.offsets[e] = off;
-      a.counts[e] = cnt[e];
-      run[e] = off;
-      off += (cnt[e] + a.align - 1) / a.align * a.align;
-    }
-    a.offsets[a.E] = off;
-  }
-  __syncthreads();
-  for (int64_t r = tid; r < a.rows; r += kPmThreads) a.perm[r] = -1;
-  __syncthreads();
-  if (tid < 32) {
-    for (int64_t base = 0; base < na; base += 32) {
-      const int64_t i = base + lane;
-      int e = i < na ? a.topk_idx[i] : -1;
-      const bool valid = e >= 0 && e < a.E;
-      e = valid ? e : MM_MAX_EXPERTS + lane;
-      const unsigned peers = __match_any_sync(0xffffffffu, e);
-      const unsigned below = peers & ((1u << lane) - 1u);
-      const int prior = valid ? run[e] : 0;
-      __syncwarp();
-      if (i < na) a.pos[i] = valid ? prior + __popc(below) : -1;
-      if (valid) {
-        a.perm[prior + __popc(below)] = static_cast<int32_t>(i);
-        if (below == 0u) run[e] = prior + __popc(peers);
-      }
-      __syncwarp();
-    }
-  }
-}
-
-// One block per row of the sorted tensor: a copy of its token's row, zeros
-// where the group is padded, nothing behind the last group.
-template <typename T>
-__global__ void __launch_bounds__(kPmThreads) permute_copy_kernel(const PermuteArgs a) {
-  pdl_enter();
-  const int64_t end = a.offsets[a.E];
-  for (int64_t r = blockIdx.x; r < end; r += gridDim.x) {
-    const int src = a.perm[r];
-    T* o = static_cast<T*>(a.xs) + r * a.H;
-    const T* x = static_cast<const T*>(a.x) + static_cast<int64_t>(src < 0 ? 0 : src / a.k) * a.H;
-    for (int h = threadIdx.x; h < a.H; h += kPmThreads) o[h] = src < 0 ? T(0.f) : x[h];
-  }
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kPmThreads) unpermute_kernel(const UnpermuteArgs a) {
-  pdl_enter();
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x)
-    for (int h = threadIdx.x; h < a.H; h += kPmThreads) {
-      float acc = 0.f;
-      for (int s = 0; s < a.k; ++s) {
-        const int64_t p = a.pos[t * a.k + s];
-        if (p < 0 || p >= a.rows) continue;
-        const float v = pm_load(static_cast<const T*>(a.ys) + p * a.H + h);
-        acc = a.w ? fmaf(a.w[t * a.k + s], v, acc) : acc + v;
-      }
-      pm_store(static_cast<T*>(a.y) + t * a.H + h, acc);
-    }
-}
-
-// Blocks [0, T): one token each; blocks [T, T + E): one group's padding.
-template <typename T>
-__global__ void __launch_bounds__(kPmThreads) unpermute_bwd_kernel(const UnpermuteBwdArgs a) {
-  pdl_enter();
-  __shared__ float red[kPmThreads / 32];
-  for (int64_t b = blockIdx.x; b < a.T + a.E; b += gridDim.x) {
-    if (b >= a.T) {
-      const int e = static_cast<int>(b - a.T);
-      int64_t r0 = static_cast<int64_t>(a.offsets[e]) + a.counts[e], r1 = a.offsets[e + 1];
-      if (r0 < 0) r0 = 0;
-      if (r1 > a.rows) r1 = a.rows;
-      for (int64_t i = r0 * a.H + threadIdx.x; i < r1 * a.H; i += kPmThreads)
-        static_cast<T*>(a.dys)[i] = T(0.f);
-      continue;
-    }
-    for (int s = 0; s < a.k; ++s) {
-      const int64_t i = b * a.k + s, p = a.pos[i];
-      const bool kept = p >= 0 && p < a.rows;
-      const float w = a.w ? a.w[i] : 1.f;
-      float dot = 0.f;
-      if (kept)
-        for (int h = threadIdx.x; h < a.H; h += kPmThreads) {
-          const float g = pm_load(static_cast<const T*>(a.dy) + b * a.H + h);
-          if (a.dw) dot = fmaf(g, pm_load(static_cast<const T*>(a.ys) + p * a.H + h), dot);
-          pm_store(static_cast<T*>(a.dys) + p * a.H + h, w * g);
-        }
-      if (a.dw == nullptr) continue;
+// Calls f(row) for the padding rows of every group, shared out over the grid's
+// warps (this one is w of n); the whole warp calls.  Rows are kept inside
+// [0, rows) whatever the tables hold.
+template <typename F>
+__device__ __forceinline__ void each_padding_row(const int32_t* offsets, const int32_t* counts, int E,
+                                                 int64_t rows, int64_t w, int64_t n, F&& f) {
+  const int lane = threadIdx.x & 31;
+  // lane l holds groups l and l + 32: first padding row, rows before and behind it in the count
+  int first[2], from[2], to[2], total = 0;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      __syncthreads();
-      if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = dot;
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        float sum = 0.f;
-        for (int q = 0; q < kPmThreads / 32; ++q) sum += red[q];
-        a.dw[i] = sum;
+  for (int i = 0; i < 2; ++i) {
+    const int e = lane + 32 * i;
+    int num = 0;
+    first[i] = 0;
+    if (e < E) {
+      int64_t p0 = static_cast<int64_t>(offsets[e]) + counts[e], p1 = offsets[e + 1];
+      p0 = p0 < 0 ? 0 : p0;
+      p1 = p1 > rows ? rows : p1;
+      first[i] = static_cast<int>(p0);
+      num = p1 > p0 ? static_cast<int>(p1 - p0) : 0;
+    }
+    int sum = num;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += up;
+    }
+    to[i] = total + sum;
+    from[i] = to[i] - num;
+    total += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  for (int64_t p = w; p < total; p += n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const unsigned hit = __ballot_sync(0xffffffffu, p >= from[i] && p < to[i]);
+      if (hit == 0) continue;
+      const int src = __ffs(hit) - 1;
+      f(static_cast<int64_t>(__shfl_sync(0xffffffffu, first[i], src)) + (p - __shfl_sync(0xffffffffu, from[i], src)));
+    }
+}
+static_assert(MM_MAX_EXPERTS <= 64, "each_padding_row: two groups a lane");
+
+// Assignments to each expert among [first, first + num) of topk_idx, added to
+// cnt in shared memory: one add per warp and expert.
+__device__ __forceinline__ void count_experts(const int32_t* topk_idx, int64_t first, int64_t num, int E,
+                                              int* cnt) {
+  const int lane = threadIdx.x & 31;
+  for (int64_t i = threadIdx.x; i - lane < num; i += blockDim.x) {
+    const int e = i < num ? topk_idx[first + i] : -1;
+    const bool valid = e >= 0 && e < E;
+    const unsigned peers = __match_any_sync(0xffffffffu, valid ? e : -1);
+    if (valid && lane == __ffs(peers) - 1) atomicAdd(&cnt[e], __popc(peers));
+  }
+}
+
+// counts [E][nblk]: the block's assignments per expert.
+__global__ void __launch_bounds__(128) permute_count_kernel(const PermuteArgs a, int tokens, int32_t* blk_cnt) {
+  pdl_enter();
+  __shared__ int cnt[MM_MAX_EXPERTS];
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) cnt[e] = 0;
+  __syncthreads();
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens;
+  const int64_t nt = a.T - t0 < tokens ? a.T - t0 : tokens;
+  count_experts(a.topk_idx, t0 * a.k, nt * a.k, a.E, cnt);
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) blk_cnt[e * gridDim.x + blockIdx.x] = cnt[e];
+}
+
+// Block b owns the assignments of `tokens` tokens from b * tokens on.  It
+// works out its own base in every group - from the blocks' counts, or
+// (blk_cnt null: few assignments) by counting all of them itself, which
+// saves a launch - then its assignments' ranks, and copies its rows, a warp
+// per token: one load, a store for each of the token's assignments.  The
+// rows are asked for (to L2) before the indices are worked out.
+template <typename Vec>
+__global__ void __launch_bounds__(kPmThreads, 2)
+permute_kernel(const PermuteArgs a, int tokens, const int32_t* blk_cnt, int row_bytes) {
+  __shared__ int s_tot[MM_MAX_EXPERTS], s_next[MM_MAX_EXPERTS], s_off[MM_MAX_EXPERTS + 1];
+  __shared__ int s_warp[kPmWarps][MM_MAX_EXPERTS];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens;
+  const int64_t nt = a.T - t0 < tokens ? a.T - t0 : tokens;
+  const char* x = static_cast<const char*>(a.x) + t0 * row_bytes;
+  if (sizeof(Vec) == 16 && tid == 0) {
+    // at most 64 KB a block: 20 MB over the grid, well inside L2
+    const int64_t bytes = nt * row_bytes < 65536 ? nt * row_bytes : 65536;
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(x), "r"(static_cast<uint32_t>(bytes)) : "memory");
+  }
+  for (int e = tid; e < a.E; e += kPmThreads) s_tot[e] = s_next[e] = 0;
+  pdl_enter();
+  __syncthreads();
+  if (blk_cnt == nullptr) {
+    count_experts(a.topk_idx, 0, t0 * a.k, a.E, s_next);
+    count_experts(a.topk_idx, t0 * a.k, (a.T - t0) * a.k, a.E, s_tot);
+    __syncthreads();
+    for (int e = tid; e < a.E; e += kPmThreads) s_tot[e] += s_next[e];
+  } else {
+    for (int e = warp; e < a.E; e += kPmWarps) {
+      int all = 0, before = 0;
+      for (int b = lane; b < static_cast<int>(gridDim.x); b += 32) {
+        const int c = blk_cnt[e * gridDim.x + b];
+        all += c;
+        before += b < static_cast<int>(blockIdx.x) ? c : 0;
       }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+      }
+      if (lane == 0) {
+        s_tot[e] = all;
+        s_next[e] = before;
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {                            // offsets: a scan of the padded counts
+    int run = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + lane, own = e < a.E ? (s_tot[e] + a.align - 1) / a.align * a.align : 0;
+      int sum = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += up;
+      }
+      if (e < a.E) {
+        s_off[e] = run + sum - own;
+        s_next[e] += run + sum - own;         // the block's next row in the group
+      }
+      run += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) s_off[a.E] = run;
+  }
+  __syncthreads();
+  // ranks, one assignment a thread and round: within the warp, then the warps in order
+  for (int64_t base = 0; base < nt * a.k; base += kPmThreads) {
+    const int64_t i = base + tid;
+    int e = i < nt * a.k ? a.topk_idx[t0 * a.k + i] : -1;
+    const bool valid = e >= 0 && e < a.E;
+    const unsigned peers = __match_any_sync(0xffffffffu, valid ? e : -1);
+    const int rank = __popc(peers & ((1u << lane) - 1u));
+    for (int q = lane; q < a.E; q += 32) s_warp[warp][q] = 0;
+    __syncwarp();
+    if (valid && rank == 0) s_warp[warp][e] = __popc(peers);
+    __syncthreads();
+    int row = -1;
+    if (valid) {
+      row = s_next[e] + rank;
+      for (int w = 0; w < warp; ++w) row += s_warp[w][e];
+    }
+    if (i < nt * a.k) {
+      a.pos[t0 * a.k + i] = row;
+      if (valid) a.perm[row] = static_cast<int32_t>(t0 * a.k + i);
+    }
+    __syncthreads();
+    for (int q = tid; q < a.E; q += kPmThreads)
+      for (int w = 0; w < kPmWarps; ++w) s_next[q] += s_warp[w][q];
+    __syncthreads();
+  }
+  // rows
+  const int nv = row_bytes / static_cast<int>(sizeof(Vec));
+  constexpr int kBatch = 4;
+  for (int64_t t = warp; t < nt; t += kPmWarps) {
+    const int my = lane < a.k ? a.pos[(t0 + t) * a.k + lane] : -1;      // the block's own writes
+    const Vec* src = reinterpret_cast<const Vec*>(x + t * row_bytes);
+    for (int c0 = 0; c0 < nv; c0 += 32 * kBatch) {      // the whole warp stays: it shares `my`
+      const int c = c0 + lane;
+      Vec v[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (c + 32 * i < nv) v[i] = src[c + 32 * i];
+      for (int s = 0; s < a.k; ++s) {
+        const int64_t row = __shfl_sync(0xffffffffu, my, s);
+        if (row < 0) continue;
+        Vec* dst = reinterpret_cast<Vec*>(static_cast<char*>(a.xs) + row * row_bytes);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          if (c + 32 * i < nv) dst[c + 32 * i] = v[i];
+      }
+    }
+  }
+  if (blockIdx.x == 0) {
+    for (int e = tid; e <= a.E; e += kPmThreads) a.offsets[e] = s_off[e];
+    for (int e = tid; e < a.E; e += kPmThreads) a.counts[e] = s_tot[e];
+  }
+  const int64_t wg = static_cast<int64_t>(blockIdx.x) * kPmWarps + warp, nw = static_cast<int64_t>(gridDim.x) * kPmWarps;
+  if (a.align > 1)
+    each_padding_row(s_off, s_tot, a.E, a.rows, wg, nw, [&](int64_t row) {
+      Vec* dst = reinterpret_cast<Vec*>(static_cast<char*>(a.xs) + row * row_bytes);
+      for (int c = lane; c < nv; c += 32) dst[c] = Vec{};
+      if (lane == 0) a.perm[row] = -1;
+    });
+  for (int64_t r = s_off[a.E] + static_cast<int64_t>(blockIdx.x) * kPmThreads + tid; r < a.rows;
+       r += static_cast<int64_t>(gridDim.x) * kPmThreads)
+    a.perm[r] = -1;
+}
+
+__global__ void permute_empty_kernel(const PermuteArgs a) {
+  pdl_enter();
+  for (int e = threadIdx.x; e <= a.E; e += blockDim.x) a.offsets[e] = 0;
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.counts[e] = 0;
+}
+
+// y[t] = sum_s w ys[pos]: a warp per token; KP >= k rows of NB vectors a lane
+// are loaded before the first is added (in slot order).  A dropped assignment
+// is a row of zeros with weight 0, so nothing of it is read.
+template <typename T, int V, int KP, int NB>
+__global__ void __launch_bounds__(kPmRowThreads) unpermute_kernel(const UnpermuteArgs a) {
+  using P = Pack<T, V>;
+  pdl_enter();
+  const int lane = threadIdx.x & 31, nv = a.H / V;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kPmRowThreads / 32) + (threadIdx.x >> 5);
+  if (t >= a.T) return;
+  int64_t my = lane < a.k ? a.pos[t * a.k + lane] : -1;
+  if (my >= a.rows) my = -1;
+  const float my_w = my < 0 ? 0.f : a.w ? a.w[t * a.k + lane] : 1.f;
+  int64_t row[KP];
+  float w[KP];
+#pragma unroll
+  for (int s = 0; s < KP; ++s) {
+    row[s] = __shfl_sync(0xffffffffu, my, s);
+    w[s] = __shfl_sync(0xffffffffu, my_w, s);
+  }
+  for (int c = lane; c < nv; c += 32 * NB) {
+    typename P::Raw raw[KP][NB];
+#pragma unroll
+    for (int s = 0; s < KP; ++s)
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+        raw[s][i] = row[s] >= 0 && c + 32 * i < nv ? row_load<T, V>(a.ys, row[s] * a.H, c + 32 * i)
+                                                   : typename P::Raw{};
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      if (c + 32 * i >= nv) break;
+      float acc[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) acc[j] = 0.f;
+#pragma unroll
+      for (int s = 0; s < KP; ++s)
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] = fmaf(w[s], P::get(raw[s][i], j), acc[j]);
+      row_store<T, V>(a.y, t * a.H, c + 32 * i, acc);
     }
   }
 }
 
-static dim3 pm_grid(int64_t n) {
-  const int64_t most = static_cast<int64_t>(num_sms()) * 8;
-  return dim3(static_cast<unsigned>(n < most ? (n > 0 ? n : 1) : most));
+// dys[pos] = w dy, dw = <dy, ys[pos]>: a warp per token, dy read once.
+template <typename T, int V, int KP>
+__global__ void __launch_bounds__(kPmRowThreads) unpermute_bwd_kernel(const UnpermuteBwdArgs a) {
+  using P = Pack<T, V>;
+  pdl_enter();
+  const int lane = threadIdx.x & 31, nv = a.H / V;
+  constexpr int kWarps = kPmRowThreads / 32;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  if (t < a.T) {
+    int64_t my = lane < a.k ? a.pos[t * a.k + lane] : -1;
+    if (my >= a.rows) my = -1;
+    const float my_w = my >= 0 && a.w ? a.w[t * a.k + lane] : 1.f;
+    int64_t row[KP];
+    float w[KP], dot[KP];
+#pragma unroll
+    for (int s = 0; s < KP; ++s) {
+      row[s] = __shfl_sync(0xffffffffu, my, s);
+      w[s] = __shfl_sync(0xffffffffu, my_w, s);
+      dot[s] = 0.f;
+    }
+    for (int c = lane; c < nv; c += 32) {
+      const auto g = row_load<T, V>(a.dy, t * a.H, c);
+      typename P::Raw raw[KP];
+      if (a.dw)
+#pragma unroll
+        for (int s = 0; s < KP; ++s)
+          raw[s] = row[s] >= 0 ? row_load<T, V>(a.ys, row[s] * a.H, c) : typename P::Raw{};
+#pragma unroll
+      for (int s = 0; s < KP; ++s) {
+        if (row[s] < 0) continue;
+        float v[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          if (a.dw) dot[s] = fmaf(P::get(g, j), P::get(raw[s], j), dot[s]);
+          v[j] = w[s] * P::get(g, j);
+        }
+        row_store<T, V>(a.dys, row[s] * a.H, c, v);
+      }
+    }
+    if (a.dw) {
+      float mine = 0.f;
+#pragma unroll
+      for (int s = 0; s < KP; ++s) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) dot[s] += __shfl_xor_sync(0xffffffffu, dot[s], o);
+        if (lane == s) mine = dot[s];
+      }
+      if (lane < a.k) a.dw[t * a.k + lane] = mine;
+    }
+  }
+  each_padding_row(a.offsets, a.counts, a.E, a.rows, t, static_cast<int64_t>(gridDim.x) * kWarps, [&](int64_t r) {
+    float zero[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) zero[j] = 0.f;
+    for (int c = lane; c < nv; c += 32) row_store<T, V>(a.dys, r * a.H, c, zero);
+  });
 }
+
+// ----------------------------------------------------------------- launches
+// Two blocks an SM at most, and at least a token for each of a block's warps.
+static int pm_blocks(int64_t T) {
+  const int64_t most = 2 * static_cast<int64_t>(num_sms()), want = (T + kPmWarps - 1) / kPmWarps;
+  return static_cast<int>(want < most ? (want > 0 ? want : 1) : most);
+}
+// Up to this many assignments every block counts all of them itself.
+constexpr int64_t kPmCountOwn = 4096;
 
 size_t permute_bytes(int64_t T, int E, int k) {
-  (void)T;
-  (void)E;
-  (void)k;
-  return 0;
+  return T * k <= kPmCountOwn ? 0 : 4 * static_cast<size_t>(E) * pm_blocks(T);
 }
 
-cudaError_t launch_permute_sort(const PermuteArgs& a, cudaStream_t st) {
-  return launch_dependent_kernel(permute_sort_kernel, dim3(1), dim3(kPmThreads), 0, st, a);
+int permute_launches(int64_t T, int k) { return T * k <= kPmCountOwn ? 1 : 2; }
+
+static int pm_tokens(const PermuteArgs& a) {
+  const int b = pm_blocks(a.T);
+  return static_cast<int>((a.T + b - 1) / b);
 }
-cudaError_t launch_permute_copy(int dtype, const PermuteArgs& a, cudaStream_t st) {
+// Blocks that own a token (the last of pm_blocks may be left without).
+static dim3 pm_grid(const PermuteArgs& a) {
+  return dim3(static_cast<unsigned>((a.T + pm_tokens(a) - 1) / pm_tokens(a)));
+}
+
+cudaError_t launch_permute_count(const PermuteArgs& a, cudaStream_t st) {
+  return launch_dependent_kernel(permute_count_kernel, pm_grid(a), dim3(128), 0, st, a, pm_tokens(a),
+                                 static_cast<int32_t*>(a.scratch));
+}
+
+cudaError_t launch_permute(int dtype, const PermuteArgs& a, cudaStream_t st) {
+  if (a.T == 0) return launch_dependent_kernel(permute_empty_kernel, dim3(1), dim3(128), 0, st, a);
+  const int row_bytes = a.H * (dtype == kDtypeBF16 ? 2 : 4);
+  const int32_t* cnt = permute_launches(a.T, a.k) > 1 ? static_cast<const int32_t*>(a.scratch) : nullptr;
   auto run = [&](auto kern) {
-    return launch_dependent_kernel(kern, pm_grid(a.rows), dim3(kPmThreads), 0, st, a);
+    return launch_dependent_kernel(kern, pm_grid(a), dim3(kPmThreads), 0, st, a, pm_tokens(a), cnt,
+                                   row_bytes);
   };
-  return dtype == kDtypeBF16 ? run(permute_copy_kernel<__nv_bfloat16>) : run(permute_copy_kernel<float>);
+  if (row_bytes % 16 == 0) return run(permute_kernel<uint4>);
+  if (row_bytes % 4 == 0) return run(permute_kernel<uint32_t>);
+  return run(permute_kernel<uint16_t>);
+}
+
+static inline int pm_kp(int k) { return k <= 1 ? 1 : k <= 2 ? 2 : k <= 4 ? 4 : 8; }
+static unsigned pm_row_blocks(int64_t T) {
+  return static_cast<unsigned>((T + kPmRowThreads / 32 - 1) / (kPmRowThreads / 32));
+}
+
+template <typename T, int V>
+static cudaError_t unpermute_pick(const UnpermuteArgs& a, cudaStream_t st) {
+  auto run = [&](auto kern) {
+    return launch_dependent_kernel(kern, dim3(pm_row_blocks(a.T)), dim3(kPmRowThreads), 0, st, a);
+  };
+  switch (pm_kp(a.k)) {
+    case 1: return run(unpermute_kernel<T, V, 1, 4>);
+    case 2: return run(unpermute_kernel<T, V, 2, 4>);
+    case 4: return run(unpermute_kernel<T, V, 4, 2>);
+    default: return run(unpermute_kernel<T, V, 8, 1>);
+  }
 }
 cudaError_t launch_unpermute(int dtype, const UnpermuteArgs& a, cudaStream_t st) {
+  if (dtype == kDtypeBF16) {
+    if (a.H % 8 == 0) return unpermute_pick<__nv_bfloat16, 8>(a, st);
+    if (a.H % 2 == 0) return unpermute_pick<__nv_bfloat16, 2>(a, st);
+    return unpermute_pick<__nv_bfloat16, 1>(a, st);
+  }
+  return a.H % 4 == 0 ? unpermute_pick<float, 4>(a, st) : unpermute_pick<float, 1>(a, st);
+}
+
+template <typename T, int V>
+static cudaError_t unpermute_bwd_pick(const UnpermuteBwdArgs& a, cudaStream_t st) {
   auto run = [&](auto kern) {
-    return launch_dependent_kernel(kern, pm_grid(a.T), dim3(kPmThreads), 0, st, a);
+    return launch_dependent_kernel(kern, dim3(pm_row_blocks(a.T)), dim3(kPmRowThreads), 0, st, a);
   };
-  return dtype == kDtypeBF16 ? run(unpermute_kernel<__nv_bfloat16>) : run(unpermute_kernel<float>);
+  switch (pm_kp(a.k)) {
+    case 1: return run(unpermute_bwd_kernel<T, V, 1>);
+    case 2: return run(unpermute_bwd_kernel<T, V, 2>);
+    case 4: return run(unpermute_bwd_kernel<T, V, 4>);
+    default: return run(unpermute_bwd_kernel<T, V, 8>);
+  }
 }
 cudaError_t launch_unpermute_bwd(int dtype, const UnpermuteBwdArgs& a, cudaStream_t st) {
-  auto run = [&](auto kern) {
-    return launch_dependent_kernel(kern, pm_grid(a.T + a.E), dim3(kPmThreads), 0, st, a);
-  };
-  return dtype == kDtypeBF16 ? run(unpermute_bwd_kernel<__nv_bfloat16>) : run(unpermute_bwd_kernel<float>);
+  if (dtype == kDtypeBF16) {
+    if (a.H % 8 == 0) return unpermute_bwd_pick<__nv_bfloat16, 8>(a, st);
+    if (a.H % 2 == 0) return unpermute_bwd_pick<__nv_bfloat16, 2>(a, st);
+    return unpermute_bwd_pick<__nv_bfloat16, 1>(a, st);
+  }
+  return a.H % 4 == 0 ? unpermute_bwd_pick<float, 4>(a, st) : unpermute_bwd_pick<float, 1>(a, st);
 }
 
 }  // namespace mm
