@@ -3,161 +3,357 @@
 // shares a power of two: e is the least integer >= -126 with amax <= 448 2^e
 // over the group's finite values, code = e4m3(x 2^-e), round to nearest even.
 // The scaling is exact, so the codes do not depend on how they are computed.
-// One lane per column, one warp per group.
+//
+// All kernels stream: each input is read and each output written once.  A
+// thread owns V consecutive columns (V / 32 of a group), always the same ones
+// of a row, and walks down the rows; V is the widest of 16, 8 and 4 that
+// divides the width (so that values and codes move in whole aligned
+// accesses), else 1.
 #include "mm_kernels.cuh"
 
 namespace mm {
 
-constexpr int kCkThreads = 256;
-constexpr int kCkWarps = kCkThreads / 32;
+constexpr int kCkThreads = 512;         // most threads of a block
 
-__device__ __forceinline__ float ck_load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float ck_load(const float* p) { return *p; }
-__device__ __forceinline__ void ck_store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void ck_store(float* p, float v) { *p = v; }
-
-// |v| of a finite value, 0 for an infinity or a NaN.
-__device__ __forceinline__ float ck_finite_abs(float v) {
-  const float a = fabsf(v);
-  return a <= 3.402823466e38f ? a : 0.f;
-}
-// Biased exponent e + 127 of a group with the given finite amax: amax = 1.m 2^p
-// and 448 = 1.75 * 2^8.
-__device__ __forceinline__ int ck_exponent(float amax) {
-  const uint32_t b = __float_as_uint(amax);
-  const int e = static_cast<int>(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
-  return (e < -126 ? -126 : e) + 127;
-}
-__device__ __forceinline__ float ck_scale(int biased) { return __uint_as_float(static_cast<uint32_t>(biased) << 23); }
-__device__ __forceinline__ float ck_inv_scale(int biased) {
-  return __uint_as_float(static_cast<uint32_t>(254 - biased) << 23);
-}
-// Two values to e4m3 (lo in the low byte); an infinity becomes a NaN.
-__device__ __forceinline__ uint16_t ck_encode2(float lo, float hi) {
-  uint16_t r;
-  const float nan = __uint_as_float(0x7fffffffu);
-  lo = fabsf(lo) <= 3.402823466e38f ? lo : nan;
-  hi = fabsf(hi) <= 3.402823466e38f ? hi : nan;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float2 ck_decode2(uint16_t c) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
-  return f16x2_to_f32x2(h);
-}
-
-// One group: lane's value to its code; returns the group's biased exponent.
-__device__ __forceinline__ int ck_group(float v, uint8_t& code) {
-  float amax = ck_finite_abs(v);
+// V elements of T as 32-bit words (V = 1 of bf16: the low half of one).
+template <typename T, int V>
+struct Words {
+  static constexpr int kBytes = V * static_cast<int>(sizeof(T));
+  static constexpr int kN = (kBytes + 3) / 4;
+  uint32_t w[kN];
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const int e = ck_exponent(amax);
-  code = static_cast<uint8_t>(ck_encode2(v * ck_inv_scale(e), 0.f) & 0xff);
+    for (int i = 0; i < kN; ++i) w[i] = 0;
+  }
+  __device__ __forceinline__ void load(const void* p) {
+    if constexpr (kBytes >= 16) {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i) {
+        const uint4 q = static_cast<const uint4*>(p)[i];
+        w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
+      }
+    } else if constexpr (kBytes == 8) {
+      const uint2 q = *static_cast<const uint2*>(p);
+      w[0] = q.x; w[1] = q.y;
+    } else if constexpr (kBytes == 4) {
+      w[0] = *static_cast<const uint32_t*>(p);
+    } else if constexpr (kBytes == 2) {
+      w[0] = *static_cast<const uint16_t*>(p);
+    } else {
+      w[0] = *static_cast<const uint8_t*>(p);
+    }
+  }
+  __device__ __forceinline__ void store(void* p) const {
+    if constexpr (kBytes >= 16) {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i)
+        static_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    } else if constexpr (kBytes == 8) {
+      *static_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else if constexpr (kBytes == 4) {
+      *static_cast<uint32_t*>(p) = w[0];
+    } else if constexpr (kBytes == 2) {
+      *static_cast<uint16_t*>(p) = static_cast<uint16_t>(w[0]);
+    } else {
+      *static_cast<uint8_t*>(p) = static_cast<uint8_t>(w[0]);
+    }
+  }
+  __device__ __forceinline__ float get(int j) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
+    return __uint_as_float((j & 1) ? (w[j / 2] & 0xffff0000u) : (w[j / 2] << 16));
+  }
+  __device__ __forceinline__ void put(const float (&v)[V]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) w[j] = __float_as_uint(v[j]);
+    } else if constexpr (V == 1) {
+      w[0] = pack_bf16x2(v[0], 0.f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; j += 2) w[j / 2] = pack_bf16x2(v[j], v[j + 1]);
+    }
+  }
+  // The largest |value| as the bits of an fp32; infinities and NaN order above.
+  __device__ __forceinline__ uint32_t abs_max_bits() const {
+    uint32_t m = 0;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) m = max(m, w[i] & 0x7fffffffu);
+      return m;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        asm("max.u16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(w[i] & 0x7fff7fffu));
+      return max(m << 16, m & 0xffff0000u);
+    }
+  }
+};
+typedef uint8_t Code;
+
+__device__ __forceinline__ float ck_scale(uint32_t biased) { return __uint_as_float(biased << 23); }
+
+// Biased exponent e + 127 of a group with the given finite amax (fp32 bits):
+// amax = 1.m 2^p and 448 = 1.75 * 2^8.
+__device__ __forceinline__ uint32_t ck_exponent(uint32_t amax) {
+  const int e = static_cast<int>(amax >> 23) - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return e < 1 ? 1u : static_cast<uint32_t>(e);
+}
+
+template <int V>
+__device__ __forceinline__ uint32_t group_max(uint32_t m) {
+#pragma unroll
+  for (int o = 1; o < 32 / V; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
+// Codes of the thread's V values and its group's biased exponent.  The whole
+// warp calls.  An infinity or a NaN gets a NaN code and no say in the scale.
+template <typename T, int V>
+__device__ __forceinline__ uint32_t ck_encode(const Words<T, V>& x, Words<Code, V>& codes) {
+  uint32_t amax = group_max<V>(x.abs_max_bits());
+  const bool odd = __any_sync(0xffffffffu, amax >= 0x7f800000u);
+  if (odd) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const uint32_t b = __float_as_uint(x.get(j)) & 0x7fffffffu;
+      m = max(m, b < 0x7f800000u ? b : 0u);
+    }
+    amax = group_max<V>(m);
+  }
+  const uint32_t e = ck_exponent(amax);
+  const float inv = ck_scale(254u - e);
+  uint16_t c[(V + 1) / 2];
+#pragma unroll
+  for (int j = 0; j < V; j += 2) {
+    float lo = x.get(j) * inv, hi = j + 1 < V ? x.get(j + 1) * inv : 0.f;
+    if (odd) {
+      const float nan = __uint_as_float(0x7fffffffu);
+      lo = fabsf(x.get(j)) <= 3.402823466e38f ? lo : nan;
+      if (j + 1 < V) hi = fabsf(x.get(j + 1)) <= 3.402823466e38f ? hi : nan;
+    }
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c[j / 2]) : "f"(hi), "f"(lo));
+  }
+  if constexpr (V >= 4) {
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) codes.w[i] = c[2 * i] | (static_cast<uint32_t>(c[2 * i + 1]) << 16);
+  } else {
+    codes.w[0] = c[0] & 0xffu;
+  }
   return e;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kCkThreads) checkpoint_pack_kernel(const CheckpointArgs a) {
-  pdl_enter();
-  const int lane = threadIdx.x & 31;
-  const int64_t G = (a.C + 31) / 32, n = a.R * G;
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(kCkWarps) + (threadIdx.x >> 5); i < n;
-       i += static_cast<int64_t>(gridDim.x) * kCkWarps) {
-    const int64_t row = i / G, c = (i % G) * 32 + lane;
-    const float v = c < a.C ? ck_load(static_cast<const T*>(a.x) + row * a.C + c) : 0.f;
-    uint8_t code;
-    const int e = ck_group(v, code);
-    if (c < a.C) a.codes[row * a.C + c] = code;
-    if (lane == 0) a.exps[i] = static_cast<uint8_t>(e);
+template <int V>
+__device__ __forceinline__ void ck_decode(const Words<Code, V>& codes, float scale, float (&v)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; j += 2) {
+    const uint16_t c = static_cast<uint16_t>(codes.w[j / 4] >> (8 * (j % 4)));
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+    const float2 f = f16x2_to_f32x2(h);
+    v[j] = f.x * scale;
+    if (j + 1 < V) v[j + 1] = f.y * scale;
   }
 }
 
+// t = exp(-|g|) and 1 / (1 + t), from which sigma(g) and 1 - sigma(g) follow
+// without cancellation for either sign.  (The fast exponential would lose
+// seven bits at g = -80; the fast division, 2 ulp, is enough for bf16.)
 template <typename T>
-__global__ void __launch_bounds__(kCkThreads) checkpoint_unpack_kernel(const CheckpointArgs a) {
-  pdl_enter();
-  const int lane = threadIdx.x & 31;
-  const int64_t G = (a.C + 31) / 32, n = a.R * G;
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(kCkWarps) + (threadIdx.x >> 5); i < n;
-       i += static_cast<int64_t>(gridDim.x) * kCkWarps) {
-    const int64_t row = i / G, c = (i % G) * 32 + lane;
-    if (c < a.C)
-      ck_store(static_cast<T*>(a.x_out) + row * a.C + c,
-               ck_decode2(a.codes[row * a.C + c]).x * ck_scale(a.exps[i]));
+__device__ __forceinline__ void sigmoid_parts(float g, float& sig, float& rest) {
+  const float t = expf(-fabsf(g));
+  const float s = sizeof(T) == 2 ? __fdividef(1.0f, 1.0f + t) : 1.0f / (1.0f + t);
+  const float ts = t * s;
+  sig = g >= 0.f ? s : ts;                    // a NaN g leaves NaN in t
+  rest = g >= 0.f ? ts : s;
+}
+
+// A block's threads cover `rpb` rows of `upr` units (of V columns, whole
+// groups), or a part of one row at a time.
+struct CkShape {
+  int upr;                    // units of a row: 32 / V for each group
+  int rpb;                    // rows of a block and step
+};
+
+// Calls body(row, first column, whether the columns are inside, its group's
+// place in the row, whether the thread writes the group's exponent) for the
+// thread's units; the whole block goes through the same number of steps.
+template <int V, typename F>
+__device__ __forceinline__ void each_unit(const CkShape& s, int64_t R, int64_t cols, F&& body) {
+  const int lrow = static_cast<int>(threadIdx.x) / s.upr;
+  const bool one = s.rpb > 1 || s.upr <= static_cast<int>(blockDim.x);
+  const int u0 = one ? static_cast<int>(threadIdx.x) - lrow * s.upr : static_cast<int>(threadIdx.x);
+  const bool mine = !one || lrow < s.rpb;
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * s.rpb; r0 < R; r0 += static_cast<int64_t>(gridDim.x) * s.rpb) {
+    const int64_t row = one ? r0 + lrow : r0;
+    for (int u = u0, left = s.upr; left > 0; u += blockDim.x, left -= blockDim.x) {
+      const int64_t c = static_cast<int64_t>(u) * V;
+      const bool unit = mine && row < R && u < s.upr;
+      body(row, c, unit && c < cols, u / (32 / V), unit && u % (32 / V) == 0);
+    }
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kCkThreads) swiglu_act_kernel(const SwigluActArgs a) {
+template <typename T, int V>
+__global__ void __launch_bounds__(kCkThreads) checkpoint_pack_kernel(const CheckpointArgs a, const CkShape s) {
   pdl_enter();
-  const int lane = threadIdx.x & 31;
-  int64_t R = a.R;
-  if (a.n_rows && *a.n_rows < R) R = *a.n_rows;
-  const int64_t I = a.I, G = (I + 31) / 32, n = R * G;
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(kCkWarps) + (threadIdx.x >> 5); i < n;
-       i += static_cast<int64_t>(gridDim.x) * kCkWarps) {
-    const int64_t row = i / G, q = i % G, c = q * 32 + lane;
-    const bool in = c < I;
-    const float g = in ? ck_load(static_cast<const T*>(a.gu) + row * 2 * I + c) : 0.f;
-    const float u = in ? ck_load(static_cast<const T*>(a.gu) + row * 2 * I + I + c) : 0.f;
-    if (in) ck_store(static_cast<T*>(a.h) + row * I + c, silu_f32(g) * u);
-    if (a.codes == nullptr) continue;
-    uint8_t cg, cu;
-    const int eg = ck_group(g, cg), eu = ck_group(u, cu);
+  const int64_t G = (a.C + 31) / 32;
+  each_unit<V>(s, a.R, a.C, [&](int64_t row, int64_t c, bool in, int g, bool lead) {
+    Words<T, V> x;
+    x.clear();
+    if (in) x.load(static_cast<const T*>(a.x) + row * a.C + c);
+    Words<Code, V> codes;
+    const uint32_t e = ck_encode<T, V>(x, codes);
+    if (in) codes.store(a.codes + row * a.C + c);
+    if (lead) a.exps[row * G + g] = static_cast<uint8_t>(e);
+  });
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kCkThreads) checkpoint_unpack_kernel(const CheckpointArgs a, const CkShape s) {
+  pdl_enter();
+  const int64_t G = (a.C + 31) / 32;
+  each_unit<V>(s, a.R, a.C, [&](int64_t row, int64_t c, bool in, int g, bool) {
+    if (!in) return;
+    Words<Code, V> codes;
+    codes.load(a.codes + row * a.C + c);
+    float v[V];
+    ck_decode<V>(codes, ck_scale(a.exps[row * G + g]), v);
+    Words<T, V> x;
+    x.put(v);
+    x.store(static_cast<T*>(a.x_out) + row * a.C + c);
+  });
+}
+
+__device__ __forceinline__ int64_t act_rows(const SwigluActArgs& a) {
+  return a.n_rows && *a.n_rows < a.R ? *a.n_rows : a.R;
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kCkThreads) swiglu_act_kernel(const SwigluActArgs a, const CkShape s) {
+  pdl_enter();
+  const int64_t I = a.I, G = (I + 31) / 32;
+  each_unit<V>(s, act_rows(a), I, [&](int64_t row, int64_t c, bool in, int grp, bool lead) {
+    Words<T, V> g, u;
+    g.clear();
+    u.clear();
+    const T* src = static_cast<const T*>(a.gu) + row * 2 * I + c;
     if (in) {
-      a.codes[row * 2 * I + c] = cg;
-      a.codes[row * 2 * I + I + c] = cu;
+      g.load(src);
+      u.load(src + I);
+      float h[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        float sig, rest;
+        sigmoid_parts<T>(g.get(j), sig, rest);
+        h[j] = g.get(j) * sig * u.get(j);
+      }
+      Words<T, V> out;
+      out.put(h);
+      out.store(static_cast<T*>(a.h) + row * I + c);
     }
-    if (lane == 0) {
-      a.exps[row * 2 * G + q] = static_cast<uint8_t>(eg);
-      a.exps[row * 2 * G + G + q] = static_cast<uint8_t>(eu);
+    if (a.codes == nullptr) return;
+    Words<Code, V> cg, cu;
+    const uint32_t eg = ck_encode<T, V>(g, cg), eu = ck_encode<T, V>(u, cu);
+    if (in) {
+      cg.store(a.codes + row * 2 * I + c);
+      cu.store(a.codes + row * 2 * I + I + c);
     }
-  }
+    if (lead) {
+      a.exps[row * 2 * G + grp] = static_cast<uint8_t>(eg);
+      a.exps[row * 2 * G + G + grp] = static_cast<uint8_t>(eu);
+    }
+  });
 }
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kCkThreads) swiglu_act_bwd_kernel(const SwigluActArgs a, const CkShape s) {
+  pdl_enter();
+  const int64_t I = a.I, G = (I + 31) / 32;
+  each_unit<V>(s, act_rows(a), I, [&](int64_t row, int64_t c, bool in, int grp, bool) {
+    if (!in) return;
+    Words<Code, V> cg, cu;
+    Words<T, V> dh;
+    cg.load(a.codes + row * 2 * I + c);
+    cu.load(a.codes + row * 2 * I + I + c);
+    dh.load(static_cast<const T*>(a.dh) + row * I + c);
+    const float sg = ck_scale(a.exps[row * 2 * G + grp]), su = ck_scale(a.exps[row * 2 * G + G + grp]);
+    float g[V], u[V];
+    ck_decode<V>(cg, sg, g);
+    ck_decode<V>(cu, su, u);
+    float dg[V], du[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      float sig, rest;
+      sigmoid_parts<T>(g[j], sig, rest);
+      const float d = dh.get(j), silu = g[j] * sig;
+      dg[j] = d * u[j] * (sig * fmaf(g[j], rest, 1.0f));
+      du[j] = d * silu;
+      u[j] *= silu;
+    }
+    Words<T, V> out;
+    out.put(dg);
+    out.store(static_cast<T*>(a.dgu) + row * 2 * I + c);
+    out.put(du);
+    out.store(static_cast<T*>(a.dgu) + row * 2 * I + I + c);
+    if (a.h) {
+      out.put(u);
+      out.store(static_cast<T*>(a.h) + row * I + c);
+    }
+  });
+}
+
+// ----------------------------------------------------------------- launches
+// Blocks of about 256 threads (whole rows where a row has fewer units), and a
+// few of them an SM: as many as 1536 threads make.
+template <typename A>
+static cudaError_t ck_launch(void (*kern)(A, CkShape), const A& a, int64_t R, int64_t cols, int V, cudaStream_t st) {
+  const int upr = static_cast<int>((cols + 31) / 32) * (32 / V);
+  CkShape s{upr, upr >= 256 ? 1 : 256 / upr};
+  const int64_t want = static_cast<int64_t>(s.rpb) * upr;
+  const int threads = want >= kCkThreads ? kCkThreads : static_cast<int>((want + 31) / 32 * 32);
+  const int64_t blocks = (R + s.rpb - 1) / s.rpb, most = static_cast<int64_t>(num_sms()) * (1536 / threads);
+  return launch_dependent_kernel(kern, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(threads), 0,
+                                 st, a, s);
+}
+
+static inline int ck_vec(int64_t cols) { return cols % 16 == 0 ? 16 : cols % 8 == 0 ? 8 : cols % 4 == 0 ? 4 : 1; }
 
 template <typename T>
-__global__ void __launch_bounds__(kCkThreads) swiglu_act_bwd_kernel(const SwigluActArgs a) {
-  pdl_enter();
-  const int lane = threadIdx.x & 31;
-  int64_t R = a.R;
-  if (a.n_rows && *a.n_rows < R) R = *a.n_rows;
-  const int64_t I = a.I, G = (I + 31) / 32, n = R * G;
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(kCkWarps) + (threadIdx.x >> 5); i < n;
-       i += static_cast<int64_t>(gridDim.x) * kCkWarps) {
-    const int64_t row = i / G, q = i % G, c = q * 32 + lane;
-    if (c >= I) continue;
-    const float g = ck_decode2(a.codes[row * 2 * I + c]).x * ck_scale(a.exps[row * 2 * G + q]);
-    const float u = ck_decode2(a.codes[row * 2 * I + I + c]).x * ck_scale(a.exps[row * 2 * G + G + q]);
-    const float dh = ck_load(static_cast<const T*>(a.dh) + row * I + c);
-    const float sig = 1.0f / (1.0f + expf(-g));
-    const float silu = g * sig;
-    ck_store(static_cast<T*>(a.dgu) + row * 2 * I + c, dh * u * (sig * (1.0f + g * (1.0f - sig))));
-    ck_store(static_cast<T*>(a.dgu) + row * 2 * I + I + c, dh * silu);
-    if (a.h) ck_store(static_cast<T*>(a.h) + row * I + c, silu * u);
+static cudaError_t checkpoint_pick(bool pack, const CheckpointArgs& a, cudaStream_t st) {
+  const int V = ck_vec(a.C);
+  auto run = [&](void (*p)(CheckpointArgs, CkShape), void (*u)(CheckpointArgs, CkShape)) {
+    return ck_launch<CheckpointArgs>(pack ? p : u, a, a.R, a.C, V, st);
+  };
+  switch (V) {
+    case 16: return run(checkpoint_pack_kernel<T, 16>, checkpoint_unpack_kernel<T, 16>);
+    case 8: return run(checkpoint_pack_kernel<T, 8>, checkpoint_unpack_kernel<T, 8>);
+    case 4: return run(checkpoint_pack_kernel<T, 4>, checkpoint_unpack_kernel<T, 4>);
+    default: return run(checkpoint_pack_kernel<T, 1>, checkpoint_unpack_kernel<T, 1>);
   }
-}
-
-static dim3 ck_grid(int64_t groups) {
-  const int64_t most = static_cast<int64_t>(num_sms()) * 8, want = (groups + kCkWarps - 1) / kCkWarps;
-  return dim3(static_cast<unsigned>(want < most ? (want > 0 ? want : 1) : most));
 }
 
 cudaError_t launch_checkpoint(int dtype, bool pack, const CheckpointArgs& a, cudaStream_t st) {
-  auto run = [&](auto kern) {
-    return launch_dependent_kernel(kern, ck_grid(a.R * ((a.C + 31) / 32)), dim3(kCkThreads), 0, st, a);
+  return dtype == kDtypeBF16 ? checkpoint_pick<__nv_bfloat16>(pack, a, st) : checkpoint_pick<float>(pack, a, st);
+}
+
+template <typename T>
+static cudaError_t swiglu_act_pick(bool backward, const SwigluActArgs& a, cudaStream_t st) {
+  const int V = ck_vec(a.I);
+  auto run = [&](void (*f)(SwigluActArgs, CkShape), void (*b)(SwigluActArgs, CkShape)) {
+    return ck_launch<SwigluActArgs>(backward ? b : f, a, a.R, a.I, V, st);
   };
-  if (dtype == kDtypeBF16)
-    return pack ? run(checkpoint_pack_kernel<__nv_bfloat16>) : run(checkpoint_unpack_kernel<__nv_bfloat16>);
-  return pack ? run(checkpoint_pack_kernel<float>) : run(checkpoint_unpack_kernel<float>);
+  switch (V) {
+    case 16: return run(swiglu_act_kernel<T, 16>, swiglu_act_bwd_kernel<T, 16>);
+    case 8: return run(swiglu_act_kernel<T, 8>, swiglu_act_bwd_kernel<T, 8>);
+    case 4: return run(swiglu_act_kernel<T, 4>, swiglu_act_bwd_kernel<T, 4>);
+    default: return run(swiglu_act_kernel<T, 1>, swiglu_act_bwd_kernel<T, 1>);
+  }
 }
 
 cudaError_t launch_swiglu_act(int dtype, bool backward, const SwigluActArgs& a, cudaStream_t st) {
-  auto run = [&](auto kern) {
-    return launch_dependent_kernel(kern, ck_grid(a.R * ((a.I + 31) / 32)), dim3(kCkThreads), 0, st, a);
-  };
-  if (dtype == kDtypeBF16)
-    return backward ? run(swiglu_act_bwd_kernel<__nv_bfloat16>) : run(swiglu_act_kernel<__nv_bfloat16>);
-  return backward ? run(swiglu_act_bwd_kernel<float>) : run(swiglu_act_kernel<float>);
+  return dtype == kDtypeBF16 ? swiglu_act_pick<__nv_bfloat16>(backward, a, st)
+                             : swiglu_act_pick<float>(backward, a, st);
 }
 
 }  // namespace mm
