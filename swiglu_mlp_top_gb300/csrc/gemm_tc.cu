@@ -1048,6 +1048,17 @@ int num_sms() {
   return n;
 }
 
+int resident_blocks(const void* fn, int threads) {
+  static std::mutex mu;
+  static std::map<std::tuple<int, const void*, int>, int> known;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::lock_guard<std::mutex> lock(mu);
+  int& n = known[std::make_tuple(dev, fn, threads)];
+  if (n == 0 && cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, 0) != cudaSuccess) n = 0;
+  return n > 0 ? n : 1;
+}
+
 cudaError_t ensure_dynamic_smem(const void* fn, size_t bytes) {
   static std::mutex mu;
   static std::map<std::pair<int, const void*>, size_t> done;

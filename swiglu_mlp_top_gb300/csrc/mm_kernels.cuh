@@ -497,4 +497,8 @@ int num_sms();   // of the current device, looked up once per device
 // made during stream capture issue no attribute changes after the first).
 cudaError_t ensure_dynamic_smem(const void* fn, size_t bytes);
 
+// Blocks of `threads` threads (no dynamic shared memory) that an SM of the
+// current device holds at once, looked up once per kernel and block size.
+int resident_blocks(const void* fn, int threads);
+
 }  // namespace mm
