@@ -10,7 +10,6 @@ must be ordered before the call by the caller.
 """
 from __future__ import annotations
 
-import contextlib
 from typing import Optional
 
 import torch
@@ -30,20 +29,21 @@ def _begin(x, name: str, ndim: int, stream):
     dt = _DTYPES.get(x.dtype)
     if dt is None:
         raise ValueError(f"unsupported dtype {x.dtype}")
-    dev = x.device
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {dev}, the current device is cuda:{torch.cuda.current_device()}")
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return dt, dev, s.cuda_stream
+    dev = x.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    if stream is not None:
+        return dt, dev, stream.cuda_stream
+    return dt, dev, torch._C._cuda_getCurrentRawStream(dev)     # current_stream() builds an object: 3 us a call
 
 
-def _arg(t, name: str, dev, dtype, shape):
+def _arg(t, name: str, dev: int, dtype, shape):
     """Address of a tensor of exactly this dtype, shape and device (None: null)."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.device != dev:
-        raise ValueError(f"{name} must be a tensor on {dev}")
-    if t.dtype != dtype:
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise ValueError(f"{name} must be a tensor on cuda:{dev}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
@@ -52,20 +52,21 @@ def _arg(t, name: str, dev, dtype, shape):
     return t.data_ptr()
 
 
-def _on(stream):
-    """Where a call's own tensors are allocated: the pool of the stream that uses them."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _empty(shape, dtype, dev, stream):
+    """A tensor of the call's own, from the pool of the stream that uses it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _scratch(workspace, need: int, dev, name: str):
-    """(tensor, bytes): the caller's workspace, or a fresh one (no header state is needed)."""
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif not isinstance(workspace, torch.Tensor) or workspace.device != dev:
-        raise ValueError(f"workspace of {name} must be a tensor on {dev}")
-    elif not workspace.is_contiguous():
+def _scratch(workspace, dev: int, name: str):
+    """Address and bytes of a workspace."""
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev:
+        raise ValueError(f"workspace of {name} must be a tensor on cuda:{dev}")
+    if not workspace.is_contiguous():
         raise ValueError(f"workspace of {name} must be contiguous")
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 # ------------------------------------------------------------- block norms
@@ -75,6 +76,13 @@ def _norm_parts(dev, dtype, T, H, post_weight, gate, pre_weight):
     return (_arg(post_weight, "post_weight", dev, dtype, (H,)),
             _arg(gate, "gate", dev, dtype, (T, H) if per_token else (H,)),
             _arg(pre_weight, "pre_weight", dev, dtype, (H,)), per_token)
+
+
+def _stat(stats: dict, key: str, T: int, dev: int, stream):
+    t = stats.get(key)
+    if t is None:
+        t = stats[key] = _empty(T, torch.float32, dev, stream)
+    return _arg(t, key, dev, torch.float32, (T,))
 
 
 def block_norm(x: torch.Tensor, f: Optional[torch.Tensor] = None, *,
@@ -93,34 +101,32 @@ def block_norm(x: torch.Tensor, f: Optional[torch.Tensor] = None, *,
     rstd_post / rstd_pre [T] fp32, which block_norm_backward needs.
     """
     dt, dev, raw = _begin(x, "x", 2, stream)
-    T, H = x.shape
+    T, H = shape = x.shape
     dtype = x.dtype
-    px = _arg(x, "x", dev, dtype, (T, H))
-    pf = _arg(f, "f", dev, dtype, (T, H))
+    px = _arg(x, "x", dev, dtype, shape)
+    pf = _arg(f, "f", dev, dtype, shape)
     post, g, pre, per_token = _norm_parts(dev, dtype, T, H, post_weight, gate, pre_weight)
     if f is None and out is not None and out is not x:
         raise ValueError("out: without f, r is x itself")
     if pre_weight is None and normed is not None:
         raise ValueError("normed needs pre_weight")
-    with _on(stream):
-        if f is None:
-            out = x
-        elif out is None:
-            out = torch.empty_like(x)
-        if pre_weight is not None and normed is None:
-            normed = torch.empty_like(x)
-        rstd = [None, None]
-        if stats is not None:
-            for i, (key, w) in enumerate((("rstd_post", post_weight), ("rstd_pre", pre_weight))):
-                if w is None:
-                    continue
-                if stats.get(key) is None:
-                    stats[key] = torch.empty(T, dtype=torch.float32, device=dev)
-                rstd[i] = _arg(stats[key], key, dev, torch.float32, (T,))
+    if f is None:
+        out, pout = x, None
+    else:
+        if out is None:
+            out = _empty(shape, dtype, dev, stream)
+        pout = _arg(out, "out", dev, dtype, shape)
+    if pre_weight is not None and normed is None:
+        normed = _empty(shape, dtype, dev, stream)
+    post_rstd = pre_rstd = None
+    if stats is not None:
+        if post is not None:
+            post_rstd = _stat(stats, "rstd_post", T, dev, stream)
+        if pre is not None:
+            pre_rstd = _stat(stats, "rstd_pre", T, dev, stream)
     rc = L.load().mm_block_norm(
-        px, pf, post, g, per_token, pre, residual_scale, eps, T, H, dt,
-        None if f is None else _arg(out, "out", dev, dtype, (T, H)),
-        _arg(normed, "normed", dev, dtype, (T, H)), rstd[0], rstd[1], raw)
+        px, pf, post, g, per_token, pre, residual_scale, eps, T, H, dt, pout,
+        _arg(normed, "normed", dev, dtype, shape), post_rstd, pre_rstd, raw)
     L.check(rc, "mm_block_norm")
     return out, normed
 
@@ -143,43 +149,42 @@ def block_norm_backward(dn: Optional[torch.Tensor], dr: Optional[torch.Tensor],
     norm (r is its x)."""
     lead, name = (dn, "dn") if pre_weight is not None else (dr, "dr")
     dt, dev, raw = _begin(lead, name, 2, stream)
-    T, H = lead.shape
+    T, H = shape = lead.shape
     dtype = lead.dtype
     post, g, pre, per_token = _norm_parts(dev, dtype, T, H, post_weight, gate, pre_weight)
-    if f is None and (post_weight is not None or gate is not None or residual_scale != 1.0):
+    if f is None and (post is not None or g is not None or residual_scale != 1.0):
         raise ValueError("post_weight, gate and residual_scale need f")
     rstd = [None, None]
-    for i, (key, w) in enumerate((("rstd_post", post_weight), ("rstd_pre", pre_weight))):
+    for i, (key, w) in enumerate((("rstd_post", post), ("rstd_pre", pre))):
         if w is not None:
             if stats is None or stats.get(key) is None:
                 raise ValueError(f"stats must hold the forward's {key}")
             rstd[i] = _arg(stats[key], key, dev, torch.float32, (T,))
-    pdn = _arg(dn, "dn", dev, dtype, (T, H)) if pre_weight is not None else None
-    pr = _arg(r, "r", dev, dtype, (T, H)) if pre_weight is not None else None
-    pdr = _arg(dr, "dr", dev, dtype, (T, H))
-    pf = _arg(f, "f", dev, dtype, (T, H))
+    pdn = pr = None
+    if pre is not None:
+        pdn, pr = _arg(dn, "dn", dev, dtype, shape), _arg(r, "r", dev, dtype, shape)
+    pdr, pf = _arg(dr, "dr", dev, dtype, shape), _arg(f, "f", dev, dtype, shape)
     lib = L.load()
-    need = lib.mm_block_norm_backward_workspace_bytes(T, H, dt)
-    with _on(stream):
-        workspace, nbytes = _scratch(workspace, need, dev, "block_norm_backward")
-        out = {"dx": torch.empty_like(lead)}
-        if f is not None:
-            out["df"] = torch.empty_like(lead)
-        if post_weight is not None:
-            out["d_post_weight"] = torch.empty(H, dtype=torch.float32, device=dev)
-        if gate is not None:
-            out["d_gate"] = torch.empty((T, H) if per_token else (H,), device=dev,
-                                        dtype=dtype if per_token else torch.float32)
-        if pre_weight is not None:
-            out["d_pre_weight"] = torch.empty(H, dtype=torch.float32, device=dev)
-
-    def at(key):
-        return out[key].data_ptr() if key in out else None
-
+    if workspace is None:
+        workspace = _empty(lib.mm_block_norm_backward_workspace_bytes(T, H, dt), torch.uint8, dev, stream)
+    pws, nbytes = _scratch(workspace, dev, "block_norm_backward")
+    out = {"dx": _empty(shape, dtype, dev, stream)}
+    pdf = pdpost = pdgate = pdpre = None
+    if f is not None:
+        t = out["df"] = _empty(shape, dtype, dev, stream)
+        pdf = t.data_ptr()
+    if post is not None:
+        t = out["d_post_weight"] = _empty(H, torch.float32, dev, stream)
+        pdpost = t.data_ptr()
+    if g is not None:
+        t = out["d_gate"] = _empty(shape if per_token else H, dtype if per_token else torch.float32, dev, stream)
+        pdgate = t.data_ptr()
+    if pre is not None:
+        t = out["d_pre_weight"] = _empty(H, torch.float32, dev, stream)
+        pdpre = t.data_ptr()
     rc = lib.mm_block_norm_backward(
         pdn, pdr, pr, pf, post, g, per_token, pre, rstd[0], rstd[1], residual_scale, T, H, dt,
-        at("dx"), at("df"), at("d_post_weight"), at("d_gate"), at("d_pre_weight"),
-        workspace.data_ptr(), nbytes, raw)
+        out["dx"].data_ptr(), pdf, pdpost, pdgate, pdpre, pws, nbytes, raw)
     L.check(rc, "mm_block_norm_backward")
     return out
 
@@ -216,18 +221,18 @@ def moe_permute(x: torch.Tensor, topk_idx: torch.Tensor, E: int, *, align: int =
     if R < 0:
         raise L.MMError(L.MM_ERR_UNSUPPORTED, "mm_moe_permute")
     plan = {} if plan is None else plan
-    with _on(stream):
-        workspace, nbytes = _scratch(workspace, lib.mm_moe_permute_workspace_bytes(T, E, k), dev,
-                                     "moe_permute")
-        if out is None:
-            out = torch.empty(R, H, dtype=x.dtype, device=dev)
-        ptrs = []
-        for key, shape in (("offsets", (E + 1,)), ("counts", (E,)), ("perm", (R,)), ("pos", (T, k))):
-            if plan.get(key) is None:
-                plan[key] = torch.empty(shape, dtype=torch.int32, device=dev)
-            ptrs.append(_arg(plan[key], key, dev, torch.int32, shape))
+    if workspace is None:
+        workspace = _empty(lib.mm_moe_permute_workspace_bytes(T, E, k), torch.uint8, dev, stream)
+    pws, nbytes = _scratch(workspace, dev, "moe_permute")
+    if out is None:
+        out = _empty((R, H), x.dtype, dev, stream)
+    ptrs = []
+    for key, shape in (("offsets", (E + 1,)), ("counts", (E,)), ("perm", (R,)), ("pos", (T, k))):
+        if plan.get(key) is None:
+            plan[key] = _empty(shape, torch.int32, dev, stream)
+        ptrs.append(_arg(plan[key], key, dev, torch.int32, shape))
     rc = lib.mm_moe_permute(px, pi, T, H, E, k, align, dt, _arg(out, "out", dev, x.dtype, (R, H)),
-                            *ptrs, workspace.data_ptr(), nbytes, raw)
+                            *ptrs, pws, nbytes, raw)
     L.check(rc, "mm_moe_permute")
     return out, plan
 
@@ -241,8 +246,7 @@ def _combine(rows, name, plan, topk_w, out, stream):
     pp = _arg(pos, "pos", dev, torch.int32, (T, k))
     pw = _arg(topk_w, "topk_w", dev, torch.float32, (T, k))
     if out is None:
-        with _on(stream):
-            out = torch.empty(T, H, dtype=rows.dtype, device=dev)
+        out = _empty((T, H), rows.dtype, dev, stream)
     rc = L.load().mm_moe_unpermute(pr, pp, pw, T, H, k, R, dt,
                                    _arg(out, "out", dev, rows.dtype, (T, H)), raw)
     L.check(rc, "mm_moe_unpermute")
@@ -284,10 +288,9 @@ def moe_unpermute_backward(dy: torch.Tensor, ys: Optional[torch.Tensor], plan: d
             _arg(topk_w, "topk_w", dev, torch.float32, (T, k)),
             _arg(plan["offsets"], "offsets", dev, torch.int32, (E + 1,)),
             _arg(counts, "counts", dev, torch.int32, (E,)))
-    with _on(stream):
-        if out is None:
-            out = torch.empty(R, H, dtype=dy.dtype, device=dev)
-        dw = torch.empty(T, k, dtype=torch.float32, device=dev) if weighted else None
+    if out is None:
+        out = _empty((R, H), dy.dtype, dev, stream)
+    dw = _empty((T, k), torch.float32, dev, stream) if weighted else None
     rc = L.load().mm_moe_unpermute_backward(
         *args, T, H, E, k, R, dt, _arg(out, "out", dev, dy.dtype, (R, H)),
         dw.data_ptr() if weighted else None, raw)
@@ -307,9 +310,8 @@ def checkpoint_pack(x: torch.Tensor, *, stream=None) -> dict:
     dt, dev, raw = _begin(x, "x", 2, stream)
     R, C = x.shape
     px = _arg(x, "x", dev, x.dtype, (R, C))
-    with _on(stream):
-        codes = torch.empty(R, C, dtype=torch.float8_e4m3fn, device=dev)
-        exps = torch.empty(R, _groups(C), dtype=torch.uint8, device=dev)
+    codes = _empty((R, C), torch.float8_e4m3fn, dev, stream)
+    exps = _empty((R, _groups(C)), torch.uint8, dev, stream)
     rc = L.load().mm_checkpoint_pack(px, R, C, dt, codes.data_ptr(), exps.data_ptr(), raw)
     L.check(rc, "mm_checkpoint_pack")
     return {"codes": codes, "exps": exps, "segments": 1}
@@ -333,8 +335,7 @@ def checkpoint_unpack(checkpoint: dict, dtype: torch.dtype = torch.bfloat16, *,
     if dtype not in _DTYPES:
         raise ValueError(f"unsupported dtype {dtype}")
     if out is None:
-        with _on(stream):
-            out = torch.empty(R, seg * C, dtype=dtype, device=codes.device)
+        out = _empty((R, seg * C), dtype, codes.device, stream)
     dt, dev, raw = _begin(out, "out", 2, stream)
     rc = L.load().mm_checkpoint_unpack(
         _arg(codes, "codes", dev, torch.float8_e4m3fn, (R, seg * C)),
@@ -364,17 +365,16 @@ def swiglu_act(gu: torch.Tensor, *, checkpoint: Optional[dict] = None,
     pg = _arg(gu, "gu", dev, gu.dtype, (R, two_i))
     pr = _rows_arg(rows, dev)
     pc = pe = None
-    with _on(stream):
-        if out is None:
-            out = torch.empty(R, I, dtype=gu.dtype, device=dev)
-        if checkpoint is not None:
-            if checkpoint.get("codes") is None:
-                checkpoint["codes"] = torch.empty(R, two_i, dtype=torch.float8_e4m3fn, device=dev)
-            if checkpoint.get("exps") is None:
-                checkpoint["exps"] = torch.empty(R, 2 * _groups(I), dtype=torch.uint8, device=dev)
-            checkpoint["segments"] = 2
-            pc = _arg(checkpoint["codes"], "codes", dev, torch.float8_e4m3fn, (R, two_i))
-            pe = _arg(checkpoint["exps"], "exps", dev, torch.uint8, (R, 2 * _groups(I)))
+    if out is None:
+        out = _empty((R, I), gu.dtype, dev, stream)
+    if checkpoint is not None:
+        if checkpoint.get("codes") is None:
+            checkpoint["codes"] = _empty((R, two_i), torch.float8_e4m3fn, dev, stream)
+        if checkpoint.get("exps") is None:
+            checkpoint["exps"] = _empty((R, 2 * _groups(I)), torch.uint8, dev, stream)
+        checkpoint["segments"] = 2
+        pc = _arg(checkpoint["codes"], "codes", dev, torch.float8_e4m3fn, (R, two_i))
+        pe = _arg(checkpoint["exps"], "exps", dev, torch.uint8, (R, 2 * _groups(I)))
     rc = L.load().mm_swiglu_act(pg, R, I, dt, pr, _arg(out, "out", dev, gu.dtype, (R, I)), pc, pe, raw)
     L.check(rc, "mm_swiglu_act")
     return out
@@ -393,11 +393,10 @@ def swiglu_act_backward(checkpoint: dict, dh: torch.Tensor, *, want_h: bool = Tr
     pd = _arg(dh, "dh", dev, dh.dtype, (R, I))
     if not want_h and h_out is not None:
         raise ValueError("h_out needs want_h")
-    with _on(stream):
-        if out is None:
-            out = torch.empty(R, 2 * I, dtype=dh.dtype, device=dev)
-        if want_h and h_out is None:
-            h_out = torch.empty(R, I, dtype=dh.dtype, device=dev)
+    if out is None:
+        out = _empty((R, 2 * I), dh.dtype, dev, stream)
+    if want_h and h_out is None:
+        h_out = _empty((R, I), dh.dtype, dev, stream)
     rc = L.load().mm_swiglu_act_backward(
         _arg(codes, "codes", dev, torch.float8_e4m3fn, (R, 2 * I)),
         _arg(exps, "exps", dev, torch.uint8, (R, 2 * _groups(I))), pd, R, I, dt, _rows_arg(rows, dev),

@@ -985,9 +985,9 @@ int mm_block_norm_backward(const void* dn, const void* dr, const void* r, const 
     return MM_ERR_INVALID_ARG;
   }
   for (const void* q : {dn, dr, r, f, post_w, gate, pre_w, static_cast<const void*>(df),
-                        static_cast<const void*>(d_gate), static_cast<const void*>(d_post_w),
-                        static_cast<const void*>(d_pre_w)})
+                        static_cast<const void*>(token_gate ? d_gate : nullptr)})
     if (!aligned16(q)) return MM_ERR_INVALID_ARG;
+  if (!aligned4(d_gate) || !aligned4(d_post_w) || !aligned4(d_pre_w)) return MM_ERR_INVALID_ARG;
   if (!aligned4(rstd_post) || !aligned4(rstd_pre)) return MM_ERR_INVALID_ARG;
   if (!workspace || !aligned16(workspace) ||
       workspace_bytes < mm_block_norm_backward_workspace_bytes(T, H, dtype))

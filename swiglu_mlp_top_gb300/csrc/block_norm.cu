@@ -46,7 +46,124 @@ __device__ __forceinline__ float inv_rms_of(float ss, int H, float eps) {
   return 1.0f / sqrtf(ss / static_cast<float>(H) + eps);
 }
 
+// Pairs of fp32 in 64 bits (fma.rn.f32x2).
+__device__ __forceinline__ u64 fmul2(u64 a, u64 b) {
+  u64 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ u64 pair2(float lo, float hi) {
+  return (static_cast<u64>(__float_as_uint(hi)) << 32) | __float_as_uint(lo);
+}
+__device__ __forceinline__ float lo2(u64 v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float hi2(u64 v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+
+// A thread's unit m of a row: V consecutive elements, or (V = 1) two single
+// columns tpr apart.  Columns behind the row read as zeros.
+template <typename T, int V>
+struct Unit {
+  static constexpr int kPairs = V / 2;
+  static constexpr bool kAsync = true;        // 16-byte cp.async
+  typedef typename Pack<T, V>::Raw Raw;
+  static __device__ __forceinline__ void copy(uint32_t slot, const void* p, int64_t base, int m, int c0, int tpr,
+                                              int nv) {
+    if (c0 + m * tpr < nv)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot),
+                   "l"(reinterpret_cast<const Raw*>(static_cast<const T*>(p) + base) + c0 + m * tpr)
+                   : "memory");
+  }
+  static __device__ __forceinline__ Raw zero() { return Raw{}; }
+  static __device__ __forceinline__ Raw load(const void* p, int64_t base, int m, int c0, int tpr, int nv) {
+    const int c = c0 + m * tpr;
+    return c < nv ? row_load<T, V>(p, base, c) : zero();
+  }
+  static __device__ __forceinline__ u64 get(const Raw& r, int k) {
+    return pair2(Pack<T, V>::get(r, 2 * k), Pack<T, V>::get(r, 2 * k + 1));
+  }
+  static __device__ __forceinline__ Raw put(const u64 (&v)[kPairs]) {
+    float o[V];
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) {
+      o[2 * k] = lo2(v[k]);
+      o[2 * k + 1] = hi2(v[k]);
+    }
+    return Pack<T, V>::put(o);
+  }
+  static __device__ __forceinline__ void store_raw(void* p, int64_t base, int m, int c0, int tpr, int nv,
+                                                   const Raw& r) {
+    if (c0 + m * tpr < nv) reinterpret_cast<Raw*>(static_cast<T*>(p) + base)[c0 + m * tpr] = r;
+  }
+  static __device__ __forceinline__ void store(void* p, int64_t base, int m, int c0, int tpr, int nv,
+                                               const u64 (&v)[kPairs]) {
+    store_raw(p, base, m, c0, tpr, nv, put(v));
+  }
+  // fp32 values by column in shared memory: four of a vector's V side by side
+  // for all of the group's threads, then the next four, so that a warp's
+  // 16-byte accesses meet every bank once.  place(): where column h is.
+  static __device__ __forceinline__ int place(int h, int tpr) {
+    const int c = h / V, j = h % V, m = c / tpr;
+    return ((m * (V / 4) + j / 4) * tpr + (c - m * tpr)) * 4 + j % 4;
+  }
+  static __device__ __forceinline__ void cols(const float* s, int m, int c0, int tpr, u64 (&v)[kPairs]) {
+    const ulonglong2* q = reinterpret_cast<const ulonglong2*>(s) + m * (V / 4) * tpr + c0;
+#pragma unroll
+    for (int k = 0; k < kPairs / 2; ++k) {
+      const ulonglong2 w = q[k * tpr];
+      v[2 * k] = w.x;
+      v[2 * k + 1] = w.y;
+    }
+  }
+  static __device__ __forceinline__ void keep(float* s, int m, int c0, int tpr, int nv, const u64 (&v)[kPairs]) {
+    if (c0 + m * tpr >= nv) return;
+    ulonglong2* q = reinterpret_cast<ulonglong2*>(s) + m * (V / 4) * tpr + c0;
+#pragma unroll
+    for (int k = 0; k < kPairs / 2; ++k) q[k * tpr] = make_ulonglong2(v[2 * k], v[2 * k + 1]);
+  }
+};
+template <typename T>
+struct Unit<T, 1> {
+  static constexpr int kPairs = 1;
+  static constexpr bool kAsync = false;       // cp.async of 4 bytes is slower than plain loads
+  struct __align__(2 * sizeof(T)) Raw {
+    T a, b;
+  };
+  static __device__ __forceinline__ void copy(uint32_t, const void*, int64_t, int, int, int, int) {}
+  static __device__ __forceinline__ Raw zero() { return Raw{T(0.f), T(0.f)}; }
+  static __device__ __forceinline__ Raw load(const void* p, int64_t base, int m, int c0, int tpr, int nv) {
+    const T* row = static_cast<const T*>(p) + base;
+    const int c = c0 + 2 * m * tpr;
+    return Raw{c < nv ? row[c] : T(0.f), c + tpr < nv ? row[c + tpr] : T(0.f)};
+  }
+  static __device__ __forceinline__ u64 get(const Raw& r, int) {
+    return pair2(static_cast<float>(r.a), static_cast<float>(r.b));
+  }
+  static __device__ __forceinline__ void store(void* p, int64_t base, int m, int c0, int tpr, int nv,
+                                               const u64 (&v)[1]) {
+    const int c = c0 + 2 * m * tpr;
+    const float a[1] = {lo2(v[0])}, b[1] = {hi2(v[0])};
+    if (c < nv) row_store<T, 1>(p, base, c, a);
+    if (c + tpr < nv) row_store<T, 1>(p, base, c + tpr, b);
+  }
+  static __device__ __forceinline__ int place(int h, int) { return h; }
+  static __device__ __forceinline__ void cols(const float* s, int m, int c0, int tpr, u64 (&v)[1]) {
+    const int c = c0 + 2 * m * tpr;
+    v[0] = pair2(s[c], s[c + tpr]);
+  }
+  static __device__ __forceinline__ void keep(float* s, int m, int c0, int tpr, int nv, const u64 (&v)[1]) {
+    const int c = c0 + 2 * m * tpr;
+    if (c < nv) s[c] = lo2(v[0]);
+    if (c + tpr < nv) s[c + tpr] = hi2(v[0]);
+  }
+};
+
+
+template <typename T>
+__device__ __forceinline__ float bn_param(const void* w, int h) {
+  return w ? static_cast<float>(static_cast<const T*>(w)[h]) : 1.f;
+}
+
 // ------------------------------------------------------------------ forward
+constexpr size_t kBnMostSmem = 224 * 1024;   // dynamic, of 227 KB a block may have
 constexpr int kBnFwdThreads = 512;      // most threads of a block (one group of them: H = 16384)
 
 template <typename T, int V, int NV>
@@ -129,6 +246,117 @@ __global__ void __launch_bounds__(kBnFwdThreads) block_norm_kernel(const BlockNo
   }
 }
 
+// Many aligned rows: a block of groups per SM walks down the rows, the next
+// row's inputs on their way to shared memory (each thread copies and reads its
+// own slots, so without a barrier), w_post g and w_pre there in fp32, sums and
+// products on pairs.  One group per row and no loop leaves the last wave of
+// blocks part empty and re-reads the parameters for every row (T = 16384,
+// H = 768, bf16: 21 us, so 18 us).
+template <typename T, int V, int NU, bool kTokenGate>
+__global__ void __launch_bounds__(kBnFwdThreads, 1)
+block_norm_ring_kernel(const BlockNormFwd a, int tpr, int span) {
+  using U = Unit<T, V>;
+  typedef typename U::Raw Raw;
+  constexpr int NP = U::kPairs, kIn = kTokenGate ? 3 : 2;
+  extern __shared__ __align__(16) float bn_smem[];
+  __shared__ float red[2 * kBnFwdThreads / 32];
+  float* w_mid = bn_smem;
+  float* w_pre = bn_smem + span;
+  const int group = threadIdx.x / tpr, c0 = threadIdx.x - group * tpr, nv = a.H / V, groups = blockDim.x / tpr;
+  constexpr int kStageBytes = kIn * NU * 32 * static_cast<int>(sizeof(Raw));
+  unsigned char* ring = reinterpret_cast<unsigned char*>(bn_smem + 2 * span) + (threadIdx.x >> 5) * (2 * kStageBytes) +
+                        (threadIdx.x & 31) * sizeof(Raw);
+  auto at = [](int i, int m) { return (i * NU + m) * 32 * static_cast<int>(sizeof(Raw)); };
+  const void* src[3] = {a.x, a.f, kTokenGate ? a.gate : nullptr};
+  auto fetch = [&](int64_t t, int stage) {
+    if (t < a.T)
+#pragma unroll
+      for (int i = 0; i < kIn; ++i)
+        if (src[i])
+#pragma unroll
+          for (int m = 0; m < NU; ++m)
+            U::copy(smem_u32(ring + stage * kStageBytes) + at(i, m), src[i], t * a.H, m, c0, tpr, nv);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < 2 * kIn * NU; ++i)      // what no copy will fill stays zero
+    *reinterpret_cast<Raw*>(ring + at(0, 0) + i * 32 * sizeof(Raw)) = U::zero();
+  pdl_enter();
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * groups + group;
+  fetch(t, 0);
+  for (int h = threadIdx.x; h < span; h += blockDim.x) {
+    const int place = U::place(h, tpr);
+    w_mid[place] = h < a.H ? bn_param<T>(a.post_w, h) * bn_param<T>(kTokenGate ? nullptr : a.gate, h) : 0.f;
+    w_pre[place] = h < a.H && a.pre_w ? bn_param<T>(a.pre_w, h) : 0.f;
+  }
+  __syncthreads();
+  const u64 scale2 = pair2(a.residual_scale, a.residual_scale);
+  for (int stage = 0; t < a.T; t += step, stage ^= 1) {
+    const int64_t base = t * a.H;
+    fetch(t + step, stage ^ 1);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    const unsigned char* here = ring + stage * kStageBytes;
+    auto value = [&](int i, int m) { return *reinterpret_cast<const Raw*>(here + at(i, m)); };
+    Raw r[NU];
+#pragma unroll
+    for (int m = 0; m < NU; ++m) r[m] = value(0, m);
+    if (a.f) {
+      Raw f[NU];
+#pragma unroll
+      for (int m = 0; m < NU; ++m) f[m] = value(1, m);
+      float rho[1] = {1.f};
+      if (a.post_w) {
+        u64 ss = 0;
+#pragma unroll
+        for (int m = 0; m < NU; ++m)
+#pragma unroll
+          for (int k = 0; k < NP; ++k) ss = ffma2(U::get(f[m], k), U::get(f[m], k), ss);
+        rho[0] = hsum2(ss);
+        group_sum(rho, red, 0, group, tpr);
+        rho[0] = inv_rms_of(rho[0], a.H, a.eps);
+        if (c0 == 0 && a.rstd_post) a.rstd_post[t] = rho[0];
+      }
+      const u64 rho2 = pair2(rho[0], rho[0]);
+#pragma unroll
+      for (int m = 0; m < NU; ++m) {
+        u64 w[NP], v[NP];
+        U::cols(w_mid, m, c0, tpr, w);
+        Raw g = U::zero();
+        if constexpr (kTokenGate) g = value(2, m);
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+          v[k] = fmul2(fmul2(U::get(f[m], k), rho2), w[k]);
+          if constexpr (kTokenGate) v[k] = fmul2(v[k], U::get(g, k));
+          v[k] = ffma2(scale2, U::get(r[m], k), v[k]);
+        }
+        r[m] = U::put(v);                     // r as stored
+        U::store_raw(a.r, base, m, c0, tpr, nv, r[m]);
+      }
+    }
+    if (a.pre_w == nullptr) continue;
+    u64 ss = 0;
+#pragma unroll
+    for (int m = 0; m < NU; ++m)
+#pragma unroll
+      for (int k = 0; k < NP; ++k) ss = ffma2(U::get(r[m], k), U::get(r[m], k), ss);
+    float rho[1] = {hsum2(ss)};
+    group_sum(rho, red, 1, group, tpr);
+    rho[0] = inv_rms_of(rho[0], a.H, a.eps);
+    if (c0 == 0 && a.rstd_pre) a.rstd_pre[t] = rho[0];
+    const u64 rho2 = pair2(rho[0], rho[0]);
+#pragma unroll
+    for (int m = 0; m < NU; ++m) {
+      u64 w[NP], v[NP];
+      U::cols(w_pre, m, c0, tpr, w);
+#pragma unroll
+      for (int k = 0; k < NP; ++k) v[k] = fmul2(fmul2(U::get(r[m], k), rho2), w[k]);
+      U::store(a.n, base, m, c0, tpr, nv, v);
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
 // ----------------------------------------------------------------- backward
 // With v = w_pre dn, e = dr + rho_r v, D = e - r rho_r^3 c_r and q = g D, the
 // two row means are linear in three sums that one pass over the row gives:
@@ -144,109 +372,6 @@ __global__ void __launch_bounds__(kBnFwdThreads) block_norm_kernel(const BlockNo
 // slots, not DRAM, set the time (1654 instructions a row of 768 columns).
 constexpr int kBnBwdThreads = 512;      // 128 registers a thread
 constexpr int kBnSums = 2;              // d_pre_w, M
-constexpr size_t kBnMostSmem = 224 * 1024;   // dynamic, of 227 KB a block may have
-
-__device__ __forceinline__ u64 fmul2(u64 a, u64 b) {
-  u64 d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ u64 pair2(float lo, float hi) {
-  return (static_cast<u64>(__float_as_uint(hi)) << 32) | __float_as_uint(lo);
-}
-__device__ __forceinline__ float lo2(u64 v) { return __uint_as_float(static_cast<uint32_t>(v)); }
-__device__ __forceinline__ float hi2(u64 v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
-
-// A thread's unit m of a row: V consecutive elements, or (V = 1) two single
-// columns tpr apart.  Columns behind the row read as zeros.
-template <typename T, int V>
-struct Unit {
-  static constexpr int kPairs = V / 2;
-  static constexpr bool kAsync = true;        // 16-byte cp.async
-  typedef typename Pack<T, V>::Raw Raw;
-  static __device__ __forceinline__ void copy(uint32_t slot, const void* p, int64_t base, int m, int c0, int tpr,
-                                              int nv) {
-    if (c0 + m * tpr < nv)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot),
-                   "l"(reinterpret_cast<const Raw*>(static_cast<const T*>(p) + base) + c0 + m * tpr)
-                   : "memory");
-  }
-  static __device__ __forceinline__ Raw zero() { return Raw{}; }
-  static __device__ __forceinline__ Raw load(const void* p, int64_t base, int m, int c0, int tpr, int nv) {
-    const int c = c0 + m * tpr;
-    return c < nv ? row_load<T, V>(p, base, c) : zero();
-  }
-  static __device__ __forceinline__ u64 get(const Raw& r, int k) {
-    return pair2(Pack<T, V>::get(r, 2 * k), Pack<T, V>::get(r, 2 * k + 1));
-  }
-  static __device__ __forceinline__ void store(void* p, int64_t base, int m, int c0, int tpr, int nv,
-                                               const u64 (&v)[kPairs]) {
-    const int c = c0 + m * tpr;
-    if (c >= nv) return;
-    float o[V];
-#pragma unroll
-    for (int k = 0; k < kPairs; ++k) {
-      o[2 * k] = lo2(v[k]);
-      o[2 * k + 1] = hi2(v[k]);
-    }
-    row_store<T, V>(p, base, c, o);
-  }
-  // fp32 values by column in shared memory (16-byte aligned, kept for every unit)
-  static __device__ __forceinline__ void cols(const float* s, int m, int c0, int tpr, u64 (&v)[kPairs]) {
-    const ulonglong2* q = reinterpret_cast<const ulonglong2*>(s + (c0 + m * tpr) * V);
-#pragma unroll
-    for (int k = 0; k < kPairs / 2; ++k) {
-      const ulonglong2 w = q[k];
-      v[2 * k] = w.x;
-      v[2 * k + 1] = w.y;
-    }
-  }
-  static __device__ __forceinline__ void keep(float* s, int m, int c0, int tpr, int nv, const u64 (&v)[kPairs]) {
-    if (c0 + m * tpr >= nv) return;
-    ulonglong2* q = reinterpret_cast<ulonglong2*>(s + (c0 + m * tpr) * V);
-#pragma unroll
-    for (int k = 0; k < kPairs / 2; ++k) q[k] = make_ulonglong2(v[2 * k], v[2 * k + 1]);
-  }
-};
-template <typename T>
-struct Unit<T, 1> {
-  static constexpr int kPairs = 1;
-  static constexpr bool kAsync = false;       // cp.async of 4 bytes is slower than plain loads
-  struct __align__(2 * sizeof(T)) Raw {
-    T a, b;
-  };
-  static __device__ __forceinline__ void copy(uint32_t, const void*, int64_t, int, int, int, int) {}
-  static __device__ __forceinline__ Raw zero() { return Raw{T(0.f), T(0.f)}; }
-  static __device__ __forceinline__ Raw load(const void* p, int64_t base, int m, int c0, int tpr, int nv) {
-    const T* row = static_cast<const T*>(p) + base;
-    const int c = c0 + 2 * m * tpr;
-    return Raw{c < nv ? row[c] : T(0.f), c + tpr < nv ? row[c + tpr] : T(0.f)};
-  }
-  static __device__ __forceinline__ u64 get(const Raw& r, int) {
-    return pair2(static_cast<float>(r.a), static_cast<float>(r.b));
-  }
-  static __device__ __forceinline__ void store(void* p, int64_t base, int m, int c0, int tpr, int nv,
-                                               const u64 (&v)[1]) {
-    const int c = c0 + 2 * m * tpr;
-    const float a[1] = {lo2(v[0])}, b[1] = {hi2(v[0])};
-    if (c < nv) row_store<T, 1>(p, base, c, a);
-    if (c + tpr < nv) row_store<T, 1>(p, base, c + tpr, b);
-  }
-  static __device__ __forceinline__ void cols(const float* s, int m, int c0, int tpr, u64 (&v)[1]) {
-    const int c = c0 + 2 * m * tpr;
-    v[0] = pair2(s[c], s[c + tpr]);
-  }
-  static __device__ __forceinline__ void keep(float* s, int m, int c0, int tpr, int nv, const u64 (&v)[1]) {
-    const int c = c0 + 2 * m * tpr;
-    if (c < nv) s[c] = lo2(v[0]);
-    if (c + tpr < nv) s[c + tpr] = hi2(v[0]);
-  }
-};
-
-template <typename T>
-__device__ __forceinline__ float bn_param(const void* w, int h) {
-  return w ? static_cast<float>(static_cast<const T*>(w)[h]) : 1.f;
-}
 
 // NU units a thread.  The next row's inputs are copied to shared memory with
 // cp.async while this one is worked on (`stages` 2; 1 where two do not fit):
@@ -326,8 +451,9 @@ block_norm_bwd_kernel(const BlockNormBwd a, int tpr, int span, int stages) {
   if (U::kAsync && stages == 2) fetch(t, 0);
   fetch_rstd(t);
   for (int h = threadIdx.x; h < span; h += blockDim.x) {
-    w_pre[h] = h < a.H && a.pre_w ? bn_param<T>(a.pre_w, h) : 0.f;
-    w_mid[h] = h < a.H ? bn_param<T>(a.post_w, h) * bn_param<T>(kTokenGate ? nullptr : a.gate, h) : 0.f;
+    const int place = U::place(h, tpr);
+    w_pre[place] = h < a.H && a.pre_w ? bn_param<T>(a.pre_w, h) : 0.f;
+    w_mid[place] = h < a.H ? bn_param<T>(a.post_w, h) * bn_param<T>(kTokenGate ? nullptr : a.gate, h) : 0.f;
   }
   __syncthreads();
   u64 s_pre[NU][NP], s_mid[NU][NP];
@@ -419,13 +545,15 @@ block_norm_bwd_kernel(const BlockNormBwd a, int tpr, int span, int stages) {
   }
   __syncthreads();
   float* part = a.partial + static_cast<int64_t>(blockIdx.x) * kBnSums * a.H;
-  for (int h = threadIdx.x; h < a.H; h += blockDim.x)
+  for (int h = threadIdx.x; h < a.H; h += blockDim.x) {
+    const int place = U::place(h, tpr);
 #pragma unroll
     for (int q = 0; q < kBnSums; ++q) {
       float sum = 0.f;
-      for (int gi = 0; gi < groups; ++gi) sum += behind[(gi * kBnSums + q) * span + h];
+      for (int gi = 0; gi < groups; ++gi) sum += behind[(gi * kBnSums + q) * span + place];
       part[q * a.H + h] = sum;
     }
+  }
 }
 
 // Rows too wide for a block's registers: the block walks the row twice (the
@@ -634,8 +762,40 @@ static cudaError_t bn_fwd_launch(const BlockNormFwd& a, int tpr, cudaStream_t st
                                  dim3(groups * tpr), 0, st, a, tpr);
 }
 
+// The ring, where two rows of every group fit beside the parameters and every
+// SM has a few rows for each group; cudaErrorNotSupported: not here.
+template <typename T, int V, int NU>
+static cudaError_t bn_ring_launch(const BlockNormFwd& a, int tpr, cudaStream_t st) {
+  const bool token_gate = a.gate != nullptr && a.gate_per_token;
+  const int span = NU * tpr * V, groups = kBnFwdThreads / tpr;
+  const size_t smem = 2 * sizeof(float) * span + 2 * (token_gate ? 3 : 2) * sizeof(T) * span * groups;
+  const int64_t sms = num_sms();
+  if (smem > kBnMostSmem || a.T < 4 * sms * groups) return cudaErrorNotSupported;
+  auto kern = token_gate ? block_norm_ring_kernel<T, V, NU, true> : block_norm_ring_kernel<T, V, NU, false>;
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent_kernel(kern, dim3(static_cast<unsigned>(sms)), dim3(groups * tpr), smem, st, a, tpr, span);
+}
+template <typename T, int V>
+static cudaError_t bn_ring_pick(const BlockNormFwd& a, cudaStream_t st) {
+  constexpr int kUnits[3] = {24 / V, 16 / V, 8 / V};
+  int best = 0;
+  const int nv = a.H / V;
+  for (int NU : kUnits)
+    if (bn_tpr(nv, NU) <= kBnFwdThreads && (best == 0 || NU * bn_tpr(nv, NU) < best * bn_tpr(nv, best))) best = NU;
+  if (best == 0) return cudaErrorNotSupported;
+  const int tpr = bn_tpr(nv, best);
+  if (best == kUnits[0]) return bn_ring_launch<T, V, kUnits[0]>(a, tpr, st);
+  if (best == kUnits[1]) return bn_ring_launch<T, V, kUnits[1]>(a, tpr, st);
+  return bn_ring_launch<T, V, kUnits[2]>(a, tpr, st);
+}
+
 template <typename T, int V>
 static cudaError_t bn_fwd_pick(const BlockNormFwd& a, cudaStream_t st) {
+  if constexpr (V > 1) {
+    const cudaError_t e = bn_ring_pick<T, V>(a, st);
+    if (e != cudaErrorNotSupported) return e;
+  }
   // up to 32 elements a thread; fewer, where a warp holds the row with fewer
   const int nv = a.H / V;
   constexpr int kMost = 32 / V;

@@ -111,16 +111,22 @@ def test_plain_norm(T, H, dtype):
     check_backward(d, r, stats, backward(d, r, stats))
 
 
-def test_many_tokens():
-    d = make(20000, 256, BF)
-    r, n, stats = forward(d)
-    check_forward(d, r, n, stats)
-    check_backward(d, r, stats, backward(d, r, stats))
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,H,post,gate,pre,branch", [
+    (20000, 256, True, "channel", True, True), (9733, 8, True, "token", True, True), (9999, 24, False, None, True, True),
+    (10001, 40, True, None, False, True), (12345, 768, False, "channel", True, True), (10000, 64, True, "channel", True, False),
+    (3000, 2432, True, "token", False, True), (5003, 1000, True, "channel", True, True), (700, 8192, True, "token", True, True),
+    (650, 12288, True, None, True, True), (11000, 33, True, "channel", True, True)])
+def test_many_tokens(T, H, post, gate, pre, branch, dtype):
+    d = make(T, H, dtype, post, gate, pre, branch=branch)
+    r, n, stats = forward(d, s=0.9 if branch else 1.0)
+    check_forward(d, r, n, stats, s=0.9 if branch else 1.0)
+    check_backward(d, r, stats, backward(d, r, stats, s=0.9 if branch else 1.0), s=0.9 if branch else 1.0)
 
 
-@pytest.mark.parametrize("dtype,H", [(BF, 768), (F32, 101)])
-def test_in_place(dtype, H):
-    d = make(40, H, dtype)
+@pytest.mark.parametrize("dtype,T,H", [(BF, 40, 768), (F32, 40, 101), (BF, 10000, 96)])
+def test_in_place(dtype, T, H):
+    d = make(T, H, dtype)
     r, n, stats = forward(d)
     x, f = d["x"].clone(), d["f"].clone()
     r2, n2 = mm.block_norm(x, f, post_weight=d["post"], gate=d["gate"], pre_weight=d["pre"], eps=EPS, out=x, normed=f)
