@@ -11,6 +11,8 @@ namespace mm {
 
 constexpr int kPmThreads = 512;         // sort and copy: two blocks an SM
 constexpr int kPmWarps = kPmThreads / 32;
+constexpr int kPmBatch = 4;             // vectors of a row in flight a lane
+constexpr int kPmKept = 2048;           // positions of a block kept in shared memory
 constexpr int kPmRowThreads = 256;      // combine and its gradient
 
 // Calls f(row) for the padding rows of every group, shared out over the grid's
@@ -56,15 +58,20 @@ __device__ __forceinline__ void each_padding_row(const int32_t* offsets, const i
 static_assert(MM_MAX_EXPERTS <= 64, "each_padding_row: two groups a lane");
 
 // Assignments to each expert among [first, first + num) of topk_idx, added to
-// cnt in shared memory: one add per warp and expert.
+// cnt in shared memory (integers: any order gives the same sums).
 __device__ __forceinline__ void count_experts(const int32_t* topk_idx, int64_t first, int64_t num, int E,
                                               int* cnt) {
-  const int lane = threadIdx.x & 31;
-  for (int64_t i = threadIdx.x; i - lane < num; i += blockDim.x) {
-    const int e = i < num ? topk_idx[first + i] : -1;
-    const bool valid = e >= 0 && e < E;
-    const unsigned peers = __match_any_sync(0xffffffffu, valid ? e : -1);
-    if (valid && lane == __ffs(peers) - 1) atomicAdd(&cnt[e], __popc(peers));
+  constexpr int kBatch = 8;                   // loads in flight a thread
+  for (int64_t i0 = threadIdx.x; i0 < num; i0 += static_cast<int64_t>(blockDim.x) * kBatch) {
+    int e[kBatch];
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const int64_t i = i0 + static_cast<int64_t>(q) * blockDim.x;
+      e[q] = i < num ? topk_idx[first + i] : -1;
+    }
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q)
+      if (e[q] >= 0 && e[q] < E) atomicAdd(&cnt[e[q]], 1);
   }
 }
 
@@ -92,17 +99,28 @@ __global__ void __launch_bounds__(kPmThreads, 2)
 permute_kernel(const PermuteArgs a, int tokens, const int32_t* blk_cnt, int row_bytes) {
   __shared__ int s_tot[MM_MAX_EXPERTS], s_next[MM_MAX_EXPERTS], s_off[MM_MAX_EXPERTS + 1];
   __shared__ int s_warp[kPmWarps][MM_MAX_EXPERTS];
+  __shared__ int s_pos[kPmKept];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens;
-  const int64_t nt = a.T - t0 < tokens ? a.T - t0 : tokens;
+  const int nt = static_cast<int>(a.T - t0 < tokens ? a.T - t0 : tokens), na = nt * a.k;
+  const int32_t* idx = a.topk_idx + t0 * a.k;
   const char* x = static_cast<const char*>(a.x) + t0 * row_bytes;
   if (sizeof(Vec) == 16 && tid == 0) {
     // at most 64 KB a block: 20 MB over the grid, well inside L2
-    const int64_t bytes = nt * row_bytes < 65536 ? nt * row_bytes : 65536;
+    const int64_t all = static_cast<int64_t>(nt) * row_bytes, bytes = all < 65536 ? all : 65536;
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(x), "r"(static_cast<uint32_t>(bytes)) : "memory");
   }
   for (int e = tid; e < a.E; e += kPmThreads) s_tot[e] = s_next[e] = 0;
   pdl_enter();
+  const int nv = row_bytes / static_cast<int>(sizeof(Vec)), chunks = (nv + 32 * kPmBatch - 1) / (32 * kPmBatch);
+  Vec v[kPmBatch];
+  auto fetch = [&](int token, int chunk) {
+    const Vec* src = reinterpret_cast<const Vec*>(x + static_cast<int64_t>(token) * row_bytes);
+    const int c = chunk * (32 * kPmBatch) + lane;
+#pragma unroll
+    for (int i = 0; i < kPmBatch; ++i)
+      if (c + 32 * i < nv) v[i] = src[c + 32 * i];
+  };
   __syncthreads();
   if (blk_cnt == nullptr) {
     count_experts(a.topk_idx, 0, t0 * a.k, a.E, s_next);
@@ -149,9 +167,9 @@ permute_kernel(const PermuteArgs a, int tokens, const int32_t* blk_cnt, int row_
   }
   __syncthreads();
   // ranks, one assignment a thread and round: within the warp, then the warps in order
-  for (int64_t base = 0; base < nt * a.k; base += kPmThreads) {
-    const int64_t i = base + tid;
-    int e = i < nt * a.k ? a.topk_idx[t0 * a.k + i] : -1;
+  for (int base = 0; base < na; base += kPmThreads) {
+    const int i = base + tid;
+    const int e = i < na ? idx[i] : -1;
     const bool valid = e >= 0 && e < a.E;
     const unsigned peers = __match_any_sync(0xffffffffu, valid ? e : -1);
     const int rank = __popc(peers & ((1u << lane) - 1u));
@@ -164,8 +182,9 @@ permute_kernel(const PermuteArgs a, int tokens, const int32_t* blk_cnt, int row_
       row = s_next[e] + rank;
       for (int w = 0; w < warp; ++w) row += s_warp[w][e];
     }
-    if (i < nt * a.k) {
+    if (i < na) {
       a.pos[t0 * a.k + i] = row;
+      if (i < kPmKept) s_pos[i] = row;
       if (valid) a.perm[row] = static_cast<int32_t>(t0 * a.k + i);
     }
     __syncthreads();
@@ -173,26 +192,25 @@ permute_kernel(const PermuteArgs a, int tokens, const int32_t* blk_cnt, int row_
       for (int w = 0; w < kPmWarps; ++w) s_next[q] += s_warp[w][q];
     __syncthreads();
   }
-  // rows
-  const int nv = row_bytes / static_cast<int>(sizeof(Vec));
-  constexpr int kBatch = 4;
-  for (int64_t t = warp; t < nt; t += kPmWarps) {
-    const int my = lane < a.k ? a.pos[(t0 + t) * a.k + lane] : -1;      // the block's own writes
-    const Vec* src = reinterpret_cast<const Vec*>(x + t * row_bytes);
-    for (int c0 = 0; c0 < nv; c0 += 32 * kBatch) {      // the whole warp stays: it shares `my`
-      const int c = c0 + lane;
-      Vec v[kBatch];
+  // rows: the next piece's load is under way while this one is stored
+  if (warp < nt) fetch(warp, 0);
+  for (int token = warp, chunk = 0; token < nt;) {
+    Vec now[kPmBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (c + 32 * i < nv) v[i] = src[c + 32 * i];
-      for (int s = 0; s < a.k; ++s) {
-        const int64_t row = __shfl_sync(0xffffffffu, my, s);
-        if (row < 0) continue;
-        Vec* dst = reinterpret_cast<Vec*>(static_cast<char*>(a.xs) + row * row_bytes);
+    for (int i = 0; i < kPmBatch; ++i) now[i] = v[i];
+    const int c = chunk * (32 * kPmBatch) + lane, first = token * a.k;
+    if (++chunk == chunks) {
+      chunk = 0;
+      token += kPmWarps;
+    }
+    if (token < nt) fetch(token, chunk);
+    for (int at = first; at < first + a.k; ++at) {
+      const int64_t row = at < kPmKept ? s_pos[at] : a.pos[t0 * a.k + at];    // the block's own writes
+      if (row < 0) continue;
+      Vec* dst = reinterpret_cast<Vec*>(static_cast<char*>(a.xs) + row * row_bytes);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-          if (c + 32 * i < nv) dst[c + 32 * i] = v[i];
-      }
+      for (int i = 0; i < kPmBatch; ++i)
+        if (c + 32 * i < nv) dst[c + 32 * i] = now[i];
     }
   }
   if (blockIdx.x == 0) {
@@ -324,7 +342,9 @@ static int pm_blocks(int64_t T) {
   const int64_t most = 2 * static_cast<int64_t>(num_sms()), want = (T + kPmWarps - 1) / kPmWarps;
   return static_cast<int>(want < most ? (want > 0 ? want : 1) : most);
 }
-// Up to this many assignments every block counts all of them itself.
+// Up to this many assignments every block counts all of them itself (T = 2048,
+// k = 2: 4.6 us, of which the launch of a counting kernel would add 1.5);
+// beyond, the counting kernel costs less (T = 4096, k = 2: 6.3 us against 6.8).
 constexpr int64_t kPmCountOwn = 4096;
 
 size_t permute_bytes(int64_t T, int E, int k) {
