@@ -46,18 +46,6 @@ __device__ __forceinline__ float inv_rms_of(float ss, int H, float eps) {
   return 1.0f / sqrtf(ss / static_cast<float>(H) + eps);
 }
 
-// Pairs of fp32 in 64 bits (fma.rn.f32x2).
-__device__ __forceinline__ u64 fmul2(u64 a, u64 b) {
-  u64 d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ u64 pair2(float lo, float hi) {
-  return (static_cast<u64>(__float_as_uint(hi)) << 32) | __float_as_uint(lo);
-}
-__device__ __forceinline__ float lo2(u64 v) { return __uint_as_float(static_cast<uint32_t>(v)); }
-__device__ __forceinline__ float hi2(u64 v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
-
 // A thread's unit m of a row: V consecutive elements, or (V = 1) two single
 // columns tpr apart.  Columns behind the row read as zeros.
 template <typename T, int V>

@@ -73,6 +73,16 @@ struct Words {
       for (int j = 0; j < V; j += 2) w[j / 2] = pack_bf16x2(v[j], v[j + 1]);
     }
   }
+  // Elements 2k and 2k + 1 (V = 1: the one, and zero).
+  __device__ __forceinline__ u64 get2(int k) const { return pair2(get(2 * k), V > 1 ? get(V > 1 ? 2 * k + 1 : 0) : 0.f); }
+  __device__ __forceinline__ void put2(int k, u64 v) {
+    if constexpr (sizeof(T) == 2) {
+      w[k] = pack_bf16x2(lo2(v), hi2(v));
+    } else {
+      w[2 * k] = __float_as_uint(lo2(v));
+      if constexpr (V > 1) w[2 * k + 1] = __float_as_uint(hi2(v));
+    }
+  }
   // The largest |value| as the bits of an fp32; infinities and NaN order above.
   __device__ __forceinline__ uint32_t abs_max_bits() const {
     uint32_t m = 0;
@@ -101,6 +111,7 @@ __device__ __forceinline__ uint32_t ck_exponent(uint32_t amax) {
 
 template <int V>
 __device__ __forceinline__ uint32_t group_max(uint32_t m) {
+  if constexpr (V == 1) return __reduce_max_sync(0xffffffffu, m);
 #pragma unroll
   for (int o = 1; o < 32 / V; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   return m;
@@ -127,9 +138,9 @@ __device__ __forceinline__ uint32_t ck_encode(Words<T, V> x, Words<Code, V>& cod
   const float inv = ck_scale(254u - e);
   uint16_t c[(V + 1) / 2];
 #pragma unroll
-  for (int j = 0; j < V; j += 2) {
-    const float lo = x.get(j) * inv, hi = j + 1 < V ? x.get(j + 1) * inv : 0.f;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c[j / 2]) : "f"(hi), "f"(lo));
+  for (int k = 0; k < (V + 1) / 2; ++k) {
+    const u64 v = fmul2(x.get2(k), pair2(inv, inv));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c[k]) : "f"(hi2(v)), "f"(lo2(v)));
   }
   if constexpr (V >= 4) {
 #pragma unroll
@@ -140,29 +151,54 @@ __device__ __forceinline__ uint32_t ck_encode(Words<T, V> x, Words<Code, V>& cod
   return e;
 }
 
+// Values of codes 2k and 2k + 1.
 template <int V>
-__device__ __forceinline__ void ck_decode(const Words<Code, V>& codes, float scale, float (&v)[V]) {
-#pragma unroll
-  for (int j = 0; j < V; j += 2) {
-    const uint16_t c = static_cast<uint16_t>(codes.w[j / 4] >> (8 * (j % 4)));
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
-    const float2 f = f16x2_to_f32x2(h);
-    v[j] = f.x * scale;
-    if (j + 1 < V) v[j + 1] = f.y * scale;
-  }
+__device__ __forceinline__ u64 ck_decode2(const Words<Code, V>& codes, int k, float scale) {
+  const uint16_t c = static_cast<uint16_t>(codes.w[k / 2] >> (16 * (k % 2)));
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+  const float2 f = f16x2_to_f32x2(h);
+  return fmul2(pair2(f.x, f.y), pair2(scale, scale));
 }
 
-// t = exp(-|g|) and 1 / (1 + t), from which sigma(g) and 1 - sigma(g) follow
-// without cancellation for either sign.  (The fast exponential would lose
-// seven bits at g = -80; the fast division, 2 ulp, is enough for bf16.)
+// sigma(g) and 1 - sigma(g) of two values: with t = exp(-|g|), 1 / (1 + t) and
+// t / (1 + t), without cancellation for either sign.  fp32 rows take expf and
+// a division.  For bf16 rows these are what a streaming kernel has no issue
+// slots for (79% of them were taken, at 41 instructions an element), so
+//   t = (2^q)^2,  q = -|g| log2(e) / 2
+// with the product in two parts (Cody and Waite: head q, tail r, 2^(q + r) =
+// 2^q (1 + r ln 2)) and the hardware's 2^x: half the argument keeps 2^q above
+// fp32's smallest normal wherever t is above its smallest subnormal.  Relative
+// error of t below 2^-20.5 (twice the instruction's 2 ulp, and four roundings).
 template <typename T>
-__device__ __forceinline__ void sigmoid_parts(float g, float& sig, float& rest) {
-  const float t = expf(-fabsf(g));
-  const float s = sizeof(T) == 2 ? __fdividef(1.0f, 1.0f + t) : 1.0f / (1.0f + t);
-  const float ts = t * s;
-  sig = g >= 0.f ? s : ts;                    // a NaN g leaves NaN in t
-  rest = g >= 0.f ? ts : s;
+__device__ __forceinline__ void sigmoid2(u64 g, u64& sig, u64& rest) {
+  const float g0 = lo2(g), g1 = hi2(g);
+  u64 t, s;
+  if constexpr (sizeof(T) == 4) {
+    t = pair2(expf(-fabsf(g0)), expf(-fabsf(g1)));
+    s = pair2(1.0f / (1.0f + lo2(t)), 1.0f / (1.0f + hi2(t)));
+  } else {
+    constexpr double kC = 0.72134752044448170368;               // log2(e) / 2
+    constexpr float kHead = static_cast<float>(kC), kTail = static_cast<float>(kC - static_cast<double>(kHead));
+    constexpr float kLn2 = 0.693147180559945f;
+    const u64 a = g | 0x8000000080000000ull;                    // -|g|
+    const u64 q = fmul2(a, pair2(kHead, kHead));
+    const u64 r = ffma2(a, pair2(kTail, kTail), ffma2(a, pair2(kHead, kHead), q ^ 0x8000000080000000ull));
+    float e0, e1;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(lo2(q)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(hi2(q)));
+    const u64 e = pair2(e0, e1), root = ffma2(e, fmul2(r, pair2(kLn2, kLn2)), e);
+    t = fmul2(root, root);
+    const u64 d = ffma2(root, root, pair2(1.0f, 1.0f));
+    float s0, s1;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s0) : "f"(lo2(d)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s1) : "f"(hi2(d)));
+    s = pair2(s0, s1);
+  }
+  const u64 ts = fmul2(t, s);
+  const bool p0 = g0 >= 0.f, p1 = g1 >= 0.f;                    // a NaN g leaves NaN in t
+  sig = pair2(p0 ? lo2(s) : lo2(ts), p1 ? hi2(s) : hi2(ts));
+  rest = pair2(p0 ? lo2(ts) : lo2(s), p1 ? hi2(ts) : hi2(s));
 }
 
 // A block's threads cover `rpb` rows of `upr` units (of V columns, whole
@@ -260,10 +296,9 @@ __global__ void __launch_bounds__(kCkThreads) checkpoint_unpack_kernel(const Che
       },
       [&](const CkUnit& q, const In& in) {
         if (!q.in) return;
-        float v[V];
-        ck_decode<V>(in.codes, ck_scale(in.e), v);
         Words<T, V> x;
-        x.put(v);
+#pragma unroll
+        for (int k = 0; k < (V + 1) / 2; ++k) x.put2(k, ck_decode2<V>(in.codes, k, ck_scale(in.e)));
         x.store(static_cast<T*>(a.x_out) + q.row * a.C + q.c);
       });
 }
@@ -294,15 +329,13 @@ __global__ void __launch_bounds__(kCkThreads) swiglu_act_kernel(const SwigluActA
       },
       [&](const CkUnit& q, const In& in) {
         if (q.in) {
-          float h[V];
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            float sig, rest;
-            sigmoid_parts<T>(in.g.get(j), sig, rest);
-            h[j] = in.g.get(j) * sig * in.u.get(j);
-          }
           Words<T, V> out;
-          out.put(h);
+#pragma unroll
+          for (int k = 0; k < (V + 1) / 2; ++k) {
+            u64 sig, rest;
+            sigmoid2<T>(in.g.get2(k), sig, rest);
+            out.put2(k, fmul2(fmul2(in.g.get2(k), sig), in.u.get2(k)));
+          }
           out.store(static_cast<T*>(a.h) + q.row * I + q.c);
         }
         if (a.codes == nullptr) return;
@@ -343,43 +376,44 @@ __global__ void __launch_bounds__(kCkThreads) swiglu_act_bwd_kernel(const Swiglu
       },
       [&](const CkUnit& q, const In& in) {
         if (!q.in) return;
-        float g[V], u[V], dg[V], du[V];
-        ck_decode<V>(in.g, ck_scale(in.eg), g);
-        ck_decode<V>(in.u, ck_scale(in.eu), u);
+        Words<T, V> dg, du, h;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          float sig, rest;
-          sigmoid_parts<T>(g[j], sig, rest);
-          const float d = in.dh.get(j), silu = g[j] * sig;
-          dg[j] = d * u[j] * (sig * fmaf(g[j], rest, 1.0f));
-          du[j] = d * silu;
-          u[j] *= silu;
+        for (int k = 0; k < (V + 1) / 2; ++k) {
+          const u64 g = ck_decode2<V>(in.g, k, ck_scale(in.eg)), u = ck_decode2<V>(in.u, k, ck_scale(in.eu));
+          const u64 d = in.dh.get2(k);
+          u64 sig, rest;
+          sigmoid2<T>(g, sig, rest);
+          const u64 silu = fmul2(g, sig);
+          dg.put2(k, fmul2(fmul2(d, u), fmul2(sig, ffma2(g, rest, pair2(1.0f, 1.0f)))));
+          du.put2(k, fmul2(d, silu));
+          h.put2(k, fmul2(u, silu));
         }
-        Words<T, V> out;
-        out.put(dg);
-        out.store(static_cast<T*>(a.dgu) + q.row * 2 * I + q.c);
-        out.put(du);
-        out.store(static_cast<T*>(a.dgu) + q.row * 2 * I + I + q.c);
-        if (a.h) {
-          out.put(u);
-          out.store(static_cast<T*>(a.h) + q.row * I + q.c);
-        }
+        dg.store(static_cast<T*>(a.dgu) + q.row * 2 * I + q.c);
+        du.store(static_cast<T*>(a.dgu) + q.row * 2 * I + I + q.c);
+        if (a.h) h.store(static_cast<T*>(a.h) + q.row * I + q.c);
       });
 }
 
 // ----------------------------------------------------------------- launches
-// Blocks of about 256 threads (whole rows where a row has fewer units), one
-// wave of them: blocks behind the first wave would run alone at the end.
+// Blocks of about 256 threads (whole rows where a row has fewer units), each
+// with about four steps, and at least one wave of them where there are so
+// many: the SMs do not run at one pace, so an even share of all rows to one
+// wave of blocks waits for the slowest (R = 32768, I = 2432, bf16: SwiGLU with
+// checkpoint 115 us, with four steps 94 us), while blocks of one step have no
+// next loads to run ahead (108 us).
 template <typename A>
 static cudaError_t ck_launch(void (*kern)(A, CkShape), const A& a, int64_t R, int64_t cols, int V, cudaStream_t st) {
   const int upr = static_cast<int>((cols + 31) / 32) * (32 / V);
   CkShape s{upr, upr >= 256 ? 1 : 256 / upr};
   const int64_t want = static_cast<int64_t>(s.rpb) * upr;
   const int threads = want >= kCkThreads ? kCkThreads : static_cast<int>((want + 31) / 32 * 32);
-  const int64_t blocks = (R + s.rpb - 1) / s.rpb;
-  const int64_t most = static_cast<int64_t>(num_sms()) * resident_blocks(reinterpret_cast<const void*>(kern), threads);
-  return launch_dependent_kernel(kern, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(threads), 0,
-                                 st, a, s);
+  const int64_t most = (R + s.rpb - 1) / s.rpb, parts = (upr + threads - 1) / threads;   // steps of a row
+  const int64_t wave = static_cast<int64_t>(num_sms()) * resident_blocks(reinterpret_cast<const void*>(kern), threads);
+  int64_t blocks = most * (s.rpb > 1 ? 1 : parts) / 4;
+  blocks = blocks > wave ? blocks : wave;
+  blocks = blocks < most ? blocks : most;
+  if (blocks > 0x7fffffff) blocks = 0x7fffffff;
+  return launch_dependent_kernel(kern, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0, st, a, s);
 }
 
 static inline int ck_vec(int64_t cols) { return cols % 16 == 0 ? 16 : cols % 8 == 0 ? 8 : cols % 4 == 0 ? 4 : 1; }

@@ -166,6 +166,16 @@ __device__ __forceinline__ u64 ffma2(u64 a, u64 b, u64 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+__device__ __forceinline__ u64 fmul2(u64 a, u64 b) {
+  u64 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ u64 pair2(float lo, float hi) {
+  return (static_cast<u64>(__float_as_uint(hi)) << 32) | __float_as_uint(lo);
+}
+__device__ __forceinline__ float lo2(u64 v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float hi2(u64 v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
 // Two bf16 (one 32-bit word, element 0 in the low half) widened to fp32.
 __device__ __forceinline__ u64 bf2(uint32_t w) {
   return (static_cast<u64>(w & 0xffff0000u) << 32) | static_cast<u64>(w << 16);
