@@ -150,6 +150,30 @@ __device__ __forceinline__ float bn_param(const void* w, int h) {
   return w ? static_cast<float>(static_cast<const T*>(w)[h]) : 1.f;
 }
 
+// w_pre and w_post g in fp32 by column, zeros behind the row (an absent w_pre
+// is zeros too: nothing is made of it; other absent factors are 1).  One
+// vector of each parameter a thread, so that their loads are in flight
+// together: a block waits for them once.
+template <typename T, int V, bool kTokenGate>
+__device__ __forceinline__ void stage_params(const void* pre, const void* post, const void* gate, int H, int tpr,
+                                             int span, float* w_pre, float* w_mid) {
+  using U = Unit<T, V>;
+  using P = Pack<T, V>;
+  for (int c = threadIdx.x; c < span / V; c += blockDim.x) {
+    const bool in = c < H / V;
+    typename P::Raw a, b, g;
+    if (in && pre) a = row_load<T, V>(pre, 0, c);
+    if (in && post) b = row_load<T, V>(post, 0, c);
+    if (in && gate && !kTokenGate) g = row_load<T, V>(gate, 0, c);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int place = U::place(c * V + j, tpr);
+      w_pre[place] = in && pre ? P::get(a, j) : 0.f;
+      w_mid[place] = in ? (post ? P::get(b, j) : 1.f) * (gate && !kTokenGate ? P::get(g, j) : 1.f) : 0.f;
+    }
+  }
+}
+
 // ------------------------------------------------------------------ forward
 constexpr size_t kBnMostSmem = 224 * 1024;   // dynamic, of 227 KB a block may have
 constexpr int kBnFwdThreads = 512;      // most threads of a block (one group of them: H = 16384)
@@ -267,17 +291,16 @@ block_norm_ring_kernel(const BlockNormFwd a, int tpr, int span) {
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
-  for (int i = 0; i < 2 * kIn * NU; ++i)      // what no copy will fill stays zero
-    *reinterpret_cast<Raw*>(ring + at(0, 0) + i * 32 * sizeof(Raw)) = U::zero();
+  for (int i = 0; i < kIn; ++i)               // what no copy will fill stays zero
+#pragma unroll
+    for (int m = 0; m < NU; ++m)
+      if (src[i] == nullptr || c0 + m * tpr >= nv)
+        for (int st = 0; st < 2; ++st) *reinterpret_cast<Raw*>(ring + st * kStageBytes + at(i, m)) = U::zero();
   pdl_enter();
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   int64_t t = static_cast<int64_t>(blockIdx.x) * groups + group;
   fetch(t, 0);
-  for (int h = threadIdx.x; h < span; h += blockDim.x) {
-    const int place = U::place(h, tpr);
-    w_mid[place] = h < a.H ? bn_param<T>(a.post_w, h) * bn_param<T>(kTokenGate ? nullptr : a.gate, h) : 0.f;
-    w_pre[place] = h < a.H && a.pre_w ? bn_param<T>(a.pre_w, h) : 0.f;
-  }
+  stage_params<T, V, kTokenGate>(a.pre_w, a.post_w, a.gate, a.H, tpr, span, w_pre, w_mid);
   __syncthreads();
   const u64 scale2 = pair2(a.residual_scale, a.residual_scale);
   for (int stage = 0; t < a.T; t += step, stage ^= 1) {
@@ -416,7 +439,9 @@ block_norm_bwd_kernel(const BlockNormBwd a, int tpr, int span, int stages) {
 #pragma unroll
       for (int i = 0; i < kIn; ++i)
 #pragma unroll
-        for (int m = 0; m < NU; ++m) *reinterpret_cast<Raw*>(ring + st * kStageBytes + at(i, m)) = U::zero();
+        for (int m = 0; m < NU; ++m)
+          if (src[i] == nullptr || c0 + m * tpr >= nv)
+            *reinterpret_cast<Raw*>(ring + st * kStageBytes + at(i, m)) = U::zero();
   } else {
 #pragma unroll
     for (int i = 0; i < kIn; ++i)
@@ -438,11 +463,7 @@ block_norm_bwd_kernel(const BlockNormBwd a, int tpr, int span, int stages) {
   };
   if (U::kAsync && stages == 2) fetch(t, 0);
   fetch_rstd(t);
-  for (int h = threadIdx.x; h < span; h += blockDim.x) {
-    const int place = U::place(h, tpr);
-    w_pre[place] = h < a.H && a.pre_w ? bn_param<T>(a.pre_w, h) : 0.f;
-    w_mid[place] = h < a.H ? bn_param<T>(a.post_w, h) * bn_param<T>(kTokenGate ? nullptr : a.gate, h) : 0.f;
-  }
+  stage_params<T, V, kTokenGate>(a.pre_w, a.post_w, a.gate, a.H, tpr, span, w_pre, w_mid);
   __syncthreads();
   u64 s_pre[NU][NP], s_mid[NU][NP];
 #pragma unroll
@@ -727,6 +748,8 @@ static BnBwdShape bn_bwd_shape_v(int64_t T, int H) {
     return s;
   }
   s.span = s.NU * s.tpr * width;
+  // one block an SM: a second wave costs a block's start and its sums again
+  // (T = 16384: 31 -> 34 us at H = 768, 124 -> 131 us at H = 4096)
   s.groups = kBnBwdThreads / s.tpr;
   const int64_t want = (T + s.groups - 1) / s.groups;
   s.grid = static_cast<int>(want < sms ? (want > 0 ? want : 1) : sms);
@@ -762,7 +785,14 @@ static cudaError_t bn_ring_launch(const BlockNormFwd& a, int tpr, cudaStream_t s
   auto kern = token_gate ? block_norm_ring_kernel<T, V, NU, true> : block_norm_ring_kernel<T, V, NU, false>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent_kernel(kern, dim3(static_cast<unsigned>(sms)), dim3(groups * tpr), smem, st, a, tpr, span);
+  // Three waves of blocks where an SM's share is above 2 MB, else one: the SMs
+  // do not run at one pace, so an even share waits for the slowest, but each
+  // block starts with a load it has nothing to run under (1 / 3 waves, us:
+  // 268 MB 46.6 / 50.5, 403 MB 68.1 / 63.2, 671 MB 108 / 100).
+  const int64_t share = a.T * a.H * static_cast<int64_t>(sizeof(T)) * (2 + token_gate + 1 + (a.pre_w != nullptr)) / sms;
+  const int64_t want = (a.T + groups - 1) / groups, most = share > (2 << 20) ? 3 * sms : sms;
+  return launch_dependent_kernel(kern, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(groups * tpr),
+                                 smem, st, a, tpr, span);
 }
 template <typename T, int V>
 static cudaError_t bn_ring_pick(const BlockNormFwd& a, cudaStream_t st) {
