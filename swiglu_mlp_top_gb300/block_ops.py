@@ -166,8 +166,11 @@ def block_norm_backward(dn: Optional[torch.Tensor], dr: Optional[torch.Tensor],
     pdr, pf = _arg(dr, "dr", dev, dtype, shape), _arg(f, "f", dev, dtype, shape)
     lib = L.load()
     if workspace is None:
-        workspace = _empty(lib.mm_block_norm_backward_workspace_bytes(T, H, dt), torch.uint8, dev, stream)
-    pws, nbytes = _scratch(workspace, dev, "block_norm_backward")
+        nbytes = lib.mm_block_norm_backward_workspace_bytes(T, H, dt)
+        workspace = _empty(nbytes, torch.uint8, dev, stream)
+        pws = workspace.data_ptr()
+    else:
+        pws, nbytes = _scratch(workspace, dev, "block_norm_backward")
     out = {"dx": _empty(shape, dtype, dev, stream)}
     pdf = pdpost = pdgate = pdpre = None
     if f is not None:
@@ -199,6 +202,15 @@ def moe_permute_workspace_bytes(T: int, E: int, k: int) -> int:
     return int(L.load().mm_moe_permute_workspace_bytes(T, E, k))
 
 
+def _table(plan: dict, key: str, shape, dev: int, stream) -> int:
+    """Address of an index table of the plan, made where it is not there."""
+    t = plan.get(key)
+    if t is not None:
+        return _arg(t, key, dev, torch.int32, shape)
+    t = plan[key] = _empty(shape, torch.int32, dev, stream)
+    return t.data_ptr()
+
+
 def moe_permute(x: torch.Tensor, topk_idx: torch.Tensor, E: int, *, align: int = 1,
                 out: Optional[torch.Tensor] = None, plan: Optional[dict] = None,
                 workspace: Optional[torch.Tensor] = None, stream=None):
@@ -222,17 +234,18 @@ def moe_permute(x: torch.Tensor, topk_idx: torch.Tensor, E: int, *, align: int =
         raise L.MMError(L.MM_ERR_UNSUPPORTED, "mm_moe_permute")
     plan = {} if plan is None else plan
     if workspace is None:
-        workspace = _empty(lib.mm_moe_permute_workspace_bytes(T, E, k), torch.uint8, dev, stream)
-    pws, nbytes = _scratch(workspace, dev, "moe_permute")
+        nbytes = lib.mm_moe_permute_workspace_bytes(T, E, k)
+        workspace = _empty(nbytes, torch.uint8, dev, stream)
+        pws = workspace.data_ptr()
+    else:
+        pws, nbytes = _scratch(workspace, dev, "moe_permute")
     if out is None:
         out = _empty((R, H), x.dtype, dev, stream)
-    ptrs = []
-    for key, shape in (("offsets", (E + 1,)), ("counts", (E,)), ("perm", (R,)), ("pos", (T, k))):
-        if plan.get(key) is None:
-            plan[key] = _empty(shape, torch.int32, dev, stream)
-        ptrs.append(_arg(plan[key], key, dev, torch.int32, shape))
-    rc = lib.mm_moe_permute(px, pi, T, H, E, k, align, dt, _arg(out, "out", dev, x.dtype, (R, H)),
-                            *ptrs, pws, nbytes, raw)
+    po = _arg(out, "out", dev, x.dtype, (R, H))
+    rc = lib.mm_moe_permute(
+        px, pi, T, H, E, k, align, dt, po, _table(plan, "offsets", (E + 1,), dev, stream),
+        _table(plan, "counts", (E,), dev, stream), _table(plan, "perm", (R,), dev, stream),
+        _table(plan, "pos", (T, k), dev, stream), pws, nbytes, raw)
     L.check(rc, "mm_moe_permute")
     return out, plan
 

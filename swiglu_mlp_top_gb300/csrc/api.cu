@@ -1000,7 +1000,7 @@ int mm_block_norm_backward(const void* dn, const void* dr, const void* r, const 
     e = counted_launch(MM_KERNEL_NORM, st, [&] { return launch_block_norm_bwd_rows(dtype, a, st); });
     if (e != cudaSuccess) return cuda_fail(e, "block norm backward");
   }
-  if (pre_w || post_w || (gate && !token_gate)) {
+  if ((pre_w || post_w || (gate && !token_gate)) && !block_norm_bwd_one_block(T, H, dtype)) {
     e = counted_launch(MM_KERNEL_NORM, st, [&] { return launch_block_norm_bwd_cols(dtype, a, st); });
     if (e != cudaSuccess) return cuda_fail(e, "block norm backward sums");
   }

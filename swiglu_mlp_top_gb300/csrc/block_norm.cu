@@ -384,6 +384,28 @@ block_norm_ring_kernel(const BlockNormFwd a, int tpr, int span) {
 constexpr int kBnBwdThreads = 512;      // 128 registers a thread
 constexpr int kBnSums = 2;              // d_pre_w, M
 
+// Column h of sum q, complete: to the gradients that follow from it.
+template <typename T>
+__device__ __forceinline__ void bn_finish(const BlockNormBwd& a, int q, int h, float s) {
+  if (q == 0) {
+    if (a.d_pre_w) a.d_pre_w[h] = s;
+    return;
+  }
+  float* d_gate = a.gate && !a.gate_per_token ? static_cast<float*>(a.d_gate) : nullptr;
+  if (a.d_post_w) a.d_post_w[h] = d_gate ? s * bn_param<T>(a.gate, h) : s;
+  if (d_gate) d_gate[h] = a.post_w ? s * bn_param<T>(a.post_w, h) : s;
+}
+
+// No tokens: zeros, whatever the parameters hold.
+__device__ __forceinline__ void bn_zero(const BlockNormBwd& a, int q, int h) {
+  if (q == 0) {
+    if (a.d_pre_w) a.d_pre_w[h] = 0.f;
+    return;
+  }
+  if (a.d_post_w) a.d_post_w[h] = 0.f;
+  if (a.gate && !a.gate_per_token) static_cast<float*>(a.d_gate)[h] = 0.f;
+}
+
 // NU units a thread.  The next row's inputs are copied to shared memory with
 // cp.async while this one is worked on (`stages` 2; 1 where two do not fit):
 // each thread copies and reads its own slots only, so the ring needs no
@@ -560,7 +582,8 @@ block_norm_bwd_kernel(const BlockNormBwd a, int tpr, int span, int stages) {
     for (int q = 0; q < kBnSums; ++q) {
       float sum = 0.f;
       for (int gi = 0; gi < groups; ++gi) sum += behind[(gi * kBnSums + q) * span + place];
-      part[q * a.H + h] = sum;
+      if (gridDim.x == 1) bn_finish<T>(a, q, h, sum);
+      else part[q * a.H + h] = sum;
     }
   }
 }
@@ -670,7 +693,11 @@ __global__ void __launch_bounds__(kBnFwdThreads, 1) block_norm_bwd_wide_kernel(c
 #pragma unroll
     for (int j = 0; j < V; ++j)
 #pragma unroll
-      for (int q = 0; q < kBnSums; ++q) part[q * a.H + c * V + j] = cols[q * a.H + c * V + j];
+      for (int q = 0; q < kBnSums; ++q) {
+        const int h = c * V + j;
+        if (gridDim.x == 1) bn_finish<T>(a, q, h, cols[q * a.H + h]);
+        else part[q * a.H + h] = cols[q * a.H + h];
+      }
 }
 
 // Sums over the blocks' partials: 32 columns x 32 slices of the blocks per
@@ -683,8 +710,7 @@ block_norm_bwd_sum_kernel(const BlockNormBwd a, int nblk) {
   pdl_enter();
   __shared__ float red[kBnSlices][32];
   const int h = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5, q = blockIdx.y;
-  float* d_gate = a.gate && !a.gate_per_token ? static_cast<float*>(a.d_gate) : nullptr;
-  if (q == 0 ? a.d_pre_w == nullptr : (a.d_post_w == nullptr && d_gate == nullptr)) return;
+  if (q == 0 ? a.d_pre_w == nullptr : (a.d_post_w == nullptr && (a.gate == nullptr || a.gate_per_token))) return;
   float s = 0.f;
   if (h < a.H)
 #pragma unroll 8
@@ -696,12 +722,8 @@ block_norm_bwd_sum_kernel(const BlockNormBwd a, int nblk) {
     s = 0.f;
 #pragma unroll
     for (int i = 0; i < kBnSlices; ++i) s += red[i][threadIdx.x];
-    if (q == 0) {
-      a.d_pre_w[h] = s;
-    } else {
-      if (a.d_post_w) a.d_post_w[h] = d_gate ? s * bn_param<T>(a.gate, h) : s;
-      if (d_gate) d_gate[h] = a.post_w ? s * bn_param<T>(a.post_w, h) : s;
-    }
+    if (nblk > 0) bn_finish<T>(a, q, h, s);
+    else bn_zero(a, q, h);
   }
 }
 
@@ -870,6 +892,10 @@ cudaError_t launch_block_norm_bwd_rows(int dtype, const BlockNormBwd& a, cudaStr
   if (dtype == kDtypeBF16)
     return s.V == 8 ? bn_bwd_pick<__nv_bfloat16, 8>(a, s, st) : bn_bwd_pick<__nv_bfloat16, 1>(a, s, st);
   return s.V == 4 ? bn_bwd_pick<float, 4>(a, s, st) : bn_bwd_pick<float, 1>(a, s, st);
+}
+
+bool block_norm_bwd_one_block(int64_t T, int H, int dtype) {
+  return T > 0 && bn_bwd_shape(T, H, dtype).grid == 1;
 }
 
 cudaError_t launch_block_norm_bwd_cols(int dtype, const BlockNormBwd& a, cudaStream_t st) {

@@ -404,6 +404,8 @@ struct BlockNormBwd {
 size_t block_norm_bwd_bytes(int64_t T, int H, int dtype);
 cudaError_t launch_block_norm(int dtype, const BlockNormFwd& a, cudaStream_t st);
 cudaError_t launch_block_norm_bwd_rows(int dtype, const BlockNormBwd& a, cudaStream_t st);
+// One block has all the rows: its kernel writes the column sums itself.
+bool block_norm_bwd_one_block(int64_t T, int H, int dtype);
 cudaError_t launch_block_norm_bwd_cols(int dtype, const BlockNormBwd& a, cudaStream_t st);
 
 // Tokens sorted by expert and back (permute.cu).
