@@ -1037,11 +1037,13 @@ int mm_moe_permute(const void* x, const int32_t* topk_idx, int64_t T, int H, int
   const PermuteArgs a{x, topk_idx, xs, offsets, counts, perm, pos, ws_at(workspace, sizeof(WsHeader)),
                       T, rows, H, E, k, align};
   cudaError_t e;
-  if (permute_launches(T, k) > 1) {
+  if (permute_counts_first(T, k)) {
     e = counted_launch(MM_KERNEL_PERMUTE, st, [&] { return launch_permute_count(a, st); });
     if (e != cudaSuccess) return cuda_fail(e, "permute count");
   }
   e = counted_launch(MM_KERNEL_PERMUTE, st, [&] { return launch_permute(dtype, a, st); });
+  if (e == cudaSuccess && T > 0 && permute_copies_apart(dtype, a))
+    e = counted_launch(MM_KERNEL_PERMUTE, st, [&] { return launch_permute_rows(dtype, a, st); });
   return e == cudaSuccess ? MM_OK : cuda_fail(e, "permute");
 }
 

@@ -442,9 +442,11 @@ struct UnpermuteBwdArgs {
   int H, E, k;
 };
 size_t permute_bytes(int64_t T, int E, int k);
-int permute_launches(int64_t T, int k);           // 2: the counts first, 1: in one kernel
+bool permute_counts_first(int64_t T, int k);      // launch_permute_count comes first
 cudaError_t launch_permute_count(const PermuteArgs& a, cudaStream_t st);
 cudaError_t launch_permute(int dtype, const PermuteArgs& a, cudaStream_t st);
+bool permute_copies_apart(int dtype, const PermuteArgs& a);   // launch_permute_rows comes last
+cudaError_t launch_permute_rows(int dtype, const PermuteArgs& a, cudaStream_t st);
 cudaError_t launch_unpermute(int dtype, const UnpermuteArgs& a, cudaStream_t st);
 cudaError_t launch_unpermute_bwd(int dtype, const UnpermuteBwdArgs& a, cudaStream_t st);
 

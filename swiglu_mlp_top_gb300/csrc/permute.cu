@@ -13,7 +13,7 @@ constexpr int kPmThreads = 512;         // sort and copy: two blocks an SM
 constexpr int kPmWarps = kPmThreads / 32;
 constexpr int kPmBatch = 4;             // vectors of a row in flight a lane
 constexpr int kPmKept = 2048;           // positions of a block kept in shared memory
-constexpr int kPmRowThreads = 256;      // combine and its gradient
+constexpr int kPmRowThreads = 128;      // combine and its gradient: small blocks, which even out the SMs' paces
 
 // Calls f(row) for the padding rows of every group, shared out over the grid's
 // warps (this one is w of n); the whole warp calls.  Rows are kept inside
@@ -91,12 +91,12 @@ __global__ void __launch_bounds__(128) permute_count_kernel(const PermuteArgs a,
 // Block b owns the assignments of `tokens` tokens from b * tokens on.  It
 // works out its own base in every group - from the blocks' counts, or
 // (blk_cnt null: few assignments) by counting all of them itself, which
-// saves a launch - then its assignments' ranks, and copies its rows, a warp
-// per token: one load, a store for each of the token's assignments.  The
+// saves a launch - then its assignments' ranks, and (copy) copies its rows, a
+// warp per token: one load, a store for each of the token's assignments.  The
 // rows are asked for (to L2) before the indices are worked out.
 template <typename Vec>
 __global__ void __launch_bounds__(kPmThreads, 2)
-permute_kernel(const PermuteArgs a, int tokens, const int32_t* blk_cnt, int row_bytes) {
+permute_kernel(const PermuteArgs a, int tokens, const int32_t* blk_cnt, int row_bytes, int copy) {
   __shared__ int s_tot[MM_MAX_EXPERTS], s_next[MM_MAX_EXPERTS], s_off[MM_MAX_EXPERTS + 1];
   __shared__ int s_warp[kPmWarps][MM_MAX_EXPERTS];
   __shared__ int s_pos[kPmKept];
@@ -105,7 +105,7 @@ permute_kernel(const PermuteArgs a, int tokens, const int32_t* blk_cnt, int row_
   const int nt = static_cast<int>(a.T - t0 < tokens ? a.T - t0 : tokens), na = nt * a.k;
   const int32_t* idx = a.topk_idx + t0 * a.k;
   const char* x = static_cast<const char*>(a.x) + t0 * row_bytes;
-  if (sizeof(Vec) == 16 && tid == 0) {
+  if (copy && sizeof(Vec) == 16 && tid == 0) {
     // at most 64 KB a block: 20 MB over the grid, well inside L2
     const int64_t all = static_cast<int64_t>(nt) * row_bytes, bytes = all < 65536 ? all : 65536;
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(x), "r"(static_cast<uint32_t>(bytes)) : "memory");
@@ -193,8 +193,8 @@ permute_kernel(const PermuteArgs a, int tokens, const int32_t* blk_cnt, int row_
     __syncthreads();
   }
   // rows: the next piece's load is under way while this one is stored
-  if (warp < nt) fetch(warp, 0);
-  for (int token = warp, chunk = 0; token < nt;) {
+  if (copy && warp < nt) fetch(warp, 0);
+  for (int token = warp, chunk = 0; copy && token < nt;) {
     Vec now[kPmBatch];
 #pragma unroll
     for (int i = 0; i < kPmBatch; ++i) now[i] = v[i];
@@ -221,7 +221,7 @@ permute_kernel(const PermuteArgs a, int tokens, const int32_t* blk_cnt, int row_
   if (a.align > 1)
     each_padding_row(s_off, s_tot, a.E, a.rows, wg, nw, [&](int64_t row) {
       Vec* dst = reinterpret_cast<Vec*>(static_cast<char*>(a.xs) + row * row_bytes);
-      for (int c = lane; c < nv; c += 32) dst[c] = Vec{};
+      for (int c = lane; copy && c < nv; c += 32) dst[c] = Vec{};
       if (lane == 0) a.perm[row] = -1;
     });
   for (int64_t r = s_off[a.E] + static_cast<int64_t>(blockIdx.x) * kPmThreads + tid; r < a.rows;
@@ -351,7 +351,14 @@ size_t permute_bytes(int64_t T, int E, int k) {
   return T * k <= kPmCountOwn ? 0 : 4 * static_cast<size_t>(E) * pm_blocks(T);
 }
 
-int permute_launches(int64_t T, int k) { return T * k <= kPmCountOwn ? 1 : 2; }
+bool permute_counts_first(int64_t T, int k) { return T * k > kPmCountOwn; }
+
+// Writes bound the copy (this GPU fills memory at 3.7-4.0 TB/s, against 6.8 of
+// a copy's two directions together).  From 256 MB of rows on, the tables are
+// made alone and the rows copied by the gradient's kernel, whose small blocks
+// even out the SMs' paces: T = 16384, k = 4, H = 4096 (537 MB) 128 -> 119 us;
+// at T = 16384, k = 2, H = 2048 (134 MB) the launch costs what it gives.
+static bool pm_copy_apart(int64_t T, int k, int row_bytes) { return T * k * row_bytes >= (256ll << 20); }
 
 static int pm_tokens(const PermuteArgs& a) {
   const int b = pm_blocks(a.T);
@@ -370,10 +377,10 @@ cudaError_t launch_permute_count(const PermuteArgs& a, cudaStream_t st) {
 cudaError_t launch_permute(int dtype, const PermuteArgs& a, cudaStream_t st) {
   if (a.T == 0) return launch_dependent_kernel(permute_empty_kernel, dim3(1), dim3(128), 0, st, a);
   const int row_bytes = a.H * (dtype == kDtypeBF16 ? 2 : 4);
-  const int32_t* cnt = permute_launches(a.T, a.k) > 1 ? static_cast<const int32_t*>(a.scratch) : nullptr;
+  const int32_t* cnt = permute_counts_first(a.T, a.k) ? static_cast<const int32_t*>(a.scratch) : nullptr;
   auto run = [&](auto kern) {
     return launch_dependent_kernel(kern, pm_grid(a), dim3(kPmThreads), 0, st, a, pm_tokens(a), cnt,
-                                   row_bytes);
+                                   row_bytes, pm_copy_apart(a.T, a.k, row_bytes) ? 0 : 1);
   };
   if (row_bytes % 16 == 0) return run(permute_kernel<uint4>);
   if (row_bytes % 4 == 0) return run(permute_kernel<uint32_t>);
@@ -425,6 +432,14 @@ cudaError_t launch_unpermute_bwd(int dtype, const UnpermuteBwdArgs& a, cudaStrea
     return unpermute_bwd_pick<__nv_bfloat16, 1>(a, st);
   }
   return a.H % 4 == 0 ? unpermute_bwd_pick<float, 4>(a, st) : unpermute_bwd_pick<float, 1>(a, st);
+}
+
+bool permute_copies_apart(int dtype, const PermuteArgs& a) {
+  return pm_copy_apart(a.T, a.k, a.H * (dtype == kDtypeBF16 ? 2 : 4));
+}
+cudaError_t launch_permute_rows(int dtype, const PermuteArgs& a, cudaStream_t st) {
+  return launch_unpermute_bwd(dtype, UnpermuteBwdArgs{a.x, nullptr, a.pos, nullptr, a.offsets, a.counts, a.xs, nullptr,
+                                                      a.T, a.rows, a.H, a.E, a.k}, st);
 }
 
 }  // namespace mm
