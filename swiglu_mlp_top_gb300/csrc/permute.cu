@@ -11,7 +11,6 @@ namespace mm {
 
 constexpr int kPmThreads = 512;         // sort and copy: two blocks an SM
 constexpr int kPmWarps = kPmThreads / 32;
-constexpr int kPmBatch = 4;             // vectors of a row in flight a lane
 constexpr int kPmKept = 2048;           // positions of a block kept in shared memory
 constexpr int kPmRowThreads = 128;      // combine and its gradient: small blocks, which even out the SMs' paces
 
@@ -97,6 +96,7 @@ __global__ void __launch_bounds__(128) permute_count_kernel(const PermuteArgs a,
 template <typename Vec>
 __global__ void __launch_bounds__(kPmThreads, 2)
 permute_kernel(const PermuteArgs a, int tokens, const int32_t* blk_cnt, int row_bytes, int copy) {
+  constexpr int kBatch = sizeof(Vec) == 16 ? 4 : 12;      // vectors of a row in flight a lane
   __shared__ int s_tot[MM_MAX_EXPERTS], s_next[MM_MAX_EXPERTS], s_off[MM_MAX_EXPERTS + 1];
   __shared__ int s_warp[kPmWarps][MM_MAX_EXPERTS];
   __shared__ int s_pos[kPmKept];
@@ -112,13 +112,13 @@ permute_kernel(const PermuteArgs a, int tokens, const int32_t* blk_cnt, int row_
   }
   for (int e = tid; e < a.E; e += kPmThreads) s_tot[e] = s_next[e] = 0;
   pdl_enter();
-  const int nv = row_bytes / static_cast<int>(sizeof(Vec)), chunks = (nv + 32 * kPmBatch - 1) / (32 * kPmBatch);
-  Vec v[kPmBatch];
+  const int nv = row_bytes / static_cast<int>(sizeof(Vec)), chunks = (nv + 32 * kBatch - 1) / (32 * kBatch);
+  Vec v[kBatch];
   auto fetch = [&](int token, int chunk) {
     const Vec* src = reinterpret_cast<const Vec*>(x + static_cast<int64_t>(token) * row_bytes);
-    const int c = chunk * (32 * kPmBatch) + lane;
+    const int c = chunk * (32 * kBatch) + lane;
 #pragma unroll
-    for (int i = 0; i < kPmBatch; ++i)
+    for (int i = 0; i < kBatch; ++i)
       if (c + 32 * i < nv) v[i] = src[c + 32 * i];
   };
   __syncthreads();
@@ -195,10 +195,10 @@ permute_kernel(const PermuteArgs a, int tokens, const int32_t* blk_cnt, int row_
   // rows: the next piece's load is under way while this one is stored
   if (copy && warp < nt) fetch(warp, 0);
   for (int token = warp, chunk = 0; copy && token < nt;) {
-    Vec now[kPmBatch];
+    Vec now[kBatch];
 #pragma unroll
-    for (int i = 0; i < kPmBatch; ++i) now[i] = v[i];
-    const int c = chunk * (32 * kPmBatch) + lane, first = token * a.k;
+    for (int i = 0; i < kBatch; ++i) now[i] = v[i];
+    const int c = chunk * (32 * kBatch) + lane, first = token * a.k;
     if (++chunk == chunks) {
       chunk = 0;
       token += kPmWarps;
@@ -209,7 +209,7 @@ permute_kernel(const PermuteArgs a, int tokens, const int32_t* blk_cnt, int row_
       if (row < 0) continue;
       Vec* dst = reinterpret_cast<Vec*>(static_cast<char*>(a.xs) + row * row_bytes);
 #pragma unroll
-      for (int i = 0; i < kPmBatch; ++i)
+      for (int i = 0; i < kBatch; ++i)
         if (c + 32 * i < nv) dst[c + 32 * i] = now[i];
     }
   }
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kPmRowThreads) unpermute_kernel(const Unpermut
 }
 
 // dys[pos] = w dy, dw = <dy, ys[pos]>: a warp per token, dy read once.
-template <typename T, int V, int KP>
+template <typename T, int V, int KP, int NB>
 __global__ void __launch_bounds__(kPmRowThreads) unpermute_bwd_kernel(const UnpermuteBwdArgs a) {
   using P = Pack<T, V>;
   pdl_enter();
@@ -298,23 +298,31 @@ __global__ void __launch_bounds__(kPmRowThreads) unpermute_bwd_kernel(const Unpe
       w[s] = __shfl_sync(0xffffffffu, my_w, s);
       dot[s] = 0.f;
     }
-    for (int c = lane; c < nv; c += 32) {
-      const auto g = row_load<T, V>(a.dy, t * a.H, c);
-      typename P::Raw raw[KP];
+    for (int c = lane; c < nv; c += 32 * NB) {
+      typename P::Raw g[NB], raw[KP][NB];
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+        g[i] = c + 32 * i < nv ? row_load<T, V>(a.dy, t * a.H, c + 32 * i) : typename P::Raw{};
       if (a.dw)
 #pragma unroll
         for (int s = 0; s < KP; ++s)
-          raw[s] = row[s] >= 0 ? row_load<T, V>(a.ys, row[s] * a.H, c) : typename P::Raw{};
+#pragma unroll
+          for (int i = 0; i < NB; ++i)
+            raw[s][i] = row[s] >= 0 && c + 32 * i < nv ? row_load<T, V>(a.ys, row[s] * a.H, c + 32 * i)
+                                                       : typename P::Raw{};
 #pragma unroll
       for (int s = 0; s < KP; ++s) {
         if (row[s] < 0) continue;
-        float v[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          if (a.dw) dot[s] = fmaf(P::get(g, j), P::get(raw[s], j), dot[s]);
-          v[j] = w[s] * P::get(g, j);
+        for (int i = 0; i < NB; ++i) {
+          float v[V];
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            if (a.dw) dot[s] = fmaf(P::get(g[i], j), P::get(raw[s][i], j), dot[s]);
+            v[j] = w[s] * P::get(g[i], j);
+          }
+          if (c + 32 * i < nv) row_store<T, V>(a.dys, row[s] * a.H, c + 32 * i, v);
         }
-        row_store<T, V>(a.dys, row[s] * a.H, c, v);
       }
     }
     if (a.dw) {
@@ -392,16 +400,21 @@ static unsigned pm_row_blocks(int64_t T) {
   return static_cast<unsigned>((T + kPmRowThreads / 32 - 1) / (kPmRowThreads / 32));
 }
 
+// Narrow accesses (rows that are not 16-byte aligned): more of them in flight.
+template <typename T, int V>
+constexpr int pm_wide() { return V * sizeof(T) == 16 ? 1 : 4; }
+
 template <typename T, int V>
 static cudaError_t unpermute_pick(const UnpermuteArgs& a, cudaStream_t st) {
+  constexpr int kWide = pm_wide<T, V>();
   auto run = [&](auto kern) {
     return launch_dependent_kernel(kern, dim3(pm_row_blocks(a.T)), dim3(kPmRowThreads), 0, st, a);
   };
   switch (pm_kp(a.k)) {
-    case 1: return run(unpermute_kernel<T, V, 1, 4>);
-    case 2: return run(unpermute_kernel<T, V, 2, 4>);
-    case 4: return run(unpermute_kernel<T, V, 4, 2>);
-    default: return run(unpermute_kernel<T, V, 8, 1>);
+    case 1: return run(unpermute_kernel<T, V, 1, 4 * kWide>);
+    case 2: return run(unpermute_kernel<T, V, 2, 4 * kWide>);
+    case 4: return run(unpermute_kernel<T, V, 4, 2 * kWide>);
+    default: return run(unpermute_kernel<T, V, 8, kWide>);
   }
 }
 cudaError_t launch_unpermute(int dtype, const UnpermuteArgs& a, cudaStream_t st) {
@@ -418,11 +431,12 @@ static cudaError_t unpermute_bwd_pick(const UnpermuteBwdArgs& a, cudaStream_t st
   auto run = [&](auto kern) {
     return launch_dependent_kernel(kern, dim3(pm_row_blocks(a.T)), dim3(kPmRowThreads), 0, st, a);
   };
+  constexpr int kWide = pm_wide<T, V>();
   switch (pm_kp(a.k)) {
-    case 1: return run(unpermute_bwd_kernel<T, V, 1>);
-    case 2: return run(unpermute_bwd_kernel<T, V, 2>);
-    case 4: return run(unpermute_bwd_kernel<T, V, 4>);
-    default: return run(unpermute_bwd_kernel<T, V, 8>);
+    case 1: return run(unpermute_bwd_kernel<T, V, 1, kWide>);
+    case 2: return run(unpermute_bwd_kernel<T, V, 2, kWide>);
+    case 4: return run(unpermute_bwd_kernel<T, V, 4, kWide>);
+    default: return run(unpermute_bwd_kernel<T, V, 8, kWide>);
   }
 }
 cudaError_t launch_unpermute_bwd(int dtype, const UnpermuteBwdArgs& a, cudaStream_t st) {
