@@ -7,19 +7,20 @@
 // All kernels stream: each input is read and each output written once.  A
 // thread owns V consecutive columns (V / 32 of a group), always the same ones
 // of a row, and walks down the rows; V is the widest of 16, 8 and 4 that
-// divides the width (so that values and codes move in whole aligned
-// accesses), else 1.
+// divides the width, so that values and codes move in whole aligned accesses.
+// Rows of other widths go in strips of 128 columns, a warp each: a lane has
+// one column of each of the strip's four groups, and single accesses.
 #include "mm_kernels.cuh"
 
 namespace mm {
 
 constexpr int kCkThreads = 512;         // most threads of a block
 
-// V elements of T as 32-bit words (V = 1 of bf16: the low half of one).
+// V elements of T (4, 8 or 16) as 32-bit words.
 template <typename T, int V>
 struct Words {
   static constexpr int kBytes = V * static_cast<int>(sizeof(T));
-  static constexpr int kN = (kBytes + 3) / 4;
+  static constexpr int kN = kBytes / 4;
   uint32_t w[kN];
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -35,12 +36,8 @@ struct Words {
     } else if constexpr (kBytes == 8) {
       const uint2 q = *static_cast<const uint2*>(p);
       w[0] = q.x; w[1] = q.y;
-    } else if constexpr (kBytes == 4) {
-      w[0] = *static_cast<const uint32_t*>(p);
-    } else if constexpr (kBytes == 2) {
-      w[0] = *static_cast<const uint16_t*>(p);
     } else {
-      w[0] = *static_cast<const uint8_t*>(p);
+      w[0] = *static_cast<const uint32_t*>(p);
     }
   }
   __device__ __forceinline__ void store(void* p) const {
@@ -50,12 +47,8 @@ struct Words {
         static_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     } else if constexpr (kBytes == 8) {
       *static_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-    } else if constexpr (kBytes == 4) {
-      *static_cast<uint32_t*>(p) = w[0];
-    } else if constexpr (kBytes == 2) {
-      *static_cast<uint16_t*>(p) = static_cast<uint16_t>(w[0]);
     } else {
-      *static_cast<uint8_t*>(p) = static_cast<uint8_t>(w[0]);
+      *static_cast<uint32_t*>(p) = w[0];
     }
   }
   __device__ __forceinline__ float get(int j) const {
@@ -66,21 +59,19 @@ struct Words {
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
       for (int j = 0; j < V; ++j) w[j] = __float_as_uint(v[j]);
-    } else if constexpr (V == 1) {
-      w[0] = pack_bf16x2(v[0], 0.f);
     } else {
 #pragma unroll
       for (int j = 0; j < V; j += 2) w[j / 2] = pack_bf16x2(v[j], v[j + 1]);
     }
   }
-  // Elements 2k and 2k + 1 (V = 1: the one, and zero).
-  __device__ __forceinline__ u64 get2(int k) const { return pair2(get(2 * k), V > 1 ? get(V > 1 ? 2 * k + 1 : 0) : 0.f); }
+  // Elements 2k and 2k + 1.
+  __device__ __forceinline__ u64 get2(int k) const { return pair2(get(2 * k), get(2 * k + 1)); }
   __device__ __forceinline__ void put2(int k, u64 v) {
     if constexpr (sizeof(T) == 2) {
       w[k] = pack_bf16x2(lo2(v), hi2(v));
     } else {
       w[2 * k] = __float_as_uint(lo2(v));
-      if constexpr (V > 1) w[2 * k + 1] = __float_as_uint(hi2(v));
+      w[2 * k + 1] = __float_as_uint(hi2(v));
     }
   }
   // The largest |value| as the bits of an fp32; infinities and NaN order above.
@@ -111,7 +102,6 @@ __device__ __forceinline__ uint32_t ck_exponent(uint32_t amax) {
 
 template <int V>
 __device__ __forceinline__ uint32_t group_max(uint32_t m) {
-  if constexpr (V == 1) return __reduce_max_sync(0xffffffffu, m);
 #pragma unroll
   for (int o = 1; o < 32 / V; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   return m;
@@ -136,18 +126,14 @@ __device__ __forceinline__ uint32_t ck_encode(Words<T, V> x, Words<Code, V>& cod
   }
   const uint32_t e = ck_exponent(amax);
   const float inv = ck_scale(254u - e);
-  uint16_t c[(V + 1) / 2];
+  uint16_t c[V / 2];
 #pragma unroll
-  for (int k = 0; k < (V + 1) / 2; ++k) {
+  for (int k = 0; k < V / 2; ++k) {
     const u64 v = fmul2(x.get2(k), pair2(inv, inv));
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c[k]) : "f"(hi2(v)), "f"(lo2(v)));
   }
-  if constexpr (V >= 4) {
 #pragma unroll
-    for (int i = 0; i < V / 4; ++i) codes.w[i] = c[2 * i] | (static_cast<uint32_t>(c[2 * i + 1]) << 16);
-  } else {
-    codes.w[0] = c[0] & 0xffu;
-  }
+  for (int i = 0; i < V / 4; ++i) codes.w[i] = c[2 * i] | (static_cast<uint32_t>(c[2 * i + 1]) << 16);
   return e;
 }
 
@@ -220,7 +206,7 @@ struct CkUnit {
 // whole block goes through the same number of steps.  The next unit's loads
 // are issued before this one's body, so that a block's arithmetic runs under
 // its loads (R = 32768, I = 2432, bf16: SwiGLU with checkpoint 124 us without).
-template <int V, typename L, typename F>
+template <int V, bool kStrip = false, typename L, typename F>
 __device__ __forceinline__ void each_unit(const CkShape& s, int64_t R, int64_t cols, L&& load, F&& body) {
   const int lrow = s.rpb > 1 ? static_cast<int>(threadIdx.x) / s.upr : 0;
   const int u0 = static_cast<int>(threadIdx.x) - lrow * s.upr;
@@ -230,11 +216,18 @@ __device__ __forceinline__ void each_unit(const CkShape& s, int64_t R, int64_t c
     const int u = part + u0;
     CkUnit q;
     q.row = r + lrow;
-    q.c = static_cast<int64_t>(u) * V;
-    q.g = u / (32 / V);
     const bool own = lrow < s.rpb && u < s.upr && q.row < R;
-    q.in = own && q.c < cols;
-    q.lead = own && u % (32 / V) == 0;
+    if constexpr (kStrip) {                   // the lane's column of the first group
+      q.c = (u >> 5) * 128 + (u & 31);
+      q.g = (u >> 5) * 4;
+      q.in = own;
+      q.lead = own && (u & 31) == 0;
+    } else {
+      q.c = static_cast<int64_t>(u) * V;
+      q.g = u / (32 / V);
+      q.in = own && q.c < cols;
+      q.lead = own && u % (32 / V) == 0;
+    }
     return q;
   };
   if (r0 >= R) return;
@@ -298,7 +291,7 @@ __global__ void __launch_bounds__(kCkThreads) checkpoint_unpack_kernel(const Che
         if (!q.in) return;
         Words<T, V> x;
 #pragma unroll
-        for (int k = 0; k < (V + 1) / 2; ++k) x.put2(k, ck_decode2<V>(in.codes, k, ck_scale(in.e)));
+        for (int k = 0; k < V / 2; ++k) x.put2(k, ck_decode2<V>(in.codes, k, ck_scale(in.e)));
         x.store(static_cast<T*>(a.x_out) + q.row * a.C + q.c);
       });
 }
@@ -331,7 +324,7 @@ __global__ void __launch_bounds__(kCkThreads) swiglu_act_kernel(const SwigluActA
         if (q.in) {
           Words<T, V> out;
 #pragma unroll
-          for (int k = 0; k < (V + 1) / 2; ++k) {
+          for (int k = 0; k < V / 2; ++k) {
             u64 sig, rest;
             sigmoid2<T>(in.g.get2(k), sig, rest);
             out.put2(k, fmul2(fmul2(in.g.get2(k), sig), in.u.get2(k)));
@@ -378,7 +371,7 @@ __global__ void __launch_bounds__(kCkThreads) swiglu_act_bwd_kernel(const Swiglu
         if (!q.in) return;
         Words<T, V> dg, du, h;
 #pragma unroll
-        for (int k = 0; k < (V + 1) / 2; ++k) {
+        for (int k = 0; k < V / 2; ++k) {
           const u64 g = ck_decode2<V>(in.g, k, ck_scale(in.eg)), u = ck_decode2<V>(in.u, k, ck_scale(in.eu));
           const u64 d = in.dh.get2(k);
           u64 sig, rest;
@@ -394,6 +387,141 @@ __global__ void __launch_bounds__(kCkThreads) swiglu_act_bwd_kernel(const Swiglu
       });
 }
 
+// ------------------------------------------------- strips of any other width
+// A lane's four columns of a strip, 32 apart.
+struct Strip {
+  float v[4];
+  __device__ __forceinline__ u64 pair(int k) const { return pair2(v[2 * k], v[2 * k + 1]); }
+  __device__ __forceinline__ void set(int k, u64 x) {
+    v[2 * k] = lo2(x);
+    v[2 * k + 1] = hi2(x);
+  }
+};
+__device__ __forceinline__ float strip_get(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float strip_get(const float* p) { return *p; }
+__device__ __forceinline__ void strip_put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void strip_put(float* p, float v) { *p = v; }
+
+// Columns of a row that starts at p, `cols` wide; zeros behind it.
+template <typename T>
+__device__ __forceinline__ Strip strip_load(const T* p, const CkUnit& q, int64_t cols) {
+  Strip x;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x.v[j] = q.in && q.c + 32 * j < cols ? strip_get(p + q.c + 32 * j) : 0.f;
+  return x;
+}
+template <typename T>
+__device__ __forceinline__ void strip_store(T* p, const CkUnit& q, int64_t cols, const Strip& x) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (q.in && q.c + 32 * j < cols) strip_put(p + q.c + 32 * j, x.v[j]);
+}
+// The strip's codes and exponents to a row of each.  The whole warp calls.
+__device__ __forceinline__ void strip_encode(const Strip& x, const CkUnit& q, int64_t cols, uint8_t* codes,
+                                             uint8_t* exps) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t b = __float_as_uint(x.v[j]) & 0x7fffffffu;
+    const bool fine = b < 0x7f800000u;
+    const uint32_t e = ck_exponent(__reduce_max_sync(0xffffffffu, fine ? b : 0u));
+    const float v = fine ? x.v[j] * ck_scale(254u - e) : __uint_as_float(0x7fffffffu);
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(0.f), "f"(v));
+    if (q.in && q.c + 32 * j < cols) codes[q.c + 32 * j] = static_cast<uint8_t>(c & 0xffu);
+    if (q.lead && q.c + 32 * j < cols) exps[q.g + j] = static_cast<uint8_t>(e);
+  }
+}
+__device__ __forceinline__ Strip strip_decode(const uint8_t* codes, const uint8_t* exps, const CkUnit& q, int64_t cols) {
+  Strip x;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const bool in = q.in && q.c + 32 * j < cols;
+    const uint16_t c = in ? codes[q.c + 32 * j] : 0;
+    const float s = in ? ck_scale(exps[q.g + j]) : 0.f;
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+    x.v[j] = f16x2_to_f32x2(h).x * s;
+  }
+  return x;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kCkThreads) checkpoint_pack_strip_kernel(const CheckpointArgs a, const CkShape s) {
+  pdl_enter();
+  const int64_t G = (a.C + 31) / 32;
+  each_unit<32, true>(
+      s, a.R, a.C, [&](const CkUnit& q) { return strip_load(static_cast<const T*>(a.x) + q.row * a.C, q, a.C); },
+      [&](const CkUnit& q, const Strip& x) { strip_encode(x, q, a.C, a.codes + q.row * a.C, a.exps + q.row * G); });
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kCkThreads) checkpoint_unpack_strip_kernel(const CheckpointArgs a, const CkShape s) {
+  pdl_enter();
+  const int64_t G = (a.C + 31) / 32;
+  each_unit<32, true>(
+      s, a.R, a.C, [&](const CkUnit& q) { return strip_decode(a.codes + q.row * a.C, a.exps + q.row * G, q, a.C); },
+      [&](const CkUnit& q, const Strip& x) { strip_store(static_cast<T*>(a.x_out) + q.row * a.C, q, a.C, x); });
+}
+
+struct StripGu {
+  Strip g, u, dh;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kCkThreads) swiglu_act_strip_kernel(const SwigluActArgs a, const CkShape s) {
+  pdl_enter();
+  const int64_t I = a.I, G = (I + 31) / 32;
+  each_unit<32, true>(
+      s, act_rows(a), I,
+      [&](const CkUnit& q) {
+        const T* src = static_cast<const T*>(a.gu) + q.row * 2 * I;
+        return StripGu{strip_load(src, q, I), strip_load(src + I, q, I), Strip{}};
+      },
+      [&](const CkUnit& q, const StripGu& in) {
+        Strip h;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          u64 sig, rest;
+          sigmoid2<T>(in.g.pair(k), sig, rest);
+          h.set(k, fmul2(fmul2(in.g.pair(k), sig), in.u.pair(k)));
+        }
+        strip_store(static_cast<T*>(a.h) + q.row * I, q, I, h);
+        if (a.codes == nullptr) return;
+        strip_encode(in.g, q, I, a.codes + q.row * 2 * I, a.exps + q.row * 2 * G);
+        strip_encode(in.u, q, I, a.codes + q.row * 2 * I + I, a.exps + q.row * 2 * G + G);
+      });
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kCkThreads) swiglu_act_bwd_strip_kernel(const SwigluActArgs a, const CkShape s) {
+  pdl_enter();
+  const int64_t I = a.I, G = (I + 31) / 32;
+  each_unit<32, true>(
+      s, act_rows(a), I,
+      [&](const CkUnit& q) {
+        return StripGu{strip_decode(a.codes + q.row * 2 * I, a.exps + q.row * 2 * G, q, I),
+                       strip_decode(a.codes + q.row * 2 * I + I, a.exps + q.row * 2 * G + G, q, I),
+                       strip_load(static_cast<const T*>(a.dh) + q.row * I, q, I)};
+      },
+      [&](const CkUnit& q, const StripGu& in) {
+        Strip dg, du, h;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          u64 sig, rest, one = pair2(1.0f, 1.0f);
+          const u64 g = in.g.pair(k), u = in.u.pair(k), d = in.dh.pair(k);
+          sigmoid2<T>(g, sig, rest);
+          const u64 silu = fmul2(g, sig);
+          dg.set(k, fmul2(fmul2(d, u), fmul2(sig, ffma2(g, rest, one))));
+          du.set(k, fmul2(d, silu));
+          h.set(k, fmul2(u, silu));
+        }
+        T* out = static_cast<T*>(a.dgu) + q.row * 2 * I;
+        strip_store(out, q, I, dg);
+        strip_store(out + I, q, I, du);
+        if (a.h) strip_store(static_cast<T*>(a.h) + q.row * I, q, I, h);
+      });
+}
+
 // ----------------------------------------------------------------- launches
 // Blocks of about 256 threads (whole rows where a row has fewer units), each
 // with about four steps, and at least one wave of them where there are so
@@ -403,7 +531,8 @@ __global__ void __launch_bounds__(kCkThreads) swiglu_act_bwd_kernel(const Swiglu
 // next loads to run ahead (108 us).
 template <typename A>
 static cudaError_t ck_launch(void (*kern)(A, CkShape), const A& a, int64_t R, int64_t cols, int V, cudaStream_t st) {
-  const int upr = static_cast<int>((cols + 31) / 32) * (32 / V);
+  const int groups = static_cast<int>((cols + 31) / 32);
+  const int upr = V == 1 ? (groups + 3) / 4 * 32 : groups * (32 / V);
   CkShape s{upr, upr >= 256 ? 1 : 256 / upr};
   const int64_t want = static_cast<int64_t>(s.rpb) * upr;
   const int threads = want >= kCkThreads ? kCkThreads : static_cast<int>((want + 31) / 32 * 32);
@@ -428,7 +557,7 @@ static cudaError_t checkpoint_pick(bool pack, const CheckpointArgs& a, cudaStrea
     case 16: return run(checkpoint_pack_kernel<T, 16>, checkpoint_unpack_kernel<T, 16>);
     case 8: return run(checkpoint_pack_kernel<T, 8>, checkpoint_unpack_kernel<T, 8>);
     case 4: return run(checkpoint_pack_kernel<T, 4>, checkpoint_unpack_kernel<T, 4>);
-    default: return run(checkpoint_pack_kernel<T, 1>, checkpoint_unpack_kernel<T, 1>);
+    default: return run(checkpoint_pack_strip_kernel<T>, checkpoint_unpack_strip_kernel<T>);
   }
 }
 
@@ -446,7 +575,7 @@ static cudaError_t swiglu_act_pick(bool backward, const SwigluActArgs& a, cudaSt
     case 16: return run(swiglu_act_kernel<T, 16>, swiglu_act_bwd_kernel<T, 16>);
     case 8: return run(swiglu_act_kernel<T, 8>, swiglu_act_bwd_kernel<T, 8>);
     case 4: return run(swiglu_act_kernel<T, 4>, swiglu_act_bwd_kernel<T, 4>);
-    default: return run(swiglu_act_kernel<T, 1>, swiglu_act_bwd_kernel<T, 1>);
+    default: return run(swiglu_act_strip_kernel<T>, swiglu_act_bwd_strip_kernel<T>);
   }
 }
 
