@@ -372,7 +372,9 @@ int mm_moe_backward(const void* x, const void* Wr,
  * order (deterministic), one rounding per output element.  Any width: rows
  * whose byte length is a multiple of 16 move in 16-byte vectors.  None of
  * these calls waits on the device (no watchdog), and none reads or writes the
- * 256-byte header of a workspace.
+ * 256-byte header of a workspace.  Outputs overlap neither inputs nor each
+ * other, but where a declaration says so.  Workspace sizes are those of the
+ * current device.
  * ---------------------------------------------------------------------- */
 
 /* Norms before and after a block, its gate and its residual scale, in one
@@ -428,8 +430,9 @@ int mm_block_norm_backward(const void* dn, const void* dr, const void* r, const 
  * rows = mm_moe_permuted_rows(T, E, k, align) (-1: outside the limits), the
  * most that any routing can need.  An expert may appear twice in a token.
  * Limits: E <= MM_MAX_EXPERTS, k <= MM_MAX_TOPK (k > E is allowed), align <=
- * MM_PERMUTE_MAX_ALIGN, T*k <= 2^30.  T = 0 zeroes offsets and counts. */
+ * MM_PERMUTE_MAX_ALIGN, H <= MM_PERMUTE_MAX_H, T*k <= 2^30.  T = 0 zeroes offsets and counts. */
 #define MM_PERMUTE_MAX_ALIGN 1024
+#define MM_PERMUTE_MAX_H (1 << 24)
 
 int64_t mm_moe_permuted_rows(int64_t T, int E, int k, int align);
 size_t mm_moe_permute_workspace_bytes(int64_t T, int E, int k);
@@ -464,6 +467,7 @@ int mm_moe_unpermute_backward(const void* dy, const void* ys, const int32_t* pos
  * An infinity or a NaN becomes a NaN code and leaves its group's scale alone.
  * Unpacking multiplies back: exact in fp32 and, above its subnormals, in bf16,
  * but for |x| > 1.9375 * 2^127, whose code stands for 2^128: an infinity there.
+ * exps are taken as packing writes them (1 .. 247).
  * Limits: C <= MM_CHECKPOINT_MAX_COLS, R*C <= 2^40.  R = 0 enqueues nothing. */
 #define MM_CHECKPOINT_MAX_COLS (1 << 20)
 

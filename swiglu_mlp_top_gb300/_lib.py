@@ -20,6 +20,7 @@ MM_MAX_TOPK = 8
 MM_NOALLOC_SCRATCH_BYTES = 16 << 20
 MM_NORM_MAX_H = 16384
 MM_PERMUTE_MAX_ALIGN = 1024
+MM_PERMUTE_MAX_H = 1 << 24
 MM_CHECKPOINT_MAX_COLS = 1 << 20
 MM_CHECKPOINT_GROUP = 32
 

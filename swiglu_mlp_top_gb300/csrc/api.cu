@@ -1025,7 +1025,7 @@ int mm_moe_permute(const void* x, const int32_t* topk_idx, int64_t T, int H, int
                    void* stream) {
   if (!valid_dtype(dtype) || T < 0 || H < 1 || E < 1 || k < 1 || align < 1) return MM_ERR_INVALID_ARG;
   const int64_t rows = mm_moe_permuted_rows(T, E, k, align);
-  if (rows < 0) return MM_ERR_UNSUPPORTED;
+  if (rows < 0 || H > MM_PERMUTE_MAX_H) return MM_ERR_UNSUPPORTED;
   if (!offsets || !counts || !aligned4(offsets) || !aligned4(counts)) return MM_ERR_INVALID_ARG;
   if (T > 0 && (!present16(x) || !present16(xs) || !topk_idx || !perm || !pos ||
                 !aligned4(topk_idx) || !aligned4(perm) || !aligned4(pos)))
@@ -1050,7 +1050,7 @@ int mm_moe_permute(const void* x, const int32_t* topk_idx, int64_t T, int H, int
 int mm_moe_unpermute(const void* ys, const int32_t* pos, const float* topk_w, int64_t T, int H,
                      int k, int64_t rows, int dtype, void* y, void* stream) {
   if (!valid_dtype(dtype) || T < 0 || H < 1 || k < 1 || rows < 0) return MM_ERR_INVALID_ARG;
-  if (k > MM_MAX_TOPK || T > (int64_t{1} << 30) / k) return MM_ERR_UNSUPPORTED;
+  if (k > MM_MAX_TOPK || T > (int64_t{1} << 30) / k || H > MM_PERMUTE_MAX_H) return MM_ERR_UNSUPPORTED;
   if (T == 0) return MM_OK;
   if (!present16(y) || !pos || !aligned4(pos) || !aligned4(topk_w) || !aligned16(ys) ||
       (rows > 0 && !ys))
@@ -1066,7 +1066,8 @@ int mm_moe_unpermute_backward(const void* dy, const void* ys, const int32_t* pos
                               int64_t T, int H, int E, int k, int64_t rows, int dtype, void* dys,
                               float* dw, void* stream) {
   if (!valid_dtype(dtype) || T < 0 || H < 1 || E < 1 || k < 1 || rows < 0) return MM_ERR_INVALID_ARG;
-  if (E > MM_MAX_EXPERTS || k > MM_MAX_TOPK || T > (int64_t{1} << 30) / k) return MM_ERR_UNSUPPORTED;
+  if (E > MM_MAX_EXPERTS || k > MM_MAX_TOPK || T > (int64_t{1} << 30) / k || H > MM_PERMUTE_MAX_H)
+    return MM_ERR_UNSUPPORTED;
   if (T == 0) return MM_OK;
   if (!present16(dy) || !pos || !offsets || !counts || !aligned4(pos) || !aligned4(topk_w) ||
       !aligned4(offsets) || !aligned4(counts) || !aligned4(dw) || !aligned16(ys) || !aligned16(dys))

@@ -167,7 +167,8 @@ __device__ __forceinline__ void sigmoid2(u64 g, u64& sig, u64& rest) {
     constexpr double kC = 0.72134752044448170368;               // log2(e) / 2
     constexpr float kHead = static_cast<float>(kC), kTail = static_cast<float>(kC - static_cast<double>(kHead));
     constexpr float kLn2 = 0.693147180559945f;
-    const u64 a = g | 0x8000000080000000ull;                    // -|g|
+    // -|g|, but no infinity, whose tail would be a NaN (t is 0 from 208 on)
+    const u64 a = pair2(fmaxf(-fabsf(g0), -256.0f), fmaxf(-fabsf(g1), -256.0f));
     const u64 q = fmul2(a, pair2(kHead, kHead));
     const u64 r = ffma2(a, pair2(kTail, kTail), ffma2(a, pair2(kHead, kHead), q ^ 0x8000000080000000ull));
     float e0, e1;
@@ -182,7 +183,7 @@ __device__ __forceinline__ void sigmoid2(u64 g, u64& sig, u64& rest) {
     s = pair2(s0, s1);
   }
   const u64 ts = fmul2(t, s);
-  const bool p0 = g0 >= 0.f, p1 = g1 >= 0.f;                    // a NaN g leaves NaN in t
+  const bool p0 = g0 >= 0.f, p1 = g1 >= 0.f;                    // a NaN g is left to the caller's product with g
   sig = pair2(p0 ? lo2(s) : lo2(ts), p1 ? hi2(s) : hi2(ts));
   rest = pair2(p0 ? lo2(ts) : lo2(s), p1 ? hi2(ts) : hi2(s));
 }

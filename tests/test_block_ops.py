@@ -63,7 +63,7 @@ def test_permute_refusals(lib):
     for kw in (dict(dt=7), dict(T=-1), dict(H=0), dict(E=0), dict(k=0), dict(align=0), dict(x=None), dict(x=ODD), dict(idx=None),
                dict(xs=None), dict(off=None), dict(cnt=None), dict(perm=None), dict(pos=None), dict(pos=ODD)):
         assert call(**kw) == BAD, kw
-    for kw in (dict(E=65), dict(k=9), dict(align=1025), dict(T=1 << 30)):
+    for kw in (dict(E=65), dict(k=9), dict(align=1025), dict(T=1 << 30), dict(H=L.MM_PERMUTE_MAX_H + 1)):
         assert call(**kw) == UNS, kw
     assert call(ws=None) == WS and call(wsb=0) == WS
     assert lib.mm_moe_permuted_rows(10, 4, 2, 8) == 20 + 4 * 7
@@ -76,14 +76,14 @@ def test_permute_refusals(lib):
         return lib.mm_moe_unpermute(ys, pos, w, T, H, k, rows, dt, y, None)
     for kw in (dict(dt=7), dict(T=-1), dict(H=0), dict(k=0), dict(rows=-1), dict(ys=None), dict(pos=None), dict(y=None), dict(w=ODD)):
         assert back(**kw) == BAD, kw
-    assert back(k=9) == UNS and back(T=0, y=None) == OK
+    assert back(k=9) == UNS and back(H=L.MM_PERMUTE_MAX_H + 1) == UNS and back(T=0, y=None) == OK
 
     def grad(dy=F, ys=F, pos=F, w=F, off=F, cnt=F, T=10, H=64, E=4, k=2, rows=20, dt=BF, dys=F, dw=F):
         return lib.mm_moe_unpermute_backward(dy, ys, pos, w, off, cnt, T, H, E, k, rows, dt, dys, dw, None)
     for kw in (dict(dt=7), dict(T=-1), dict(H=0), dict(E=0), dict(k=0), dict(rows=-1), dict(dy=None), dict(ys=None),
                dict(pos=None), dict(off=None), dict(cnt=None), dict(dys=None), dict(w=None), dict(dys=ODD), dict(dw=ODD)):
         assert grad(**kw) == BAD, kw
-    assert grad(k=9) == UNS and grad(E=65) == UNS and grad(T=0, dy=None) == OK
+    assert grad(k=9) == UNS and grad(E=65) == UNS and grad(H=L.MM_PERMUTE_MAX_H + 1) == UNS and grad(T=0, dy=None) == OK
 
 
 def test_checkpoint_refusals(lib):

@@ -116,7 +116,7 @@ def test_plain_norm(T, H, dtype):
     (20000, 256, True, "channel", True, True), (9733, 8, True, "token", True, True), (9999, 24, False, None, True, True),
     (10001, 40, True, None, False, True), (12345, 768, False, "channel", True, True), (10000, 64, True, "channel", True, False),
     (3000, 2432, True, "token", False, True), (5003, 1000, True, "channel", True, True), (700, 8192, True, "token", True, True),
-    (650, 12288, True, None, True, True), (11000, 33, True, "channel", True, True)])
+    (650, 12288, True, None, True, True), (40, 12288, True, "token", True, True), (11000, 33, True, "channel", True, True)])
 def test_many_tokens(T, H, post, gate, pre, branch, dtype):
     d = make(T, H, dtype, post, gate, pre, branch=branch)
     r, n, stats = forward(d, s=0.9 if branch else 1.0)
@@ -198,6 +198,25 @@ def test_gradient_against_differences():
         slope = ((loss(1) - loss(-1)) / (2 * h)).item()
         want = (grads[key].double() * way).sum().item()
         assert abs(slope - want) <= (64 * U32 / h + 2.0 ** -17) * terms, (name, slope, want, terms)
+
+
+def test_more_elements_than_32_bits_count():
+    """Rows on both sides of element 2^31, against the 64-bit forms."""
+    T, H = 2 ** 21 + 40, 1024
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    big = lambda: torch.randn(T, H, generator=gen, device="cuda", dtype=BF)  # noqa: E731
+    x, f, dn = big(), big(), big()
+    w = torch.rand(H, generator=gen, device="cuda").to(BF) + 0.5
+    stats = {}
+    r, n = mm.block_norm(x, f, post_weight=w, pre_weight=w, eps=EPS, stats=stats)
+    got = mm.block_norm_backward(dn, None, r, f, stats, post_weight=w, pre_weight=w)
+    rows = [0, 7, 2 ** 20, 2 ** 21 - 1, 2 ** 21, 2 ** 21 + 39]
+    some = dict(x=x[rows], f=f[rows], post=w, gate=None, pre=w, dn=dn[rows], dr=None)
+    part = {k: v[rows] for k, v in stats.items()}
+    check_forward(some, r[rows], n[rows], part)
+    want = ref.norm_backward(some["dn"], None, r[rows], some["f"], w, None, w, 1.0, part["rstd_post"], part["rstd_pre"])
+    for k in ("dx", "df"):
+        close(got[k][rows], want[k], 2 ** -8 * want[k].abs() + 1.01 * 384 * U32 * want[k + "_terms"], k)
 
 
 def test_side_stream_and_graph():

@@ -153,6 +153,34 @@ def test_rows_behind_the_last_are_left_alone(I):
         assert torch.equal(got, h) if count > 0 else bool((got == 7).all())
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("I", [32, 33])
+def test_infinite_gate(I, dtype):
+    """SiLU(inf) = inf; the product with u carries its sign."""
+    gu = torch.ones(2, 2 * I, dtype=dtype, device="cuda")
+    gu[0, 5] = float("inf")
+    gu[1, 5], gu[1, I + 5] = float("inf"), -2.0
+    h = mm.swiglu_act(gu)
+    assert h[0, 5] == float("inf") and h[1, 5] == -float("inf") and (~h.isfinite()).sum() == 2
+
+
+def test_more_elements_than_32_bits_count():
+    """Rows on both sides of byte 2^32 of the codes and of gu."""
+    R, I = 1_100_000, 2048
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    gu = torch.randn(R, 2 * I, generator=gen, device="cuda", dtype=BF)
+    ck = {}
+    h = mm.swiglu_act(gu, checkpoint=ck)
+    dgu, h2 = mm.swiglu_act_backward(ck, h)
+    rows = [0, 2 ** 19 - 1, 2 ** 19, 2 ** 20 - 1, 2 ** 20, R - 1]
+    small = {}
+    hs = mm.swiglu_act(gu[rows], checkpoint=small)
+    ds, hs2 = mm.swiglu_act_backward(small, h[rows])
+    assert torch.equal(h[rows], hs) and torch.equal(dgu[rows], ds) and torch.equal(h2[rows], hs2)
+    assert torch.equal(ck["exps"][rows], small["exps"])
+    assert torch.equal(ck["codes"].view(torch.uint8)[rows], small["codes"].view(torch.uint8))
+
+
 def test_no_rows():
     ck = {}
     h = mm.swiglu_act(torch.empty(0, 128, dtype=BF, device="cuda"), checkpoint=ck)

@@ -101,6 +101,31 @@ def test_no_tokens():
     assert y.shape == (0, 64) and dys.shape == (0, 64) and dw.shape == (0, 2)
 
 
+def test_more_elements_than_32_bits_count():
+    """Rows behind element 2^31 of the sorted tensor: copied, combined, and their gradient."""
+    T, H, E, k = 300_000, 2048, 8, 4
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(T, H, generator=gen, device="cuda", dtype=BF)
+    idx = torch.randint(0, E, (T, k), generator=gen, device="cuda", dtype=torch.int32)
+    w = torch.rand(T, k, generator=gen, device="cuda")
+    xs, plan = mm.moe_permute(x, idx, E)
+    assert xs.numel() > 2 ** 31 and int(plan["offsets"][-1]) == T * k
+    for rows in (slice(0, 1000), slice(2 ** 20 - 500, 2 ** 20 + 500), slice(T * k - 1000, T * k)):
+        a = plan["perm"][rows].long()
+        assert torch.equal(plan["pos"].view(-1)[a], torch.arange(T * k, device="cuda", dtype=torch.int32)[rows])
+        assert torch.equal(xs[rows], x[a // k]) and bool((a[1:] > a[:-1]).sum() >= 997)
+    y = mm.moe_unpermute(xs, plan, w)
+    dys, dw = mm.moe_unpermute_backward(y, xs, plan, w, out=torch.empty_like(xs))
+    for t in (0, T // 2, T - 1):                        # a token's rows are its own: y = x times its weights
+        scale = w[t].double().sum().item()
+        close(y[t], x[t].double().cpu() * scale, (2 ** -8 + 9 * U32) * x[t].double().cpu().abs() * scale, "y")
+        for s in range(k):
+            want = y[t].double().cpu() * w[t, s].double().item()
+            close(dys[int(plan["pos"][t, s])], want, (2 ** -8 + 2 * U32) * want.abs(), "dys")
+        terms = y[t].double().cpu() * x[t].double().cpu()
+        close(dw[t], terms.sum().expand(k), (H + 1) * U32 * terms.abs().sum().expand(k), "dw")
+
+
 def test_rows_outside_the_tensor_are_left_out():
     """A pos that no plan holds adds nothing instead of being read."""
     ys = torch.ones(4, 64, dtype=BF, device="cuda")
