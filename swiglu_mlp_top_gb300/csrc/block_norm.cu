@@ -411,9 +411,10 @@ __device__ __forceinline__ void bn_zero(const BlockNormBwd& a, int q, int h) {
 // each thread copies and reads its own slots only, so the ring needs no
 // barrier, and its registers hold only sums and D.  Without it a group's
 // loads, reduction and stores follow one another and DRAM idles between them
-// (T = 16384, H = 768, bf16: 41 us, with it 32 us,
-// of 22 us that its bytes take at the measured copy rate).  bf16 rows of odd width
-// (2-byte accesses, which cp.async does not move) load into registers.
+// (T = 16384, H = 768, bf16: 41 us, with it 31 us, of which the second kernel
+// takes 3; the bytes take 22 us at the measured copy rate).  Rows that are not
+// 16-byte aligned load into registers: cp.async of 4 bytes took 74 us where
+// plain loads take 26 (T = 4097, H = 1001, fp32; 15 us at the copy rate).
 // Dynamic shared memory: w_pre and w_post g by column (`span` floats each: the
 // columns of every unit, zeros behind the row), then the ring
 // [stages][inputs][NU][threads], in whose place [groups][kBnSums][span] stands
@@ -536,7 +537,7 @@ block_norm_bwd_kernel(const BlockNormBwd a, int tpr, int span, int stages) {
     turn ^= 1;
     const float k_r = rho_r * rho_r * (s[0] * inv_h) * rho_r;               // rho_r^3 c_r
     const float k_f = a.post_w ? rho_f * rho_f * ((s[1] - k_r * s[2]) * inv_h) : 0.f;  // rho_f^2 c_f
-    const u64 k_r2 = pair2(-k_r, -k_r), k_f2 = pair2(-k_f, -k_f);
+    const u64 k_r2 = pair2(-k_r, -k_r), k_f2 = pair2(-k_f * rho_f, -k_f * rho_f);
 #pragma unroll
     for (int m = 0; m < NU; ++m) {
       u64 wm[NP], o[NP];
@@ -552,13 +553,14 @@ block_norm_bwd_kernel(const BlockNormBwd a, int tpr, int span, int stages) {
       const Raw f = value(here, kInF, m), g = kTokenGate ? value(here, kInGate, m) : U::zero();
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
-        const u64 fk = U::get(f, k), u = fmul2(fk, rho_f2);
+        const u64 fk = U::get(f, k);
+        u64 d = fmul2(e[m][k], rho_f2);                                     // D rho_f
         if constexpr (kTokenGate) {
-          o[k] = fmul2(fmul2(e[m][k], u), wm[k]);                           // wm is w_post here
-          e[m][k] = fmul2(e[m][k], U::get(g, k));
+          o[k] = fmul2(fmul2(d, fk), wm[k]);                                // wm is w_post here
+          d = fmul2(d, U::get(g, k));
         }
-        s_mid[m][k] = ffma2(e[m][k], u, s_mid[m][k]);
-        e[m][k] = fmul2(rho_f2, ffma2(fk, k_f2, fmul2(wm[k], e[m][k])));
+        s_mid[m][k] = ffma2(d, fk, s_mid[m][k]);
+        e[m][k] = ffma2(fk, k_f2, fmul2(wm[k], d));
       }
       if constexpr (kTokenGate) U::store(a.d_gate, base, m, c0, tpr, nv, o);
       U::store(a.df, base, m, c0, tpr, nv, e[m]);
@@ -736,7 +738,7 @@ static inline int bn_vec(int dtype, int H) {
 static inline int bn_tpr(int nv, int NV) { return (nv + 32 * NV - 1) / (32 * NV) * 32; }
 
 // Backward: a thread takes up to 24 elements of bf16 (three 16-byte vectors
-// of each input) and 16 of fp32 or of an unaligned width, as its registers
+// of each input), 16 of fp32 or 8 of an unaligned width, as its registers
 // allow; the fewest idle lanes decide between the unit counts, more units a
 // thread where that is equal (fewer warps to add up).  A row that needs more
 // than a block's threads so is `wide`.

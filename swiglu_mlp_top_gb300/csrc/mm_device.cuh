@@ -172,7 +172,9 @@ __device__ __forceinline__ u64 fmul2(u64 a, u64 b) {
   return d;
 }
 __device__ __forceinline__ u64 pair2(float lo, float hi) {
-  return (static_cast<u64>(__float_as_uint(hi)) << 32) | __float_as_uint(lo);
+  u64 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
 }
 __device__ __forceinline__ float lo2(u64 v) { return __uint_as_float(static_cast<uint32_t>(v)); }
 __device__ __forceinline__ float hi2(u64 v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
