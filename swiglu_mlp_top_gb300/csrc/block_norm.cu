@@ -739,9 +739,9 @@ static inline int bn_tpr(int nv, int NV) { return (nv + 32 * NV - 1) / (32 * NV)
 
 // Backward: a thread takes up to 24 elements of bf16 (three 16-byte vectors
 // of each input), 16 of fp32 or 8 of an unaligned width, as its registers
-// allow; the fewest idle lanes decide between the unit counts, more units a
-// thread where that is equal (fewer warps to add up).  A row that needs more
-// than a block's threads so is `wide`.
+// allow; the most threads with columns decide between the unit counts, two
+// units where that is equal (H = 1024, fp32: 38 us, with one 41, with four
+// 43).  A row that needs more than a block's threads so is `wide`.
 template <int V> struct BnUnits;
 template <> struct BnUnits<8> { static constexpr int kMost = 3, kSome = 2, kFew = 1; };
 template <> struct BnUnits<4> { static constexpr int kMost = 4, kSome = 2, kFew = 1; };
@@ -756,10 +756,13 @@ static BnBwdShape bn_bwd_shape_v(int64_t T, int H) {
   using N = BnUnits<V>;
   constexpr int width = V == 1 ? 2 : V;       // elements of a unit
   BnBwdShape s{V, 0, 0, 1, 1, 0, false};
-  for (int NU : {N::kMost, N::kSome, N::kFew}) {
+  int best = 0;
+  for (int NU : {N::kSome, N::kMost, N::kFew}) {
     const int tpr = (H + 32 * NU * width - 1) / (32 * NU * width) * 32;
     if (tpr > kBnBwdThreads) continue;
-    if (s.NU == 0 || NU * tpr < s.NU * s.tpr) {
+    const int busy = kBnBwdThreads / tpr * ((H + NU * width - 1) / (NU * width));   // threads with columns
+    if (busy > best) {
+      best = busy;
       s.NU = NU;
       s.tpr = tpr;
     }
@@ -775,6 +778,9 @@ static BnBwdShape bn_bwd_shape_v(int64_t T, int H) {
   // one block an SM: a second wave costs a block's start and its sums again
   // (T = 16384: 31 -> 34 us at H = 768, 124 -> 131 us at H = 4096)
   s.groups = kBnBwdThreads / s.tpr;
+  // few rows: one block, which needs no second kernel, where its groups take a
+  // row each or, being many, a few (T = 24, H = 960, fp32: 7.9 -> 6.3 us)
+  if (T <= (V > 1 && s.groups >= 8 ? 4 : 1) * s.groups) return s;
   const int64_t want = (T + s.groups - 1) / s.groups;
   s.grid = static_cast<int>(want < sms ? (want > 0 ? want : 1) : sms);
   return s;
@@ -821,10 +827,15 @@ static cudaError_t bn_ring_launch(const BlockNormFwd& a, int tpr, cudaStream_t s
 template <typename T, int V>
 static cudaError_t bn_ring_pick(const BlockNormFwd& a, cudaStream_t st) {
   constexpr int kUnits[3] = {24 / V, 16 / V, 8 / V};
-  int best = 0;
+  int best = 0, busy = 0;
   const int nv = a.H / V;
-  for (int NU : kUnits)
-    if (bn_tpr(nv, NU) <= kBnFwdThreads && (best == 0 || NU * bn_tpr(nv, NU) < best * bn_tpr(nv, best))) best = NU;
+  for (int NU : {kUnits[1], kUnits[0], kUnits[2]}) {      // the most threads with columns
+    const int tpr = bn_tpr(nv, NU), b = tpr > kBnFwdThreads ? 0 : kBnFwdThreads / tpr * ((nv + NU - 1) / NU);
+    if (b > busy) {
+      busy = b;
+      best = NU;
+    }
+  }
   if (best == 0) return cudaErrorNotSupported;
   const int tpr = bn_tpr(nv, best);
   if (best == kUnits[0]) return bn_ring_launch<T, V, kUnits[0]>(a, tpr, st);

@@ -10,6 +10,8 @@
 // divides the width, so that values and codes move in whole aligned accesses.
 // Rows of other widths go in strips of 128 columns, a warp each: a lane has
 // one column of each of the strip's four groups, and single accesses.
+#include <algorithm>
+#include <cstdlib>
 #include "mm_kernels.cuh"
 
 namespace mm {
@@ -546,20 +548,29 @@ static cudaError_t ck_launch(void (*kern)(A, CkShape), const A& a, int64_t R, in
   return launch_dependent_kernel(kern, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0, st, a, s);
 }
 
-static inline int ck_vec(int64_t cols) { return cols % 16 == 0 ? 16 : cols % 8 == 0 ? 8 : cols % 4 == 0 ? 4 : 1; }
+// Columns a thread: the widest of 16, 8, 4 that divides the width, up to a
+// bound by what the registers hold beside the next unit's loads.  fp32 rows
+// take 8 (4 in the backward), us with 16 / 8 / 4: R = 4000, I = 8192 forward
+// 79 / 69 / 81, backward 120 / 101 / 94.  1: strips.
+static inline int ck_vec(int64_t cols, int most) {
+  for (int v = most; v >= 4; v /= 2)
+    if (cols % v == 0) return v;
+  return 1;
+}
+
+typedef void (*CheckpointKernel)(CheckpointArgs, CkShape);
+typedef void (*SwigluActKernel)(SwigluActArgs, CkShape);
 
 template <typename T>
 static cudaError_t checkpoint_pick(bool pack, const CheckpointArgs& a, cudaStream_t st) {
-  const int V = ck_vec(a.C);
-  auto run = [&](void (*p)(CheckpointArgs, CkShape), void (*u)(CheckpointArgs, CkShape)) {
-    return ck_launch<CheckpointArgs>(pack ? p : u, a, a.R, a.C, V, st);
-  };
-  switch (V) {
-    case 16: return run(checkpoint_pack_kernel<T, 16>, checkpoint_unpack_kernel<T, 16>);
-    case 8: return run(checkpoint_pack_kernel<T, 8>, checkpoint_unpack_kernel<T, 8>);
-    case 4: return run(checkpoint_pack_kernel<T, 4>, checkpoint_unpack_kernel<T, 4>);
-    default: return run(checkpoint_pack_strip_kernel<T>, checkpoint_unpack_strip_kernel<T>);
-  }
+  constexpr int kMost = sizeof(T) == 2 ? 16 : 8;
+  const int V = ck_vec(a.C, kMost);
+  CheckpointKernel k;
+  if (V == kMost) k = pack ? checkpoint_pack_kernel<T, kMost> : checkpoint_unpack_kernel<T, kMost>;
+  else if (V == 8) k = pack ? checkpoint_pack_kernel<T, 8> : checkpoint_unpack_kernel<T, 8>;
+  else if (V == 4) k = pack ? checkpoint_pack_kernel<T, 4> : checkpoint_unpack_kernel<T, 4>;
+  else k = pack ? checkpoint_pack_strip_kernel<T> : checkpoint_unpack_strip_kernel<T>;
+  return ck_launch<CheckpointArgs>(k, a, a.R, a.C, V, st);
 }
 
 cudaError_t launch_checkpoint(int dtype, bool pack, const CheckpointArgs& a, cudaStream_t st) {
@@ -568,16 +579,14 @@ cudaError_t launch_checkpoint(int dtype, bool pack, const CheckpointArgs& a, cud
 
 template <typename T>
 static cudaError_t swiglu_act_pick(bool backward, const SwigluActArgs& a, cudaStream_t st) {
-  const int V = ck_vec(a.I);
-  auto run = [&](void (*f)(SwigluActArgs, CkShape), void (*b)(SwigluActArgs, CkShape)) {
-    return ck_launch<SwigluActArgs>(backward ? b : f, a, a.R, a.I, V, st);
-  };
-  switch (V) {
-    case 16: return run(swiglu_act_kernel<T, 16>, swiglu_act_bwd_kernel<T, 16>);
-    case 8: return run(swiglu_act_kernel<T, 8>, swiglu_act_bwd_kernel<T, 8>);
-    case 4: return run(swiglu_act_kernel<T, 4>, swiglu_act_bwd_kernel<T, 4>);
-    default: return run(swiglu_act_strip_kernel<T>, swiglu_act_bwd_strip_kernel<T>);
-  }
+  constexpr int kMost = sizeof(T) == 2 ? 16 : 8, kMostBwd = sizeof(T) == 2 ? 16 : 4;
+  const int V = ck_vec(a.I, backward ? kMostBwd : kMost);
+  SwigluActKernel k;
+  if (V == 1) k = backward ? swiglu_act_bwd_strip_kernel<T> : swiglu_act_strip_kernel<T>;
+  else if (backward) k = V == kMostBwd ? swiglu_act_bwd_kernel<T, kMostBwd> : V == 8 ? swiglu_act_bwd_kernel<T, 8>
+                                                                                   : swiglu_act_bwd_kernel<T, 4>;
+  else k = V == kMost ? swiglu_act_kernel<T, kMost> : V == 8 ? swiglu_act_kernel<T, 8> : swiglu_act_kernel<T, 4>;
+  return ck_launch<SwigluActArgs>(k, a, a.R, a.I, V, st);
 }
 
 cudaError_t launch_swiglu_act(int dtype, bool backward, const SwigluActArgs& a, cudaStream_t st) {

@@ -18,6 +18,16 @@ template <> struct Pack<__nv_bfloat16, 8> {
                       pack_bf16x2(v[6], v[7]));
   }
 };
+template <> struct Pack<__nv_bfloat16, 4> {
+  typedef uint2 Raw;
+  static __device__ __forceinline__ float get(const Raw& r, int j) {
+    const uint32_t w = j < 2 ? r.x : r.y;
+    return __uint_as_float((j & 1) ? (w & 0xffff0000u) : (w << 16));
+  }
+  static __device__ __forceinline__ Raw put(const float (&v)[4]) {
+    return make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  }
+};
 template <> struct Pack<__nv_bfloat16, 2> {
   typedef uint32_t Raw;
   static __device__ __forceinline__ float get(const Raw& r, int j) {
@@ -38,6 +48,11 @@ template <> struct Pack<float, 4> {
   static __device__ __forceinline__ Raw put(const float (&v)[4]) {
     return make_float4(v[0], v[1], v[2], v[3]);
   }
+};
+template <> struct Pack<float, 2> {
+  typedef float2 Raw;
+  static __device__ __forceinline__ float get(const Raw& r, int j) { return j ? r.y : r.x; }
+  static __device__ __forceinline__ Raw put(const float (&v)[2]) { return make_float2(v[0], v[1]); }
 };
 template <> struct Pack<float, 1> {
   typedef float Raw;

@@ -74,7 +74,7 @@ __device__ __forceinline__ void count_experts(const int32_t* topk_idx, int64_t f
   }
 }
 
-// counts [E][nblk]: the block's assignments per expert.
+// counts [block][E]: the block's assignments per expert.
 __global__ void __launch_bounds__(128) permute_count_kernel(const PermuteArgs a, int tokens, int32_t* blk_cnt) {
   pdl_enter();
   __shared__ int cnt[MM_MAX_EXPERTS];
@@ -84,28 +84,29 @@ __global__ void __launch_bounds__(128) permute_count_kernel(const PermuteArgs a,
   const int64_t nt = a.T - t0 < tokens ? a.T - t0 : tokens;
   count_experts(a.topk_idx, t0 * a.k, nt * a.k, a.E, cnt);
   __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += blockDim.x) blk_cnt[e * gridDim.x + blockIdx.x] = cnt[e];
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) blk_cnt[blockIdx.x * a.E + e] = cnt[e];
 }
 
 // Block b owns the assignments of `tokens` tokens from b * tokens on.  It
 // works out its own base in every group - from the blocks' counts, or
 // (blk_cnt null: few assignments) by counting all of them itself, which
-// saves a launch - then its assignments' ranks, and (copy) copies its rows, a
-// warp per token: one load, a store for each of the token's assignments.  The
-// rows are asked for (to L2) before the indices are worked out.
+// saves a launch - then its assignments' ranks, and (copy) copies its rows, in
+// pieces shared out over its warps: one load, a store for each of the token's
+// assignments.  The rows are asked for (to L2) before the indices are worked
+// out.  Blocks from `owners` on own no token; they zero padding.
 template <typename Vec>
 __global__ void __launch_bounds__(kPmThreads, 2)
-permute_kernel(const PermuteArgs a, int tokens, const int32_t* blk_cnt, int row_bytes, int copy) {
-  constexpr int kBatch = sizeof(Vec) == 16 ? 4 : 12;      // vectors of a row in flight a lane
+permute_kernel(const PermuteArgs a, int tokens, int owners, const int32_t* blk_cnt, int row_bytes, int copy) {
+  constexpr int kBatch = sizeof(Vec) == 16 ? 4 : sizeof(Vec) == 8 ? 6 : 12;      // vectors of a row in flight a lane
   __shared__ int s_tot[MM_MAX_EXPERTS], s_next[MM_MAX_EXPERTS], s_off[MM_MAX_EXPERTS + 1];
   __shared__ int s_warp[kPmWarps][MM_MAX_EXPERTS];
   __shared__ int s_pos[kPmKept];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens;
+  const int64_t t0 = static_cast<int>(blockIdx.x) < owners ? static_cast<int64_t>(blockIdx.x) * tokens : a.T;
   const int nt = static_cast<int>(a.T - t0 < tokens ? a.T - t0 : tokens), na = nt * a.k;
   const int32_t* idx = a.topk_idx + t0 * a.k;
   const char* x = static_cast<const char*>(a.x) + t0 * row_bytes;
-  if (copy && sizeof(Vec) == 16 && tid == 0) {
+  if (copy && nt > 0 && sizeof(Vec) == 16 && tid == 0) {
     // at most 64 KB a block: 20 MB over the grid, well inside L2
     const int64_t all = static_cast<int64_t>(nt) * row_bytes, bytes = all < 65536 ? all : 65536;
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(x), "r"(static_cast<uint32_t>(bytes)) : "memory");
@@ -121,6 +122,7 @@ permute_kernel(const PermuteArgs a, int tokens, const int32_t* blk_cnt, int row_
     for (int i = 0; i < kBatch; ++i)
       if (c + 32 * i < nv) v[i] = src[c + 32 * i];
   };
+  const int own = tid < na ? idx[tid] : -1;    // the first round's, on its way meanwhile
   __syncthreads();
   if (blk_cnt == nullptr) {
     count_experts(a.topk_idx, 0, t0 * a.k, a.E, s_next);
@@ -128,22 +130,22 @@ permute_kernel(const PermuteArgs a, int tokens, const int32_t* blk_cnt, int row_
     __syncthreads();
     for (int e = tid; e < a.E; e += kPmThreads) s_tot[e] += s_next[e];
   } else {
-    for (int e = warp; e < a.E; e += kPmWarps) {
+    // thread: one expert, every `parts`-th block
+    const int e = tid % a.E, part = tid / a.E, parts = kPmThreads / a.E;
+    if (part < parts) {
       int all = 0, before = 0;
-      for (int b = lane; b < static_cast<int>(gridDim.x); b += 32) {
-        const int c = blk_cnt[e * gridDim.x + b];
-        all += c;
-        before += b < static_cast<int>(blockIdx.x) ? c : 0;
-      }
+      for (int b0 = part; b0 < owners; b0 += 8 * parts) {
+        int c[8];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        all += __shfl_xor_sync(0xffffffffu, all, o);
-        before += __shfl_xor_sync(0xffffffffu, before, o);
+        for (int q = 0; q < 8; ++q) c[q] = b0 + q * parts < owners ? blk_cnt[(b0 + q * parts) * a.E + e] : 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          all += c[q];
+          before += b0 + q * parts < static_cast<int>(blockIdx.x) ? c[q] : 0;
+        }
       }
-      if (lane == 0) {
-        s_tot[e] = all;
-        s_next[e] = before;
-      }
+      atomicAdd(&s_tot[e], all);              // integers: any order gives the same sums
+      atomicAdd(&s_next[e], before);
     }
   }
   __syncthreads();
@@ -169,7 +171,7 @@ permute_kernel(const PermuteArgs a, int tokens, const int32_t* blk_cnt, int row_
   // ranks, one assignment a thread and round: within the warp, then the warps in order
   for (int base = 0; base < na; base += kPmThreads) {
     const int i = base + tid;
-    const int e = i < na ? idx[i] : -1;
+    const int e = base == 0 ? own : i < na ? idx[i] : -1;
     const bool valid = e >= 0 && e < a.E;
     const unsigned peers = __match_any_sync(0xffffffffu, valid ? e : -1);
     const int rank = __popc(peers & ((1u << lane) - 1u));
@@ -193,17 +195,18 @@ permute_kernel(const PermuteArgs a, int tokens, const int32_t* blk_cnt, int row_
     __syncthreads();
   }
   // rows: the next piece's load is under way while this one is stored
-  if (copy && warp < nt) fetch(warp, 0);
-  for (int token = warp, chunk = 0; copy && token < nt;) {
+  int item = warp, token = item / chunks, chunk = item - token * chunks;
+  const int items = copy ? nt * chunks : 0;
+  if (item < items) fetch(token, chunk);
+  while (item < items) {
     Vec now[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) now[i] = v[i];
     const int c = chunk * (32 * kBatch) + lane, first = token * a.k;
-    if (++chunk == chunks) {
-      chunk = 0;
-      token += kPmWarps;
-    }
-    if (token < nt) fetch(token, chunk);
+    item += kPmWarps;
+    token = item / chunks;
+    chunk = item - token * chunks;
+    if (item < items) fetch(token, chunk);
     for (int at = first; at < first + a.k; ++at) {
       const int64_t row = at < kPmKept ? s_pos[at] : a.pos[t0 * a.k + at];    // the block's own writes
       if (row < 0) continue;
@@ -217,7 +220,7 @@ permute_kernel(const PermuteArgs a, int tokens, const int32_t* blk_cnt, int row_
     for (int e = tid; e <= a.E; e += kPmThreads) a.offsets[e] = s_off[e];
     for (int e = tid; e < a.E; e += kPmThreads) a.counts[e] = s_tot[e];
   }
-  const int64_t wg = static_cast<int64_t>(blockIdx.x) * kPmWarps + warp, nw = static_cast<int64_t>(gridDim.x) * kPmWarps;
+  const int64_t wg = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x, nw = static_cast<int64_t>(gridDim.x) * kPmWarps;
   if (a.align > 1)
     each_padding_row(s_off, s_tot, a.E, a.rows, wg, nw, [&](int64_t row) {
       Vec* dst = reinterpret_cast<Vec*>(static_cast<char*>(a.xs) + row * row_bytes);
@@ -235,15 +238,19 @@ __global__ void permute_empty_kernel(const PermuteArgs a) {
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.counts[e] = 0;
 }
 
-// y[t] = sum_s w ys[pos]: a warp per token; KP >= k rows of NB vectors a lane
+// y[t] = sum_s w ys[pos]: 2^wshift warps of a block share a token's row (one
+// where there are tokens enough for every warp); KP >= k rows of NB vectors a lane
 // are loaded before the first is added (in slot order).  A dropped assignment
 // is a row of zeros with weight 0, so nothing of it is read.
-template <typename T, int V, int KP, int NB>
-__global__ void __launch_bounds__(kPmRowThreads) unpermute_kernel(const UnpermuteArgs a) {
+template <typename T, int V, int KP, int NB, bool kShare>
+__global__ void __launch_bounds__(kShare ? kPmThreads : kPmRowThreads)
+unpermute_kernel(const UnpermuteArgs a, int wshift) {
   using P = Pack<T, V>;
   pdl_enter();
-  const int lane = threadIdx.x & 31, nv = a.H / V;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kPmRowThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nv = a.H / V;
+  if (!kShare) wshift = 0;
+  const int wpt = 1 << wshift;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> (5 + wshift)) + (warp >> wshift);
   if (t >= a.T) return;
   int64_t my = lane < a.k ? a.pos[t * a.k + lane] : -1;
   if (my >= a.rows) my = -1;
@@ -255,7 +262,7 @@ __global__ void __launch_bounds__(kPmRowThreads) unpermute_kernel(const Unpermut
     row[s] = __shfl_sync(0xffffffffu, my, s);
     w[s] = __shfl_sync(0xffffffffu, my_w, s);
   }
-  for (int c = lane; c < nv; c += 32 * NB) {
+  for (int c = (warp & (wpt - 1)) * (32 * NB) + lane; c < nv; c += 32 * NB * wpt) {
     typename P::Raw raw[KP][NB];
 #pragma unroll
     for (int s = 0; s < KP; ++s)
@@ -278,14 +285,19 @@ __global__ void __launch_bounds__(kPmRowThreads) unpermute_kernel(const Unpermut
   }
 }
 
-// dys[pos] = w dy, dw = <dy, ys[pos]>: a warp per token, dy read once.
-template <typename T, int V, int KP, int NB>
-__global__ void __launch_bounds__(kPmRowThreads) unpermute_bwd_kernel(const UnpermuteBwdArgs a) {
+// dys[pos] = w dy, dw = <dy, ys[pos]>: dy read once, by 2^wshift warps a token
+// (more than one: all the block's), whose parts of a dot product are added in
+// their order.
+template <typename T, int V, int KP, int NB, bool kShare>
+__global__ void __launch_bounds__(kShare ? kPmThreads : kPmRowThreads)
+unpermute_bwd_kernel(const UnpermuteBwdArgs a, int wshift) {
   using P = Pack<T, V>;
   pdl_enter();
-  const int lane = threadIdx.x & 31, nv = a.H / V;
-  constexpr int kWarps = kPmRowThreads / 32;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  __shared__ float s_dot[kPmWarps][KP];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, nv = a.H / V;
+  if (!kShare) wshift = 0;
+  const int wpt = 1 << wshift;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (warps >> wshift) + (warp >> wshift);
   if (t < a.T) {
     int64_t my = lane < a.k ? a.pos[t * a.k + lane] : -1;
     if (my >= a.rows) my = -1;
@@ -298,7 +310,7 @@ __global__ void __launch_bounds__(kPmRowThreads) unpermute_bwd_kernel(const Unpe
       w[s] = __shfl_sync(0xffffffffu, my_w, s);
       dot[s] = 0.f;
     }
-    for (int c = lane; c < nv; c += 32 * NB) {
+    for (int c = (warp & (wpt - 1)) * (32 * NB) + lane; c < nv; c += 32 * NB * wpt) {
       typename P::Raw g[NB], raw[KP][NB];
 #pragma unroll
       for (int i = 0; i < NB; ++i)
@@ -333,10 +345,18 @@ __global__ void __launch_bounds__(kPmRowThreads) unpermute_bwd_kernel(const Unpe
         for (int o = 16; o > 0; o >>= 1) dot[s] += __shfl_xor_sync(0xffffffffu, dot[s], o);
         if (lane == s) mine = dot[s];
       }
-      if (lane < a.k) a.dw[t * a.k + lane] = mine;
+      if (kShare) {                           // the block's one token
+        if (lane < KP) s_dot[warp][lane] = mine;
+        __syncthreads();
+        mine = 0.f;
+        if (warp == 0 && lane < KP)
+          for (int q = 0; q < wpt; ++q) mine += s_dot[q][lane];
+      }
+      if ((warp & (wpt - 1)) == 0 && lane < a.k) a.dw[t * a.k + lane] = mine;
     }
   }
-  each_padding_row(a.offsets, a.counts, a.E, a.rows, t, static_cast<int64_t>(gridDim.x) * kWarps, [&](int64_t r) {
+  each_padding_row(a.offsets, a.counts, a.E, a.rows, static_cast<int64_t>(warp) * gridDim.x + blockIdx.x,
+                   static_cast<int64_t>(gridDim.x) * warps, [&](int64_t r) {
     float zero[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) zero[j] = 0.f;
@@ -345,10 +365,10 @@ __global__ void __launch_bounds__(kPmRowThreads) unpermute_bwd_kernel(const Unpe
 }
 
 // ----------------------------------------------------------------- launches
-// Two blocks an SM at most, and at least a token for each of a block's warps.
+// Blocks that own tokens: two an SM at most.
 static int pm_blocks(int64_t T) {
-  const int64_t most = 2 * static_cast<int64_t>(num_sms()), want = (T + kPmWarps - 1) / kPmWarps;
-  return static_cast<int>(want < most ? (want > 0 ? want : 1) : most);
+  const int64_t most = 2 * static_cast<int64_t>(num_sms());
+  return static_cast<int>(T < most ? (T > 0 ? T : 1) : most);
 }
 // Up to this many assignments every block counts all of them itself (T = 2048,
 // k = 2: 4.6 us, of which the launch of a counting kernel would add 1.5);
@@ -372,13 +392,11 @@ static int pm_tokens(const PermuteArgs& a) {
   const int b = pm_blocks(a.T);
   return static_cast<int>((a.T + b - 1) / b);
 }
-// Blocks that own a token (the last of pm_blocks may be left without).
-static dim3 pm_grid(const PermuteArgs& a) {
-  return dim3(static_cast<unsigned>((a.T + pm_tokens(a) - 1) / pm_tokens(a)));
-}
+// The blocks that do own a token (the last of pm_blocks may be left without).
+static int pm_owners(const PermuteArgs& a) { return static_cast<int>((a.T + pm_tokens(a) - 1) / pm_tokens(a)); }
 
 cudaError_t launch_permute_count(const PermuteArgs& a, cudaStream_t st) {
-  return launch_dependent_kernel(permute_count_kernel, pm_grid(a), dim3(128), 0, st, a, pm_tokens(a),
+  return launch_dependent_kernel(permute_count_kernel, dim3(pm_owners(a)), dim3(128), 0, st, a, pm_tokens(a),
                                  static_cast<int32_t*>(a.scratch));
 }
 
@@ -386,66 +404,104 @@ cudaError_t launch_permute(int dtype, const PermuteArgs& a, cudaStream_t st) {
   if (a.T == 0) return launch_dependent_kernel(permute_empty_kernel, dim3(1), dim3(128), 0, st, a);
   const int row_bytes = a.H * (dtype == kDtypeBF16 ? 2 : 4);
   const int32_t* cnt = permute_counts_first(a.T, a.k) ? static_cast<const int32_t*>(a.scratch) : nullptr;
+  // and blocks for the padding, where the tokens' own would take long over it
+  const int owners = pm_owners(a);
+  const int64_t pad = (a.rows - a.T * a.k + 3) / 4, most = pm_blocks(int64_t{1} << 40);
+  const int grid = static_cast<int>(pad < owners ? owners : pad < most ? pad : most);
   auto run = [&](auto kern) {
-    return launch_dependent_kernel(kern, pm_grid(a), dim3(kPmThreads), 0, st, a, pm_tokens(a), cnt,
-                                   row_bytes, pm_copy_apart(a.T, a.k, row_bytes) ? 0 : 1);
+    return launch_dependent_kernel(kern, dim3(grid > owners ? grid : owners), dim3(kPmThreads), 0, st, a, pm_tokens(a),
+                                   owners, cnt, row_bytes, pm_copy_apart(a.T, a.k, row_bytes) ? 0 : 1);
   };
   if (row_bytes % 16 == 0) return run(permute_kernel<uint4>);
+  if (row_bytes % 8 == 0) return run(permute_kernel<uint2>);
   if (row_bytes % 4 == 0) return run(permute_kernel<uint32_t>);
   return run(permute_kernel<uint16_t>);
 }
 
 static inline int pm_kp(int k) { return k <= 1 ? 1 : k <= 2 ? 2 : k <= 4 ? 4 : 8; }
-static unsigned pm_row_blocks(int64_t T) {
-  return static_cast<unsigned>((T + kPmRowThreads / 32 - 1) / (kPmRowThreads / 32));
+// Warps that share a token: one, and more where there are fewer tokens than
+// eight warps an SM, as far as the row has pieces of `piece` vectors for them
+// (T = 4, k = 7, H = 7424, bf16: 17.6 us with one warp a token).
+// log2 of it.
+static int pm_wshift(int64_t T, int nv, int piece) {
+  int s = 0;
+  while ((1 << s) < kPmWarps && (T << s) < 8ll * num_sms() && (piece << s) < nv) ++s;
+  return s;
+}
+// Blocks of 128 threads, or of one token's warps; `more` rows of padding may
+// want more of them.
+static void pm_row_grid(int64_t T, int wshift, int64_t more, dim3& grid, dim3& block) {
+  const int wpt = 1 << wshift;
+  const int warps = wpt > 1 ? wpt : kPmRowThreads / 32;
+  const int64_t own = wpt > 1 ? T : (T + warps - 1) / warps;
+  const int64_t pad = (more + 1) / 2, most = 4 * static_cast<int64_t>(num_sms());
+  const int64_t want = pad < most ? pad : most;
+  grid = dim3(static_cast<unsigned>(own > want ? own : want));
+  block = dim3(32 * warps);
 }
 
 // Narrow accesses (rows that are not 16-byte aligned): more of them in flight.
 template <typename T, int V>
-constexpr int pm_wide() { return V * sizeof(T) == 16 ? 1 : 4; }
+constexpr int pm_wide() { return V * sizeof(T) == 16 ? 1 : V * sizeof(T) == 8 ? 2 : 4; }
 
+template <typename T, int V, int KP, int NB>
+static cudaError_t unpermute_run(const UnpermuteArgs& a, cudaStream_t st) {
+  const int wshift = pm_wshift(a.T, a.H / V, 32 * NB);
+  dim3 grid, block;
+  pm_row_grid(a.T, wshift, 0, grid, block);
+  auto kern = wshift > 0 ? unpermute_kernel<T, V, KP, NB, true> : unpermute_kernel<T, V, KP, NB, false>;
+  return launch_dependent_kernel(kern, grid, block, 0, st, a, wshift);
+}
 template <typename T, int V>
 static cudaError_t unpermute_pick(const UnpermuteArgs& a, cudaStream_t st) {
   constexpr int kWide = pm_wide<T, V>();
-  auto run = [&](auto kern) {
-    return launch_dependent_kernel(kern, dim3(pm_row_blocks(a.T)), dim3(kPmRowThreads), 0, st, a);
-  };
   switch (pm_kp(a.k)) {
-    case 1: return run(unpermute_kernel<T, V, 1, 4 * kWide>);
-    case 2: return run(unpermute_kernel<T, V, 2, 4 * kWide>);
-    case 4: return run(unpermute_kernel<T, V, 4, 2 * kWide>);
-    default: return run(unpermute_kernel<T, V, 8, kWide>);
+    case 1: return unpermute_run<T, V, 1, 4 * kWide>(a, st);
+    case 2: return unpermute_run<T, V, 2, 4 * kWide>(a, st);
+    case 4: return unpermute_run<T, V, 4, 2 * kWide>(a, st);
+    default: return unpermute_run<T, V, 8, kWide>(a, st);
   }
 }
 cudaError_t launch_unpermute(int dtype, const UnpermuteArgs& a, cudaStream_t st) {
   if (dtype == kDtypeBF16) {
     if (a.H % 8 == 0) return unpermute_pick<__nv_bfloat16, 8>(a, st);
+    if (a.H % 4 == 0) return unpermute_pick<__nv_bfloat16, 4>(a, st);
     if (a.H % 2 == 0) return unpermute_pick<__nv_bfloat16, 2>(a, st);
     return unpermute_pick<__nv_bfloat16, 1>(a, st);
   }
-  return a.H % 4 == 0 ? unpermute_pick<float, 4>(a, st) : unpermute_pick<float, 1>(a, st);
+  if (a.H % 4 == 0) return unpermute_pick<float, 4>(a, st);
+  if (a.H % 2 == 0) return unpermute_pick<float, 2>(a, st);
+  return unpermute_pick<float, 1>(a, st);
 }
 
+template <typename T, int V, int KP>
+static cudaError_t unpermute_bwd_run(const UnpermuteBwdArgs& a, cudaStream_t st) {
+  constexpr int kWide = pm_wide<T, V>();
+  const int wshift = pm_wshift(a.T, a.H / V, 32 * kWide);
+  dim3 grid, block;
+  pm_row_grid(a.T, wshift, a.rows > a.T * a.k ? a.rows - a.T * a.k : 0, grid, block);
+  auto kern = wshift > 0 ? unpermute_bwd_kernel<T, V, KP, kWide, true> : unpermute_bwd_kernel<T, V, KP, kWide, false>;
+  return launch_dependent_kernel(kern, grid, block, 0, st, a, wshift);
+}
 template <typename T, int V>
 static cudaError_t unpermute_bwd_pick(const UnpermuteBwdArgs& a, cudaStream_t st) {
-  auto run = [&](auto kern) {
-    return launch_dependent_kernel(kern, dim3(pm_row_blocks(a.T)), dim3(kPmRowThreads), 0, st, a);
-  };
-  constexpr int kWide = pm_wide<T, V>();
   switch (pm_kp(a.k)) {
-    case 1: return run(unpermute_bwd_kernel<T, V, 1, kWide>);
-    case 2: return run(unpermute_bwd_kernel<T, V, 2, kWide>);
-    case 4: return run(unpermute_bwd_kernel<T, V, 4, kWide>);
-    default: return run(unpermute_bwd_kernel<T, V, 8, kWide>);
+    case 1: return unpermute_bwd_run<T, V, 1>(a, st);
+    case 2: return unpermute_bwd_run<T, V, 2>(a, st);
+    case 4: return unpermute_bwd_run<T, V, 4>(a, st);
+    default: return unpermute_bwd_run<T, V, 8>(a, st);
   }
 }
 cudaError_t launch_unpermute_bwd(int dtype, const UnpermuteBwdArgs& a, cudaStream_t st) {
   if (dtype == kDtypeBF16) {
     if (a.H % 8 == 0) return unpermute_bwd_pick<__nv_bfloat16, 8>(a, st);
+    if (a.H % 4 == 0) return unpermute_bwd_pick<__nv_bfloat16, 4>(a, st);
     if (a.H % 2 == 0) return unpermute_bwd_pick<__nv_bfloat16, 2>(a, st);
     return unpermute_bwd_pick<__nv_bfloat16, 1>(a, st);
   }
-  return a.H % 4 == 0 ? unpermute_bwd_pick<float, 4>(a, st) : unpermute_bwd_pick<float, 1>(a, st);
+  if (a.H % 4 == 0) return unpermute_bwd_pick<float, 4>(a, st);
+  if (a.H % 2 == 0) return unpermute_bwd_pick<float, 2>(a, st);
+  return unpermute_bwd_pick<float, 1>(a, st);
 }
 
 bool permute_copies_apart(int dtype, const PermuteArgs& a) {
