@@ -303,6 +303,7 @@ block_norm_ring_kernel(const BlockNormFwd a, int tpr, int span) {
   stage_params<T, V, kTokenGate>(a.pre_w, a.post_w, a.gate, a.H, tpr, span, w_pre, w_mid);
   __syncthreads();
   const u64 scale2 = pair2(a.residual_scale, a.residual_scale);
+  int turn = 0;               // flips with every sum: a row may have one or two
   for (int stage = 0; t < a.T; t += step, stage ^= 1) {
     const int64_t base = t * a.H;
     fetch(t + step, stage ^ 1);
@@ -324,7 +325,8 @@ block_norm_ring_kernel(const BlockNormFwd a, int tpr, int span) {
 #pragma unroll
           for (int k = 0; k < NP; ++k) ss = ffma2(U::get(f[m], k), U::get(f[m], k), ss);
         rho[0] = hsum2(ss);
-        group_sum(rho, red, 0, group, tpr);
+        group_sum(rho, red, turn, group, tpr);
+        turn ^= 1;
         rho[0] = inv_rms_of(rho[0], a.H, a.eps);
         if (c0 == 0 && a.rstd_post) a.rstd_post[t] = rho[0];
       }
@@ -352,7 +354,8 @@ block_norm_ring_kernel(const BlockNormFwd a, int tpr, int span) {
 #pragma unroll
       for (int k = 0; k < NP; ++k) ss = ffma2(U::get(r[m], k), U::get(r[m], k), ss);
     float rho[1] = {hsum2(ss)};
-    group_sum(rho, red, 1, group, tpr);
+    group_sum(rho, red, turn, group, tpr);
+    turn ^= 1;
     rho[0] = inv_rms_of(rho[0], a.H, a.eps);
     if (c0 == 0 && a.rstd_pre) a.rstd_pre[t] = rho[0];
     const u64 rho2 = pair2(rho[0], rho[0]);

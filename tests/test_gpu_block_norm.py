@@ -167,6 +167,18 @@ def test_no_tokens():
         assert got[k].shape == (768,) and not got[k].any()
 
 
+@pytest.mark.parametrize("post,pre", [(False, True), (True, False), (True, True)])
+def test_rows_of_several_warps_many_times(post, pre):
+    """Sums of consecutive rows go through the same few words of shared memory:
+    one or two sums a row, the same bits every time."""
+    d = make(6000, 2048, BF, post=post, pre=pre)
+    r, n, stats = forward(d)
+    check_forward(d, r, n, stats)
+    for _ in range(20):
+        r2, n2, stats2 = forward(d)
+        assert torch.equal(r, r2) and (n is None or torch.equal(n, n2)) and all(torch.equal(stats[k], stats2[k]) for k in stats)
+
+
 def test_same_bits_every_time():
     d = make(3000, 768, BF)
     r, n, stats = forward(d)
