@@ -125,12 +125,17 @@ struct Unit<T, 1> {
   static __device__ __forceinline__ u64 get(const Raw& r, int) {
     return pair2(static_cast<float>(r.a), static_cast<float>(r.b));
   }
+  static __device__ __forceinline__ Raw put(const u64 (&v)[1]) { return Raw{T(lo2(v[0])), T(hi2(v[0]))}; }
+  static __device__ __forceinline__ void store_raw(void* p, int64_t base, int m, int c0, int tpr, int nv,
+                                                   const Raw& r) {
+    T* row = static_cast<T*>(p) + base;
+    const int c = c0 + 2 * m * tpr;
+    if (c < nv) row[c] = r.a;
+    if (c + tpr < nv) row[c + tpr] = r.b;
+  }
   static __device__ __forceinline__ void store(void* p, int64_t base, int m, int c0, int tpr, int nv,
                                                const u64 (&v)[1]) {
-    const int c = c0 + 2 * m * tpr;
-    const float a[1] = {lo2(v[0])}, b[1] = {hi2(v[0])};
-    if (c < nv) row_store<T, 1>(p, base, c, a);
-    if (c + tpr < nv) row_store<T, 1>(p, base, c + tpr, b);
+    store_raw(p, base, m, c0, tpr, nv, put(v));
   }
   static __device__ __forceinline__ int place(int h, int) { return h; }
   static __device__ __forceinline__ void cols(const float* s, int m, int c0, int tpr, u64 (&v)[1]) {
@@ -150,6 +155,18 @@ __device__ __forceinline__ float bn_param(const void* w, int h) {
   return w ? static_cast<float>(static_cast<const T*>(w)[h]) : 1.f;
 }
 
+// The V values of vector c to their columns in shared memory.
+template <typename U, int V>
+__device__ __forceinline__ void columns_put(float* s, int c, int tpr, const float (&v)[V]) {
+  if constexpr (V == 1) {
+    s[c] = v[0];
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; j += 4)
+      *reinterpret_cast<float4*>(s + U::place(c * V + j, tpr)) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+  }
+}
+
 // w_pre and w_post g in fp32 by column, zeros behind the row (an absent w_pre
 // is zeros too: nothing is made of it; other absent factors are 1).  One
 // vector of each parameter a thread, so that their loads are in flight
@@ -165,12 +182,14 @@ __device__ __forceinline__ void stage_params(const void* pre, const void* post, 
     if (in && pre) a = row_load<T, V>(pre, 0, c);
     if (in && post) b = row_load<T, V>(post, 0, c);
     if (in && gate && !kTokenGate) g = row_load<T, V>(gate, 0, c);
+    float p[V], m[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int place = U::place(c * V + j, tpr);
-      w_pre[place] = in && pre ? P::get(a, j) : 0.f;
-      w_mid[place] = in ? (post ? P::get(b, j) : 1.f) * (gate && !kTokenGate ? P::get(g, j) : 1.f) : 0.f;
+      p[j] = in && pre ? P::get(a, j) : 0.f;
+      m[j] = in ? (post ? P::get(b, j) : 1.f) * (gate && !kTokenGate ? P::get(g, j) : 1.f) : 0.f;
     }
+    columns_put<U, V>(w_pre, c, tpr, p);
+    columns_put<U, V>(w_mid, c, tpr, m);
   }
 }
 
@@ -263,7 +282,9 @@ __global__ void __launch_bounds__(kBnFwdThreads) block_norm_kernel(const BlockNo
 // own slots, so without a barrier), w_post g and w_pre there in fp32, sums and
 // products on pairs.  One group per row and no loop leaves the last wave of
 // blocks part empty and re-reads the parameters for every row (T = 16384,
-// H = 768, bf16: 21 us, so 18 us).
+// H = 768, bf16: 21 us, so 18 us).  Unaligned rows take it whatever their
+// number, with the next row in registers: re-reading the parameters in single
+// elements is what costs them most.
 template <typename T, int V, int NU, bool kTokenGate>
 __global__ void __launch_bounds__(kBnFwdThreads, 1)
 block_norm_ring_kernel(const BlockNormFwd a, int tpr, int span) {
@@ -280,22 +301,32 @@ block_norm_ring_kernel(const BlockNormFwd a, int tpr, int span) {
                         (threadIdx.x & 31) * sizeof(Raw);
   auto at = [](int i, int m) { return (i * NU + m) * 32 * static_cast<int>(sizeof(Raw)); };
   const void* src[3] = {a.x, a.f, kTokenGate ? a.gate : nullptr};
+  Raw next[U::kAsync ? 1 : kIn][U::kAsync ? 1 : NU], now[U::kAsync ? 1 : kIn][U::kAsync ? 1 : NU];
   auto fetch = [&](int64_t t, int stage) {
     if (t < a.T)
 #pragma unroll
       for (int i = 0; i < kIn; ++i)
         if (src[i])
 #pragma unroll
-          for (int m = 0; m < NU; ++m)
-            U::copy(smem_u32(ring + stage * kStageBytes) + at(i, m), src[i], t * a.H, m, c0, tpr, nv);
-    asm volatile("cp.async.commit_group;" ::: "memory");
+          for (int m = 0; m < NU; ++m) {
+            if constexpr (U::kAsync)
+              U::copy(smem_u32(ring + stage * kStageBytes) + at(i, m), src[i], t * a.H, m, c0, tpr, nv);
+            else
+              next[i][m] = U::load(src[i], t * a.H, m, c0, tpr, nv);
+          }
+    if constexpr (U::kAsync) asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
   for (int i = 0; i < kIn; ++i)               // what no copy will fill stays zero
 #pragma unroll
-    for (int m = 0; m < NU; ++m)
-      if (src[i] == nullptr || c0 + m * tpr >= nv)
-        for (int st = 0; st < 2; ++st) *reinterpret_cast<Raw*>(ring + st * kStageBytes + at(i, m)) = U::zero();
+    for (int m = 0; m < NU; ++m) {
+      if constexpr (U::kAsync) {
+        if (src[i] == nullptr || c0 + m * tpr >= nv)
+          for (int st = 0; st < 2; ++st) *reinterpret_cast<Raw*>(ring + st * kStageBytes + at(i, m)) = U::zero();
+      } else {
+        next[i][m] = U::zero();
+      }
+    }
   pdl_enter();
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   int64_t t = static_cast<int64_t>(blockIdx.x) * groups + group;
@@ -306,10 +337,19 @@ block_norm_ring_kernel(const BlockNormFwd a, int tpr, int span) {
   int turn = 0;               // flips with every sum: a row may have one or two
   for (int stage = 0; t < a.T; t += step, stage ^= 1) {
     const int64_t base = t * a.H;
+    if constexpr (!U::kAsync) {
+#pragma unroll
+      for (int i = 0; i < kIn; ++i)
+#pragma unroll
+        for (int m = 0; m < NU; ++m) now[i][m] = next[i][m];
+    }
     fetch(t + step, stage ^ 1);
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    if constexpr (U::kAsync) asm volatile("cp.async.wait_group 1;" ::: "memory");
     const unsigned char* here = ring + stage * kStageBytes;
-    auto value = [&](int i, int m) { return *reinterpret_cast<const Raw*>(here + at(i, m)); };
+    auto value = [&](int i, int m) -> Raw {
+      if constexpr (U::kAsync) return *reinterpret_cast<const Raw*>(here + at(i, m));
+      else return now[i][m];
+    };
     Raw r[NU];
 #pragma unroll
     for (int m = 0; m < NU; ++m) r[m] = value(0, m);
@@ -368,7 +408,7 @@ block_norm_ring_kernel(const BlockNormFwd a, int tpr, int span) {
       U::store(a.n, base, m, c0, tpr, nv, v);
     }
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if constexpr (U::kAsync) asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // ----------------------------------------------------------------- backward
@@ -581,14 +621,46 @@ block_norm_bwd_kernel(const BlockNormBwd a, int tpr, int span, int stages) {
   }
   __syncthreads();
   float* part = a.partial + static_cast<int64_t>(blockIdx.x) * kBnSums * a.H;
-  for (int h = threadIdx.x; h < a.H; h += blockDim.x) {
-    const int place = U::place(h, tpr);
+  using P = Pack<T, V>;
+  const bool one = gridDim.x == 1, chan_gate = a.gate != nullptr && !kTokenGate;
+  for (int c = threadIdx.x; c < nv; c += blockDim.x) {
+    typename P::Raw gate, post;
+    if (one && chan_gate) gate = row_load<T, V>(a.gate, 0, c);
+    if (one && a.post_w) post = row_load<T, V>(a.post_w, 0, c);
+    float sum[kBnSums][V];
 #pragma unroll
     for (int q = 0; q < kBnSums; ++q) {
-      float sum = 0.f;
-      for (int gi = 0; gi < groups; ++gi) sum += behind[(gi * kBnSums + q) * span + place];
-      if (gridDim.x == 1) bn_finish<T>(a, q, h, sum);
-      else part[q * a.H + h] = sum;
+#pragma unroll
+      for (int j = 0; j < V; ++j) sum[q][j] = 0.f;
+      for (int gi = 0; gi < groups; ++gi) {
+        const float* from = behind + (gi * kBnSums + q) * span;
+        if constexpr (V == 1) {
+          sum[q][0] += from[c];
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; j += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(from + U::place(c * V + j, tpr));
+            sum[q][j] += x.x;
+            sum[q][j + 1] += x.y;
+            sum[q][j + 2] += x.z;
+            sum[q][j + 3] += x.w;
+          }
+        }
+      }
+    }
+    if (!one) {
+#pragma unroll
+      for (int q = 0; q < kBnSums; ++q)
+#pragma unroll
+        for (int j = 0; j < V; ++j) part[q * a.H + c * V + j] = sum[q][j];
+      continue;
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {             // complete: as bn_finish
+      const int h = c * V + j;
+      if (a.d_pre_w) a.d_pre_w[h] = sum[0][j];
+      if (a.d_post_w) a.d_post_w[h] = chan_gate ? sum[1][j] * P::get(gate, j) : sum[1][j];
+      if (chan_gate) static_cast<float*>(a.d_gate)[h] = a.post_w ? sum[1][j] * P::get(post, j) : sum[1][j];
     }
   }
 }
@@ -807,14 +879,21 @@ static cudaError_t bn_fwd_launch(const BlockNormFwd& a, int tpr, cudaStream_t st
 }
 
 // The ring, where two rows of every group fit beside the parameters and every
-// SM has a few rows for each group; cudaErrorNotSupported: not here.
+// SM has a few rows for each group, and for unaligned rows;
+// cudaErrorNotSupported: not here.
+template <typename T, int V> struct BnFwdUnits {
+  static constexpr int kWidth = V == 1 ? 2 : V;           // elements of a unit
+  static constexpr int kMost = V > 1 ? 24 / V : sizeof(T) == 2 ? 8 : 4;
+  static constexpr int kSome = V > 1 ? 16 / V : kMost / 2, kFew = V > 1 ? 8 / V : kMost / 4;
+};
 template <typename T, int V, int NU>
 static cudaError_t bn_ring_launch(const BlockNormFwd& a, int tpr, cudaStream_t st) {
   const bool token_gate = a.gate != nullptr && a.gate_per_token;
-  const int span = NU * tpr * V, groups = kBnFwdThreads / tpr;
-  const size_t smem = 2 * sizeof(float) * span + 2 * (token_gate ? 3 : 2) * sizeof(T) * span * groups;
+  const int span = NU * tpr * BnFwdUnits<T, V>::kWidth, groups = kBnFwdThreads / tpr;
+  const size_t ring = V > 1 ? 2 * (token_gate ? 3 : 2) * sizeof(T) * span * groups : 0;
+  const size_t smem = 2 * sizeof(float) * span + ring;
   const int64_t sms = num_sms();
-  if (smem > kBnMostSmem || a.T < 4 * sms * groups) return cudaErrorNotSupported;
+  if (smem > kBnMostSmem || (V > 1 && a.T < 4 * sms * groups)) return cudaErrorNotSupported;
   auto kern = token_gate ? block_norm_ring_kernel<T, V, NU, true> : block_norm_ring_kernel<T, V, NU, false>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
@@ -829,29 +908,27 @@ static cudaError_t bn_ring_launch(const BlockNormFwd& a, int tpr, cudaStream_t s
 }
 template <typename T, int V>
 static cudaError_t bn_ring_pick(const BlockNormFwd& a, cudaStream_t st) {
-  constexpr int kUnits[3] = {24 / V, 16 / V, 8 / V};
-  int best = 0, busy = 0;
-  const int nv = a.H / V;
-  for (int NU : {kUnits[1], kUnits[0], kUnits[2]}) {      // the most threads with columns
-    const int tpr = bn_tpr(nv, NU), b = tpr > kBnFwdThreads ? 0 : kBnFwdThreads / tpr * ((nv + NU - 1) / NU);
+  using N = BnFwdUnits<T, V>;
+  int best = 0, busy = 0, tpr = 0;
+  for (int NU : {N::kSome, N::kMost, N::kFew}) {          // the most threads with columns
+    const int lanes = (a.H + NU * N::kWidth - 1) / (NU * N::kWidth), t = (lanes + 31) / 32 * 32;
+    const int b = t > kBnFwdThreads ? 0 : kBnFwdThreads / t * lanes;
     if (b > busy) {
       busy = b;
       best = NU;
+      tpr = t;
     }
   }
   if (best == 0) return cudaErrorNotSupported;
-  const int tpr = bn_tpr(nv, best);
-  if (best == kUnits[0]) return bn_ring_launch<T, V, kUnits[0]>(a, tpr, st);
-  if (best == kUnits[1]) return bn_ring_launch<T, V, kUnits[1]>(a, tpr, st);
-  return bn_ring_launch<T, V, kUnits[2]>(a, tpr, st);
+  if (best == N::kMost) return bn_ring_launch<T, V, N::kMost>(a, tpr, st);
+  if (best == N::kSome) return bn_ring_launch<T, V, N::kSome>(a, tpr, st);
+  return bn_ring_launch<T, V, N::kFew>(a, tpr, st);
 }
 
 template <typename T, int V>
 static cudaError_t bn_fwd_pick(const BlockNormFwd& a, cudaStream_t st) {
-  if constexpr (V > 1) {
-    const cudaError_t e = bn_ring_pick<T, V>(a, st);
-    if (e != cudaErrorNotSupported) return e;
-  }
+  const cudaError_t ring = bn_ring_pick<T, V>(a, st);
+  if (ring != cudaErrorNotSupported) return ring;
   // up to 32 elements a thread; fewer, where a warp holds the row with fewer
   const int nv = a.H / V;
   constexpr int kMost = 32 / V;
