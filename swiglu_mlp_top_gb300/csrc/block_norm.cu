@@ -194,6 +194,7 @@ __device__ __forceinline__ void stage_params(const void* pre, const void* post, 
 }
 
 // ------------------------------------------------------------------ forward
+// Many wide rows: a group of threads per row, everything in registers.
 constexpr size_t kBnMostSmem = 224 * 1024;   // dynamic, of 227 KB a block may have
 constexpr int kBnFwdThreads = 512;      // most threads of a block (one group of them: H = 16384)
 
@@ -277,14 +278,15 @@ __global__ void __launch_bounds__(kBnFwdThreads) block_norm_kernel(const BlockNo
   }
 }
 
-// Many aligned rows: a block of groups per SM walks down the rows, the next
-// row's inputs on their way to shared memory (each thread copies and reads its
-// own slots, so without a barrier), w_post g and w_pre there in fp32, sums and
-// products on pairs.  One group per row and no loop leaves the last wave of
-// blocks part empty and re-reads the parameters for every row (T = 16384,
-// H = 768, bf16: 21 us, so 18 us).  Unaligned rows take it whatever their
-// number, with the next row in registers: re-reading the parameters in single
-// elements is what costs them most.
+// The rule: a block of groups per SM walks down the rows, the next row's
+// inputs on their way to shared memory (each thread copies and reads its own
+// slots, so without a barrier), w_post g and w_pre there in fp32, sums and
+// products on pairs.  Against one group per row and no loop (above, kept for
+// wide rows) no last wave is left part empty, and the parameters
+// are read once a block instead of once a row, by all its threads: bf16,
+// H = 768, T = 16384 21 -> 18 us, T = 1 3.6 -> 2.2 us.  Unaligned rows have
+// the next row in registers; the parameters re-read in single elements were
+// what cost them most (T = 16384, H = 461 with a token gate: 57 -> 20 us).
 template <typename T, int V, int NU, bool kTokenGate>
 __global__ void __launch_bounds__(kBnFwdThreads, 1)
 block_norm_ring_kernel(const BlockNormFwd a, int tpr, int span) {
@@ -328,8 +330,9 @@ block_norm_ring_kernel(const BlockNormFwd a, int tpr, int span) {
       }
     }
   pdl_enter();
+  // rows go to blocks first: few of them to an SM each
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-  int64_t t = static_cast<int64_t>(blockIdx.x) * groups + group;
+  int64_t t = static_cast<int64_t>(group) * gridDim.x + blockIdx.x;
   fetch(t, 0);
   stage_params<T, V, kTokenGate>(a.pre_w, a.post_w, a.gate, a.H, tpr, span, w_pre, w_mid);
   __syncthreads();
@@ -854,8 +857,9 @@ static BnBwdShape bn_bwd_shape_v(int64_t T, int H) {
   // (T = 16384: 31 -> 34 us at H = 768, 124 -> 131 us at H = 4096)
   s.groups = kBnBwdThreads / s.tpr;
   // few rows: one block, which needs no second kernel, where its groups take a
-  // row each or, being many, a few (T = 24, H = 960, fp32: 7.9 -> 6.3 us)
-  if (T <= (V > 1 && s.groups >= 8 ? 4 : 1) * s.groups) return s;
+  // row each or, being many, two (T = 10, H = 896, bf16: 7.5 us, of which the
+  // second kernel would add 2)
+  if (T <= (V > 1 && s.groups >= 8 ? 2 : 1) * s.groups) return s;
   const int64_t want = (T + s.groups - 1) / s.groups;
   s.grid = static_cast<int>(want < sms ? (want > 0 ? want : 1) : sms);
   return s;
@@ -878,8 +882,10 @@ static cudaError_t bn_fwd_launch(const BlockNormFwd& a, int tpr, cudaStream_t st
                                  dim3(groups * tpr), 0, st, a, tpr);
 }
 
-// The ring, where two rows of every group fit beside the parameters and every
-// SM has a few rows for each group, and for unaligned rows;
+// The ring, where two rows of every group fit beside the parameters.  Not
+// where many rows would go through a block one at a time, each waiting for its
+// sums: there one block per row leaves several on an SM (bf16, 30 M elements:
+// H = 5120, two groups, 44 us against 50; H = 8192, one group, 50 against 44).
 // cudaErrorNotSupported: not here.
 template <typename T, int V> struct BnFwdUnits {
   static constexpr int kWidth = V == 1 ? 2 : V;           // elements of a unit
@@ -893,7 +899,7 @@ static cudaError_t bn_ring_launch(const BlockNormFwd& a, int tpr, cudaStream_t s
   const size_t ring = V > 1 ? 2 * (token_gate ? 3 : 2) * sizeof(T) * span * groups : 0;
   const size_t smem = 2 * sizeof(float) * span + ring;
   const int64_t sms = num_sms();
-  if (smem > kBnMostSmem || (V > 1 && a.T < 4 * sms * groups)) return cudaErrorNotSupported;
+  if (smem > kBnMostSmem || (V > 1 && groups == 1 && a.T > 4 * sms)) return cudaErrorNotSupported;
   auto kern = token_gate ? block_norm_ring_kernel<T, V, NU, true> : block_norm_ring_kernel<T, V, NU, false>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
@@ -902,9 +908,9 @@ static cudaError_t bn_ring_launch(const BlockNormFwd& a, int tpr, cudaStream_t s
   // block starts with a load it has nothing to run under (1 / 3 waves, us:
   // 268 MB 46.6 / 50.5, 403 MB 68.1 / 63.2, 671 MB 108 / 100).
   const int64_t share = a.T * a.H * static_cast<int64_t>(sizeof(T)) * (2 + token_gate + 1 + (a.pre_w != nullptr)) / sms;
-  const int64_t want = (a.T + groups - 1) / groups, most = share > (2 << 20) ? 3 * sms : sms;
-  return launch_dependent_kernel(kern, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(groups * tpr),
-                                 smem, st, a, tpr, span);
+  const int64_t most = share > (2 << 20) ? 3 * sms : sms;
+  return launch_dependent_kernel(kern, dim3(static_cast<unsigned>(a.T < most ? a.T : most)), dim3(groups * tpr), smem,
+                                 st, a, tpr, span);
 }
 template <typename T, int V>
 static cudaError_t bn_ring_pick(const BlockNormFwd& a, cudaStream_t st) {
@@ -929,18 +935,12 @@ template <typename T, int V>
 static cudaError_t bn_fwd_pick(const BlockNormFwd& a, cudaStream_t st) {
   const cudaError_t ring = bn_ring_pick<T, V>(a, st);
   if (ring != cudaErrorNotSupported) return ring;
-  // up to 32 elements a thread; fewer, where a warp holds the row with fewer
+  // 32 or 24 elements a thread, whichever leaves fewer idle
   const int nv = a.H / V;
-  constexpr int kMost = 32 / V;
-  constexpr int kSome = kMost * 3 / 4, kHalf = kMost / 2, kFew = kMost / 4;
-  if (nv <= 32 * kFew) return bn_fwd_launch<T, V, kFew>(a, 32, st);
-  const int options[3] = {kMost, kSome, kHalf};
-  int best = kMost;
-  for (int NV : options)
-    if (NV * bn_tpr(nv, NV) < best * bn_tpr(nv, best) && bn_tpr(nv, NV) <= kBnFwdThreads) best = NV;
-  if (best == kMost) return bn_fwd_launch<T, V, kMost>(a, bn_tpr(nv, kMost), st);
-  if (best == kSome) return bn_fwd_launch<T, V, kSome>(a, bn_tpr(nv, kSome), st);
-  return bn_fwd_launch<T, V, kHalf>(a, bn_tpr(nv, kHalf), st);
+  constexpr int kMost = 32 / V, kSome = 24 / V;
+  const int tpr = bn_tpr(nv, kSome);
+  if (tpr <= kBnFwdThreads && kSome * tpr < kMost * bn_tpr(nv, kMost)) return bn_fwd_launch<T, V, kSome>(a, tpr, st);
+  return bn_fwd_launch<T, V, kMost>(a, bn_tpr(nv, kMost), st);
 }
 
 cudaError_t launch_block_norm(int dtype, const BlockNormFwd& a, cudaStream_t st) {

@@ -115,7 +115,7 @@ def test_plain_norm(T, H, dtype):
 @pytest.mark.parametrize("T,H,post,gate,pre,branch", [
     (20000, 256, True, "channel", True, True), (9733, 8, True, "token", True, True), (9999, 24, False, None, True, True),
     (10001, 40, True, None, False, True), (12345, 768, False, "channel", True, True), (10000, 64, True, "channel", True, False),
-    (3000, 2432, True, "token", False, True), (5003, 1000, True, "channel", True, True), (700, 8192, True, "token", True, True),
+    (3000, 2432, True, "token", False, True), (5003, 1000, True, "channel", True, True), (640, 6528, True, "channel", True, True), (1300, 8192, False, None, True, True), (700, 8192, True, "token", True, True),
     (650, 12288, True, None, True, True), (40, 12288, True, "token", True, True), (11000, 33, True, "channel", True, True)])
 def test_many_tokens(T, H, post, gate, pre, branch, dtype):
     d = make(T, H, dtype, post, gate, pre, branch=branch)
