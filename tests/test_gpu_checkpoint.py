@@ -31,7 +31,7 @@ def same(got, want):
     return torch.equal(got.isnan(), want.isnan()) and torch.equal(got[~got.isnan()], want[~want.isnan()])
 
 
-SHAPES = [(1, 1), (1, 2432), (3, 31), (5, 32), (4, 33), (100, 768), (17, 1000), (9, 1001), (64, 4864), (300, 200), (7, 48),
+SHAPES = [(3, 100), (70, 36), (5, 2051), (4, 20000), (2, 4100), (3, 8193), (1, 1), (1, 2432), (3, 31), (5, 32), (4, 33), (100, 768), (17, 1000), (9, 1001), (64, 4864), (300, 200), (7, 48),
           (2000, 96), (33, 24)]
 
 
@@ -88,7 +88,7 @@ def test_every_code_comes_back():
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("R,I", [(1, 1), (1, 2432), (3, 31), (100, 768), (17, 1000), (9, 1001), (130, 48), (31, 24), (600, 96)])
+@pytest.mark.parametrize("R,I", [(3, 100), (70, 36), (5, 2051), (3, 20000), (2, 4100), (3, 8193), (1, 1), (1, 2432), (3, 31), (100, 768), (17, 1000), (9, 1001), (130, 48), (31, 24), (600, 96)])
 def test_swiglu_and_its_gradient(R, I, dtype):
     u_ = U[dtype]
     gu = torch.cat([spread(R, I, dtype), spread(R, I, dtype, seed=1)], 1)

@@ -80,7 +80,8 @@ def check(T, H, E, k, align, dtype, how="skewed"):
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("T,H,E,k,align", [
     (1, 768, 8, 2, 1), (1, 8, 1, 1, 1), (2, 1, 2, 2, 3), (16, 768, 8, 2, 64), (33, 72, 4, 1, 16), (100, 7, 8, 8, 1),
-    (65, 1001, 64, 6, 5), (257, 256, 64, 8, 128), (1000, 96, 3, 2, 1), (2049, 40, 8, 2, 64), (700, 2432, 5, 3, 7), (4100, 8192, 8, 4, 16),
+    (65, 1001, 64, 6, 5), (257, 256, 64, 8, 128), (1000, 96, 3, 2, 1), (2049, 40, 8, 2, 64), (700, 2432, 5, 3, 7), (50, 100, 8, 2, 4), (9, 12, 3, 1, 1), (3, 8192, 8, 2, 16), (2, 4097, 9, 7, 2), (40, 6404, 64, 8, 128),
+    (1, 3000, 64, 4, 1), (4100, 8192, 8, 4, 16),
     (40, 10, 2, 5, 4), (5000, 64, 16, 4, 1), (20001, 8, 64, 2, 1024)])
 def test_sort_and_back(T, H, E, k, align, dtype):
     check(T, H, E, k, align, dtype)
