@@ -374,7 +374,7 @@ int mm_moe_backward(const void* x, const void* Wr,
  * these calls waits on the device (no watchdog), and none reads or writes the
  * 256-byte header of a workspace.  Outputs overlap neither inputs nor each
  * other, but where a declaration says so.  Workspace sizes are those of the
- * current device.
+ * current device; where a size is 0, no workspace is needed (NULL will do).
  * ---------------------------------------------------------------------- */
 
 /* Norms before and after a block, its gate and its residual scale, in one

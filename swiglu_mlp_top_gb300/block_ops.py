@@ -60,13 +60,18 @@ def _empty(shape, dtype, dev, stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _scratch(workspace, dev: int, name: str):
-    """Address and bytes of a workspace."""
+def _scratch(workspace, need: int, dev: int, stream, name: str):
+    """(address, bytes, owner) of the caller's workspace, or of a fresh one where one is needed."""
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = _empty(need, torch.uint8, dev, stream)
+        return workspace.data_ptr(), need, workspace
     if not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev:
         raise ValueError(f"workspace of {name} must be a tensor on cuda:{dev}")
     if not workspace.is_contiguous():
         raise ValueError(f"workspace of {name} must be contiguous")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 # ------------------------------------------------------------- block norms
@@ -165,12 +170,8 @@ def block_norm_backward(dn: Optional[torch.Tensor], dr: Optional[torch.Tensor],
         pdn, pr = _arg(dn, "dn", dev, dtype, shape), _arg(r, "r", dev, dtype, shape)
     pdr, pf = _arg(dr, "dr", dev, dtype, shape), _arg(f, "f", dev, dtype, shape)
     lib = L.load()
-    if workspace is None:
-        nbytes = lib.mm_block_norm_backward_workspace_bytes(T, H, dt)
-        workspace = _empty(nbytes, torch.uint8, dev, stream)
-        pws = workspace.data_ptr()
-    else:
-        pws, nbytes = _scratch(workspace, dev, "block_norm_backward")
+    pws, nbytes, keep = _scratch(workspace, lib.mm_block_norm_backward_workspace_bytes(T, H, dt), dev, stream,
+                                 "block_norm_backward")
     out = {"dx": _empty(shape, dtype, dev, stream)}
     pdf = pdpost = pdgate = pdpre = None
     if f is not None:
@@ -188,6 +189,7 @@ def block_norm_backward(dn: Optional[torch.Tensor], dr: Optional[torch.Tensor],
     rc = lib.mm_block_norm_backward(
         pdn, pdr, pr, pf, post, g, per_token, pre, rstd[0], rstd[1], residual_scale, T, H, dt,
         out["dx"].data_ptr(), pdf, pdpost, pdgate, pdpre, pws, nbytes, raw)
+    del keep                                    # until the work is enqueued
     L.check(rc, "mm_block_norm_backward")
     return out
 
@@ -233,12 +235,7 @@ def moe_permute(x: torch.Tensor, topk_idx: torch.Tensor, E: int, *, align: int =
     if R < 0:
         raise L.MMError(L.MM_ERR_UNSUPPORTED, "mm_moe_permute")
     plan = {} if plan is None else plan
-    if workspace is None:
-        nbytes = lib.mm_moe_permute_workspace_bytes(T, E, k)
-        workspace = _empty(nbytes, torch.uint8, dev, stream)
-        pws = workspace.data_ptr()
-    else:
-        pws, nbytes = _scratch(workspace, dev, "moe_permute")
+    pws, nbytes, keep = _scratch(workspace, lib.mm_moe_permute_workspace_bytes(T, E, k), dev, stream, "moe_permute")
     if out is None:
         out = _empty((R, H), x.dtype, dev, stream)
     po = _arg(out, "out", dev, x.dtype, (R, H))
@@ -246,6 +243,7 @@ def moe_permute(x: torch.Tensor, topk_idx: torch.Tensor, E: int, *, align: int =
         px, pi, T, H, E, k, align, dt, po, _table(plan, "offsets", (E + 1,), dev, stream),
         _table(plan, "counts", (E,), dev, stream), _table(plan, "perm", (R,), dev, stream),
         _table(plan, "pos", (T, k), dev, stream), pws, nbytes, raw)
+    del keep                                    # until the work is enqueued
     L.check(rc, "mm_moe_permute")
     return out, plan
 

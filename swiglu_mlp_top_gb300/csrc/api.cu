@@ -958,7 +958,8 @@ int mm_block_norm(const void* x, const void* f, const void* post_w, const void* 
 
 size_t mm_block_norm_backward_workspace_bytes(int64_t T, int H, int dtype) {
   if (!valid_dtype(dtype) || T < 0 || H < 1 || H > MM_NORM_MAX_H) return 0;
-  return sizeof(WsHeader) + align_up(block_norm_bwd_bytes(T, H, dtype));
+  const size_t scratch = T > 0 && block_norm_bwd_one_block(T, H, dtype) ? 0 : block_norm_bwd_bytes(T, H, dtype);
+  return scratch ? sizeof(WsHeader) + align_up(scratch) : 0;
 }
 
 int mm_block_norm_backward(const void* dn, const void* dr, const void* r, const void* f,
@@ -989,12 +990,11 @@ int mm_block_norm_backward(const void* dn, const void* dr, const void* r, const 
     if (!aligned16(q)) return MM_ERR_INVALID_ARG;
   if (!aligned4(d_gate) || !aligned4(d_post_w) || !aligned4(d_pre_w)) return MM_ERR_INVALID_ARG;
   if (!aligned4(rstd_post) || !aligned4(rstd_pre)) return MM_ERR_INVALID_ARG;
-  if (!workspace || !aligned16(workspace) ||
-      workspace_bytes < mm_block_norm_backward_workspace_bytes(T, H, dtype))
-    return MM_ERR_WORKSPACE;
+  const size_t need = mm_block_norm_backward_workspace_bytes(T, H, dtype);
+  if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return MM_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   BlockNormBwd a{dn, dr, r, f, post_w, gate, pre_w, rstd_post, rstd_pre, dx, df, d_post_w, d_gate,
-                 d_pre_w, f32_at(workspace, sizeof(WsHeader)), T, H, token_gate, residual_scale};
+                 d_pre_w, need > 0 ? f32_at(workspace, sizeof(WsHeader)) : nullptr, T, H, token_gate, residual_scale};
   cudaError_t e = cudaSuccess;
   if (T > 0) {
     e = counted_launch(MM_KERNEL_NORM, st, [&] { return launch_block_norm_bwd_rows(dtype, a, st); });
@@ -1016,7 +1016,8 @@ int64_t mm_moe_permuted_rows(int64_t T, int E, int k, int align) {
 
 size_t mm_moe_permute_workspace_bytes(int64_t T, int E, int k) {
   if (mm_moe_permuted_rows(T, E, k, 1) < 0) return 0;
-  return sizeof(WsHeader) + align_up(permute_bytes(T, E, k));
+  const size_t scratch = permute_bytes(T, E, k);
+  return scratch ? sizeof(WsHeader) + align_up(scratch) : 0;
 }
 
 int mm_moe_permute(const void* x, const int32_t* topk_idx, int64_t T, int H, int E, int k,
@@ -1030,12 +1031,11 @@ int mm_moe_permute(const void* x, const int32_t* topk_idx, int64_t T, int H, int
   if (T > 0 && (!present16(x) || !present16(xs) || !topk_idx || !perm || !pos ||
                 !aligned4(topk_idx) || !aligned4(perm) || !aligned4(pos)))
     return MM_ERR_INVALID_ARG;
-  if (!workspace || !aligned16(workspace) ||
-      workspace_bytes < mm_moe_permute_workspace_bytes(T, E, k))
-    return MM_ERR_WORKSPACE;
+  const size_t need = mm_moe_permute_workspace_bytes(T, E, k);
+  if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return MM_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const PermuteArgs a{x, topk_idx, xs, offsets, counts, perm, pos, ws_at(workspace, sizeof(WsHeader)),
-                      T, rows, H, E, k, align};
+  const PermuteArgs a{x, topk_idx, xs, offsets, counts, perm, pos,
+                      need > 0 ? ws_at(workspace, sizeof(WsHeader)) : nullptr, T, rows, H, E, k, align};
   cudaError_t e;
   if (permute_counts_first(T, k)) {
     e = counted_launch(MM_KERNEL_PERMUTE, st, [&] { return launch_permute_count(a, st); });

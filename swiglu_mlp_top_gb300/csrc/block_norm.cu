@@ -623,7 +623,7 @@ block_norm_bwd_kernel(const BlockNormBwd a, int tpr, int span, int stages) {
     U::keep(mine + span, m, c0, tpr, nv, s_mid[m]);
   }
   __syncthreads();
-  float* part = a.partial + static_cast<int64_t>(blockIdx.x) * kBnSums * a.H;
+  float* part = a.partial + static_cast<int64_t>(blockIdx.x) * kBnSums * a.H;   // not used by one block
   using P = Pack<T, V>;
   const bool one = gridDim.x == 1, chan_gate = a.gate != nullptr && !kTokenGate;
   for (int c = threadIdx.x; c < nv; c += blockDim.x) {
@@ -870,6 +870,7 @@ static BnBwdShape bn_bwd_shape(int64_t T, int H, int dtype) {
 }
 
 size_t block_norm_bwd_bytes(int64_t T, int H, int dtype) {
+  if (T == 0) return 0;
   return 4 * static_cast<size_t>(bn_bwd_shape(T, H, dtype).grid) * kBnSums * H;
 }
 

@@ -51,10 +51,11 @@ def test_block_norm_backward_refusals(lib):
                dict(pre=None, dpre=None, dn=None, dr=None)):
         assert norm_bwd(lib, **kw) == BAD, kw
     assert norm_bwd(lib, H=L.MM_NORM_MAX_H + 1) == UNS
-    assert norm_bwd(lib, wsb=10) == WS and norm_bwd(lib, ws=None) == WS and norm_bwd(lib, ws=ODD) == WS
+    if lib.mm_block_norm_backward_workspace_bytes(10000, 768, BF):                # several blocks: there is a GPU
+        assert norm_bwd(lib, T=10000, wsb=10) == WS and norm_bwd(lib, T=10000, ws=None) == WS and norm_bwd(lib, T=10000, ws=ODD) == WS
     assert lib.mm_block_norm_backward_workspace_bytes(10, 768, 7) == 0
     assert lib.mm_block_norm_backward_workspace_bytes(10, L.MM_NORM_MAX_H + 1, BF) == 0
-    assert lib.mm_block_norm_backward_workspace_bytes(10, 768, BF) > 256
+    assert lib.mm_block_norm_backward_workspace_bytes(0, 768, BF) == 0            # none needed
 
 
 def test_permute_refusals(lib):
@@ -65,7 +66,8 @@ def test_permute_refusals(lib):
         assert call(**kw) == BAD, kw
     for kw in (dict(E=65), dict(k=9), dict(align=1025), dict(T=1 << 30), dict(H=L.MM_PERMUTE_MAX_H + 1)):
         assert call(**kw) == UNS, kw
-    assert call(ws=None) == WS and call(wsb=0) == WS
+    assert call(T=5000, ws=None) == WS and call(T=5000, wsb=0) == WS and call(T=5000, ws=ODD) == WS
+    assert lib.mm_moe_permute_workspace_bytes(10, 4, 2) == 0                      # none needed
     assert lib.mm_moe_permuted_rows(10, 4, 2, 8) == 20 + 4 * 7
     assert lib.mm_moe_permuted_rows(1, 64, 2, 8) == 2 + 2 * 7          # no more groups than assignments
     assert lib.mm_moe_permuted_rows(0, 4, 2, 8) == 0

@@ -74,7 +74,7 @@ def check_backward(d, r, stats, got, s=1.0, dr=True):
         close(got[k], want[k], bound, k)
 
 
-SHAPES = [(1, 768), (1, 1), (3, 8), (5, 7), (33, 64), (70, 1000), (129, 1001), (200, 2432), (17, 4096), (9, 8192),
+SHAPES = [(1, 768), (1, 1), (3, 8), (5, 7), (33, 64), (70, 1000), (129, 1001), (200, 2432), (17, 4096), (9, 8192), (7, 8191), (6, 4097),
           (5, 16384), (3, 16383), (1500, 768), (2100, 96)]
 
 
@@ -287,5 +287,7 @@ def test_refusals():
         mm.block_norm_backward(d["dn"], d["dr"], r, f, {}, pre_weight=w)
     with pytest.raises(ValueError):
         mm.block_norm_backward(d["dn"], d["dr"], r, None, stats, pre_weight=w, gate=w)
+    d = make(1000, 64, BF)
+    r, n, stats = forward(d)
     with pytest.raises(mm._lib.MMError):
         backward(d, r, stats, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))

@@ -117,3 +117,58 @@ def test_training_step(full_fp32, T, H, I, E, k, align):
     # what the 8 bits cost against the unquantised gradient: a step of 2^-4 on g and u
     true = torch.cat(ref.swiglu_backward(gua[:, :I], gua[:, I:], dha)[:2], 1)
     assert (dga - true).norm() <= 2 * 2.0 ** -4 * true.norm()
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own workspace, give what they give alone."""
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    T, H, E, k = 3000, 768, 8, 2
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+
+    def inputs():
+        rand = lambda *s: torch.randn(*s, generator=gen, device="cuda").bfloat16()  # noqa: E731
+        return dict(x=rand(T, H), f=rand(T, H), w=rand(H), dn=rand(T, H), w_route=torch.rand(T, k, generator=gen, device="cuda"),
+                    idx=torch.randint(0, E, (T, k), generator=gen, device="cuda", dtype=torch.int32))
+
+    def step(q, stream):
+        stats, ck = {}, {}
+        r, n = mm.block_norm(q["x"], q["f"], post_weight=q["w"], gate=q["w"], pre_weight=q["w"], stats=stats, stream=stream)
+        g = mm.block_norm_backward(q["dn"], None, r, q["f"], stats, post_weight=q["w"], gate=q["w"], pre_weight=q["w"], stream=stream)
+        xs, plan = mm.moe_permute(n, q["idx"], E, stream=stream)
+        h = mm.swiglu_act(xs, checkpoint=ck, stream=stream)
+        dgu, _ = mm.swiglu_act_backward(ck, h, stream=stream)
+        return [r, n, *(g[k] for k in sorted(g)), xs, mm.moe_unpermute(dgu, plan, q["w_route"], stream=stream)]
+
+    qs = [inputs(), inputs()]
+    alone = [step(q, None) for q in qs]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = [step(q, s) for q, s in zip(qs, side)]
+        torch.cuda.synchronize()
+        for a, b in zip(alone, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_two_graphs_share_a_workspace_on_one_stream():
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    H, sizes = 512, (2500, 4000)
+    rand = lambda *s: torch.randn(*s, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    w = rand(H)
+    ws = mm.new_workspace(max(mm.block_norm_backward_workspace_bytes(T, H, torch.bfloat16) for T in sizes))
+    qs, graphs, outs = [(rand(T, H), rand(T, H)) for T in sizes], [], []
+
+    def step(x, dn, **kw):
+        stats = {}
+        mm.block_norm(x, pre_weight=w, stats=stats)
+        return mm.block_norm_backward(dn, None, x, None, stats, pre_weight=w, **kw)
+
+    want = [step(*q) for q in qs]
+    for q in qs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(step(*q, workspace=ws))
+    for i in (0, 1, 0, 0, 1):
+        graphs[i].replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, outs):
+        assert all(torch.equal(a[k], b[k]) for k in a)
