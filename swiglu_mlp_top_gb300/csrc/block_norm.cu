@@ -61,10 +61,6 @@ struct Unit {
                    : "memory");
   }
   static __device__ __forceinline__ Raw zero() { return Raw{}; }
-  static __device__ __forceinline__ Raw load(const void* p, int64_t base, int m, int c0, int tpr, int nv) {
-    const int c = c0 + m * tpr;
-    return c < nv ? row_load<T, V>(p, base, c) : zero();
-  }
   static __device__ __forceinline__ u64 get(const Raw& r, int k) {
     return pair2(Pack<T, V>::get(r, 2 * k), Pack<T, V>::get(r, 2 * k + 1));
   }
@@ -115,7 +111,6 @@ struct Unit<T, 1> {
   struct __align__(2 * sizeof(T)) Raw {
     T a, b;
   };
-  static __device__ __forceinline__ void copy(uint32_t, const void*, int64_t, int, int, int, int) {}
   static __device__ __forceinline__ Raw zero() { return Raw{T(0.f), T(0.f)}; }
   static __device__ __forceinline__ Raw load(const void* p, int64_t base, int m, int c0, int tpr, int nv) {
     const T* row = static_cast<const T*>(p) + base;

@@ -7,11 +7,10 @@
 // All kernels stream: each input is read and each output written once.  A
 // thread owns V consecutive columns (V / 32 of a group), always the same ones
 // of a row, and walks down the rows; V is the widest of 16, 8 and 4 that
-// divides the width, so that values and codes move in whole aligned accesses.
+// divides the width (within what ck_vec allows the type), so that values and
+// codes move in whole aligned accesses.
 // Rows of other widths go in strips of 128 columns, a warp each: a lane has
 // one column of each of the strip's four groups, and single accesses.
-#include <algorithm>
-#include <cstdlib>
 #include "mm_kernels.cuh"
 
 namespace mm {
@@ -169,7 +168,7 @@ __device__ __forceinline__ void sigmoid2(u64 g, u64& sig, u64& rest) {
     constexpr double kC = 0.72134752044448170368;               // log2(e) / 2
     constexpr float kHead = static_cast<float>(kC), kTail = static_cast<float>(kC - static_cast<double>(kHead));
     constexpr float kLn2 = 0.693147180559945f;
-    // -|g|, but no infinity, whose tail would be a NaN (t is 0 from 208 on)
+    // -|g|, but no infinity, whose tail would be a NaN (t is 0 from 104 on)
     const u64 a = pair2(fmaxf(-fabsf(g0), -256.0f), fmaxf(-fabsf(g1), -256.0f));
     const u64 q = fmul2(a, pair2(kHead, kHead));
     const u64 r = ffma2(a, pair2(kTail, kTail), ffma2(a, pair2(kHead, kHead), q ^ 0x8000000080000000ull));
