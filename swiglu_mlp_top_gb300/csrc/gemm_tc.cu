@@ -1053,10 +1053,14 @@ int resident_blocks(const void* fn, int threads) {
   static std::map<std::tuple<int, const void*, int>, int> known;
   int dev = 0;
   cudaGetDevice(&dev);
-  std::lock_guard<std::mutex> lock(mu);
-  int& n = known[std::make_tuple(dev, fn, threads)];
-  if (n == 0 && cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, 0) != cudaSuccess) n = 0;
-  return n > 0 ? n : 1;
+  try {
+    std::lock_guard<std::mutex> lock(mu);
+    int& n = known[std::make_tuple(dev, fn, threads)];
+    if (n == 0 && cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, 0) != cudaSuccess) n = 0;
+    return n > 0 ? n : 1;
+  } catch (...) {                             // no host memory for the table: callers are C entries
+    return 1;
+  }
 }
 
 cudaError_t ensure_dynamic_smem(const void* fn, size_t bytes) {
@@ -1064,13 +1068,17 @@ cudaError_t ensure_dynamic_smem(const void* fn, size_t bytes) {
   static std::map<std::pair<int, const void*>, size_t> done;
   int dev = 0;
   cudaGetDevice(&dev);
-  std::lock_guard<std::mutex> lock(mu);
-  auto it = done.find({dev, fn});
-  if (it != done.end() && it->second >= bytes) return cudaSuccess;
-  const cudaError_t e =
-      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-  if (e == cudaSuccess) done[{dev, fn}] = bytes;
-  return e;
+  try {
+    std::lock_guard<std::mutex> lock(mu);
+    size_t& most = done[{dev, fn}];
+    if (most >= bytes) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess) most = bytes;
+    return e;
+  } catch (...) {                             // no host memory for the table: callers are C entries
+    return cudaErrorMemoryAllocation;
+  }
 }
 
 // Launch with programmatic stream serialisation (the kernel may start while
