@@ -110,7 +110,8 @@ router_kernel(const Tin* __restrict__ x, const Tin* __restrict__ Wr, const float
   static_assert(kPerWarp % TPW == 0, "passes cover a warp's tokens");
 
   // the dispatch kernel may launch as soon as router blocks start to leave
-  // (it waits for this grid before reading the routing results)
+  // (it waits for this grid before reading the routing results; this grid is
+  // no programmatic dependent, so everything before it has finished)
   if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int rblk = blockIdx.x;                     // router block: tokens [64 rblk, +64)
   const int nblk = static_cast<int>((T + kRouteTokensPerBlock - 1) / kRouteTokensPerBlock);
@@ -672,8 +673,11 @@ dispatch_kernel(const Tin* __restrict__ x, int64_t T, int H, int E, int k,
         : "memory");
   }
 
-  // the routing results come from the router grid, launched just before
-  // (x is the caller's input and may be read at once)
+  // the routing results come from the router grid, launched just before.  x
+  // may be read at once: it is the caller's input, and the router let this
+  // grid launch only when everything before the router had finished
+  // (router_tc_kernel triggers behind its wait, router_kernel is launched
+  // without programmatic serialisation)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -866,8 +870,6 @@ router_tc_kernel(const __grid_constant__ RtMaps M, int64_t T, int H, int E, int 
                  const float* __restrict__ bias, int32_t* __restrict__ topk_idx,
                  float* __restrict__ topk_w, int32_t* __restrict__ blk_cnt,
                  float* __restrict__ blk_prob, const RouteExtras X, int nkb, uint32_t stage_bytes) {
-  // the dispatch kernel may launch as soon as router blocks start to leave
-  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ unsigned char rt_raw[];
   uint8_t* smem = align1024(rt_raw);
   __shared__ __align__(8) uint64_t full[kRtStages], empty[kRtStages], lbar, drained;
@@ -908,6 +910,9 @@ router_tc_kernel(const __grid_constant__ RtMaps M, int64_t T, int H, int E, int 
   // previous kernel of the stream, whose outputs (x, Wr, the bias, or the
   // buffers written here) are touched only once it has finished
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // only now may the dispatch kernel launch: it copies its x rows at once,
+  // without a wait of its own, and x may be that kernel's output
+  if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid < EP) s_bias[tid] = (bias != nullptr && tid < E) ? bias[tid] : 0.f;
   tc_fence_before();
   __syncthreads();
