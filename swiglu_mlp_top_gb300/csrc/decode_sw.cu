@@ -156,40 +156,26 @@ decode_sw_kernel(const __grid_constant__ SwMaps M, const SwArgs A) {
     // >= Np, whose products land in TMEM lanes that are never read.  A down
     // stage = the three Wd tiles of one TMEM pass (blocks past H read as 0).
     //
-    // As a programmatic dependent of the previous call, the weights of the
-    // first S stages are requested before griddepcontrol.wait (they need
-    // nothing from the previous kernel); the x tiles of those stages wait for
-    // it, and are requested before any stage is reused.
+    // The previous kernel of the stream, beside which this one starts, may
+    // write a weight as well as x (an unpacked checkpoint, a normed matrix):
+    // nothing is read before it has finished.  (Asking for the weights early
+    // saved nothing: T = 16 / 64 / 100 take 13.7 / 16.5 / 19.4 us, with the
+    // first stages loaded before the wait 14.4 / 16.4 / 19.0, with them only
+    // prefetched into L2 13.8 / 16.4 / 19.4.)
     const uint64_t pol = l2_evict_first_policy();
-    bool waited = !A.pdl;
-    int n_def = 0, def_s[kSwMaxStages], def_kb[kSwMaxStages];
-    auto flush = [&]() {
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-      waited = true;
-      for (int i = 0; i < n_def; ++i)
-        tma_load_3d(ring + def_s[i] * SB, &M.x, &full[def_s[i]], 0, 0, def_kb[i]);
-      n_def = 0;
-    };
+    if (A.pdl) asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int u = cta; ok && u < A.n_units; u += G) {
       for (int kb0 = 0; kb0 < KB_H; kb0 += nkb) {
-        if (!waited && p_it >= S) flush();
         int s;
         if (!acquire(s)) { ok = false; break; }
         uint8_t* st = ring + s * SB;
         mbar_arrive_expect_tx(&full[s], xpart + 2 * wpart);
-        if (waited) {
-          tma_load_3d(st, &M.x, &full[s], 0, 0, kb0);
-        } else {
-          def_s[n_def] = s;
-          def_kb[n_def] = kb0;
-          ++n_def;
-        }
+        tma_load_3d(st, &M.x, &full[s], 0, 0, kb0);
         tma_load_3d_hint(st + xpart, &M.wg, &full[s], 0, u * kSwRows, kb0, pol);
         tma_load_3d_hint(st + xpart + wpart, &M.wu, &full[s], 0, u * kSwRows, kb0, pol);
         ++p_it;
       }
       for (int p = 0; ok && p < n_pass; ++p) {
-        if (!waited && p_it >= S) flush();
         int s;
         if (!acquire(s)) { ok = false; break; }
         mbar_arrive_expect_tx(&full[s], kSwPassBlocks * kSwDTile);
@@ -197,7 +183,6 @@ decode_sw_kernel(const __grid_constant__ SwMaps M, const SwArgs A) {
         ++p_it;
       }
     }
-    if (!waited) flush();
   }
   if (tid == 32) {
     const uint32_t idesc_gu = idesc_bf16_f32(128, kSwRows);

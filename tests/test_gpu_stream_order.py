@@ -89,3 +89,52 @@ def test_moe_forward_behind_the_operator_that_makes_x(T, H, I, E, k, separate, m
         rows = np.linspace(0, T - 1, 40).astype(int)
         want = ref_y_rows(inp64, ref, idx, rows, k)
         assert rel_err(b["out"].double().cpu().numpy()[rows], want) <= Y_TOL["bf16"]
+
+
+# the streaming kernel of 5 to 128 tokens, with its two unit sizes, and the
+# paths on both sides of it
+@pytest.mark.parametrize("T", [1, 16, 64, 100, 300])
+@pytest.mark.parametrize("made,by", [(m, b) for m in ("x", "Wg", "Wu", "Wd") for b in ("unpack", "norm")] + [("x", "a call before")])
+def test_swiglu_ffn_behind_the_operator_that_makes_an_operand(T, made, by):
+    H, I = 256, 128
+    g = to_dev(moe_inputs(T, H, I, 0, "bf16", seed=T))
+    shape = g[made].shape
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    raw = [(g[made].float().std() * torch.randn(shape, generator=gen, device="cuda")).to(BF) for _ in range(CALLS)]
+    packed = [mm.checkpoint_pack(r) for r in raw]
+    ones, buf = torch.full(shape[1:], 0.05, dtype=BF, device="cuda"), torch.empty(shape, dtype=BF, device="cuda")
+    ws = mm.new_workspace(mm.ffn_workspace_bytes(T, H, I, BF))
+    outs = [torch.empty(T, H, dtype=BF, device="cuda") for _ in range(CALLS)]
+
+    def make(i):
+        if by == "unpack":
+            mm.checkpoint_unpack(packed[i], BF, out=buf)
+        elif by == "norm":
+            mm.block_norm(raw[i], pre_weight=ones, normed=buf)
+        else:
+            mm.swiglu_ffn(raw[i], g["Wg"], g["Wu"], g["Wd"], out=buf, workspace=ws)
+
+    def ffn(**kw):
+        p = dict(g, **{made: buf})
+        return mm.swiglu_ffn(p["x"], p["Wg"], p["Wu"], p["Wd"], **kw)
+
+    make(0)
+    ffn(workspace=ws)                                  # kernels loaded, attributes set
+    torch.cuda.synchronize()
+    for i in range(CALLS):
+        make(i)
+        ffn(out=outs[i], workspace=ws)
+    torch.cuda.synchronize()
+    for i in range(CALLS):
+        make(i)
+        torch.cuda.synchronize()
+        alone = ffn(workspace=mm.new_workspace(ws.numel()))
+        assert torch.equal(outs[i], alone), i
+    p = {n: to_f64(v.cpu()) for n, v in dict(g, **{made: buf}).items() if v is not None}
+    want = oracle.swiglu_ffn(p["x"], p["Wg"], p["Wu"], p["Wd"])
+    # more than 128 tokens: h is kept in fp16, whose step below 2^-14 is 2^-24.
+    # An h that small is off by up to 2^-25 whatever its size, and with every
+    # one of them off y is by 2^-25 sum_i |Wd|: nothing beside the tolerance for
+    # y of order one, but the FFN of an FFN's output is y ~ 1e-6 here.
+    tiny = 2.0 ** -25 * np.abs(p["Wd"]).sum(1).max() / np.sqrt(np.mean(want ** 2)) if T > 128 else 0.0
+    assert rel_err(outs[-1].double().cpu().numpy(), want) <= Y_TOL["bf16"] + tiny

@@ -45,3 +45,35 @@ def test_a_successor_launches_only_behind_the_wait(name, body):
     the kernels before its predecessor, would read what those still write."""
     trigger = TRIGGER.search(body)
     assert trigger is None or WAIT.search(body).start() <= trigger.start(), name
+
+
+LOAD = r"tma_load|tma_gather|row_load|\bcp\.async\.(?!bulk\.prefetch)"
+
+
+def straight_line(body):
+    """The body without comments and lambdas, and {name: body} of those: what a
+    lambda does happens where it is called."""
+    code, lambdas = re.sub(r"//[^\n]*", "", body), {}
+    while True:
+        m = re.search(r"auto (\w+) = \[[^]]*\]\([^)]*\)[^{;]*\{", code)
+        if m is None:
+            return code, lambdas
+        depth, j = 1, m.end()
+        while depth:
+            depth += {"{": 1, "}": -1}.get(code[j], 0)
+            j += 1
+        lambdas[m.group(1)] = code[m.end():j]
+        code = code[:m.start()] + code[j:]
+
+
+@pytest.mark.parametrize("name,body", [pytest.param(n, b, id=n) for n, b in KERNELS
+                                       if WAIT.search(b) and n != "routing.cu:dispatch_kernel"])
+def test_nothing_is_loaded_before_the_wait(name, body):
+    """What a kernel reads may be its predecessor's output, a weight as well as
+    an activation.  The dispatch alone copies rows of x first: its predecessor
+    is always the router, which lets it launch only behind its own wait.  (A
+    prefetch into L2 reads nothing.)"""
+    code, lambdas = straight_line(body)
+    loaders = [n for n, b in lambdas.items() if re.search(LOAD, b)]
+    load = re.search("|".join([LOAD] + [rf"\b{n}\(" for n in loaders]), code)
+    assert load is None or WAIT.search(code).start() < load.start(), (name, load.group())
