@@ -993,6 +993,7 @@ int mm_block_norm_backward(const void* dn, const void* dr, const void* r, const 
   const size_t need = mm_block_norm_backward_workspace_bytes(T, H, dtype);
   if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return MM_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!post_w && !gate) f = nullptr;          // nothing depends on it: df = D
   BlockNormBwd a{dn, dr, r, f, post_w, gate, pre_w, rstd_post, rstd_pre, dx, df, d_post_w, d_gate,
                  d_pre_w, need > 0 ? f32_at(workspace, sizeof(WsHeader)) : nullptr, T, H, token_gate, residual_scale};
   cudaError_t e = cudaSuccess;

@@ -34,3 +34,25 @@ def test_without_a_post_norm_df_does_not_see_f(dtype, H, T, gate, bad):
     assert b["df"].isfinite().all()
     for key in ("dx", "df", "d_pre_weight"):
         assert torch.equal(a[key], b[key]), key
+
+
+@pytest.mark.parametrize("H", [768, 16384])
+@pytest.mark.parametrize("pre", [False, True])
+def test_f_is_not_needed_without_a_post_norm_and_a_gate(H, pre):
+    """df = D, through the C entry with no f at all."""
+    T, lib = 300, mm._lib.load()
+    gen = torch.Generator().manual_seed(H)
+    rand = lambda *shape: torch.randn(*shape, generator=gen).to(BF).cuda()  # noqa: E731
+    r, f, dr, dn, w, stats = rand(T, H), rand(T, H), rand(T, H), rand(T, H), rand(H), {}
+    mm.block_norm(r, pre_weight=w, stats=stats)
+    kw = dict(pre_weight=w) if pre else {}
+    want = mm.block_norm_backward(dn if pre else None, dr, r, f, stats, residual_scale=0.5, **kw)
+    dx, df, dw = torch.empty_like(r), torch.empty_like(r), torch.empty(H, device="cuda")
+    ws = mm.new_workspace(mm.block_norm_backward_workspace_bytes(T, H, BF))
+    ptr = lambda t: t.data_ptr() if pre else None  # noqa: E731
+    assert lib.mm_block_norm_backward(
+        ptr(dn), dr.data_ptr(), ptr(r), None, None, None, 0, ptr(w), None, ptr(stats["rstd_pre"]), 0.5, T, H,
+        mm._lib.MM_DTYPE_BF16, dx.data_ptr(), df.data_ptr(), None, None, ptr(dw), ws.data_ptr(), ws.numel(),
+        torch.cuda.current_stream().cuda_stream) == mm._lib.MM_OK
+    assert torch.equal(dx, want["dx"]) and torch.equal(df, want["df"])
+    assert not pre or torch.equal(dw, want["d_pre_weight"])
