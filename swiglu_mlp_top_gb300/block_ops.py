@@ -151,7 +151,9 @@ def block_norm_backward(dn: Optional[torch.Tensor], dr: Optional[torch.Tensor],
     dr = dL/dr (None: zero), from r, f and the forward's stats.  Returns a
     dict of what has a gradient: dx, df, d_post_weight and d_pre_weight
     (fp32 [H]), d_gate (fp32 [H], or x's dtype [T, H]).  f None: the plain
-    norm (r is its x)."""
+    norm (r is its x).  Without pre_weight there is no n, and dn must be None."""
+    if dn is not None and pre_weight is None:
+        raise ValueError("dn needs pre_weight: without it there is no n")
     lead, name = (dn, "dn") if pre_weight is not None else (dr, "dr")
     dt, dev, raw = _begin(lead, name, 2, stream)
     T, H = shape = lead.shape

@@ -123,6 +123,13 @@ def test_python_calls_refuse_what_is_not_on_the_gpu():
             call()
 
 
+def test_a_gradient_without_its_output_is_refused():
+    """dn belongs to the norm behind r; without that norm it must not be dropped in silence."""
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="dn needs pre_weight"):
+        mm.block_norm_backward(x, x, x, x, None)
+
+
 # ---------------------------------- the 64-bit forms against differences
 D = 2.0 ** -14
 # a central difference is off by D^2 / 6 times a third derivative (a few
