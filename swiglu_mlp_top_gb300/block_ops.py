@@ -103,7 +103,9 @@ def block_norm(x: torch.Tensor, f: Optional[torch.Tensor] = None, *,
     three may be None (left out); f None is a plain norm (r is x).  Returns
     (r, n), n None without pre_weight.  out / normed: r and n; `out` may be x
     and `normed` may be f (in place).  With a dict `stats`, it receives
-    rstd_post / rstd_pre [T] fp32, which block_norm_backward needs.
+    rstd_post / rstd_pre [T] fp32, which block_norm_backward needs; tensors
+    that it holds already are written anew, so give each layer a dict of its
+    own until its backward has run.
     """
     dt, dev, raw = _begin(x, "x", 2, stream)
     T, H = shape = x.shape
