@@ -383,15 +383,17 @@ def swiglu_act(gu: torch.Tensor, *, checkpoint: Optional[dict] = None,
     if out is None:
         out = _empty((R, I), gu.dtype, dev, stream)
     if checkpoint is not None:
-        if checkpoint.get("codes") is None:
-            checkpoint["codes"] = _empty((R, two_i), torch.float8_e4m3fn, dev, stream)
-        if checkpoint.get("exps") is None:
-            checkpoint["exps"] = _empty((R, 2 * _groups(I)), torch.uint8, dev, stream)
-        checkpoint["segments"] = 2
-        pc = _arg(checkpoint["codes"], "codes", dev, torch.float8_e4m3fn, (R, two_i))
-        pe = _arg(checkpoint["exps"], "exps", dev, torch.uint8, (R, 2 * _groups(I)))
+        codes, exps = checkpoint.get("codes"), checkpoint.get("exps")
+        if codes is None:
+            codes = _empty((R, two_i), torch.float8_e4m3fn, dev, stream)
+        if exps is None:
+            exps = _empty((R, 2 * _groups(I)), torch.uint8, dev, stream)
+        pc = _arg(codes, "codes", dev, torch.float8_e4m3fn, (R, two_i))
+        pe = _arg(exps, "exps", dev, torch.uint8, (R, 2 * _groups(I)))
     rc = L.load().mm_swiglu_act(pg, R, I, dt, pr, _arg(out, "out", dev, gu.dtype, (R, I)), pc, pe, raw)
     L.check(rc, "mm_swiglu_act")
+    if checkpoint is not None:                  # not before: a refused call leaves it as it was
+        checkpoint.update(codes=codes, exps=exps, segments=2)
     return out
 
 

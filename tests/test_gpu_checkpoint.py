@@ -258,3 +258,20 @@ def test_refusals():
     odd = torch.zeros(4 * 64 + 1, dtype=BF, device="cuda")[1:].view(4, 64)
     with pytest.raises(mm._lib.MMError):
         mm.checkpoint_pack(odd)
+
+
+def test_a_refused_call_leaves_the_checkpoint_alone():
+    """100 columns in one segment and twice 50 columns both take four exponents
+    a row: a checkpoint that a refused call relabels would unpack to other values."""
+    x = spread(6, 100, BF).cuda()
+    ck = mm.checkpoint_pack(x)
+    want = mm.checkpoint_unpack(ck, F32)
+    wide, kept = torch.zeros(6, 120, dtype=BF, device="cuda"), dict(ck)
+    for kw in (dict(), dict(out=torch.zeros(6, 61, dtype=BF, device="cuda"))):
+        with pytest.raises(ValueError):
+            mm.swiglu_act(wide, checkpoint=ck, **kw)
+        assert ck == kept and torch.equal(mm.checkpoint_unpack(ck, F32), want)
+    empty = {}
+    with pytest.raises(ValueError):
+        mm.swiglu_act(wide, checkpoint=empty, out=torch.zeros(6, 61, dtype=BF, device="cuda"))
+    assert not empty
