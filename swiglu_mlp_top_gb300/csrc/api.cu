@@ -6,6 +6,7 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
+#include <utility>
 #include <vector>
 
 #include "mm_kernels.cuh"
@@ -247,7 +248,7 @@ struct Profiler {
   int kernel = 0;
   int max = 0;
   int used = 0;
-  std::vector<cudaEvent_t> start, stop;
+  std::vector<std::pair<cudaEvent_t, cudaEvent_t>> events;    // before and behind a launch
 };
 Profiler g_prof;
 
@@ -260,16 +261,22 @@ cudaError_t counted_launch(int kernel, cudaStream_t st, F&& launch) {
     std::lock_guard<std::mutex> lock(g_prof.mu);
     if (g_prof.kernel == kernel && g_prof.used < g_prof.max) {
       const int i = g_prof.used;
-      if (i >= static_cast<int>(g_prof.start.size())) {
-        cudaEvent_t e0, e1;
+      if (i >= static_cast<int>(g_prof.events.size())) {
+        cudaEvent_t e0 = nullptr, e1 = nullptr;
+        bool kept = false;
         if (cudaEventCreate(&e0) == cudaSuccess && cudaEventCreate(&e1) == cudaSuccess) {
-          g_prof.start.push_back(e0);
-          g_prof.stop.push_back(e1);
+          try {
+            g_prof.events.emplace_back(e0, e1);
+            kept = true;
+          } catch (...) {                     // no host memory: the launch goes untimed
+          }
         }
+        if (!kept && e0) cudaEventDestroy(e0);
+        if (!kept && e1) cudaEventDestroy(e1);
       }
-      if (i < static_cast<int>(g_prof.start.size())) {
-        a = g_prof.start[i];
-        b = g_prof.stop[i];
+      if (i < static_cast<int>(g_prof.events.size())) {
+        a = g_prof.events[i].first;
+        b = g_prof.events[i].second;
         ++g_prof.used;
       }
     }
@@ -1165,10 +1172,10 @@ int mm_profile_stop(double* total_ms, int* launches) {
   double sum = 0.0;
   int n = g_prof.used;
   for (int i = 0; i < n; ++i) {
-    cudaError_t e = cudaEventSynchronize(g_prof.stop[i]);
+    cudaError_t e = cudaEventSynchronize(g_prof.events[i].second);
     if (e != cudaSuccess) return cuda_fail(e, "profile sync");
     float ms = 0.f;
-    e = cudaEventElapsedTime(&ms, g_prof.start[i], g_prof.stop[i]);
+    e = cudaEventElapsedTime(&ms, g_prof.events[i].first, g_prof.events[i].second);
     if (e != cudaSuccess) return cuda_fail(e, "profile elapsed");
     sum += ms;
   }

@@ -943,6 +943,17 @@ static EncodeTiledFn get_encode_fn() {
   return fn;
 }
 
+// Keeps an encoded map for the next call.  Without host memory for it the map
+// is encoded anew then: no exception leaves through the C entries.
+template <typename Cache, typename Key>
+static void remember(Cache& cache, const Key& key, const CUtensorMap& map) {
+  try {
+    if (cache.size() > 4096) cache.clear();
+    cache.emplace(key, map);
+  } catch (...) {
+  }
+}
+
 // 16-bit row-major [outer, inner] matrix (bf16 or fp16), box = box_inner
 // (inner) x box_rows (outer), zero fill outside the matrix.  Cached by
 // (ptr, shape, box, type, swizzle).
@@ -970,8 +981,7 @@ bool make_map_16(CUtensorMap* out, const void* ptr, uint64_t inner, uint64_t out
                          CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return false;
-  if (cache.size() > 4096) cache.clear();
-  cache.emplace(key, *out);
+  remember(cache, key, *out);
   return true;
 }
 
@@ -999,8 +1009,7 @@ bool make_map_2d(CUtensorMap* out, const void* ptr, bool fp32, uint64_t inner, u
                          CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return false;
-  if (cache.size() > 4096) cache.clear();
-  cache.emplace(key, *out);
+  remember(cache, key, *out);
   return true;
 }
 
@@ -1030,8 +1039,7 @@ bool make_map_3d(CUtensorMap* out, const void* ptr, const uint64_t dims[3],
                          estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return false;
-  if (cache.size() > 4096) cache.clear();
-  cache.emplace(key, *out);
+  remember(cache, key, *out);
   return true;
 }
 
