@@ -189,7 +189,9 @@ __device__ __forceinline__ void stage_params(const void* pre, const void* post, 
 }
 
 // ------------------------------------------------------------------ forward
-// Many wide rows: a group of threads per row, everything in registers.
+// The rows that the ring below does not take (bn_ring_pick): many that fill a
+// block each, and wider ones than its shared memory holds twice.  A group of
+// threads per row, everything in registers.
 constexpr size_t kBnMostSmem = 224 * 1024;   // dynamic, of 227 KB a block may have
 constexpr int kBnFwdThreads = 512;      // most threads of a block (one group of them: H = 16384)
 
@@ -276,10 +278,11 @@ __global__ void __launch_bounds__(kBnFwdThreads) block_norm_kernel(const BlockNo
 // The rule: a block of groups per SM walks down the rows, the next row's
 // inputs on their way to shared memory (each thread copies and reads its own
 // slots, so without a barrier), w_post g and w_pre there in fp32, sums and
-// products on pairs.  Against one group per row and no loop (above, kept for
-// wide rows) no last wave is left part empty, and the parameters
-// are read once a block instead of once a row, by all its threads: bf16,
-// H = 768, T = 16384 21 -> 18 us, T = 1 3.6 -> 2.2 us.  Unaligned rows have
+// products on pairs.  Against one group per row and no loop (above) no last
+// wave is left part empty, and the parameters are read once a block instead of
+// once a row, by all its threads: bf16, H = 768, T = 16384 21 -> 18 us, T = 1
+// 3.6 -> 2.2 us; fp32 with a token gate 48 -> 40 and 4.5 -> 2.4 us; fp32, H =
+// 6144, T = 608 21.7 -> 14.3 us.  Unaligned rows have
 // the next row in registers; the parameters re-read in single elements were
 // what cost them most (T = 16384, H = 461 with a token gate: 57 -> 20 us).
 template <typename T, int V, int NU, bool kTokenGate>
@@ -899,53 +902,61 @@ static cudaError_t bn_fwd_launch(const BlockNormFwd& a, int tpr, cudaStream_t st
 // sums: there one block per row leaves several on an SM (bf16, 30 M elements:
 // H = 5120, two groups, 44 us against 50; H = 8192, one group, 50 against 44).
 // cudaErrorNotSupported: not here.
-template <typename T, int V> struct BnFwdUnits {
+// A thread takes up to 24 elements of an aligned row (16 of fp32 with a token
+// gate, whose three inputs of 24 never fit), or 16 / 8 of an unaligned one.
+template <typename T, int V, bool kTokenGate> struct BnFwdUnits {
   static constexpr int kWidth = V == 1 ? 2 : V;           // elements of a unit
-  static constexpr int kMost = V > 1 ? 24 / V : sizeof(T) == 2 ? 8 : 4;
+  static constexpr int kMost = V == 1 ? 16 / static_cast<int>(sizeof(T)) : (sizeof(T) == 4 && kTokenGate ? 16 : 24) / V;
   static constexpr int kSome = V > 1 ? 16 / V : kMost / 2, kFew = V > 1 ? 8 / V : kMost / 4;
+  // dynamic shared memory of blocks of `groups` groups of tpr threads, NU units each
+  static size_t smem(int NU, int tpr, int groups) {
+    const size_t span = static_cast<size_t>(NU) * tpr * kWidth;
+    return 2 * sizeof(float) * span + (V > 1 ? 2 * (kTokenGate ? 3 : 2) * sizeof(T) * span * groups : 0);
+  }
 };
-template <typename T, int V, int NU>
+template <typename T, int V, int NU, bool kTokenGate>
 static cudaError_t bn_ring_launch(const BlockNormFwd& a, int tpr, cudaStream_t st) {
-  const bool token_gate = a.gate != nullptr && a.gate_per_token;
-  const int span = NU * tpr * BnFwdUnits<T, V>::kWidth, groups = kBnFwdThreads / tpr;
-  const size_t ring = V > 1 ? 2 * (token_gate ? 3 : 2) * sizeof(T) * span * groups : 0;
-  const size_t smem = 2 * sizeof(float) * span + ring;
+  using N = BnFwdUnits<T, V, kTokenGate>;
+  const int span = NU * tpr * N::kWidth, groups = kBnFwdThreads / tpr;
+  const size_t smem = N::smem(NU, tpr, groups);
   const int64_t sms = num_sms();
-  if (smem > kBnMostSmem || (V > 1 && groups == 1 && a.T > 4 * sms)) return cudaErrorNotSupported;
-  auto kern = token_gate ? block_norm_ring_kernel<T, V, NU, true> : block_norm_ring_kernel<T, V, NU, false>;
+  auto kern = block_norm_ring_kernel<T, V, NU, kTokenGate>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   // Three waves of blocks where an SM's share is above 2 MB, else one: the SMs
   // do not run at one pace, so an even share waits for the slowest, but each
   // block starts with a load it has nothing to run under (1 / 3 waves, us:
   // 268 MB 46.6 / 50.5, 403 MB 68.1 / 63.2, 671 MB 108 / 100).
-  const int64_t share = a.T * a.H * static_cast<int64_t>(sizeof(T)) * (2 + token_gate + 1 + (a.pre_w != nullptr)) / sms;
+  const int64_t share = a.T * a.H * static_cast<int64_t>(sizeof(T)) * (2 + kTokenGate + 1 + (a.pre_w != nullptr)) / sms;
   const int64_t most = share > (2 << 20) ? 3 * sms : sms;
   return launch_dependent_kernel(kern, dim3(static_cast<unsigned>(a.T < most ? a.T : most)), dim3(groups * tpr), smem,
                                  st, a, tpr, span);
 }
-template <typename T, int V>
+template <typename T, int V, bool kTokenGate>
 static cudaError_t bn_ring_pick(const BlockNormFwd& a, cudaStream_t st) {
-  using N = BnFwdUnits<T, V>;
+  using N = BnFwdUnits<T, V, kTokenGate>;
   int best = 0, busy = 0, tpr = 0;
-  for (int NU : {N::kSome, N::kMost, N::kFew}) {          // the most threads with columns
+  for (int NU : {N::kSome, N::kMost, N::kFew}) {          // the most threads with columns, of what fits
     const int lanes = (a.H + NU * N::kWidth - 1) / (NU * N::kWidth), t = (lanes + 31) / 32 * 32;
-    const int b = t > kBnFwdThreads ? 0 : kBnFwdThreads / t * lanes;
+    if (t > kBnFwdThreads || N::smem(NU, t, kBnFwdThreads / t) > kBnMostSmem) continue;
+    const int b = kBnFwdThreads / t * lanes;
     if (b > busy) {
       busy = b;
       best = NU;
       tpr = t;
     }
   }
-  if (best == 0) return cudaErrorNotSupported;
-  if (best == N::kMost) return bn_ring_launch<T, V, N::kMost>(a, tpr, st);
-  if (best == N::kSome) return bn_ring_launch<T, V, N::kSome>(a, tpr, st);
-  return bn_ring_launch<T, V, N::kFew>(a, tpr, st);
+  if (best == 0 || (V > 1 && kBnFwdThreads / tpr == 1 && a.T > 4 * static_cast<int64_t>(num_sms())))
+    return cudaErrorNotSupported;
+  if (best == N::kMost) return bn_ring_launch<T, V, N::kMost, kTokenGate>(a, tpr, st);
+  if (best == N::kSome) return bn_ring_launch<T, V, N::kSome, kTokenGate>(a, tpr, st);
+  return bn_ring_launch<T, V, N::kFew, kTokenGate>(a, tpr, st);
 }
 
 template <typename T, int V>
 static cudaError_t bn_fwd_pick(const BlockNormFwd& a, cudaStream_t st) {
-  const cudaError_t ring = bn_ring_pick<T, V>(a, st);
+  const bool token_gate = a.gate != nullptr && a.gate_per_token;
+  const cudaError_t ring = token_gate ? bn_ring_pick<T, V, true>(a, st) : bn_ring_pick<T, V, false>(a, st);
   if (ring != cudaErrorNotSupported) return ring;
   // 32 or 24 elements a thread, whichever leaves fewer idle
   const int nv = a.H / V;

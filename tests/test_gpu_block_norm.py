@@ -291,3 +291,17 @@ def test_refusals():
     r, n, stats = forward(d)
     with pytest.raises(mm._lib.MMError):
         backward(d, r, stats, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+# widths on both sides of what the looping kernel holds in shared memory, where
+# the element count a thread is the widest, the next or the narrowest that fits
+@pytest.mark.parametrize("dtype,gate,H", [
+    (F32, "token", 640), (F32, "token", 2304), (F32, "token", 5120), (F32, "token", 7168), (F32, "token", 7172),
+    (F32, "channel", 5380), (F32, "channel", 6144), (F32, "channel", 9216), (F32, "channel", 9220),
+    (BF, "token", 10752), (BF, "token", 10760), (BF, "channel", 12288), (BF, "channel", 12296), (BF, "channel", 8193), (F32, "channel", 4097)])
+@pytest.mark.parametrize("T", [1, 610])
+def test_widths_at_the_border_of_shared_memory(T, H, gate, dtype):
+    d = make(T, H, dtype, gate=gate)
+    r, n, stats = forward(d, s=0.9)
+    check_forward(d, r, n, stats, s=0.9)
+    check_backward(d, r, stats, backward(d, r, stats, s=0.9), s=0.9)
