@@ -408,7 +408,9 @@ int mm_block_norm(const void* x, const void* f, const void* post_w, const void* 
  * dn, r, rstd_pre, d_pre_w go with pre_w; rstd_post, d_post_w with post_w; f
  * is needed with post_w or gate and not read without; df NULL: the plain norm
  * (f NULL above).  The fp32 sums need 4-byte alignment only.  Every gradient
- * is overwritten; no output may overlap an input.  T = 0 zeroes the sums. */
+ * is overwritten; no output may overlap an input.  T = 0 zeroes the sums.
+ * Without pre_w, post_w and a channel gate there are no sums, and no workspace
+ * is needed whatever its size. */
 size_t mm_block_norm_backward_workspace_bytes(int64_t T, int H, int dtype);
 
 int mm_block_norm_backward(const void* dn, const void* dr, const void* r, const void* f,

@@ -174,8 +174,9 @@ def block_norm_backward(dn: Optional[torch.Tensor], dr: Optional[torch.Tensor],
         pdn, pr = _arg(dn, "dn", dev, dtype, shape), _arg(r, "r", dev, dtype, shape)
     pdr, pf = _arg(dr, "dr", dev, dtype, shape), _arg(f, "f", dev, dtype, shape)
     lib = L.load()
-    pws, nbytes, keep = _scratch(workspace, lib.mm_block_norm_backward_workspace_bytes(T, H, dt), dev, stream,
-                                 "block_norm_backward")
+    sums = post is not None or pre is not None or (g is not None and not per_token)
+    need = lib.mm_block_norm_backward_workspace_bytes(T, H, dt) if sums else 0
+    pws, nbytes, keep = _scratch(workspace, need, dev, stream, "block_norm_backward")
     out = {"dx": _empty(shape, dtype, dev, stream)}
     pdf = pdpost = pdgate = pdpre = None
     if f is not None:

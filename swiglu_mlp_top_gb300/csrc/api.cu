@@ -997,7 +997,8 @@ int mm_block_norm_backward(const void* dn, const void* dr, const void* r, const 
     if (!aligned16(q)) return MM_ERR_INVALID_ARG;
   if (!aligned4(d_gate) || !aligned4(d_post_w) || !aligned4(d_pre_w)) return MM_ERR_INVALID_ARG;
   if (!aligned4(rstd_post) || !aligned4(rstd_pre)) return MM_ERR_INVALID_ARG;
-  const size_t need = mm_block_norm_backward_workspace_bytes(T, H, dtype);
+  const bool sums = pre_w || post_w || (gate && !token_gate);
+  const size_t need = sums ? mm_block_norm_backward_workspace_bytes(T, H, dtype) : 0;
   if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return MM_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!post_w && !gate) f = nullptr;          // nothing depends on it: df = D
@@ -1008,7 +1009,7 @@ int mm_block_norm_backward(const void* dn, const void* dr, const void* r, const 
     e = counted_launch(MM_KERNEL_NORM, st, [&] { return launch_block_norm_bwd_rows(dtype, a, st); });
     if (e != cudaSuccess) return cuda_fail(e, "block norm backward");
   }
-  if ((pre_w || post_w || (gate && !token_gate)) && !block_norm_bwd_one_block(T, H, dtype)) {
+  if (sums && !block_norm_bwd_one_block(T, H, dtype)) {
     e = counted_launch(MM_KERNEL_NORM, st, [&] { return launch_block_norm_bwd_cols(dtype, a, st); });
     if (e != cudaSuccess) return cuda_fail(e, "block norm backward sums");
   }

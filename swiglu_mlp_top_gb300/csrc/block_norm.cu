@@ -629,6 +629,7 @@ block_norm_bwd_kernel(const BlockNormBwd a, int tpr, int span, int stages) {
   }
   // the block's column sums: each group's side by side, then added in order
   if constexpr (U::kAsync) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (gridDim.x > 1 && a.partial == nullptr) return;                          // none asked for
   __syncthreads();
   float* mine = behind + group * kBnSums * span;
 #pragma unroll
@@ -782,6 +783,7 @@ __global__ void __launch_bounds__(kBnFwdThreads, 1) block_norm_bwd_wide_kernel(c
       }
     }
   }
+  if (gridDim.x > 1 && a.partial == nullptr) return;          // no sums asked for
   float* part = a.partial + static_cast<int64_t>(blockIdx.x) * kBnSums * a.H;
   for (int c = threadIdx.x; c < nv; c += kBnFwdThreads)
 #pragma unroll

@@ -395,7 +395,7 @@ struct BlockNormBwd {
   float* d_post_w;
   void* d_gate;               // fp32 [H], or x's dtype [T, H] with gate_per_token
   float* d_pre_w;
-  float* partial;             // workspace, block_norm_bwd_bytes()
+  float* partial;             // workspace, block_norm_bwd_bytes(); null: no column sums, or one block
   int64_t T;
   int H;
   int gate_per_token;

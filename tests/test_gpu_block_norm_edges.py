@@ -56,3 +56,20 @@ def test_f_is_not_needed_without_a_post_norm_and_a_gate(H, pre):
         torch.cuda.current_stream().cuda_stream) == mm._lib.MM_OK
     assert torch.equal(dx, want["dx"]) and torch.equal(df, want["df"])
     assert not pre or torch.equal(dw, want["d_pre_weight"])
+
+
+@pytest.mark.parametrize("T,H", [(5000, 768), (5000, 1001), (200, 16384), (3, 768)])
+@pytest.mark.parametrize("gate", [None, "token"])
+def test_no_sums_need_no_workspace(T, H, gate):
+    lib = mm._lib.load()
+    gen = torch.Generator().manual_seed(H)
+    rand = lambda *shape: torch.randn(*shape, generator=gen).to(BF).cuda()  # noqa: E731
+    f, dr, g = rand(T, H), rand(T, H), rand(T, H) if gate else None
+    dx, df, dg = torch.empty_like(f), torch.empty_like(f), torch.empty_like(f)
+    assert lib.mm_block_norm_backward(
+        None, dr.data_ptr(), None, f.data_ptr(), None, g.data_ptr() if gate else None, 1, None, None, None, 0.5, T, H,
+        mm._lib.MM_DTYPE_BF16, dx.data_ptr(), df.data_ptr(), None, dg.data_ptr() if gate else None, None, None, 0,
+        torch.cuda.current_stream().cuda_stream) == mm._lib.MM_OK
+    assert torch.equal(dx, dr / 2)
+    assert torch.equal(df, (dr.float() * g.float()).to(BF) if gate else dr)
+    assert not gate or torch.equal(dg, (dr.float() * f.float()).to(BF))
