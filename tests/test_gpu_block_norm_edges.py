@@ -73,3 +73,51 @@ def test_no_sums_need_no_workspace(T, H, gate):
     assert torch.equal(dx, dr / 2)
     assert torch.equal(df, (dr.float() * g.float()).to(BF) if gate else dr)
     assert not gate or torch.equal(dg, (dr.float() * f.float()).to(BF))
+
+
+# ------------------------------------------------- every row counts, exactly
+def whole_numbers(T, H, dtype):
+    """[T, H] of a row's number (1 .. 5) times a column's (1 or 2), and their
+    sums over the rows: whole numbers below 2^24, which fp32 adds without a
+    rounding in any order."""
+    rows = (torch.arange(T, device="cuda") * 7 // 3 % 5 + 1)[:, None]
+    cols = torch.arange(H, device="cuda")[None] % 2 + 1
+    total = rows.sum() * cols[0]
+    assert int(total.max()) < 2 ** 24
+    return (rows * cols).to(dtype), total.float()
+
+
+def check_sums(T, H, dtype):
+    v, total = whole_numbers(T, H, dtype)
+    one, w = torch.ones(T, H, dtype=dtype, device="cuda"), torch.ones(H, dtype=dtype, device="cuda")
+    stats = {k: torch.ones(T, device="cuda") for k in ("rstd_post", "rstd_pre")}
+    # d_pre_weight = sum dn r rho_r of dn = v, r = rho_r = 1, and of dn = 1, r = v
+    for dn, r in ((v, one), (one, v)):
+        got = mm.block_norm_backward(dn, None, r, None, stats, pre_weight=w)
+        assert torch.equal(got["d_pre_weight"], total)
+    # D = dr without a norm behind r: d_post_weight = sum g D f rho_f and d_gate
+    # = sum D p, of D = v and f = p = 1; twice and half of it by the other factor
+    got = mm.block_norm_backward(None, v, None, one, stats, post_weight=2 * w, gate=w / 2)
+    assert torch.equal(got["d_post_weight"], total / 2) and torch.equal(got["d_gate"], 2 * total)
+    got = mm.block_norm_backward(None, one, None, v, stats, gate=w)
+    assert torch.equal(got["d_gate"], total)
+    got = mm.block_norm_backward(None, v, None, one, stats, post_weight=w, gate=one)
+    assert torch.equal(got["d_post_weight"], total)
+
+
+@pytest.mark.parametrize("dtype,H", [(BF, 8), (BF, 96), (BF, 256), (BF, 768), (BF, 2048), (BF, 4104), (BF, 12288), (BF, 16384), (BF, 33),
+                                     (BF, 1001), (BF, 4095), (BF, 5001), (F32, 64), (F32, 768), (F32, 8192), (F32, 8196), (F32, 1001)])
+@pytest.mark.parametrize("waves", [0, 1, 2, 5])
+@pytest.mark.parametrize("more", [-1, 0, 1])
+def test_column_sums_hold_every_row_once(H, dtype, waves, more):
+    """Token counts around one, whole rounds of the grid's groups of threads (1
+    to 16 a block, a block an SM at most), and the border to a single block."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for groups in (1, 2, 4, 5, 8, 16):
+        T = max(1, (groups if waves == 0 else sms * groups * waves) + more)
+        if T * H <= 2 ** 26:
+            check_sums(T, H, dtype)
+
+
+def test_column_sums_of_more_elements_than_32_bits_count():
+    check_sums(2 ** 21 + 41, 1024, BF)
