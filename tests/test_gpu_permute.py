@@ -219,3 +219,103 @@ def test_refusals():
         mm.moe_unpermute_backward(x, xs[:3], plan, w)
     with pytest.raises(ValueError):
         mm.moe_unpermute(xs.float(), plan, w, out=torch.zeros(4, 64, dtype=BF, device="cuda"))
+
+
+def on_a_stream_and_in_a_graph(T, H, E, k, align):
+    """The permute with a workspace, on another stream and captured; replays
+    follow changed indices and changed rows."""
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    need = mm.moe_permute_workspace_bytes(T, E, k)
+    assert need > 0
+    x = torch.randn(T, H, generator=gen, device="cuda").to(BF)
+    idx = torch.randint(0, E, (T, k), generator=gen, device="cuda", dtype=torch.int32)
+    w = torch.rand(T, k, generator=gen, device="cuda")
+    out = torch.zeros(mm.moe_permuted_rows(T, E, k, align), H, dtype=BF, device="cuda")
+    ws = mm.new_workspace(need)
+
+    def call(stream=None, out=None, ws=None):
+        xs, plan = mm.moe_permute(x, idx, E, align=align, out=out, workspace=ws, stream=stream)
+        return xs, mm.moe_unpermute(xs, plan, w, stream=stream), plan
+
+    def same(a, b):
+        return torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and all(torch.equal(a[2][key], b[2][key]) for key in a[2])
+
+    def right(got):
+        """Against the indices: every assignment in its expert's group, in order, and its row copied."""
+        xs, _, plan = got
+        pos, flat = plan["pos"].view(-1).long(), idx.view(-1).long()
+        group, order = plan["offsets"].long()[flat], torch.argsort(flat, stable=True)
+        first = torch.cumsum(torch.bincount(flat, minlength=E), 0) - torch.bincount(flat, minlength=E)
+        rank = torch.empty_like(order)
+        rank[order] = torch.arange(T * k, device="cuda") - first[flat[order]]
+        assert torch.equal(pos, group + rank) and torch.equal(plan["counts"].long(), torch.bincount(flat, minlength=E))
+        for s in range(k):                              # slot by slot: a copy of all rows at once would be as large again
+            assert torch.equal(xs[pos.view(T, k)[:, s]], x)
+
+    here = call(out=out.clone())
+    right(here)
+    side, o2 = torch.cuda.Stream(), out.clone()
+    torch.cuda.synchronize()
+    there = call(side, o2, ws)
+    side.synchronize()
+    assert same(here, there)
+    del there, o2
+    graph, o3 = torch.cuda.CUDAGraph(), out.clone()
+    with torch.cuda.graph(graph):
+        captured = call(out=o3, ws=ws)
+    for turn in range(3):
+        idx.copy_((idx * 5 + turn) % E)
+        x.neg_()
+        o3.zero_()
+        ws[256:].random_(0, 255, generator=gen)         # nothing is taken over from the last replay
+        graph.replay()
+        torch.cuda.synchronize()
+        right(captured)
+        assert same(captured, call(out=out.clone()))
+
+
+# with the counting kernel, and with the rows copied by a kernel of their own
+# (from 256 MB on)
+@pytest.mark.parametrize("T,H,E,k,align", [(3000, 768, 8, 2, 64), (2049, 40, 64, 2, 1), (70001, 8, 5, 8, 16), (16385, 4096, 8, 2, 16)])
+def test_workspace_on_a_side_stream_and_in_a_graph(T, H, E, k, align):
+    on_a_stream_and_in_a_graph(T, H, E, k, align)
+
+
+def test_calls_of_different_sizes_share_a_workspace():
+    """Large, small, large on one stream, one workspace, nothing between them;
+    and two captured graphs over it, replayed in any order."""
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    cases = []
+    for T, H, E, k in ((20000, 256, 64, 4), (2500, 768, 8, 2), (33000, 2048, 16, 2), (4099, 72, 3, 3)):
+        x = torch.randn(T, H, generator=gen, device="cuda").to(BF)
+        idx = torch.randint(-1, E + 1, (T, k), generator=gen, device="cuda", dtype=torch.int32)
+        cases.append((x, idx, E, torch.zeros(mm.moe_permuted_rows(T, E, k, 8), H, dtype=BF, device="cuda")))
+    sizes = [mm.moe_permute_workspace_bytes(x.shape[0], E, idx.shape[1]) for x, idx, E, _ in cases]
+    assert all(s > 0 for s in sizes) and sizes[0] > sizes[1]
+    ws = mm.new_workspace(max(sizes))
+
+    def run(c, ws):
+        x, idx, E, out = c
+        xs, plan = mm.moe_permute(x, idx, E, align=8, out=out, workspace=ws)
+        return [xs, *(plan[key] for key in sorted(plan))]
+
+    want = []
+    for c, size in zip(cases, sizes):
+        want.append([t.clone() for t in run(c, mm.new_workspace(size))])
+        c[3].zero_()
+    torch.cuda.synchronize()
+    got = [run(c, ws) for c in cases + cases[:2]]
+    torch.cuda.synchronize()
+    for a, b in zip(want + want[:2], got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    graphs, outs = [], []
+    for c in cases:
+        c[3].zero_()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(run(c, ws))
+    for i in (0, 1, 0, 2, 3, 1, 0, 2, 3):
+        graphs[i].replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, outs):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
