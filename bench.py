@@ -899,6 +899,84 @@ def run_stream_floor(args):
                       "peak_source": src}), flush=True)
 
 
+#: Forms of the operators around the experts' products that perf/operators.py
+#: does not list, timed beside its cases.
+BLOCK_OPS_MORE = [
+    dict(name="norm_bwd_t16384_h768_tokengate", op="norm_bwd", T=16384, H=768, dtype="bf16", post=True, pre=True, gate="token", s=1.0),
+    dict(name="norm_bwd_t16384_h768_plain", op="norm_bwd", T=16384, H=768, dtype="bf16", post=False, pre=True, gate=None, s=1.0),
+    dict(name="permute_bwd_t16384_e8k2", op="permute_bwd", T=16384, H=768, E=8, k=2, align=64, drop=0.0, dtype="bf16"),
+    dict(name="act_r32768_i2432_no_checkpoint", op="act", R=32768, I=2432, dtype="bf16", bare=True),
+    dict(name="act_save_r16000_i1001", op="act", R=16000, I=1001, dtype="bf16"),
+    dict(name="act_bwd_r16000_i1001", op="act_bwd", R=16000, I=1001, dtype="bf16"),
+    dict(name="checkpoint_r32768_c2432", op="checkpoint", R=32768, C=2432, dtype="bf16"),
+]
+
+
+def run_block_ops(args):
+    """The operators around the experts' products at the cases of
+    perf/operators.py and a few more, one JSON line each: `device_us`, a pass
+    in a replayed CUDA graph; `call_us`, a pass among others through the Python
+    call (bound by the host where it is above the device's); `plain_us`, the
+    elementary torch form; and the bytes that a pass cannot do without, at the
+    measured copy rate.  The inputs rotate over several sets (twice L2 or 16
+    sets, at least 3); medians of 7 regions."""
+    import swiglu_mlp_top_gb300 as mm
+    from perf import operators as ops
+    dev = torch.device("cuda", 0)
+    torch.cuda.set_device(dev)
+    peaks, src = measured_peaks()
+
+    def region_us(enqueue, passes):
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        times = []
+        for _ in range(7):
+            torch.cuda.synchronize()
+            e0.record()
+            enqueue()
+            e1.record()
+            torch.cuda.synchronize()
+            times.append(e0.elapsed_time(e1) / passes * 1e3)
+        return statistics.median(times)
+
+    for case in ops.listed() + BLOCK_OPS_MORE:
+        bare = case.get("bare", False)
+        # without a checkpoint: g, u and h, 2 bytes each
+        nbytes = case["R"] * case["I"] * 6 if bare else ops.work(case)["bytes"]
+        n_set = max(3, min(16, int(np.ceil(2.0 * L2_BYTES / nbytes))))
+        states = [ops.prepare(case, s) for s in range(n_set)]
+
+        def one(i, own):
+            ops.own = own
+            st = states[i % n_set]
+            return mm.swiglu_act(st["gu"], out=st["h"]) if own and bare else ops.run(st)
+
+        def loop(n, own):
+            for i in range(n):
+                one(i, own)
+
+        loop(max(args.warmup, n_set), True)
+        torch.cuda.synchronize()
+        passes = 4 * n_set
+        graph = torch.cuda.CUDAGraph()
+        with ClockSampler(0) as clk:
+            with torch.cuda.graph(graph):
+                loop(passes, True)
+            graph.replay()
+            device = region_us(graph.replay, passes)
+            call = region_us(lambda: loop(200, True), 200)
+            plain = None
+            if not bare:
+                loop(3, False)
+                plain = region_us(lambda: loop(6, False), 6)
+        ops.own = False
+        floor = nbytes / (peaks["hbm_gbs"] * 1e3)
+        print(json.dumps({"case": case["name"], "device_us": round(device, 2), "call_us": round(call, 2),
+                          "plain_us": None if plain is None else round(plain, 1), "bytes": int(nbytes),
+                          "floor_us": round(floor, 3), "frac_of_copy_rate": round(floor / device, 3),
+                          "input_sets": n_set, "peak_source": src, "clocks": clk.summary()}), flush=True)
+        del graph, states
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -919,6 +997,9 @@ def main():
                          "name such as backward:moe_e8k2_t16384_skew) for a profiler, and exit")
     ap.add_argument("--stream-floor", action="store_true",
                     help="measure the one-launch streaming floor at the decode rows' weight sizes")
+    ap.add_argument("--block-ops", action="store_true",
+                    help="time the operators around the experts' products (norms, token sort, "
+                         "8-bit checkpoints), one JSON line a case")
     args = ap.parse_args()
     if args.warmup < 3:
         args.warmup = 3
@@ -927,6 +1008,9 @@ def main():
         return
     if args.stream_floor:
         run_stream_floor(args)
+        return
+    if args.block_ops:
+        run_block_ops(args)
         return
     w = WORKLOADS[args.workload]
     if args.impl == "reference":
