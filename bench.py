@@ -69,8 +69,8 @@ WGRAD_TRAFFIC_BYTES = {"moe_e4k1_t8192": 146360320 + 49101312}
 DECODE_TRAFFIC_BYTES = {"decode_moe_e8k2_t64": 89892096 + 2775296,
                         "decode_moe_e8k2_t16": 89829888 + 2516736,
                         "decode_moe_e8k2_t4": 87931648 + 1900544,
-                        "decode_dense_t16": 11309056 + 0,
-                        "dense_t100": 11440128 + 0,
+                        "decode_dense_t16": 11280896 + 0,
+                        "dense_t100": 11411200 + 0,
                         "decode_dense_t1": 11309056 + 0}
 
 

@@ -483,7 +483,8 @@ int mm_checkpoint_unpack(const void* codes, const uint8_t* exps, int64_t R, int6
  * checkpoint: g and u packed as above, each half with its own groups (codes
  * [R, 2I], exps [R, 2 ceil(I/32)]).  n_rows (device int32, nullable): rows
  * from *n_rows on are left alone (the offsets[E] of a permute).  2I <=
- * MM_CHECKPOINT_MAX_COLS. */
+ * MM_CHECKPOINT_MAX_COLS.  Here and in the backward exp(-|g|) is good to
+ * 2^-20.5 relative for bf16 rows, and to fp32's expf for fp32 rows. */
 int mm_swiglu_act(const void* gu, int64_t R, int I, int dtype, const int32_t* n_rows, void* h,
                   void* codes, uint8_t* exps, void* stream);
 
