@@ -1,7 +1,10 @@
 """The order in which the kernels' sources wait for their predecessor and let
 their successor launch (programmatic dependent launch), read from the sources:
 a violation is a race that no run has to show.  Lexical order is execution
-order here: in every kernel both stand in straight-line code."""
+order: both stand in straight-line code, but for the grouped GEMM, where a
+later down slot triggers at once and its epilogue waits.  That slot's
+successor is the next slot, whose early loads were complete before the first
+one, or the next call's first kernel, which loads nothing early."""
 import os
 import re
 
