@@ -495,6 +495,78 @@ int mm_swiglu_act_backward(const void* codes, const uint8_t* exps, const void* d
                            int dtype, const int32_t* n_rows, void* dgu, void* h, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Experts' products   (the pages' expert loop of [L13] §3 step 5, for rows
+ * sorted by mm_moe_permute or any tables of its form)
+ *
+ * Group e is rows [offsets[e], offsets[e+1]) of the sorted tensors; its first
+ * counts[e] rows hold an assignment, the rest is padding.  offsets (int32
+ * [E+1], ascending) and counts (int32 [E]) are device memory; both NULL: all
+ * rows are one group (E = 1).  The tables may start at any row; entries
+ * outside [0, rows] are taken as the nearest inside.
+ * In results that have rows (ys, dxs) a group's padding rows become zeros and
+ * rows from offsets[E] on (and before offsets[0]) are left as they were; what
+ * stands in padding rows and behind in inputs (NaN too) has no effect.
+ * Sums in fp32 in a fixed order (deterministic), one rounding per element.
+ * Outputs overlap neither inputs nor each other.  `status_ws` (nullable: no
+ * report) is a zeroed workspace of >= 256 bytes read by mm_check_status(),
+ * where a device wait that exceeded its time limit is recorded; `workspace`
+ * is plain scratch (its header is not used), and may be NULL where the size
+ * is 0.
+ * Limits: E <= MM_MAX_EXPERTS; K, N <= MM_GROUPED_MAX_DIM; rows <=
+ * MM_GROUPED_MAX_ROWS.  rows = 0 enqueues nothing, but that dw is zeroed.
+ * ---------------------------------------------------------------------- */
+#define MM_GROUPED_MAX_DIM (1 << 20)
+#define MM_GROUPED_MAX_ROWS ((1 << 30) + (1 << 17))
+
+/* ys[r] = w[e] xs[r]:  xs [rows, K], w [E, N, K], ys [rows, N], all of dtype. */
+size_t mm_grouped_matmul_workspace_bytes(int64_t rows, int K, int N, int E, int dtype);
+
+int mm_grouped_matmul(const void* xs, const void* w, const int32_t* offsets, const int32_t* counts,
+                      int64_t rows, int K, int N, int E, int dtype, void* ys, void* workspace,
+                      size_t workspace_bytes, void* status_ws, void* stream);
+
+/* Its gradients for dys = dL/dys [rows, N]:
+ *   dxs[r] = w[e]^T dys[r]  [rows, K] in dtype       (nullable; needs w)
+ *   dw[e] = sum over the group's counts[e] rows of dys[r] xs[r]^T, fp32
+ *           [E, N, K], overwritten; zeros for an empty group (nullable; needs xs) */
+size_t mm_grouped_matmul_backward_workspace_bytes(int64_t rows, int K, int N, int E, int dtype);
+
+int mm_grouped_matmul_backward(const void* dys, const void* xs, const void* w,
+                               const int32_t* offsets, const int32_t* counts, int64_t rows, int K,
+                               int N, int E, int dtype, void* dxs, float* dw, void* workspace,
+                               size_t workspace_bytes, void* status_ws, void* stream);
+
+/* Microscaled 4-bit floating point (OCP MX: e2m1 elements, a power of two per
+ * 32 columns).  With amax over a group's magnitudes, e is the least integer
+ * >= -126 with amax <= 6 * 2^e, and
+ *   codes [R, 16 G]     G = ceil(C/32): e2m1 of x * 2^-e, to nearest, ties to
+ *                       the even code, two to a byte (the even column in the
+ *                       low half); the last group is filled up with zeros
+ *   exps  [ceil(G/4), R, 4]  e + 127 of four neighbouring groups of a row next
+ *                       to each other; 127 where there is no group
+ * so that a value of a group is off by at most a quarter of itself or, below
+ * 2^e, by 2^-2 * 2^e.  A group that holds an infinity or a NaN gets the byte
+ * 255 and stands for NaN in all its columns.
+ * Dequantising multiplies back: exact in fp32 and bf16, but for |x| above
+ * 1.25 * 2^127, whose code can stand for 2^128: an infinity there.
+ * Matrices of E experts are quantised as E * N rows.  n_rows (device int32,
+ * nullable): rows from *n_rows on are left alone.
+ * Limits: C <= MM_GROUPED_MAX_DIM, R <= 2^31 - 1.  R = 0 enqueues nothing. */
+int mm_mx4_quantize(const void* x, int64_t R, int64_t C, int dtype, const int32_t* n_rows,
+                    void* codes, uint8_t* exps, void* stream);
+int mm_mx4_dequantize(const void* codes, const uint8_t* exps, int64_t R, int64_t C, int dtype,
+                      const int32_t* n_rows, void* x, void* stream);
+
+/* mm_grouped_matmul with w in 4 bits (codes [E * N, 16 G], exps), for xs in
+ * 4 bits (x: codes, x_exps) or in bf16 (x_exps NULL); ys is bf16:
+ *   ys[r, n] = sum_k v(xs[r, k]) v(w[e, n, k]),  v() the values stood for. */
+size_t mm_mx4_matmul_workspace_bytes(int64_t rows, int K, int N, int E, int x_in_4_bits);
+
+int mm_mx4_matmul(const void* x, const uint8_t* x_exps, const void* w_codes, const uint8_t* w_exps,
+                  const int32_t* offsets, const int32_t* counts, int64_t rows, int K, int N, int E,
+                  void* ys, void* workspace, size_t workspace_bytes, void* status_ws, void* stream);
+
+/* ------------------------------------------------------------------------
  * Status
  * ---------------------------------------------------------------------- */
 /* Synchronises `stream`, reads and clears the device status word kept at
@@ -527,7 +599,9 @@ typedef enum {
   MM_KERNEL_BWD_ROUTER = 11, /* backward: dispatch, router gradient, dx combine */
   MM_KERNEL_NORM = 12,      /* block norm, forward and backward             */
   MM_KERNEL_PERMUTE = 13,   /* tokens sorted by expert and back             */
-  MM_KERNEL_CHECKPOINT = 14 /* 8-bit checkpoints and the SwiGLU activation  */
+  MM_KERNEL_CHECKPOINT = 14, /* 8-bit checkpoints and the SwiGLU activation */
+  MM_KERNEL_GROUPED = 15,   /* experts' products, forward and backward      */
+  MM_KERNEL_MX4 = 16        /* 4-bit microscaled quantisation               */
 } mm_kernel_id;
 
 /* Number of kernels this library has enqueued since it was loaded. */

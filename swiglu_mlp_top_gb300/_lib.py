@@ -23,6 +23,8 @@ MM_PERMUTE_MAX_ALIGN = 1024
 MM_PERMUTE_MAX_H = 1 << 24
 MM_CHECKPOINT_MAX_COLS = 1 << 20
 MM_CHECKPOINT_GROUP = 32
+MM_GROUPED_MAX_DIM = 1 << 20
+MM_GROUPED_MAX_ROWS = (1 << 30) + (1 << 17)
 
 _vp, _i32, _i64, _f32, _sz = C.c_void_p, C.c_int, C.c_int64, C.c_float, C.c_size_t
 _pp = C.POINTER(C.c_void_p)
@@ -91,6 +93,17 @@ SIGNATURES = {
     "mm_checkpoint_unpack": (_i32, [_vp, _vp, _i64, _i64, _i32, _vp, _vp]),
     "mm_swiglu_act": (_i32, [_vp, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp]),
     "mm_swiglu_act_backward": (_i32, [_vp, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _vp]),
+    "mm_grouped_matmul_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32, _i32]),
+    "mm_grouped_matmul": (_i32, [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _vp, _vp, _sz,
+                                 _vp, _vp]),
+    "mm_grouped_matmul_backward_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32, _i32]),
+    "mm_grouped_matmul_backward": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32,
+                                          _vp, _vp, _vp, _sz, _vp, _vp]),
+    "mm_mx4_quantize": (_i32, [_vp, _i64, _i64, _i32, _vp, _vp, _vp, _vp]),
+    "mm_mx4_dequantize": (_i32, [_vp, _vp, _i64, _i64, _i32, _vp, _vp, _vp]),
+    "mm_mx4_matmul_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32, _i32]),
+    "mm_mx4_matmul": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _sz,
+                             _vp, _vp]),
     "mm_check_status": (_i32, [_vp, _vp]),
     "mm_watchdog_selftest": (_i32, [_vp, _sz, C.c_uint32, _vp]),
     "mm_launch_count": (C.c_uint64, []),
@@ -99,7 +112,7 @@ SIGNATURES = {
 }
 MM_KERNEL_ROUTER, MM_KERNEL_DISPATCH, MM_KERNEL_GATEUP, MM_KERNEL_DOWN, MM_KERNEL_DECODE = 1, 3, 4, 5, 7
 MM_KERNEL_BWD_DGRAD, MM_KERNEL_BWD_SWIGLU, MM_KERNEL_BWD_WGRAD, MM_KERNEL_BWD_ROUTER = 8, 9, 10, 11
-MM_KERNEL_NORM, MM_KERNEL_PERMUTE, MM_KERNEL_CHECKPOINT = 12, 13, 14
+MM_KERNEL_NORM, MM_KERNEL_PERMUTE, MM_KERNEL_CHECKPOINT, MM_KERNEL_GROUPED, MM_KERNEL_MX4 = 12, 13, 14, 15, 16
 
 _lib = None
 

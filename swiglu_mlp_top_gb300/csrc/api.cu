@@ -1150,6 +1150,130 @@ int mm_swiglu_act_backward(const void* codes, const uint8_t* exps, const void* d
   return e == cudaSuccess ? MM_OK : cuda_fail(e, "swiglu act backward");
 }
 
+// ------------------------------------------------------- experts' products
+static bool grouped_args_ok(const int32_t* offsets, const int32_t* counts, int64_t rows, int K, int N, int E) {
+  if (rows < 0 || K < 1 || N < 1 || E < 1) return false;
+  if ((offsets != nullptr) != (counts != nullptr) || (offsets == nullptr && E != 1)) return false;
+  return aligned4(offsets) && aligned4(counts);
+}
+static bool grouped_in_limits(int64_t rows, int K, int N, int E) {
+  return E <= MM_MAX_EXPERTS && K <= MM_GROUPED_MAX_DIM && N <= MM_GROUPED_MAX_DIM && rows <= MM_GROUPED_MAX_ROWS;
+}
+static bool status_ok(const void* status_ws) { return aligned16(status_ws); }
+
+size_t mm_grouped_matmul_workspace_bytes(int64_t rows, int K, int N, int E, int dtype) {
+  (void)rows; (void)K; (void)N; (void)E; (void)dtype;
+  return 0;
+}
+
+int mm_grouped_matmul(const void* xs, const void* w, const int32_t* offsets, const int32_t* counts,
+                      int64_t rows, int K, int N, int E, int dtype, void* ys, void* workspace,
+                      size_t workspace_bytes, void* status_ws, void* stream) {
+  if (!valid_dtype(dtype) || !grouped_args_ok(offsets, counts, rows, K, N, E)) return MM_ERR_INVALID_ARG;
+  if (!grouped_in_limits(rows, K, N, E)) return MM_ERR_UNSUPPORTED;
+  if (!status_ok(status_ws)) return MM_ERR_INVALID_ARG;
+  if (rows == 0) return MM_OK;
+  if (!present16(xs) || !present16(w) || !present16(ys)) return MM_ERR_INVALID_ARG;
+  const size_t need = mm_grouped_matmul_workspace_bytes(rows, K, N, E, dtype);
+  if (need > 0 && (!present16(workspace) || workspace_bytes < need)) return MM_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const GroupedArgs a{xs, nullptr, w, ys, GroupTables{offsets, counts, rows, E}, K, N};
+  cudaError_t e = counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_grouped_simt(dtype, kGroupedForward, a, st); });
+  return e == cudaSuccess ? MM_OK : cuda_fail(e, "grouped matmul");
+}
+
+size_t mm_grouped_matmul_backward_workspace_bytes(int64_t rows, int K, int N, int E, int dtype) {
+  (void)rows; (void)K; (void)N; (void)E; (void)dtype;
+  return 0;
+}
+
+int mm_grouped_matmul_backward(const void* dys, const void* xs, const void* w,
+                               const int32_t* offsets, const int32_t* counts, int64_t rows, int K,
+                               int N, int E, int dtype, void* dxs, float* dw, void* workspace,
+                               size_t workspace_bytes, void* status_ws, void* stream) {
+  if (!valid_dtype(dtype) || !grouped_args_ok(offsets, counts, rows, K, N, E)) return MM_ERR_INVALID_ARG;
+  if (!grouped_in_limits(rows, K, N, E)) return MM_ERR_UNSUPPORTED;
+  if (!status_ok(status_ws) || !aligned16(dxs) || !aligned16(dw)) return MM_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {
+    if (dw == nullptr) return MM_OK;
+    cudaError_t e = cudaMemsetAsync(dw, 0, sizeof(float) * E * static_cast<size_t>(N) * K, st);
+    return e == cudaSuccess ? MM_OK : cuda_fail(e, "grouped matmul backward");
+  }
+  if (!present16(dys) || !aligned16(xs) || !aligned16(w) || (dxs == nullptr && dw == nullptr) ||
+      (dxs != nullptr && w == nullptr) || (dw != nullptr && xs == nullptr))
+    return MM_ERR_INVALID_ARG;
+  const size_t need = mm_grouped_matmul_backward_workspace_bytes(rows, K, N, E, dtype);
+  if (need > 0 && (!present16(workspace) || workspace_bytes < need)) return MM_ERR_WORKSPACE;
+  GroupedArgs a{xs, dys, w, dxs, GroupTables{offsets, counts, rows, E}, K, N};
+  cudaError_t e = cudaSuccess;
+  if (dxs != nullptr)
+    e = counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_grouped_simt(dtype, kGroupedDgrad, a, st); });
+  if (e == cudaSuccess && dw != nullptr) {
+    a.out = dw;
+    e = counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_grouped_simt(dtype, kGroupedWgrad, a, st); });
+  }
+  return e == cudaSuccess ? MM_OK : cuda_fail(e, "grouped matmul backward");
+}
+
+static int mx4_impl(bool quantise, const void* x, void* x_out, void* codes, uint8_t* exps, int64_t R,
+                    int64_t C, int dtype, const int32_t* n_rows, void* stream) {
+  if (!valid_dtype(dtype) || R < 0 || C < 1) return MM_ERR_INVALID_ARG;
+  if (C > MM_GROUPED_MAX_DIM || R > 0x7fffffff) return MM_ERR_UNSUPPORTED;
+  if (R == 0) return MM_OK;
+  if (!present16(quantise ? x : x_out) || !present16(codes) || !present16(exps) || !aligned4(n_rows))
+    return MM_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const Mx4Args a{x, x_out, static_cast<uint8_t*>(codes), exps, n_rows, R, static_cast<int>(C)};
+  cudaError_t e = counted_launch(MM_KERNEL_MX4, st, [&] { return launch_mx4(dtype, quantise, a, st); });
+  return e == cudaSuccess ? MM_OK : cuda_fail(e, quantise ? "mx4 quantize" : "mx4 dequantize");
+}
+
+int mm_mx4_quantize(const void* x, int64_t R, int64_t C, int dtype, const int32_t* n_rows,
+                    void* codes, uint8_t* exps, void* stream) {
+  return mx4_impl(true, x, nullptr, codes, exps, R, C, dtype, n_rows, stream);
+}
+
+int mm_mx4_dequantize(const void* codes, const uint8_t* exps, int64_t R, int64_t C, int dtype,
+                      const int32_t* n_rows, void* x, void* stream) {
+  return mx4_impl(false, nullptr, x, const_cast<void*>(codes), const_cast<uint8_t*>(exps), R, C, dtype,
+                  n_rows, stream);
+}
+
+size_t mm_mx4_matmul_workspace_bytes(int64_t rows, int K, int N, int E, int x_in_4_bits) {
+  if (rows < 1 || K < 1 || N < 1 || E < 1 || !grouped_in_limits(rows, K, N, E)) return 0;
+  return align_up(2 * static_cast<size_t>(E) * N * K) + (x_in_4_bits ? align_up(2 * static_cast<size_t>(rows) * K) : 0);
+}
+
+int mm_mx4_matmul(const void* x, const uint8_t* x_exps, const void* w_codes, const uint8_t* w_exps,
+                  const int32_t* offsets, const int32_t* counts, int64_t rows, int K, int N, int E,
+                  void* ys, void* workspace, size_t workspace_bytes, void* status_ws, void* stream) {
+  if (!grouped_args_ok(offsets, counts, rows, K, N, E)) return MM_ERR_INVALID_ARG;
+  if (!grouped_in_limits(rows, K, N, E) || static_cast<int64_t>(E) * N > 0x7fffffff) return MM_ERR_UNSUPPORTED;
+  if (!status_ok(status_ws)) return MM_ERR_INVALID_ARG;
+  if (rows == 0) return MM_OK;
+  if (!present16(x) || !aligned16(x_exps) || !present16(w_codes) || !present16(w_exps) || !present16(ys))
+    return MM_ERR_INVALID_ARG;
+  const size_t need = mm_mx4_matmul_workspace_bytes(rows, K, N, E, x_exps != nullptr);
+  if (need > 0 && (!present16(workspace) || workspace_bytes < need)) return MM_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  void* w16 = workspace;
+  const Mx4Args wa{nullptr, w16, static_cast<uint8_t*>(const_cast<void*>(w_codes)), const_cast<uint8_t*>(w_exps),
+                   nullptr, static_cast<int64_t>(E) * N, K};
+  cudaError_t e = counted_launch(MM_KERNEL_MX4, st, [&] { return launch_mx4(kDtypeBF16, false, wa, st); });
+  if (e == cudaSuccess && x_exps != nullptr) {
+    void* x16 = ws_at(workspace, align_up(2 * static_cast<size_t>(E) * N * K));
+    const Mx4Args xa{nullptr, x16, static_cast<uint8_t*>(const_cast<void*>(x)), const_cast<uint8_t*>(x_exps),
+                     nullptr, rows, K};
+    e = counted_launch(MM_KERNEL_MX4, st, [&] { return launch_mx4(kDtypeBF16, false, xa, st); });
+    x = x16;
+  }
+  if (e != cudaSuccess) return cuda_fail(e, "mx4 matmul");
+  const GroupedArgs a{x, nullptr, w16, ys, GroupTables{offsets, counts, rows, E}, K, N};
+  e = counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_grouped_simt(kDtypeBF16, kGroupedForward, a, st); });
+  return e == cudaSuccess ? MM_OK : cuda_fail(e, "mx4 matmul");
+}
+
 uint64_t mm_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }
 
 int mm_profile_start(int kernel_id, int max_launches) {
@@ -1157,7 +1281,8 @@ int mm_profile_start(int kernel_id, int max_launches) {
     case MM_KERNEL_ROUTER: case MM_KERNEL_DISPATCH: case MM_KERNEL_GATEUP: case MM_KERNEL_DOWN:
     case MM_KERNEL_DECODE: case MM_KERNEL_BWD_DGRAD: case MM_KERNEL_BWD_SWIGLU:
     case MM_KERNEL_BWD_WGRAD: case MM_KERNEL_BWD_ROUTER: case MM_KERNEL_NORM:
-    case MM_KERNEL_PERMUTE: case MM_KERNEL_CHECKPOINT: break;
+    case MM_KERNEL_PERMUTE: case MM_KERNEL_CHECKPOINT: case MM_KERNEL_GROUPED:
+    case MM_KERNEL_MX4: break;
     default: return MM_ERR_INVALID_ARG;
   }
   if (max_launches < 1 || max_launches > 100000) return MM_ERR_INVALID_ARG;

@@ -472,6 +472,36 @@ struct SwigluActArgs {
 cudaError_t launch_checkpoint(int dtype, bool pack, const CheckpointArgs& a, cudaStream_t st);
 cudaError_t launch_swiglu_act(int dtype, bool backward, const SwigluActArgs& a, cudaStream_t st);
 
+// Experts' products (grouped_simt.cu): rows grouped by the tables of a sort.
+struct GroupTables {
+  const int32_t* offsets;     // device [E + 1], or null: one group of all the rows (E = 1)
+  const int32_t* counts;      // device [E]
+  int64_t rows;               // rows of the sorted tensors
+  int E;
+};
+constexpr int kGroupedForward = 0, kGroupedDgrad = 1, kGroupedWgrad = 2;
+struct GroupedArgs {
+  const void* xs;             // [rows, K]
+  const void* dys;            // [rows, N]
+  const void* w;              // [E, N, K]
+  void* out;                  // forward: [rows, N]; dgrad: [rows, K]; wgrad: fp32 [E, N, K]
+  GroupTables g;
+  int K, N;
+};
+cudaError_t launch_grouped_simt(int dtype, int op, const GroupedArgs& p, cudaStream_t st);
+
+// 4-bit microscaled tensors (mx4.cu).
+struct Mx4Args {
+  const void* x;              // quantise: [R, C]
+  void* x_out;                // dequantise: [R, C]
+  uint8_t* codes;             // [R, 16 ceil(C / 32)]
+  uint8_t* exps;              // [ceil(C / 128), R, 4]
+  const int32_t* n_rows;      // device: rows from here on are left alone; null: R
+  int64_t R;
+  int C;
+};
+cudaError_t launch_mx4(int dtype, bool quantise, const Mx4Args& a, cudaStream_t st);
+
 // Workspace of the path that `path` (AUTO: the automatic choice) resolves to
 // for a dense call of this shape; 0 when that path does not take it.
 size_t dense_workspace_for_path(int64_t T, int H, int I, int dtype, int path);
