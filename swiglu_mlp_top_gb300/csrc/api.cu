@@ -1161,9 +1161,41 @@ static bool grouped_in_limits(int64_t rows, int K, int N, int E) {
 }
 static bool status_ok(const void* status_ws) { return aligned16(status_ws); }
 
+// Copies with rows that start on 16 bytes, for the bf16 operands whose rows do not.
+struct GroupedLayout {
+  size_t xs, dys, w, total;
+};
+static size_t repitched_bytes(int64_t rows, int cols) {
+  return cols % 8 ? align_up(2 * static_cast<size_t>(rows) * pitch8(cols)) : 0;
+}
+static GroupedLayout grouped_layout(int64_t rows, int K, int N, int E, int dtype, bool backward) {
+  GroupedLayout L{0, 0, 0, 0};
+  if (dtype != kDtypeBF16) return L;
+  L.dys = repitched_bytes(rows, K);
+  L.w = L.dys + (backward ? repitched_bytes(rows, N) : 0);
+  L.total = L.w + repitched_bytes(static_cast<int64_t>(E) * N, K);
+  return L;
+}
+static size_t grouped_bytes(int64_t rows, int K, int N, int E, int dtype, bool backward) {
+  if (!valid_dtype(dtype) || rows < 1 || K < 1 || N < 1 || E < 1 || !grouped_in_limits(rows, K, N, E)) return 0;
+  return grouped_layout(rows, K, N, E, dtype, backward).total;
+}
+// p, or its copy at `to`.
+static cudaError_t repitched(const void** p, char* to, int64_t rows, int cols, cudaStream_t st) {
+  if (cols % 8 == 0) return cudaSuccess;
+  const void* src = *p;
+  *p = to;
+  return counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_repitch(src, to, rows, cols, st); });
+}
+static cudaError_t grouped_launch(int dtype, int op, const GroupedArgs& a, void* status_ws, cudaStream_t st) {
+  return counted_launch(MM_KERNEL_GROUPED, st, [&] {
+    return dtype == kDtypeBF16 ? launch_grouped_tc(op, a, static_cast<WsHeader*>(status_ws), st)
+                               : launch_grouped_simt(dtype, op, a, st);
+  });
+}
+
 size_t mm_grouped_matmul_workspace_bytes(int64_t rows, int K, int N, int E, int dtype) {
-  (void)rows; (void)K; (void)N; (void)E; (void)dtype;
-  return 0;
+  return grouped_bytes(rows, K, N, E, dtype, false);
 }
 
 int mm_grouped_matmul(const void* xs, const void* w, const int32_t* offsets, const int32_t* counts,
@@ -1177,14 +1209,19 @@ int mm_grouped_matmul(const void* xs, const void* w, const int32_t* offsets, con
   const size_t need = mm_grouped_matmul_workspace_bytes(rows, K, N, E, dtype);
   if (need > 0 && (!present16(workspace) || workspace_bytes < need)) return MM_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const GroupedArgs a{xs, nullptr, w, ys, GroupTables{offsets, counts, rows, E}, K, N};
-  cudaError_t e = counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_grouped_simt(dtype, kGroupedForward, a, st); });
+  GroupedArgs a{xs, nullptr, w, ys, GroupTables{offsets, counts, rows, E}, K, N};
+  cudaError_t e = cudaSuccess;
+  if (need > 0) {
+    const GroupedLayout L = grouped_layout(rows, K, N, E, dtype, false);
+    e = repitched(&a.xs, ws_at(workspace, L.xs), rows, K, st);
+    if (e == cudaSuccess) e = repitched(&a.w, ws_at(workspace, L.w), static_cast<int64_t>(E) * N, K, st);
+  }
+  if (e == cudaSuccess) e = grouped_launch(dtype, kGroupedForward, a, status_ws, st);
   return e == cudaSuccess ? MM_OK : cuda_fail(e, "grouped matmul");
 }
 
 size_t mm_grouped_matmul_backward_workspace_bytes(int64_t rows, int K, int N, int E, int dtype) {
-  (void)rows; (void)K; (void)N; (void)E; (void)dtype;
-  return 0;
+  return grouped_bytes(rows, K, N, E, dtype, true);
 }
 
 int mm_grouped_matmul_backward(const void* dys, const void* xs, const void* w,
@@ -1207,11 +1244,17 @@ int mm_grouped_matmul_backward(const void* dys, const void* xs, const void* w,
   if (need > 0 && (!present16(workspace) || workspace_bytes < need)) return MM_ERR_WORKSPACE;
   GroupedArgs a{xs, dys, w, dxs, GroupTables{offsets, counts, rows, E}, K, N};
   cudaError_t e = cudaSuccess;
-  if (dxs != nullptr)
-    e = counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_grouped_simt(dtype, kGroupedDgrad, a, st); });
+  if (need > 0) {
+    const GroupedLayout L = grouped_layout(rows, K, N, E, dtype, true);
+    e = repitched(&a.dys, ws_at(workspace, L.dys), rows, N, st);
+    if (e == cudaSuccess && dxs != nullptr)
+      e = repitched(&a.w, ws_at(workspace, L.w), static_cast<int64_t>(E) * N, K, st);
+    if (e == cudaSuccess && dw != nullptr) e = repitched(&a.xs, ws_at(workspace, L.xs), rows, K, st);
+  }
+  if (e == cudaSuccess && dxs != nullptr) e = grouped_launch(dtype, kGroupedDgrad, a, status_ws, st);
   if (e == cudaSuccess && dw != nullptr) {
     a.out = dw;
-    e = counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_grouped_simt(dtype, kGroupedWgrad, a, st); });
+    e = grouped_launch(dtype, kGroupedWgrad, a, status_ws, st);
   }
   return e == cudaSuccess ? MM_OK : cuda_fail(e, "grouped matmul backward");
 }
@@ -1240,9 +1283,21 @@ int mm_mx4_dequantize(const void* codes, const uint8_t* exps, int64_t R, int64_t
                   n_rows, stream);
 }
 
+struct Mx4Layout {
+  size_t w, x, product, total;
+};
+static Mx4Layout mx4_layout(int64_t rows, int K, int N, int E, bool four) {
+  Mx4Layout L;
+  L.w = 0;
+  L.x = align_up(2 * static_cast<size_t>(E) * N * K);
+  L.product = L.x + (four ? align_up(2 * static_cast<size_t>(rows) * K) : 0);
+  L.total = L.product + grouped_bytes(rows, K, N, E, kDtypeBF16, false);
+  return L;
+}
+
 size_t mm_mx4_matmul_workspace_bytes(int64_t rows, int K, int N, int E, int x_in_4_bits) {
   if (rows < 1 || K < 1 || N < 1 || E < 1 || !grouped_in_limits(rows, K, N, E)) return 0;
-  return align_up(2 * static_cast<size_t>(E) * N * K) + (x_in_4_bits ? align_up(2 * static_cast<size_t>(rows) * K) : 0);
+  return mx4_layout(rows, K, N, E, x_in_4_bits != 0).total;
 }
 
 int mm_mx4_matmul(const void* x, const uint8_t* x_exps, const void* w_codes, const uint8_t* w_exps,
@@ -1254,24 +1309,18 @@ int mm_mx4_matmul(const void* x, const uint8_t* x_exps, const void* w_codes, con
   if (rows == 0) return MM_OK;
   if (!present16(x) || !aligned16(x_exps) || !present16(w_codes) || !present16(w_exps) || !present16(ys))
     return MM_ERR_INVALID_ARG;
-  const size_t need = mm_mx4_matmul_workspace_bytes(rows, K, N, E, x_exps != nullptr);
-  if (need > 0 && (!present16(workspace) || workspace_bytes < need)) return MM_ERR_WORKSPACE;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  void* w16 = workspace;
-  const Mx4Args wa{nullptr, w16, static_cast<uint8_t*>(const_cast<void*>(w_codes)), const_cast<uint8_t*>(w_exps),
-                   nullptr, static_cast<int64_t>(E) * N, K};
-  cudaError_t e = counted_launch(MM_KERNEL_MX4, st, [&] { return launch_mx4(kDtypeBF16, false, wa, st); });
-  if (e == cudaSuccess && x_exps != nullptr) {
-    void* x16 = ws_at(workspace, align_up(2 * static_cast<size_t>(E) * N * K));
-    const Mx4Args xa{nullptr, x16, static_cast<uint8_t*>(const_cast<void*>(x)), const_cast<uint8_t*>(x_exps),
-                     nullptr, rows, K};
-    e = counted_launch(MM_KERNEL_MX4, st, [&] { return launch_mx4(kDtypeBF16, false, xa, st); });
-    x = x16;
+  const Mx4Layout L = mx4_layout(rows, K, N, E, x_exps != nullptr);
+  if (!present16(workspace) || workspace_bytes < L.total) return MM_ERR_WORKSPACE;
+  int rc = mx4_impl(false, nullptr, ws_at(workspace, L.w), const_cast<void*>(w_codes), const_cast<uint8_t*>(w_exps),
+                    static_cast<int64_t>(E) * N, K, kDtypeBF16, nullptr, stream);
+  if (rc == MM_OK && x_exps != nullptr) {
+    rc = mx4_impl(false, nullptr, ws_at(workspace, L.x), const_cast<void*>(x), const_cast<uint8_t*>(x_exps), rows, K,
+                  kDtypeBF16, nullptr, stream);
+    x = ws_at(workspace, L.x);
   }
-  if (e != cudaSuccess) return cuda_fail(e, "mx4 matmul");
-  const GroupedArgs a{x, nullptr, w16, ys, GroupTables{offsets, counts, rows, E}, K, N};
-  e = counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_grouped_simt(kDtypeBF16, kGroupedForward, a, st); });
-  return e == cudaSuccess ? MM_OK : cuda_fail(e, "mx4 matmul");
+  if (rc != MM_OK) return rc;
+  return mm_grouped_matmul(x, ws_at(workspace, L.w), offsets, counts, rows, K, N, E, kDtypeBF16, ys,
+                           ws_at(workspace, L.product), L.total - L.product, status_ws, stream);
 }
 
 uint64_t mm_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }

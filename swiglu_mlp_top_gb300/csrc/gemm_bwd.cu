@@ -52,18 +52,6 @@ constexpr int kBwSmem = kBwStages * 2 * kBwTile + kBwEpiWarps * kBwStage + 1024 
 // with the static arrays (s_off, s_tstart, s_tmem, s_abort) within the 227 KiB of a block
 static_assert(kBwSmem + 8 * (kBwMaxGroups + 1) + kBwMaxGroups + 16 <= 232448, "shared memory budget");
 
-// UMMA descriptor of an MN-major 128 x 64 tile stored as two 64 x 64
-// 128-byte-swizzled TMA boxes (see the file comment).
-__device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);   // start address
-  d |= static_cast<uint64_t>(8192u >> 4) << 16;            // leading byte offset: next 64 along M/N
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;            // stride byte offset: next 8 K-rows
-  d |= static_cast<uint64_t>(1u) << 46;                    // descriptor version
-  d |= static_cast<uint64_t>(2u) << 61;                    // 128-byte swizzle
-  return d;
-}
-
 struct BwTile {
   int p, g, row0, rows, m0, n0, kb0, nkb;   // problem / group, rows or M block, N block, K range
 };

@@ -1043,6 +1043,22 @@ bool make_map_3d(CUtensorMap* out, const void* ptr, const uint64_t dims[3],
   return true;
 }
 
+bool make_map(CUtensorMap* out, CUtensorMapDataType type, int rank, uint64_t address, const uint64_t* dims,
+              const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swz) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (enc == nullptr || rank < 2 || rank > 4) return false;
+  cuuint64_t d[4], st[3];
+  cuuint32_t bx[4], one[4] = {1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    bx[i] = box[i];
+    if (i + 1 < rank) st[i] = strides[i];
+  }
+  return enc(out, type, static_cast<cuuint32_t>(rank), reinterpret_cast<void*>(address), d, st, bx, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int num_sms() {
   constexpr int kMaxDev = 64;
   static int cached[kMaxDev] = {};

@@ -197,7 +197,7 @@ static cudaError_t simt(int op, const GroupedArgs& p, cudaStream_t st) {
 }
 
 cudaError_t launch_grouped_simt(int dtype, int op, const GroupedArgs& p, cudaStream_t st) {
-  return dtype == kDtypeBF16 ? simt<__nv_bfloat16>(op, p, st) : simt<float>(op, p, st);
+  return dtype == kDtypeBF16 ? cudaErrorInvalidValue : simt<float>(op, p, st);
 }
 
 }  // namespace mm

@@ -490,6 +490,13 @@ struct GroupedArgs {
 };
 cudaError_t launch_grouped_simt(int dtype, int op, const GroupedArgs& p, cudaStream_t st);
 
+// The same on the tensor cores for bf16 (grouped_tc.cu).  Rows start on 16
+// bytes where a multiple of 8 elements makes a row; operands of other widths
+// come as copies with rows of pitch8() elements, zeros behind the row.
+constexpr int pitch8(int n) { return (n + 7) / 8 * 8; }
+cudaError_t launch_repitch(const void* src, void* dst, int64_t rows, int cols, cudaStream_t st);
+cudaError_t launch_grouped_tc(int op, const GroupedArgs& p, WsHeader* hdr, cudaStream_t st);
+
 // 4-bit microscaled tensors (mx4.cu).
 struct Mx4Args {
   const void* x;              // quantise: [R, C]
@@ -523,6 +530,11 @@ bool make_map_2d(CUtensorMap* out, const void* ptr, bool fp32, uint64_t inner, u
 bool make_map_3d(CUtensorMap* out, const void* ptr, const uint64_t dims[3],
                  const uint64_t strides[2], const uint32_t box[3], bool is_f16 = false,
                  CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B);
+
+// Tensor map of 2 to 4 dimensions (strides in bytes, from the second dimension
+// on), encoded anew; zero fill outside.
+bool make_map(CUtensorMap* out, CUtensorMapDataType type, int rank, uint64_t address, const uint64_t* dims,
+              const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swz);
 
 int num_sms();   // of the current device, looked up once per device
 

@@ -57,7 +57,7 @@ def check(counts, align, K, N, dtype, whole, start=0, tail=3):
     mark = torch.full((rows, K), 7.0, dtype=dtype)
     dx, dw = mm.grouped_matmul_backward(dyg, xg, wg, gplan, out=mark.cuda(), dw=torch.full(shape, 7.0, device="cuda"), status_workspace=status)
     (wdx, tdx), (wdw, tdw) = ref.matmul_backward(dy, x, w, plan, mark)
-    mm.check_status(status)
+    assert mm.check_status(status) == 0
     longest = max(counts) if counts else rows
     if whole:
         # every partial sum is a whole number below 2^24: fp32 holds it, and one rounding remains
@@ -256,7 +256,7 @@ def check_mx4(counts, align, K, N, four, whole, tail=3):
     status = mm.new_workspace(256)
     mark = torch.full((rows, N), 7.0, dtype=BF)
     y = mm.mx4_matmul(xg, wq, on_gpu(plan), out=mark.cuda(), status_workspace=status)
-    mm.check_status(status)
+    assert mm.check_status(status) == 0
     want, terms = ref.matmul(xv, wv, plan, mark)
     if whole:
         assert terms.max() < 2 ** 20
@@ -409,7 +409,7 @@ def test_two_graphs_share_a_workspace():
     for _ in range(3):
         for graph, _ in made:
             graph.replay()
-    mm.check_status(status)
+    assert mm.check_status(status) == 0
     for (_, outs), w in zip(made, want):
         for got, ref_ in zip(outs, w):
             assert torch.equal(got, ref_)
