@@ -1283,14 +1283,14 @@ int mm_mx4_dequantize(const void* codes, const uint8_t* exps, int64_t R, int64_t
                   n_rows, stream);
 }
 
+// bf16 rows: the weights as bf16, then mm_grouped_matmul.
 struct Mx4Layout {
-  size_t w, x, product, total;
+  size_t w, product, total;
 };
 static Mx4Layout mx4_layout(int64_t rows, int K, int N, int E, bool four) {
-  Mx4Layout L;
-  L.w = 0;
-  L.x = align_up(2 * static_cast<size_t>(E) * N * K);
-  L.product = L.x + (four ? align_up(2 * static_cast<size_t>(rows) * K) : 0);
+  Mx4Layout L{0, 0, 0};
+  if (four) return L;
+  L.product = align_up(2 * static_cast<size_t>(E) * N * K);
   L.total = L.product + grouped_bytes(rows, K, N, E, kDtypeBF16, false);
   return L;
 }
@@ -1310,14 +1310,15 @@ int mm_mx4_matmul(const void* x, const uint8_t* x_exps, const void* w_codes, con
   if (!present16(x) || !aligned16(x_exps) || !present16(w_codes) || !present16(w_exps) || !present16(ys))
     return MM_ERR_INVALID_ARG;
   const Mx4Layout L = mx4_layout(rows, K, N, E, x_exps != nullptr);
-  if (!present16(workspace) || workspace_bytes < L.total) return MM_ERR_WORKSPACE;
-  int rc = mx4_impl(false, nullptr, ws_at(workspace, L.w), const_cast<void*>(w_codes), const_cast<uint8_t*>(w_exps),
-                    static_cast<int64_t>(E) * N, K, kDtypeBF16, nullptr, stream);
-  if (rc == MM_OK && x_exps != nullptr) {
-    rc = mx4_impl(false, nullptr, ws_at(workspace, L.x), const_cast<void*>(x), const_cast<uint8_t*>(x_exps), rows, K,
-                  kDtypeBF16, nullptr, stream);
-    x = ws_at(workspace, L.x);
+  if (L.total > 0 && (!present16(workspace) || workspace_bytes < L.total)) return MM_ERR_WORKSPACE;
+  if (x_exps != nullptr) {
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const Mx4MatmulArgs a{x, x_exps, w_codes, w_exps, ys, GroupTables{offsets, counts, rows, E}, K, N};
+    cudaError_t e = counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_mx4_tc(a, static_cast<WsHeader*>(status_ws), st); });
+    return e == cudaSuccess ? MM_OK : cuda_fail(e, "mx4 matmul");
   }
+  const int rc = mx4_impl(false, nullptr, ws_at(workspace, L.w), const_cast<void*>(w_codes), const_cast<uint8_t*>(w_exps),
+                          static_cast<int64_t>(E) * N, K, kDtypeBF16, nullptr, stream);
   if (rc != MM_OK) return rc;
   return mm_grouped_matmul(x, ws_at(workspace, L.w), offsets, counts, rows, K, N, E, kDtypeBF16, ys,
                            ws_at(workspace, L.product), L.total - L.product, status_ws, stream);

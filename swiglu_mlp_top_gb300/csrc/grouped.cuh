@@ -1,6 +1,8 @@
 // Row groups of the experts' products, read from the device tables of a sort.
 #pragma once
 
+#include <algorithm>
+
 #include "mm_kernels.cuh"
 
 namespace mm {
@@ -65,6 +67,143 @@ __device__ __forceinline__ GroupTile find_group_tile(const GroupTables& g, int64
   r.s.r1 = __shfl_sync(0xffffffffu, second ? s[1].r1 : s[0].r1, src);
   r.s.n = __shfl_sync(0xffffffffu, second ? s[1].n : s[0].n, src);
   return r;
+}
+
+// Schedule of the tensor-core kernels: CTA pairs make tiles of 256 rows (of a
+// group, or of a weight gradient) x nt columns.
+struct GmTables {
+  int r0[MM_MAX_EXPERTS], r1[MM_MAX_EXPERTS], n[MM_MAX_EXPERTS], tstart[MM_MAX_EXPERTS + 1];
+  uint8_t order[MM_MAX_EXPERTS];   // wgrad: groups by descending rows
+};
+
+struct GmTile {
+  int e, m0, mrows, mvalid, n0, k0, krows;
+};
+
+// Reads the tables, one group a lane (two rounds); the tiles' prefix sums.
+template <int OP>
+__device__ __forceinline__ void gm_tables(const GroupTables& g, GmTables& s, int ntn) {
+  const int lane = threadIdx.x & 31, E = g.E;
+  for (int e = lane; e < E; e += 32) {
+    const GroupSpan sp = group_span(g, e);
+    s.r0[e] = sp.r0;
+    s.r1[e] = sp.r1;
+    s.n[e] = sp.n;
+  }
+  __syncwarp();
+  if constexpr (OP == kGroupedWgrad) {
+    for (int e = lane; e < E; e += 32) {
+      int pos = 0;
+      for (int o = 0; o < E; ++o) pos += (s.n[o] > s.n[e] || (s.n[o] == s.n[e] && o < e)) ? 1 : 0;
+      s.order[pos] = static_cast<uint8_t>(e);
+    }
+  } else {
+    int base = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = e0 + lane;
+      const int mine = e < E ? ((s.r1[e] - s.r0[e] + 255) / 256) * ntn : 0;
+      int inc = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      if (e < E) s.tstart[e] = base + inc - mine;
+      base += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) s.tstart[E] = base;
+  }
+}
+
+template <int OP>
+__device__ __forceinline__ GmTile gm_tile(int t, int E, int M, int K, const GmTables& s, int ntn, int nt, int rank) {
+  GmTile ti;
+  if constexpr (OP == kGroupedWgrad) {
+    const int per = ((M + 255) / 256) * ntn;
+    ti.e = s.order[t / per];
+    const int local = t % per;
+    ti.m0 = (local / ntn) * 256 + rank * 128;
+    ti.mrows = ti.mvalid = min(128, M - ti.m0);
+    ti.n0 = (local % ntn) * nt;
+    ti.k0 = s.r0[ti.e];
+    ti.krows = s.n[ti.e];
+  } else {
+    int lo = 0, hi = E - 1;              // last group with tstart <= t
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s.tstart[mid] <= t) lo = mid; else hi = mid - 1;
+    }
+    const int local = t - s.tstart[lo];
+    ti.e = lo;
+    ti.m0 = s.r0[lo] + (local / ntn) * 256 + rank * 128;
+    ti.mrows = s.r1[lo] - ti.m0;             // may be negative for the odd CTA
+    ti.mvalid = s.r0[lo] + s.n[lo] - ti.m0;
+    ti.n0 = (local % ntn) * nt;
+    ti.k0 = 0;
+    ti.krows = K;
+  }
+  return ti;
+}
+
+// The j-th tile of pair c of nc.  wgrad: rounds alternately forwards and
+// backwards over the groups in descending length, so that the pairs with a
+// round's longest tiles take the next one's shortest.
+template <int OP>
+__device__ __forceinline__ int gm_index(int j, int c, int nc) {
+  if constexpr (OP == kGroupedWgrad) return j * nc + ((j & 1) ? nc - 1 - c : c);
+  return j * nc + c;
+}
+
+// A warp's 32 rows x 64 columns of bf16 (a row a lane) out through its stage of
+// 128-byte rows (16-byte chunk q of row i at chunk q ^ (i & 7)); `rem` rows are
+// the group's.
+__device__ __forceinline__ void store_rows_bf16(const uint32_t (&pk)[32], uint8_t* wstage, const CUtensorMap* map,
+                                                void* outp, int aligned, int row, int col, int rem, int N, int lane) {
+  if (lane == 0) bulk_wait_read();                 // the previous piece's store has read the stage
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    *reinterpret_cast<uint4*>(wstage + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+        make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+  if (aligned && rem == 32) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(map, wstage, col, row);
+      bulk_commit();
+    }
+    return;
+  }
+  __syncwarp();
+  uint16_t* o = static_cast<uint16_t*>(outp) + static_cast<int64_t>(row) * N + col;
+  if (aligned) {
+    // a group's ragged end: 16 bytes a lane, four rows at once
+    if (col + 8 * (lane & 7) < N)
+      for (int i = lane >> 3; i < rem; i += 4)
+        *reinterpret_cast<uint4*>(o + static_cast<int64_t>(i) * N + 8 * (lane & 7)) =
+            *reinterpret_cast<const uint4*>(wstage + i * 128 + (((lane & 7) ^ (i & 7)) << 4));
+    return;
+  }
+  // rows that start anywhere: element by element
+  for (int i = 0; i < rem; ++i)
+#pragma unroll
+    for (int c = lane; c < 64; c += 32)
+      if (col + c < N)
+        o[static_cast<int64_t>(i) * N + c] =
+            *reinterpret_cast<const uint16_t*>(wstage + i * 128 + ((((c >> 3) ^ (i & 7)) << 4) | ((c & 7) << 1)));
+}
+
+// ---------------------------------------------------------------- host side
+// Result rows in bf16: store boxes of 64 x 32.
+inline bool map_out_rows(CUtensorMap* m, void* p, int cols, int64_t rows) {
+  const uint64_t d[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)}, s[1] = {static_cast<uint64_t>(cols) * 2};
+  const uint32_t b[2] = {64, 32};
+  return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, reinterpret_cast<uint64_t>(p), d, s, b,
+                  CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// Tiles of 256 rows that any grouping of the rows can need.
+inline int64_t row_tiles256(const GroupTables& g) {
+  return g.offsets ? std::min<int64_t>(g.rows, g.rows / 256 + g.E) : (g.rows + 255) / 256;
 }
 
 }  // namespace mm

@@ -11,8 +11,6 @@
 // Operands come in slices of 16 of the summed index, transposed into shared
 // memory where the index is contiguous; the next slice is in registers while
 // this one is multiplied.
-#include <algorithm>
-
 #include "grouped.cuh"
 #include "pack.cuh"
 

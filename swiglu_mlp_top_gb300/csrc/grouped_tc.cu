@@ -18,8 +18,6 @@
 // be NaN: the TMA brings a group's last slice to a barrier of its own CTA, the
 // producer warp writes zeros over the rows behind the group, in both operands,
 // and hands the slice on.
-#include <algorithm>
-
 #include "grouped.cuh"
 
 namespace mm {
@@ -32,6 +30,11 @@ constexpr int kGmWarpProducer = kGmEpiWarps, kGmWarpMma = kGmEpiWarps + 1;
 constexpr int kGmStage = 32 * 128;                    // epilogue: 32 rows x 128 bytes per warp
 constexpr int kGmSmem = kGmStages * 2 * kGmTile + kGmEpiWarps * kGmStage + 1024 + 256;
 
+// Slices of the summed index per accumulation in TMEM.  The tensor cores cut
+// off where they add to the accumulator; a weight gradient, kept in fp32 and
+// summed over thousands of rows, adds chunks of 512 rows in fp32 registers.
+template <int OP> constexpr int kGmChunk = OP == kGroupedWgrad ? 8 : 1 << 30;
+
 struct GmParams {
   CUtensorMap a, b, out;
   GroupTables g;
@@ -43,93 +46,8 @@ struct GmParams {
   void* outp;
 };
 
-struct GmTables {
-  int r0[MM_MAX_EXPERTS], r1[MM_MAX_EXPERTS], n[MM_MAX_EXPERTS], tstart[MM_MAX_EXPERTS + 1];
-  uint8_t order[MM_MAX_EXPERTS];   // wgrad: groups by descending rows
-};
-
 // with the static arrays within the 227 KiB of a block
 static_assert(kGmSmem + sizeof(GmTables) + 64 <= 232448, "shared memory budget");
-
-struct GmTile {
-  int e, m0, mrows, mvalid, n0, k0, krows, nkb;
-};
-
-// Reads the tables, one group a lane (two rounds); the tiles' prefix sums.
-template <int OP>
-__device__ __forceinline__ void gm_tables(const GmParams& P, GmTables& s, int ntn) {
-  const int lane = threadIdx.x & 31;
-  for (int e = lane; e < P.g.E; e += 32) {
-    const GroupSpan sp = group_span(P.g, e);
-    s.r0[e] = sp.r0;
-    s.r1[e] = sp.r1;
-    s.n[e] = sp.n;
-  }
-  __syncwarp();
-  if constexpr (OP == kGroupedWgrad) {
-    for (int e = lane; e < P.g.E; e += 32) {
-      int pos = 0;
-      for (int o = 0; o < P.g.E; ++o) pos += (s.n[o] > s.n[e] || (s.n[o] == s.n[e] && o < e)) ? 1 : 0;
-      s.order[pos] = static_cast<uint8_t>(e);
-    }
-  } else {
-    int base = 0;
-    for (int e0 = 0; e0 < P.g.E; e0 += 32) {
-      const int e = e0 + lane;
-      const int mine = e < P.g.E ? ((s.r1[e] - s.r0[e] + 255) / 256) * ntn : 0;
-      int inc = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-      }
-      if (e < P.g.E) s.tstart[e] = base + inc - mine;
-      base += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    if (lane == 0) s.tstart[P.g.E] = base;
-  }
-}
-
-template <int OP>
-__device__ __forceinline__ GmTile gm_tile(int t, const GmParams& P, const GmTables& s, int ntn, int rank) {
-  GmTile ti;
-  if constexpr (OP == kGroupedWgrad) {
-    const int per = ((P.M + 255) / 256) * ntn;
-    ti.e = s.order[t / per];
-    const int local = t % per;
-    ti.m0 = (local / ntn) * 256 + rank * 128;
-    ti.mrows = ti.mvalid = min(128, P.M - ti.m0);
-    ti.n0 = (local % ntn) * 256;
-    ti.k0 = s.r0[ti.e];
-    ti.krows = s.n[ti.e];
-    ti.nkb = (ti.krows + 63) / 64;
-  } else {
-    int lo = 0, hi = P.g.E - 1;              // last group with tstart <= t
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s.tstart[mid] <= t) lo = mid; else hi = mid - 1;
-    }
-    const int local = t - s.tstart[lo];
-    ti.e = lo;
-    ti.m0 = s.r0[lo] + (local / ntn) * 256 + rank * 128;
-    ti.mrows = s.r1[lo] - ti.m0;             // may be negative for the odd CTA
-    ti.mvalid = s.r0[lo] + s.n[lo] - ti.m0;
-    ti.n0 = (local % ntn) * 256;
-    ti.k0 = 0;
-    ti.krows = P.K;
-    ti.nkb = (P.K + 63) / 64;
-  }
-  return ti;
-}
-
-// The j-th tile of pair c of nc.  wgrad: rounds alternately forwards and
-// backwards over the groups in descending length, so that the pairs with a
-// round's longest tiles take the next one's shortest.
-template <int OP>
-__device__ __forceinline__ int gm_index(int j, int c, int nc) {
-  if constexpr (OP == kGroupedWgrad) return j * nc + ((j & 1) ? nc - 1 - c : c);
-  return j * nc + c;
-}
 
 template <int OP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGmThreads, 1)
@@ -173,7 +91,7 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
     // tables and operands may be the previous kernel's output
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    gm_tables<OP>(P, s_tab, ntn);
+    gm_tables<OP>(P.g, s_tab, ntn);
   }
   if (warp == kGmWarpMma) {
     tmem_alloc_cta2(&s_tmem, 512);
@@ -193,9 +111,10 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
     for (int j = 0; ok && j * nc < total; ++j) {
       const int tile = gm_index<OP>(j, cluster, nc);
       if (tile >= total) continue;               // the last round's missing tiles
-      const GmTile ti = gm_tile<OP>(tile, P, s_tab, ntn, rank);
+      const GmTile ti = gm_tile<OP>(tile, P.g.E, P.M, P.K, s_tab, ntn, 256, rank);
       const int ncol = ti.n0 + 128 * rank;       // this CTA's half of the columns
-      for (int kb = 0; kb < ti.nkb; ++kb, ++it) {
+      const int nkb = (ti.krows + 63) / 64;
+      for (int kb = 0; kb < nkb; ++kb, ++it) {
         const int s = it % kGmStages;
         const uint32_t ph = (it / kGmStages) & 1;
         ok = lane != 0 || mbar_wait(&empty[s], ph ^ 1, abort, hdr, 111);
@@ -289,15 +208,20 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
       for (int j = 0; ok && j * nc < total; ++j) {
         const int tile = gm_index<OP>(j, cluster, nc);
         if (tile >= total) continue;
-        const GmTile ti = gm_tile<OP>(tile, P, s_tab, ntn, 0);
-        if (ti.nkb == 0) continue;                 // the epilogue writes zeros for it
-        const int acc = used & 1;
-        const uint32_t aph = (used >> 1) & 1;
-        ++used;
-        if (!mbar_wait(&tempty[acc], aph ^ 1, abort, hdr, 113)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t d = tmem + acc * 256;
-        for (int kb = 0; kb < ti.nkb; ++kb, ++it) {
+        const GmTile ti = gm_tile<OP>(tile, P.g.E, P.M, P.K, s_tab, ntn, 256, 0);
+        const int nkb = (ti.krows + 63) / 64;      // 0: an empty group, zeros from the epilogue
+        uint32_t d = 0;
+        int acc = 0;
+        for (int kb = 0; kb < nkb; ++kb, ++it) {
+          const bool first = kb % kGmChunk<OP> == 0;
+          if (first) {
+            acc = used & 1;
+            const uint32_t aph = (used >> 1) & 1;
+            ++used;
+            if (!mbar_wait(&tempty[acc], aph ^ 1, abort, hdr, 113)) { ok = false; break; }
+            tc_fence_after();
+            d = tmem + acc * 256;
+          }
           const int s = it % kGmStages;
           const uint32_t ph = (it / kGmStages) & 1;
           if (!mbar_wait<OP == kGroupedWgrad>(&full[s], ph, abort, hdr, 114)) { ok = false; break; }
@@ -311,12 +235,11 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
             if (kk >= steps) break;
             const uint64_t ad = kAMn ? smem_desc_sw128_mn(a0 + kk * 2048) : smem_desc_sw128(a0 + kk * 32);
             const uint64_t bd = kBMn ? smem_desc_sw128_mn(b0 + kk * 2048) : smem_desc_sw128(b0 + kk * 32);
-            umma_f16_cta2(d, ad, bd, idesc, (kb | kk) ? 1u : 0u);
+            umma_f16_cta2(d, ad, bd, idesc, (!first || kk) ? 1u : 0u);
           }
           umma_commit_cta2_mc(&empty[s], 0x3);
+          if (kb + 1 == nkb || (kb + 1) % kGmChunk<OP> == 0) umma_commit_cta2_mc(&tfull[acc], 0x3);
         }
-        if (!ok) break;
-        umma_commit_cta2_mc(&tfull[acc], 0x3);
       }
       umma_commit_cta2_mc(drained, 0x1);
       mbar_wait(drained, 0, nullptr, hdr, 115);
@@ -328,88 +251,97 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
     uint8_t* wstage = sEpi + warp * kGmStage;
     const uint32_t te0 = mapa_shared(smem_u32(&tempty[0]), 0);
     const uint32_t te1 = mapa_shared(smem_u32(&tempty[1]), 0);
-    constexpr bool kF32 = OP == kGroupedWgrad;
-    constexpr int kPiece = kF32 ? 32 : 64;         // columns of a staged piece (128 bytes)
     int used = 0;
     for (int j = 0; j * nc < total; ++j) {
       const int tile = gm_index<OP>(j, cluster, nc);
       if (tile >= total) continue;
-      const GmTile ti = gm_tile<OP>(tile, P, s_tab, ntn, rank);
-      const bool sums = ti.nkb > 0;
-      const int acc = used & 1;
-      if (sums) {
+      const GmTile ti = gm_tile<OP>(tile, P.g.E, P.M, P.K, s_tab, ntn, 256, rank);
+      const int rem = min(32, ti.mrows - quad * 32);            // rows of the group in this warp's 32
+      const int col0 = ti.n0 + half * 128;
+      const int row = ti.m0 + quad * 32;
+      if constexpr (OP == kGroupedWgrad) {
+        // the sums of all slices, chunk by chunk in registers
+        float sum[128];
+#pragma unroll
+        for (int c = 0; c < 128; ++c) sum[c] = 0.f;
+        const int chunks = ((ti.krows + 63) / 64 + kGmChunk<OP> - 1) / kGmChunk<OP>;
+        bool ok = true;
+        for (int i = 0; i < chunks; ++i) {
+          const int acc = used & 1;
+          const uint32_t aph = (used >> 1) & 1;
+          ++used;
+          ok = warp_wait(&tfull[acc], aph, abort, hdr, 116);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t tb = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 256 + half * 128;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t r[16];
+            tmem_ld_32x32b_x16(tb + 16 * c, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < 16; ++q) sum[16 * c + q] += __uint_as_float(r[q]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(acc ? te1 : te0);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int col = col0 + 32 * c;
+          if (rem <= 0 || col >= P.N) continue;    // warp-uniform
+          if (lane == 0) bulk_wait_read();         // the previous piece's store has read the stage
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<float4*>(wstage + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                make_float4(sum[32 * c + 4 * q], sum[32 * c + 4 * q + 1], sum[32 * c + 4 * q + 2], sum[32 * c + 4 * q + 3]);
+          if (P.out_aligned) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_3d(&P.out, wstage, col, row, ti.e);
+              bulk_commit();
+            }
+          } else {
+            // rows that start anywhere: element by element
+            __syncwarp();
+            float* o = static_cast<float*>(P.outp) + (static_cast<int64_t>(ti.e) * P.M + row) * P.N + col + lane;
+            if (col + lane < P.N)
+              for (int i = 0; i < rem; ++i)
+                o[static_cast<int64_t>(i) * P.N] =
+                    *reinterpret_cast<const float*>(wstage + i * 128 + ((((lane >> 2) ^ (i & 7)) << 4) | ((lane & 3) << 2)));
+          }
+        }
+      } else {
+        const int acc = used & 1;
         const uint32_t aph = (used >> 1) & 1;
         ++used;
         if (!warp_wait(&tfull[acc], aph, abort, hdr, 116)) break;
         tc_fence_after();
-      }
-      const int rem = min(32, ti.mrows - quad * 32);            // rows of the group in this warp's 32
-      const bool counts = sums && quad * 32 + lane < ti.mvalid; // this lane's row is not padding
-      const uint32_t tb = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 256 + half * 128;
+        const bool counts = quad * 32 + lane < ti.mvalid;       // this lane's row is not padding
+        const uint32_t tb = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 256 + half * 128;
 #pragma unroll 1
-      for (int c = 0; c < 128; c += kPiece) {
-        const int col = ti.n0 + half * 128 + c;
-        uint32_t r[kPiece];
-#pragma unroll
-        for (int h = 0; h < kPiece; h += 32)
-          tmem_ld_32x32b_x32(tb + c + h, *reinterpret_cast<uint32_t(*)[32]>(r + h));   // every lane (warp-collective)
-        tmem_ld_wait();
-        if (rem <= 0 || col >= P.N) continue;      // warp-uniform
-        uint32_t pk[32];
-#pragma unroll
-        for (int q = 0; q < 32; ++q) {
-          if constexpr (kF32) pk[q] = r[q];
-          else pk[q] = pack_bf16x2(__uint_as_float(r[2 * q]), __uint_as_float(r[2 * q + 1]));
-          if (!counts) pk[q] = 0u;
-        }
-        if (lane == 0) bulk_wait_read();           // the previous piece's store has read the stage
-        __syncwarp();
-        // 128-byte rows, 16-byte chunk q of row i at chunk q ^ (i & 7)
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          *reinterpret_cast<uint4*>(wstage + lane * 128 + ((q ^ (lane & 7)) << 4)) =
-              make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
-        const int row = ti.m0 + quad * 32;
-        if (P.out_aligned && (kF32 || rem == 32)) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if constexpr (kF32) tma_store_3d(&P.out, wstage, col, row, ti.e);
-            else tma_store_2d(&P.out, wstage, col, row);
-            bulk_commit();
+        for (int c = 0; c < 128; c += 64) {
+          uint32_t lo[32], hi[32];
+          tmem_ld_32x32b_x32(tb + c, lo);          // every lane (warp-collective)
+          tmem_ld_32x32b_x32(tb + c + 32, hi);
+          tmem_ld_wait();
+          if (c == 64) {                           // the accumulator is read: the next tile may have it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(acc ? te1 : te0);
           }
-          continue;
-        }
-        __syncwarp();
-        const int64_t o = (kF32 ? static_cast<int64_t>(ti.e) * P.M + row : static_cast<int64_t>(row)) * P.N + col;
-        if (P.out_aligned) {
-          // a group's ragged end: 16 bytes a lane, four rows at once
-          for (int i = lane >> 3; i < rem; i += 4)
-            if (col + 8 * (lane & 7) < P.N)
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.outp) + o + static_cast<int64_t>(i) * P.N + 8 * (lane & 7)) =
-                  *reinterpret_cast<const uint4*>(wstage + i * 128 + (((lane & 7) ^ (i & 7)) << 4));
-        } else {
-          // rows that start anywhere: element by element
-          for (int i = 0; i < rem; ++i) {
+          if (rem <= 0 || col0 + c >= P.N) continue;            // warp-uniform
+          uint32_t pk[32];
 #pragma unroll
-            for (int h = 0; h < kPiece; h += 32) {
-              const int cc = h + lane;
-              if (col + cc >= P.N) continue;
-              const int64_t to = o + static_cast<int64_t>(i) * P.N + cc;
-              if constexpr (kF32)
-                static_cast<float*>(P.outp)[to] =
-                    *reinterpret_cast<const float*>(wstage + i * 128 + ((((cc >> 2) ^ (i & 7)) << 4) | ((cc & 3) << 2)));
-              else
-                static_cast<uint16_t*>(P.outp)[to] =
-                    *reinterpret_cast<const uint16_t*>(wstage + i * 128 + ((((cc >> 3) ^ (i & 7)) << 4) | ((cc & 7) << 1)));
-            }
+          for (int q = 0; q < 16; ++q) {
+            pk[q] = counts ? pack_bf16x2(__uint_as_float(lo[2 * q]), __uint_as_float(lo[2 * q + 1])) : 0u;
+            pk[16 + q] = counts ? pack_bf16x2(__uint_as_float(hi[2 * q]), __uint_as_float(hi[2 * q + 1])) : 0u;
           }
+          store_rows_bf16(pk, wstage, &P.out, P.outp, P.out_aligned, row, col0 + c, rem, P.N, lane);
         }
-      }
-      if (sums) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(acc ? te1 : te0);
       }
     }
     if (lane == 0) bulk_wait_all();   // this warp's tensor stores have landed
@@ -493,12 +425,6 @@ static bool map_rows_mn(CUtensorMap* m, const void* p, int cols, int64_t rows, i
   const uint32_t b[2] = {64, 64};
   return make_map(m, kBf, 2, reinterpret_cast<uint64_t>(p), d, s, b, kSw);
 }
-// Result rows in bf16: store boxes of 64 x 32.
-static bool map_out_rows(CUtensorMap* m, void* p, int cols, int64_t rows) {
-  const uint64_t d[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)}, s[1] = {static_cast<uint64_t>(cols) * 2};
-  const uint32_t b[2] = {64, 32};
-  return make_map(m, kBf, 2, reinterpret_cast<uint64_t>(p), d, s, b, kSw);
-}
 // Weight gradients fp32 [E, N, K]: store boxes of 32 x 32.
 static bool map_out_weights(CUtensorMap* m, void* p, int K, int N, int E) {
   const uint64_t d[3] = {static_cast<uint64_t>(K), static_cast<uint64_t>(N), static_cast<uint64_t>(E)};
@@ -515,11 +441,6 @@ static cudaError_t gm_launch(const GmParams& p, int64_t tiles, WsHeader* hdr, cu
   if (e != cudaSuccess) return e;
   const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(tiles, num_sms() / 2));
   return launch_dependent_kernel(fn, dim3(static_cast<unsigned>(2 * pairs)), dim3(kGmThreads), kGmSmem, st, p, hdr);
-}
-
-// Tiles of 256 rows that any grouping of the rows can need.
-static int64_t row_tiles256(const GroupTables& g) {
-  return g.offsets ? std::min<int64_t>(g.rows, g.rows / 256 + g.E) : (g.rows + 255) / 256;
 }
 
 cudaError_t launch_grouped_tc(int op, const GroupedArgs& a, WsHeader* hdr, cudaStream_t st) {

@@ -386,6 +386,47 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
          | (static_cast<uint32_t>(M >> 4) << 24);    // M / 16
 }
 
+// ---------------------------------------------------------------- 4-bit operands
+// Shared-memory descriptor of 32 rows x 16 bytes next to each other, no
+// swizzle (8-row groups 128 bytes apart): the source of a tcgen05.cp.
+__device__ __forceinline__ uint64_t smem_desc_rows16(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);   // start address
+  d |= static_cast<uint64_t>(128u >> 4) << 32;             // stride byte offset
+  d |= static_cast<uint64_t>(1u) << 46;                    // descriptor version
+  return d;
+}
+// 32 rows x 16 bytes of shared memory -> four TMEM columns, repeated over the
+// four groups of 32 lanes, in both CTAs of the pair (each from its own shared
+// memory); ordered before the tcgen05.mma that this thread issues next.
+__device__ __forceinline__ void tmem_cp_scales_cta2(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// Instruction descriptor, kind::mxf4 with scales of 32 elements: e2m1 A and B
+// (both K-major, packed), ue8m0 scales, fp32 D.  `pair`: which two bytes of
+// the scale words (0 or 2).
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int pair) {
+  return (static_cast<uint32_t>(pair) << 4)          // B scale bytes
+         | (1u << 7) | (1u << 10)                    // A, B format: e2m1
+         | (static_cast<uint32_t>(N >> 3) << 17)     // N / 8
+         | (1u << 23)                                // scale format: ue8m0
+         | (static_cast<uint32_t>(M >> 4) << 24)     // M / 16
+         | (static_cast<uint32_t>(pair) << 29);      // A scale bytes
+}
+// D (+)= (A * scales) * (B * scales)^T over the CTA pair, 64 4-bit elements of
+// the summed index, issued by the even CTA.
+__device__ __forceinline__ void umma_mxf4_cta2(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                               uint32_t idesc, uint32_t sa, uint32_t sb,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sa), "r"(sb)
+      : "memory");
+}
+
 // 32 lanes x 32 consecutive 32-bit columns: thread i of the warp receives
 // row (lane base + i), columns [col, col + 32).
 __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -558,6 +599,18 @@ __device__ __forceinline__ void bulk_wait_read() {
 // Wait until every committed bulk group of this thread has completed.
 __device__ __forceinline__ void bulk_wait_all() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+// ---------------------------------------------------------------- cp.async, 4 bytes
+// Copies 4 bytes to shared memory without waiting, or writes zeros there.
+__device__ __forceinline__ void cp_async4(uint32_t smem_dst, const void* src, bool read) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_dst), "l"(src), "r"(read ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until at most `LEFT` of this thread's groups are on their way.
+template <int LEFT>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
 // ---------------------------------------------------------------- misc

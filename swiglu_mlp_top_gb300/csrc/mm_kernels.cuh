@@ -497,6 +497,18 @@ constexpr int pitch8(int n) { return (n + 7) / 8 * 8; }
 cudaError_t launch_repitch(const void* src, void* dst, int64_t rows, int cols, cudaStream_t st);
 cudaError_t launch_grouped_tc(int op, const GroupedArgs& p, WsHeader* hdr, cudaStream_t st);
 
+// Products of 4-bit rows and 4-bit weights on the tensor cores (mx4_tc.cu).
+struct Mx4MatmulArgs {
+  const void* x;              // codes [rows, 16 G]
+  const uint8_t* x_exps;      // [ceil(G / 4), rows, 4]
+  const void* w;              // codes [E * N, 16 G]
+  const uint8_t* w_exps;      // [ceil(G / 4), E * N, 4]
+  void* out;                  // bf16 [rows, N]
+  GroupTables g;
+  int K, N;
+};
+cudaError_t launch_mx4_tc(const Mx4MatmulArgs& p, WsHeader* hdr, cudaStream_t st);
+
 // 4-bit microscaled tensors (mx4.cu).
 struct Mx4Args {
   const void* x;              // quantise: [R, C]

@@ -1,0 +1,290 @@
+// Products of rows and weights in microscaled 4-bit floating point on the
+// 5th-generation tensor cores: ys = v(xs) v(w[e])^T, fp32 accumulators.
+//
+// tcgen05.mma kind::mxf4 over a CTA pair multiplies 256 rows x 256 columns x
+// 64 packed e2m1 elements and scales each group of 32 by its power of two,
+// which it reads from TMEM.  As for bf16 (grouped_tc.cu): a tile of 256 x 256,
+// operands by TMA into a ring of stages of 128 bytes a row (256 elements),
+// half of the weights' rows in each CTA.
+//
+// Scales.  The four scale bytes of 128 columns of a row are one word, and a
+// TMEM column holds the words of 32 rows.  tcgen05.cp takes 32 x 16 bytes from
+// shared memory to four columns, where the 16 bytes at l are the words of rows
+// l, l + 32, l + 64, l + 96.  A word's rows lie next to each other in memory
+// ([columns / 128, rows, 4]), so a warp reads 32 of them at once and any first
+// row will do; two warps bring them with 4-byte cp.async, three stages ahead,
+// one the rows' and one the weights' (all 256 columns in each CTA: a CTA
+// scales its own half of the rows).
+//
+// TMEM: one accumulator of 256 columns (two would leave no room for scales)
+// and two stages of scales, 24 columns each.  The epilogue packs the
+// accumulator into registers and hands it back before it stores.
+#include "grouped.cuh"
+
+namespace mm {
+
+constexpr int kMtStages = 5;
+constexpr int kMtTile = 128 * 128;                    // 16 KiB: 128 rows x 256 elements
+constexpr int kMtScA = 1024, kMtScB = 2048;           // scale words of a stage: 128 and 256 rows x 2
+constexpr int kMtStageBytes = 2 * kMtTile + kMtScA + kMtScB;
+constexpr int kMtEpiWarps = 8;
+constexpr int kMtWarpProducer = kMtEpiWarps, kMtWarpMma = kMtEpiWarps + 1, kMtWarpScales = kMtEpiWarps + 2;
+constexpr int kMtThreads = 32 * (kMtEpiWarps + 4);
+constexpr int kMtEpi = 32 * 128;
+constexpr int kMtSmem = kMtStages * kMtStageBytes + kMtEpiWarps * kMtEpi + 1024 + 256;
+static_assert(kMtSmem + sizeof(GmTables) + 64 <= 232448, "shared memory budget");
+constexpr int kMtAhead = 3;                           // stages of scales on their way
+static_assert(kMtAhead < kMtStages, "a stage is handed on before the ring comes round to it");
+constexpr uint32_t kMtScales = 256, kMtScaleCols = 24;   // TMEM: 8 columns of A's, 16 of B's
+
+struct MtParams {
+  CUtensorMap a, b, out;
+  GroupTables g;
+  const uint8_t* a_sc;      // [words, rows, 4]
+  const uint8_t* b_sc;      // [words, E * N, 4]
+  int N;                    // columns of the result
+  int stages;               // stages of 256 elements
+  int words;                // scale words of a row
+  int out_aligned;
+  void* outp;
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMtThreads, 1)
+mx4_tc_kernel(const __grid_constant__ MtParams P, WsHeader* hdr) {
+  extern __shared__ unsigned char smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + kMtStages * kMtTile;
+  uint8_t* sEpi = sB + kMtStages * kMtTile;
+  uint8_t* sScA = sEpi + kMtEpiWarps * kMtEpi;
+  uint8_t* sScB = sScA + kMtStages * kMtScA;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sScB + kMtStages * kMtScB);
+  uint64_t* full = bars;                   // [stages] even CTA: both CTAs' bytes and scales
+  uint64_t* empty = bars + kMtStages;      // [stages] each CTA: released by the pair's MMAs
+  uint64_t* tfull = bars + 2 * kMtStages;  // each CTA: accumulator ready
+  uint64_t* tempty = tfull + 1;            // even CTA: both CTAs' epilogues have read it
+  uint64_t* drained = tempty + 1;          // even CTA: all MMAs finished
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  __shared__ GmTables s_tab;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int cluster = blockIdx.x >> 1, nc = gridDim.x >> 1;
+  const int ntn = (P.N + 255) / 256;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMtStages; ++s) {
+      mbar_init(&full[s], 1 + 2 * 2);      // the bytes, and two warps of scales in each CTA
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(tfull, 1);
+    mbar_init(tempty, 2 * kMtEpiWarps);
+    mbar_init(drained, 1);
+    fence_mbar_init();
+    s_abort = 0;
+  }
+  if (warp == 0) {
+    // tables and operands may be the previous kernel's output
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    gm_tables<kGroupedForward>(P.g, s_tab, ntn);
+  }
+  if (warp == kMtWarpMma) {
+    tmem_alloc_cta2(&s_tmem, 512);
+    tmem_relinquish_cta2();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const int total = s_tab.tstart[P.g.E];
+  volatile int* abort = &s_abort;
+
+  if (warp == kMtWarpProducer) {
+    // ------------------------------------------------ TMA (both CTAs)
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int tile = cluster; ok && tile < total; tile += nc) {
+        const GmTile ti = gm_tile<kGroupedForward>(tile, P.g.E, 0, 0, s_tab, ntn, 256, rank);
+        for (int kb = 0; kb < P.stages; ++kb, ++it) {
+          const int s = it % kMtStages;
+          const uint32_t ph = (it / kMtStages) & 1;
+          if (!mbar_wait(&empty[s], ph ^ 1, abort, hdr, 121)) { ok = false; break; }
+          const uint32_t fb = mapa_shared(smem_u32(&full[s]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 4 * kMtTile);
+          tma_load_2d_cta2(sA + s * kMtTile, &P.a, fb, kb * 128, ti.m0);
+          tma_load_3d_cta2(sB + s * kMtTile, &P.b, fb, kb * 128, ti.n0 + 128 * rank, ti.e);
+        }
+      }
+      if (!ok && rank == 0) {
+        // a wait gave up: the copies in flight land before the block ends
+        for (int j = 0; j < kMtStages; ++j) {
+          const int i2 = it - 1 - j;
+          if (i2 < 0) break;
+          mbar_wait(&full[i2 % kMtStages], (i2 / kMtStages) & 1, nullptr, hdr, 122);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp >= kMtWarpScales) {
+    // ------------------------------------------------ scales (both CTAs): a warp for A's, one for B's
+    const bool is_b = warp > kMtWarpScales;
+    const uint8_t* src = is_b ? P.b_sc : P.a_sc;
+    const int64_t pitch = is_b ? static_cast<int64_t>(P.g.E) * P.N : P.g.rows;     // rows of a word
+    uint8_t* dst = is_b ? sScB : sScA;
+    const int bytes = is_b ? kMtScB : kMtScA, atoms = is_b ? 2 : 1;
+    int it = 0;
+    bool ok = true;
+    // stage i's scales have landed: visible to the tensor core, and told to the even CTA
+    auto hand_on = [&](int i) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&full[i % kMtStages]), 0));
+    };
+    for (int tile = cluster; ok && tile < total; tile += nc) {
+      const GmTile ti = gm_tile<kGroupedForward>(tile, P.g.E, 0, 0, s_tab, ntn, 256, rank);
+      const int64_t row0 = is_b ? static_cast<int64_t>(ti.e) * P.N + ti.n0 : ti.m0;
+      const int have = is_b ? P.N - ti.n0 : static_cast<int>(min(P.g.rows - ti.m0, static_cast<int64_t>(128)));
+      for (int kb = 0; kb < P.stages; ++kb, ++it) {
+        const int s = it % kMtStages;
+        const uint32_t ph = (it / kMtStages) & 1;
+        ok = warp_wait(&empty[s], ph ^ 1, abort, hdr, 123);
+        if (!ok) break;
+        const uint32_t to = smem_u32(dst + s * bytes) + lane * 16;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int word = 2 * kb + c;
+          const bool in = word < P.words;
+          const uint8_t* from = src + (static_cast<int64_t>(in ? word : 0) * pitch + row0) * 4;
+          for (int at = 0; at < atoms; ++at) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = at * 128 + i * 32 + lane;
+              const bool read = in && r < have;
+              // where there is nothing, zeros: 2^-127, which scales zeros or rows that are not stored
+              cp_async4(to + (c * atoms + at) * 512 + i * 4, read ? from + 4 * r : src, read);
+            }
+          }
+        }
+        cp_async_commit();
+        if (it >= kMtAhead - 1) {
+          cp_async_wait<kMtAhead - 1>();
+          hand_on(it - (kMtAhead - 1));
+        }
+      }
+    }
+    cp_async_wait<0>();
+    if (ok)
+      for (int i = max(0, it - (kMtAhead - 1)); i < it; ++i) hand_on(i);
+  } else if (warp == kMtWarpMma) {
+    // ------------------------------------------------ MMA (even CTA)
+    if (rank == 0 && lane == 0) {
+      int it = 0, used = 0;
+      bool ok = true;
+      for (int tile = cluster; ok && tile < total; tile += nc, ++used) {
+        if (!mbar_wait(tempty, (used & 1) ^ 1, abort, hdr, 124)) { ok = false; break; }
+        tc_fence_after();
+        for (int kb = 0; kb < P.stages; ++kb, ++it) {
+          const int s = it % kMtStages;
+          const uint32_t ph = (it / kMtStages) & 1;
+          if (!mbar_wait<true>(&full[s], ph, abort, hdr, 125)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t ca = smem_u32(sScA + s * kMtScA), cb = smem_u32(sScB + s * kMtScB);
+          const uint32_t ta = tmem + kMtScales + (it & 1) * kMtScaleCols, tb = ta + 8;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            tmem_cp_scales_cta2(ta + 4 * c, smem_desc_rows16(ca + 512 * c));
+            tmem_cp_scales_cta2(tb + 8 * c, smem_desc_rows16(cb + 1024 * c));
+            tmem_cp_scales_cta2(tb + 8 * c + 4, smem_desc_rows16(cb + 1024 * c + 512));
+          }
+          const uint32_t a0 = smem_u32(sA + s * kMtTile), b0 = smem_u32(sB + s * kMtTile);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_mxf4_cta2(tmem, smem_desc_sw128(a0 + kk * 32), smem_desc_sw128(b0 + kk * 32),
+                           idesc_mxf4(256, 256, 2 * (kk & 1)), ta + 4 * (kk >> 1), tb + 8 * (kk >> 1), (kb | kk) ? 1u : 0u);
+          umma_commit_cta2_mc(&empty[s], 0x3);
+        }
+        if (!ok) break;
+        umma_commit_cta2_mc(tfull, 0x3);
+      }
+      umma_commit_cta2_mc(drained, 0x1);
+      mbar_wait(drained, 0, nullptr, hdr, 126);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------ epilogue (warps 0-7, both CTAs)
+    const int quad = warp & 3, half = warp >> 2;
+    uint8_t* wstage = sEpi + warp * kMtEpi;
+    const uint32_t te = mapa_shared(smem_u32(tempty), 0);
+    int used = 0;
+    for (int tile = cluster; tile < total; tile += nc, ++used) {
+      const GmTile ti = gm_tile<kGroupedForward>(tile, P.g.E, 0, 0, s_tab, ntn, 256, rank);
+      if (!warp_wait(tfull, used & 1, abort, hdr, 127)) break;
+      tc_fence_after();
+      const int rem = min(32, ti.mrows - quad * 32);            // rows of the group in this warp's 32
+      const bool counts = quad * 32 + lane < ti.mvalid;         // this lane's row is not padding
+      const uint32_t tb = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 128;
+      uint32_t pk[2][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(tb + 32 * c, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+          pk[c >> 1][16 * (c & 1) + q] = counts ? pack_bf16x2(__uint_as_float(r[2 * q]), __uint_as_float(r[2 * q + 1])) : 0u;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(te);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int col = ti.n0 + half * 128 + 64 * c;
+        if (rem > 0 && col < P.N)
+          store_rows_bf16(pk[c], wstage, &P.out, P.outp, P.out_aligned, ti.m0 + quad * 32, col, rem, P.N, lane);
+      }
+    }
+    if (lane == 0) bulk_wait_all();   // this warp's tensor stores have landed
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == kMtWarpMma) tmem_dealloc_cta2(tmem, 512);
+}
+
+// =============================================================== host side
+cudaError_t launch_mx4_tc(const Mx4MatmulArgs& a, WsHeader* hdr, cudaStream_t st) {
+  MtParams p;
+  memset(&p, 0, sizeof(p));
+  const int groups = (a.K + 31) / 32;
+  p.g = a.g;
+  p.a_sc = a.x_exps;
+  p.b_sc = a.w_exps;
+  p.N = a.N;
+  p.words = (groups + 3) / 4;
+  p.stages = (groups + 7) / 8;
+  p.outp = a.out;
+  p.out_aligned = a.N % 8 == 0;
+  const uint64_t row = 16 * static_cast<uint64_t>(groups);
+  const uint64_t da[2] = {row, static_cast<uint64_t>(a.g.rows)}, sa[1] = {row};
+  const uint64_t db[3] = {row, static_cast<uint64_t>(a.N), static_cast<uint64_t>(a.g.E)}, sb[2] = {row, row * a.N};
+  const uint32_t box[3] = {128, 128, 1};
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  if (!make_map(&p.a, u8, 2, reinterpret_cast<uint64_t>(a.x), da, sa, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&p.b, u8, 3, reinterpret_cast<uint64_t>(a.w), db, sb, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      (p.out_aligned && !map_out_rows(&p.out, a.out, a.N, a.g.rows)))
+    return cudaErrorInvalidValue;
+  const int64_t tiles = row_tiles256(a.g) * ((a.N + 255) / 256);
+  if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
+  const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(mx4_tc_kernel), kMtSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(tiles, num_sms() / 2));
+  return launch_dependent_kernel(mx4_tc_kernel, dim3(static_cast<unsigned>(2 * pairs)), dim3(kMtThreads), kMtSmem, st,
+                                 p, hdr);
+}
+
+}  // namespace mm
