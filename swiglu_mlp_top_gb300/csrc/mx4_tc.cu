@@ -12,9 +12,11 @@
 // shared memory to four columns, where the 16 bytes at l are the words of rows
 // l, l + 32, l + 64, l + 96.  A word's rows lie next to each other in memory
 // ([columns / 128, rows, 4]), so a warp reads 32 of them at once and any first
-// row will do; two warps bring them with 4-byte cp.async, three stages ahead,
-// one the rows' and one the weights' (all 256 columns in each CTA: a CTA
-// scales its own half of the rows).
+// row will do.  Four warps take a stage each in turn (all 256 columns' scales
+// in each CTA: a CTA scales its own half of the rows): they load a stage's
+// words before its place in the ring is free, and store 16 bytes a lane.  (Two
+// warps that copied every stage word by word with cp.async made the stages
+// follow each other at 2000 cycles, most of it the way of one stage's words.)
 //
 // TMEM: one accumulator of 256 columns (two would leave no room for scales)
 // and two stages of scales, 24 columns each.  The epilogue packs the
@@ -25,16 +27,15 @@ namespace mm {
 
 constexpr int kMtStages = 5;
 constexpr int kMtTile = 128 * 128;                    // 16 KiB: 128 rows x 256 elements
-constexpr int kMtScA = 1024, kMtScB = 2048;           // scale words of a stage: 128 and 256 rows x 2
-constexpr int kMtStageBytes = 2 * kMtTile + kMtScA + kMtScB;
+constexpr int kMtSc = 2 * (128 + 256) * 4;            // scale words of a stage: of 128 rows and 256 columns, twice
+constexpr int kMtStageBytes = 2 * kMtTile + kMtSc;
 constexpr int kMtEpiWarps = 8;
 constexpr int kMtWarpProducer = kMtEpiWarps, kMtWarpMma = kMtEpiWarps + 1, kMtWarpScales = kMtEpiWarps + 2;
-constexpr int kMtThreads = 32 * (kMtEpiWarps + 4);
+constexpr int kMtScaleWarps = 4;
+constexpr int kMtThreads = 32 * (kMtEpiWarps + 2 + kMtScaleWarps);
 constexpr int kMtEpi = 32 * 128;
 constexpr int kMtSmem = kMtStages * kMtStageBytes + kMtEpiWarps * kMtEpi + 1024 + 256;
 static_assert(kMtSmem + sizeof(GmTables) + 64 <= 232448, "shared memory budget");
-constexpr int kMtAhead = 3;                           // stages of scales on their way
-static_assert(kMtAhead < kMtStages, "a stage is handed on before the ring comes round to it");
 constexpr uint32_t kMtScales = 256, kMtScaleCols = 24;   // TMEM: 8 columns of A's, 16 of B's
 
 struct MtParams {
@@ -56,9 +57,8 @@ mx4_tc_kernel(const __grid_constant__ MtParams P, WsHeader* hdr) {
   uint8_t* sA = smem;
   uint8_t* sB = sA + kMtStages * kMtTile;
   uint8_t* sEpi = sB + kMtStages * kMtTile;
-  uint8_t* sScA = sEpi + kMtEpiWarps * kMtEpi;
-  uint8_t* sScB = sScA + kMtStages * kMtScA;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sScB + kMtStages * kMtScB);
+  uint8_t* sSc = sEpi + kMtEpiWarps * kMtEpi;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sSc + kMtStages * kMtSc);
   uint64_t* full = bars;                   // [stages] even CTA: both CTAs' bytes and scales
   uint64_t* empty = bars + kMtStages;      // [stages] each CTA: released by the pair's MMAs
   uint64_t* tfull = bars + 2 * kMtStages;  // each CTA: accumulator ready
@@ -75,7 +75,7 @@ mx4_tc_kernel(const __grid_constant__ MtParams P, WsHeader* hdr) {
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMtStages; ++s) {
-      mbar_init(&full[s], 1 + 2 * 2);      // the bytes, and two warps of scales in each CTA
+      mbar_init(&full[s], 1 + 2);          // the bytes, and each CTA's scales
       mbar_init(&empty[s], 1);
     }
     mbar_init(tfull, 1);
@@ -129,55 +129,46 @@ mx4_tc_kernel(const __grid_constant__ MtParams P, WsHeader* hdr) {
     }
     __syncwarp();
   } else if (warp >= kMtWarpScales) {
-    // ------------------------------------------------ scales (both CTAs): a warp for A's, one for B's
-    const bool is_b = warp > kMtWarpScales;
-    const uint8_t* src = is_b ? P.b_sc : P.a_sc;
-    const int64_t pitch = is_b ? static_cast<int64_t>(P.g.E) * P.N : P.g.rows;     // rows of a word
-    uint8_t* dst = is_b ? sScB : sScA;
-    const int bytes = is_b ? kMtScB : kMtScA, atoms = is_b ? 2 : 1;
-    int it = 0;
-    bool ok = true;
-    // stage i's scales have landed: visible to the tensor core, and told to the even CTA
-    auto hand_on = [&](int i) {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&full[i % kMtStages]), 0));
-    };
-    for (int tile = cluster; ok && tile < total; tile += nc) {
-      const GmTile ti = gm_tile<kGroupedForward>(tile, P.g.E, 0, 0, s_tab, ntn, 256, rank);
-      const int64_t row0 = is_b ? static_cast<int64_t>(ti.e) * P.N + ti.n0 : ti.m0;
-      const int have = is_b ? P.N - ti.n0 : static_cast<int>(min(P.g.rows - ti.m0, static_cast<int64_t>(128)));
-      for (int kb = 0; kb < P.stages; ++kb, ++it) {
-        const int s = it % kMtStages;
-        const uint32_t ph = (it / kMtStages) & 1;
-        ok = warp_wait(&empty[s], ph ^ 1, abort, hdr, 123);
-        if (!ok) break;
-        const uint32_t to = smem_u32(dst + s * bytes) + lane * 16;
+    // ------------------------------------------------ scales (both CTAs): four warps, a stage each in turn
+    const int64_t a_rows = P.g.rows, b_rows = static_cast<int64_t>(P.g.E) * P.N;
+    const uint32_t* a_sc = reinterpret_cast<const uint32_t*>(P.a_sc);
+    const uint32_t* b_sc = reinterpret_cast<const uint32_t*>(P.b_sc);
+    const int mine = total > cluster ? (total - cluster + nc - 1) / nc * P.stages : 0;      // stages of all tiles
+    int have = -1;
+    GmTile ti;
+    for (int it = warp - kMtWarpScales; it < mine; it += kMtScaleWarps) {
+      const int nth = it / P.stages, kb = it - nth * P.stages;
+      if (nth != have) ti = gm_tile<kGroupedForward>(cluster + nth * nc, P.g.E, 0, 0, s_tab, ntn, 256, rank);
+      have = nth;
+      // a lane's words of rows lane, + 32, + 64, + 96 of each 128; where there is
+      // nothing, zeros: 2^-127, which scales zeros or rows that are not stored
+      uint32_t w[6][4];
+      const int64_t b0 = static_cast<int64_t>(ti.e) * P.N + ti.n0;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int word = 2 * kb + c;
-          const bool in = word < P.words;
-          const uint8_t* from = src + (static_cast<int64_t>(in ? word : 0) * pitch + row0) * 4;
-          for (int at = 0; at < atoms; ++at) {
+      for (int c = 0; c < 2; ++c) {
+        const int word = 2 * kb + c;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = at * 128 + i * 32 + lane;
-              const bool read = in && r < have;
-              // where there is nothing, zeros: 2^-127, which scales zeros or rows that are not stored
-              cp_async4(to + (c * atoms + at) * 512 + i * 4, read ? from + 4 * r : src, read);
-            }
-          }
-        }
-        cp_async_commit();
-        if (it >= kMtAhead - 1) {
-          cp_async_wait<kMtAhead - 1>();
-          hand_on(it - (kMtAhead - 1));
+        for (int i = 0; i < 4; ++i) {
+          const int r = i * 32 + lane;
+          w[3 * c][i] = word < P.words && ti.m0 + r < a_rows ? a_sc[word * a_rows + ti.m0 + r] : 0u;
+          w[3 * c + 1][i] = word < P.words && ti.n0 + r < P.N ? b_sc[word * b_rows + b0 + r] : 0u;
+          w[3 * c + 2][i] = word < P.words && ti.n0 + 128 + r < P.N ? b_sc[word * b_rows + b0 + 128 + r] : 0u;
         }
       }
+      const int s = it % kMtStages;
+      const uint32_t ph = (it / kMtStages) & 1;
+      if (!warp_wait(&empty[s], ph ^ 1, abort, hdr, 123)) break;
+      uint4* to = reinterpret_cast<uint4*>(sSc + s * kMtSc) + lane;
+#pragma unroll
+      for (int q = 0; q < 6; ++q) to[32 * q] = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+      fence_proxy_async_smem();                // visible to the tensor core, and told to the even CTA
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive(&full[s]);
+        else mbar_arrive_cluster(mapa_shared(smem_u32(&full[s]), 0));
+      }
     }
-    cp_async_wait<0>();
-    if (ok)
-      for (int i = max(0, it - (kMtAhead - 1)); i < it; ++i) hand_on(i);
+    __syncwarp();
   } else if (warp == kMtWarpMma) {
     // ------------------------------------------------ MMA (even CTA)
     if (rank == 0 && lane == 0) {
@@ -191,13 +182,13 @@ mx4_tc_kernel(const __grid_constant__ MtParams P, WsHeader* hdr) {
           const uint32_t ph = (it / kMtStages) & 1;
           if (!mbar_wait<true>(&full[s], ph, abort, hdr, 125)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t ca = smem_u32(sScA + s * kMtScA), cb = smem_u32(sScB + s * kMtScB);
+          const uint32_t sc = smem_u32(sSc + s * kMtSc);
           const uint32_t ta = tmem + kMtScales + (it & 1) * kMtScaleCols, tb = ta + 8;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            tmem_cp_scales_cta2(ta + 4 * c, smem_desc_rows16(ca + 512 * c));
-            tmem_cp_scales_cta2(tb + 8 * c, smem_desc_rows16(cb + 1024 * c));
-            tmem_cp_scales_cta2(tb + 8 * c + 4, smem_desc_rows16(cb + 1024 * c + 512));
+            tmem_cp_scales_cta2(ta + 4 * c, smem_desc_rows16(sc + 1536 * c));
+            tmem_cp_scales_cta2(tb + 8 * c, smem_desc_rows16(sc + 1536 * c + 512));
+            tmem_cp_scales_cta2(tb + 8 * c + 4, smem_desc_rows16(sc + 1536 * c + 1024));
           }
           const uint32_t a0 = smem_u32(sA + s * kMtTile), b0 = smem_u32(sB + s * kMtTile);
 #pragma unroll
