@@ -194,12 +194,13 @@ __device__ __forceinline__ void store_rows_bf16(const uint32_t (&pk)[32], uint8_
 }
 
 // ---------------------------------------------------------------- host side
-// Result rows in bf16: store boxes of 64 x 32.
-inline bool map_out_rows(CUtensorMap* m, void* p, int cols, int64_t rows) {
+// Result rows in bf16: store boxes of `box` columns (64 or 32) x 32 rows, swizzled
+// over the box's row.
+inline bool map_out_rows(CUtensorMap* m, void* p, int cols, int64_t rows, int box) {
   const uint64_t d[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)}, s[1] = {static_cast<uint64_t>(cols) * 2};
-  const uint32_t b[2] = {64, 32};
+  const uint32_t b[2] = {static_cast<uint32_t>(box), 32};
   return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, reinterpret_cast<uint64_t>(p), d, s, b,
-                  CU_TENSOR_MAP_SWIZZLE_128B);
+                  box == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 // Tiles of 256 rows that any grouping of the rows can need.
 inline int64_t row_tiles256(const GroupTables& g) {

@@ -469,7 +469,7 @@ cudaError_t launch_grouped_tc(int op, const GroupedArgs& a, WsHeader* hdr, cudaS
   p.b_blocks = !fwd && a.K % 64 == 0;
   ok = fwd ? map_kmajor(&p.a, a.xs, a.K, a.g.rows, kp) && map_weights(&p.b, a.w, a.K, kp, a.N, a.g.E)
            : map_kmajor(&p.a, a.dys, a.N, a.g.rows, np) && map_weights_mn(&p.b, a.w, a.K, kp, a.N, a.g.E, p.b_blocks);
-  ok = ok && (!p.out_aligned || map_out_rows(&p.out, a.out, p.N, a.g.rows));
+  ok = ok && (!p.out_aligned || map_out_rows(&p.out, a.out, p.N, a.g.rows, 64));
   if (!ok) return cudaErrorInvalidValue;
   const int64_t tiles = row_tiles256(a.g) * ((p.N + 255) / 256);
   return fwd ? gm_launch<kGroupedForward>(p, tiles, hdr, st) : gm_launch<kGroupedDgrad>(p, tiles, hdr, st);

@@ -164,10 +164,22 @@ __device__ __forceinline__ uint8_t* align1024(unsigned char* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
 
+// One lane of the full warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+
 // Warp-uniform bounded wait: every lane waits, then the warp agrees.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
                                           WsHeader* hdr, unsigned where) {
-  const bool ok = mbar_wait(bar, parity, abort, hdr, where);
+  const bool ok = mbar_wait<CLUSTER>(bar, parity, abort, hdr, where);
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -595,6 +607,10 @@ __device__ __forceinline__ void bulk_commit() {
 // Wait until every committed bulk group of this thread has finished READING shared memory.
 __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+// The same, but for the newest group.
+__device__ __forceinline__ void bulk_wait_read_but_one() {
+  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
 }
 // Wait until every committed bulk group of this thread has completed.
 __device__ __forceinline__ void bulk_wait_all() {

@@ -3,9 +3,10 @@
 //
 // tcgen05.mma kind::mxf4 over a CTA pair multiplies 256 rows x 256 columns x
 // 64 packed e2m1 elements and scales each group of 32 by its power of two,
-// which it reads from TMEM.  As for bf16 (grouped_tc.cu): a tile of 256 x 256,
+// which it reads from TMEM.  As for bf16 (grouped_tc.cu): tiles of 256 rows,
 // operands by TMA into a ring of stages of 128 bytes a row (256 elements),
-// half of the weights' rows in each CTA.
+// half of the weights' rows in each CTA.  A tile has up to 224 columns: an even
+// share of N in multiples of 32.
 //
 // Scales.  The four scale bytes of 128 columns of a row are one word, and a
 // TMEM column holds the words of 32 rows.  tcgen05.cp takes 32 x 16 bytes from
@@ -18,25 +19,34 @@
 // warps that copied every stage word by word with cp.async made the stages
 // follow each other at 2000 cycles, most of it the way of one stage's words.)
 //
-// TMEM: one accumulator of 256 columns (two would leave no room for scales)
-// and two stages of scales, 24 columns each.  The epilogue packs the
-// accumulator into registers and hands it back before it stores.
+// TMEM: two accumulators of up to 224 columns, so that the epilogue of a tile
+// runs under the products of the next, and two stages of scales, 24 columns
+// each.  (One accumulator of 256: the tensor cores wait 4000 cycles a tile for
+// the epilogue of both CTAs.)
+//
+// The MMA warp goes through its loop as a whole and issues from one lane, so
+// that descriptors stay in uniform registers: issued from a loop of one lane,
+// the eleven instructions of a stage take 950 cycles, twice the tensor cores'
+// time.
 #include "grouped.cuh"
 
 namespace mm {
 
 constexpr int kMtStages = 5;
-constexpr int kMtTile = 128 * 128;                    // 16 KiB: 128 rows x 256 elements
+constexpr int kMtMaxN = 224;                          // columns of a tile
+constexpr int kMtTileA = 128 * 128;                   // 16 KiB: 128 rows x 256 elements
+constexpr int kMtTileB = kMtMaxN / 2 * 128;
 constexpr int kMtSc = 2 * (128 + 256) * 4;            // scale words of a stage: of 128 rows and 256 columns, twice
-constexpr int kMtStageBytes = 2 * kMtTile + kMtSc;
+constexpr int kMtStageBytes = kMtTileA + kMtTileB + kMtSc;
 constexpr int kMtEpiWarps = 8;
 constexpr int kMtWarpProducer = kMtEpiWarps, kMtWarpMma = kMtEpiWarps + 1, kMtWarpScales = kMtEpiWarps + 2;
 constexpr int kMtScaleWarps = 4;
 constexpr int kMtThreads = 32 * (kMtEpiWarps + 2 + kMtScaleWarps);
-constexpr int kMtEpi = 32 * 128;
+constexpr int kMtEpi = 2 * 32 * 64;                   // per warp: two pieces of 32 rows x 32 columns
 constexpr int kMtSmem = kMtStages * kMtStageBytes + kMtEpiWarps * kMtEpi + 1024 + 256;
 static_assert(kMtSmem + sizeof(GmTables) + 64 <= 232448, "shared memory budget");
-constexpr uint32_t kMtScales = 256, kMtScaleCols = 24;   // TMEM: 8 columns of A's, 16 of B's
+constexpr uint32_t kMtScales = 2 * kMtMaxN, kMtScaleCols = 24;   // TMEM: 8 columns of A's, 16 of B's
+static_assert(kMtScales + 2 * kMtScaleCols <= 512, "TMEM columns");
 
 struct MtParams {
   CUtensorMap a, b, out;
@@ -44,6 +54,7 @@ struct MtParams {
   const uint8_t* a_sc;      // [words, rows, 4]
   const uint8_t* b_sc;      // [words, E * N, 4]
   int N;                    // columns of the result
+  int nt;                   // columns of a tile, a multiple of 32
   int stages;               // stages of 256 elements
   int words;                // scale words of a row
   int out_aligned;
@@ -55,15 +66,15 @@ mx4_tc_kernel(const __grid_constant__ MtParams P, WsHeader* hdr) {
   extern __shared__ unsigned char smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint8_t* sA = smem;
-  uint8_t* sB = sA + kMtStages * kMtTile;
-  uint8_t* sEpi = sB + kMtStages * kMtTile;
+  uint8_t* sB = sA + kMtStages * kMtTileA;
+  uint8_t* sEpi = sB + kMtStages * kMtTileB;
   uint8_t* sSc = sEpi + kMtEpiWarps * kMtEpi;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sSc + kMtStages * kMtSc);
   uint64_t* full = bars;                   // [stages] even CTA: both CTAs' bytes and scales
   uint64_t* empty = bars + kMtStages;      // [stages] each CTA: released by the pair's MMAs
-  uint64_t* tfull = bars + 2 * kMtStages;  // each CTA: accumulator ready
-  uint64_t* tempty = tfull + 1;            // even CTA: both CTAs' epilogues have read it
-  uint64_t* drained = tempty + 1;          // even CTA: all MMAs finished
+  uint64_t* tfull = bars + 2 * kMtStages;  // [2] each CTA: accumulator ready
+  uint64_t* tempty = tfull + 2;            // [2] even CTA: both CTAs' epilogues have read it
+  uint64_t* drained = tempty + 2;          // even CTA: all MMAs finished
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ GmTables s_tab;
@@ -71,15 +82,17 @@ mx4_tc_kernel(const __grid_constant__ MtParams P, WsHeader* hdr) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
   const int cluster = blockIdx.x >> 1, nc = gridDim.x >> 1;
-  const int ntn = (P.N + 255) / 256;
+  const int ntn = (P.N + P.nt - 1) / P.nt;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMtStages; ++s) {
       mbar_init(&full[s], 1 + 2);          // the bytes, and each CTA's scales
       mbar_init(&empty[s], 1);
     }
-    mbar_init(tfull, 1);
-    mbar_init(tempty, 2 * kMtEpiWarps);
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 2 * kMtEpiWarps);
+    }
     mbar_init(drained, 1);
     fence_mbar_init();
     s_abort = 0;
@@ -107,15 +120,15 @@ mx4_tc_kernel(const __grid_constant__ MtParams P, WsHeader* hdr) {
       int it = 0;
       bool ok = true;
       for (int tile = cluster; ok && tile < total; tile += nc) {
-        const GmTile ti = gm_tile<kGroupedForward>(tile, P.g.E, 0, 0, s_tab, ntn, 256, rank);
+        const GmTile ti = gm_tile<kGroupedForward>(tile, P.g.E, 0, 0, s_tab, ntn, P.nt, rank);
         for (int kb = 0; kb < P.stages; ++kb, ++it) {
           const int s = it % kMtStages;
           const uint32_t ph = (it / kMtStages) & 1;
           if (!mbar_wait(&empty[s], ph ^ 1, abort, hdr, 121)) { ok = false; break; }
           const uint32_t fb = mapa_shared(smem_u32(&full[s]), 0);
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 4 * kMtTile);
-          tma_load_2d_cta2(sA + s * kMtTile, &P.a, fb, kb * 128, ti.m0);
-          tma_load_3d_cta2(sB + s * kMtTile, &P.b, fb, kb * 128, ti.n0 + 128 * rank, ti.e);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kMtTileA + P.nt * 128);
+          tma_load_2d_cta2(sA + s * kMtTileA, &P.a, fb, kb * 128, ti.m0);
+          tma_load_3d_cta2(sB + s * kMtTileB, &P.b, fb, kb * 128, ti.n0 + P.nt / 2 * rank, ti.e);
         }
       }
       if (!ok && rank == 0) {
@@ -138,7 +151,7 @@ mx4_tc_kernel(const __grid_constant__ MtParams P, WsHeader* hdr) {
     GmTile ti;
     for (int it = warp - kMtWarpScales; it < mine; it += kMtScaleWarps) {
       const int nth = it / P.stages, kb = it - nth * P.stages;
-      if (nth != have) ti = gm_tile<kGroupedForward>(cluster + nth * nc, P.g.E, 0, 0, s_tab, ntn, 256, rank);
+      if (nth != have) ti = gm_tile<kGroupedForward>(cluster + nth * nc, P.g.E, 0, 0, s_tab, ntn, P.nt, rank);
       have = nth;
       // a lane's words of rows lane, + 32, + 64, + 96 of each 128; where there is
       // nothing, zeros: 2^-127, which scales zeros or rows that are not stored
@@ -171,71 +184,115 @@ mx4_tc_kernel(const __grid_constant__ MtParams P, WsHeader* hdr) {
     __syncwarp();
   } else if (warp == kMtWarpMma) {
     // ------------------------------------------------ MMA (even CTA)
-    if (rank == 0 && lane == 0) {
-      int it = 0, used = 0;
+    if (rank == 0) {
+      const bool leader = elect_one();
+      const int tiles = __shfl_sync(0xffffffffu, total, 0);
+      const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t id0 = idesc_mxf4(256, 0, 0) | (static_cast<uint32_t>(P.nt >> 3) << 17);
+      const uint32_t id2 = idesc_mxf4(256, 0, 2) | (static_cast<uint32_t>(P.nt >> 3) << 17);
+      const uint64_t da = smem_desc_sw128(smem_u32(sA)), db = smem_desc_sw128(smem_u32(sB));
+      const uint64_t ds = smem_desc_rows16(smem_u32(sSc));
+      int s = 0, used = 0;
+      uint32_t ph = 0, sc = base + kMtScales;
       bool ok = true;
-      for (int tile = cluster; ok && tile < total; tile += nc, ++used) {
-        if (!mbar_wait(tempty, (used & 1) ^ 1, abort, hdr, 124)) { ok = false; break; }
-        tc_fence_after();
-        for (int kb = 0; kb < P.stages; ++kb, ++it) {
-          const int s = it % kMtStages;
-          const uint32_t ph = (it / kMtStages) & 1;
-          if (!mbar_wait<true>(&full[s], ph, abort, hdr, 125)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t sc = smem_u32(sSc + s * kMtSc);
-          const uint32_t ta = tmem + kMtScales + (it & 1) * kMtScaleCols, tb = ta + 8;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            tmem_cp_scales_cta2(ta + 4 * c, smem_desc_rows16(sc + 1536 * c));
-            tmem_cp_scales_cta2(tb + 8 * c, smem_desc_rows16(sc + 1536 * c + 512));
-            tmem_cp_scales_cta2(tb + 8 * c + 4, smem_desc_rows16(sc + 1536 * c + 1024));
-          }
-          const uint32_t a0 = smem_u32(sA + s * kMtTile), b0 = smem_u32(sB + s * kMtTile);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_mxf4_cta2(tmem, smem_desc_sw128(a0 + kk * 32), smem_desc_sw128(b0 + kk * 32),
-                           idesc_mxf4(256, 256, 2 * (kk & 1)), ta + 4 * (kk >> 1), tb + 8 * (kk >> 1), (kb | kk) ? 1u : 0u);
-          umma_commit_cta2_mc(&empty[s], 0x3);
-        }
+      for (int tile = cluster; ok && tile < tiles; tile += nc, ++used) {
+        ok = warp_wait(&tempty[used & 1], ((used >> 1) & 1) ^ 1, abort, hdr, 124);
         if (!ok) break;
-        umma_commit_cta2_mc(tfull, 0x3);
+        tc_fence_after();
+        const uint32_t d = base + (used & 1) * kMtMaxN;
+        for (int kb = 0; kb < P.stages; ++kb) {
+          ok = warp_wait<true>(&full[s], ph, abort, hdr, 125);
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            const uint64_t dss = ds + static_cast<uint64_t>(s * (kMtSc / 16));
+            const uint64_t das = da + static_cast<uint64_t>(s * (kMtTileA / 16));
+            const uint64_t dbs = db + static_cast<uint64_t>(s * (kMtTileB / 16));
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              tmem_cp_scales_cta2(sc + 4 * c, dss + 96 * c);
+              tmem_cp_scales_cta2(sc + 8 + 8 * c, dss + 96 * c + 32);
+              tmem_cp_scales_cta2(sc + 8 + 8 * c + 4, dss + 96 * c + 64);
+            }
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_mxf4_cta2(d, das + 2 * kk, dbs + 2 * kk, (kk & 1) ? id2 : id0, sc + 4 * (kk >> 1), sc + 8 + 8 * (kk >> 1),
+                             (kb | kk) ? 1u : 0u);
+            umma_commit_cta2_mc(&empty[s], 0x3);
+            if (kb + 1 == P.stages) umma_commit_cta2_mc(&tfull[used & 1], 0x3);
+          }
+          __syncwarp();
+          sc ^= (base + kMtScales) ^ (base + kMtScales + kMtScaleCols);
+          if (++s == kMtStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
       }
-      umma_commit_cta2_mc(drained, 0x1);
-      mbar_wait(drained, 0, nullptr, hdr, 126);
+      if (leader) umma_commit_cta2_mc(drained, 0x1);
+      __syncwarp();
+      warp_wait(drained, 0, nullptr, hdr, 126);
     }
     __syncwarp();
   } else {
     // ------------------------------------------------ epilogue (warps 0-7, both CTAs)
     const int quad = warp & 3, half = warp >> 2;
     uint8_t* wstage = sEpi + warp * kMtEpi;
-    const uint32_t te = mapa_shared(smem_u32(tempty), 0);
-    int used = 0;
+    const uint32_t te0 = mapa_shared(smem_u32(&tempty[0]), 0), te1 = mapa_shared(smem_u32(&tempty[1]), 0);
+    int used = 0, piece = 0;
     for (int tile = cluster; tile < total; tile += nc, ++used) {
-      const GmTile ti = gm_tile<kGroupedForward>(tile, P.g.E, 0, 0, s_tab, ntn, 256, rank);
-      if (!warp_wait(tfull, used & 1, abort, hdr, 127)) break;
+      const GmTile ti = gm_tile<kGroupedForward>(tile, P.g.E, 0, 0, s_tab, ntn, P.nt, rank);
+      if (!warp_wait(&tfull[used & 1], (used >> 1) & 1, abort, hdr, 127)) break;
       tc_fence_after();
       const int rem = min(32, ti.mrows - quad * 32);            // rows of the group in this warp's 32
       const bool counts = quad * 32 + lane < ti.mvalid;         // this lane's row is not padding
-      const uint32_t tb = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 128;
-      uint32_t pk[2][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      const uint32_t tb = tmem + (static_cast<uint32_t>(quad * 32) << 16) + (used & 1) * kMtMaxN;
+      const int row = ti.m0 + quad * 32;
+      // pieces of 32 columns, every other one
+#pragma unroll 1
+      for (int c = 32 * half; c < P.nt; c += 64) {
         uint32_t r[32];
-        tmem_ld_32x32b_x32(tb + 32 * c, r);
+        tmem_ld_32x32b_x32(tb + c, r);             // every lane (warp-collective)
         tmem_ld_wait();
+        const int col = ti.n0 + c;
+        if (rem <= 0 || col >= P.N) continue;      // warp-uniform
+        uint32_t pk[16];
 #pragma unroll
         for (int q = 0; q < 16; ++q)
-          pk[c >> 1][16 * (c & 1) + q] = counts ? pack_bf16x2(__uint_as_float(r[2 * q]), __uint_as_float(r[2 * q + 1])) : 0u;
+          pk[q] = counts ? pack_bf16x2(__uint_as_float(r[2 * q]), __uint_as_float(r[2 * q + 1])) : 0u;
+        uint8_t* stage = wstage + (piece++ & 1) * (kMtEpi / 2);
+        if (lane == 0) bulk_wait_read_but_one();   // the store before the last has read this half
+        __syncwarp();
+        // 64-byte rows, 16-byte chunk q of row i at chunk q ^ ((i >> 1) & 3)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint4*>(stage + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
+              make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+        if (P.out_aligned && rem == 32) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tma_store_2d(&P.out, stage, col, row);
+        } else {
+          __syncwarp();
+          uint16_t* o = static_cast<uint16_t*>(P.outp) + static_cast<int64_t>(row) * P.N + col;
+          if (P.out_aligned) {
+            // a group's ragged end: 16 bytes a lane, eight rows at once
+            if (col + 8 * (lane & 3) < P.N)
+              for (int i = lane >> 2; i < rem; i += 8)
+                *reinterpret_cast<uint4*>(o + static_cast<int64_t>(i) * P.N + 8 * (lane & 3)) =
+                    *reinterpret_cast<const uint4*>(stage + i * 64 + (((lane & 3) ^ ((i >> 1) & 3)) << 4));
+          } else if (col + lane < P.N) {
+            // rows that start anywhere: element by element
+            for (int i = 0; i < rem; ++i)
+              o[static_cast<int64_t>(i) * P.N + lane] =
+                  *reinterpret_cast<const uint16_t*>(stage + i * 64 + ((((lane >> 3) ^ ((i >> 1) & 3)) << 4) | ((lane & 7) << 1)));
+          }
+        }
+        if (lane == 0) bulk_commit();              // one group a piece, with or without a store in it
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(te);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int col = ti.n0 + half * 128 + 64 * c;
-        if (rem > 0 && col < P.N)
-          store_rows_bf16(pk[c], wstage, &P.out, P.outp, P.out_aligned, ti.m0 + quad * 32, col, rem, P.N, lane);
-      }
+      if (lane == 0) mbar_arrive_cluster((used & 1) ? te1 : te0);
     }
     if (lane == 0) bulk_wait_all();   // this warp's tensor stores have landed
   }
@@ -263,13 +320,16 @@ cudaError_t launch_mx4_tc(const Mx4MatmulArgs& a, WsHeader* hdr, cudaStream_t st
   const uint64_t row = 16 * static_cast<uint64_t>(groups);
   const uint64_t da[2] = {row, static_cast<uint64_t>(a.g.rows)}, sa[1] = {row};
   const uint64_t db[3] = {row, static_cast<uint64_t>(a.N), static_cast<uint64_t>(a.g.E)}, sb[2] = {row, row * a.N};
-  const uint32_t box[3] = {128, 128, 1};
+  // an even share of the columns
+  const int ntn = (a.N + kMtMaxN - 1) / kMtMaxN;
+  p.nt = ((a.N + ntn - 1) / ntn + 31) / 32 * 32;
+  const uint32_t boxa[2] = {128, 128}, boxb[3] = {128, static_cast<uint32_t>(p.nt / 2), 1};
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  if (!make_map(&p.a, u8, 2, reinterpret_cast<uint64_t>(a.x), da, sa, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_map(&p.b, u8, 3, reinterpret_cast<uint64_t>(a.w), db, sb, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      (p.out_aligned && !map_out_rows(&p.out, a.out, a.N, a.g.rows)))
+  if (!make_map(&p.a, u8, 2, reinterpret_cast<uint64_t>(a.x), da, sa, boxa, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&p.b, u8, 3, reinterpret_cast<uint64_t>(a.w), db, sb, boxb, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      (p.out_aligned && !map_out_rows(&p.out, a.out, a.N, a.g.rows, 32)))
     return cudaErrorInvalidValue;
-  const int64_t tiles = row_tiles256(a.g) * ((a.N + 255) / 256);
+  const int64_t tiles = row_tiles256(a.g) * ntn;
   if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(mx4_tc_kernel), kMtSmem);
   if (e != cudaSuccess) return e;
