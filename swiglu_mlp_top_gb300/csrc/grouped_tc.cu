@@ -284,7 +284,7 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(acc ? te1 : te0);
+          if (lane == 0) mbar_signal_cluster(acc ? te1 : te0);
         }
         if (!ok) break;
 #pragma unroll
@@ -331,7 +331,7 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
           if (c == 64) {                           // the accumulator is read: the next tile may have it
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(acc ? te1 : te0);
+            if (lane == 0) mbar_signal_cluster(acc ? te1 : te0);
           }
           if (rem <= 0 || col0 + c >= P.N) continue;            // warp-uniform
           uint32_t pk[32];

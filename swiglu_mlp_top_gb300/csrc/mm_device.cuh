@@ -498,6 +498,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
+// The same for a signal that orders no memory of this CTA for the other one
+// (an accumulator has been read, after tcgen05.wait::ld and the fence before a
+// thread sync): a release over the cluster waits for this thread's earlier
+// writes, 2000 cycles behind an epilogue's stores.
+__device__ __forceinline__ void mbar_signal_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 // 2-D tiled TMA load into this CTA's shared memory whose completion is
 // signalled on an mbarrier that may live in the peer CTA of the pair.
 __device__ __forceinline__ void tma_load_2d_cta2(void* smem_dst, const void* tmap,
@@ -607,10 +614,6 @@ __device__ __forceinline__ void bulk_commit() {
 // Wait until every committed bulk group of this thread has finished READING shared memory.
 __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-// The same, but for the newest group.
-__device__ __forceinline__ void bulk_wait_read_but_one() {
-  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
 }
 // Wait until every committed bulk group of this thread has completed.
 __device__ __forceinline__ void bulk_wait_all() {

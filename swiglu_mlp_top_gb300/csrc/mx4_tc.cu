@@ -239,7 +239,7 @@ mx4_tc_kernel(const __grid_constant__ MtParams P, WsHeader* hdr) {
     const int quad = warp & 3, half = warp >> 2;
     uint8_t* wstage = sEpi + warp * kMtEpi;
     const uint32_t te0 = mapa_shared(smem_u32(&tempty[0]), 0), te1 = mapa_shared(smem_u32(&tempty[1]), 0);
-    int used = 0, piece = 0;
+    int used = 0;
     for (int tile = cluster; tile < total; tile += nc, ++used) {
       const GmTile ti = gm_tile<kGroupedForward>(tile, P.g.E, 0, 0, s_tab, ntn, P.nt, rank);
       if (!warp_wait(&tfull[used & 1], (used >> 1) & 1, abort, hdr, 127)) break;
@@ -248,32 +248,51 @@ mx4_tc_kernel(const __grid_constant__ MtParams P, WsHeader* hdr) {
       const bool counts = quad * 32 + lane < ti.mvalid;         // this lane's row is not padding
       const uint32_t tb = tmem + (static_cast<uint32_t>(quad * 32) << 16) + (used & 1) * kMtMaxN;
       const int row = ti.m0 + quad * 32;
-      // pieces of 32 columns, every other one
-#pragma unroll 1
-      for (int c = 32 * half; c < P.nt; c += 64) {
+      // every other piece of 32 columns, packed, so that the accumulator is free before the stores
+      uint32_t pk[4][16];
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const int c = 32 * half + 64 * p;
+        if (c >= P.nt) continue;                   // warp-uniform
         uint32_t r[32];
         tmem_ld_32x32b_x32(tb + c, r);             // every lane (warp-collective)
         tmem_ld_wait();
-        const int col = ti.n0 + c;
-        if (rem <= 0 || col >= P.N) continue;      // warp-uniform
-        uint32_t pk[16];
 #pragma unroll
         for (int q = 0; q < 16; ++q)
-          pk[q] = counts ? pack_bf16x2(__uint_as_float(r[2 * q]), __uint_as_float(r[2 * q + 1])) : 0u;
-        uint8_t* stage = wstage + (piece++ & 1) * (kMtEpi / 2);
-        if (lane == 0) bulk_wait_read_but_one();   // the store before the last has read this half
+          pk[p][q] = counts ? pack_bf16x2(__uint_as_float(r[2 * q]), __uint_as_float(r[2 * q + 1])) : 0u;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_signal_cluster((used & 1) ? te1 : te0);
+      if (rem <= 0) continue;                      // warp-uniform
+#pragma unroll
+      for (int b = 0; b < 4; b += 2) {
+        const int c0 = ti.n0 + 32 * half + 64 * b; // two pieces at once: columns c0 and c0 + 64
+        if (32 * half + 64 * b >= P.nt || c0 >= P.N) break;
+        const bool two = 32 * half + 64 * b + 64 < P.nt && c0 + 64 < P.N;
+        if (lane == 0) bulk_wait_read();           // the stores before have read the stage
         __syncwarp();
         // 64-byte rows, 16-byte chunk q of row i at chunk q ^ ((i >> 1) & 3)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<uint4*>(stage + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
-              make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<uint4*>(wstage + p * (kMtEpi / 2) + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
+                make_uint4(pk[b + p][4 * q], pk[b + p][4 * q + 1], pk[b + p][4 * q + 2], pk[b + p][4 * q + 3]);
         if (P.out_aligned && rem == 32) {
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) tma_store_2d(&P.out, stage, col, row);
-        } else {
-          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&P.out, wstage, c0, row);
+            if (two) tma_store_2d(&P.out, wstage + kMtEpi / 2, c0 + 64, row);
+            bulk_commit();
+          }
+          continue;
+        }
+        __syncwarp();
+        for (int p = 0; p < 1 + two; ++p) {
+          const uint8_t* stage = wstage + p * (kMtEpi / 2);
+          const int col = c0 + 64 * p;
           uint16_t* o = static_cast<uint16_t*>(P.outp) + static_cast<int64_t>(row) * P.N + col;
           if (P.out_aligned) {
             // a group's ragged end: 16 bytes a lane, eight rows at once
@@ -288,11 +307,8 @@ mx4_tc_kernel(const __grid_constant__ MtParams P, WsHeader* hdr) {
                   *reinterpret_cast<const uint16_t*>(stage + i * 64 + ((((lane >> 3) ^ ((i >> 1) & 3)) << 4) | ((lane & 7) << 1)));
           }
         }
-        if (lane == 0) bulk_commit();              // one group a piece, with or without a store in it
+        __syncwarp();
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster((used & 1) ? te1 : te0);
     }
     if (lane == 0) bulk_wait_all();   // this warp's tensor stores have landed
   }
