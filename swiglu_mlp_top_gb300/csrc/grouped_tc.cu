@@ -128,7 +128,7 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
           if (rows >= 64) {
             if (lane == 0) {
               if (rank == 0) mbar_arrive_expect_tx(&full[s], 4 * kGmTile);
-              else mbar_arrive_cluster(fb);
+              else mbar_signal_cluster(fb);
               if (P.a_blocks) {
                 tma_load_3d_cta2(a, &P.a, fb, 0, krow, ti.m0 / 64);
               } else {
