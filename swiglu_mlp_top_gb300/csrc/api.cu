@@ -1187,8 +1187,12 @@ static cudaError_t repitched(const void** p, char* to, int64_t rows, int cols, c
   *p = to;
   return counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_repitch(src, to, rows, cols, st); });
 }
+// Few rows, which start on 16 bytes, go to the kernel that streams the weights.
+constexpr int64_t kStreamRows = 256;
+static bool grouped_streams(int64_t rows, int K) { return rows <= kStreamRows && K % 8 == 0; }
 static cudaError_t grouped_launch(int dtype, int op, const GroupedArgs& a, void* status_ws, cudaStream_t st) {
   return counted_launch(MM_KERNEL_GROUPED, st, [&] {
+    if (dtype == kDtypeBF16 && op == kGroupedForward && grouped_streams(a.g.rows, a.K)) return launch_grouped_stream(a, st);
     return dtype == kDtypeBF16 ? launch_grouped_tc(op, a, static_cast<WsHeader*>(status_ws), st)
                                : launch_grouped_simt(dtype, op, a, st);
   });
@@ -1289,7 +1293,7 @@ struct Mx4Layout {
 };
 static Mx4Layout mx4_layout(int64_t rows, int K, int N, int E, bool four) {
   Mx4Layout L{0, 0, 0};
-  if (four) return L;
+  if (four || grouped_streams(rows, K)) return L;
   L.product = align_up(2 * static_cast<size_t>(E) * N * K);
   L.total = L.product + grouped_bytes(rows, K, N, E, kDtypeBF16, false);
   return L;
@@ -1311,10 +1315,12 @@ int mm_mx4_matmul(const void* x, const uint8_t* x_exps, const void* w_codes, con
     return MM_ERR_INVALID_ARG;
   const Mx4Layout L = mx4_layout(rows, K, N, E, x_exps != nullptr);
   if (L.total > 0 && (!present16(workspace) || workspace_bytes < L.total)) return MM_ERR_WORKSPACE;
-  if (x_exps != nullptr) {
+  if (x_exps != nullptr || grouped_streams(rows, K)) {
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const Mx4MatmulArgs a{x, x_exps, w_codes, w_exps, ys, GroupTables{offsets, counts, rows, E}, K, N};
-    cudaError_t e = counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_mx4_tc(a, static_cast<WsHeader*>(status_ws), st); });
+    cudaError_t e = counted_launch(MM_KERNEL_GROUPED, st, [&] {
+      return x_exps ? launch_mx4_tc(a, static_cast<WsHeader*>(status_ws), st) : launch_mx4_stream(a, st);
+    });
     return e == cudaSuccess ? MM_OK : cuda_fail(e, "mx4 matmul");
   }
   const int rc = mx4_impl(false, nullptr, ws_at(workspace, L.w), const_cast<void*>(w_codes), const_cast<uint8_t*>(w_exps),

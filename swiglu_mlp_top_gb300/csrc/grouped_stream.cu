@@ -1,0 +1,247 @@
+// Experts' products for few rows: ys[r, n] = sum_k x[r, k] w[e, n, k] with bf16
+// rows and weights in bf16 or in 4 bits.  Bound by reading each needed weight
+// row once, and below some ten MB by the latency of doing so.
+//
+// A block takes 16 rows of w (output columns) of one expert and up to 32 of
+// its rows of x; its four warps share out the summed index in steps of 32
+// (4 bits: 128) columns.  A warp multiplies with mma.sync m16n8k16, the
+// weights as the M operand straight from global memory: the order of the
+// summed index is free as long as both operands use the same, so a lane takes
+// 16 contiguous bytes of a weight row, which are 8 values (4 bits: a whole
+// group of 32 and its scale), and the same columns of x.  All loads of a few
+// steps are in flight before the first product.  (The tensor cores of
+// tcgen05 want their operands in shared memory and tiles of 128 rows: for
+// these shapes a longer way to the same bytes.)
+//
+// 4 bits to bf16: with a nibble's sign at bit 15 and its exponent and fraction
+// at bits 8..6, the bf16 is the value times 2^-126, subnormals included; one
+// multiplication by 2^(126 + e) makes it the value times its scale, exactly.
+#include "grouped.cuh"
+
+namespace mm {
+
+constexpr int kGsWarps = 4, kGsThreads = 32 * kGsWarps;
+constexpr int kGsRows = 16;                  // rows of w per block
+
+struct GsParams {
+  const __nv_bfloat16* x;   // [rows, K], K a multiple of 8
+  const uint8_t* w;         // bf16 [E, N, K], or codes [E * N, 16 G]
+  const uint32_t* sc;       // scale words [words, E * N]
+  __nv_bfloat16* out;       // [rows, N]
+  GroupTables g;
+  int K, N;
+};
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Eight values of a word of codes times the scale, as four pairs of bf16.
+// TWO: 2^126 (0x7e80) and the scale apart, where their product overflows.
+template <bool TWO>
+__device__ __forceinline__ uint4 e2m1_bf16(uint32_t codes, uint32_t f1, uint32_t f2) {
+  const uint32_t even = codes & 0x0f0f0f0fu, odd = (codes >> 4) & 0x0f0f0f0fu;
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // nibbles 2i and 2i + 1 in the two halves (selector bit 3: the sign of a byte below 16, zero)
+    uint32_t p;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(p) : "r"(even), "r"(odd), "r"(0x8080 | i | (4 + i) << 8));
+    v[i] = bf16x2_mul((p * 0x1040u) & 0x81c081c0u, f1);
+    if constexpr (TWO) v[i] = bf16x2_mul(v[i], f2);
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+template <bool MX4, int NT>
+struct GsTraits {
+  static constexpr int kParts = MX4 ? 4 : 1;                 // 8-column pieces of a lane's step
+  static constexpr int kCols = 32 * kParts;                  // columns of a step
+  // steps in flight: as many as registers hold beside the pieces of x
+  static constexpr int kUnroll = MX4 ? (NT == 1 ? 2 : 1) : (NT == 1 ? 6 : NT == 2 ? 4 : 2);
+};
+
+// A warp's share of 16 rows of w times NT * 8 rows of x.
+template <bool MX4, int NT>
+__device__ __forceinline__ void gs_sum(const GsParams& P, int64_t wrow, int wlast, const __nv_bfloat16* x, int rows,
+                                       float (&acc)[NT][4]) {
+  typedef GsTraits<MX4, NT> Tr;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int steps = (P.K + Tr::kCols - 1) / Tr::kCols;
+  const int groups = (P.K + 31) / 32;
+  const int64_t pitch = MX4 ? 16 * static_cast<int64_t>(groups) : 2 * static_cast<int64_t>(P.K);     // bytes of a weight row
+  // rows of w behind the last one are read as the last one, and not stored
+  const int64_t r0 = wrow + min(g, wlast), r1 = wrow + min(g + 8, wlast);
+  const uint8_t *w0 = P.w + r0 * pitch + 16 * t, *w1 = P.w + r1 * pitch + 16 * t;
+  const int64_t srows = static_cast<int64_t>(P.g.E) * P.N;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  for (int s0 = warp; s0 < steps; s0 += kGsWarps * Tr::kUnroll) {
+    uint4 a[Tr::kUnroll][2], b[Tr::kUnroll][Tr::kParts][NT];
+    uint32_t sw[Tr::kUnroll][2];
+#pragma unroll
+    for (int u = 0; u < Tr::kUnroll; ++u) {
+      const int s = s0 + u * kGsWarps;
+      const int k = s * Tr::kCols + 8 * Tr::kParts * t;      // this lane's first column
+      const bool in = s < steps && k < P.K;
+      a[u][0] = in ? __ldg(reinterpret_cast<const uint4*>(w0 + 64 * static_cast<int64_t>(s))) : zero;
+      a[u][1] = in ? __ldg(reinterpret_cast<const uint4*>(w1 + 64 * static_cast<int64_t>(s))) : zero;
+      if constexpr (MX4) {
+        sw[u][0] = in ? __ldg(P.sc + s * srows + r0) : 0u;
+        sw[u][1] = in ? __ldg(P.sc + s * srows + r1) : 0u;
+      }
+#pragma unroll
+      for (int q = 0; q < Tr::kParts; ++q)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          b[u][q][j] = s < steps && k + 8 * q < P.K && 8 * j + g < rows
+                           ? __ldg(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(8 * j + g) * P.K + k + 8 * q))
+                           : zero;
+    }
+#pragma unroll
+    for (int u = 0; u < Tr::kUnroll; ++u) {
+      if (s0 + u * kGsWarps >= steps) break;                 // warp-uniform
+      uint32_t f[2][2];
+      bool two = false;
+      if constexpr (MX4) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t byte = (sw[u][i] >> (8 * t)) & 255u;
+          // 2^126 * 2^(byte - 127) in bf16; 255 stands for NaN, 0 is 2^-127
+          f[i][0] = byte <= 128u ? (byte + 126u) << 7 : 0x7e80u;
+          f[i][1] = byte == 255u ? 0x7fffu : byte <= 128u ? 0x3f80u : byte << 7;
+          f[i][0] |= f[i][0] << 16;
+          f[i][1] |= f[i][1] << 16;
+          two |= byte > 128u;
+        }
+        two = __any_sync(0xffffffffu, two);
+      }
+#pragma unroll
+      for (int q = 0; q < Tr::kParts; ++q) {
+        uint4 v0 = a[u][0], v1 = a[u][1];
+        if constexpr (MX4) {
+          const uint32_t c0 = q == 0 ? a[u][0].x : q == 1 ? a[u][0].y : q == 2 ? a[u][0].z : a[u][0].w;
+          const uint32_t c1 = q == 0 ? a[u][1].x : q == 1 ? a[u][1].y : q == 2 ? a[u][1].z : a[u][1].w;
+          v0 = two ? e2m1_bf16<true>(c0, f[0][0], f[0][1]) : e2m1_bf16<false>(c0, f[0][0], 0u);
+          v1 = two ? e2m1_bf16<true>(c1, f[1][0], f[1][1]) : e2m1_bf16<false>(c1, f[1][0], 0u);
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          mma_bf16(acc[j], v0.x, v1.x, v0.y, v1.y, b[u][q][j].x, b[u][q][j].y);
+          mma_bf16(acc[j], v0.z, v1.z, v0.w, v1.w, b[u][q][j].z, b[u][q][j].w);
+        }
+      }
+    }
+  }
+}
+
+// 16 columns of `rows` rows (at most 8 NT): the warps' sums joined in warp order.
+template <bool MX4, int NT>
+__device__ __forceinline__ void gs_rows(const GsParams& P, int e, int n0, int64_t row0, int rows, float* s_part) {
+  float acc[NT][4];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+  gs_sum<MX4, NT>(P, static_cast<int64_t>(e) * P.N + n0, P.N - 1 - n0, P.x + row0 * P.K, rows, acc);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  __syncthreads();                             // the last use of s_part is over
+  // [warp][row of x][row of w]
+  float* mine = s_part + warp * (32 * kGsRows);
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mine[(8 * j + 2 * t + (i & 1)) * kGsRows + g + 8 * (i >> 1)] = acc[j][i];
+  __syncthreads();
+  for (int v = threadIdx.x; v < rows * (kGsRows / 2); v += kGsThreads) {
+    const int r = v / (kGsRows / 2), c = 2 * (v % (kGsRows / 2));
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kGsWarps; ++w) {
+      const float2 p = *reinterpret_cast<const float2*>(s_part + w * (32 * kGsRows) + r * kGsRows + c);
+      sum.x += p.x;
+      sum.y += p.y;
+    }
+    __nv_bfloat16* o = P.out + (row0 + r) * P.N + n0 + c;
+    if (P.N % 2 == 0) {
+      if (n0 + c < P.N) *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(sum.x, sum.y);
+    } else {
+      if (n0 + c < P.N) o[0] = __float2bfloat16_rn(sum.x);
+      if (n0 + c + 1 < P.N) o[1] = __float2bfloat16_rn(sum.y);
+    }
+  }
+}
+
+template <bool MX4>
+__global__ void __launch_bounds__(kGsThreads, 4)
+grouped_stream_kernel(const GsParams P) {
+  __shared__ __align__(16) float s_part[kGsWarps * 32 * kGsRows];
+  __shared__ GroupSpan s_span[MM_MAX_EXPERTS];
+  __shared__ int s_group[MM_MAX_EXPERTS];      // the groups that have rows
+  __shared__ int s_count;
+  pdl_enter();
+  if (threadIdx.x < 32) {
+    int count = 0;
+    for (int e0 = 0; e0 < P.g.E; e0 += 32) {
+      const int e = e0 + threadIdx.x;
+      const GroupSpan s = e < P.g.E ? group_span(P.g, e) : GroupSpan{0, 0, 0};
+      const uint32_t has = __ballot_sync(0xffffffffu, s.r1 > s.r0);
+      if (s.r1 > s.r0) {
+        const int at = count + __popc(has & ((1u << threadIdx.x) - 1u));
+        s_group[at] = e;
+        s_span[at] = s;
+      }
+      count += __popc(has);
+    }
+    if (threadIdx.x == 0) s_count = count;
+  }
+  __syncthreads();
+  const int tiles = (P.N + kGsRows - 1) / kGsRows;
+  const int64_t units = static_cast<int64_t>(s_count) * tiles;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int i = static_cast<int>(u / tiles), n0 = static_cast<int>(u % tiles) * kGsRows;
+    const GroupSpan s = s_span[i];
+    const int e = s_group[i];
+    for (int r = 0; r < s.n; r += 32) {
+      const int rows = min(32, s.n - r);
+      const int64_t row0 = s.r0 + r;
+      if (rows <= 8) gs_rows<MX4, 1>(P, e, n0, row0, rows, s_part);
+      else if (rows <= 16) gs_rows<MX4, 2>(P, e, n0, row0, rows, s_part);
+      else gs_rows<MX4, 4>(P, e, n0, row0, rows, s_part);
+    }
+    // padding rows of the group
+    const int cols = min(kGsRows, P.N - n0);
+    for (int v = threadIdx.x; v < (s.r1 - s.r0 - s.n) * kGsRows; v += kGsThreads)
+      if (v % kGsRows < cols)
+        P.out[(static_cast<int64_t>(s.r0) + s.n + v / kGsRows) * P.N + n0 + v % kGsRows] = __float2bfloat16_rn(0.f);
+  }
+}
+
+template <bool MX4>
+static cudaError_t gs_launch(const GsParams& p, cudaStream_t st) {
+  const int64_t units = std::min<int64_t>(p.g.E, p.g.rows) * ((p.N + kGsRows - 1) / kGsRows);
+  const int64_t most = static_cast<int64_t>(num_sms()) * resident_blocks(reinterpret_cast<const void*>(grouped_stream_kernel<MX4>), kGsThreads);
+  return launch_dependent_kernel(grouped_stream_kernel<MX4>, dim3(static_cast<unsigned>(std::min(units, most))),
+                                 dim3(kGsThreads), 0, st, p);
+}
+
+cudaError_t launch_grouped_stream(const GroupedArgs& a, cudaStream_t st) {
+  return gs_launch<false>(GsParams{static_cast<const __nv_bfloat16*>(a.xs), static_cast<const uint8_t*>(a.w), nullptr,
+                                   static_cast<__nv_bfloat16*>(a.out), a.g, a.K, a.N}, st);
+}
+cudaError_t launch_mx4_stream(const Mx4MatmulArgs& a, cudaStream_t st) {
+  return gs_launch<true>(GsParams{static_cast<const __nv_bfloat16*>(a.x), static_cast<const uint8_t*>(a.w),
+                                  reinterpret_cast<const uint32_t*>(a.w_exps), static_cast<__nv_bfloat16*>(a.out), a.g,
+                                  a.K, a.N}, st);
+}
+
+}  // namespace mm
