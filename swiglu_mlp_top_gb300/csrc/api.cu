@@ -1187,14 +1187,22 @@ static cudaError_t repitched(const void** p, char* to, int64_t rows, int cols, c
   *p = to;
   return counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_repitch(src, to, rows, cols, st); });
 }
-// Few rows, which start on 16 bytes, go to the kernel that streams the weights.
-constexpr int64_t kStreamRows = 256;
-static bool grouped_streams(int64_t rows, int K) { return rows <= kStreamRows && K % 8 == 0; }
+// Few rows, which start on 16 bytes, go to the kernel that streams the weights
+// (grouped_stream.cu).  Its time grows with the rows of an expert, the tiles'
+// with the weights: at E = 8, K = 768, N = 4864 and 32 rows 13.4 us against
+// 17.8 of the tiles, at 128 rows 19 against 15; at E = 64, K = 2048, N = 1024 and
+// 512 rows 50 against 54, at 1024 70 against 55; one matrix of 4096 x 4096 and 16
+// rows 10 against 26.  With weights in 4 bits the tiles need a bf16 copy of
+// the weights first: 128 rows 20 against 27, 256 29 against 27; E = 64, 1024
+// rows 66 against 119; one matrix, 64 rows 26 against 34, 128 57 against 34.
+static bool grouped_streams(int64_t rows, int K, int E, bool w_in_4_bits) {
+  return K % 8 == 0 && rows <= (w_in_4_bits ? 64 + 16 * E : 32 + 6 * E);
+}
 static cudaError_t grouped_launch(int dtype, int op, const GroupedArgs& a, void* status_ws, cudaStream_t st) {
   return counted_launch(MM_KERNEL_GROUPED, st, [&] {
-    if (dtype == kDtypeBF16 && op == kGroupedForward && grouped_streams(a.g.rows, a.K)) return launch_grouped_stream(a, st);
+    if (dtype == kDtypeBF16 && op == kGroupedForward && grouped_streams(a.g.rows, a.K, a.g.E, false)) return launch_grouped_stream(a, st);
     return dtype == kDtypeBF16 ? launch_grouped_tc(op, a, static_cast<WsHeader*>(status_ws), st)
-                               : launch_grouped_simt(dtype, op, a, st);
+                               : launch_grouped_simt(op, a, st);
   });
 }
 
@@ -1293,7 +1301,7 @@ struct Mx4Layout {
 };
 static Mx4Layout mx4_layout(int64_t rows, int K, int N, int E, bool four) {
   Mx4Layout L{0, 0, 0};
-  if (four || grouped_streams(rows, K)) return L;
+  if (four || grouped_streams(rows, K, E, true)) return L;
   L.product = align_up(2 * static_cast<size_t>(E) * N * K);
   L.total = L.product + grouped_bytes(rows, K, N, E, kDtypeBF16, false);
   return L;
@@ -1315,7 +1323,7 @@ int mm_mx4_matmul(const void* x, const uint8_t* x_exps, const void* w_codes, con
     return MM_ERR_INVALID_ARG;
   const Mx4Layout L = mx4_layout(rows, K, N, E, x_exps != nullptr);
   if (L.total > 0 && (!present16(workspace) || workspace_bytes < L.total)) return MM_ERR_WORKSPACE;
-  if (x_exps != nullptr || grouped_streams(rows, K)) {
+  if (x_exps != nullptr || grouped_streams(rows, K, E, true)) {
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const Mx4MatmulArgs a{x, x_exps, w_codes, w_exps, ys, GroupTables{offsets, counts, rows, E}, K, N};
     cudaError_t e = counted_launch(MM_KERNEL_GROUPED, st, [&] {

@@ -24,6 +24,24 @@ __device__ __forceinline__ GroupSpan group_span(const GroupTables& g, int e) {
   return s;
 }
 
+// The groups that have rows, in order; by the block's first warp.
+__device__ __forceinline__ void groups_with_rows(const GroupTables& g, GroupSpan* spans, int* groups, int* count) {
+  if (threadIdx.x >= 32) return;
+  int n = 0;
+  for (int e0 = 0; e0 < g.E; e0 += 32) {
+    const int e = e0 + threadIdx.x;
+    const GroupSpan s = e < g.E ? group_span(g, e) : GroupSpan{0, 0, 0};
+    const uint32_t has = __ballot_sync(0xffffffffu, s.r1 > s.r0);
+    if (s.r1 > s.r0) {
+      const int at = n + __popc(has & ((1u << threadIdx.x) - 1u));
+      groups[at] = e;
+      spans[at] = s;
+    }
+    n += __popc(has);
+  }
+  if (threadIdx.x == 0) *count = n;
+}
+
 // Where the tile with index t lies among tiles of `block` rows of every group
 // in order, `cols` tiles to a row of tiles.  Called by a full warp; every lane
 // gets the answer; e < 0: there is no such tile.

@@ -3,7 +3,7 @@
 // row once, and below some ten MB by the latency of doing so.
 //
 // A block takes 16 rows of w (output columns) of one expert and up to 32 of
-// its rows of x; its four warps share out the summed index in steps of 32
+// its rows of x; its four or eight warps share out the summed index in steps of 32
 // (4 bits: 128) columns.  A warp multiplies with mma.sync m16n8k16, the
 // weights as the M operand straight from global memory: the order of the
 // summed index is free as long as both operands use the same, so a lane takes
@@ -20,7 +20,6 @@
 
 namespace mm {
 
-constexpr int kGsWarps = 4, kGsThreads = 32 * kGsWarps;
 constexpr int kGsRows = 16;                  // rows of w per block
 
 struct GsParams {
@@ -71,7 +70,7 @@ struct GsTraits {
 };
 
 // A warp's share of 16 rows of w times NT * 8 rows of x.
-template <bool MX4, int NT>
+template <bool MX4, int WARPS, int NT>
 __device__ __forceinline__ void gs_sum(const GsParams& P, int64_t wrow, int wlast, const __nv_bfloat16* x, int rows,
                                        float (&acc)[NT][4]) {
   typedef GsTraits<MX4, NT> Tr;
@@ -85,12 +84,12 @@ __device__ __forceinline__ void gs_sum(const GsParams& P, int64_t wrow, int wlas
   const uint8_t *w0 = P.w + r0 * pitch + 16 * t, *w1 = P.w + r1 * pitch + 16 * t;
   const int64_t srows = static_cast<int64_t>(P.g.E) * P.N;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  for (int s0 = warp; s0 < steps; s0 += kGsWarps * Tr::kUnroll) {
+  for (int s0 = warp; s0 < steps; s0 += WARPS * Tr::kUnroll) {
     uint4 a[Tr::kUnroll][2], b[Tr::kUnroll][Tr::kParts][NT];
     uint32_t sw[Tr::kUnroll][2];
 #pragma unroll
     for (int u = 0; u < Tr::kUnroll; ++u) {
-      const int s = s0 + u * kGsWarps;
+      const int s = s0 + u * WARPS;
       const int k = s * Tr::kCols + 8 * Tr::kParts * t;      // this lane's first column
       const bool in = s < steps && k < P.K;
       a[u][0] = in ? __ldg(reinterpret_cast<const uint4*>(w0 + 64 * static_cast<int64_t>(s))) : zero;
@@ -109,7 +108,7 @@ __device__ __forceinline__ void gs_sum(const GsParams& P, int64_t wrow, int wlas
     }
 #pragma unroll
     for (int u = 0; u < Tr::kUnroll; ++u) {
-      if (s0 + u * kGsWarps >= steps) break;                 // warp-uniform
+      if (s0 + u * WARPS >= steps) break;                 // warp-uniform
       uint32_t f[2][2];
       bool two = false;
       if constexpr (MX4) {
@@ -145,14 +144,14 @@ __device__ __forceinline__ void gs_sum(const GsParams& P, int64_t wrow, int wlas
 }
 
 // 16 columns of `rows` rows (at most 8 NT): the warps' sums joined in warp order.
-template <bool MX4, int NT>
+template <bool MX4, int WARPS, int NT>
 __device__ __forceinline__ void gs_rows(const GsParams& P, int e, int n0, int64_t row0, int rows, float* s_part) {
   float acc[NT][4];
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
-  gs_sum<MX4, NT>(P, static_cast<int64_t>(e) * P.N + n0, P.N - 1 - n0, P.x + row0 * P.K, rows, acc);
+  gs_sum<MX4, WARPS, NT>(P, static_cast<int64_t>(e) * P.N + n0, P.N - 1 - n0, P.x + row0 * P.K, rows, acc);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   __syncthreads();                             // the last use of s_part is over
   // [warp][row of x][row of w]
@@ -162,11 +161,11 @@ __device__ __forceinline__ void gs_rows(const GsParams& P, int e, int n0, int64_
 #pragma unroll
     for (int i = 0; i < 4; ++i) mine[(8 * j + 2 * t + (i & 1)) * kGsRows + g + 8 * (i >> 1)] = acc[j][i];
   __syncthreads();
-  for (int v = threadIdx.x; v < rows * (kGsRows / 2); v += kGsThreads) {
+  for (int v = threadIdx.x; v < rows * (kGsRows / 2); v += 32 * WARPS) {
     const int r = v / (kGsRows / 2), c = 2 * (v % (kGsRows / 2));
     float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < kGsWarps; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
       const float2 p = *reinterpret_cast<const float2*>(s_part + w * (32 * kGsRows) + r * kGsRows + c);
       sum.x += p.x;
       sum.y += p.y;
@@ -181,29 +180,15 @@ __device__ __forceinline__ void gs_rows(const GsParams& P, int e, int n0, int64_
   }
 }
 
-template <bool MX4>
-__global__ void __launch_bounds__(kGsThreads, 4)
+template <bool MX4, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, 16 / WARPS)
 grouped_stream_kernel(const GsParams P) {
-  __shared__ __align__(16) float s_part[kGsWarps * 32 * kGsRows];
+  __shared__ __align__(16) float s_part[WARPS * 32 * kGsRows];
   __shared__ GroupSpan s_span[MM_MAX_EXPERTS];
   __shared__ int s_group[MM_MAX_EXPERTS];      // the groups that have rows
   __shared__ int s_count;
   pdl_enter();
-  if (threadIdx.x < 32) {
-    int count = 0;
-    for (int e0 = 0; e0 < P.g.E; e0 += 32) {
-      const int e = e0 + threadIdx.x;
-      const GroupSpan s = e < P.g.E ? group_span(P.g, e) : GroupSpan{0, 0, 0};
-      const uint32_t has = __ballot_sync(0xffffffffu, s.r1 > s.r0);
-      if (s.r1 > s.r0) {
-        const int at = count + __popc(has & ((1u << threadIdx.x) - 1u));
-        s_group[at] = e;
-        s_span[at] = s;
-      }
-      count += __popc(has);
-    }
-    if (threadIdx.x == 0) s_count = count;
-  }
+  groups_with_rows(P.g, s_span, s_group, &s_count);
   __syncthreads();
   const int tiles = (P.N + kGsRows - 1) / kGsRows;
   const int64_t units = static_cast<int64_t>(s_count) * tiles;
@@ -214,32 +199,41 @@ grouped_stream_kernel(const GsParams P) {
     for (int r = 0; r < s.n; r += 32) {
       const int rows = min(32, s.n - r);
       const int64_t row0 = s.r0 + r;
-      if (rows <= 8) gs_rows<MX4, 1>(P, e, n0, row0, rows, s_part);
-      else if (rows <= 16) gs_rows<MX4, 2>(P, e, n0, row0, rows, s_part);
-      else gs_rows<MX4, 4>(P, e, n0, row0, rows, s_part);
+      if (rows <= 8) gs_rows<MX4, WARPS, 1>(P, e, n0, row0, rows, s_part);
+      else if (rows <= 16) gs_rows<MX4, WARPS, 2>(P, e, n0, row0, rows, s_part);
+      else gs_rows<MX4, WARPS, 4>(P, e, n0, row0, rows, s_part);
     }
     // padding rows of the group
     const int cols = min(kGsRows, P.N - n0);
-    for (int v = threadIdx.x; v < (s.r1 - s.r0 - s.n) * kGsRows; v += kGsThreads)
+    for (int v = threadIdx.x; v < (s.r1 - s.r0 - s.n) * kGsRows; v += 32 * WARPS)
       if (v % kGsRows < cols)
         P.out[(static_cast<int64_t>(s.r0) + s.n + v / kGsRows) * P.N + n0 + v % kGsRows] = __float2bfloat16_rn(0.f);
   }
 }
 
+template <bool MX4, int WARPS>
+static cudaError_t gs_launch(const GsParams& p, int64_t units, cudaStream_t st) {
+  auto fn = grouped_stream_kernel<MX4, WARPS>;
+  const int64_t most = static_cast<int64_t>(num_sms()) * resident_blocks(reinterpret_cast<const void*>(fn), 32 * WARPS);
+  return launch_dependent_kernel(fn, dim3(static_cast<unsigned>(std::min(units, most))), dim3(32 * WARPS), 0, st, p);
+}
+// Eight warps share out the summed index of a tile where four would leave most
+// of an SM's warps without one: K = 4096 and N = 4096 for one expert 10.6 ->
+// 8.5 us (4 bits 9.0 -> 6.4), two experts with K = 2432, N = 768 6.6 -> 5.1;
+// with a tile for every four warps they are slower by 10 to 30%.
 template <bool MX4>
-static cudaError_t gs_launch(const GsParams& p, cudaStream_t st) {
+static cudaError_t gs_choose(const GsParams& p, cudaStream_t st) {
   const int64_t units = std::min<int64_t>(p.g.E, p.g.rows) * ((p.N + kGsRows - 1) / kGsRows);
-  const int64_t most = static_cast<int64_t>(num_sms()) * resident_blocks(reinterpret_cast<const void*>(grouped_stream_kernel<MX4>), kGsThreads);
-  return launch_dependent_kernel(grouped_stream_kernel<MX4>, dim3(static_cast<unsigned>(std::min(units, most))),
-                                 dim3(kGsThreads), 0, st, p);
+  const bool wide = units <= 2 * num_sms();
+  return wide ? gs_launch<MX4, 8>(p, units, st) : gs_launch<MX4, 4>(p, units, st);
 }
 
 cudaError_t launch_grouped_stream(const GroupedArgs& a, cudaStream_t st) {
-  return gs_launch<false>(GsParams{static_cast<const __nv_bfloat16*>(a.xs), static_cast<const uint8_t*>(a.w), nullptr,
+  return gs_choose<false>(GsParams{static_cast<const __nv_bfloat16*>(a.xs), static_cast<const uint8_t*>(a.w), nullptr,
                                    static_cast<__nv_bfloat16*>(a.out), a.g, a.K, a.N}, st);
 }
 cudaError_t launch_mx4_stream(const Mx4MatmulArgs& a, cudaStream_t st) {
-  return gs_launch<true>(GsParams{static_cast<const __nv_bfloat16*>(a.x), static_cast<const uint8_t*>(a.w),
+  return gs_choose<true>(GsParams{static_cast<const __nv_bfloat16*>(a.x), static_cast<const uint8_t*>(a.w),
                                   reinterpret_cast<const uint32_t*>(a.w_exps), static_cast<__nv_bfloat16*>(a.out), a.g,
                                   a.K, a.N}, st);
 }

@@ -488,7 +488,7 @@ struct GroupedArgs {
   GroupTables g;
   int K, N;
 };
-cudaError_t launch_grouped_simt(int dtype, int op, const GroupedArgs& p, cudaStream_t st);
+cudaError_t launch_grouped_simt(int op, const GroupedArgs& p, cudaStream_t st);      // fp32
 
 // The same on the tensor cores for bf16 (grouped_tc.cu).  Rows start on 16
 // bytes where a multiple of 8 elements makes a row; operands of other widths
