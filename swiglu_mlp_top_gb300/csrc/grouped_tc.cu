@@ -354,21 +354,45 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
   if (warp == kGmWarpMma) tmem_dealloc_cta2(tmem, 512);
 }
 
-// Rows of 2-byte elements that start anywhere -> rows of pitch8(cols), a
-// 16-byte vector a thread.
+// Rows of 2-byte elements that start anywhere -> rows of pitch8(cols), zeros
+// behind the row; a 16-byte vector a thread, from the two aligned vectors that
+// hold it (K = 1001, 16.7 MB: REPITCH us).
 __global__ void __launch_bounds__(256)
-repitch_kernel(const uint16_t* __restrict__ src, uint4* __restrict__ dst, const int64_t vectors, const int cols,
-               const int per_row) {
+repitch_kernel(const uint16_t* __restrict__ src, uint4* __restrict__ dst, const int64_t vectors, const int64_t elements,
+               const int cols, const int per_row) {
   pdl_enter();
   const int64_t v = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (v >= vectors) return;
-  const int64_t row = v / per_row;
+  const int64_t row = vectors <= 0xffffffffll ? static_cast<uint32_t>(v) / static_cast<uint32_t>(per_row) : v / per_row;
   const int c = static_cast<int>(v - row * per_row) * 8;
-  const uint16_t* s = src + row * cols + c;
-  uint32_t e[8];
+  const int64_t at = row * cols + c;           // first element
+  const int64_t base = at & ~int64_t{7};
+  uint32_t out[4];
+  if (base + 16 <= elements) {
+    const uint4 lo = __ldg(reinterpret_cast<const uint4*>(src + base)), hi = __ldg(reinterpret_cast<const uint4*>(src + base) + 1);
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    const int shift = static_cast<int>(at - base);           // elements, 0..7
+    uint32_t u[6];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) e[j] = c + j < cols ? s[j] : 0u;
-  dst[v] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+    for (int j = 0; j < 6; ++j) u[j] = shift & 4 ? w[j + 2] : w[j];
+    uint32_t t[5];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) t[j] = shift & 2 ? u[j + 1] : u[j];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) out[j] = shift & 1 ? __funnelshift_r(t[j], t[j + 1], 16) : t[j];
+  } else {                                     // the tensor ends inside the second vector
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t a = at + 2 * j < elements ? src[at + 2 * j] : 0u, b = at + 2 * j + 1 < elements ? src[at + 2 * j + 1] : 0u;
+      out[j] = a | b << 16;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {                // columns behind the row
+    if (c + 2 * j >= cols) out[j] = 0u;
+    else if (c + 2 * j + 1 >= cols) out[j] &= 0xffffu;
+  }
+  dst[v] = make_uint4(out[0], out[1], out[2], out[3]);
 }
 
 // =============================================================== host side
@@ -377,7 +401,7 @@ cudaError_t launch_repitch(const void* src, void* dst, int64_t rows, int cols, c
   const int64_t vectors = rows * per_row, blocks = (vectors + 255) / 256;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   return launch_dependent_kernel(repitch_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st,
-                                 static_cast<const uint16_t*>(src), static_cast<uint4*>(dst), vectors, cols, per_row);
+                                 static_cast<const uint16_t*>(src), static_cast<uint4*>(dst), vectors, rows * cols, cols, per_row);
 }
 
 static const CUtensorMapDataType kBf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;

@@ -10,9 +10,13 @@
 // The maximum is taken over magnitudes as integers, in which an infinity or a
 // NaN is above every number: it gives the byte 255 and a group of NaN.
 //
-// Bound by memory: 2 + 0.53 bytes a value in bf16.  16 lanes take a word of
-// four groups (128 columns), 8 columns a lane: 16-byte loads and 4-byte
-// stores without gaps, the group's maximum in two exchanges.
+// Bound by memory (2 + 0.53 bytes a value in bf16) where few enough
+// instructions go into a value.  Rows of whole 32-byte pieces: a lane takes 16
+// columns in 32-byte loads, magnitudes and products stay packed in bf16 (a
+// product that bf16 cannot hold is below 2^-126 and becomes zero either way),
+// 6 instructions a value.  Other rows: 8 columns a lane, as wide as the rows'
+// alignment allows; narrow rows are written element by element, neighbouring
+// lanes next to each other.
 #include "pack.cuh"
 #include "mm_kernels.cuh"
 
@@ -80,6 +84,109 @@ __device__ __forceinline__ void mx_load(const T* row, int c, int C, typename Pac
   }
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// 32 bytes in one access, from a 32-byte boundary.
+__device__ __forceinline__ void load32(const void* p, uint32_t (&v)[8]) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "l"(p));
+}
+// The scale byte of a group whose largest magnitude has these fp32 bits.
+__device__ __forceinline__ uint32_t mx4_byte(uint32_t top) {
+  const int q = static_cast<int>(top >> 23);
+  return q == 255 ? 255u : static_cast<uint32_t>(max(q - 2 + ((top & 0x7fffffu) > 0x400000u), 1));
+}
+
+constexpr int kMxWideLanes = 8;              // lanes of a word, 16 columns each
+
+// Rows of C columns that are whole pieces of 16 (32 bytes aligned).
+template <typename T>
+__global__ void __launch_bounds__(kMxThreads)
+mx4_quantize_wide_kernel(const T* __restrict__ x, uint8_t* __restrict__ codes, uint8_t* __restrict__ exps,
+                         const int32_t* n_rows, const int64_t R, const int C) {
+  constexpr bool kBf = sizeof(T) == 2;
+  constexpr int kUnits = kBf ? 4 : 2, kLoads = kBf ? 1 : 2;
+  pdl_enter();
+  const int groups = (C + 31) / 32, words = (groups + 3) / 4;
+  const int64_t rows = n_rows ? min(static_cast<int64_t>(max(*n_rows, 0)), R) : R;
+  const int l = threadIdx.x % kMxWideLanes;
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * (kMxThreads / kMxWideLanes) + threadIdx.x / kMxWideLanes) * kUnits;
+  MxUnit at = mx_unit(first, words);
+  MxUnit units[kUnits];
+  uint32_t raw[kUnits][8 * kLoads];
+#pragma unroll
+  for (int q = 0; q < kUnits; ++q) {
+    units[q] = at;
+    const int c = at.word * 128 + 16 * l;
+    if (at.row < rows && c < C) {
+      const T* from = x + at.row * C + c;
+#pragma unroll
+      for (int h = 0; h < kLoads; ++h) load32(from + 8 * h, *reinterpret_cast<uint32_t(*)[8]>(&raw[q][8 * h]));
+    } else {
+#pragma unroll
+      for (int h = 0; h < 8 * kLoads; ++h) raw[q][h] = 0u;
+    }
+    if (++at.word == words) {
+      at.word = 0;
+      ++at.row;
+    }
+  }
+  const uint32_t mask = 0xffu << (threadIdx.x & 24);
+#pragma unroll
+  for (int q = 0; q < kUnits; ++q) {
+    if (units[q].row >= rows) break;           // the 8 lanes of a unit agree
+    uint32_t top;
+    if constexpr (kBf) {
+      uint32_t m = raw[q][0] & 0x7fff7fffu;
+#pragma unroll
+      for (int h = 1; h < 8; ++h) m = max_u16x2(m, raw[q][h] & 0x7fff7fffu);
+      top = max(m & 0xffff0000u, m << 16);
+    } else {
+      top = raw[q][0] & 0x7fffffffu;
+#pragma unroll
+      for (int h = 1; h < 16; ++h) top = max(top, raw[q][h] & 0x7fffffffu);
+    }
+    top = max(top, __shfl_xor_sync(mask, top, 1));
+    uint32_t byte = mx4_byte(top);
+    const uint32_t scale = (254u - min(byte, 253u)) << 23;       // 2^-e
+    float v[16];
+    if constexpr (kBf) {
+      const uint32_t s2 = (scale >> 16) | scale;
+#pragma unroll
+      for (int h = 0; h < 8; ++h) {
+        const uint32_t w = mul_bf16x2(raw[q][h], s2);
+        v[2 * h] = __uint_as_float(w << 16);
+        v[2 * h + 1] = __uint_as_float(w & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 16; ++h) v[h] = __uint_as_float(raw[q][h]) * __uint_as_float(scale);
+    }
+    const int group = units[q].word * 4 + l / 2;
+    if (group < groups) {
+      // a lane behind the last column of its group has zeros there
+      uint2 c = make_uint2(e2m1x8(*reinterpret_cast<const float(*)[8]>(v)), e2m1x8(*reinterpret_cast<const float(*)[8]>(v + 8)));
+      if (byte == 255u) c = make_uint2(0u, 0u);
+      *reinterpret_cast<uint2*>(codes + units[q].row * (16 * static_cast<int64_t>(groups)) + group * 16 + (l & 1) * 8) = c;
+    } else {
+      byte = 127;
+    }
+    byte <<= 8 * (l / 2);
+    byte |= __shfl_xor_sync(mask, byte, 2);
+    byte |= __shfl_xor_sync(mask, byte, 4);
+    if (l == 0) reinterpret_cast<uint32_t*>(exps)[units[q].word * R + units[q].row] = byte;
+  }
+}
+
 template <typename T, int V>
 __global__ void __launch_bounds__(kMxThreads)
 mx4_quantize_kernel(const T* __restrict__ x, uint8_t* __restrict__ codes, uint8_t* __restrict__ exps,
@@ -114,8 +221,7 @@ mx4_quantize_kernel(const T* __restrict__ x, uint8_t* __restrict__ codes, uint8_
     }
     top = max(top, __shfl_xor_sync(mask, top, 1));
     top = max(top, __shfl_xor_sync(mask, top, 2));
-    const int q2 = static_cast<int>(top >> 23);
-    uint32_t byte = q2 == 255 ? 255u : static_cast<uint32_t>(max(q2 - 2 + ((top & 0x7fffffu) > 0x400000u), 1));
+    uint32_t byte = mx4_byte(top);
     const float scale = __uint_as_float((254u - min(byte, 253u)) << 23);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] *= scale;
@@ -180,32 +286,69 @@ mx4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restri
   }
 }
 
-template <typename T, int V>
-static cudaError_t mx4_launch(bool quantise, const Mx4Args& a, cudaStream_t st) {
-  const int64_t units = a.R * ((a.C + 127) / 128);
-  constexpr int kPer = kMxThreads / kMxLanes * kMxUnits;
-  const int64_t blocks = (units + kPer - 1) / kPer;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(blocks));
-  if (quantise)
-    return launch_dependent_kernel(mx4_quantize_kernel<T, V>, grid, dim3(kMxThreads), 0, st,
-                                   static_cast<const T*>(a.x), a.codes, a.exps, a.n_rows, a.R, a.C);
-  return launch_dependent_kernel(mx4_dequantize_kernel<T, V>, grid, dim3(kMxThreads), 0, st,
-                                 static_cast<const uint8_t*>(a.codes), static_cast<const uint8_t*>(a.exps),
-                                 static_cast<T*>(a.x_out), a.n_rows, a.R, a.C);
+// Rows that start anywhere: neighbouring lanes write neighbouring elements.
+template <typename T>
+__global__ void __launch_bounds__(kMxThreads)
+mx4_dequantize_narrow_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ exps, T* __restrict__ x,
+                             const int32_t* n_rows, const int64_t R, const int C) {
+  pdl_enter();
+  const int groups = (C + 31) / 32, words = (groups + 3) / 4;
+  const int64_t rows = n_rows ? min(static_cast<int64_t>(max(*n_rows, 0)), R) : R;
+  const int lane = threadIdx.x & 31;
+  const MxUnit u = mx_unit(static_cast<int64_t>(blockIdx.x) * (kMxThreads / 32) + (threadIdx.x >> 5), words);
+  if (u.row >= rows) return;                   // a warp's word of 128 columns
+  const uint32_t word = reinterpret_cast<const uint32_t*>(exps)[u.word * R + u.row];
+  const uint8_t* from = codes + u.row * (16 * static_cast<int64_t>(groups));
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int c = u.word * 128 + 32 * g + lane;
+    if (c >= C) break;
+    const uint32_t code = (from[c >> 1] >> (4 * (c & 1))) & 15u;
+    const uint32_t byte = (word >> (8 * g)) & 255u;
+    // 2^(byte - 127): subnormal for byte 0, NaN for 255
+    const float scale = byte == 255u ? __uint_as_float(0x7fffffffu)
+                                     : __uint_as_float(byte ? byte << 23 : 0x400000u);
+    // sign at bit 31, exponent and fraction at 24..22: the value times 2^-126
+    const float v = __uint_as_float((code & 8u) << 28 | (code & 7u) << 22) * 0x1p126f;
+    x[u.row * C + c] = static_cast<T>(v * scale);
+  }
 }
 
-// Accesses as wide as every row's alignment allows.
+// A grid of `per` words of 128 columns a block.
+template <typename Kern, typename... Args>
+static cudaError_t mx4_launch(Kern fn, int per, const Mx4Args& a, cudaStream_t st, Args... args) {
+  const int64_t blocks = (a.R * ((a.C + 127) / 128) + per - 1) / per;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  return launch_dependent_kernel(fn, dim3(static_cast<unsigned>(blocks)), dim3(kMxThreads), 0, st, args..., a.n_rows, a.R, a.C);
+}
+
+template <typename T>
+static cudaError_t mx4_quantize(const Mx4Args& a, cudaStream_t st) {
+  const T* x = static_cast<const T*>(a.x);
+  constexpr int kPer = kMxThreads / kMxLanes * kMxUnits;
+  if (a.C % 16 == 0 && reinterpret_cast<uintptr_t>(x) % 32 == 0)
+    return mx4_launch(mx4_quantize_wide_kernel<T>, kMxThreads / kMxWideLanes * (sizeof(T) == 2 ? 4 : 2), a, st, x, a.codes, a.exps);
+  if constexpr (sizeof(T) == 2)
+    if (a.C % 8 == 0) return mx4_launch(mx4_quantize_kernel<T, 8>, kPer, a, st, x, a.codes, a.exps);
+  if (a.C % 4 == 0) return mx4_launch(mx4_quantize_kernel<T, 4>, kPer, a, st, x, a.codes, a.exps);
+  if (a.C % 2 == 0) return mx4_launch(mx4_quantize_kernel<T, 2>, kPer, a, st, x, a.codes, a.exps);
+  return mx4_launch(mx4_quantize_kernel<T, 1>, kPer, a, st, x, a.codes, a.exps);
+}
+
+template <typename T>
+static cudaError_t mx4_dequantize(const Mx4Args& a, cudaStream_t st) {
+  const uint8_t *codes = a.codes, *exps = a.exps;
+  T* x = static_cast<T*>(a.x_out);
+  constexpr int kWide = 16 / sizeof(T), kPer = kMxThreads / kMxLanes * kMxUnits;
+  if (a.C % kWide == 0) return mx4_launch(mx4_dequantize_kernel<T, kWide>, kPer, a, st, codes, exps, x);
+  if constexpr (sizeof(T) == 2)
+    if (a.C % 4 == 0) return mx4_launch(mx4_dequantize_kernel<T, 4>, kPer, a, st, codes, exps, x);
+  return mx4_launch(mx4_dequantize_narrow_kernel<T>, kMxThreads / 32, a, st, codes, exps, x);
+}
+
 cudaError_t launch_mx4(int dtype, bool quantise, const Mx4Args& a, cudaStream_t st) {
-  if (dtype == kDtypeBF16) {
-    if (a.C % 8 == 0) return mx4_launch<__nv_bfloat16, 8>(quantise, a, st);
-    if (a.C % 4 == 0) return mx4_launch<__nv_bfloat16, 4>(quantise, a, st);
-    if (a.C % 2 == 0) return mx4_launch<__nv_bfloat16, 2>(quantise, a, st);
-    return mx4_launch<__nv_bfloat16, 1>(quantise, a, st);
-  }
-  if (a.C % 4 == 0) return mx4_launch<float, 4>(quantise, a, st);
-  if (a.C % 2 == 0) return mx4_launch<float, 2>(quantise, a, st);
-  return mx4_launch<float, 1>(quantise, a, st);
+  if (dtype == kDtypeBF16) return quantise ? mx4_quantize<__nv_bfloat16>(a, st) : mx4_dequantize<__nv_bfloat16>(a, st);
+  return quantise ? mx4_quantize<float>(a, st) : mx4_dequantize<float>(a, st);
 }
 
 }  // namespace mm

@@ -197,6 +197,7 @@ def test_quantise_at_the_edges(dtype):
     x[12, :32] = 2.0 ** -124 * 1.5
     x[13, :32] = 2.0 ** -124 * 1.75
     x[14] = -0.0
+    x[15, :3] = torch.tensor([2.0 ** -127, -(2.0 ** -127) * 1.5, 2.0 ** -129])    # subnormal, and not zero
     q, values = quantised(x.to(dtype))
     back = mm.mx4_dequantize(q, F32).cpu().double()
     same = torch.where(values.abs() >= 2.0 ** 128, torch.sign(values) * torch.inf, values)
