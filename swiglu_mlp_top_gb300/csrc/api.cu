@@ -1161,32 +1161,6 @@ static bool grouped_in_limits(int64_t rows, int K, int N, int E) {
 }
 static bool status_ok(const void* status_ws) { return aligned16(status_ws); }
 
-// Copies with rows that start on 16 bytes, for the bf16 operands whose rows do not.
-struct GroupedLayout {
-  size_t xs, dys, w, total;
-};
-static size_t repitched_bytes(int64_t rows, int cols) {
-  return cols % 8 ? align_up(2 * static_cast<size_t>(rows) * pitch8(cols)) : 0;
-}
-static GroupedLayout grouped_layout(int64_t rows, int K, int N, int E, int dtype, bool backward) {
-  GroupedLayout L{0, 0, 0, 0};
-  if (dtype != kDtypeBF16) return L;
-  L.dys = repitched_bytes(rows, K);
-  L.w = L.dys + (backward ? repitched_bytes(rows, N) : 0);
-  L.total = L.w + repitched_bytes(static_cast<int64_t>(E) * N, K);
-  return L;
-}
-static size_t grouped_bytes(int64_t rows, int K, int N, int E, int dtype, bool backward) {
-  if (!valid_dtype(dtype) || rows < 1 || K < 1 || N < 1 || E < 1 || !grouped_in_limits(rows, K, N, E)) return 0;
-  return grouped_layout(rows, K, N, E, dtype, backward).total;
-}
-// p, or its copy at `to`.
-static cudaError_t repitched(const void** p, char* to, int64_t rows, int cols, cudaStream_t st) {
-  if (cols % 8 == 0) return cudaSuccess;
-  const void* src = *p;
-  *p = to;
-  return counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_repitch(src, to, rows, cols, st); });
-}
 // Few rows, which start on 16 bytes, go to the kernel that streams the weights
 // (grouped_stream.cu).  Its time grows with the rows of an expert, the tiles'
 // with the weights: at E = 8, K = 768, N = 4864 and 32 rows 13.4 us against
@@ -1198,12 +1172,93 @@ static cudaError_t repitched(const void** p, char* to, int64_t rows, int cols, c
 static bool grouped_streams(int64_t rows, int K, int E, bool w_in_4_bits) {
   return K % 8 == 0 && rows <= (w_in_4_bits ? 64 + 16 * E : 32 + 6 * E);
 }
-static cudaError_t grouped_launch(int dtype, int op, const GroupedArgs& a, void* status_ws, cudaStream_t st) {
-  return counted_launch(MM_KERNEL_GROUPED, st, [&] {
-    if (dtype == kDtypeBF16 && op == kGroupedForward && grouped_streams(a.g.rows, a.K, a.g.E, false)) return launch_grouped_stream(a, st);
-    return dtype == kDtypeBF16 ? launch_grouped_tc(op, a, static_cast<WsHeader*>(status_ws), st)
-                               : launch_grouped_simt(op, a, st);
+// What a call of a product needs beside its tensors.
+struct GroupedPlan {
+  int planes;                 // 0: no tensor cores; 1: bf16; 3: fp32 as planes of bf16
+  int splits[3];              // parts of the sums, by operation
+  size_t flag;                // planes 3: the word that turns the call over to the CUDA cores
+  size_t xs, dys, w;          // copies: rows that start on 16 bytes, or planes
+  size_t parts;               // one set, for the operations one after the other
+  size_t total;
+};
+// fp32: a forward pass of few rows streams its weights on the CUDA cores
+// (grouped_simt.cu), all else goes to the tensor cores: T = 1000, E = 4, K = 768,
+// N = 2432 148 -> 50 us, 8000 rows, E = 8 634 -> 163; 64 rows, E = 8 equal.
+static bool f32_on_tensor_cores(int64_t rows, int E, bool backward) {
+  return (backward || rows > f32_stream_rows(E)) && rows <= int64_t{1} << 29;       // three planes of rows are counted in 32 bits
+}
+
+static GroupedPlan grouped_plan(int64_t rows, int K, int N, int E, int dtype, bool backward) {
+  GroupedPlan L;
+  memset(&L, 0, sizeof(L));
+  L.planes = dtype == kDtypeBF16 ? 1 : f32_on_tensor_cores(rows, E, backward) ? 3 : 0;
+  L.splits[0] = L.splits[1] = L.splits[2] = 1;
+  if (L.planes == 0) return L;
+  const GroupTables g{reinterpret_cast<const int32_t*>(E > 1 ? 4 : 0), nullptr, rows, E};   // the same bound for every table
+  const int first = backward ? kGroupedDgrad : kGroupedForward, last = backward ? kGroupedWgrad : kGroupedForward;
+  size_t off = 0, parts = 0;
+  auto copy = [&](size_t* at, int64_t r, int cols) {
+    *at = off;
+    if (L.planes == 3 || cols % 8) off += align_up(2 * static_cast<size_t>(L.planes) * r * pitch8(cols));
+  };
+  if (L.planes == 3) off += kAlign;
+  copy(&L.xs, rows, K);
+  if (backward) copy(&L.dys, rows, N);
+  copy(&L.w, static_cast<int64_t>(E) * N, K);
+  for (int op = first; op <= last; ++op) {
+    L.splits[op] = grouped_splits(op, g, K, N, L.planes);
+    parts = std::max(parts, grouped_parts_bytes(op, g, K, N, L.splits[op]));
+  }
+  L.parts = off;
+  L.total = off + align_up(parts);
+  return L;
+}
+static size_t grouped_bytes(int64_t rows, int K, int N, int E, int dtype, bool backward) {
+  if (!valid_dtype(dtype) || rows < 1 || K < 1 || N < 1 || E < 1 || !grouped_in_limits(rows, K, N, E)) return 0;
+  if (!backward && dtype == kDtypeBF16 && grouped_streams(rows, K, E, false)) return 0;
+  return grouped_plan(rows, K, N, E, dtype, backward).total;
+}
+// Makes the operands of `a` ready that are not null: as given, or their copies.
+static cudaError_t grouped_operands(const GroupedPlan& L, GroupedArgs& a, void* ws, cudaStream_t st) {
+  const int64_t wrows = static_cast<int64_t>(a.g.E) * a.N;
+  struct { const void** p; size_t at; int64_t rows; int cols, grouped; } each[3] = {
+      {&a.xs, L.xs, a.g.rows, a.K, 1}, {&a.dys, L.dys, a.g.rows, a.N, 1}, {&a.w, L.w, wrows, a.K, 0}};
+  SplitTensors t;
+  t.n = 0;
+  for (auto& o : each) {
+    if (*o.p == nullptr || L.planes == 0 || (L.planes == 1 && o.cols % 8 == 0)) continue;
+    void* to = ws_at(ws, o.at);
+    if (L.planes == 3) {
+      t.t[t.n++] = SplitTensor{*o.p, to, o.rows, o.cols, o.grouped};
+    } else {
+      const void* src = *o.p;
+      const cudaError_t e = counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_repitch(src, to, o.rows, o.cols, st); });
+      if (e != cudaSuccess) return e;
+    }
+    *o.p = to;
+  }
+  if (t.n == 0) return cudaSuccess;
+  int* flag = reinterpret_cast<int*>(ws_at(ws, L.flag));
+  const cudaError_t e = cudaMemsetAsync(flag, 0, sizeof(int), st);
+  if (e != cudaSuccess) return e;
+  return counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_grouped_split(t, a.g, flag, st); });
+}
+
+// One operation on operands that grouped_operands() has made ready in `a`;
+// `given` has the caller's.
+static cudaError_t grouped_launch(const GroupedPlan& L, int dtype, int op, const GroupedArgs& a, const GroupedArgs& given,
+                                  void* ws, void* status_ws, cudaStream_t st) {
+  if (L.planes == 0) return counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_grouped_simt(op, given, nullptr, st); });
+  const int* flag = L.planes == 3 ? reinterpret_cast<const int*>(ws_at(ws, L.flag)) : nullptr;
+  const GroupedTcExtras x{L.planes, L.splits[op], L.splits[op] > 1 ? ws_at(ws, L.parts) : nullptr, flag};
+  cudaError_t e = counted_launch(MM_KERNEL_GROUPED, st, [&] {
+    return launch_grouped_tc(op, a, x, static_cast<WsHeader*>(status_ws), st);
   });
+  if (e == cudaSuccess && x.splits > 1)
+    e = counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_grouped_join(op, dtype, a, x, st); });
+  if (e == cudaSuccess && flag != nullptr)
+    e = counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_grouped_simt(op, given, flag, st); });
+  return e;
 }
 
 size_t mm_grouped_matmul_workspace_bytes(int64_t rows, int K, int N, int E, int dtype) {
@@ -1221,14 +1276,16 @@ int mm_grouped_matmul(const void* xs, const void* w, const int32_t* offsets, con
   const size_t need = mm_grouped_matmul_workspace_bytes(rows, K, N, E, dtype);
   if (need > 0 && (!present16(workspace) || workspace_bytes < need)) return MM_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  GroupedArgs a{xs, nullptr, w, ys, GroupTables{offsets, counts, rows, E}, K, N};
+  const GroupedArgs given{xs, nullptr, w, ys, GroupTables{offsets, counts, rows, E}, K, N};
   cudaError_t e = cudaSuccess;
-  if (need > 0) {
-    const GroupedLayout L = grouped_layout(rows, K, N, E, dtype, false);
-    e = repitched(&a.xs, ws_at(workspace, L.xs), rows, K, st);
-    if (e == cudaSuccess) e = repitched(&a.w, ws_at(workspace, L.w), static_cast<int64_t>(E) * N, K, st);
+  if (dtype == kDtypeBF16 && grouped_streams(rows, K, E, false)) {
+    e = counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_grouped_stream(given, st); });
+  } else {
+    const GroupedPlan L = grouped_plan(rows, K, N, E, dtype, false);
+    GroupedArgs a = given;
+    e = grouped_operands(L, a, workspace, st);
+    if (e == cudaSuccess) e = grouped_launch(L, dtype, kGroupedForward, a, given, workspace, status_ws, st);
   }
-  if (e == cudaSuccess) e = grouped_launch(dtype, kGroupedForward, a, status_ws, st);
   return e == cudaSuccess ? MM_OK : cuda_fail(e, "grouped matmul");
 }
 
@@ -1254,19 +1311,16 @@ int mm_grouped_matmul_backward(const void* dys, const void* xs, const void* w,
     return MM_ERR_INVALID_ARG;
   const size_t need = mm_grouped_matmul_backward_workspace_bytes(rows, K, N, E, dtype);
   if (need > 0 && (!present16(workspace) || workspace_bytes < need)) return MM_ERR_WORKSPACE;
-  GroupedArgs a{xs, dys, w, dxs, GroupTables{offsets, counts, rows, E}, K, N};
-  cudaError_t e = cudaSuccess;
-  if (need > 0) {
-    const GroupedLayout L = grouped_layout(rows, K, N, E, dtype, true);
-    e = repitched(&a.dys, ws_at(workspace, L.dys), rows, N, st);
-    if (e == cudaSuccess && dxs != nullptr)
-      e = repitched(&a.w, ws_at(workspace, L.w), static_cast<int64_t>(E) * N, K, st);
-    if (e == cudaSuccess && dw != nullptr) e = repitched(&a.xs, ws_at(workspace, L.xs), rows, K, st);
-  }
-  if (e == cudaSuccess && dxs != nullptr) e = grouped_launch(dtype, kGroupedDgrad, a, status_ws, st);
+  GroupedArgs given{xs, dys, w, dxs, GroupTables{offsets, counts, rows, E}, K, N};
+  const GroupedPlan L = grouped_plan(rows, K, N, E, dtype, true);
+  GroupedArgs a = given;
+  if (dxs == nullptr) a.w = nullptr;
+  if (dw == nullptr) a.xs = nullptr;
+  cudaError_t e = grouped_operands(L, a, workspace, st);
+  if (e == cudaSuccess && dxs != nullptr) e = grouped_launch(L, dtype, kGroupedDgrad, a, given, workspace, status_ws, st);
   if (e == cudaSuccess && dw != nullptr) {
-    a.out = dw;
-    e = grouped_launch(dtype, kGroupedWgrad, a, status_ws, st);
+    a.out = given.out = dw;
+    e = grouped_launch(L, dtype, kGroupedWgrad, a, given, workspace, status_ws, st);
   }
   return e == cudaSuccess ? MM_OK : cuda_fail(e, "grouped matmul backward");
 }

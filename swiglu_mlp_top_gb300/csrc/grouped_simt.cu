@@ -70,13 +70,14 @@ struct SimtSlice {
 template <int OP, int V, int TM>
 __global__ void __launch_bounds__(2 * TM, 512 / (2 * TM))
 grouped_simt_kernel(const float* __restrict__ a, const float* __restrict__ b, float* __restrict__ out,
-                    const GroupTables g, const int M, const int N, const int K) {
+                    const GroupTables g, const int M, const int N, const int K, const int* only_if) {
   constexpr bool kAKc = OP != 2, kBKc = OP == 0;
   typedef SimtSlice<kAKc, V, TM, 2 * TM> SliceA;
   typedef SimtSlice<kBKc, V, kSimtN, 2 * TM> SliceB;
   constexpr int kPitchA = SliceA::kPitch, kPitchB = SliceB::kPitch;
   __shared__ __align__(16) float sA[2][kSimtK * kPitchA], sB[2][kSimtK * kPitchB];
   pdl_enter();
+  if (only_if != nullptr && *only_if == 0) return;
   const int cols = (N + kSimtN - 1) / kSimtN;
   // this block's tile: rows [m0, mend) of A of which those below mval count, columns from n0
   int m0, mend, mval, n0, k0 = 0, kend = K;
@@ -231,11 +232,11 @@ grouped_simt_few_kernel(const float* __restrict__ x, const float* __restrict__ w
 
 template <int OP, int V, int TM>
 static cudaError_t simt_tiles(const void* a, const void* b, void* out, const GroupTables& g, int M, int N, int K,
-                              int64_t tiles, cudaStream_t st) {
+                              int64_t tiles, const int* only_if, cudaStream_t st) {
   if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
   return launch_dependent_kernel(grouped_simt_kernel<OP, V, TM>, dim3(static_cast<unsigned>(tiles)), dim3(2 * TM), 0, st,
                                  static_cast<const float*>(a), static_cast<const float*>(b), static_cast<float*>(out), g,
-                                 M, N, K);
+                                 M, N, K, only_if);
 }
 
 // Tiles of `tm` rows that any grouping of the rows can need (wgrad: that there are).
@@ -249,19 +250,19 @@ static int64_t simt_row_tiles(int op, const GroupTables& g, int M, int tm) {
 // against SIMT_128).
 template <int OP>
 static cudaError_t simt(const void* a, const void* b, void* out, const GroupTables& g, int M, int N, int K, bool vec,
-                        cudaStream_t st) {
+                        const int* only_if, cudaStream_t st) {
   const int64_t cols = (N + kSimtN - 1) / kSimtN;
   const int64_t big = simt_row_tiles(OP, g, M, 128) * cols, small = simt_row_tiles(OP, g, M, 64) * cols;
   if (big >= 4 * num_sms())
-    return vec ? simt_tiles<OP, 4, 128>(a, b, out, g, M, N, K, big, st) : simt_tiles<OP, 1, 128>(a, b, out, g, M, N, K, big, st);
-  return vec ? simt_tiles<OP, 4, 64>(a, b, out, g, M, N, K, small, st) : simt_tiles<OP, 1, 64>(a, b, out, g, M, N, K, small, st);
+    return vec ? simt_tiles<OP, 4, 128>(a, b, out, g, M, N, K, big, only_if, st) : simt_tiles<OP, 1, 128>(a, b, out, g, M, N, K, big, only_if, st);
+  return vec ? simt_tiles<OP, 4, 64>(a, b, out, g, M, N, K, small, only_if, st) : simt_tiles<OP, 1, 64>(a, b, out, g, M, N, K, small, only_if, st);
 }
 
-cudaError_t launch_grouped_simt(int op, const GroupedArgs& p, cudaStream_t st) {
+cudaError_t launch_grouped_simt(int op, const GroupedArgs& p, const int* only_if, cudaStream_t st) {
   const bool k4 = p.K % 4 == 0, kn4 = k4 && p.N % 4 == 0;
-  if (op == kGroupedWgrad) return simt<kGroupedWgrad>(p.dys, p.xs, p.out, p.g, p.N, p.K, 0, kn4, st);
-  if (op == kGroupedDgrad) return simt<kGroupedDgrad>(p.dys, p.w, p.out, p.g, 0, p.K, p.N, kn4, st);
-  if (p.g.rows > 16 + 4 * p.g.E) return simt<kGroupedForward>(p.xs, p.w, p.out, p.g, 0, p.N, p.K, k4, st);
+  if (op == kGroupedWgrad) return simt<kGroupedWgrad>(p.dys, p.xs, p.out, p.g, p.N, p.K, 0, kn4, only_if, st);
+  if (op == kGroupedDgrad) return simt<kGroupedDgrad>(p.dys, p.w, p.out, p.g, 0, p.K, p.N, kn4, only_if, st);
+  if (p.g.rows > f32_stream_rows(p.g.E)) return simt<kGroupedForward>(p.xs, p.w, p.out, p.g, 0, p.N, p.K, k4, only_if, st);
   const int64_t units = std::min<int64_t>(p.g.E, p.g.rows) * ((p.N + kSimtFewW - 1) / kSimtFewW);
   auto fn = k4 ? grouped_simt_few_kernel<4> : grouped_simt_few_kernel<1>;
   const int64_t most = static_cast<int64_t>(num_sms()) * resident_blocks(reinterpret_cast<const void*>(fn), 128);

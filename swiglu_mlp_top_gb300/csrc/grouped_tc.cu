@@ -8,7 +8,8 @@
 // A and half of B in each CTA's shared memory), in slices of 64 of the summed
 // index through a ring of six stages; two accumulators, so that the epilogue
 // of one tile runs under the products of the next.  Warps: 8 epilogue, 1 TMA,
-// 1 MMA (even CTA).
+// 1 MMA (even CTA; it goes through its loop as a whole and issues from one
+// lane, which keeps descriptors in uniform registers).
 //
 // Groups start and end at any row, which only the device knows.  Where rows
 // are the M index, a tile reads rows past its group (rows of A have no
@@ -18,22 +19,34 @@
 // be NaN: the TMA brings a group's last slice to a barrier of its own CTA, the
 // producer warp writes zeros over the rows behind the group, in both operands,
 // and hands the slice on.
+//
+// fp32 operands come as three bf16 planes (split_kernel): x = h + m + l, each
+// the nearest bf16 of what the ones before leave, so that 24 bits are kept and
+// of the nine products the three below 2^-25 are left out.  h h' adds up in one
+// accumulator and the five smaller products in the other; both are added in
+// fp32 registers every 512 of the summed index.
+//
+// Few tiles with a long sum are cut into `splits` parts of the sum, each an
+// fp32 tile of its own in the workspace, and join_kernel adds them in order.
 #include "grouped.cuh"
 
 namespace mm {
 
-constexpr int kGmStages = 6;
+constexpr int kGmRing = 6;                            // tiles of A (and of B) in the ring
 constexpr int kGmTile = 128 * 64 * 2;                 // 16 KiB: 128 rows x one slice
 constexpr int kGmEpiWarps = 8;
 constexpr int kGmThreads = 32 * (kGmEpiWarps + 2);
 constexpr int kGmWarpProducer = kGmEpiWarps, kGmWarpMma = kGmEpiWarps + 1;
 constexpr int kGmStage = 32 * 128;                    // epilogue: 32 rows x 128 bytes per warp
-constexpr int kGmSmem = kGmStages * 2 * kGmTile + kGmEpiWarps * kGmStage + 1024 + 256;
+constexpr int kGmSmem = kGmRing * 2 * kGmTile + kGmEpiWarps * kGmStage + 1024 + 256;
+// with the static arrays within the 227 KiB of a block
+static_assert(kGmSmem + sizeof(GmTables) + 64 <= 232448, "shared memory budget");
 
 // Slices of the summed index per accumulation in TMEM.  The tensor cores cut
-// off where they add to the accumulator; a weight gradient, kept in fp32 and
-// summed over thousands of rows, adds chunks of 512 rows in fp32 registers.
-template <int OP> constexpr int kGmChunk = OP == kGroupedWgrad ? 8 : 1 << 30;
+// off where they add to the accumulator; results in fp32 add chunks of 512 in
+// fp32 registers (a weight gradient over 9500 rows is 4.7e-7 off, relative,
+// where one accumulation is 1.3e-6 off).
+template <bool F32> constexpr int kGmChunk = F32 ? 8 : 1 << 30;
 
 struct GmParams {
   CUtensorMap a, b, out;
@@ -42,30 +55,37 @@ struct GmParams {
   int N;              // columns of the result
   int K;              // forward, dgrad: length of the sum
   int a_blocks, b_blocks;   // the MN-major map has 64-column blocks as a dimension: one box for both
+  int a_plane, b_plane;     // three planes: rows (b of forward and dgrad: experts) from one to the next
+  int splits;         // parts of the sum
+  int out_plane;      // rows (wgrad: experts) of a part's result
   int out_aligned;    // the result's rows start on 16 bytes: tensor stores
   void* outp;
+  int64_t ldo;        // elements from one row of the result to the next
+  const int* skip;    // not null: nothing is done where it holds something
 };
 
-// with the static arrays within the 227 KiB of a block
-static_assert(kGmSmem + sizeof(GmTables) + 64 <= 232448, "shared memory budget");
-
-template <int OP>
+// OP, PLANES: 1 (bf16) or 3 (fp32).  F32: the result, or its parts, in fp32.
+template <int OP, int PLANES, bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGmThreads, 1)
 grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
+  constexpr int kStages = kGmRing / PLANES;
+  constexpr int kAccs = PLANES == 1 ? 2 : 1;   // accumulators by turns; three planes: one pair of them
+  constexpr int kStep = PLANES * kGmTile;      // bytes of an operand's stage
+  constexpr bool kWgrad = OP == kGroupedWgrad;
   extern __shared__ unsigned char smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint8_t* sA = smem;
-  uint8_t* sB = smem + kGmStages * kGmTile;
-  uint8_t* sEpi = sB + kGmStages * kGmTile;
+  uint8_t* sB = smem + kGmRing * kGmTile;
+  uint8_t* sEpi = sB + kGmRing * kGmTile;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sEpi + kGmEpiWarps * kGmStage);
   uint64_t* full = bars;                   // [stages] even CTA: both CTAs' bytes
-  uint64_t* empty = bars + kGmStages;      // [stages] each CTA: released by the pair's MMAs
-  uint64_t* tfull = bars + 2 * kGmStages;  // [2] each CTA: accumulator ready
+  uint64_t* empty = bars + kStages;        // [stages] each CTA: released by the pair's MMAs
+  uint64_t* tfull = bars + 2 * kStages;    // [2] each CTA: accumulator ready
   uint64_t* tempty = tfull + 2;            // [2] even CTA: both CTAs' epilogues done
   uint64_t* drained = tempty + 2;          // even CTA: all MMAs finished
   uint64_t* part = drained + 1;            // wgrad, each CTA: a group's last slice has landed
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort;
+  __shared__ int s_abort, s_total;
   __shared__ GmTables s_tab;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -74,8 +94,8 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
   const int ntn = (P.N + 255) / 256;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kGmStages; ++s) {
-      mbar_init(&full[s], OP == kGroupedWgrad ? 2 : 1);   // wgrad: each CTA's producer arrives
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], kWgrad ? 2 : 1);   // wgrad: each CTA's producer arrives
       mbar_init(&empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -92,6 +112,11 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     gm_tables<OP>(P.g, s_tab, ntn);
+    __syncwarp();
+    if (lane == 0) {
+      const bool none = P.skip != nullptr && *P.skip != 0;
+      s_total = none ? 0 : P.splits * (kWgrad ? P.g.E * ((P.M + 255) / 256) * ntn : s_tab.tstart[P.g.E]);
+    }
   }
   if (warp == kGmWarpMma) {
     tmem_alloc_cta2(&s_tmem, 512);
@@ -101,8 +126,14 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const int total = OP == kGroupedWgrad ? P.g.E * ((P.M + 255) / 256) * ntn : s_tab.tstart[P.g.E];
+  const int total = s_total;
   volatile int* abort = &s_abort;
+  // the slices [k0, k1) of a tile's part of the sum
+  auto slices = [&](const GmTile& ti, int tile, int& k0, int& k1) {
+    const int nkb = (ti.krows + 63) / 64, sp = tile % P.splits;
+    k0 = static_cast<int>(static_cast<int64_t>(nkb) * sp / P.splits);
+    k1 = static_cast<int>(static_cast<int64_t>(nkb) * (sp + 1) / P.splits);
+  };
 
   if (warp == kGmWarpProducer) {
     // ------------------------------------------------ TMA (both CTAs)
@@ -111,51 +142,62 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
     for (int j = 0; ok && j * nc < total; ++j) {
       const int tile = gm_index<OP>(j, cluster, nc);
       if (tile >= total) continue;               // the last round's missing tiles
-      const GmTile ti = gm_tile<OP>(tile, P.g.E, P.M, P.K, s_tab, ntn, 256, rank);
+      const GmTile ti = gm_tile<OP>(tile / P.splits, P.g.E, P.M, P.K, s_tab, ntn, 256, rank);
       const int ncol = ti.n0 + 128 * rank;       // this CTA's half of the columns
-      const int nkb = (ti.krows + 63) / 64;
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const int s = it % kGmStages;
-        const uint32_t ph = (it / kGmStages) & 1;
+      int k0, k1;
+      slices(ti, tile, k0, k1);
+      for (int kb = k0; kb < k1; ++kb, ++it) {
+        const int s = it % kStages;
+        const uint32_t ph = (it / kStages) & 1;
         ok = lane != 0 || mbar_wait(&empty[s], ph ^ 1, abort, hdr, 111);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
         const uint32_t fb = mapa_shared(smem_u32(&full[s]), 0);
-        uint8_t* a = sA + s * kGmTile;
-        uint8_t* b = sB + s * kGmTile;
-        if constexpr (OP == kGroupedWgrad) {
+        uint8_t* a = sA + s * kStep;
+        uint8_t* b = sB + s * kStep;
+        if constexpr (kWgrad) {
           const int krow = ti.k0 + kb * 64, rows = ti.krows - kb * 64;
           if (rows >= 64) {
             if (lane == 0) {
-              if (rank == 0) mbar_arrive_expect_tx(&full[s], 4 * kGmTile);
+              if (rank == 0) mbar_arrive_expect_tx(&full[s], 4 * kStep);
               else mbar_signal_cluster(fb);
-              if (P.a_blocks) {
-                tma_load_3d_cta2(a, &P.a, fb, 0, krow, ti.m0 / 64);
-              } else {
-                tma_load_2d_cta2(a, &P.a, fb, ti.m0, krow);
-                tma_load_2d_cta2(a + kGmTile / 2, &P.a, fb, ti.m0 + 64, krow);
-              }
-              if (P.b_blocks) {
-                tma_load_3d_cta2(b, &P.b, fb, 0, krow, ncol / 64);
-              } else {
-                tma_load_2d_cta2(b, &P.b, fb, ncol, krow);
-                tma_load_2d_cta2(b + kGmTile / 2, &P.b, fb, ncol + 64, krow);
+#pragma unroll
+              for (int p = 0; p < PLANES; ++p) {
+                uint8_t *ap = a + p * kGmTile, *bp = b + p * kGmTile;
+                const int ar = krow + p * P.a_plane, br = krow + p * P.b_plane;
+                if (P.a_blocks) {
+                  tma_load_3d_cta2(ap, &P.a, fb, 0, ar, ti.m0 / 64);
+                } else {
+                  tma_load_2d_cta2(ap, &P.a, fb, ti.m0, ar);
+                  tma_load_2d_cta2(ap + kGmTile / 2, &P.a, fb, ti.m0 + 64, ar);
+                }
+                if (P.b_blocks) {
+                  tma_load_3d_cta2(bp, &P.b, fb, 0, br, ncol / 64);
+                } else {
+                  tma_load_2d_cta2(bp, &P.b, fb, ncol, br);
+                  tma_load_2d_cta2(bp + kGmTile / 2, &P.b, fb, ncol + 64, br);
+                }
               }
             }
           } else {
             if (lane == 0) {
-              mbar_arrive_expect_tx(part, 2 * kGmTile);
-              if (P.a_blocks) {
-                tma_load_3d(a, &P.a, part, 0, krow, ti.m0 / 64);
-              } else {
-                tma_load_2d(a, &P.a, part, ti.m0, krow);
-                tma_load_2d(a + kGmTile / 2, &P.a, part, ti.m0 + 64, krow);
-              }
-              if (P.b_blocks) {
-                tma_load_3d(b, &P.b, part, 0, krow, ncol / 64);
-              } else {
-                tma_load_2d(b, &P.b, part, ncol, krow);
-                tma_load_2d(b + kGmTile / 2, &P.b, part, ncol + 64, krow);
+              mbar_arrive_expect_tx(part, 2 * kStep);
+#pragma unroll
+              for (int p = 0; p < PLANES; ++p) {
+                uint8_t *ap = a + p * kGmTile, *bp = b + p * kGmTile;
+                const int ar = krow + p * P.a_plane, br = krow + p * P.b_plane;
+                if (P.a_blocks) {
+                  tma_load_3d(ap, &P.a, part, 0, ar, ti.m0 / 64);
+                } else {
+                  tma_load_2d(ap, &P.a, part, ti.m0, ar);
+                  tma_load_2d(ap + kGmTile / 2, &P.a, part, ti.m0 + 64, ar);
+                }
+                if (P.b_blocks) {
+                  tma_load_3d(bp, &P.b, part, 0, br, ncol / 64);
+                } else {
+                  tma_load_2d(bp, &P.b, part, ncol, br);
+                  tma_load_2d(bp + kGmTile / 2, &P.b, part, ncol + 64, br);
+                }
               }
             }
             ok = warp_wait(part, parts & 1, abort, hdr, 117);
@@ -163,9 +205,9 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
             if (!ok) break;
             // a half tile is 64 rows of 128 bytes: rows [rows, multiple of 16) become zeros
             const int clear = ((rows + 15) / 16 * 16 - rows) * 8;        // 16-byte vectors of a half
-            for (int v = lane; v < 4 * clear; v += 32) {
+            for (int v = lane; v < 4 * PLANES * clear; v += 32) {
               const int h = v / clear;
-              uint8_t* half = (h & 2 ? b : a) + (h & 1) * (kGmTile / 2);
+              uint8_t* half = (h & 1 ? b : a) + (h >> 1) * (kGmTile / 2);
               reinterpret_cast<uint4*>(half + rows * 128)[v - h * clear] = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();
@@ -176,73 +218,103 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
             }
           }
         } else if (lane == 0) {
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 4 * kGmTile);
-          tma_load_2d_cta2(a, &P.a, fb, kb * 64, ti.m0);
-          if constexpr (OP == kGroupedForward) {
-            tma_load_3d_cta2(b, &P.b, fb, kb * 64, ncol, ti.e);
-          } else if (P.b_blocks) {
-            tma_load_4d_cta2(b, &P.b, fb, 0, kb * 64, ncol / 64, ti.e);
-          } else {
-            tma_load_3d_cta2(b, &P.b, fb, ncol, kb * 64, ti.e);
-            tma_load_3d_cta2(b + kGmTile / 2, &P.b, fb, ncol + 64, kb * 64, ti.e);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 4 * kStep);
+#pragma unroll
+          for (int p = 0; p < PLANES; ++p) {
+            uint8_t *ap = a + p * kGmTile, *bp = b + p * kGmTile;
+            const int e = ti.e + p * P.b_plane;
+            tma_load_2d_cta2(ap, &P.a, fb, kb * 64, ti.m0 + p * P.a_plane);
+            if constexpr (OP == kGroupedForward) {
+              tma_load_3d_cta2(bp, &P.b, fb, kb * 64, ncol, e);
+            } else if (P.b_blocks) {
+              tma_load_4d_cta2(bp, &P.b, fb, 0, kb * 64, ncol / 64, e);
+            } else {
+              tma_load_3d_cta2(bp, &P.b, fb, ncol, kb * 64, e);
+              tma_load_3d_cta2(bp + kGmTile / 2, &P.b, fb, ncol + 64, kb * 64, e);
+            }
           }
         }
       }
     }
     if (!ok && lane == 0 && rank == 0) {
       // a wait gave up: the copies in flight land before the block ends
-      for (int j = 0; j < kGmStages; ++j) {
+      for (int j = 0; j < kStages; ++j) {
         const int i2 = it - 1 - j;
         if (i2 < 0) break;
-        mbar_wait(&full[i2 % kGmStages], (i2 / kGmStages) & 1, nullptr, hdr, 112);
+        mbar_wait(&full[i2 % kStages], (i2 / kStages) & 1, nullptr, hdr, 112);
       }
     }
     __syncwarp();
   } else if (warp == kGmWarpMma) {
     // ------------------------------------------------ MMA (even CTA)
-    if (rank == 0 && lane == 0) {
-      constexpr uint32_t kAMn = OP == kGroupedWgrad ? 1u : 0u, kBMn = OP == kGroupedForward ? 0u : 1u;
+    if (rank == 0) {
+      constexpr uint32_t kAMn = kWgrad ? 1u : 0u, kBMn = OP == kGroupedForward ? 0u : 1u;
       constexpr uint32_t idesc = idesc_bf16_f32(256, 256) | (kAMn << 15) | (kBMn << 16);
-      int it = 0, used = 0;
+      constexpr uint64_t kAK = kAMn ? 2048 / 16 : 32 / 16, kBK = kBMn ? 2048 / 16 : 32 / 16;   // 16 of the summed index
+      const bool leader = elect_one();
+      const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
+      const int tiles = __shfl_sync(0xffffffffu, total, 0);
+      const uint64_t da = kAMn ? smem_desc_sw128_mn(smem_u32(sA)) : smem_desc_sw128(smem_u32(sA));
+      const uint64_t db = kBMn ? smem_desc_sw128_mn(smem_u32(sB)) : smem_desc_sw128(smem_u32(sB));
+      int s = 0, used = 0;
+      uint32_t ph = 0;
       bool ok = true;
-      for (int j = 0; ok && j * nc < total; ++j) {
+      for (int j = 0; ok && j * nc < tiles; ++j) {
         const int tile = gm_index<OP>(j, cluster, nc);
-        if (tile >= total) continue;
-        const GmTile ti = gm_tile<OP>(tile, P.g.E, P.M, P.K, s_tab, ntn, 256, 0);
-        const int nkb = (ti.krows + 63) / 64;      // 0: an empty group, zeros from the epilogue
-        uint32_t d = 0;
+        if (tile >= tiles) continue;
+        const GmTile ti = gm_tile<OP>(tile / P.splits, P.g.E, P.M, P.K, s_tab, ntn, 256, 0);
+        int k0, k1;
+        slices(ti, tile, k0, k1);                  // none: the epilogue writes zeros
+        k0 = __shfl_sync(0xffffffffu, k0, 0);
+        k1 = __shfl_sync(0xffffffffu, k1, 0);
+        const int krows = __shfl_sync(0xffffffffu, ti.krows, 0);
         int acc = 0;
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const bool first = kb % kGmChunk<OP> == 0;
+        for (int kb = k0; kb < k1; ++kb) {
+          const bool first = (kb - k0) % kGmChunk<F32> == 0;
           if (first) {
-            acc = used & 1;
-            const uint32_t aph = (used >> 1) & 1;
+            acc = used % kAccs;
+            ok = warp_wait(&tempty[acc], ((used / kAccs) & 1) ^ 1, abort, hdr, 113);
+            if (!ok) break;
             ++used;
-            if (!mbar_wait(&tempty[acc], aph ^ 1, abort, hdr, 113)) { ok = false; break; }
             tc_fence_after();
-            d = tmem + acc * 256;
           }
-          const int s = it % kGmStages;
-          const uint32_t ph = (it / kGmStages) & 1;
-          if (!mbar_wait<OP == kGroupedWgrad>(&full[s], ph, abort, hdr, 114)) { ok = false; break; }
+          ok = warp_wait<kWgrad>(&full[s], ph, abort, hdr, 114);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t a0 = smem_u32(sA + s * kGmTile);
-          const uint32_t b0 = smem_u32(sB + s * kGmTile);
           // wgrad: the steps of 16 rows that hold one of the group's
-          const int steps = OP == kGroupedWgrad ? min(4, (ti.krows - kb * 64 + 15) / 16) : 4;
+          const int steps = kWgrad ? min(4, (krows - kb * 64 + 15) / 16) : 4;
+          const bool last = kb + 1 == k1 || (kb + 1 - k0) % kGmChunk<F32> == 0;
+          if (leader) {
+            const uint64_t as = da + static_cast<uint64_t>(s * (kStep / 16)), bs = db + static_cast<uint64_t>(s * (kStep / 16));
+            if constexpr (PLANES == 1) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            if (kk >= steps) break;
-            const uint64_t ad = kAMn ? smem_desc_sw128_mn(a0 + kk * 2048) : smem_desc_sw128(a0 + kk * 32);
-            const uint64_t bd = kBMn ? smem_desc_sw128_mn(b0 + kk * 2048) : smem_desc_sw128(b0 + kk * 32);
-            umma_f16_cta2(d, ad, bd, idesc, (!first || kk) ? 1u : 0u);
+              for (int kk = 0; kk < 4; ++kk)
+                if (kk < steps)
+                  umma_f16_cta2(base + acc * 256, as + kk * kAK, bs + kk * kBK, idesc, (!first || kk) ? 1u : 0u);
+            } else {
+              // the products of planes pa and pb: h h' in the first accumulator, the others in the second
+              constexpr int kPa[6] = {0, 2, 0, 1, 1, 0}, kPb[6] = {0, 0, 2, 1, 0, 1};
+#pragma unroll
+              for (int c = 0; c < 6; ++c)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  if (kk < steps)
+                    umma_f16_cta2(base + (c ? 256 : 0), as + kPa[c] * (kGmTile / 16) + kk * kAK,
+                                  bs + kPb[c] * (kGmTile / 16) + kk * kBK, idesc, (!first || kk || c > 1) ? 1u : 0u);
+            }
+            umma_commit_cta2_mc(&empty[s], 0x3);
+            if (last) umma_commit_cta2_mc(&tfull[acc], 0x3);
           }
-          umma_commit_cta2_mc(&empty[s], 0x3);
-          if (kb + 1 == nkb || (kb + 1) % kGmChunk<OP> == 0) umma_commit_cta2_mc(&tfull[acc], 0x3);
+          __syncwarp();
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
         }
       }
-      umma_commit_cta2_mc(drained, 0x1);
-      mbar_wait(drained, 0, nullptr, hdr, 115);
+      if (leader) umma_commit_cta2_mc(drained, 0x1);
+      __syncwarp();
+      warp_wait(drained, 0, nullptr, hdr, 115);
     }
     __syncwarp();
   } else {
@@ -255,63 +327,78 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
     for (int j = 0; j * nc < total; ++j) {
       const int tile = gm_index<OP>(j, cluster, nc);
       if (tile >= total) continue;
-      const GmTile ti = gm_tile<OP>(tile, P.g.E, P.M, P.K, s_tab, ntn, 256, rank);
+      const GmTile ti = gm_tile<OP>(tile / P.splits, P.g.E, P.M, P.K, s_tab, ntn, 256, rank);
       const int rem = min(32, ti.mrows - quad * 32);            // rows of the group in this warp's 32
+      const bool counts = quad * 32 + lane < ti.mvalid;         // this lane's row is not padding
       const int col0 = ti.n0 + half * 128;
       const int row = ti.m0 + quad * 32;
-      if constexpr (OP == kGroupedWgrad) {
+      if constexpr (F32) {
         // the sums of all slices, chunk by chunk in registers
         float sum[128];
 #pragma unroll
         for (int c = 0; c < 128; ++c) sum[c] = 0.f;
-        const int chunks = ((ti.krows + 63) / 64 + kGmChunk<OP> - 1) / kGmChunk<OP>;
+        int k0, k1;
+        slices(ti, tile, k0, k1);
         bool ok = true;
-        for (int i = 0; i < chunks; ++i) {
-          const int acc = used & 1;
-          const uint32_t aph = (used >> 1) & 1;
-          ++used;
-          ok = warp_wait(&tfull[acc], aph, abort, hdr, 116);
+        for (int kb = k0; kb < k1; kb += kGmChunk<F32>) {
+          const int acc = used % kAccs;
+          ok = warp_wait(&tfull[acc], (used / kAccs) & 1, abort, hdr, 116);
           if (!ok) break;
+          ++used;
           tc_fence_after();
           const uint32_t tb = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 256 + half * 128;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            uint32_t r[16];
-            tmem_ld_32x32b_x16(tb + 16 * c, r);
-            tmem_ld_wait();
+          for (int h = 0; h < (PLANES == 1 ? 1 : 2); ++h)
 #pragma unroll
-            for (int q = 0; q < 16; ++q) sum[16 * c + q] += __uint_as_float(r[q]);
-          }
+            for (int c = 0; c < 8; ++c) {
+              uint32_t r[16];
+              tmem_ld_32x32b_x16(tb + (PLANES == 1 ? 0 : 256 - 256 * h) + 16 * c, r);    // the small products first
+              tmem_ld_wait();
+#pragma unroll
+              for (int q = 0; q < 16; ++q) sum[16 * c + q] += __uint_as_float(r[q]);
+            }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_signal_cluster(acc ? te1 : te0);
         }
         if (!ok) break;
+        const int sp = tile % P.splits;
+        const int64_t orow = kWgrad ? (static_cast<int64_t>(ti.e) + static_cast<int64_t>(sp) * P.out_plane) * P.M + row
+                                    : row + static_cast<int64_t>(sp) * P.out_plane;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int col = col0 + 32 * c;
           if (rem <= 0 || col >= P.N) continue;    // warp-uniform
           if (lane == 0) bulk_wait_read();         // the previous piece's store has read the stage
           __syncwarp();
+          // 128-byte rows, 16-byte chunk q of row i at chunk q ^ (i & 7)
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             *reinterpret_cast<float4*>(wstage + lane * 128 + ((q ^ (lane & 7)) << 4)) =
-                make_float4(sum[32 * c + 4 * q], sum[32 * c + 4 * q + 1], sum[32 * c + 4 * q + 2], sum[32 * c + 4 * q + 3]);
-          if (P.out_aligned) {
+                counts ? make_float4(sum[32 * c + 4 * q], sum[32 * c + 4 * q + 1], sum[32 * c + 4 * q + 2], sum[32 * c + 4 * q + 3])
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+          if (P.out_aligned && (kWgrad || rem == 32)) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_3d(&P.out, wstage, col, row, ti.e);
+              if constexpr (kWgrad) tma_store_3d(&P.out, wstage, col, row, ti.e + sp * P.out_plane);
+              else tma_store_2d(&P.out, wstage, col, static_cast<int>(orow));
               bulk_commit();
             }
-          } else {
+            continue;
+          }
+          __syncwarp();
+          float* o = static_cast<float*>(P.outp) + orow * P.ldo + col;
+          if (P.out_aligned) {
+            // a group's ragged end: 16 bytes a lane, four rows at once
+            if (col + 4 * (lane & 7) < P.N)
+              for (int i = lane >> 3; i < rem; i += 4)
+                *reinterpret_cast<float4*>(o + i * P.ldo + 4 * (lane & 7)) =
+                    *reinterpret_cast<const float4*>(wstage + i * 128 + (((lane & 7) ^ (i & 7)) << 4));
+          } else if (col + lane < P.N) {
             // rows that start anywhere: element by element
-            __syncwarp();
-            float* o = static_cast<float*>(P.outp) + (static_cast<int64_t>(ti.e) * P.M + row) * P.N + col + lane;
-            if (col + lane < P.N)
-              for (int i = 0; i < rem; ++i)
-                o[static_cast<int64_t>(i) * P.N] =
-                    *reinterpret_cast<const float*>(wstage + i * 128 + ((((lane >> 2) ^ (i & 7)) << 4) | ((lane & 3) << 2)));
+            for (int i = 0; i < rem; ++i)
+              o[i * P.ldo + lane] = *reinterpret_cast<const float*>(wstage + i * 128 + ((((lane >> 2) ^ (i & 7)) << 4) | ((lane & 3) << 2)));
           }
         }
       } else {
@@ -320,7 +407,6 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
         ++used;
         if (!warp_wait(&tfull[acc], aph, abort, hdr, 116)) break;
         tc_fence_after();
-        const bool counts = quad * 32 + lane < ti.mvalid;       // this lane's row is not padding
         const uint32_t tb = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 256 + half * 128;
 #pragma unroll 1
         for (int c = 0; c < 128; c += 64) {
@@ -352,6 +438,116 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
   cluster_sync();
   tc_fence_after();
   if (warp == kGmWarpMma) tmem_dealloc_cta2(tmem, 512);
+}
+
+// Whether row r holds an assignment (1), is padding of a group (0) or lies
+// outside every group (-1).  Called by a full warp.
+__device__ __forceinline__ int row_kind(const GroupTables& g, int64_t r) {
+  if (g.offsets == nullptr) return 1;
+  const int lane = threadIdx.x & 31;
+  int kind = -1;
+  for (int e = lane; e < g.E; e += 32) {
+    const GroupSpan s = group_span(g, e);
+    if (r >= s.r0 && r < s.r1) kind = r < s.r0 + s.n ? 1 : 0;
+  }
+  const uint32_t valid = __ballot_sync(0xffffffffu, kind == 1), pad = __ballot_sync(0xffffffffu, kind == 0);
+  return valid ? 1 : pad ? 0 : -1;
+}
+
+// fp32 rows as three planes of bf16, [3, rows, pitch8(cols)]; rows that hold no
+// assignment as zeros.  *flag is set where a value has no such planes: an
+// infinity, a NaN, above 2^127 (h may round to infinity) or below 2^-100 but
+// not zero (l may fall below bf16's smallest).  A warp a row, the tensors' rows
+// one after the other.
+__device__ __forceinline__ void split_vector(const float (&x)[8], uint4 (&planes)[3], bool& bad) {
+  uint32_t p[3][4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float a = x[2 * j], b = x[2 * j + 1];
+    const float lo = fminf(fabsf(a) == 0.f ? 1.f : fabsf(a), fabsf(b) == 0.f ? 1.f : fabsf(b));
+    bad |= !(fabsf(a) < 0x1p127f) | !(fabsf(b) < 0x1p127f) | (lo < 0x1p-100f);
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      p[q][j] = pack_bf16x2(a, b);
+      a -= __uint_as_float(p[q][j] << 16);
+      b -= __uint_as_float(p[q][j] & 0xffff0000u);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 3; ++q) planes[q] = make_uint4(p[q][0], p[q][1], p[q][2], p[q][3]);
+}
+
+__global__ void __launch_bounds__(256)
+split_kernel(const SplitTensors S, const GroupTables g, int* flag) {
+  pdl_enter();
+  int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  int i = 0;
+  while (i < S.n && r >= S.t[i].rows) r -= S.t[i++].rows;
+  if (i == S.n) return;
+  const SplitTensor T = S.t[i];
+  const bool valid = !T.grouped || row_kind(g, r) == 1;
+  const int per = (T.cols + 7) / 8, lane = threadIdx.x & 31;
+  const float* s = static_cast<const float*>(T.src) + r * T.cols;
+  uint4* dst = static_cast<uint4*>(T.dst) + r * per;
+  const bool vec = T.cols % 4 == 0;            // rows start on 16 bytes
+  bool bad = false;
+  for (int v0 = lane; v0 < per; v0 += 64) {    // two vectors of eight columns a lane
+    float x[2][8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 8; j += 4) {
+        const int c = 8 * (v0 + 32 * h) + j;
+        if (vec) {
+          const float4 f = valid && c < T.cols ? __ldg(reinterpret_cast<const float4*>(s + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          x[h][j] = f.x; x[h][j + 1] = f.y; x[h][j + 2] = f.z; x[h][j + 3] = f.w;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[h][j + e] = valid && c + e < T.cols ? __ldg(s + c + e) : 0.f;
+        }
+      }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 p[3];
+      split_vector(x[h], p, bad);
+      if (v0 + 32 * h < per)
+#pragma unroll
+        for (int q = 0; q < 3; ++q) dst[q * T.rows * per + v0 + 32 * h] = p[q];
+    }
+  }
+  if (bad) *flag = 1;
+}
+
+// out[r, c] = the sum over the parts, in order, in T; padding rows zero, rows
+// outside the groups left alone.  A warp a row.
+template <typename T>
+__global__ void __launch_bounds__(256)
+join_kernel(const float* __restrict__ parts, T* __restrict__ out, const GroupTables g, const int64_t rows, const int cols,
+            const int pitch, const int splits, const int* skip) {
+  pdl_enter();
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (r >= rows || (skip != nullptr && *skip != 0)) return;
+  const int kind = row_kind(g, r);
+  if (kind < 0) return;
+  const bool vec = cols % 4 == 0;
+  for (int c = 4 * (threadIdx.x & 31); c < cols; c += 128) {
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (kind == 1)
+      for (int s = 0; s < splits; ++s) {
+        const float4 v = *reinterpret_cast<const float4*>(parts + (s * rows + r) * pitch + c);
+        sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
+      }
+    T* o = out + r * cols + c;
+    const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+    if (vec) {
+      if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+      else *reinterpret_cast<float4*>(o) = sum;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i < cols) o[i] = static_cast<T>(v[i]);
+    }
+  }
 }
 
 // Rows of 2-byte elements that start anywhere -> rows of pitch8(cols), zeros
@@ -449,17 +645,17 @@ static bool map_rows_mn(CUtensorMap* m, const void* p, int cols, int64_t rows, i
   const uint32_t b[2] = {64, 64};
   return make_map(m, kBf, 2, reinterpret_cast<uint64_t>(p), d, s, b, kSw);
 }
-// Weight gradients fp32 [E, N, K]: store boxes of 32 x 32.
-static bool map_out_weights(CUtensorMap* m, void* p, int K, int N, int E) {
-  const uint64_t d[3] = {static_cast<uint64_t>(K), static_cast<uint64_t>(N), static_cast<uint64_t>(E)};
-  const uint64_t s[2] = {static_cast<uint64_t>(K) * 4, static_cast<uint64_t>(K) * 4 * N};
+// fp32 [planes, rows, cols], rows of `pitch` elements: store boxes of 32 x 32.
+static bool map_out_f32(CUtensorMap* m, void* p, int cols, int64_t pitch, int64_t rows, int64_t planes) {
+  const uint64_t d[3] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows), static_cast<uint64_t>(planes)};
+  const uint64_t s[2] = {static_cast<uint64_t>(pitch) * 4, static_cast<uint64_t>(pitch) * 4 * rows};
   const uint32_t b[3] = {32, 32, 1};
-  return make_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, reinterpret_cast<uint64_t>(p), d, s, b, kSw);
+  return make_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, planes ? 3 : 2, reinterpret_cast<uint64_t>(p), d, s, b, kSw);
 }
 
-template <int OP>
+template <int OP, int PLANES, bool F32>
 static cudaError_t gm_launch(const GmParams& p, int64_t tiles, WsHeader* hdr, cudaStream_t st) {
-  auto fn = grouped_tc_kernel<OP>;
+  auto fn = grouped_tc_kernel<OP, PLANES, F32>;
   if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(fn), kGmSmem);
   if (e != cudaSuccess) return e;
@@ -467,36 +663,102 @@ static cudaError_t gm_launch(const GmParams& p, int64_t tiles, WsHeader* hdr, cu
   return launch_dependent_kernel(fn, dim3(static_cast<unsigned>(2 * pairs)), dim3(kGmThreads), kGmSmem, st, p, hdr);
 }
 
-cudaError_t launch_grouped_tc(int op, const GroupedArgs& a, WsHeader* hdr, cudaStream_t st) {
+// Tiles of a call, and the parts that its sums are cut into: as many as the
+// pairs of SMs have room for, where that saves more slices in a row than the
+// second launch costs.  A slice takes 0.3 us, of three planes six times that;
+// a part has 2.4 us of them at least (K = 8192, N = 512, 300 rows 47 -> 17 us;
+// wgrad 768 x 768 over 16384 rows 107 -> 29 us; with 12 slices saved, 10 us
+// became 15).
+static int64_t gm_tiles(int op, const GroupTables& g, int K, int N) {
+  if (op == kGroupedWgrad) return g.E * ((N + 255) / 256) * static_cast<int64_t>((K + 255) / 256);
+  return row_tiles256(g) * (((op == kGroupedForward ? N : K) + 255) / 256);
+}
+int grouped_splits(int op, const GroupTables& g, int K, int N, int planes) {
+  const int64_t slices = op == kGroupedWgrad ? g.rows / (64 * static_cast<int64_t>(g.E))
+                                             : ((op == kGroupedForward ? K : N) + 63) / 64;
+  const int64_t room = (num_sms() / 2) / std::max<int64_t>(1, gm_tiles(op, g, K, N));
+  const int64_t weight = planes == 3 ? 6 : 1;
+  const int64_t parts = std::min(room, std::min(slices, slices * weight / 8));
+  return parts > 1 && (slices - slices / parts) * weight >= 24 ? static_cast<int>(parts) : 1;
+}
+static int pitch4(int n) { return (n + 3) / 4 * 4; }
+size_t grouped_parts_bytes(int op, const GroupTables& g, int K, int N, int splits) {
+  if (splits < 2) return 0;
+  const int64_t rows = op == kGroupedWgrad ? static_cast<int64_t>(g.E) * N : g.rows;
+  return 4 * static_cast<size_t>(splits) * rows * pitch4(op == kGroupedForward ? N : K);
+}
+
+// One operand set: bf16 as given (planes 1), or three planes of bf16.
+template <int PLANES>
+static cudaError_t gm_run(int op, const GroupedArgs& a, const GroupedTcExtras& x, WsHeader* hdr, cudaStream_t st) {
   GmParams p;
   memset(&p, 0, sizeof(p));
+  const bool fwd = op == kGroupedForward, wgrad = op == kGroupedWgrad, parts = x.splits > 1;
+  const int64_t kp = pitch8(a.K), np = pitch8(a.N), R = a.g.rows;
+  const int E = a.g.E;
   p.g = a.g;
-  p.outp = a.out;
-  const int64_t kp = pitch8(a.K), np = pitch8(a.N);
-  bool ok;
-  if (op == kGroupedWgrad) {
-    p.M = a.N;
-    p.N = a.K;
-    p.a_blocks = a.N % 64 == 0;
-    p.b_blocks = a.K % 64 == 0;
-    p.out_aligned = a.K % 4 == 0;
-    ok = map_rows_mn(&p.a, a.dys, a.N, a.g.rows, np, p.a_blocks) &&
-         map_rows_mn(&p.b, a.xs, a.K, a.g.rows, kp, p.b_blocks) &&
-         (!p.out_aligned || map_out_weights(&p.out, a.out, a.K, a.N, a.g.E));
-    const int64_t tiles = a.g.E * ((a.N + 255) / 256) * static_cast<int64_t>((a.K + 255) / 256);
-    return ok ? gm_launch<kGroupedWgrad>(p, tiles, hdr, st) : cudaErrorInvalidValue;
-  }
-  const bool fwd = op == kGroupedForward;
+  p.M = wgrad ? a.N : 0;
   p.N = fwd ? a.N : a.K;
   p.K = fwd ? a.K : a.N;
-  p.out_aligned = p.N % 8 == 0;
-  p.b_blocks = !fwd && a.K % 64 == 0;
-  ok = fwd ? map_kmajor(&p.a, a.xs, a.K, a.g.rows, kp) && map_weights(&p.b, a.w, a.K, kp, a.N, a.g.E)
-           : map_kmajor(&p.a, a.dys, a.N, a.g.rows, np) && map_weights_mn(&p.b, a.w, a.K, kp, a.N, a.g.E, p.b_blocks);
-  ok = ok && (!p.out_aligned || map_out_rows(&p.out, a.out, p.N, a.g.rows, 64));
+  p.splits = x.splits;
+  p.skip = x.skip;
+  p.a_plane = static_cast<int>(R);
+  p.b_plane = wgrad ? static_cast<int>(R) : E;
+  const bool f32 = wgrad || PLANES == 3 || parts;
+  p.outp = parts ? x.parts : a.out;
+  p.ldo = parts ? pitch4(p.N) : p.N;
+  p.out_plane = wgrad ? E : static_cast<int>(R);
+  p.out_aligned = p.ldo % (f32 ? 4 : 8) == 0;
+  bool ok;
+  if (wgrad) {
+    p.a_blocks = a.N % 64 == 0;
+    p.b_blocks = a.K % 64 == 0;
+    ok = map_rows_mn(&p.a, a.dys, a.N, PLANES * R, np, p.a_blocks) && map_rows_mn(&p.b, a.xs, a.K, PLANES * R, kp, p.b_blocks);
+  } else if (fwd) {
+    ok = map_kmajor(&p.a, a.xs, a.K, PLANES * R, kp) && map_weights(&p.b, a.w, a.K, kp, a.N, PLANES * E);
+  } else {
+    p.b_blocks = a.K % 64 == 0;
+    ok = map_kmajor(&p.a, a.dys, a.N, PLANES * R, np) && map_weights_mn(&p.b, a.w, a.K, kp, a.N, PLANES * E, p.b_blocks);
+  }
+  if (ok && p.out_aligned)
+    ok = !f32 ? map_out_rows(&p.out, p.outp, p.N, R, 64)
+         : wgrad ? map_out_f32(&p.out, p.outp, p.N, p.ldo, a.N, static_cast<int64_t>(p.splits) * E)
+                 : map_out_f32(&p.out, p.outp, p.N, p.ldo, p.splits * R, 0);
   if (!ok) return cudaErrorInvalidValue;
-  const int64_t tiles = row_tiles256(a.g) * ((p.N + 255) / 256);
-  return fwd ? gm_launch<kGroupedForward>(p, tiles, hdr, st) : gm_launch<kGroupedDgrad>(p, tiles, hdr, st);
+  const int64_t tiles = gm_tiles(op, a.g, a.K, a.N) * p.splits;
+  if (wgrad) return gm_launch<kGroupedWgrad, PLANES, true>(p, tiles, hdr, st);
+  if constexpr (PLANES == 1)
+    if (!parts)
+      return fwd ? gm_launch<kGroupedForward, 1, false>(p, tiles, hdr, st) : gm_launch<kGroupedDgrad, 1, false>(p, tiles, hdr, st);
+  return fwd ? gm_launch<kGroupedForward, PLANES, true>(p, tiles, hdr, st) : gm_launch<kGroupedDgrad, PLANES, true>(p, tiles, hdr, st);
+}
+
+cudaError_t launch_grouped_tc(int op, const GroupedArgs& a, const GroupedTcExtras& x, WsHeader* hdr, cudaStream_t st) {
+  return x.planes == 3 ? gm_run<3>(op, a, x, hdr, st) : gm_run<1>(op, a, x, hdr, st);
+}
+
+cudaError_t launch_grouped_split(const SplitTensors& t, const GroupTables& g, int* flag, cudaStream_t st) {
+  int64_t rows = 0;
+  for (int i = 0; i < t.n; ++i) rows += t.t[i].rows;
+  const int64_t blocks = (rows + 7) / 8;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  return launch_dependent_kernel(split_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, t, g, flag);
+}
+
+cudaError_t launch_grouped_join(int op, int dtype, const GroupedArgs& a, const GroupedTcExtras& x, cudaStream_t st) {
+  const bool wgrad = op == kGroupedWgrad;
+  const int64_t rows = wgrad ? static_cast<int64_t>(a.g.E) * a.N : a.g.rows;
+  const int cols = op == kGroupedForward ? a.N : a.K;
+  const GroupTables g = wgrad ? GroupTables{nullptr, nullptr, rows, 1} : a.g;
+  const int64_t blocks = (rows + 7) / 8;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(blocks));
+  const float* parts = static_cast<const float*>(x.parts);
+  if (wgrad || dtype == kDtypeF32)
+    return launch_dependent_kernel(join_kernel<float>, grid, dim3(256), 0, st, parts, static_cast<float*>(a.out), g, rows,
+                                   cols, pitch4(cols), x.splits, x.skip);
+  return launch_dependent_kernel(join_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, parts, static_cast<__nv_bfloat16*>(a.out),
+                                 g, rows, cols, pitch4(cols), x.splits, x.skip);
 }
 
 }  // namespace mm

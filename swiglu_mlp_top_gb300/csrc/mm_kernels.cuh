@@ -488,14 +488,40 @@ struct GroupedArgs {
   GroupTables g;
   int K, N;
 };
-cudaError_t launch_grouped_simt(int op, const GroupedArgs& p, cudaStream_t st);      // fp32
+// fp32 multiply-adds (grouped_simt.cu); only_if not null: nothing is done where
+// it holds 0 (not for the forward pass of up to f32_stream_rows).
+constexpr int f32_stream_rows(int E) { return 16 + 4 * E; }
+cudaError_t launch_grouped_simt(int op, const GroupedArgs& p, const int* only_if, cudaStream_t st);
 
-// The same on the tensor cores for bf16 (grouped_tc.cu).  Rows start on 16
-// bytes where a multiple of 8 elements makes a row; operands of other widths
-// come as copies with rows of pitch8() elements, zeros behind the row.
+// On the tensor cores (grouped_tc.cu): bf16 operands (planes 1), or fp32 ones
+// as three planes of bf16 each, [3, rows, pitch8(cols)] (launch_grouped_split).
+// Rows start on 16 bytes: operands of bf16 whose width is no multiple of 8
+// come as copies with rows of pitch8() elements (launch_repitch).
 constexpr int pitch8(int n) { return (n + 7) / 8 * 8; }
 cudaError_t launch_repitch(const void* src, void* dst, int64_t rows, int cols, cudaStream_t st);
-cudaError_t launch_grouped_tc(int op, const GroupedArgs& p, WsHeader* hdr, cudaStream_t st);
+// fp32 tensors as planes, in one launch; sets *flag where a value cannot be
+// split; rows of a `grouped` tensor without an assignment become zeros.
+struct SplitTensor {
+  const void* src;            // fp32 [rows, cols]
+  void* dst;                  // bf16 [3, rows, pitch8(cols)]
+  int64_t rows;
+  int cols, grouped;
+};
+struct SplitTensors {
+  SplitTensor t[3];
+  int n;
+};
+cudaError_t launch_grouped_split(const SplitTensors& t, const GroupTables& g, int* flag, cudaStream_t st);
+struct GroupedTcExtras {
+  int planes;                 // 1 or 3
+  int splits;                 // parts of the sums (grouped_splits), added by launch_grouped_join
+  void* parts;                // grouped_parts_bytes(); null with one part
+  const int* skip;            // device: nothing is done where it holds something; or null
+};
+int grouped_splits(int op, const GroupTables& g, int K, int N, int planes);
+size_t grouped_parts_bytes(int op, const GroupTables& g, int K, int N, int splits);
+cudaError_t launch_grouped_tc(int op, const GroupedArgs& p, const GroupedTcExtras& x, WsHeader* hdr, cudaStream_t st);
+cudaError_t launch_grouped_join(int op, int dtype, const GroupedArgs& p, const GroupedTcExtras& x, cudaStream_t st);
 
 // Products of 4-bit rows and 4-bit weights on the tensor cores (mx4_tc.cu).
 struct Mx4MatmulArgs {

@@ -6,7 +6,10 @@ value, block_reference.U relative.  A sum of n products in fp32 is off by at
 most n + 1 roundings of 2^-24 on the sum of the terms' magnitudes; inside the
 tensor cores an addition may cut off instead of rounding, a whole step of
 2^-23, so 2 (n + 1) there.  Products of two bf16 or two 4-bit values are
-exact in fp32.
+exact in fp32.  fp32 operands of many rows are multiplied there as three bf16
+parts each (8 + 8 + 8 bits: all of fp32's 24), without the products of parts
+below 2^-25 of the whole: less than one more rounding per product, where the
+six products that are added take no more steps than n sums (16 at a time).
 """
 import torch
 
@@ -56,10 +59,10 @@ def matmul_backward(dy, x, w, plan, before):
     return dx, (dw.view(w.shape), terms.view(w.shape))
 
 
-def close_sum(got, want, terms, n, dtype, cores, what):
+def close_sum(got, want, terms, n, dtype, what):
     """got within half a step of want and the roundings of a sum of n products."""
     u = U[dtype]
-    sums = (2 if cores else 1) * (n + 1) * U32 * terms
+    sums = 2 * (n + 1) * U32 * terms
     close(got, want, u * want.abs() + (1 + u) * sums, what)
 
 

@@ -47,7 +47,7 @@ def check(counts, align, K, N, dtype, whole, start=0, tail=3):
     x, dy = make(rows, K, dtype, gen, whole, plan), make(rows, N, dtype, gen, whole, plan)
     shape = (N, K) if plan is None else (E, N, K)
     w = torch.randint(-2, 3, shape, generator=gen).to(dtype) if whole else (torch.randn(*shape, generator=gen) * 0.1).to(dtype)
-    gplan, cores = on_gpu(plan), dtype == BF
+    gplan = on_gpu(plan)
     xg, wg, dyg = x.cuda(), w.cuda(), dy.cuda()
     status = mm.new_workspace(256)
 
@@ -66,9 +66,9 @@ def check(counts, align, K, N, dtype, whole, start=0, tail=3):
         assert torch.equal(dx.cpu(), wdx.to(dtype)), "dxs"
         assert torch.equal(dw.cpu(), wdw.float()), "dw"
     else:
-        ref.close_sum(y, want, terms, K, dtype, cores, "ys")
-        ref.close_sum(dx, wdx, tdx, N, dtype, cores, "dxs")
-        ref.close_sum(dw, wdw, tdw, longest, F32, cores, "dw")
+        ref.close_sum(y, want, terms, K, dtype, "ys")
+        ref.close_sum(dx, wdx, tdx, N, dtype, "dxs")
+        ref.close_sum(dw, wdw, tdw, longest, F32, "dw")
 
 
 SIZES = [
@@ -95,6 +95,48 @@ def test_products(counts, align, K, N, dtype):
     (16, 16, 1, 2432, 768, "even"), (3, 1, 1, 768, 4864, "skewed"), (64, 4000, 1, 64, 64, "even")])
 def test_many_groups(E, total, align, K, N, how, dtype):
     check(groups(E, total, how), align, K, N, dtype, whole=False)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("counts,align,K,N", [
+    # few tiles with a long sum: cut into parts
+    ([300], 1, 4096, 130), ([300], 1, 130, 4096), ([270, 500], 16, 2050, 72), ([3000], 1, 72, 60), ([100, 4000], 1, 64, 136), ([0, 700], 3, 1030, 257),
+    ([2500, 0], 1, 33, 65)])
+def test_sums_in_parts(counts, align, K, N, dtype):
+    check(counts, align, K, N, dtype, whole=True)
+    check(counts, align, K, N, dtype, whole=False, start=align)
+
+
+def test_fp32_of_every_size():
+    """Values that bf16 parts cannot hold (infinities, NaN, above 2^127, below
+    2^-100) anywhere among the operands: the results are those of fp32 products."""
+    gen = torch.Generator().manual_seed(12)
+    E, K, N, counts = 2, 72, 40, [200, 150]
+    plan = ref.tables(counts, 8)
+    rows = int(plan["offsets"][-1]) + 3
+    gplan = on_gpu(plan)
+    for what, value in (("x", torch.inf), ("x", torch.nan), ("w", -torch.inf), ("x", 1.9 * 2.0 ** 127), ("w", 2.0 ** -120), ("dy", torch.inf), ("dy", 2.0 ** -130)):
+        x, dy, w = torch.randn(rows, K, generator=gen), torch.randn(rows, N, generator=gen), torch.randn(E, N, K, generator=gen)
+        if value == 2.0 ** -120:
+            w = w * value                        # all of them: fp32's accuracy is wanted there too
+        elif value == 2.0 ** -130:
+            dy = dy * value
+        else:
+            {"x": x, "w": w[0], "dy": dy}[what][5, 7] = value
+            if value == 1.9 * 2.0 ** 127:
+                w, dy = w / 64, dy / 64          # no sum overflows
+        y = mm.grouped_matmul(x.cuda(), w.cuda(), gplan, out=torch.zeros(rows, N, device="cuda"))
+        dx, dw = mm.grouped_matmul_backward(dy.cuda(), x.cuda(), w.cuda(), gplan, out=torch.zeros(rows, K, device="cuda"))
+        want, terms = ref.matmul(x, w, plan, torch.zeros(rows, N))
+        (wdx, tdx), (wdw, tdw) = ref.matmul_backward(dy, x, w, plan, torch.zeros(rows, K))
+        for got, exact, size, n, name in ((y, want, terms, K, "ys"), (dx, wdx, tdx, N, "dxs"), (dw, wdw, tdw, 200, "dw")):
+            got = got.cpu()
+            fine = exact.abs() < 2.0 ** 127
+            assert torch.equal(torch.isnan(got), torch.isnan(exact)), (what, value, name)
+            assert bool((got[exact.abs() == torch.inf] == exact[exact.abs() == torch.inf].float()).all()), (what, value, name)
+            # results near fp32's smallest have steps of 2^-149
+            close(torch.where(fine, got.double(), 0.0), torch.where(fine, exact, 0.0),
+                  torch.where(fine, 2.0 ** -24 * exact.abs() + 2 * (n + 1) * 2.0 ** -24 * size + n * 2.0 ** -149, 0.0), name)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -263,7 +305,7 @@ def check_mx4(counts, align, K, N, four, whole, tail=3):
         assert terms.max() < 2 ** 20
         assert torch.equal(y.cpu(), want.to(BF))
     else:
-        ref.close_sum(y, want, terms, K, BF, True, "ys")
+        ref.close_sum(y, want, terms, K, BF, "ys")
 
 
 @pytest.mark.parametrize("four", [True, False])
@@ -291,7 +333,7 @@ def test_mx4_scales_of_every_size(rows, four):
     wq, wv = mm.mx4_quantize(w.cuda()), ref.stored(w)[1]
     xg, xv = (mm.mx4_quantize(x.cuda()), ref.stored(x)[1]) if four else (x.cuda(), x)
     want, terms = ref.matmul(xv, wv, None, torch.zeros(rows, N))
-    ref.close_sum(mm.mx4_matmul(xg, wq), want, terms, K, BF, True, "ys")
+    ref.close_sum(mm.mx4_matmul(xg, wq), want, terms, K, BF, "ys")
 
 
 @pytest.mark.parametrize("four", [True, False])
