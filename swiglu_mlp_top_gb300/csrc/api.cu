@@ -1221,18 +1221,18 @@ static size_t grouped_bytes(int64_t rows, int K, int N, int E, int dtype, bool b
 // Makes the operands of `a` ready that are not null: as given, or their copies.
 static cudaError_t grouped_operands(const GroupedPlan& L, GroupedArgs& a, void* ws, cudaStream_t st) {
   const int64_t wrows = static_cast<int64_t>(a.g.E) * a.N;
-  struct { const void** p; size_t at; int64_t rows; int cols, grouped; } each[3] = {
-      {&a.xs, L.xs, a.g.rows, a.K, 1}, {&a.dys, L.dys, a.g.rows, a.N, 1}, {&a.w, L.w, wrows, a.K, 0}};
+  struct { const void** p; size_t at; int64_t rows; int cols, per_group; } each[3] = {
+      {&a.xs, L.xs, a.g.rows, a.K, 0}, {&a.dys, L.dys, a.g.rows, a.N, 0}, {&a.w, L.w, wrows, a.K, a.N}};
   SplitTensors t;
   t.n = 0;
   for (auto& o : each) {
     if (*o.p == nullptr || L.planes == 0 || (L.planes == 1 && o.cols % 8 == 0)) continue;
     void* to = ws_at(ws, o.at);
     if (L.planes == 3) {
-      t.t[t.n++] = SplitTensor{*o.p, to, o.rows, o.cols, o.grouped};
+      t.t[t.n++] = SplitTensor{*o.p, to, o.rows, o.cols, o.per_group};
     } else {
       const void* src = *o.p;
-      const cudaError_t e = counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_repitch(src, to, o.rows, o.cols, st); });
+      const cudaError_t e = counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_repitch(src, to, o.rows, o.cols, a.g, o.per_group, st); });
       if (e != cudaSuccess) return e;
     }
     *o.p = to;
@@ -1326,14 +1326,16 @@ int mm_grouped_matmul_backward(const void* dys, const void* xs, const void* w,
 }
 
 static int mx4_impl(bool quantise, const void* x, void* x_out, void* codes, uint8_t* exps, int64_t R,
-                    int64_t C, int dtype, const int32_t* n_rows, void* stream) {
+                    int64_t C, int dtype, const int32_t* n_rows, void* stream, const GroupTables& g = GroupTables{},
+                    int per_group = 0) {
   if (!valid_dtype(dtype) || R < 0 || C < 1) return MM_ERR_INVALID_ARG;
   if (C > MM_GROUPED_MAX_DIM || R > 0x7fffffff) return MM_ERR_UNSUPPORTED;
   if (R == 0) return MM_OK;
   if (!present16(quantise ? x : x_out) || !present16(codes) || !present16(exps) || !aligned4(n_rows))
     return MM_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const Mx4Args a{x, x_out, static_cast<uint8_t*>(codes), exps, n_rows, R, static_cast<int>(C)};
+  const Mx4Args a{x, x_out, static_cast<uint8_t*>(codes), exps, n_rows, R, static_cast<int>(C), g,
+                  g.offsets ? per_group : 0};
   cudaError_t e = counted_launch(MM_KERNEL_MX4, st, [&] { return launch_mx4(dtype, quantise, a, st); });
   return e == cudaSuccess ? MM_OK : cuda_fail(e, quantise ? "mx4 quantize" : "mx4 dequantize");
 }
@@ -1386,7 +1388,7 @@ int mm_mx4_matmul(const void* x, const uint8_t* x_exps, const void* w_codes, con
     return e == cudaSuccess ? MM_OK : cuda_fail(e, "mx4 matmul");
   }
   const int rc = mx4_impl(false, nullptr, ws_at(workspace, L.w), const_cast<void*>(w_codes), const_cast<uint8_t*>(w_exps),
-                          static_cast<int64_t>(E) * N, K, kDtypeBF16, nullptr, stream);
+                          static_cast<int64_t>(E) * N, K, kDtypeBF16, nullptr, stream, GroupTables{offsets, counts, rows, E}, N);
   if (rc != MM_OK) return rc;
   return mm_grouped_matmul(x, ws_at(workspace, L.w), offsets, counts, rows, K, N, E, kDtypeBF16, ys,
                            ws_at(workspace, L.product), L.total - L.product, status_ws, stream);

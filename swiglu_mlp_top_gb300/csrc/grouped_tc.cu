@@ -4,9 +4,10 @@
 //   dgrad    dxs = dys w[e]       A = dys [rows, N]  K-major,   B = w[e] with its K contiguous (MN-major)
 //   wgrad    dw[e] = dys^T xs     A = dys, B = xs, both MN-major; the summed index is the group's rows
 //
-// A CTA pair makes a tile of 256 x 256 (tcgen05.mma.cta_group::2: 128 rows of
-// A and half of B in each CTA's shared memory), in slices of 64 of the summed
-// index through a ring of six stages; two accumulators, so that the epilogue
+// A CTA pair makes a tile of 256 x 256, or 256 x 128 where those fit into half
+// the pairs of SMs (tcgen05.mma.cta_group::2: 128 rows of A and half of B in
+// each CTA's shared memory), in slices of 64 of the summed index through a
+// ring of six stages; two accumulators, so that the epilogue
 // of one tile runs under the products of the next.  Warps: 8 epilogue, 1 TMA,
 // 1 MMA (even CTA; it goes through its loop as a whole and issues from one
 // lane, which keeps descriptors in uniform registers).
@@ -53,8 +54,9 @@ struct GmParams {
   GroupTables g;
   int M;              // wgrad: rows of a dw matrix
   int N;              // columns of the result
+  int nt;             // columns of a tile: 256 or 128
   int K;              // forward, dgrad: length of the sum
-  int a_blocks, b_blocks;   // the MN-major map has 64-column blocks as a dimension: one box for both
+  int a_blocks, b_blocks;   // the MN-major map has 64-column blocks as a dimension: so many in a box
   int a_plane, b_plane;     // three planes: rows (b of forward and dgrad: experts) from one to the next
   int splits;         // parts of the sum
   int out_plane;      // rows (wgrad: experts) of a part's result
@@ -91,7 +93,8 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
   const int cluster = blockIdx.x >> 1, nc = gridDim.x >> 1;
-  const int ntn = (P.N + 255) / 256;
+  const int ntn = (P.N + P.nt - 1) / P.nt;
+  const int b_bytes = P.nt / 2 * 128;          // of one tile of B in a CTA
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -142,8 +145,8 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
     for (int j = 0; ok && j * nc < total; ++j) {
       const int tile = gm_index<OP>(j, cluster, nc);
       if (tile >= total) continue;               // the last round's missing tiles
-      const GmTile ti = gm_tile<OP>(tile / P.splits, P.g.E, P.M, P.K, s_tab, ntn, 256, rank);
-      const int ncol = ti.n0 + 128 * rank;       // this CTA's half of the columns
+      const GmTile ti = gm_tile<OP>(tile / P.splits, P.g.E, P.M, P.K, s_tab, ntn, P.nt, rank);
+      const int ncol = ti.n0 + P.nt / 2 * rank;  // this CTA's half of the columns
       int k0, k1;
       slices(ti, tile, k0, k1);
       for (int kb = k0; kb < k1; ++kb, ++it) {
@@ -159,7 +162,7 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
           const int krow = ti.k0 + kb * 64, rows = ti.krows - kb * 64;
           if (rows >= 64) {
             if (lane == 0) {
-              if (rank == 0) mbar_arrive_expect_tx(&full[s], 4 * kStep);
+              if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * PLANES * (kGmTile + b_bytes));
               else mbar_signal_cluster(fb);
 #pragma unroll
               for (int p = 0; p < PLANES; ++p) {
@@ -175,13 +178,13 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
                   tma_load_3d_cta2(bp, &P.b, fb, 0, br, ncol / 64);
                 } else {
                   tma_load_2d_cta2(bp, &P.b, fb, ncol, br);
-                  tma_load_2d_cta2(bp + kGmTile / 2, &P.b, fb, ncol + 64, br);
+                  if (P.nt == 256) tma_load_2d_cta2(bp + kGmTile / 2, &P.b, fb, ncol + 64, br);
                 }
               }
             }
           } else {
             if (lane == 0) {
-              mbar_arrive_expect_tx(part, 2 * kStep);
+              mbar_arrive_expect_tx(part, PLANES * (kGmTile + b_bytes));
 #pragma unroll
               for (int p = 0; p < PLANES; ++p) {
                 uint8_t *ap = a + p * kGmTile, *bp = b + p * kGmTile;
@@ -196,7 +199,7 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
                   tma_load_3d(bp, &P.b, part, 0, br, ncol / 64);
                 } else {
                   tma_load_2d(bp, &P.b, part, ncol, br);
-                  tma_load_2d(bp + kGmTile / 2, &P.b, part, ncol + 64, br);
+                  if (P.nt == 256) tma_load_2d(bp + kGmTile / 2, &P.b, part, ncol + 64, br);
                 }
               }
             }
@@ -218,7 +221,7 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
             }
           }
         } else if (lane == 0) {
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 4 * kStep);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * PLANES * (kGmTile + b_bytes));
 #pragma unroll
           for (int p = 0; p < PLANES; ++p) {
             uint8_t *ap = a + p * kGmTile, *bp = b + p * kGmTile;
@@ -230,7 +233,7 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
               tma_load_4d_cta2(bp, &P.b, fb, 0, kb * 64, ncol / 64, e);
             } else {
               tma_load_3d_cta2(bp, &P.b, fb, ncol, kb * 64, e);
-              tma_load_3d_cta2(bp + kGmTile / 2, &P.b, fb, ncol + 64, kb * 64, e);
+              if (P.nt == 256) tma_load_3d_cta2(bp + kGmTile / 2, &P.b, fb, ncol + 64, kb * 64, e);
             }
           }
         }
@@ -249,7 +252,7 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
     // ------------------------------------------------ MMA (even CTA)
     if (rank == 0) {
       constexpr uint32_t kAMn = kWgrad ? 1u : 0u, kBMn = OP == kGroupedForward ? 0u : 1u;
-      constexpr uint32_t idesc = idesc_bf16_f32(256, 256) | (kAMn << 15) | (kBMn << 16);
+      const uint32_t idesc = idesc_bf16_f32(256, 0) | (static_cast<uint32_t>(P.nt >> 3) << 17) | (kAMn << 15) | (kBMn << 16);
       constexpr uint64_t kAK = kAMn ? 2048 / 16 : 32 / 16, kBK = kBMn ? 2048 / 16 : 32 / 16;   // 16 of the summed index
       const bool leader = elect_one();
       const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
@@ -262,7 +265,7 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
       for (int j = 0; ok && j * nc < tiles; ++j) {
         const int tile = gm_index<OP>(j, cluster, nc);
         if (tile >= tiles) continue;
-        const GmTile ti = gm_tile<OP>(tile / P.splits, P.g.E, P.M, P.K, s_tab, ntn, 256, 0);
+        const GmTile ti = gm_tile<OP>(tile / P.splits, P.g.E, P.M, P.K, s_tab, ntn, P.nt, 0);
         int k0, k1;
         slices(ti, tile, k0, k1);                  // none: the epilogue writes zeros
         k0 = __shfl_sync(0xffffffffu, k0, 0);
@@ -327,10 +330,11 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
     for (int j = 0; j * nc < total; ++j) {
       const int tile = gm_index<OP>(j, cluster, nc);
       if (tile >= total) continue;
-      const GmTile ti = gm_tile<OP>(tile / P.splits, P.g.E, P.M, P.K, s_tab, ntn, 256, rank);
+      const GmTile ti = gm_tile<OP>(tile / P.splits, P.g.E, P.M, P.K, s_tab, ntn, P.nt, rank);
       const int rem = min(32, ti.mrows - quad * 32);            // rows of the group in this warp's 32
       const bool counts = quad * 32 + lane < ti.mvalid;         // this lane's row is not padding
-      const int col0 = ti.n0 + half * 128;
+      const int hc = P.nt / 2;                     // columns of this warp's half
+      const int col0 = ti.n0 + half * hc;
       const int row = ti.m0 + quad * 32;
       if constexpr (F32) {
         // the sums of all slices, chunk by chunk in registers
@@ -346,11 +350,12 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
           if (!ok) break;
           ++used;
           tc_fence_after();
-          const uint32_t tb = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 256 + half * 128;
+          const uint32_t tb = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 256 + half * hc;
 #pragma unroll
           for (int h = 0; h < (PLANES == 1 ? 1 : 2); ++h)
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
+              if (16 * c >= hc) break;
               uint32_t r[16];
               tmem_ld_32x32b_x16(tb + (PLANES == 1 ? 0 : 256 - 256 * h) + 16 * c, r);    // the small products first
               tmem_ld_wait();
@@ -368,7 +373,7 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int col = col0 + 32 * c;
-          if (rem <= 0 || col >= P.N) continue;    // warp-uniform
+          if (rem <= 0 || 32 * c >= hc || col >= P.N) continue;    // warp-uniform
           if (lane == 0) bulk_wait_read();         // the previous piece's store has read the stage
           __syncwarp();
           // 128-byte rows, 16-byte chunk q of row i at chunk q ^ (i & 7)
@@ -407,14 +412,14 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
         ++used;
         if (!warp_wait(&tfull[acc], aph, abort, hdr, 116)) break;
         tc_fence_after();
-        const uint32_t tb = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 256 + half * 128;
+        const uint32_t tb = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 256 + half * hc;
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 64) {
+        for (int c = 0; c < hc; c += 64) {
           uint32_t lo[32], hi[32];
           tmem_ld_32x32b_x32(tb + c, lo);          // every lane (warp-collective)
           tmem_ld_32x32b_x32(tb + c + 32, hi);
           tmem_ld_wait();
-          if (c == 64) {                           // the accumulator is read: the next tile may have it
+          if (c + 64 == hc) {                      // the accumulator is read: the next tile may have it
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_signal_cluster(acc ? te1 : te0);
@@ -485,7 +490,8 @@ split_kernel(const SplitTensors S, const GroupTables g, int* flag) {
   while (i < S.n && r >= S.t[i].rows) r -= S.t[i++].rows;
   if (i == S.n) return;
   const SplitTensor T = S.t[i];
-  const bool valid = !T.grouped || row_kind(g, r) == 1;
+  if (T.per_group && g.offsets != nullptr && group_span(g, static_cast<int>(r / T.per_group)).n == 0) return;
+  const bool valid = T.per_group || row_kind(g, r) == 1;
   const int per = (T.cols + 7) / 8, lane = threadIdx.x & 31;
   const float* s = static_cast<const float*>(T.src) + r * T.cols;
   uint4* dst = static_cast<uint4*>(T.dst) + r * per;
@@ -552,14 +558,16 @@ join_kernel(const float* __restrict__ parts, T* __restrict__ out, const GroupTab
 
 // Rows of 2-byte elements that start anywhere -> rows of pitch8(cols), zeros
 // behind the row; a 16-byte vector a thread, from the two aligned vectors that
-// hold it (K = 1001, 16.7 MB: REPITCH us).
+// hold it.  per_group: rows of a group's matrix, left out where the group has
+// no rows; 0: every row.
 __global__ void __launch_bounds__(256)
 repitch_kernel(const uint16_t* __restrict__ src, uint4* __restrict__ dst, const int64_t vectors, const int64_t elements,
-               const int cols, const int per_row) {
+               const int cols, const int per_row, const GroupTables g, const int per_group) {
   pdl_enter();
   const int64_t v = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (v >= vectors) return;
   const int64_t row = vectors <= 0xffffffffll ? static_cast<uint32_t>(v) / static_cast<uint32_t>(per_row) : v / per_row;
+  if (per_group && group_span(g, static_cast<int>(row / per_group)).n == 0) return;
   const int c = static_cast<int>(v - row * per_row) * 8;
   const int64_t at = row * cols + c;           // first element
   const int64_t base = at & ~int64_t{7};
@@ -592,12 +600,14 @@ repitch_kernel(const uint16_t* __restrict__ src, uint4* __restrict__ dst, const 
 }
 
 // =============================================================== host side
-cudaError_t launch_repitch(const void* src, void* dst, int64_t rows, int cols, cudaStream_t st) {
+cudaError_t launch_repitch(const void* src, void* dst, int64_t rows, int cols, const GroupTables& g, int per_group,
+                           cudaStream_t st) {
   const int per_row = pitch8(cols) / 8;
   const int64_t vectors = rows * per_row, blocks = (vectors + 255) / 256;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   return launch_dependent_kernel(repitch_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st,
-                                 static_cast<const uint16_t*>(src), static_cast<uint4*>(dst), vectors, rows * cols, cols, per_row);
+                                 static_cast<const uint16_t*>(src), static_cast<uint4*>(dst), vectors, rows * cols, cols, per_row, g,
+                                 g.offsets ? per_group : 0);
 }
 
 static const CUtensorMapDataType kBf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -609,21 +619,21 @@ static bool map_kmajor(CUtensorMap* m, const void* p, int cols, int64_t rows, in
   const uint32_t b[2] = {64, 128};
   return make_map(m, kBf, 2, reinterpret_cast<uint64_t>(p), d, s, b, kSw);
 }
-// [E, N, K] K-major: box 64 x 128 x 1.
-static bool map_weights(CUtensorMap* m, const void* p, int K, int64_t pitch, int N, int E) {
+// [E, N, K] K-major: box 64 x `rows` x 1.
+static bool map_weights(CUtensorMap* m, const void* p, int K, int64_t pitch, int N, int E, int rows) {
   const uint64_t d[3] = {static_cast<uint64_t>(K), static_cast<uint64_t>(N), static_cast<uint64_t>(E)};
   const uint64_t s[2] = {static_cast<uint64_t>(pitch) * 2, static_cast<uint64_t>(pitch) * 2 * N};
-  const uint32_t b[3] = {64, 128, 1};
+  const uint32_t b[3] = {64, static_cast<uint32_t>(rows), 1};
   return make_map(m, kBf, 3, reinterpret_cast<uint64_t>(p), d, s, b, kSw);
 }
 // [E, N, K] with K as the operand's M / N index: boxes of 64 columns x 64 rows,
-// two at once where the columns are whole blocks of 64.
-static bool map_weights_mn(CUtensorMap* m, const void* p, int K, int64_t pitch, int N, int E, bool blocks) {
+// `blocks` of them at once where the columns are whole blocks of 64 (else 0).
+static bool map_weights_mn(CUtensorMap* m, const void* p, int K, int64_t pitch, int N, int E, int blocks) {
   const uint64_t row = static_cast<uint64_t>(pitch) * 2;
   if (blocks) {
     const uint64_t d[4] = {64, static_cast<uint64_t>(N), static_cast<uint64_t>(K / 64), static_cast<uint64_t>(E)};
     const uint64_t s[3] = {row, 128, row * N};
-    const uint32_t b[4] = {64, 64, 2, 1};
+    const uint32_t b[4] = {64, 64, static_cast<uint32_t>(blocks), 1};
     return make_map(m, kBf, 4, reinterpret_cast<uint64_t>(p), d, s, b, kSw);
   }
   const uint64_t d[3] = {static_cast<uint64_t>(K), static_cast<uint64_t>(N), static_cast<uint64_t>(E)};
@@ -632,13 +642,13 @@ static bool map_weights_mn(CUtensorMap* m, const void* p, int K, int64_t pitch, 
   return make_map(m, kBf, 3, reinterpret_cast<uint64_t>(p), d, s, b, kSw);
 }
 // [rows, cols] with the rows as the summed index: boxes of 64 columns x 64
-// rows, two at once where the columns are whole blocks of 64.
-static bool map_rows_mn(CUtensorMap* m, const void* p, int cols, int64_t rows, int64_t pitch, bool blocks) {
+// rows, `blocks` of them at once where the columns are whole blocks of 64 (else 0).
+static bool map_rows_mn(CUtensorMap* m, const void* p, int cols, int64_t rows, int64_t pitch, int blocks) {
   const uint64_t row = static_cast<uint64_t>(pitch) * 2;
   if (blocks) {
     const uint64_t d[3] = {64, static_cast<uint64_t>(rows), static_cast<uint64_t>(cols / 64)};
     const uint64_t s[2] = {row, 128};
-    const uint32_t b[3] = {64, 64, 2};
+    const uint32_t b[3] = {64, 64, static_cast<uint32_t>(blocks)};
     return make_map(m, kBf, 3, reinterpret_cast<uint64_t>(p), d, s, b, kSw);
   }
   const uint64_t d[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)}, s[1] = {row};
@@ -669,14 +679,18 @@ static cudaError_t gm_launch(const GmParams& p, int64_t tiles, WsHeader* hdr, cu
 // a part has 2.4 us of them at least (K = 8192, N = 512, 300 rows 47 -> 17 us;
 // wgrad 768 x 768 over 16384 rows 107 -> 29 us; with 12 slices saved, 10 us
 // became 15).
-static int64_t gm_tiles(int op, const GroupTables& g, int K, int N) {
-  if (op == kGroupedWgrad) return g.E * ((N + 255) / 256) * static_cast<int64_t>((K + 255) / 256);
-  return row_tiles256(g) * (((op == kGroupedForward ? N : K) + 255) / 256);
+static int64_t gm_tiles(int op, const GroupTables& g, int K, int N, int nt) {
+  if (op == kGroupedWgrad) return g.E * ((N + 255) / 256) * static_cast<int64_t>((K + nt - 1) / nt);
+  return row_tiles256(g) * (((op == kGroupedForward ? N : K) + nt - 1) / nt);
+}
+static int gm_columns(int op, const GroupTables& g, int K, int N) {
+  const int cols = op == kGroupedForward ? N : K;
+  return cols <= 128 || 2 * gm_tiles(op, g, K, N, 256) <= num_sms() / 2 ? 128 : 256;
 }
 int grouped_splits(int op, const GroupTables& g, int K, int N, int planes) {
   const int64_t slices = op == kGroupedWgrad ? g.rows / (64 * static_cast<int64_t>(g.E))
                                              : ((op == kGroupedForward ? K : N) + 63) / 64;
-  const int64_t room = (num_sms() / 2) / std::max<int64_t>(1, gm_tiles(op, g, K, N));
+  const int64_t room = (num_sms() / 2) / std::max<int64_t>(1, gm_tiles(op, g, K, N, gm_columns(op, g, K, N)));
   const int64_t weight = planes == 3 ? 6 : 1;
   const int64_t parts = std::min(room, std::min(slices, slices * weight / 8));
   return parts > 1 && (slices - slices / parts) * weight >= 24 ? static_cast<int>(parts) : 1;
@@ -699,6 +713,7 @@ static cudaError_t gm_run(int op, const GroupedArgs& a, const GroupedTcExtras& x
   p.g = a.g;
   p.M = wgrad ? a.N : 0;
   p.N = fwd ? a.N : a.K;
+  p.nt = gm_columns(op, a.g, a.K, a.N);
   p.K = fwd ? a.K : a.N;
   p.splits = x.splits;
   p.skip = x.skip;
@@ -711,13 +726,13 @@ static cudaError_t gm_run(int op, const GroupedArgs& a, const GroupedTcExtras& x
   p.out_aligned = p.ldo % (f32 ? 4 : 8) == 0;
   bool ok;
   if (wgrad) {
-    p.a_blocks = a.N % 64 == 0;
-    p.b_blocks = a.K % 64 == 0;
+    p.a_blocks = a.N % 64 == 0 ? 2 : 0;
+    p.b_blocks = a.K % 64 == 0 ? p.nt / 128 : 0;
     ok = map_rows_mn(&p.a, a.dys, a.N, PLANES * R, np, p.a_blocks) && map_rows_mn(&p.b, a.xs, a.K, PLANES * R, kp, p.b_blocks);
   } else if (fwd) {
-    ok = map_kmajor(&p.a, a.xs, a.K, PLANES * R, kp) && map_weights(&p.b, a.w, a.K, kp, a.N, PLANES * E);
+    ok = map_kmajor(&p.a, a.xs, a.K, PLANES * R, kp) && map_weights(&p.b, a.w, a.K, kp, a.N, PLANES * E, p.nt / 2);
   } else {
-    p.b_blocks = a.K % 64 == 0;
+    p.b_blocks = a.K % 64 == 0 ? p.nt / 128 : 0;
     ok = map_kmajor(&p.a, a.dys, a.N, PLANES * R, np) && map_weights_mn(&p.b, a.w, a.K, kp, a.N, PLANES * E, p.b_blocks);
   }
   if (ok && p.out_aligned)
@@ -725,7 +740,7 @@ static cudaError_t gm_run(int op, const GroupedArgs& a, const GroupedTcExtras& x
          : wgrad ? map_out_f32(&p.out, p.outp, p.N, p.ldo, a.N, static_cast<int64_t>(p.splits) * E)
                  : map_out_f32(&p.out, p.outp, p.N, p.ldo, p.splits * R, 0);
   if (!ok) return cudaErrorInvalidValue;
-  const int64_t tiles = gm_tiles(op, a.g, a.K, a.N) * p.splits;
+  const int64_t tiles = gm_tiles(op, a.g, a.K, a.N, p.nt) * p.splits;
   if (wgrad) return gm_launch<kGroupedWgrad, PLANES, true>(p, tiles, hdr, st);
   if constexpr (PLANES == 1)
     if (!parts)

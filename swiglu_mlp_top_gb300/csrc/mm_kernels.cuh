@@ -498,14 +498,17 @@ cudaError_t launch_grouped_simt(int op, const GroupedArgs& p, const int* only_if
 // Rows start on 16 bytes: operands of bf16 whose width is no multiple of 8
 // come as copies with rows of pitch8() elements (launch_repitch).
 constexpr int pitch8(int n) { return (n + 7) / 8 * 8; }
-cudaError_t launch_repitch(const void* src, void* dst, int64_t rows, int cols, cudaStream_t st);
+// per_group: the rows are matrices of so many rows, one a group, and those of
+// groups without rows are left out (here, in SplitTensor and in Mx4Args); 0: rows.
+cudaError_t launch_repitch(const void* src, void* dst, int64_t rows, int cols, const GroupTables& g, int per_group,
+                           cudaStream_t st);
 // fp32 tensors as planes, in one launch; sets *flag where a value cannot be
-// split; rows of a `grouped` tensor without an assignment become zeros.
+// split; rows of the sorted tensors without an assignment become zeros.
 struct SplitTensor {
   const void* src;            // fp32 [rows, cols]
   void* dst;                  // bf16 [3, rows, pitch8(cols)]
   int64_t rows;
-  int cols, grouped;
+  int cols, per_group;
 };
 struct SplitTensors {
   SplitTensor t[3];
@@ -548,6 +551,8 @@ struct Mx4Args {
   const int32_t* n_rows;      // device: rows from here on are left alone; null: R
   int64_t R;
   int C;
+  GroupTables g;              // dequantise, with per_group: the groups
+  int per_group;
 };
 cudaError_t launch_mx4(int dtype, bool quantise, const Mx4Args& a, cudaStream_t st);
 

@@ -10,6 +10,9 @@
 // The maximum is taken over magnitudes as integers, in which an infinity or a
 // NaN is above every number: it gives the byte 255 and a group of NaN.
 //
+// per_group: the rows are matrices of so many rows, one a group, and those of
+// groups without rows are left out.
+//
 // Bound by memory (2 + 0.53 bytes a value in bf16) where few enough
 // instructions go into a value.  Rows of whole 32-byte pieces: a lane takes 16
 // columns in 32-byte loads, magnitudes and products stay packed in bf16 (a
@@ -17,8 +20,8 @@
 // 6 instructions a value.  Other rows: 8 columns a lane, as wide as the rows'
 // alignment allows; narrow rows are written element by element, neighbouring
 // lanes next to each other.
+#include "grouped.cuh"
 #include "pack.cuh"
-#include "mm_kernels.cuh"
 
 namespace mm {
 
@@ -241,7 +244,7 @@ mx4_quantize_kernel(const T* __restrict__ x, uint8_t* __restrict__ codes, uint8_
 template <typename T, int V>
 __global__ void __launch_bounds__(kMxThreads)
 mx4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ exps, T* __restrict__ x,
-                      const int32_t* n_rows, const int64_t R, const int C) {
+                      const GroupTables g, const int per_group, const int32_t* n_rows, const int64_t R, const int C) {
   pdl_enter();
   const int groups = (C + 31) / 32, words = (groups + 3) / 4;
   const int64_t rows = n_rows ? min(static_cast<int64_t>(max(*n_rows, 0)), R) : R;
@@ -254,7 +257,8 @@ mx4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restri
   for (int q = 0; q < kMxUnits; ++q) {
     units[q] = at;
     const int group = at.word * 4 + l / 4;
-    if (at.row < rows && group < groups) {
+    if (per_group && at.row < rows && group_span(g, static_cast<int>(at.row / per_group)).n == 0) units[q].row = R;
+    if (units[q].row < rows && group < groups) {
       code[q] = *reinterpret_cast<const uint32_t*>(codes + at.row * (16 * static_cast<int64_t>(groups)) + group * 16 + (l & 3) * 4);
       word[q] = reinterpret_cast<const uint32_t*>(exps)[at.word * R + at.row];
     }
@@ -290,13 +294,14 @@ mx4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restri
 template <typename T>
 __global__ void __launch_bounds__(kMxThreads)
 mx4_dequantize_narrow_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ exps, T* __restrict__ x,
-                             const int32_t* n_rows, const int64_t R, const int C) {
+                             const GroupTables g, const int per_group, const int32_t* n_rows, const int64_t R, const int C) {
   pdl_enter();
   const int groups = (C + 31) / 32, words = (groups + 3) / 4;
   const int64_t rows = n_rows ? min(static_cast<int64_t>(max(*n_rows, 0)), R) : R;
   const int lane = threadIdx.x & 31;
   const MxUnit u = mx_unit(static_cast<int64_t>(blockIdx.x) * (kMxThreads / 32) + (threadIdx.x >> 5), words);
   if (u.row >= rows) return;                   // a warp's word of 128 columns
+  if (per_group && group_span(g, static_cast<int>(u.row / per_group)).n == 0) return;
   const uint32_t word = reinterpret_cast<const uint32_t*>(exps)[u.word * R + u.row];
   const uint8_t* from = codes + u.row * (16 * static_cast<int64_t>(groups));
 #pragma unroll
@@ -340,10 +345,10 @@ static cudaError_t mx4_dequantize(const Mx4Args& a, cudaStream_t st) {
   const uint8_t *codes = a.codes, *exps = a.exps;
   T* x = static_cast<T*>(a.x_out);
   constexpr int kWide = 16 / sizeof(T), kPer = kMxThreads / kMxLanes * kMxUnits;
-  if (a.C % kWide == 0) return mx4_launch(mx4_dequantize_kernel<T, kWide>, kPer, a, st, codes, exps, x);
+  if (a.C % kWide == 0) return mx4_launch(mx4_dequantize_kernel<T, kWide>, kPer, a, st, codes, exps, x, a.g, a.per_group);
   if constexpr (sizeof(T) == 2)
-    if (a.C % 4 == 0) return mx4_launch(mx4_dequantize_kernel<T, 4>, kPer, a, st, codes, exps, x);
-  return mx4_launch(mx4_dequantize_narrow_kernel<T>, kMxThreads / 32, a, st, codes, exps, x);
+    if (a.C % 4 == 0) return mx4_launch(mx4_dequantize_kernel<T, 4>, kPer, a, st, codes, exps, x, a.g, a.per_group);
+  return mx4_launch(mx4_dequantize_narrow_kernel<T>, kMxThreads / 32, a, st, codes, exps, x, a.g, a.per_group);
 }
 
 cudaError_t launch_mx4(int dtype, bool quantise, const Mx4Args& a, cudaStream_t st) {

@@ -21,6 +21,16 @@ _GROUP = 32          # columns that share a scale
 _WORD = 4            # scales of a row next to each other
 
 
+def _device(t, name: str, stream):
+    """(device, raw stream) of a call's leading tensor, whatever its type."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev, stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+
+
 def _plan_args(plan: Optional[dict], dev: int):
     """(offsets, counts, E) of a plan; (None, None, 1) without."""
     if plan is None:
@@ -136,26 +146,17 @@ def grouped_matmul_backward(dys: torch.Tensor, xs: Optional[torch.Tensor], w: Op
 
 
 # --------------------------------------------- microscaled 4-bit floating point
-def _mx4_shapes(lead, C: int):
-    """Shapes of codes and exps for values [*lead, C]."""
-    groups, rows = -(-C // _GROUP), 1
-    for n in lead:
-        rows *= n
-    return (*lead, groups * _GROUP // 2), (-(-groups // _WORD), rows, _WORD)
-
-
-def _mx4_args(q: dict, name: str, dev: Optional[int]):
-    """(codes, exps, shape of the values) of a 4-bit tensor, checked against each other."""
-    codes, exps, C = q["codes"], q["exps"], q["cols"]
-    if not isinstance(codes, torch.Tensor) or codes.dim() not in (2, 3) or not codes.is_cuda:
+def _mx4_args(q: dict, name: str, dev: int):
+    """(address of codes, of exps, shape of the values) of a 4-bit tensor, checked against each other."""
+    codes, C = q["codes"], q["cols"]
+    if not isinstance(codes, torch.Tensor) or codes.dim() not in (2, 3):
         raise ValueError(f"codes of {name} must be a CUDA tensor [..., R, bytes]")
     if not isinstance(C, int) or C < 1:
         raise ValueError(f"cols of {name} must be a positive whole number")
-    dev = codes.get_device() if dev is None else dev
-    lead = tuple(codes.shape[:-1])
-    cs, es = _mx4_shapes(lead, C)
-    return (_arg(codes, f"codes of {name}", dev, torch.uint8, cs),
-            _arg(exps, f"exps of {name}", dev, torch.uint8, es), (*lead, C))
+    lead, groups = codes.shape[:-1], -(-C // _GROUP)
+    rows = lead[0] if len(lead) == 1 else lead[0] * lead[1]
+    return (_arg(codes, "codes", dev, torch.uint8, (*lead, groups * (_GROUP // 2))),
+            _arg(q["exps"], "exps", dev, torch.uint8, (-(-groups // _WORD), rows, _WORD)), (*lead, C))
 
 
 def mx4_quantize(x: torch.Tensor, *, rows: Optional[torch.Tensor] = None, out: Optional[dict] = None,
@@ -168,17 +169,23 @@ def mx4_quantize(x: torch.Tensor, *, rows: Optional[torch.Tensor] = None, out: O
     if not isinstance(x, torch.Tensor) or x.dim() not in (2, 3):
         raise ValueError("x must be [R, C] or [E, N, C]")
     dt, dev, raw = _begin(x, "x", x.dim(), stream)
-    C, lead = x.shape[-1], tuple(x.shape[:-1])
-    px = _arg(x, "x", dev, x.dtype, x.shape)
-    pr = _rows_arg(rows, dev)
+    shape = x.shape
+    lead, C = shape[:-1], shape[-1]
+    if C < 1:
+        raise ValueError("x must have columns")
+    R = lead[0] if len(lead) == 1 else lead[0] * lead[1]
+    px, pr = _arg(x, "x", dev, x.dtype, shape), _rows_arg(rows, dev)
     if out is None:
-        cs, es = _mx4_shapes(lead, C)
-        out = {"codes": _empty(cs, torch.uint8, dev, stream), "exps": _empty(es, torch.uint8, dev, stream),
-               "cols": C}
-    pc, pe, shape = _mx4_args(out, "out", dev)
-    if shape != (*lead, C):
-        raise ValueError(f"out holds {list(shape)}, x is {list(x.shape)}")
-    rc = L.load().mm_mx4_quantize(px, x.numel() // C if C else 0, C, dt, pr, pc, pe, raw)
+        groups = -(-C // _GROUP)
+        codes = _empty((*lead, groups * (_GROUP // 2)), torch.uint8, dev, stream)
+        exps = _empty((-(-groups // _WORD), R, _WORD), torch.uint8, dev, stream)
+        out = {"codes": codes, "exps": exps, "cols": C}
+        pc, pe = codes.data_ptr(), exps.data_ptr()
+    else:
+        pc, pe, held = _mx4_args(out, "out", dev)
+        if held != shape:
+            raise ValueError(f"out holds {list(held)}, x is {list(shape)}")
+    rc = L.load().mm_mx4_quantize(px, R, C, dt, pr, pc, pe, raw)
     L.check(rc, "mm_mx4_quantize")
     return out
 
@@ -187,16 +194,14 @@ def mx4_dequantize(q: dict, dtype: torch.dtype = torch.bfloat16, *, rows: Option
                    out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values that a 4-bit tensor stands for (mm_mx4_dequantize), in
     `dtype`; rows as in mx4_quantize."""
-    pc, pe, shape = _mx4_args(q, "q", None)
-    if dtype not in _DTYPES:
+    dev, raw = _device(q["codes"], "codes of q", stream)
+    pc, pe, shape = _mx4_args(q, "q", dev)
+    dt = _DTYPES.get(dtype)
+    if dt is None:
         raise ValueError(f"unsupported dtype {dtype}")
     if out is None:
-        out = _empty(shape, dtype, q["codes"].get_device(), stream)
-    dt, dev, raw = _begin(out, "out", len(shape), stream)
-    pc, pe, shape = _mx4_args(q, "q", dev)
-    R = 1
-    for n in shape[:-1]:
-        R *= n
+        out = _empty(shape, dtype, dev, stream)
+    R = shape[0] if len(shape) == 2 else shape[0] * shape[1]
     rc = L.load().mm_mx4_dequantize(pc, pe, R, shape[-1], dt, _rows_arg(rows, dev),
                                     _arg(out, "out", dev, dtype, shape), raw)
     L.check(rc, "mm_mx4_dequantize")
@@ -247,13 +252,3 @@ def mx4_matmul(x: Union[torch.Tensor, dict], w: dict, plan: Optional[dict] = Non
     del keep                                    # until the work is enqueued
     L.check(rc, "mm_mx4_matmul")
     return out
-
-
-def _device(t, name: str, stream):
-    """(device, raw stream) of a call's leading tensor, whatever its type."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    dev = t.get_device()
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
-    return dev, stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
