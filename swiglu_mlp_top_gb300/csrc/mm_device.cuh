@@ -498,10 +498,11 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
-// The same for a signal that orders no memory of this CTA for the other one
-// (an accumulator has been read, after tcgen05.wait::ld and the fence before a
-// thread sync): a release over the cluster waits for this thread's earlier
-// writes, 2000 cycles behind an epilogue's stores.
+// The same for a signal that no generic read of the other CTA relies on (an
+// accumulator has been read, after tcgen05.wait::ld and the fence before a
+// thread sync; a stage of this CTA's own shared memory is ready for its tensor
+// core, after a proxy fence): a release over the cluster waits for this
+// thread's earlier writes, 2000 cycles behind an epilogue's stores.
 __device__ __forceinline__ void mbar_signal_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }

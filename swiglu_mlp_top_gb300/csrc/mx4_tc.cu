@@ -13,7 +13,7 @@
 // shared memory to four columns, where the 16 bytes at l are the words of rows
 // l, l + 32, l + 64, l + 96.  A word's rows lie next to each other in memory
 // ([columns / 128, rows, 4]), so a warp reads 32 of them at once and any first
-// row will do.  Four warps take a stage each in turn (all 256 columns' scales
+// row will do.  Five warps take a stage each in turn (all 256 columns' scales
 // in each CTA: a CTA scales its own half of the rows): they load a stage's
 // words before its place in the ring is free, and store 16 bytes a lane.  (Two
 // warps that copied every stage word by word with cp.async made the stages
@@ -40,7 +40,8 @@ constexpr int kMtSc = 2 * (128 + 256) * 4;            // scale words of a stage:
 constexpr int kMtStageBytes = kMtTileA + kMtTileB + kMtSc;
 constexpr int kMtEpiWarps = 8;
 constexpr int kMtWarpProducer = kMtEpiWarps, kMtWarpMma = kMtEpiWarps + 1, kMtWarpScales = kMtEpiWarps + 2;
-constexpr int kMtScaleWarps = 4;
+constexpr int kMtScaleWarps = 5;
+static_assert(kMtScaleWarps <= kMtStages, "a stage has one warp at a time: a wait tells two neighbouring phases apart");
 constexpr int kMtThreads = 32 * (kMtEpiWarps + 2 + kMtScaleWarps);
 constexpr int kMtEpi = 2 * 32 * 64;                   // per warp: two pieces of 32 rows x 32 columns
 constexpr int kMtSmem = kMtStages * kMtStageBytes + kMtEpiWarps * kMtEpi + 1024 + 256;
@@ -142,7 +143,7 @@ mx4_tc_kernel(const __grid_constant__ MtParams P, WsHeader* hdr) {
     }
     __syncwarp();
   } else if (warp >= kMtWarpScales) {
-    // ------------------------------------------------ scales (both CTAs): four warps, a stage each in turn
+    // ------------------------------------------------ scales (both CTAs): a warp a stage, in turn
     const int64_t a_rows = P.g.rows, b_rows = static_cast<int64_t>(P.g.E) * P.N;
     const uint32_t* a_sc = reinterpret_cast<const uint32_t*>(P.a_sc);
     const uint32_t* b_sc = reinterpret_cast<const uint32_t*>(P.b_sc);
@@ -178,7 +179,10 @@ mx4_tc_kernel(const __grid_constant__ MtParams P, WsHeader* hdr) {
       __syncwarp();
       if (lane == 0) {
         if (rank == 0) mbar_arrive(&full[s]);
-        else mbar_arrive_cluster(mapa_shared(smem_u32(&full[s]), 0));
+        // the fences have put the words where this SM's tensor core reads them;
+        // a release over the cluster would keep the lane from its next stage
+        // (dense 8192 x 4096 x 8192: 119 us, 86 without)
+        else mbar_signal_cluster(mapa_shared(smem_u32(&full[s]), 0));
       }
     }
     __syncwarp();
