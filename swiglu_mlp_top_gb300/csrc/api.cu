@@ -1166,9 +1166,9 @@ static bool status_ok(const void* status_ws) { return aligned16(status_ws); }
 // with the weights: at E = 8, K = 768, N = 4864 and 32 rows 13.4 us against
 // 17.8 of the tiles, at 128 rows 19 against 15; at E = 64, K = 2048, N = 1024 and
 // 512 rows 50 against 54, at 1024 70 against 55; one matrix of 4096 x 4096 and 16
-// rows 10 against 26.  With weights in 4 bits the tiles need a bf16 copy of
-// the weights first: 128 rows 20 against 27, 256 29 against 27; E = 64, 1024
-// rows 66 against 119; one matrix, 64 rows 26 against 34, 128 57 against 34.
+// rows 10 against 26.  With weights in 4 bits, which the tiles have to convert:
+// 128 rows 20 us against 23, 256 29 against 24; E = 64, 1024 rows 66 against 88,
+// 2048 104 against 88; one matrix, 64 rows 26 against 28, 128 50 against 28.
 static bool grouped_streams(int64_t rows, int K, int E, bool w_in_4_bits) {
   return K % 8 == 0 && rows <= (w_in_4_bits ? 64 + 16 * E : 32 + 6 * E);
 }
@@ -1351,15 +1351,33 @@ int mm_mx4_dequantize(const void* codes, const uint8_t* exps, int64_t R, int64_t
                   n_rows, stream);
 }
 
-// bf16 rows: the weights as bf16, then mm_grouped_matmul.
+// How a product with 4-bit weights is made.
+enum Mx4Path {
+  kMx4Cores,                  // both in 4 bits (mx4_tc.cu)
+  kMx4Stream,                 // few bf16 rows (grouped_stream.cu)
+  kMx4Convert,                // bf16 rows, the weights converted on their way to the tensor cores (mx4_tc.cu)
+  kMx4Copy                    // a bf16 copy of the weights, then mm_grouped_matmul
+};
 struct Mx4Layout {
-  size_t w, product, total;
+  Mx4Path path;
+  size_t w, x, total;         // x: rows that start on 16 bytes, or the scratch of the product
 };
 static Mx4Layout mx4_layout(int64_t rows, int K, int N, int E, bool four) {
-  Mx4Layout L{0, 0, 0};
-  if (four || grouped_streams(rows, K, E, true)) return L;
-  L.product = align_up(2 * static_cast<size_t>(E) * N * K);
-  L.total = L.product + grouped_bytes(rows, K, N, E, kDtypeBF16, false);
+  Mx4Layout L{kMx4Cores, 0, 0, 0};
+  if (four) return L;
+  const GroupedPlan P = grouped_plan(rows, K, N, E, kDtypeBF16, false);
+  // The copy pays where two tiles of rows or more take each matrix, or where the
+  // sums are cut into parts: E = 8, K = 768, N = 4864 and 2048 rows 32 us
+  // converted against 40, 8192 rows 79 against 71; one matrix 4096 x 4096, 256
+  // rows 28 against 37, 1024 rows 44 against 32; 4096 x 512, 256 rows 24 against 14.
+  const bool copy = rows >= 512 * static_cast<int64_t>(E) || P.splits[kGroupedForward] > 1;
+  L.path = grouped_streams(rows, K, E, true) ? kMx4Stream : copy ? kMx4Copy : kMx4Convert;
+  if (L.path == kMx4Copy) {
+    L.x = align_up(2 * static_cast<size_t>(E) * N * K);
+    L.total = L.x + grouped_bytes(rows, K, N, E, kDtypeBF16, false);
+  } else if (L.path == kMx4Convert && K % 8) {
+    L.total = align_up(2 * static_cast<size_t>(rows) * pitch8(K));
+  }
   return L;
 }
 
@@ -1379,19 +1397,27 @@ int mm_mx4_matmul(const void* x, const uint8_t* x_exps, const void* w_codes, con
     return MM_ERR_INVALID_ARG;
   const Mx4Layout L = mx4_layout(rows, K, N, E, x_exps != nullptr);
   if (L.total > 0 && (!present16(workspace) || workspace_bytes < L.total)) return MM_ERR_WORKSPACE;
-  if (x_exps != nullptr || grouped_streams(rows, K, E, true)) {
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const Mx4MatmulArgs a{x, x_exps, w_codes, w_exps, ys, GroupTables{offsets, counts, rows, E}, K, N};
-    cudaError_t e = counted_launch(MM_KERNEL_GROUPED, st, [&] {
-      return x_exps ? launch_mx4_tc(a, static_cast<WsHeader*>(status_ws), st) : launch_mx4_stream(a, st);
-    });
-    return e == cudaSuccess ? MM_OK : cuda_fail(e, "mx4 matmul");
+  const GroupTables g{offsets, counts, rows, E};
+  if (L.path == kMx4Copy) {
+    const int rc = mx4_impl(false, nullptr, ws_at(workspace, L.w), const_cast<void*>(w_codes), const_cast<uint8_t*>(w_exps),
+                            static_cast<int64_t>(E) * N, K, kDtypeBF16, nullptr, stream, g, N);
+    if (rc != MM_OK) return rc;
+    return mm_grouped_matmul(x, ws_at(workspace, L.w), offsets, counts, rows, K, N, E, kDtypeBF16, ys,
+                             ws_at(workspace, L.x), L.total - L.x, status_ws, stream);
   }
-  const int rc = mx4_impl(false, nullptr, ws_at(workspace, L.w), const_cast<void*>(w_codes), const_cast<uint8_t*>(w_exps),
-                          static_cast<int64_t>(E) * N, K, kDtypeBF16, nullptr, stream, GroupTables{offsets, counts, rows, E}, N);
-  if (rc != MM_OK) return rc;
-  return mm_grouped_matmul(x, ws_at(workspace, L.w), offsets, counts, rows, K, N, E, kDtypeBF16, ys,
-                           ws_at(workspace, L.product), L.total - L.product, status_ws, stream);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  WsHeader* hdr = static_cast<WsHeader*>(status_ws);
+  Mx4MatmulArgs a{x, x_exps, w_codes, w_exps, ys, g, K, N};
+  cudaError_t e = cudaSuccess;
+  if (L.path == kMx4Convert && K % 8) {
+    a.x = ws_at(workspace, L.x);
+    e = counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_repitch(x, ws_at(workspace, L.x), rows, K, g, 0, st); });
+  }
+  if (e == cudaSuccess)
+    e = counted_launch(MM_KERNEL_GROUPED, st, [&] {
+      return L.path == kMx4Cores ? launch_mx4_tc(a, hdr, st) : L.path == kMx4Stream ? launch_mx4_stream(a, st) : launch_mx4w_tc(a, hdr, st);
+    });
+  return e == cudaSuccess ? MM_OK : cuda_fail(e, "mx4 matmul");
 }
 
 uint64_t mm_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }

@@ -225,4 +225,10 @@ inline int64_t row_tiles256(const GroupTables& g) {
   return g.offsets ? std::min<int64_t>(g.rows, g.rows / 256 + g.E) : (g.rows + 255) / 256;
 }
 
+// Columns of a tile: 128 where that is all, or where tiles of 256 would fill at
+// most half the pairs of SMs.
+inline int gm_columns(int64_t row_tiles, int cols) {
+  return cols <= 128 || 2 * row_tiles * ((cols + 255) / 256) <= num_sms() / 2 ? 128 : 256;
+}
+
 }  // namespace mm

@@ -12,11 +12,8 @@
 // steps are in flight before the first product.  (The tensor cores of
 // tcgen05 want their operands in shared memory and tiles of 128 rows: for
 // these shapes a longer way to the same bytes.)
-//
-// 4 bits to bf16: with a nibble's sign at bit 15 and its exponent and fraction
-// at bits 8..6, the bf16 is the value times 2^-126, subnormals included; one
-// multiplication by 2^(126 + e) makes it the value times its scale, exactly.
 #include "grouped.cuh"
+#include "mx4.cuh"
 
 namespace mm {
 
@@ -38,29 +35,6 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-// Eight values of a word of codes times the scale, as four pairs of bf16.
-// TWO: 2^126 (0x7e80) and the scale apart, where their product overflows.
-template <bool TWO>
-__device__ __forceinline__ uint4 e2m1_bf16(uint32_t codes, uint32_t f1, uint32_t f2) {
-  const uint32_t even = codes & 0x0f0f0f0fu, odd = (codes >> 4) & 0x0f0f0f0fu;
-  uint32_t v[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    // nibbles 2i and 2i + 1 in the two halves (selector bit 3: the sign of a byte below 16, zero)
-    uint32_t p;
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(p) : "r"(even), "r"(odd), "r"(0x8080 | i | (4 + i) << 8));
-    v[i] = bf16x2_mul((p * 0x1040u) & 0x81c081c0u, f1);
-    if constexpr (TWO) v[i] = bf16x2_mul(v[i], f2);
-  }
-  return make_uint4(v[0], v[1], v[2], v[3]);
-}
-
 template <bool MX4, int NT>
 struct GsTraits {
   static constexpr int kParts = MX4 ? 4 : 1;                 // 8-column pieces of a lane's step
@@ -115,11 +89,7 @@ __device__ __forceinline__ void gs_sum(const GsParams& P, int64_t wrow, int wlas
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const uint32_t byte = (sw[u][i] >> (8 * t)) & 255u;
-          // 2^126 * 2^(byte - 127) in bf16; 255 stands for NaN, 0 is 2^-127
-          f[i][0] = byte <= 128u ? (byte + 126u) << 7 : 0x7e80u;
-          f[i][1] = byte == 255u ? 0x7fffu : byte <= 128u ? 0x3f80u : byte << 7;
-          f[i][0] |= f[i][0] << 16;
-          f[i][1] |= f[i][1] << 16;
+          mx4_factors(byte, f[i][0], f[i][1]);
           two |= byte > 128u;
         }
         two = __any_sync(0xffffffffu, two);

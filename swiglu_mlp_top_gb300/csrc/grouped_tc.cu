@@ -679,13 +679,14 @@ static cudaError_t gm_launch(const GmParams& p, int64_t tiles, WsHeader* hdr, cu
 // a part has 2.4 us of them at least (K = 8192, N = 512, 300 rows 47 -> 17 us;
 // wgrad 768 x 768 over 16384 rows 107 -> 29 us; with 12 slices saved, 10 us
 // became 15).
+static int64_t gm_row_tiles(int op, const GroupTables& g, int N) {
+  return op == kGroupedWgrad ? g.E * static_cast<int64_t>((N + 255) / 256) : row_tiles256(g);
+}
 static int64_t gm_tiles(int op, const GroupTables& g, int K, int N, int nt) {
-  if (op == kGroupedWgrad) return g.E * ((N + 255) / 256) * static_cast<int64_t>((K + nt - 1) / nt);
-  return row_tiles256(g) * (((op == kGroupedForward ? N : K) + nt - 1) / nt);
+  return gm_row_tiles(op, g, N) * (((op == kGroupedForward ? N : K) + nt - 1) / nt);
 }
 static int gm_columns(int op, const GroupTables& g, int K, int N) {
-  const int cols = op == kGroupedForward ? N : K;
-  return cols <= 128 || 2 * gm_tiles(op, g, K, N, 256) <= num_sms() / 2 ? 128 : 256;
+  return gm_columns(gm_row_tiles(op, g, N), op == kGroupedForward ? N : K);
 }
 int grouped_splits(int op, const GroupTables& g, int K, int N, int planes) {
   const int64_t slices = op == kGroupedWgrad ? g.rows / (64 * static_cast<int64_t>(g.E))

@@ -29,6 +29,7 @@
 // the eleven instructions of a stage take 950 cycles, twice the tensor cores'
 // time.
 #include "grouped.cuh"
+#include "mx4.cuh"
 
 namespace mm {
 
@@ -324,6 +325,264 @@ mx4_tc_kernel(const __grid_constant__ MtParams P, WsHeader* hdr) {
   if (warp == kMtWarpMma) tmem_dealloc_cta2(tmem, 512);
 }
 
+// ===================================================== bf16 rows, 4-bit weights
+// ys = x v(w[e])^T with x in bf16: the forward kernel of grouped_tc.cu (tiles of
+// 256 x 256 or 256 x 128, slices of 64, kind::f16), whose B tiles are made from
+// codes instead of loaded.  Six warps take a stage each in turn: a lane loads
+// the 32 bytes of codes and the scale word of four rows (one stage ahead of the
+// one that it converts), multiplies (mx4.cuh, 19 instructions for 8 values) and
+// stores 16 bytes at a time where the swizzled TMA layout has them.  Reads each
+// needed weight once in 4 bits: with a bf16 copy of the weights first (and no
+// copy of x) T = 256, E = 8, K = 768, N = 4864 took 28 us.
+constexpr int kMwRing = 6, kMwTile = 128 * 64 * 2;
+constexpr int kMwWarpConvert = kMtEpiWarps + 2, kMwConverters = 6;
+static_assert(kMwConverters <= kMwRing, "a stage has one warp at a time: a wait tells two neighbouring phases apart");
+constexpr int kMwThreads = 32 * (kMtEpiWarps + 2 + kMwConverters);
+constexpr int kMwStage = 32 * 128;                    // epilogue: 32 rows x 128 bytes per warp
+constexpr int kMwSmem = kMwRing * 2 * kMwTile + kMtEpiWarps * kMwStage + 1024 + 256;
+static_assert(kMwSmem + sizeof(GmTables) + 64 <= 232448, "shared memory budget");
+
+struct MwParams {
+  CUtensorMap a, out;
+  GroupTables g;
+  const uint8_t* w;         // codes [E * N, 16 groups]
+  const uint32_t* sc;       // [words, E * N]
+  int N, K, nt, groups;
+  int out_aligned;
+  void* outp;
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMwThreads, 1)
+mx4w_tc_kernel(const __grid_constant__ MwParams P, WsHeader* hdr) {
+  extern __shared__ unsigned char smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + kMwRing * kMwTile;
+  uint8_t* sEpi = sB + kMwRing * kMwTile;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sEpi + kMtEpiWarps * kMwStage);
+  uint64_t* full = bars;                   // [stages] even CTA: both CTAs' rows and weights
+  uint64_t* empty = bars + kMwRing;        // [stages] each CTA: released by the pair's MMAs
+  uint64_t* tfull = bars + 2 * kMwRing;    // [2] each CTA: accumulator ready
+  uint64_t* tempty = tfull + 2;            // [2] even CTA: both CTAs' epilogues have read it
+  uint64_t* drained = tempty + 2;          // even CTA: all MMAs finished
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  __shared__ GmTables s_tab;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int cluster = blockIdx.x >> 1, nc = gridDim.x >> 1;
+  const int ntn = (P.N + P.nt - 1) / P.nt, slices = (P.K + 63) / 64;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMwRing; ++s) {
+      mbar_init(&full[s], 1 + 2);          // the bytes of A, and each CTA's converted weights
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 2 * kMtEpiWarps);
+    }
+    mbar_init(drained, 1);
+    fence_mbar_init();
+    s_abort = 0;
+  }
+  if (warp == 0) {
+    // tables and operands may be the previous kernel's output
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    gm_tables<kGroupedForward>(P.g, s_tab, ntn);
+  }
+  if (warp == kMtWarpMma) {
+    tmem_alloc_cta2(&s_tmem, 512);
+    tmem_relinquish_cta2();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const int total = s_tab.tstart[P.g.E];
+  volatile int* abort = &s_abort;
+
+  if (warp == kMtWarpProducer) {
+    // ------------------------------------------------ TMA: rows of x (both CTAs)
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int tile = cluster; ok && tile < total; tile += nc) {
+        const GmTile ti = gm_tile<kGroupedForward>(tile, P.g.E, 0, 0, s_tab, ntn, P.nt, rank);
+        for (int kb = 0; kb < slices; ++kb, ++it) {
+          const int s = it % kMwRing;
+          const uint32_t ph = (it / kMwRing) & 1;
+          if (!mbar_wait(&empty[s], ph ^ 1, abort, hdr, 131)) { ok = false; break; }
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kMwTile);
+          tma_load_2d_cta2(sA + s * kMwTile, &P.a, mapa_shared(smem_u32(&full[s]), 0), kb * 64, ti.m0);
+        }
+      }
+      if (!ok && rank == 0) {
+        // a wait gave up: the copies in flight land before the block ends
+        for (int j = 0; j < kMwRing; ++j) {
+          const int i2 = it - 1 - j;
+          if (i2 < 0) break;
+          mbar_wait(&full[i2 % kMwRing], (i2 / kMwRing) & 1, nullptr, hdr, 132);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp >= kMwWarpConvert) {
+    // ------------------------------------------------ weights (both CTAs): a warp a stage, in turn
+    const int64_t rows = static_cast<int64_t>(P.g.E) * P.N, pitch = 16 * static_cast<int64_t>(P.groups);
+    const int mine = total > cluster ? (total - cluster + nc - 1) / nc * slices : 0;      // stages of all tiles
+    const int per = P.nt / 64;             // rows of a lane
+    struct Loaded {
+      uint4 c[4][2];
+      uint32_t sc[4];
+    };
+    // the codes of stage `it`: two groups of rows lane, + 32, + 64, + 96
+    auto load = [&](int it, Loaded& v) {
+      const int nth = it / slices, kb = it - nth * slices;
+      const GmTile ti = gm_tile<kGroupedForward>(cluster + nth * nc, P.g.E, 0, 0, s_tab, ntn, P.nt, rank);
+      const int n0 = ti.n0 + P.nt / 2 * rank;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = n0 + 32 * i + lane;
+        const bool in = i < per && n < P.N;
+        const int64_t r = static_cast<int64_t>(ti.e) * P.N + n;
+        const uint4* from = reinterpret_cast<const uint4*>(P.w + r * pitch) + 2 * kb;
+        // where there is nothing, zeros of scale 2^-127
+        v.c[i][0] = in ? __ldg(from) : make_uint4(0u, 0u, 0u, 0u);
+        v.c[i][1] = in && 2 * kb + 1 < P.groups ? __ldg(from + 1) : make_uint4(0u, 0u, 0u, 0u);
+        v.sc[i] = in ? __ldg(P.sc + (kb >> 1) * rows + r) >> (16 * (kb & 1)) : 0u;
+      }
+    };
+    auto convert = [&](int it, const Loaded& v) {
+      const int s = it % kMwRing;
+      const uint32_t ph = (it / kMwRing) & 1;
+      if (!warp_wait(&empty[s], ph ^ 1, abort, hdr, 133)) return false;
+      uint8_t* tile = sB + s * kMwTile;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i >= per) break;
+        const int r = 32 * i + lane;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t byte = (v.sc[i] >> (8 * h)) & 255u;
+          uint32_t f1, f2;
+          mx4_factors(byte, f1, f2);
+          const bool two = __any_sync(0xffffffffu, byte > 128u);
+          const uint32_t c[4] = {v.c[i][h].x, v.c[i][h].y, v.c[i][h].z, v.c[i][h].w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            // 128-byte rows, 16-byte chunk j of row r at chunk j ^ (r & 7)
+            *reinterpret_cast<uint4*>(tile + r * 128 + (((4 * h + q) ^ (r & 7)) << 4)) =
+                two ? e2m1_bf16<true>(c[q], f1, f2) : e2m1_bf16<false>(c[q], f1, 0u);
+        }
+      }
+      fence_proxy_async_smem();            // where this SM's tensor core reads them
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive(&full[s]);
+        else mbar_signal_cluster(mapa_shared(smem_u32(&full[s]), 0));
+      }
+      return true;
+    };
+    Loaded a, b;
+    int it = warp - kMwWarpConvert;
+    if (it < mine) load(it, a);
+    while (it < mine) {
+      if (it + kMwConverters < mine) load(it + kMwConverters, b);
+      if (!convert(it, a)) break;
+      it += kMwConverters;
+      if (it >= mine) break;
+      if (it + kMwConverters < mine) load(it + kMwConverters, a);
+      if (!convert(it, b)) break;
+      it += kMwConverters;
+    }
+    __syncwarp();
+  } else if (warp == kMtWarpMma) {
+    // ------------------------------------------------ MMA (even CTA)
+    if (rank == 0) {
+      const bool leader = elect_one();
+      const int tiles = __shfl_sync(0xffffffffu, total, 0);
+      const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t idesc = idesc_bf16_f32(256, 0) | (static_cast<uint32_t>(P.nt >> 3) << 17);
+      const uint64_t da = smem_desc_sw128(smem_u32(sA)), db = smem_desc_sw128(smem_u32(sB));
+      int s = 0, used = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int tile = cluster; ok && tile < tiles; tile += nc, ++used) {
+        ok = warp_wait(&tempty[used & 1], ((used >> 1) & 1) ^ 1, abort, hdr, 134);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = base + (used & 1) * 256;
+        for (int kb = 0; kb < slices; ++kb) {
+          ok = warp_wait<true>(&full[s], ph, abort, hdr, 135);
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            const uint64_t as = da + static_cast<uint64_t>(s * (kMwTile / 16)), bs = db + static_cast<uint64_t>(s * (kMwTile / 16));
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) umma_f16_cta2(d, as + 2 * kk, bs + 2 * kk, idesc, (kb | kk) ? 1u : 0u);
+            umma_commit_cta2_mc(&empty[s], 0x3);
+            if (kb + 1 == slices) umma_commit_cta2_mc(&tfull[used & 1], 0x3);
+          }
+          __syncwarp();
+          if (++s == kMwRing) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (leader) umma_commit_cta2_mc(drained, 0x1);
+      __syncwarp();
+      warp_wait(drained, 0, nullptr, hdr, 136);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------ epilogue (warps 0-7, both CTAs)
+    const int quad = warp & 3, half = warp >> 2, hc = P.nt / 2;
+    uint8_t* wstage = sEpi + warp * kMwStage;
+    const uint32_t te0 = mapa_shared(smem_u32(&tempty[0]), 0), te1 = mapa_shared(smem_u32(&tempty[1]), 0);
+    int used = 0;
+    for (int tile = cluster; tile < total; tile += nc, ++used) {
+      const GmTile ti = gm_tile<kGroupedForward>(tile, P.g.E, 0, 0, s_tab, ntn, P.nt, rank);
+      if (!warp_wait(&tfull[used & 1], (used >> 1) & 1, abort, hdr, 137)) break;
+      tc_fence_after();
+      const int rem = min(32, ti.mrows - quad * 32);            // rows of the group in this warp's 32
+      const bool counts = quad * 32 + lane < ti.mvalid;         // this lane's row is not padding
+      const uint32_t tb = tmem + (static_cast<uint32_t>(quad * 32) << 16) + (used & 1) * 256 + half * hc;
+#pragma unroll 1
+      for (int c = 0; c < hc; c += 64) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(tb + c + 32 * h, r);  // every lane (warp-collective)
+          tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < 16; ++q)
+            pk[16 * h + q] = counts ? pack_bf16x2(__uint_as_float(r[2 * q]), __uint_as_float(r[2 * q + 1])) : 0u;
+        }
+        if (c + 64 == hc) {                        // the accumulator is read: the next tile may have it
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_signal_cluster((used & 1) ? te1 : te0);
+        }
+        const int col = ti.n0 + half * hc + c;
+        if (rem > 0 && col < P.N)
+          store_rows_bf16(pk, wstage, &P.out, P.outp, P.out_aligned, ti.m0 + quad * 32, col, rem, P.N, lane);
+      }
+    }
+    if (lane == 0) bulk_wait_all();   // this warp's tensor stores have landed
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == kMtWarpMma) tmem_dealloc_cta2(tmem, 512);
+}
+
 // =============================================================== host side
 cudaError_t launch_mx4_tc(const Mx4MatmulArgs& a, WsHeader* hdr, cudaStream_t st) {
   MtParams p;
@@ -350,12 +609,38 @@ cudaError_t launch_mx4_tc(const Mx4MatmulArgs& a, WsHeader* hdr, cudaStream_t st
       (p.out_aligned && !map_out_rows(&p.out, a.out, a.N, a.g.rows, 32)))
     return cudaErrorInvalidValue;
   const int64_t tiles = row_tiles256(a.g) * ntn;
-  if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
+  if (tiles * p.stages > 0x3fffffff) return cudaErrorInvalidValue;
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(mx4_tc_kernel), kMtSmem);
   if (e != cudaSuccess) return e;
   const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(tiles, num_sms() / 2));
   return launch_dependent_kernel(mx4_tc_kernel, dim3(static_cast<unsigned>(2 * pairs)), dim3(kMtThreads), kMtSmem, st,
                                  p, hdr);
+}
+
+cudaError_t launch_mx4w_tc(const Mx4MatmulArgs& a, WsHeader* hdr, cudaStream_t st) {
+  MwParams p;
+  memset(&p, 0, sizeof(p));
+  p.g = a.g;
+  p.w = static_cast<const uint8_t*>(a.w);
+  p.sc = reinterpret_cast<const uint32_t*>(a.w_exps);
+  p.N = a.N;
+  p.K = a.K;
+  p.groups = (a.K + 31) / 32;
+  p.nt = gm_columns(row_tiles256(a.g), a.N);
+  p.outp = a.out;
+  p.out_aligned = a.N % 8 == 0;
+  const uint64_t da[2] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.g.rows)}, sa[1] = {2 * static_cast<uint64_t>(pitch8(a.K))};
+  const uint32_t box[2] = {64, 128};
+  if (!make_map(&p.a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, reinterpret_cast<uint64_t>(a.x), da, sa, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      (p.out_aligned && !map_out_rows(&p.out, a.out, a.N, a.g.rows, 64)))
+    return cudaErrorInvalidValue;
+  const int64_t tiles = row_tiles256(a.g) * ((a.N + p.nt - 1) / p.nt);
+  if (tiles * ((a.K + 63) / 64) > 0x3fffffff) return cudaErrorInvalidValue;
+  const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(mx4w_tc_kernel), kMwSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(tiles, num_sms() / 2));
+  return launch_dependent_kernel(mx4w_tc_kernel, dim3(static_cast<unsigned>(2 * pairs)), dim3(kMwThreads), kMwSmem, st, p,
+                                 hdr);
 }
 
 }  // namespace mm
