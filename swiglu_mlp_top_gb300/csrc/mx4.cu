@@ -21,6 +21,7 @@
 // alignment allows; narrow rows are written element by element, neighbouring
 // lanes next to each other.
 #include "grouped.cuh"
+#include "mx4.cuh"
 #include "pack.cuh"
 
 namespace mm {
@@ -92,11 +93,6 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 // 32 bytes in one access, from a 32-byte boundary.
 __device__ __forceinline__ void load32(const void* p, uint32_t (&v)[8]) {
   asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -166,7 +162,7 @@ mx4_quantize_wide_kernel(const T* __restrict__ x, uint8_t* __restrict__ codes, u
       const uint32_t s2 = (scale >> 16) | scale;
 #pragma unroll
       for (int h = 0; h < 8; ++h) {
-        const uint32_t w = mul_bf16x2(raw[q][h], s2);
+        const uint32_t w = bf16x2_mul(raw[q][h], s2);
         v[2 * h] = __uint_as_float(w << 16);
         v[2 * h + 1] = __uint_as_float(w & 0xffff0000u);
       }
@@ -290,6 +286,48 @@ mx4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restri
   }
 }
 
+// bf16 rows of whole 32-byte pieces: 16 columns a lane.
+__global__ void __launch_bounds__(kMxThreads)
+mx4_dequantize_wide_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ exps, __nv_bfloat16* __restrict__ x,
+                           const GroupTables g, const int per_group, const int32_t* n_rows, const int64_t R, const int C) {
+  pdl_enter();
+  const int groups = (C + 31) / 32, words = (groups + 3) / 4;
+  const int64_t rows = n_rows ? min(static_cast<int64_t>(max(*n_rows, 0)), R) : R;
+  const int l = threadIdx.x % kMxWideLanes;
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * (kMxThreads / kMxWideLanes) + threadIdx.x / kMxWideLanes) * kMxUnits;
+  MxUnit at = mx_unit(first, words);
+  int64_t to[kMxUnits];                        // first element, -1: nothing to write
+  uint2 code[kMxUnits];
+  uint32_t word[kMxUnits];
+#pragma unroll
+  for (int q = 0; q < kMxUnits; ++q) {
+    const int c = at.word * 128 + 16 * l;
+    to[q] = at.row < rows && c < C ? at.row * C + c : -1;
+    if (per_group && to[q] >= 0 && group_span(g, static_cast<int>(at.row / per_group)).n == 0) to[q] = -1;
+    if (to[q] >= 0) {
+      code[q] = *reinterpret_cast<const uint2*>(codes + at.row * (16 * static_cast<int64_t>(groups)) + at.word * 64 + 8 * l);
+      word[q] = reinterpret_cast<const uint32_t*>(exps)[at.word * R + at.row];
+    }
+    if (++at.word == words) {
+      at.word = 0;
+      ++at.row;
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < kMxUnits; ++q) {
+    if (to[q] < 0) continue;
+    const uint32_t byte = (word[q] >> (8 * (l / 2))) & 255u;
+    uint32_t f1, f2;
+    mx4_factors(byte, f1, f2);
+    const bool two = byte > 128u;
+    const uint4 a = two ? e2m1_bf16<true>(code[q].x, f1, f2) : e2m1_bf16<false>(code[q].x, f1, 0u);
+    const uint4 b = two ? e2m1_bf16<true>(code[q].y, f1, f2) : e2m1_bf16<false>(code[q].y, f1, 0u);
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(x + to[q]), "r"(a.x), "r"(a.y), "r"(a.z),
+                 "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+  }
+}
+
 // Rows that start anywhere: neighbouring lanes write neighbouring elements.
 template <typename T>
 __global__ void __launch_bounds__(kMxThreads)
@@ -345,6 +383,9 @@ static cudaError_t mx4_dequantize(const Mx4Args& a, cudaStream_t st) {
   const uint8_t *codes = a.codes, *exps = a.exps;
   T* x = static_cast<T*>(a.x_out);
   constexpr int kWide = 16 / sizeof(T), kPer = kMxThreads / kMxLanes * kMxUnits;
+  if constexpr (sizeof(T) == 2)
+    if (a.C % 16 == 0 && reinterpret_cast<uintptr_t>(x) % 32 == 0)
+      return mx4_launch(mx4_dequantize_wide_kernel, kMxThreads / kMxWideLanes * kMxUnits, a, st, codes, exps, x, a.g, a.per_group);
   if (a.C % kWide == 0) return mx4_launch(mx4_dequantize_kernel<T, kWide>, kPer, a, st, codes, exps, x, a.g, a.per_group);
   if constexpr (sizeof(T) == 2)
     if (a.C % 4 == 0) return mx4_launch(mx4_dequantize_kernel<T, 4>, kPer, a, st, codes, exps, x, a.g, a.per_group);
