@@ -913,15 +913,16 @@ BLOCK_OPS_MORE = [
 
 
 def run_block_ops(args):
-    """The operators around the experts' products at the cases of
-    perf/operators.py and a few more, one JSON line each: `device_us`, a pass
-    in a replayed CUDA graph; `call_us`, a pass among others through the Python
-    call (bound by the host where it is above the device's); `plain_us`, the
-    elementary torch form; and the bytes that a pass cannot do without, at the
-    measured copy rate.  The inputs rotate over several sets (twice L2 or 16
-    sets, at least 3); medians of 7 regions."""
+    """The operators around the experts' products and the products by expert at
+    the cases of perf/operators.py and perf/more_operators.py and a few more,
+    one JSON line each: `device_us`, a pass in a replayed CUDA graph;
+    `call_us`, a pass among others through the Python call (bound by the host
+    where it is above the device's); `plain_us`, the elementary torch form; and
+    the bytes that a pass cannot do without, at the measured copy rate, and its
+    operations.  The inputs rotate over several sets (twice L2 or 16 sets, at
+    least 3); medians of 7 regions."""
     import swiglu_mlp_top_gb300 as mm
-    from perf import operators as ops
+    from perf import more_operators, operators
     dev = torch.device("cuda", 0)
     torch.cuda.set_device(dev)
     peaks, src = measured_peaks()
@@ -938,7 +939,8 @@ def run_block_ops(args):
             times.append(e0.elapsed_time(e1) / passes * 1e3)
         return statistics.median(times)
 
-    for case in ops.listed() + BLOCK_OPS_MORE:
+    for ops, case in ([(operators, c) for c in operators.listed() + BLOCK_OPS_MORE] +
+                      [(more_operators, c) for c in more_operators.listed()]):
         bare = case.get("bare", False)
         # without a checkpoint: g, u and h, 2 bytes each
         nbytes = case["R"] * case["I"] * 6 if bare else ops.work(case)["bytes"]
@@ -973,6 +975,7 @@ def run_block_ops(args):
         print(json.dumps({"case": case["name"], "device_us": round(device, 2), "call_us": round(call, 2),
                           "plain_us": None if plain is None else round(plain, 1), "bytes": int(nbytes),
                           "floor_us": round(floor, 3), "frac_of_copy_rate": round(floor / device, 3),
+                          "tflops": round(ops.work(case)["flops"] / device / 1e6, 1),
                           "input_sets": n_set, "peak_source": src, "clocks": clk.summary()}), flush=True)
         del graph, states
 

@@ -507,11 +507,17 @@ int mm_swiglu_act_backward(const void* codes, const uint8_t* exps, const void* d
  * rows from offsets[E] on (and before offsets[0]) are left as they were; what
  * stands in padding rows and behind in inputs (NaN too) has no effect.
  * Sums in fp32 in a fixed order (deterministic), one rounding per element.
+ * fp32 operands of more than a few rows are multiplied on the tensor cores as
+ * three bf16 parts each, which hold all 24 bits (six of the nine products; the
+ * others are below 2^-25); a call whose operands hold an infinity, a NaN, a
+ * magnitude of 2^127 or more or one below 2^-100 that is not zero, in a row
+ * that counts, runs on the CUDA cores instead, with the same accuracy.
  * Outputs overlap neither inputs nor each other.  `status_ws` (nullable: no
  * report) is a zeroed workspace of >= 256 bytes read by mm_check_status(),
  * where a device wait that exceeded its time limit is recorded; `workspace`
- * is plain scratch (its header is not used), and may be NULL where the size
- * is 0.
+ * is plain scratch (its header is not used, and what it holds before the call
+ * does not matter), and may be NULL where the size is 0.  Sizes are those of
+ * the current device.
  * Limits: E <= MM_MAX_EXPERTS; K, N <= MM_GROUPED_MAX_DIM; rows <=
  * MM_GROUPED_MAX_ROWS.  rows = 0 enqueues nothing, but that dw is zeroed.
  * ---------------------------------------------------------------------- */

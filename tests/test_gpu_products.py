@@ -179,6 +179,24 @@ def test_tables_that_point_outside():
         assert bool(((y == 64) | (y == 7) | (y == 0)).all()) and dw.shape == (3, 32, 64)
 
 
+def test_tables_that_point_outside_many_rows():
+    """The same where tiles of rows are taken, and with weights in 4 bits."""
+    R, K, N = 700, 72, 136
+    x, w = torch.ones(R, K, dtype=BF, device="cuda"), torch.ones(3, N, K, dtype=BF, device="cuda")
+    wq, xq = mm.mx4_quantize(w), mm.mx4_quantize(x)
+    status = mm.new_workspace(256)
+    for off, cnt in (([-50, 300, 2 ** 30, 2 ** 31 - 1], [2 ** 31 - 1] * 3), ([-2 ** 31, -5, 400, 701], [-1, 5, 2 ** 30]), ([600, 300, 10, 0], [4, 4, 4])):
+        plan = {"offsets": torch.tensor(off, dtype=torch.int32, device="cuda"), "counts": torch.tensor(cnt, dtype=torch.int32, device="cuda")}
+        for dtype in (BF, F32):
+            y = mm.grouped_matmul(x.to(dtype), w.to(dtype), plan, out=torch.full((R, N), 7.0, dtype=dtype, device="cuda"), status_workspace=status)
+            mm.grouped_matmul_backward(y, x.to(dtype), w.to(dtype), plan, status_workspace=status)
+            assert bool(((y == K) | (y == 7) | (y == 0)).all())
+        for xs in (x, xq):
+            y = mm.mx4_matmul(xs, wq, plan, out=torch.full((R, N), 7.0, dtype=BF, device="cuda"), status_workspace=status)
+            assert bool(((y == K) | (y == 7) | (y == 0)).all())
+    assert mm.check_status(status) == 0
+
+
 def test_refusals_on_the_device():
     x, w = torch.zeros(6, 64, dtype=BF, device="cuda"), torch.zeros(2, 32, 64, dtype=BF, device="cuda")
     plan = on_gpu(ref.tables([2, 4]))
@@ -433,19 +451,27 @@ def test_captured_and_replayed_with_another_routing(T, K, N):
             assert torch.equal(got, want)
 
 
-def test_two_graphs_share_a_workspace():
-    """One scratch and one status word for two captured graphs on one stream."""
-    E, K, N, T = 3, 65, 50, 70
+@pytest.mark.parametrize("E,K,N,counts", [(3, 65, 50, [30, 0, 40]), (1, 2050, 72, [700]), (2, 130, 257, [600, 900])])
+def test_two_graphs_share_a_workspace(E, K, N, counts):
+    """One scratch, with anything in it, and one status word for two captured
+    graphs on one stream; the second set holds values that fp32 products on the
+    tensor cores turn over to the CUDA cores."""
     gen = torch.Generator().manual_seed(0)
-    plan, status = on_gpu(ref.tables([30, 0, 40])), mm.new_workspace(256)
-    ws = torch.empty(max(mm.grouped_matmul_workspace_bytes(T, K, N, E, BF), mm.grouped_matmul_backward_workspace_bytes(T, K, N, E, BF),
-                         mm.mx4_matmul_workspace_bytes(T, K, N, E, True), 256), dtype=torch.uint8, device="cuda")
-    sets = [[torch.randn(*s, generator=gen).to(BF).cuda() for s in ((T, K), (E, N, K), (T, N))] for _ in range(2)]
+    T = sum(counts)
+    plan, status = on_gpu(ref.tables(counts)), mm.new_workspace(256)
+    need = [f(T, K, N, E, d) for f in (mm.grouped_matmul_workspace_bytes, mm.grouped_matmul_backward_workspace_bytes) for d in (BF, F32)]
+    ws = torch.full((max(*need, mm.mx4_matmul_workspace_bytes(T, K, N, E, False), 256),), 255, dtype=torch.uint8, device="cuda")
+    sets = [[torch.randn(*s, generator=gen).cuda() for s in ((T, K), (E, N, K), (T, N))] for _ in range(2)]
+    sets[1][0][3, 5] = 2.0 ** -126
     kw = dict(workspace=ws, status_workspace=status)
 
-    def call(x, w, dy):
-        return (mm.grouped_matmul(x, w, plan, **kw), *mm.grouped_matmul_backward(dy, x, w, plan, **kw),
-                mm.mx4_matmul(mm.mx4_quantize(x), mm.mx4_quantize(w), plan, **kw))
+    def call(*tensors):
+        out = []
+        for dtype in (BF, F32):
+            x, w, dy = (t.to(dtype) for t in tensors)
+            out += [mm.grouped_matmul(x, w, plan, **kw), *mm.grouped_matmul_backward(dy, x, w, plan, **kw)]
+        x, wq = tensors[0].to(BF), mm.mx4_quantize(tensors[1].to(BF))
+        return (*out, mm.mx4_matmul(mm.mx4_quantize(x), wq, plan, **kw), mm.mx4_matmul(x, wq, plan, **kw))
 
     want = [[t.clone() for t in call(*s)] for s in sets]
     made = [graph_of(lambda s=s: call(*s)) for s in sets]
@@ -485,7 +511,8 @@ def test_the_same_bits_every_time():
     q, wq = mm.mx4_quantize(x), mm.mx4_quantize(w)
     first = None
     for _ in range(4):
-        outs = (mm.grouped_matmul(x, w, plan), *mm.grouped_matmul_backward(dy, x, w, plan), mm.mx4_matmul(q, wq, plan), mm.mx4_matmul(x[:40], wq, on_gpu(ref.tables([5] * 8))))
+        outs = (mm.grouped_matmul(x, w, plan), *mm.grouped_matmul_backward(dy, x, w, plan), mm.mx4_matmul(q, wq, plan), mm.mx4_matmul(x[:40], wq, on_gpu(ref.tables([5] * 8))),
+                mm.mx4_matmul(x, wq, plan), mm.grouped_matmul(x.float(), w.float(), plan), *mm.grouped_matmul_backward(dy[:, :64].float().contiguous(), x.float(), w[0, :64].float()))
         first = first or outs
         for a, b in zip(outs, first):
             assert torch.equal(a, b)
