@@ -24,22 +24,52 @@ __device__ __forceinline__ GroupSpan group_span(const GroupTables& g, int e) {
   return s;
 }
 
-// The groups that have rows, in order; by the block's first warp.
-__device__ __forceinline__ void groups_with_rows(const GroupTables& g, GroupSpan* spans, int* groups, int* count) {
+// The groups' rows in chunks of at most MOST, group after group: chunk c
+// belongs to the last group whose `first` is not above c.  PADDING: a group's
+// padding is cut up with its rows; else a group that has padding alone is one
+// chunk.  By the block's first warp.
+struct GroupChunks {
+  GroupSpan span[MM_MAX_EXPERTS];
+  int first[MM_MAX_EXPERTS];                   // behind the last group: their number
+  int count;
+};
+
+template <int MOST, bool PADDING>
+__device__ __forceinline__ void group_chunks(const GroupTables& g, GroupChunks* t) {
+  static_assert(MM_MAX_EXPERTS == 64, "two groups a lane");
   if (threadIdx.x >= 32) return;
-  int n = 0;
-  for (int e0 = 0; e0 < g.E; e0 += 32) {
-    const int e = e0 + threadIdx.x;
-    const GroupSpan s = e < g.E ? group_span(g, e) : GroupSpan{0, 0, 0};
-    const uint32_t has = __ballot_sync(0xffffffffu, s.r1 > s.r0);
-    if (s.r1 > s.r0) {
-      const int at = n + __popc(has & ((1u << threadIdx.x) - 1u));
-      groups[at] = e;
-      spans[at] = s;
-    }
-    n += __popc(has);
+  const int lane = threadIdx.x;
+  GroupSpan s[2];
+  int mine[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int e = 2 * lane + i;
+    s[i] = e < g.E ? group_span(g, e) : GroupSpan{0, 0, 0};
+    mine[i] = s[i].r1 == s[i].r0 ? 0 : PADDING ? (s[i].r1 - s[i].r0 + MOST - 1) / MOST : max(1, (s[i].n + MOST - 1) / MOST);
   }
-  if (threadIdx.x == 0) *count = n;
+  int upto = mine[0] + mine[1];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  t->span[2 * lane] = s[0];
+  t->span[2 * lane + 1] = s[1];
+  t->first[2 * lane] = upto - mine[1] - mine[0];
+  t->first[2 * lane + 1] = upto - mine[1];
+  if (lane == 31) t->count = upto;
+}
+
+// The group of chunk c < count; by a full warp.
+__device__ __forceinline__ int chunk_group(const GroupChunks& t, int c) {
+  const int lane = threadIdx.x & 31;
+  return __popc(__ballot_sync(0xffffffffu, t.first[lane] <= c)) + __popc(__ballot_sync(0xffffffffu, t.first[lane + 32] <= c)) - 1;
+}
+
+// Chunks of `most` rows that any grouping of the rows can give.
+inline int64_t most_chunks(const GroupTables& g, int most) {
+  const int64_t groups = std::min<int64_t>(g.E, g.rows);
+  return groups + (g.rows - groups) / most;
 }
 
 // Where the tile with index t lies among tiles of `block` rows of every group

@@ -1,6 +1,9 @@
-// Experts' products on the CUDA cores with fp32 multiply-adds (fp32 rows;
-// the tensor cores' TF32 keeps 11 bits of each operand, which misses fp32's
-// accuracy by three digits).
+// Experts' products of fp32 rows on the CUDA cores with fp32 multiply-adds:
+// few rows of a forward pass, and the calls whose values cannot be split into
+// three bf16 parts for the tensor cores (grouped_tc.cu), told by a flag on the
+// device that the tile kernel returns on.  The tiles are bound by the
+// multiply-adds (T = 1000, E = 4, K = 768, N = 2432: 148 us, of which 52 at 72
+// Tflop/s; the tensor cores take 50).
 //
 //   forward   ys[r, n]  = sum_k xs[r, k] w[e, n, k]       A = xs, B = w[e], both with k contiguous
 //   dgrad     dxs[r, k] = sum_n dys[r, n] w[e, n, k]      A = dys, B = w[e] with its output index contiguous
@@ -13,7 +16,8 @@
 // this one is multiplied.
 //
 // Few rows (forward): a warp takes four rows of w times up to eight rows of x,
-// with the summed index over its lanes, and reads each row of w once.
+// with the summed index over its lanes; an expert's next eight rows go to
+// another warp (20 rows, K = N = 2048: 126 us one after the other, 53).
 #include "grouped.cuh"
 #include "pack.cuh"
 
@@ -172,61 +176,60 @@ grouped_simt_kernel(const float* __restrict__ a, const float* __restrict__ b, fl
   }
 }
 
-// Few rows: four rows of w (a warp's) times the group's rows of x, eight at a
-// time.  V = 4: rows start on 16 bytes.
+// Few rows: four rows of w (a warp's) times up to eight of the group's rows of
+// x.  V = 4: rows start on 16 bytes.
 constexpr int kSimtFewW = 4, kSimtFewX = 8;
 
 template <int V>
 __global__ void __launch_bounds__(128)
 grouped_simt_few_kernel(const float* __restrict__ x, const float* __restrict__ w, float* __restrict__ out,
                         const GroupTables g, const int N, const int K) {
-  __shared__ GroupSpan s_span[MM_MAX_EXPERTS];
-  __shared__ int s_group[MM_MAX_EXPERTS], s_count;
+  __shared__ GroupChunks s_chunks;
   pdl_enter();
-  groups_with_rows(g, s_span, s_group, &s_count);
+  group_chunks<kSimtFewX, true>(g, &s_chunks);
   __syncthreads();
   const int lane = threadIdx.x & 31;
   const int tiles = (N + kSimtFewW - 1) / kSimtFewW;
-  const int64_t units = static_cast<int64_t>(s_count) * tiles;
+  const int64_t units = static_cast<int64_t>(s_chunks.count) * tiles;
   for (int64_t u = blockIdx.x * 4ll + (threadIdx.x >> 5); u < units; u += gridDim.x * 4ll) {
-    const int i = static_cast<int>(u / tiles), n0 = static_cast<int>(u % tiles) * kSimtFewW;
-    const GroupSpan s = s_span[i];
+    const int chunk = static_cast<int>(u / tiles), n0 = static_cast<int>(u % tiles) * kSimtFewW;
+    const int e = chunk_group(s_chunks, chunk);
+    const GroupSpan s = s_chunks.span[e];
+    const int r = (chunk - s_chunks.first[e]) * kSimtFewX;
     const float* wr[kSimtFewW];
 #pragma unroll
     for (int q = 0; q < kSimtFewW; ++q)        // rows of w behind the last one are read as the last one, and not stored
-      wr[q] = w + (static_cast<int64_t>(s_group[i]) * N + min(n0 + q, N - 1)) * K;
-    for (int r = 0; r < s.r1 - s.r0; r += kSimtFewX) {
-      const int rows = min(kSimtFewX, s.n - r);      // <= 0: padding alone
-      const float* xr = x + static_cast<int64_t>(s.r0 + r) * K;
-      float acc[kSimtFewX * kSimtFewW];              // [row of x][row of w]
+      wr[q] = w + (static_cast<int64_t>(e) * N + min(n0 + q, N - 1)) * K;
+    const int rows = min(kSimtFewX, s.n - r);        // <= 0: padding alone
+    const float* xr = x + static_cast<int64_t>(s.r0 + r) * K;
+    float acc[kSimtFewX * kSimtFewW];              // [row of x][row of w]
 #pragma unroll
-      for (int q = 0; q < kSimtFewX * kSimtFewW; ++q) acc[q] = 0.f;
-      if (rows > 0)
+    for (int q = 0; q < kSimtFewX * kSimtFewW; ++q) acc[q] = 0.f;
+    if (rows > 0)
 #pragma unroll 2
-        for (int k = V * lane; k < K; k += 32 * V) {
-          float wv[kSimtFewW][V], xv[V];
+      for (int k = V * lane; k < K; k += 32 * V) {
+        float wv[kSimtFewW][V], xv[V];
 #pragma unroll
-          for (int q = 0; q < kSimtFewW; ++q) {
-            const auto raw = *reinterpret_cast<const typename Pack<float, V>::Raw*>(wr[q] + k);
+        for (int q = 0; q < kSimtFewW; ++q) {
+          const auto raw = *reinterpret_cast<const typename Pack<float, V>::Raw*>(wr[q] + k);
 #pragma unroll
-            for (int e = 0; e < V; ++e) wv[q][e] = Pack<float, V>::get(raw, e);
-          }
-#pragma unroll
-          for (int j = 0; j < kSimtFewX; ++j) {
-            if (j >= rows) break;
-            const auto raw = *reinterpret_cast<const typename Pack<float, V>::Raw*>(xr + static_cast<int64_t>(j) * K + k);
-#pragma unroll
-            for (int e = 0; e < V; ++e) xv[e] = Pack<float, V>::get(raw, e);
-#pragma unroll
-            for (int q = 0; q < kSimtFewW; ++q)
-#pragma unroll
-              for (int e = 0; e < V; ++e) acc[j * kSimtFewW + q] = fmaf(wv[q][e], xv[e], acc[j * kSimtFewW + q]);
-          }
+          for (int e = 0; e < V; ++e) wv[q][e] = Pack<float, V>::get(raw, e);
         }
-      const float sum = reduce_scatter(acc, lane);   // lane: row of x lane / 4, row of w lane % 4
-      const int row = r + lane / kSimtFewW, n = n0 + lane % kSimtFewW;
-      if (row < s.r1 - s.r0 && n < N) out[static_cast<int64_t>(s.r0 + row) * N + n] = row < s.n ? sum : 0.f;
-    }
+#pragma unroll
+        for (int j = 0; j < kSimtFewX; ++j) {
+          if (j >= rows) break;
+          const auto raw = *reinterpret_cast<const typename Pack<float, V>::Raw*>(xr + static_cast<int64_t>(j) * K + k);
+#pragma unroll
+          for (int e = 0; e < V; ++e) xv[e] = Pack<float, V>::get(raw, e);
+#pragma unroll
+          for (int q = 0; q < kSimtFewW; ++q)
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[j * kSimtFewW + q] = fmaf(wv[q][e], xv[e], acc[j * kSimtFewW + q]);
+        }
+      }
+    const float sum = reduce_scatter(acc, lane);   // lane: row of x lane / 4, row of w lane % 4
+    const int row = r + lane / kSimtFewW, n = n0 + lane % kSimtFewW;
+    if (row < s.r1 - s.r0 && n < N) out[static_cast<int64_t>(s.r0 + row) * N + n] = row < s.n ? sum : 0.f;
   }
 }
 
@@ -246,8 +249,8 @@ static int64_t simt_row_tiles(int op, const GroupTables& g, int M, int tm) {
 }
 
 // Tiles of 64 rows where tiles of 128 would not go round the SMs four times:
-// the last round is shorter (T = 1000, E = 4, K = 768, N = 2432: SIMT_64 us
-// against SIMT_128).
+// the last round is shorter (T = 1000, E = 4, K = 768, N = 2432: 148 us against
+// 153).
 template <int OP>
 static cudaError_t simt(const void* a, const void* b, void* out, const GroupTables& g, int M, int N, int K, bool vec,
                         const int* only_if, cudaStream_t st) {
@@ -263,7 +266,7 @@ cudaError_t launch_grouped_simt(int op, const GroupedArgs& p, const int* only_if
   if (op == kGroupedWgrad) return simt<kGroupedWgrad>(p.dys, p.xs, p.out, p.g, p.N, p.K, 0, kn4, only_if, st);
   if (op == kGroupedDgrad) return simt<kGroupedDgrad>(p.dys, p.w, p.out, p.g, 0, p.K, p.N, kn4, only_if, st);
   if (p.g.rows > f32_stream_rows(p.g.E)) return simt<kGroupedForward>(p.xs, p.w, p.out, p.g, 0, p.N, p.K, k4, only_if, st);
-  const int64_t units = std::min<int64_t>(p.g.E, p.g.rows) * ((p.N + kSimtFewW - 1) / kSimtFewW);
+  const int64_t units = most_chunks(p.g, kSimtFewX) * ((p.N + kSimtFewW - 1) / kSimtFewW);
   auto fn = k4 ? grouped_simt_few_kernel<4> : grouped_simt_few_kernel<1>;
   const int64_t most = static_cast<int64_t>(num_sms()) * resident_blocks(reinterpret_cast<const void*>(fn), 128);
   return launch_dependent_kernel(fn, dim3(static_cast<unsigned>(std::min((units + 3) / 4, most))), dim3(128), 0, st,

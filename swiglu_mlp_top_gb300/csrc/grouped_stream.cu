@@ -3,21 +3,24 @@
 // row once, and below some ten MB by the latency of doing so.
 //
 // A block takes 16 rows of w (output columns) of one expert and up to 32 of
-// its rows of x; its four or eight warps share out the summed index in steps of 32
-// (4 bits: 128) columns.  A warp multiplies with mma.sync m16n8k16, the
-// weights as the M operand straight from global memory: the order of the
-// summed index is free as long as both operands use the same, so a lane takes
-// 16 contiguous bytes of a weight row, which are 8 values (4 bits: a whole
-// group of 32 and its scale), and the same columns of x.  All loads of a few
-// steps are in flight before the first product.  (The tensor cores of
-// tcgen05 want their operands in shared memory and tiles of 128 rows: for
-// these shapes a longer way to the same bytes.)
+// its rows of x; an expert with more rows has them shared out over blocks (64
+// tokens of a skewed routing, E = 8, k = 2, K = 2432, N = 768, 4 bits: 16 us
+// one after the other, 12).  The block's four or eight warps share out the
+// summed index in steps of 32 (4 bits: 128) columns.  A warp multiplies with
+// mma.sync m16n8k16, the weights as the M operand straight from global memory:
+// the order of the summed index is free as long as both operands use the same,
+// so a lane takes 16 contiguous bytes of a weight row, which are 8 values (4
+// bits: a whole group of 32 and its scale), and the same columns of x.  All
+// loads of a few steps are in flight before the first product.  (The tensor
+// cores of tcgen05 want their operands in shared memory and tiles of 128 rows:
+// for these shapes a longer way to the same bytes.)
 #include "grouped.cuh"
 #include "mx4.cuh"
 
 namespace mm {
 
 constexpr int kGsRows = 16;                  // rows of w per block
+constexpr int kGsMost = 32;                  // rows of x
 
 struct GsParams {
   const __nv_bfloat16* x;   // [rows, K], K a multiple of 8
@@ -125,7 +128,7 @@ __device__ __forceinline__ void gs_rows(const GsParams& P, int e, int n0, int64_
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   __syncthreads();                             // the last use of s_part is over
   // [warp][row of x][row of w]
-  float* mine = s_part + warp * (32 * kGsRows);
+  float* mine = s_part + warp * (kGsMost * kGsRows);
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -136,7 +139,7 @@ __device__ __forceinline__ void gs_rows(const GsParams& P, int e, int n0, int64_
     float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
-      const float2 p = *reinterpret_cast<const float2*>(s_part + w * (32 * kGsRows) + r * kGsRows + c);
+      const float2 p = *reinterpret_cast<const float2*>(s_part + w * (kGsMost * kGsRows) + r * kGsRows + c);
       sum.x += p.x;
       sum.y += p.y;
     }
@@ -153,26 +156,27 @@ __device__ __forceinline__ void gs_rows(const GsParams& P, int e, int n0, int64_
 template <bool MX4, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS)
 grouped_stream_kernel(const GsParams P) {
-  __shared__ __align__(16) float s_part[WARPS * 32 * kGsRows];
-  __shared__ GroupSpan s_span[MM_MAX_EXPERTS];
-  __shared__ int s_group[MM_MAX_EXPERTS];      // the groups that have rows
-  __shared__ int s_count;
+  __shared__ __align__(16) float s_part[WARPS * kGsMost * kGsRows];
+  __shared__ GroupChunks s_chunks;
   pdl_enter();
-  groups_with_rows(P.g, s_span, s_group, &s_count);
+  group_chunks<kGsMost, false>(P.g, &s_chunks);
   __syncthreads();
   const int tiles = (P.N + kGsRows - 1) / kGsRows;
-  const int64_t units = static_cast<int64_t>(s_count) * tiles;
+  const int64_t units = static_cast<int64_t>(s_chunks.count) * tiles;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int i = static_cast<int>(u / tiles), n0 = static_cast<int>(u % tiles) * kGsRows;
-    const GroupSpan s = s_span[i];
-    const int e = s_group[i];
-    for (int r = 0; r < s.n; r += 32) {
-      const int rows = min(32, s.n - r);
-      const int64_t row0 = s.r0 + r;
-      if (rows <= 8) gs_rows<MX4, WARPS, 1>(P, e, n0, row0, rows, s_part);
-      else if (rows <= 16) gs_rows<MX4, WARPS, 2>(P, e, n0, row0, rows, s_part);
-      else gs_rows<MX4, WARPS, 4>(P, e, n0, row0, rows, s_part);
-    }
+    const int chunk = static_cast<int>(u / tiles), n0 = static_cast<int>(u % tiles) * kGsRows;
+    const int e = chunk_group(s_chunks, chunk);
+    const GroupSpan s = s_chunks.span[e];
+    const int c = chunk - s_chunks.first[e], of = (s.n + kGsMost - 1) / kGsMost;
+    const int each = of > 1 ? ((s.n + of - 1) / of + 7) / 8 * 8 : kGsMost;
+    const int rows = min(each, s.n - c * each);
+    const int64_t row0 = static_cast<int64_t>(s.r0) + c * each;
+    if (rows <= 0) {
+    } else if (rows <= 8) gs_rows<MX4, WARPS, 1>(P, e, n0, row0, rows, s_part);
+    else if (rows <= 16) gs_rows<MX4, WARPS, 2>(P, e, n0, row0, rows, s_part);
+    else if (rows <= 24) gs_rows<MX4, WARPS, 3>(P, e, n0, row0, rows, s_part);
+    else gs_rows<MX4, WARPS, 4>(P, e, n0, row0, rows, s_part);
+    if (c > 0) continue;
     // padding rows of the group
     const int cols = min(kGsRows, P.N - n0);
     for (int v = threadIdx.x; v < (s.r1 - s.r0 - s.n) * kGsRows; v += 32 * WARPS)
@@ -193,7 +197,7 @@ static cudaError_t gs_launch(const GsParams& p, int64_t units, cudaStream_t st) 
 // with a tile for every four warps they are slower by 10 to 30%.
 template <bool MX4>
 static cudaError_t gs_choose(const GsParams& p, cudaStream_t st) {
-  const int64_t units = std::min<int64_t>(p.g.E, p.g.rows) * ((p.N + kGsRows - 1) / kGsRows);
+  const int64_t units = most_chunks(p.g, kGsMost) * ((p.N + kGsRows - 1) / kGsRows);
   const bool wide = units <= 2 * num_sms();
   return wide ? gs_launch<MX4, 8>(p, units, st) : gs_launch<MX4, 4>(p, units, st);
 }
