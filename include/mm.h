@@ -511,7 +511,8 @@ int mm_swiglu_act_backward(const void* codes, const uint8_t* exps, const void* d
  * three bf16 parts each, which hold all 24 bits (six of the nine products; the
  * others are below 2^-25); a call whose operands hold an infinity, a NaN, a
  * magnitude of 2^127 or more or one below 2^-100 that is not zero, in a row
- * that counts, runs on the CUDA cores instead, with the same accuracy.
+ * that counts, runs on the CUDA cores instead, with the same accuracy.  (On the
+ * tensor cores a sum within 2^-7 of the largest number may become an infinity.)
  * Outputs overlap neither inputs nor each other.  `status_ws` (nullable: no
  * report) is a zeroed workspace of >= 256 bytes read by mm_check_status(),
  * where a device wait that exceeded its time limit is recorded; `workspace`

@@ -97,6 +97,19 @@ def test_many_groups(E, total, align, K, N, how, dtype):
     check(groups(E, total, how), align, K, N, dtype, whole=False)
 
 
+@pytest.mark.parametrize("counts,align", [
+    # few rows, most of them one expert's: its rows are shared out over blocks
+    ([32], 1), ([17], 1), ([0, 33], 1), ([25, 0, 18], 1), ([9, 33, 2], 2), ([66, 3, 0, 1, 0, 0, 0, 0], 1), ([50, 0, 0, 5, 0, 0, 0, 0], 8),
+    # the same for fp32
+    ([15], 1), ([0, 19], 1), ([9, 0, 14], 1), ([9, 0, 8], 4), ([40, 0, 0, 1, 0, 0, 0, 0], 1), ([17, 0, 0, 7, 0, 0, 0, 0], 16)])
+def test_few_rows_of_one_expert(counts, align):
+    for K, N in ((256, 40), (2432, 72), (8, 17), (4096, 16)):
+        for dtype in (BF, F32):
+            check(counts, align, K, N, dtype, whole=True)
+    check(counts, align, 264, 100, BF, whole=False)
+    check(counts, align, 264, 100, F32, whole=False)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("counts,align,K,N", [
     # few tiles with a long sum: cut into parts
@@ -155,6 +168,21 @@ def test_no_rows():
     q = mm.mx4_quantize(x)
     assert mm.mx4_dequantize(q).shape == (0, 64)
     assert mm.mx4_matmul(q, mm.mx4_quantize(w), plan).shape == (0, 32)
+
+
+@pytest.mark.parametrize("sx,sw", [(-40, -40), (-60, -50), (-60, -66), (60, 50)])
+def test_fp32_of_every_magnitude(sx, sw):
+    """Products far from 1, down to those below the smallest normal number,
+    where a sum is off by that number's steps."""
+    gen = torch.Generator().manual_seed(6)
+    R, K, N = 200, 96, 72
+    x, w, dy = torch.randn(R, K, generator=gen) * 2.0 ** sx, torch.randn(N, K, generator=gen) * 2.0 ** sw, torch.randn(R, N, generator=gen) * 2.0 ** sw
+    y, dw = mm.grouped_matmul(x.cuda(), w.cuda()), mm.grouped_matmul_backward(dy.cuda(), x.cuda(), None)[1]
+    for got, a, b, n in ((y, x, w.T, K), (dw, dy.T, x, R)):
+        want, terms = a.double() @ b.double(), a.double().abs() @ b.double().abs()
+        # each of the at most six products and their sums: 2^-24 of the terms' sizes, or half of the smallest step
+        bound = 2 * (n + 1) * (2.0 ** -24 * terms + 6 * 2.0 ** -150)
+        assert bool(((got.double().cpu() - want).abs() <= bound).all())
 
 
 def test_one_gradient_at_a_time():
@@ -331,6 +359,15 @@ def check_mx4(counts, align, K, N, four, whole, tail=3):
 def test_mx4_products(counts, align, K, N, four):
     check_mx4(counts, align, K, N, four, whole=True)
     check_mx4(counts, align, K, N, four, whole=False)
+
+
+@pytest.mark.parametrize("counts,align", [
+    # few bf16 rows, most of them one expert's
+    ([75], 1), ([33], 1), ([49, 40], 1), ([90, 0, 16], 1), ([65, 0, 9], 16), ([150, 9, 24, 0, 0, 0, 0, 0], 1), ([97, 0, 0, 2, 0, 0, 0, 0], 32)])
+def test_mx4_few_rows_of_one_expert(counts, align):
+    for K, N in ((256, 40), (2432, 72), (8, 17), (4096, 16)):
+        check_mx4(counts, align, K, N, False, whole=True)
+    check_mx4(counts, align, 264, 100, False, whole=False)
 
 
 @pytest.mark.parametrize("four", [True, False])
