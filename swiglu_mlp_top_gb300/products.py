@@ -9,6 +9,7 @@ what a device wait that gave up would report.
 """
 from __future__ import annotations
 
+from functools import lru_cache
 from typing import Optional, Union
 
 import torch
@@ -19,6 +20,12 @@ from .block_ops import _arg, _begin, _empty, _rows_arg, _scratch
 
 _GROUP = 32          # columns that share a scale
 _WORD = 4            # scales of a row next to each other
+
+
+@lru_cache(maxsize=1024)
+def _need(query: str, dev: int, *sizes) -> int:
+    """Scratch of a call on the current device `dev`: a function of the sizes alone."""
+    return getattr(L.load(), query)(*sizes)
 
 
 def _device(t, name: str, stream):
@@ -85,7 +92,7 @@ def grouped_matmul(xs: torch.Tensor, w: torch.Tensor, plan: Optional[dict] = Non
     px = _arg(xs, "xs", dev, xs.dtype, (R, K))
     pw = _arg(w, "w", dev, xs.dtype, _weight_shape(E, plan is not None, N, K))
     lib = L.load()
-    need = lib.mm_grouped_matmul_workspace_bytes(R, K, N, E, dt)
+    need = _need("mm_grouped_matmul_workspace_bytes", dev, R, K, N, E, dt)
     ps = _status_arg(status_workspace, dev)
     pws, nbytes, keep = _scratch(workspace, need, dev, stream, "grouped_matmul")
     if out is None:
@@ -130,7 +137,7 @@ def grouped_matmul_backward(dys: torch.Tensor, xs: Optional[torch.Tensor], w: Op
     if dw is not None and xs is None:
         raise ValueError("dw needs xs")
     lib = L.load()
-    need = lib.mm_grouped_matmul_backward_workspace_bytes(R, K, N, E, dt)
+    need = _need("mm_grouped_matmul_backward_workspace_bytes", dev, R, K, N, E, dt)
     ps = _status_arg(status_workspace, dev)
     pws, nbytes, keep = _scratch(workspace, need, dev, stream, "grouped_matmul_backward")
     if w is not None and out is None:
@@ -242,7 +249,7 @@ def mx4_matmul(x: Union[torch.Tensor, dict], w: dict, plan: Optional[dict] = Non
     if wshape != _weight_shape(E, plan is not None, N, K):
         raise ValueError(f"w must be {list(_weight_shape(E, plan is not None, N, K))}, got {list(wshape)}")
     lib = L.load()
-    need = lib.mm_mx4_matmul_workspace_bytes(R, K, N, E, four)
+    need = _need("mm_mx4_matmul_workspace_bytes", dev, R, K, N, E, four)
     ps = _status_arg(status_workspace, dev)
     pws, nbytes, keep = _scratch(workspace, need, dev, stream, "mx4_matmul")
     if out is None:
