@@ -1,5 +1,6 @@
-// Experts' products of fp32 rows on the CUDA cores with fp32 multiply-adds:
-// few rows of a forward pass, and the calls whose values cannot be split into
+// Experts' products of fp32 rows on the CUDA cores with fp32 multiply-adds: few
+// rows of a forward pass with a width that is no multiple of 8 (others:
+// grouped_stream.cu), and the calls whose values cannot be split into
 // three bf16 parts for the tensor cores (grouped_tc.cu), told by a flag on the
 // device that the tile kernel returns on.  The tiles are bound by the
 // multiply-adds (T = 1000, E = 4, K = 768, N = 2432: 148 us, of which 52 at 72
@@ -159,12 +160,15 @@ grouped_simt_kernel(const float* __restrict__ a, const float* __restrict__ b, fl
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int m = m0 + (i < 4 ? 4 * ty + i : TM / 2 + 4 * ty + i - 4);
-    if (m >= mend) continue;                       // padding rows hold zeros: their A was left out
+    if (m >= mend) continue;
+    const bool counts = m < mval;                  // padding rows become zeros, whatever B holds
     float* row = out + out0 + static_cast<int64_t>(m) * N;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int n = n0 + 64 * h + 4 * tx;
-      const float v[4] = {lo2(acc[i][2 * h]), hi2(acc[i][2 * h]), lo2(acc[i][2 * h + 1]), hi2(acc[i][2 * h + 1])};
+      float v[4] = {lo2(acc[i][2 * h]), hi2(acc[i][2 * h]), lo2(acc[i][2 * h + 1]), hi2(acc[i][2 * h + 1])};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = counts ? v[j] : 0.f;
       if (V == 4 && OP != 0) {                     // N is a multiple of 4
         if (n < N) *reinterpret_cast<float4*>(row + n) = make_float4(v[0], v[1], v[2], v[3]);
       } else {

@@ -103,11 +103,12 @@ def test_many_groups(E, total, align, K, N, how, dtype):
     # the same for fp32
     ([15], 1), ([0, 19], 1), ([9, 0, 14], 1), ([9, 0, 8], 4), ([40, 0, 0, 1, 0, 0, 0, 0], 1), ([17, 0, 0, 7, 0, 0, 0, 0], 16)])
 def test_few_rows_of_one_expert(counts, align):
-    for K, N in ((256, 40), (2432, 72), (8, 17), (4096, 16)):
+    for K, N in ((256, 40), (2432, 72), (8, 17), (4096, 16), (1001, 33), (36, 20)):
         for dtype in (BF, F32):
             check(counts, align, K, N, dtype, whole=True)
-    check(counts, align, 264, 100, BF, whole=False)
-    check(counts, align, 264, 100, F32, whole=False)
+    for K in (264, 100, 65):
+        check(counts, align, K, 100, BF, whole=False)
+        check(counts, align, K, 100, F32, whole=False)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -120,11 +121,12 @@ def test_sums_in_parts(counts, align, K, N, dtype):
     check(counts, align, K, N, dtype, whole=False, start=align)
 
 
-def test_fp32_of_every_size():
+@pytest.mark.parametrize("counts", [[200, 150], [20, 15], [40, 3]])
+def test_fp32_of_every_size(counts):
     """Values that bf16 parts cannot hold (infinities, NaN, above 2^127, below
     2^-100) anywhere among the operands: the results are those of fp32 products."""
     gen = torch.Generator().manual_seed(12)
-    E, K, N, counts = 2, 72, 40, [200, 150]
+    E, K, N = 2, 72, 40
     plan = ref.tables(counts, 8)
     rows = int(plan["offsets"][-1]) + 3
     gplan = on_gpu(plan)
@@ -170,12 +172,13 @@ def test_no_rows():
     assert mm.mx4_matmul(q, mm.mx4_quantize(w), plan).shape == (0, 32)
 
 
+@pytest.mark.parametrize("R", [200, 30])
 @pytest.mark.parametrize("sx,sw", [(-40, -40), (-60, -50), (-60, -66), (60, 50)])
-def test_fp32_of_every_magnitude(sx, sw):
+def test_fp32_of_every_magnitude(sx, sw, R):
     """Products far from 1, down to those below the smallest normal number,
     where a sum is off by that number's steps."""
     gen = torch.Generator().manual_seed(6)
-    R, K, N = 200, 96, 72
+    K, N = 96, 72
     x, w, dy = torch.randn(R, K, generator=gen) * 2.0 ** sx, torch.randn(N, K, generator=gen) * 2.0 ** sw, torch.randn(R, N, generator=gen) * 2.0 ** sw
     y, dw = mm.grouped_matmul(x.cuda(), w.cuda()), mm.grouped_matmul_backward(dy.cuda(), x.cuda(), None)[1]
     for got, a, b, n in ((y, x, w.T, K), (dw, dy.T, x, R)):
