@@ -507,12 +507,13 @@ int mm_swiglu_act_backward(const void* codes, const uint8_t* exps, const void* d
  * rows from offsets[E] on (and before offsets[0]) are left as they were; what
  * stands in padding rows and behind in inputs (NaN too) has no effect.
  * Sums in fp32 in a fixed order (deterministic), one rounding per element.
- * fp32 operands of more than a few rows are multiplied on the tensor cores as
- * three bf16 parts each, which hold all 24 bits (six of the nine products; the
- * others are below 2^-25); a call whose operands hold an infinity, a NaN, a
- * magnitude of 2^127 or more or one below 2^-100 that is not zero, in a row
- * that counts, runs on the CUDA cores instead, with the same accuracy.  (On the
- * tensor cores a sum within 2^-7 of the largest number may become an infinity.)
+ * fp32 operands are multiplied on the tensor cores as three bf16 parts each,
+ * which hold all 24 bits (six of the nine products; the others are below
+ * 2^-25).  Where operands hold an infinity, a NaN, a magnitude of 2^127 or more
+ * or one below 2^-100 that is not zero, in a row that counts, the call (of few
+ * rows: the results that it touches) is made on the CUDA cores instead, with
+ * the same accuracy.  (On the tensor cores a sum within 2^-7 of the largest
+ * number may become an infinity.)
  * Outputs overlap neither inputs nor each other.  `status_ws` (nullable: no
  * report) is a zeroed workspace of >= 256 bytes read by mm_check_status(),
  * where a device wait that exceeded its time limit is recorded; `workspace`

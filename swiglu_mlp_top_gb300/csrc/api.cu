@@ -1169,8 +1169,12 @@ static bool status_ok(const void* status_ws) { return aligned16(status_ws); }
 // rows 10 against 26.  With weights in 4 bits, which the tiles have to convert:
 // 128 rows 20 us against 23, 256 29 against 24; E = 64, 1024 rows 66 against 88,
 // 2048 104 against 88; one matrix, 64 rows 26 against 28, 128 50 against 28.
-static bool grouped_streams(int64_t rows, int K, int E, bool w_in_4_bits) {
-  return K % 8 == 0 && rows <= (w_in_4_bits ? 64 + 16 * E : 32 + 6 * E);
+// fp32, which the tiles first have to split: K = N = 2048, E = 8, 60 rows 63 us
+// against 131, 250 rows 117 against 133, 500 rows 177 against 133; E = 32, K = N
+// = 1024, 500 rows 66 against 135, 2000 rows 174 against 139; one matrix, 64
+// rows 26 against 35, 130 rows 57 against 36.
+static bool grouped_streams(int64_t rows, int K, int E, int dtype, bool w_in_4_bits) {
+  return K % 8 == 0 && rows <= (w_in_4_bits ? 64 + 16 * E : dtype == kDtypeBF16 ? 32 + 6 * E : 32 + 32 * E);
 }
 // What a call of a product needs beside its tensors.
 struct GroupedPlan {
@@ -1181,9 +1185,10 @@ struct GroupedPlan {
   size_t parts;               // one set, for the operations one after the other
   size_t total;
 };
-// fp32: a forward pass of few rows streams its weights on the CUDA cores
-// (grouped_simt.cu), all else goes to the tensor cores: T = 1000, E = 4, K = 768,
-// N = 2432 148 -> 50 us, 8000 rows, E = 8 634 -> 163; 64 rows, E = 8 equal.
+// fp32 that is not streamed: a forward pass of few rows, whose width keeps them
+// from starting on 16 bytes, goes to the CUDA cores (grouped_simt.cu), all else
+// to the tensor cores: T = 1000, E = 4, K = 768, N = 2432 148 -> 50 us, 8000
+// rows, E = 8 634 -> 163; 64 rows, E = 8 equal.
 static bool f32_on_tensor_cores(int64_t rows, int E, bool backward) {
   return (backward || rows > f32_stream_rows(E)) && rows <= int64_t{1} << 29;       // three planes of rows are counted in 32 bits
 }
@@ -1215,7 +1220,7 @@ static GroupedPlan grouped_plan(int64_t rows, int K, int N, int E, int dtype, bo
 }
 static size_t grouped_bytes(int64_t rows, int K, int N, int E, int dtype, bool backward) {
   if (!valid_dtype(dtype) || rows < 1 || K < 1 || N < 1 || E < 1 || !grouped_in_limits(rows, K, N, E)) return 0;
-  if (!backward && dtype == kDtypeBF16 && grouped_streams(rows, K, E, false)) return 0;
+  if (!backward && grouped_streams(rows, K, E, dtype, false)) return 0;
   return grouped_plan(rows, K, N, E, dtype, backward).total;
 }
 // Makes the operands of `a` ready that are not null: as given, or their copies.
@@ -1278,8 +1283,8 @@ int mm_grouped_matmul(const void* xs, const void* w, const int32_t* offsets, con
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const GroupedArgs given{xs, nullptr, w, ys, GroupTables{offsets, counts, rows, E}, K, N};
   cudaError_t e = cudaSuccess;
-  if (dtype == kDtypeBF16 && grouped_streams(rows, K, E, false)) {
-    e = counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_grouped_stream(given, st); });
+  if (grouped_streams(rows, K, E, dtype, false)) {
+    e = counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_grouped_stream(dtype, given, st); });
   } else {
     const GroupedPlan L = grouped_plan(rows, K, N, E, dtype, false);
     GroupedArgs a = given;
@@ -1371,7 +1376,7 @@ static Mx4Layout mx4_layout(int64_t rows, int K, int N, int E, bool four) {
   // converted against 40, 8192 rows 79 against 71; one matrix 4096 x 4096, 256
   // rows 28 against 37, 1024 rows 44 against 32; 4096 x 512, 256 rows 24 against 14.
   const bool copy = rows >= 512 * static_cast<int64_t>(E) || P.splits[kGroupedForward] > 1;
-  L.path = grouped_streams(rows, K, E, true) ? kMx4Stream : copy ? kMx4Copy : kMx4Convert;
+  L.path = grouped_streams(rows, K, E, kDtypeBF16, true) ? kMx4Stream : copy ? kMx4Copy : kMx4Convert;
   if (L.path == kMx4Copy) {
     L.x = align_up(2 * static_cast<size_t>(E) * N * K);
     L.total = L.x + grouped_bytes(rows, K, N, E, kDtypeBF16, false);

@@ -202,6 +202,28 @@ __device__ __forceinline__ int gm_index(int j, int c, int nc) {
   return j * nc + c;
 }
 
+// Eight fp32 values as three bf16 parts, each the nearest of what the ones
+// before leave.  bad: a value has no such parts, being an infinity, a NaN, above
+// 2^127 (the first may round to infinity) or below 2^-100 but not zero (the
+// last may fall below bf16's smallest).
+__device__ __forceinline__ void split_vector(const float (&x)[8], uint4 (&planes)[3], bool& bad) {
+  uint32_t p[3][4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float a = x[2 * j], b = x[2 * j + 1];
+    const float lo = fminf(fabsf(a) == 0.f ? 1.f : fabsf(a), fabsf(b) == 0.f ? 1.f : fabsf(b));
+    bad |= !(fabsf(a) < 0x1p127f) | !(fabsf(b) < 0x1p127f) | (lo < 0x1p-100f);
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      p[q][j] = pack_bf16x2(a, b);
+      a -= __uint_as_float(p[q][j] << 16);
+      b -= __uint_as_float(p[q][j] & 0xffff0000u);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 3; ++q) planes[q] = make_uint4(p[q][0], p[q][1], p[q][2], p[q][3]);
+}
+
 // A warp's 32 rows x 64 columns of bf16 (a row a lane) out through its stage of
 // 128-byte rows (16-byte chunk q of row i at chunk q ^ (i & 7)); `rem` rows are
 // the group's.

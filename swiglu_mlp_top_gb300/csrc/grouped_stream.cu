@@ -1,5 +1,5 @@
 // Experts' products for few rows: ys[r, n] = sum_k x[r, k] w[e, n, k] with bf16
-// rows and weights in bf16 or in 4 bits.  Bound by reading each needed weight
+// rows and weights in bf16 or in 4 bits, or both in fp32.  Bound by reading each needed weight
 // row once, and below some ten MB by the latency of doing so.
 //
 // A block takes 16 rows of w (output columns) of one expert and up to 32 of
@@ -14,6 +14,13 @@
 // loads of a few steps are in flight before the first product.  (The tensor
 // cores of tcgen05 want their operands in shared memory and tiles of 128 rows:
 // for these shapes a longer way to the same bytes.)
+//
+// fp32 values are split into three bf16 parts in registers, of whose nine
+// products six are made (grouped_tc.cu); every 32 columns' sum is added in
+// fp32.  A block that meets a value without such parts makes its results with
+// multiply-adds.  (One token, E = 8, K = 1024, N = 2048: 6.7 us, 7.7 with
+// multiply-adds alone; four rows, K = N = 2048: 9.6 against 31; from some 16
+// rows of an expert on, splitting and the six products bound it.)
 #include "grouped.cuh"
 #include "mx4.cuh"
 
@@ -22,11 +29,13 @@ namespace mm {
 constexpr int kGsRows = 16;                  // rows of w per block
 constexpr int kGsMost = 32;                  // rows of x
 
+enum GsKind { kGsBf16, kGsMx4, kGsF32 };
+
 struct GsParams {
-  const __nv_bfloat16* x;   // [rows, K], K a multiple of 8
-  const uint8_t* w;         // bf16 [E, N, K], or codes [E * N, 16 G]
+  const void* x;            // [rows, K], K a multiple of 8
+  const uint8_t* w;         // [E, N, K], or codes [E * N, 16 G]
   const uint32_t* sc;       // scale words [words, E * N]
-  __nv_bfloat16* out;       // [rows, N]
+  void* out;                // [rows, N], as x
   GroupTables g;
   int K, N;
 };
@@ -38,6 +47,9 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+template <GsKind KIND> struct GsKindTraits { typedef __nv_bfloat16 Row; };
+template <> struct GsKindTraits<kGsF32> { typedef float Row; };
+
 template <bool MX4, int NT>
 struct GsTraits {
   static constexpr int kParts = MX4 ? 4 : 1;                 // 8-column pieces of a lane's step
@@ -116,17 +128,111 @@ __device__ __forceinline__ void gs_sum(const GsParams& P, int64_t wrow, int wlas
   }
 }
 
+// The same in fp32.  Returns whether a value cannot be split.
+template <int WARPS, int NT>
+__device__ __forceinline__ bool gs_sum_f32(const GsParams& P, int64_t wrow, int wlast, const float* x, int rows, float (&acc)[NT][4]) {
+  constexpr int kUnroll = NT == 1 ? 3 : NT == 2 ? 2 : 1;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int steps = (P.K + 31) / 32;
+  const float* w = reinterpret_cast<const float*>(P.w);
+  const float *w0 = w + (wrow + min(g, wlast)) * P.K, *w1 = w + (wrow + min(g + 8, wlast)) * P.K;
+  bool bad = false;
+  auto load = [](float (&v)[8], const float* p, bool in) {
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 a = in ? __ldg(reinterpret_cast<const float4*>(p)) : zero, b = in ? __ldg(reinterpret_cast<const float4*>(p) + 1) : zero;
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  };
+  for (int s0 = warp; s0 < steps; s0 += WARPS * kUnroll) {
+    float a[kUnroll][2][8], b[kUnroll][NT][8];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int s = s0 + u * WARPS, k = 32 * s + 8 * t;      // this lane's first column
+      const bool in = s < steps && k < P.K;
+      load(a[u][0], w0 + k, in);
+      load(a[u][1], w1 + k, in);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) load(b[u][j], x + static_cast<int64_t>(8 * j + g) * P.K + k, in && 8 * j + g < rows);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (s0 + u * WARPS >= steps) break;                    // warp-uniform
+      uint4 v0[3], v1[3];
+      split_vector(a[u][0], v0, bad);
+      split_vector(a[u][1], v1, bad);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        uint4 y[3];
+        split_vector(b[u][j], y, bad);
+        // the small products first
+        constexpr int kPa[6] = {2, 0, 1, 1, 0, 0}, kPb[6] = {0, 2, 1, 0, 1, 0};
+        float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int i = 0; i < 6; ++i) {
+          const uint4 &p = v0[kPa[i]], &q = v1[kPa[i]], &z = y[kPb[i]];
+          mma_bf16(c[0], p.x, q.x, p.y, q.y, z.x, z.y);
+          mma_bf16(c[1], p.z, q.z, p.w, q.w, z.z, z.w);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][i] += c[0][i] + c[1][i];
+      }
+    }
+  }
+  return bad;
+}
+
+// Two neighbouring results (the second one may lie behind the last column).
+__device__ __forceinline__ void gs_store(__nv_bfloat16* o, float a, float b, int left, bool even) {
+  if (even) {
+    if (left > 0) *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(a, b);
+  } else {
+    if (left > 0) o[0] = __float2bfloat16_rn(a);
+    if (left > 1) o[1] = __float2bfloat16_rn(b);
+  }
+}
+__device__ __forceinline__ void gs_store(float* o, float a, float b, int left, bool even) {
+  if (even) {
+    if (left > 0) *reinterpret_cast<float2*>(o) = make_float2(a, b);
+  } else {
+    if (left > 0) o[0] = a;
+    if (left > 1) o[1] = b;
+  }
+}
+
 // 16 columns of `rows` rows (at most 8 NT): the warps' sums joined in warp order.
-template <bool MX4, int WARPS, int NT>
+template <GsKind KIND, int WARPS, int NT>
 __device__ __forceinline__ void gs_rows(const GsParams& P, int e, int n0, int64_t row0, int rows, float* s_part) {
+  typedef typename GsKindTraits<KIND>::Row Row;
   float acc[NT][4];
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
-  gs_sum<MX4, WARPS, NT>(P, static_cast<int64_t>(e) * P.N + n0, P.N - 1 - n0, P.x + row0 * P.K, rows, acc);
+  const Row* x = static_cast<const Row*>(P.x) + row0 * P.K;
+  Row* out = static_cast<Row*>(P.out) + row0 * P.N + n0;
+  const int64_t wrow = static_cast<int64_t>(e) * P.N + n0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  __syncthreads();                             // the last use of s_part is over
+  if constexpr (KIND == kGsF32) {
+    const bool bad = gs_sum_f32<WARPS, NT>(P, wrow, P.N - 1 - n0, x, rows, acc);
+    if (__syncthreads_or(bad)) {               // and the last use of s_part is over
+      const float* w = reinterpret_cast<const float*>(P.w) + wrow * P.K;
+      for (int v = warp; v < rows * kGsRows; v += WARPS) {
+        const int r = v / kGsRows, c = v % kGsRows;
+        if (n0 + c >= P.N) continue;
+        float sum = 0.f;
+        for (int k = lane; k < P.K; k += 32)
+          sum = fmaf(__ldg(w + static_cast<int64_t>(c) * P.K + k), __ldg(x + static_cast<int64_t>(r) * P.K + k), sum);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) out[static_cast<int64_t>(r) * P.N + c] = sum;
+      }
+      return;
+    }
+  } else {
+    gs_sum<KIND == kGsMx4, WARPS, NT>(P, wrow, P.N - 1 - n0, x, rows, acc);
+    __syncthreads();                           // the last use of s_part is over
+  }
   // [warp][row of x][row of w]
   float* mine = s_part + warp * (kGsMost * kGsRows);
 #pragma unroll
@@ -143,21 +249,16 @@ __device__ __forceinline__ void gs_rows(const GsParams& P, int e, int n0, int64_
       sum.x += p.x;
       sum.y += p.y;
     }
-    __nv_bfloat16* o = P.out + (row0 + r) * P.N + n0 + c;
-    if (P.N % 2 == 0) {
-      if (n0 + c < P.N) *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(sum.x, sum.y);
-    } else {
-      if (n0 + c < P.N) o[0] = __float2bfloat16_rn(sum.x);
-      if (n0 + c + 1 < P.N) o[1] = __float2bfloat16_rn(sum.y);
-    }
+    gs_store(out + static_cast<int64_t>(r) * P.N + c, sum.x, sum.y, P.N - n0 - c, P.N % 2 == 0);
   }
 }
 
-template <bool MX4, int WARPS>
+template <GsKind KIND, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS)
 grouped_stream_kernel(const GsParams P) {
   __shared__ __align__(16) float s_part[WARPS * kGsMost * kGsRows];
   __shared__ GroupChunks s_chunks;
+  typedef typename GsKindTraits<KIND>::Row Row;
   pdl_enter();
   group_chunks<kGsMost, false>(P.g, &s_chunks);
   __syncthreads();
@@ -172,22 +273,22 @@ grouped_stream_kernel(const GsParams P) {
     const int rows = min(each, s.n - c * each);
     const int64_t row0 = static_cast<int64_t>(s.r0) + c * each;
     if (rows <= 0) {
-    } else if (rows <= 8) gs_rows<MX4, WARPS, 1>(P, e, n0, row0, rows, s_part);
-    else if (rows <= 16) gs_rows<MX4, WARPS, 2>(P, e, n0, row0, rows, s_part);
-    else if (rows <= 24) gs_rows<MX4, WARPS, 3>(P, e, n0, row0, rows, s_part);
-    else gs_rows<MX4, WARPS, 4>(P, e, n0, row0, rows, s_part);
+    } else if (rows <= 8) gs_rows<KIND, WARPS, 1>(P, e, n0, row0, rows, s_part);
+    else if (rows <= 16) gs_rows<KIND, WARPS, 2>(P, e, n0, row0, rows, s_part);
+    else if (rows <= 24) gs_rows<KIND, WARPS, 3>(P, e, n0, row0, rows, s_part);
+    else gs_rows<KIND, WARPS, 4>(P, e, n0, row0, rows, s_part);
     if (c > 0) continue;
     // padding rows of the group
     const int cols = min(kGsRows, P.N - n0);
     for (int v = threadIdx.x; v < (s.r1 - s.r0 - s.n) * kGsRows; v += 32 * WARPS)
       if (v % kGsRows < cols)
-        P.out[(static_cast<int64_t>(s.r0) + s.n + v / kGsRows) * P.N + n0 + v % kGsRows] = __float2bfloat16_rn(0.f);
+        static_cast<Row*>(P.out)[(static_cast<int64_t>(s.r0) + s.n + v / kGsRows) * P.N + n0 + v % kGsRows] = Row(0.f);
   }
 }
 
-template <bool MX4, int WARPS>
+template <GsKind KIND, int WARPS>
 static cudaError_t gs_launch(const GsParams& p, int64_t units, cudaStream_t st) {
-  auto fn = grouped_stream_kernel<MX4, WARPS>;
+  auto fn = grouped_stream_kernel<KIND, WARPS>;
   const int64_t most = static_cast<int64_t>(num_sms()) * resident_blocks(reinterpret_cast<const void*>(fn), 32 * WARPS);
   return launch_dependent_kernel(fn, dim3(static_cast<unsigned>(std::min(units, most))), dim3(32 * WARPS), 0, st, p);
 }
@@ -195,21 +296,20 @@ static cudaError_t gs_launch(const GsParams& p, int64_t units, cudaStream_t st) 
 // of an SM's warps without one: K = 4096 and N = 4096 for one expert 10.6 ->
 // 8.5 us (4 bits 9.0 -> 6.4), two experts with K = 2432, N = 768 6.6 -> 5.1;
 // with a tile for every four warps they are slower by 10 to 30%.
-template <bool MX4>
+template <GsKind KIND>
 static cudaError_t gs_choose(const GsParams& p, cudaStream_t st) {
   const int64_t units = most_chunks(p.g, kGsMost) * ((p.N + kGsRows - 1) / kGsRows);
   const bool wide = units <= 2 * num_sms();
-  return wide ? gs_launch<MX4, 8>(p, units, st) : gs_launch<MX4, 4>(p, units, st);
+  return wide ? gs_launch<KIND, 8>(p, units, st) : gs_launch<KIND, 4>(p, units, st);
 }
 
-cudaError_t launch_grouped_stream(const GroupedArgs& a, cudaStream_t st) {
-  return gs_choose<false>(GsParams{static_cast<const __nv_bfloat16*>(a.xs), static_cast<const uint8_t*>(a.w), nullptr,
-                                   static_cast<__nv_bfloat16*>(a.out), a.g, a.K, a.N}, st);
+cudaError_t launch_grouped_stream(int dtype, const GroupedArgs& a, cudaStream_t st) {
+  const GsParams p{a.xs, static_cast<const uint8_t*>(a.w), nullptr, a.out, a.g, a.K, a.N};
+  return dtype == kDtypeBF16 ? gs_choose<kGsBf16>(p, st) : gs_choose<kGsF32>(p, st);
 }
 cudaError_t launch_mx4_stream(const Mx4MatmulArgs& a, cudaStream_t st) {
-  return gs_choose<true>(GsParams{static_cast<const __nv_bfloat16*>(a.x), static_cast<const uint8_t*>(a.w),
-                                  reinterpret_cast<const uint32_t*>(a.w_exps), static_cast<__nv_bfloat16*>(a.out), a.g,
-                                  a.K, a.N}, st);
+  return gs_choose<kGsMx4>(GsParams{a.x, static_cast<const uint8_t*>(a.w), reinterpret_cast<const uint32_t*>(a.w_exps), a.out, a.g,
+                                    a.K, a.N}, st);
 }
 
 }  // namespace mm

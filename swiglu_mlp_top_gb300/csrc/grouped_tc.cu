@@ -460,28 +460,8 @@ __device__ __forceinline__ int row_kind(const GroupTables& g, int64_t r) {
 }
 
 // fp32 rows as three planes of bf16, [3, rows, pitch8(cols)]; rows that hold no
-// assignment as zeros.  *flag is set where a value has no such planes: an
-// infinity, a NaN, above 2^127 (h may round to infinity) or below 2^-100 but
-// not zero (l may fall below bf16's smallest).  A warp a row, the tensors' rows
-// one after the other.
-__device__ __forceinline__ void split_vector(const float (&x)[8], uint4 (&planes)[3], bool& bad) {
-  uint32_t p[3][4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float a = x[2 * j], b = x[2 * j + 1];
-    const float lo = fminf(fabsf(a) == 0.f ? 1.f : fabsf(a), fabsf(b) == 0.f ? 1.f : fabsf(b));
-    bad |= !(fabsf(a) < 0x1p127f) | !(fabsf(b) < 0x1p127f) | (lo < 0x1p-100f);
-#pragma unroll
-    for (int q = 0; q < 3; ++q) {
-      p[q][j] = pack_bf16x2(a, b);
-      a -= __uint_as_float(p[q][j] << 16);
-      b -= __uint_as_float(p[q][j] & 0xffff0000u);
-    }
-  }
-#pragma unroll
-  for (int q = 0; q < 3; ++q) planes[q] = make_uint4(p[q][0], p[q][1], p[q][2], p[q][3]);
-}
-
+// assignment as zeros.  *flag is set where a value has no such planes.  A warp
+// a row, the tensors' rows one after the other.
 __global__ void __launch_bounds__(256)
 split_kernel(const SplitTensors S, const GroupTables g, int* flag) {
   pdl_enter();

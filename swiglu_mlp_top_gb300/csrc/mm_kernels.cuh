@@ -542,7 +542,7 @@ cudaError_t launch_mx4_tc(const Mx4MatmulArgs& p, WsHeader* hdr, cudaStream_t st
 cudaError_t launch_mx4w_tc(const Mx4MatmulArgs& p, WsHeader* hdr, cudaStream_t st);
 
 // Few bf16 rows times bf16 or 4-bit weights (grouped_stream.cu).
-cudaError_t launch_grouped_stream(const GroupedArgs& p, cudaStream_t st);
+cudaError_t launch_grouped_stream(int dtype, const GroupedArgs& p, cudaStream_t st);
 cudaError_t launch_mx4_stream(const Mx4MatmulArgs& p, cudaStream_t st);    // x: bf16 [rows, K], x_exps null
 
 // 4-bit microscaled tensors (mx4.cu).
