@@ -10,6 +10,7 @@ must be ordered before the call by the caller.
 """
 from __future__ import annotations
 
+from functools import lru_cache
 from typing import Optional
 
 import torch
@@ -52,8 +53,15 @@ def _arg(t, name: str, dev: int, dtype, shape):
     return t.data_ptr()
 
 
+@lru_cache(maxsize=None)
+def _cuda(dev: int) -> torch.device:
+    return torch.device("cuda", dev)
+
+
 def _empty(shape, dtype, dev, stream):
     """A tensor of the call's own, from the pool of the stream that uses it."""
+    if type(dev) is int:
+        dev = _cuda(dev)                        # a device by its number costs 1 us more
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
