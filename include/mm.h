@@ -513,7 +513,8 @@ int mm_swiglu_act_backward(const void* codes, const uint8_t* exps, const void* d
  * or one below 2^-100 that is not zero, in a row that counts, the call (of few
  * rows: the results that it touches) is made on the CUDA cores instead, with
  * the same accuracy.  (On the tensor cores a sum within 2^-7 of the largest
- * number may become an infinity.)
+ * number may become an infinity, of its sign; one whose terms overflow to both
+ * sides is an infinity or a NaN.)
  * Outputs overlap neither inputs nor each other.  `status_ws` (nullable: no
  * report) is a zeroed workspace of >= 256 bytes read by mm_check_status(),
  * where a device wait that exceeded its time limit is recorded; `workspace`

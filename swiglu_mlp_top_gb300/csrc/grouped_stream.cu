@@ -17,8 +17,8 @@
 //
 // fp32 values are split into three bf16 parts in registers, of whose nine
 // products six are made (grouped_tc.cu); every 32 columns' sum is added in
-// fp32.  A block that meets a value without such parts makes its results with
-// multiply-adds.  (One token, E = 8, K = 1024, N = 2048: 6.7 us, 7.7 with
+// fp32.  A block that meets a value without such parts, or whose sums overflow,
+// makes its results with multiply-adds.  (One token, E = 8, K = 1024, N = 2048: 6.7 us, 7.7 with
 // multiply-adds alone; four rows, K = N = 2048: 9.6 against 31; from some 16
 // rows of an expert on, splitting and the six products bound it.)
 #include "grouped.cuh"
@@ -128,7 +128,7 @@ __device__ __forceinline__ void gs_sum(const GsParams& P, int64_t wrow, int wlas
   }
 }
 
-// The same in fp32.  Returns whether a value cannot be split.
+// The same in fp32.  Returns whether a value cannot be split or a sum has overflowed.
 template <int WARPS, int NT>
 __device__ __forceinline__ bool gs_sum_f32(const GsParams& P, int64_t wrow, int wlast, const float* x, int rows, float (&acc)[NT][4]) {
   constexpr int kUnroll = NT == 1 ? 3 : NT == 2 ? 2 : 1;
@@ -179,6 +179,11 @@ __device__ __forceinline__ bool gs_sum_f32(const GsParams& P, int64_t wrow, int 
       }
     }
   }
+  // products that overflow may do so to different sides, h h' and the small ones
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bad |= !(fabsf(acc[j][i]) < INFINITY);
   return bad;
 }
 

@@ -352,16 +352,25 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
           tc_fence_after();
           const uint32_t tb = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 256 + half * hc;
 #pragma unroll
-          for (int h = 0; h < (PLANES == 1 ? 1 : 2); ++h)
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              if (16 * c >= hc) break;
-              uint32_t r[16];
-              tmem_ld_32x32b_x16(tb + (PLANES == 1 ? 0 : 256 - 256 * h) + 16 * c, r);    // the small products first
+          for (int c = 0; c < 8; ++c) {
+            if (16 * c >= hc) break;
+            uint32_t r[16];
+            tmem_ld_32x32b_x16(tb + 16 * c, r);
+            if constexpr (PLANES == 3) {
+              // the small products first; where h h' has overflowed, they have too,
+              // maybe to the other side, and h h' alone says what the sum is
+              uint32_t small[16];
+              tmem_ld_32x32b_x16(tb + 256 + 16 * c, small);
               tmem_ld_wait();
 #pragma unroll
-              for (int q = 0; q < 16; ++q) sum[16 * c + q] += __uint_as_float(r[q]);
+              for (int q = 0; q < 16; ++q)
+                sum[16 * c + q] += fabsf(__uint_as_float(r[q])) < INFINITY ? __uint_as_float(small[q]) : 0.f;
+            } else {
+              tmem_ld_wait();
             }
+#pragma unroll
+            for (int q = 0; q < 16; ++q) sum[16 * c + q] += __uint_as_float(r[q]);
+          }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_signal_cluster(acc ? te1 : te0);
