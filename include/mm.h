@@ -515,12 +515,14 @@ int mm_swiglu_act_backward(const void* codes, const uint8_t* exps, const void* d
  * the same accuracy.  (On the tensor cores a sum within 2^-7 of the largest
  * number may become an infinity, of its sign; one whose terms overflow to both
  * sides is an infinity or a NaN.)
- * Outputs overlap neither inputs nor each other.  `status_ws` (nullable: no
- * report) is a zeroed workspace of >= 256 bytes read by mm_check_status(),
- * where a device wait that exceeded its time limit is recorded; `workspace`
- * is plain scratch (its header is not used, and what it holds before the call
- * does not matter), and may be NULL where the size is 0.  Sizes are those of
- * the current device.
+ * Outputs overlap neither inputs nor each other.  A device wait that exceeded
+ * its time limit is recorded in the header of `status_ws` (nullable; a zeroed
+ * workspace of >= 256 bytes) or, without one, of `workspace`, for
+ * mm_check_status(); with neither there is no report.  Nothing else in a
+ * workspace's header is read or written, so that other calls may share the
+ * workspace; what it holds behind the header before the call does not matter,
+ * and it may be NULL where the size is 0.  Sizes are those of the current
+ * device.
  * Limits: E <= MM_MAX_EXPERTS; K, N <= MM_GROUPED_MAX_DIM; rows <=
  * MM_GROUPED_MAX_ROWS.  rows = 0 enqueues nothing, but that dw is zeroed.
  * ---------------------------------------------------------------------- */

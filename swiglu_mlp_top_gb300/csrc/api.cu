@@ -1160,6 +1160,12 @@ static bool grouped_in_limits(int64_t rows, int K, int N, int E) {
   return E <= MM_MAX_EXPERTS && K <= MM_GROUPED_MAX_DIM && N <= MM_GROUPED_MAX_DIM && rows <= MM_GROUPED_MAX_ROWS;
 }
 static bool status_ok(const void* status_ws) { return aligned16(status_ws); }
+// Where a wait that gives up is recorded: in status_ws, else in the header of
+// the workspace, where the call has one.
+static WsHeader* status_header(void* status_ws, void* workspace, size_t workspace_bytes) {
+  if (status_ws != nullptr) return static_cast<WsHeader*>(status_ws);
+  return present16(workspace) && workspace_bytes >= sizeof(WsHeader) ? static_cast<WsHeader*>(workspace) : nullptr;
+}
 
 // Few rows, which start on 16 bytes, go to the kernel that streams the weights
 // (grouped_stream.cu).  Its time grows with the rows of an expert, the tiles'
@@ -1201,11 +1207,12 @@ static GroupedPlan grouped_plan(int64_t rows, int K, int N, int E, int dtype, bo
   if (L.planes == 0) return L;
   const GroupTables g{reinterpret_cast<const int32_t*>(E > 1 ? 4 : 0), nullptr, rows, E};   // the same bound for every table
   const int first = backward ? kGroupedDgrad : kGroupedForward, last = backward ? kGroupedWgrad : kGroupedForward;
-  size_t off = 0, parts = 0;
+  size_t off = sizeof(WsHeader), parts = 0;    // a workspace's header stays as it is
   auto copy = [&](size_t* at, int64_t r, int cols) {
     *at = off;
     if (L.planes == 3 || cols % 8) off += align_up(2 * static_cast<size_t>(L.planes) * r * pitch8(cols));
   };
+  L.flag = off;
   if (L.planes == 3) off += kAlign;
   copy(&L.xs, rows, K);
   if (backward) copy(&L.dys, rows, N);
@@ -1215,7 +1222,8 @@ static GroupedPlan grouped_plan(int64_t rows, int K, int N, int E, int dtype, bo
     parts = std::max(parts, grouped_parts_bytes(op, g, K, N, L.splits[op]));
   }
   L.parts = off;
-  L.total = off + align_up(parts);
+  off += align_up(parts);
+  L.total = off > sizeof(WsHeader) ? off : 0;
   return L;
 }
 static size_t grouped_bytes(int64_t rows, int K, int N, int E, int dtype, bool backward) {
@@ -1252,12 +1260,12 @@ static cudaError_t grouped_operands(const GroupedPlan& L, GroupedArgs& a, void* 
 // One operation on operands that grouped_operands() has made ready in `a`;
 // `given` has the caller's.
 static cudaError_t grouped_launch(const GroupedPlan& L, int dtype, int op, const GroupedArgs& a, const GroupedArgs& given,
-                                  void* ws, void* status_ws, cudaStream_t st) {
+                                  void* ws, WsHeader* hdr, cudaStream_t st) {
   if (L.planes == 0) return counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_grouped_simt(op, given, nullptr, st); });
   const int* flag = L.planes == 3 ? reinterpret_cast<const int*>(ws_at(ws, L.flag)) : nullptr;
   const GroupedTcExtras x{L.planes, L.splits[op], L.splits[op] > 1 ? ws_at(ws, L.parts) : nullptr, flag};
   cudaError_t e = counted_launch(MM_KERNEL_GROUPED, st, [&] {
-    return launch_grouped_tc(op, a, x, static_cast<WsHeader*>(status_ws), st);
+    return launch_grouped_tc(op, a, x, hdr, st);
   });
   if (e == cudaSuccess && x.splits > 1)
     e = counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_grouped_join(op, dtype, a, x, st); });
@@ -1289,7 +1297,7 @@ int mm_grouped_matmul(const void* xs, const void* w, const int32_t* offsets, con
     const GroupedPlan L = grouped_plan(rows, K, N, E, dtype, false);
     GroupedArgs a = given;
     e = grouped_operands(L, a, workspace, st);
-    if (e == cudaSuccess) e = grouped_launch(L, dtype, kGroupedForward, a, given, workspace, status_ws, st);
+    if (e == cudaSuccess) e = grouped_launch(L, dtype, kGroupedForward, a, given, workspace, status_header(status_ws, workspace, workspace_bytes), st);
   }
   return e == cudaSuccess ? MM_OK : cuda_fail(e, "grouped matmul");
 }
@@ -1321,11 +1329,12 @@ int mm_grouped_matmul_backward(const void* dys, const void* xs, const void* w,
   GroupedArgs a = given;
   if (dxs == nullptr) a.w = nullptr;
   if (dw == nullptr) a.xs = nullptr;
+  WsHeader* hdr = status_header(status_ws, workspace, workspace_bytes);
   cudaError_t e = grouped_operands(L, a, workspace, st);
-  if (e == cudaSuccess && dxs != nullptr) e = grouped_launch(L, dtype, kGroupedDgrad, a, given, workspace, status_ws, st);
+  if (e == cudaSuccess && dxs != nullptr) e = grouped_launch(L, dtype, kGroupedDgrad, a, given, workspace, hdr, st);
   if (e == cudaSuccess && dw != nullptr) {
     a.out = given.out = dw;
-    e = grouped_launch(L, dtype, kGroupedWgrad, a, given, workspace, status_ws, st);
+    e = grouped_launch(L, dtype, kGroupedWgrad, a, given, workspace, hdr, st);
   }
   return e == cudaSuccess ? MM_OK : cuda_fail(e, "grouped matmul backward");
 }
@@ -1368,7 +1377,7 @@ struct Mx4Layout {
   size_t w, x, total;         // x: rows that start on 16 bytes, or the scratch of the product
 };
 static Mx4Layout mx4_layout(int64_t rows, int K, int N, int E, bool four) {
-  Mx4Layout L{kMx4Cores, 0, 0, 0};
+  Mx4Layout L{kMx4Cores, sizeof(WsHeader), sizeof(WsHeader), 0};
   if (four) return L;
   const GroupedPlan P = grouped_plan(rows, K, N, E, kDtypeBF16, false);
   // The copy pays where two tiles of rows or more take each matrix, or where the
@@ -1378,10 +1387,10 @@ static Mx4Layout mx4_layout(int64_t rows, int K, int N, int E, bool four) {
   const bool copy = rows >= 512 * static_cast<int64_t>(E) || P.splits[kGroupedForward] > 1;
   L.path = grouped_streams(rows, K, E, kDtypeBF16, true) ? kMx4Stream : copy ? kMx4Copy : kMx4Convert;
   if (L.path == kMx4Copy) {
-    L.x = align_up(2 * static_cast<size_t>(E) * N * K);
+    L.x = L.w + align_up(2 * static_cast<size_t>(E) * N * K);
     L.total = L.x + grouped_bytes(rows, K, N, E, kDtypeBF16, false);
   } else if (L.path == kMx4Convert && K % 8) {
-    L.total = align_up(2 * static_cast<size_t>(rows) * pitch8(K));
+    L.total = L.x + align_up(2 * static_cast<size_t>(rows) * pitch8(K));
   }
   return L;
 }
@@ -1403,15 +1412,15 @@ int mm_mx4_matmul(const void* x, const uint8_t* x_exps, const void* w_codes, con
   const Mx4Layout L = mx4_layout(rows, K, N, E, x_exps != nullptr);
   if (L.total > 0 && (!present16(workspace) || workspace_bytes < L.total)) return MM_ERR_WORKSPACE;
   const GroupTables g{offsets, counts, rows, E};
+  WsHeader* hdr = status_header(status_ws, workspace, workspace_bytes);
   if (L.path == kMx4Copy) {
     const int rc = mx4_impl(false, nullptr, ws_at(workspace, L.w), const_cast<void*>(w_codes), const_cast<uint8_t*>(w_exps),
                             static_cast<int64_t>(E) * N, K, kDtypeBF16, nullptr, stream, g, N);
     if (rc != MM_OK) return rc;
     return mm_grouped_matmul(x, ws_at(workspace, L.w), offsets, counts, rows, K, N, E, kDtypeBF16, ys,
-                             ws_at(workspace, L.x), L.total - L.x, status_ws, stream);
+                             ws_at(workspace, L.x), L.total - L.x, hdr, stream);
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  WsHeader* hdr = static_cast<WsHeader*>(status_ws);
   Mx4MatmulArgs a{x, x_exps, w_codes, w_exps, ys, g, K, N};
   cudaError_t e = cudaSuccess;
   if (L.path == kMx4Convert && K % 8) {

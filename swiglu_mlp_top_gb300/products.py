@@ -4,8 +4,10 @@ marshalling only; the formulas and limits stand in include/mm.h.
 
 Tensors, devices and streams as in block_ops.py.  `plan` is what moe_permute
 returns (its offsets and counts); without one, all rows take one matrix.
-`status_workspace` (new_workspace(256)) is read by check_status() and holds
-what a device wait that gave up would report.
+check_status() of `workspace` or, where one is given, of `status_workspace`
+(new_workspace(256)) tells of a device wait that gave up; without either
+nothing does.  A `workspace` comes from new_workspace() and may be shared with
+other calls on its stream.
 """
 from __future__ import annotations
 

@@ -74,3 +74,58 @@ def test_fp32_overflow_stays_in_its_results(rows):
         assert torch.equal(y[keep], clean[keep])
     want, terms = ref.matmul(x, w, None, torch.zeros(rows, N))
     ref.close_sum(torch.where(keep, y, 0.0), torch.where(keep, want, 0.0), torch.where(keep, terms, 0.0), K, F32, "ys")
+
+
+# ------------------------------------------------------------ a shared workspace
+def calls_with_scratch(gen):
+    """Calls that use a workspace, by name: (call with keyword arguments, bytes)."""
+    E, K, N, T = 3, 65, 50, 400
+    plan = on_gpu(ref.tables([150, 0, 250]))
+    x, w, dy = (torch.randn(*s, generator=gen).cuda() for s in ((T, K), (E, N, K), (T, N)))
+    xb, wb, dyb = x.to(BF), w.to(BF), dy.to(BF)
+    wq, xl, wl = mm.mx4_quantize(wb), torch.randn(300, 4096, generator=gen).to(BF).cuda(), torch.randn(130, 4096, generator=gen).to(BF).cuda()
+    wlq = mm.mx4_quantize(wl)
+    fw, bw, mx = mm.grouped_matmul_workspace_bytes, mm.grouped_matmul_backward_workspace_bytes, mm.mx4_matmul_workspace_bytes
+    return {
+        "bf16": (lambda **kw: mm.grouped_matmul(xb, wb, plan, **kw), fw(T, K, N, E, BF)),
+        "fp32": (lambda **kw: mm.grouped_matmul(x, w, plan, **kw), fw(T, K, N, E, F32)),
+        "parts": (lambda **kw: mm.grouped_matmul(xl, wl, **kw), fw(300, 4096, 130, 1, BF)),
+        "bf16 backward": (lambda **kw: mm.grouped_matmul_backward(dyb, xb, wb, plan, **kw), bw(T, K, N, E, BF)),
+        "fp32 backward": (lambda **kw: mm.grouped_matmul_backward(dy, x, w, plan, **kw), bw(T, K, N, E, F32)),
+        "4-bit weights, converted": (lambda **kw: mm.mx4_matmul(xb, wq, plan, **kw), mx(T, K, N, E, False)),
+        "4-bit weights, copied": (lambda **kw: mm.mx4_matmul(xl, wlq, **kw), mx(300, 4096, 130, 1, False)),
+    }
+
+
+def tensors(out):
+    return [out] if isinstance(out, torch.Tensor) else [t for t in out if t is not None]
+
+
+def test_the_header_of_a_workspace_stays_as_it_is():
+    """Its 256 bytes hold other calls' state; anything may stand behind them."""
+    for name, (call, need) in calls_with_scratch(torch.Generator().manual_seed(21)).items():
+        assert need > 256, name
+        want = [t.clone() for t in tensors(call())]
+        for fill in (0, 255):
+            ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+            ws[:256] = torch.arange(256, dtype=torch.uint8, device="cuda")
+            got = tensors(call(workspace=ws))
+            assert torch.equal(ws[:256].cpu(), torch.arange(256, dtype=torch.uint8)), name
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+
+
+def test_one_workspace_for_a_model_and_its_products():
+    """The decode kernel of moe_forward keeps the counter of its grid barrier in the header."""
+    gen = torch.Generator().manual_seed(22)
+    T, H, I, E, k = 16, 256, 128, 4, 2
+    x, wr = torch.randn(T, H, generator=gen).to(BF).cuda(), (torch.randn(E, H, generator=gen) * 0.1).to(BF).cuda()
+    mats = lambda *s: [(torch.randn(*s, generator=gen) * 0.05).to(BF).cuda() for _ in range(E)]  # noqa: E731
+    Wg, Wu, Wd = mats(I, H), mats(I, H), mats(H, I)
+    calls = calls_with_scratch(gen)
+    want = mm.moe_forward(x, wr, Wg, Wu, Wd, k, coef=0.0)[0]
+    ws = mm.new_workspace(max(mm.moe_workspace_bytes(T, H, I, E, k, BF), *(need for _, need in calls.values())))
+    for name, (call, _) in calls.items():
+        call(workspace=ws)
+        assert mm.check_status(ws) == 0, name
+        y = mm.moe_forward(x, wr, Wg, Wu, Wd, k, coef=0.0, workspace=ws)[0]
+        assert mm.check_status(ws) == 0 and torch.equal(y, want), name
