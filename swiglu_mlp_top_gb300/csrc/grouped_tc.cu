@@ -25,7 +25,7 @@
 // the nearest bf16 of what the ones before leave, so that 24 bits are kept and
 // of the nine products the three below 2^-25 are left out.  h h' adds up in one
 // accumulator and the five smaller products in the other; both are added in
-// fp32 registers every 512 of the summed index.
+// fp32 registers every 256 of the summed index.
 //
 // Few tiles with a long sum are cut into `splits` parts of the sum, each an
 // fp32 tile of its own in the workspace, and join_kernel adds them in order.
@@ -44,10 +44,13 @@ constexpr int kGmSmem = kGmRing * 2 * kGmTile + kGmEpiWarps * kGmStage + 1024 + 
 static_assert(kGmSmem + sizeof(GmTables) + 64 <= 232448, "shared memory budget");
 
 // Slices of the summed index per accumulation in TMEM.  The tensor cores cut
-// off where they add to the accumulator; results in fp32 add chunks of 512 in
-// fp32 registers: a weight gradient over 512 rows is 2.3e-7 off, relative to
-// its root mean square, one over 9500 rows 4.1e-7.
-template <bool F32> constexpr int kGmChunk = F32 ? 8 : 1 << 30;
+// off where they add to the accumulator; results in fp32 add chunks of 256 in
+// fp32 registers.  Relative to their root mean square, results over 2048 and
+// more are 2.4e-7 off (3.2e-7 where all terms have one sign), with chunks of 512
+// 4.8e-7 (7.1e-7), with 128 1.4e-7 (1.5e-7).  fp32 products, which have one pair of accumulators, take
+// 3 to 5% more time than with 512 and 128 takes 8 to 10% more again; weight gradients of bf16 rows, which have two
+// by turns, as long as with 512, with 128 12% longer (T = 16384, 2432 -> 768).
+template <bool F32> constexpr int kGmChunk = F32 ? 4 : 1 << 30;
 
 struct GmParams {
   CUtensorMap a, b, out;

@@ -129,3 +129,32 @@ def test_one_workspace_for_a_model_and_its_products():
         assert mm.check_status(ws) == 0, name
         y = mm.moe_forward(x, wr, Wg, Wu, Wd, k, coef=0.0, workspace=ws)[0]
         assert mm.check_status(ws) == 0 and torch.equal(y, want), name
+
+
+# ------------------------------------------------------------- how exact fp32 is
+def off(got, want):
+    """Root mean square of the error, relative to the result's."""
+    return float((got.double() - want).norm() / want.norm())
+
+
+@pytest.mark.parametrize("signs", [True, False])
+@pytest.mark.parametrize("rows,K", [(32, 2048), (5, 2049), (400, 96), (400, 768), (400, 4096), (4096, 2048), (4096, 8192)])
+def test_fp32_results_are_as_exact_as_fp32(rows, K, signs):
+    """Sums of K products, streamed, in tiles and in parts, in every direction.
+
+    An accumulator of the tensor cores takes at most 16 additions (256 summed
+    columns), each of which cuts off half a step of 2^-23 on the mean, on a
+    partial sum that is half the chunk's on the mean where all terms have one
+    sign: 4 * 2^-23 of the chunk, which is the largest of the cases.  Adding the
+    chunks rounds K / 256 + 1 times, each time off by 2^-25 in the root mean
+    square at most, independent of one another."""
+    bound = 4 * 2.0 ** -23 + (K / 256 + 1) ** 0.5 * 2.0 ** -25
+    gen = torch.Generator(device="cuda").manual_seed(rows + K)
+    make = torch.randn if signs else torch.rand
+    a, b, c = (make(*s, generator=gen, device="cuda") for s in ((rows, K), (256, K), (K, 256)))
+    assert off(mm.grouped_matmul(a, b), a.double() @ b.double().T) <= bound
+    assert off(mm.grouped_matmul_backward(a, None, c)[0], a.double() @ c.double()) <= bound
+    d, e = make(K, 320, generator=gen, device="cuda"), c
+    for dtype in (F32, BF):
+        d, e = d.to(dtype), e.to(dtype)
+        assert off(mm.grouped_matmul_backward(d, e, None)[1], d.double().T @ e.double()) <= bound
