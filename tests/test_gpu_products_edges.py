@@ -158,3 +158,68 @@ def test_fp32_results_are_as_exact_as_fp32(rows, K, signs):
     for dtype in (F32, BF):
         d, e = d.to(dtype), e.to(dtype)
         assert off(mm.grouped_matmul_backward(d, e, None)[1], d.double().T @ e.double()) <= bound
+
+
+# Products of one term a sum are exact, whatever the parts that the term is made
+# of: each of the six products of parts that are made shows in the result's bits.
+KINDS = {
+    # the dense factor's values, the others': all three parts times one, one times all three, two times two
+    "24 x 1": ((2 ** 23, 2 ** 24), None), "1 x 24": (None, (2 ** 23, 2 ** 24)), "12 x 12": ((2 ** 11, 2 ** 12), (2 ** 11, 2 ** 12))}
+
+
+def numbers(between, gen, *shape):
+    """Odd whole numbers of so many bits, or powers of two, of either sign."""
+    sign = 1 - 2 * torch.randint(0, 2, shape, generator=gen)
+    if between is None:
+        return (sign * torch.exp2(torch.randint(-8, 9, shape, generator=gen).float())).float()
+    return (sign * (torch.randint(*between, shape, generator=gen) | 1)).float()
+
+
+def one_each(m, axis, spans, gen):
+    """m with one value along `axis` kept in each of the spans, zeros elsewhere (the spans split the rows)."""
+    out = torch.zeros_like(m)
+    for a, b in spans:
+        if b > a:
+            part, n = m[a:b], m[a:b].shape[axis]
+            at = torch.randint(0, n, (part.shape[1 - axis],), generator=gen).unsqueeze(axis)
+            out[a:b].scatter_(axis, at, part.gather(axis, at))
+    return out
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("counts,K,N", [
+    (None, 264, 200), ([9, 0, 17], 2432, 72), (None, 97, 40),                      # few rows
+    ([300, 0, 257], 768, 264), ([300, 0, 257], 515, 130), ([70, 3, 200], 65, 33),  # tiles, also with copies of rows
+    ([40, 600], 96, 2050), ([300], 4096, 130), ([3000], 72, 60)])                  # sums in parts
+def test_fp32_products_use_every_part(counts, K, N, kind):
+    left, right = KINDS[kind]
+    gen = torch.Generator().manual_seed(K + N)
+    plan = None if counts is None else ref.tables(counts, 4)
+    R, E = (20, 1) if plan is None else (int(plan["offsets"][-1]), len(counts))
+    gplan = on_gpu(plan)
+    rows = [(a, b) for _, a, b, _ in ref.spans(plan, R)]
+
+    def weights(between, axis=None):
+        w = numbers(between, gen, E * N, K)
+        if axis is not None:
+            w = one_each(w, axis, [(e * N, (e + 1) * N) for e in range(E)], gen)
+        return w.view(E, N, K) if plan is not None else w
+
+    def same(got, want):
+        assert torch.equal(got.cpu().double(), want)
+
+    zeros = lambda width: torch.zeros(R, width)  # noqa: E731
+    for dense_first in (True, False):            # which factor is dense
+        lo, hi = (left, right) if dense_first else (right, left)
+        x, dy = numbers(lo, gen, R, K), numbers(lo, gen, R, N)
+        w, v = (weights(hi, 1), weights(hi, 0)) if dense_first else (weights(hi), weights(hi))
+        if not dense_first:
+            x, dy = one_each(x, 1, [(0, R)], gen), one_each(dy, 1, [(0, R)], gen)
+        same(mm.grouped_matmul(x.cuda(), w.cuda(), gplan), ref.matmul(x, w, plan, zeros(N))[0])
+        same(mm.grouped_matmul_backward(dy.cuda(), None, v.cuda(), gplan)[0], ref.matmul(dy, v.transpose(-1, -2), plan, zeros(K))[0])
+        x, dy = numbers(lo, gen, R, K), numbers(hi, gen, R, N)
+        if dense_first:
+            dy = one_each(dy, 0, rows, gen)      # one row of dy and all of x, or the other way round
+        else:
+            x = one_each(x, 0, rows, gen)
+        same(mm.grouped_matmul_backward(dy.cuda(), x.cuda(), None, gplan)[1], ref.matmul_backward(dy, x, torch.zeros_like(v), plan, zeros(K))[1][0])
