@@ -279,7 +279,7 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
           const bool first = (kb - k0) % kGmChunk<F32> == 0;
           if (first) {
             acc = used % kAccs;
-            ok = warp_wait(&tempty[acc], ((used / kAccs) & 1) ^ 1, abort, hdr, 113);
+            ok = warp_wait<true>(&tempty[acc], ((used / kAccs) & 1) ^ 1, abort, hdr, 113);
             if (!ok) break;
             ++used;
             tc_fence_after();

@@ -498,13 +498,21 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
-// The same for a signal that no generic read of the other CTA relies on (an
-// accumulator has been read, after tcgen05.wait::ld and the fence before a
-// thread sync; a stage of this CTA's own shared memory is ready for its tensor
-// core, after a proxy fence): a release over the cluster waits for this
-// thread's earlier writes, 2000 cycles behind an epilogue's stores.
+// The same without a release: for an arrival that hands on nothing that was
+// written (it counts, or it says that an accumulator has been read, behind
+// tcgen05.wait::ld and the tcgen05 fence before a thread sync, which order that).
+// (A release over the cluster takes 1900 cycles, even of a warp that has
+// written nothing.)
 __device__ __forceinline__ void mbar_signal_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// The same with a release, over the cluster, of what was written to this CTA's
+// own shared memory alone (where its tensor core reads it, behind a proxy
+// fence): all that a stage written by warps hands on, and without the wait for
+// writes to global memory.
+__device__ __forceinline__ void mbar_release_smem_cluster(uint32_t cluster_addr) {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+  mbar_signal_cluster(cluster_addr);
 }
 // 2-D tiled TMA load into this CTA's shared memory whose completion is
 // signalled on an mbarrier that may live in the peer CTA of the pair.

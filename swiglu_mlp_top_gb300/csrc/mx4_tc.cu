@@ -180,10 +180,9 @@ mx4_tc_kernel(const __grid_constant__ MtParams P, WsHeader* hdr) {
       __syncwarp();
       if (lane == 0) {
         if (rank == 0) mbar_arrive(&full[s]);
-        // the fences have put the words where this SM's tensor core reads them;
-        // a release over the cluster would keep the lane from its next stage
-        // (dense 8192 x 4096 x 8192: 119 us, 86 without)
-        else mbar_signal_cluster(mapa_shared(smem_u32(&full[s]), 0));
+        // a release of all writes would keep the lane from its next stage (dense
+        // 8192 x 4096 x 8192: 119 us, 86 without)
+        else mbar_release_smem_cluster(mapa_shared(smem_u32(&full[s]), 0));
       }
     }
     __syncwarp();
@@ -201,7 +200,7 @@ mx4_tc_kernel(const __grid_constant__ MtParams P, WsHeader* hdr) {
       uint32_t ph = 0, sc = base + kMtScales;
       bool ok = true;
       for (int tile = cluster; ok && tile < tiles; tile += nc, ++used) {
-        ok = warp_wait(&tempty[used & 1], ((used >> 1) & 1) ^ 1, abort, hdr, 124);
+        ok = warp_wait<true>(&tempty[used & 1], ((used >> 1) & 1) ^ 1, abort, hdr, 124);
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = base + (used & 1) * kMtMaxN;
@@ -482,7 +481,7 @@ mx4w_tc_kernel(const __grid_constant__ MwParams P, WsHeader* hdr) {
       __syncwarp();
       if (lane == 0) {
         if (rank == 0) mbar_arrive(&full[s]);
-        else mbar_signal_cluster(mapa_shared(smem_u32(&full[s]), 0));
+        else mbar_release_smem_cluster(mapa_shared(smem_u32(&full[s]), 0));
       }
       return true;
     };
@@ -511,7 +510,7 @@ mx4w_tc_kernel(const __grid_constant__ MwParams P, WsHeader* hdr) {
       uint32_t ph = 0;
       bool ok = true;
       for (int tile = cluster; ok && tile < tiles; tile += nc, ++used) {
-        ok = warp_wait(&tempty[used & 1], ((used >> 1) & 1) ^ 1, abort, hdr, 134);
+        ok = warp_wait<true>(&tempty[used & 1], ((used >> 1) & 1) ^ 1, abort, hdr, 134);
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = base + (used & 1) * 256;
