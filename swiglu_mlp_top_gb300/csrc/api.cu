@@ -1196,7 +1196,7 @@ struct GroupedPlan {
 // to the tensor cores: T = 1000, E = 4, K = 768, N = 2432 148 -> 50 us, 8000
 // rows, E = 8 634 -> 163; 64 rows, E = 8 equal.
 static bool f32_on_tensor_cores(int64_t rows, int E, bool backward) {
-  return (backward || rows > f32_stream_rows(E)) && rows <= int64_t{1} << 29;       // three planes of rows are counted in 32 bits
+  return (backward || rows > f32_few_rows(E)) && rows <= int64_t{1} << 29;       // three planes of rows are counted in 32 bits
 }
 
 static GroupedPlan grouped_plan(int64_t rows, int K, int N, int E, int dtype, bool backward) {

@@ -269,7 +269,9 @@ cudaError_t launch_grouped_simt(int op, const GroupedArgs& p, const int* only_if
   const bool k4 = p.K % 4 == 0, kn4 = k4 && p.N % 4 == 0;
   if (op == kGroupedWgrad) return simt<kGroupedWgrad>(p.dys, p.xs, p.out, p.g, p.N, p.K, 0, kn4, only_if, st);
   if (op == kGroupedDgrad) return simt<kGroupedDgrad>(p.dys, p.w, p.out, p.g, 0, p.K, p.N, kn4, only_if, st);
-  if (p.g.rows > f32_stream_rows(p.g.E)) return simt<kGroupedForward>(p.xs, p.w, p.out, p.g, 0, p.N, p.K, k4, only_if, st);
+  // the few rows' kernel knows no only_if
+  if (only_if != nullptr || p.g.rows > f32_few_rows(p.g.E))
+    return simt<kGroupedForward>(p.xs, p.w, p.out, p.g, 0, p.N, p.K, k4, only_if, st);
   const int64_t units = most_chunks(p.g, kSimtFewX) * ((p.N + kSimtFewW - 1) / kSimtFewW);
   auto fn = k4 ? grouped_simt_few_kernel<4> : grouped_simt_few_kernel<1>;
   const int64_t most = static_cast<int64_t>(num_sms()) * resident_blocks(reinterpret_cast<const void*>(fn), 128);

@@ -489,8 +489,9 @@ struct GroupedArgs {
   int K, N;
 };
 // fp32 multiply-adds (grouped_simt.cu); only_if not null: nothing is done where
-// it holds 0 (not for the forward pass of up to f32_stream_rows).
-constexpr int f32_stream_rows(int E) { return 16 + 4 * E; }
+// it holds 0.  Without it, a forward pass of up to f32_few_rows is made by warps
+// instead of tiles.
+constexpr int f32_few_rows(int E) { return 16 + 4 * E; }
 cudaError_t launch_grouped_simt(int op, const GroupedArgs& p, const int* only_if, cudaStream_t st);
 
 // On the tensor cores (grouped_tc.cu): bf16 operands (planes 1), or fp32 ones
