@@ -330,9 +330,10 @@ mx4_tc_kernel(const __grid_constant__ MtParams P, WsHeader* hdr) {
 // codes instead of loaded.  Six warps take a stage each in turn: a lane loads
 // the 32 bytes of codes and the scale word of four rows (one stage ahead of the
 // one that it converts), multiplies (mx4.cuh, 19 instructions for 8 values) and
-// stores 16 bytes at a time where the swizzled TMA layout has them.  Reads each
-// needed weight once in 4 bits: with a bf16 copy of the weights first (and no
-// copy of x) T = 256, E = 8, K = 768, N = 4864 took 28 us.
+// stores 16 bytes at a time where the swizzled TMA layout has them.  The
+// weights are read and converted in 4 bits for each tile of 256 rows that needs
+// them, once where an expert has no more rows; with a bf16 copy of the weights
+// first (and no copy of x) T = 256, E = 8, K = 768, N = 4864 took 28 us.
 constexpr int kMwRing = 6, kMwTile = 128 * 64 * 2;
 constexpr int kMwWarpConvert = kMtEpiWarps + 2, kMwConverters = 6;
 static_assert(kMwConverters <= kMwRing, "a stage has one warp at a time: a wait tells two neighbouring phases apart");
