@@ -508,13 +508,11 @@ int mm_swiglu_act_backward(const void* codes, const uint8_t* exps, const void* d
  * stands in padding rows and behind in inputs (NaN too) has no effect.
  * Sums in fp32 in a fixed order (deterministic), one rounding per element.
  * fp32 operands are multiplied on the tensor cores as three bf16 parts each,
- * which hold all 24 bits (six of the nine products; the others are below
- * 2^-25).  Where operands hold an infinity, a NaN, a magnitude of 2^127 or more
- * or one below 2^-100 that is not zero, in a row that counts, the call (of few
+ * which hold all 24 bits of every number (six of the nine products; the others
+ * are below 2^-25).  Where operands hold an infinity, a NaN or a magnitude of
+ * 2^103 or more in a row that counts, or sums reach 2^80, the operation (of few
  * rows: the results that it touches) is made on the CUDA cores instead, with
- * the same accuracy.  (On the tensor cores a sum within 2^-7 of the largest
- * number may become an infinity, of its sign; one whose terms overflow to both
- * sides is an infinity or a NaN.)
+ * the same accuracy, in four to nine times the time.
  * Outputs overlap neither inputs nor each other.  A device wait that exceeded
  * its time limit is recorded in the header of `status_ws` (nullable; a zeroed
  * workspace of >= 256 bytes) or, without one, of `workspace`, for

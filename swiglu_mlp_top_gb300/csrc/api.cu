@@ -1193,7 +1193,7 @@ static bool grouped_streams(int64_t rows, int K, int E, int dtype, bool w_in_4_b
 struct GroupedPlan {
   int planes;                 // 0: no tensor cores; 1: bf16; 3: fp32 as planes of bf16
   int splits[3];              // parts of the sums, by operation
-  size_t flag;                // planes 3: the word that turns the call over to the CUDA cores
+  size_t flag;                // planes 3: words that turn the call, or an operation of it, over to the CUDA cores
   size_t xs, dys, w;          // copies: rows that start on 16 bytes, or planes
   size_t parts;               // one set, for the operations one after the other
   size_t total;
@@ -1259,7 +1259,7 @@ static cudaError_t grouped_operands(const GroupedPlan& L, GroupedArgs& a, void* 
   }
   if (t.n == 0) return cudaSuccess;
   int* flag = reinterpret_cast<int*>(ws_at(ws, L.flag));
-  const cudaError_t e = cudaMemsetAsync(flag, 0, sizeof(int), st);
+  const cudaError_t e = cudaMemsetAsync(flag, 0, 4 * sizeof(int), st);
   if (e != cudaSuccess) return e;
   return counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_grouped_split(t, a.g, flag, st); });
 }
@@ -1269,8 +1269,8 @@ static cudaError_t grouped_operands(const GroupedPlan& L, GroupedArgs& a, void* 
 static cudaError_t grouped_launch(const GroupedPlan& L, int dtype, int op, const GroupedArgs& a, const GroupedArgs& given,
                                   void* ws, WsHeader* hdr, cudaStream_t st) {
   if (L.planes == 0) return counted_launch(MM_KERNEL_GROUPED, st, [&] { return launch_grouped_simt(op, given, nullptr, st); });
-  const int* flag = L.planes == 3 ? reinterpret_cast<const int*>(ws_at(ws, L.flag)) : nullptr;
-  const GroupedTcExtras x{L.planes, L.splits[op], L.splits[op] > 1 ? ws_at(ws, L.parts) : nullptr, flag};
+  int* flag = L.planes == 3 ? reinterpret_cast<int*>(ws_at(ws, L.flag)) : nullptr;
+  const GroupedTcExtras x{L.planes, L.splits[op], L.splits[op] > 1 ? ws_at(ws, L.parts) : nullptr, flag, flag ? flag + 1 + op : nullptr};
   cudaError_t e = counted_launch(MM_KERNEL_GROUPED, st, [&] {
     return launch_grouped_tc(op, a, x, hdr, st);
   });

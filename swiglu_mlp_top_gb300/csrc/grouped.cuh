@@ -202,17 +202,22 @@ __device__ __forceinline__ int gm_index(int j, int c, int nc) {
   return j * nc + c;
 }
 
-// Eight fp32 values as three bf16 parts, each the nearest of what the ones
-// before leave.  bad: a value has no such parts, being an infinity, a NaN, above
-// 2^127 (the first may round to infinity) or below 2^-100 but not zero (the
-// last may fall below bf16's smallest).
-__device__ __forceinline__ void split_vector(const float (&x)[8], uint4 (&planes)[3], bool& bad) {
+// Eight fp32 values times 2^24 as three bf16 parts, each the nearest of what the
+// ones before leave.  fp32 numbers are whole multiples of 2^-149, so that the
+// scaled ones' parts are multiples of 2^-125, and what is left of 24 bits behind
+// two parts has eight: nothing is lost, however small a value is.  Products come
+// out times 2^48 (kSplitUnscale takes that away).  Values from kSplitMost on (of
+// which the first part may round to infinity), infinities and NaN have no such
+// parts; one of their parts is not finite then, and no sum with it is.
+constexpr float kSplitScale = 0x1p24f, kSplitUnscale = 0x1p-48f, kSplitMost = 0x1p103f;
+
+__device__ __forceinline__ void split_vector(const float (&x)[8], uint4 (&planes)[3]) {
   uint32_t p[3][4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    float a = x[2 * j], b = x[2 * j + 1];
-    const float lo = fminf(fabsf(a) == 0.f ? 1.f : fabsf(a), fabsf(b) == 0.f ? 1.f : fabsf(b));
-    bad |= !(fabsf(a) < 0x1p127f) | !(fabsf(b) < 0x1p127f) | (lo < 0x1p-100f);
+    // rounded by name, or the compiler subtracts the first part in one operation
+    // with the scaling and keeps both values (60 rows, E = 8, K = N = 2048: 65 us, 45)
+    float a = __fmul_rn(x[2 * j], kSplitScale), b = __fmul_rn(x[2 * j + 1], kSplitScale);
 #pragma unroll
     for (int q = 0; q < 3; ++q) {
       p[q][j] = pack_bf16x2(a, b);

@@ -1,8 +1,9 @@
 // Experts' products of fp32 rows on the CUDA cores with fp32 multiply-adds: few
 // rows of a forward pass with a width that is no multiple of 8 (others:
 // grouped_stream.cu), and the calls whose values cannot be split into
-// three bf16 parts for the tensor cores (grouped_tc.cu), told by a flag on the
-// device that the tile kernel returns on.  The tiles are bound by the
+// three bf16 parts for the tensor cores (grouped_tc.cu), or whose results are
+// too large for that, told by flags on the device without which the tile kernel
+// returns.  The tiles are bound by the
 // multiply-adds (T = 1000, E = 4, K = 768, N = 2432: 148 us, of which 52 at 72
 // Tflop/s; the tensor cores take 50).
 //
@@ -82,7 +83,7 @@ grouped_simt_kernel(const float* __restrict__ a, const float* __restrict__ b, fl
   constexpr int kPitchA = SliceA::kPitch, kPitchB = SliceB::kPitch;
   __shared__ __align__(16) float sA[2][kSimtK * kPitchA], sB[2][kSimtK * kPitchB];
   pdl_enter();
-  if (only_if != nullptr && *only_if == 0) return;
+  if (only_if != nullptr && only_if[0] == 0 && only_if[1 + OP] == 0) return;
   const int cols = (N + kSimtN - 1) / kSimtN;
   // this block's tile: rows [m0, mend) of A of which those below mval count, columns from n0
   int m0, mend, mval, n0, k0 = 0, kend = K;

@@ -17,10 +17,11 @@
 //
 // fp32 values are split into three bf16 parts in registers, of whose nine
 // products six are made (grouped_tc.cu); every 32 columns' sum is added in
-// fp32.  A block that meets a value without such parts, or whose sums overflow,
-// makes its results with multiply-adds.  (One token, E = 8, K = 1024, N = 2048: 6.7 us, 7.7 with
-// multiply-adds alone; four rows, K = N = 2048: 9.6 against 31; from some 16
-// rows of an expert on, splitting and the six products bound it.)
+// fp32.  A block whose sums are not finite (a value without such parts, or a sum
+// of 2^80 and more) makes its results with multiply-adds.  (Four rows of one
+// matrix, K = N = 2048: 8.6 us, 31 with multiply-adds alone.  From some 16 rows of
+// an expert on, splitting bounds it: with a test of each value in it, a quarter
+// of its instructions, 60 rows at E = 8 took 59 us for 45.)
 #include "grouped.cuh"
 #include "mx4.cuh"
 
@@ -128,7 +129,7 @@ __device__ __forceinline__ void gs_sum(const GsParams& P, int64_t wrow, int wlas
   }
 }
 
-// The same in fp32.  Returns whether a value cannot be split or a sum has overflowed.
+// The same in fp32.  Returns whether a sum is not finite: a value has no parts, or the sum is too large.
 template <int WARPS, int NT>
 __device__ __forceinline__ bool gs_sum_f32(const GsParams& P, int64_t wrow, int wlast, const float* x, int rows, float (&acc)[NT][4]) {
   constexpr int kUnroll = NT == 1 ? 3 : NT == 2 ? 2 : 1;
@@ -137,7 +138,6 @@ __device__ __forceinline__ bool gs_sum_f32(const GsParams& P, int64_t wrow, int 
   const int steps = (P.K + 31) / 32;
   const float* w = reinterpret_cast<const float*>(P.w);
   const float *w0 = w + (wrow + min(g, wlast)) * P.K, *w1 = w + (wrow + min(g + 8, wlast)) * P.K;
-  bool bad = false;
   auto load = [](float (&v)[8], const float* p, bool in) {
     const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
     const float4 a = in ? __ldg(reinterpret_cast<const float4*>(p)) : zero, b = in ? __ldg(reinterpret_cast<const float4*>(p) + 1) : zero;
@@ -159,12 +159,12 @@ __device__ __forceinline__ bool gs_sum_f32(const GsParams& P, int64_t wrow, int 
     for (int u = 0; u < kUnroll; ++u) {
       if (s0 + u * WARPS >= steps) break;                    // warp-uniform
       uint4 v0[3], v1[3];
-      split_vector(a[u][0], v0, bad);
-      split_vector(a[u][1], v1, bad);
+      split_vector(a[u][0], v0);
+      split_vector(a[u][1], v1);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         uint4 y[3];
-        split_vector(b[u][j], y, bad);
+        split_vector(b[u][j], y);
         // the small products first
         constexpr int kPa[6] = {2, 0, 1, 1, 0, 0}, kPb[6] = {0, 2, 1, 0, 1, 0};
         float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -179,11 +179,14 @@ __device__ __forceinline__ bool gs_sum_f32(const GsParams& P, int64_t wrow, int 
       }
     }
   }
-  // products that overflow may do so to different sides, h h' and the small ones
+  bool bad = false;
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) bad |= !(fabsf(acc[j][i]) < INFINITY);
+    for (int i = 0; i < 4; ++i) {
+      bad |= !(fabsf(acc[j][i]) < INFINITY);
+      acc[j][i] *= kSplitUnscale;
+    }
   return bad;
 }
 

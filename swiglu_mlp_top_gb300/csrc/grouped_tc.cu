@@ -21,11 +21,13 @@
 // producer warp writes zeros over the rows behind the group, in both operands,
 // and hands the slice on.
 //
-// fp32 operands come as three bf16 planes (split_kernel): x = h + m + l, each
-// the nearest bf16 of what the ones before leave, so that 24 bits are kept and
-// of the nine products the three below 2^-25 are left out.  h h' adds up in one
-// accumulator and the five smaller products in the other; both are added in
-// fp32 registers every 256 of the summed index.
+// fp32 operands come as three bf16 planes (split_kernel): 2^24 x = h + m + l, each
+// the nearest bf16 of what the ones before leave, so that 24 bits are kept, of
+// the smallest numbers too; of the nine products the three below 2^-25 are left
+// out.  h h' adds up in one accumulator and the five smaller products in the
+// other; both are added in fp32 registers every 256 of the summed index, and the
+// result is scaled back by 2^-48.  What is not finite on the way (large operands,
+// sums of 2^80 and more) sets a flag, and the CUDA cores do the operation.
 //
 // Few tiles with a long sum are cut into `splits` parts of the sum, each an
 // fp32 tile of its own in the workspace, and join_kernel adds them in order.
@@ -67,6 +69,7 @@ struct GmParams {
   void* outp;
   int64_t ldo;        // elements from one row of the result to the next
   const int* skip;    // not null: nothing is done where it holds something
+  int* over;          // not null: set where a result is not finite
 };
 
 // OP, PLANES: 1 (bf16) or 3 (fp32).  F32: the result, or its parts, in fp32.
@@ -355,30 +358,30 @@ grouped_tc_kernel(const __grid_constant__ GmParams P, WsHeader* hdr) {
           tc_fence_after();
           const uint32_t tb = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 256 + half * hc;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            if (16 * c >= hc) break;
-            uint32_t r[16];
-            tmem_ld_32x32b_x16(tb + 16 * c, r);
-            if constexpr (PLANES == 3) {
-              // the small products first; where h h' has overflowed, they have too,
-              // maybe to the other side, and h h' alone says what the sum is
-              uint32_t small[16];
-              tmem_ld_32x32b_x16(tb + 256 + 16 * c, small);
+          for (int h = 0; h < (PLANES == 1 ? 1 : 2); ++h)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              if (16 * c >= hc) break;
+              uint32_t r[16];
+              tmem_ld_32x32b_x16(tb + (PLANES == 1 ? 0 : 256 - 256 * h) + 16 * c, r);    // the small products first
               tmem_ld_wait();
 #pragma unroll
-              for (int q = 0; q < 16; ++q)
-                sum[16 * c + q] += fabsf(__uint_as_float(r[q])) < INFINITY ? __uint_as_float(small[q]) : 0.f;
-            } else {
-              tmem_ld_wait();
+              for (int q = 0; q < 16; ++q) sum[16 * c + q] += __uint_as_float(r[q]);
             }
-#pragma unroll
-            for (int q = 0; q < 16; ++q) sum[16 * c + q] += __uint_as_float(r[q]);
-          }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_signal_cluster(acc ? te1 : te0);
         }
         if (!ok) break;
+        if (PLANES == 3 && P.splits == 1) {
+          bool over = false;
+#pragma unroll
+          for (int c = 0; c < 128; ++c) {
+            over |= !(fabsf(sum[c]) < INFINITY);
+            sum[c] *= kSplitUnscale;
+          }
+          if (over && counts) *P.over = 1;
+        }
         const int sp = tile % P.splits;
         const int64_t orow = kWgrad ? (static_cast<int64_t>(ti.e) + static_cast<int64_t>(sp) * P.out_plane) * P.M + row
                                     : row + static_cast<int64_t>(sp) * P.out_plane;
@@ -471,7 +474,7 @@ __device__ __forceinline__ int row_kind(const GroupTables& g, int64_t r) {
   return valid ? 1 : pad ? 0 : -1;
 }
 
-// fp32 rows as three planes of bf16, [3, rows, pitch8(cols)]; rows that hold no
+// fp32 rows times 2^24 as three planes of bf16, [3, rows, pitch8(cols)]; rows that hold no
 // assignment as zeros.  *flag is set where a value has no such planes.  A warp
 // a row, the tensors' rows one after the other.
 __global__ void __launch_bounds__(256)
@@ -507,7 +510,9 @@ split_kernel(const SplitTensors S, const GroupTables g, int* flag) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint4 p[3];
-      split_vector(x[h], p, bad);
+      split_vector(x[h], p);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) bad |= !(fabsf(x[h][e]) < kSplitMost);
       if (v0 + 32 * h < per)
 #pragma unroll
         for (int q = 0; q < 3; ++q) dst[q * T.rows * per + v0 + 32 * h] = p[q];
@@ -516,12 +521,13 @@ split_kernel(const SplitTensors S, const GroupTables g, int* flag) {
   if (bad) *flag = 1;
 }
 
-// out[r, c] = the sum over the parts, in order, in T; padding rows zero, rows
-// outside the groups left alone.  A warp a row.
+// out[r, c] = the sum over the parts, in order, times `scale`, in T; padding rows
+// zero, rows outside the groups left alone; *over (or null) is set where a sum is
+// not finite.  A warp a row.
 template <typename T>
 __global__ void __launch_bounds__(256)
 join_kernel(const float* __restrict__ parts, T* __restrict__ out, const GroupTables g, const int64_t rows, const int cols,
-            const int pitch, const int splits, const int* skip) {
+            const int pitch, const int splits, const float scale, const int* skip, int* over) {
   pdl_enter();
   const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (r >= rows || (skip != nullptr && *skip != 0)) return;
@@ -536,10 +542,15 @@ join_kernel(const float* __restrict__ parts, T* __restrict__ out, const GroupTab
         sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
       }
     T* o = out + r * cols + c;
-    const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+    float v[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (over != nullptr && c + i < cols && !(fabsf(v[i]) < INFINITY)) *over = 1;
+      v[i] *= scale;
+    }
     if (vec) {
       if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-      else *reinterpret_cast<float4*>(o) = sum;
+      else *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -710,6 +721,7 @@ static cudaError_t gm_run(int op, const GroupedArgs& a, const GroupedTcExtras& x
   p.K = fwd ? a.K : a.N;
   p.splits = x.splits;
   p.skip = x.skip;
+  p.over = x.over;
   p.a_plane = static_cast<int>(R);
   p.b_plane = wgrad ? static_cast<int>(R) : E;
   const bool f32 = wgrad || PLANES == 3 || parts;
@@ -762,11 +774,12 @@ cudaError_t launch_grouped_join(int op, int dtype, const GroupedArgs& a, const G
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(blocks));
   const float* parts = static_cast<const float*>(x.parts);
+  const float scale = x.planes == 3 ? kSplitUnscale : 1.f;
   if (wgrad || dtype == kDtypeF32)
     return launch_dependent_kernel(join_kernel<float>, grid, dim3(256), 0, st, parts, static_cast<float*>(a.out), g, rows,
-                                   cols, pitch4(cols), x.splits, x.skip);
+                                   cols, pitch4(cols), x.splits, scale, x.skip, x.over);
   return launch_dependent_kernel(join_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, parts, static_cast<__nv_bfloat16*>(a.out),
-                                 g, rows, cols, pitch4(cols), x.splits, x.skip);
+                                 g, rows, cols, pitch4(cols), x.splits, scale, x.skip, x.over);
 }
 
 }  // namespace mm

@@ -489,7 +489,7 @@ struct GroupedArgs {
   int K, N;
 };
 // fp32 multiply-adds (grouped_simt.cu); only_if not null: nothing is done where
-// it holds 0.  Without it, a forward pass of up to f32_few_rows is made by warps
+// [0] and [1 + op] hold 0.  Without it, a forward pass of up to f32_few_rows is made by warps
 // instead of tiles.
 constexpr int f32_few_rows(int E) { return 16 + 4 * E; }
 cudaError_t launch_grouped_simt(int op, const GroupedArgs& p, const int* only_if, cudaStream_t st);
@@ -503,8 +503,8 @@ constexpr int pitch8(int n) { return (n + 7) / 8 * 8; }
 // groups without rows are left out (here, in SplitTensor and in Mx4Args); 0: rows.
 cudaError_t launch_repitch(const void* src, void* dst, int64_t rows, int cols, const GroupTables& g, int per_group,
                            cudaStream_t st);
-// fp32 tensors as planes, in one launch; sets *flag where a value cannot be
-// split; rows of the sorted tensors without an assignment become zeros.
+// fp32 tensors times 2^24 as planes, in one launch; sets *flag where a value cannot
+// be split; rows of the sorted tensors without an assignment become zeros.
 struct SplitTensor {
   const void* src;            // fp32 [rows, cols]
   void* dst;                  // bf16 [3, rows, pitch8(cols)]
@@ -521,6 +521,7 @@ struct GroupedTcExtras {
   int splits;                 // parts of the sums (grouped_splits), added by launch_grouped_join
   void* parts;                // grouped_parts_bytes(); null with one part
   const int* skip;            // device: nothing is done where it holds something; or null
+  int* over;                  // device, three planes: set where a result is not finite; or null
 };
 int grouped_splits(int op, const GroupTables& g, int K, int N, int planes);
 size_t grouped_parts_bytes(int op, const GroupTables& g, int K, int N, int splits);

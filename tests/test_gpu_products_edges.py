@@ -56,24 +56,59 @@ def test_fp32_sums_that_overflow(rows, K, N, top):
 
 @pytest.mark.parametrize("rows", [8, 300])
 def test_fp32_overflow_stays_in_its_results(rows):
-    """A result whose products overflow to both sides is not finite, and the others do not change by a bit."""
+    """A result whose products overflow to both sides is not finite, the others are as ever."""
     gen = torch.Generator().manual_seed(rows)
     K, N = 264, 72
     x, w = torch.randn(rows, K, generator=gen), torch.randn(N, K, generator=gen)
-    clean = mm.grouped_matmul(x.cuda(), w.cuda()).cpu()
     x[3] *= 2.0 ** 100
     w[7] *= 2.0 ** 80
     y = mm.grouped_matmul(x.cuda(), w.cuda()).cpu()
     # products of 2^180 of both signs: their sum, rounded once, is an infinity; added one by one in
-    # fp32 they are inf - inf, a NaN; the tensor cores add sixteen products wider than fp32 before
-    # they round, and keep the first infinity.  A finite number is none of these.
+    # fp32 they are inf - inf, a NaN.  A finite number is neither.
     assert not bool(y[3, 7].isfinite())
     keep = torch.ones(rows, N, dtype=torch.bool)
-    keep[3], keep[:, 7] = False, False
-    if rows > 40:                             # tiles: no result depends on its neighbours
-        assert torch.equal(y[keep], clean[keep])
+    keep[3, 7] = False
     want, terms = ref.matmul(x, w, None, torch.zeros(rows, N))
     ref.close_sum(torch.where(keep, y, 0.0), torch.where(keep, want, 0.0), torch.where(keep, terms, 0.0), K, F32, "ys")
+
+
+@pytest.mark.parametrize("rows,K,N", [(8, 96, 72), (300, 264, 72), (300, 515, 130), (300, 4096, 130)])
+def test_tiny_numbers_do_not_turn_a_call_over(rows, K, N):
+    """Tails of a softmax, down to fp32's smallest: the call stays where it is made, which the bits of the other results tell."""
+    gen = torch.Generator().manual_seed(rows + N)
+    x, w, dy = torch.randn(rows, K, generator=gen), torch.randn(N, K, generator=gen), torch.randn(rows, N, generator=gen)
+
+    def call(x, dy):
+        return [t.cpu() for t in (mm.grouped_matmul(x.cuda(), w.cuda()), *mm.grouped_matmul_backward(dy.cuda(), x.cuda(), w.cuda()))]
+
+    clean = call(x, dy)
+    small = torch.tensor([2.0 ** -149, -1.3e-33, 2.0 ** -126, 1e-38, -3e-42, 7e-31])
+    x[3, :6], dy[3, :6] = small, small
+    y, dx, dw = call(x, dy)
+    rest = torch.arange(rows) != 3
+    assert torch.equal(y[rest], clean[0][rest]) and torch.equal(dx[rest], clean[1][rest]) and torch.equal(dw[6:, 6:], clean[2][6:, 6:])
+    for got, (want, terms), n in ((y, ref.matmul(x, w, None, torch.zeros(rows, N)), K), *zip((dx, dw), ref.matmul_backward(dy, x, w, None, torch.zeros(rows, K)), (N, rows))):
+        ref.close_sum(got, want, terms, n, F32, "")
+
+
+@pytest.mark.parametrize("rows,K,N", [(20, 264, 72), (5, 97, 40), (300, 264, 200), (300, 65, 33), (300, 4096, 130)])
+@pytest.mark.parametrize("scale", [0, 30, -30])
+def test_fp32_products_of_numbers_of_every_size(rows, K, N, scale):
+    """24 bits at every exponent from fp32's smallest number to 2^79, times a
+    power of two in its place: one term a sum, rounded once where it is subnormal.
+
+    The tensor cores' sums are scaled by 2^48, in which the term is exact."""
+    gen = torch.Generator().manual_seed(rows + K + scale)
+    x = numbers((2 ** 23, 2 ** 24), gen, rows, K) * torch.exp2(torch.randint(-149, 56 - max(scale, 0), (rows, K), generator=gen).double()).float()
+    dy = numbers((2 ** 23, 2 ** 24), gen, rows, N) * torch.exp2(torch.randint(-149, 56 - max(scale, 0), (rows, N), generator=gen).double()).float()
+    one = lambda axis, *s: one_each(torch.full(s, 2.0 ** scale), axis, [(0, s[0])], gen)  # noqa: E731
+    w, v = one(1, N, K), one(0, N, K)
+    y = mm.grouped_matmul(x.cuda(), w.cuda()).cpu()
+    dx = mm.grouped_matmul_backward(dy.cuda(), None, v.cuda())[0].cpu()
+    assert torch.equal(y, (x.double() @ w.double().T).float()) and torch.equal(dx, (dy.double() @ v.double()).float())
+    u = one(0, rows, N)
+    dw = mm.grouped_matmul_backward(u.cuda(), x.cuda(), None)[1].cpu()
+    assert torch.equal(dw, (u.double().T @ x.double()).float())
 
 
 # ------------------------------------------------------------ a shared workspace
