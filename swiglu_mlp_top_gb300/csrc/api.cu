@@ -1175,19 +1175,18 @@ static WsHeader* status_header(void* status_ws, void* workspace, size_t workspac
 // rows 10 against 26.  With weights in 4 bits, which the tiles have to convert:
 // 128 rows 20 us against 23, 256 29 against 24; E = 64, 1024 rows 66 against 88,
 // 2048 104 against 88; one matrix, 64 rows 26 against 28, 128 50 against 28.
-// fp32, which the tiles first have to split: K = N = 2048, E = 8, 60 rows 63 us
-// against 131, 250 rows 117 against 133, 500 rows 177 against 133; E = 32, K = N
-// = 1024, 500 rows 66 against 135, 2000 rows 174 against 139; one matrix, 64
-// rows 26 against 35, 130 rows 57 against 36.
+// fp32, which the tiles first have to split: E = 8, K = 768, N = 4864, 72 rows 34
+// us against 116, 288 rows 80 against 117; E = 32, K = N = 1024, 528 rows 48
+// against 140, 1056 rows 80 against 140; one matrix of 2048 x 2048, 64 rows 19
+// against 37.
 // How many of the rows are one expert's only the device knows, and a matrix is
 // read again for every 32 rows of its expert.  The factors of E bound what a
 // routing costs that gives all rows to one expert: E = 64, K = 2048, N = 1024 at
 // the most rows that are streamed (evenly routed in brackets): bf16, 416 rows 19
 // us against 14 (45 against 53), 4 bits, 1088 rows 49 against 26 (53 against
-// 86), fp32, 1568 rows 229 against 104 (296 against 504); with 32 E
-// instead of 24, 2080 rows 299 against 101 (397 against 489).
+// 86), fp32, 2080 rows 214 against 105 (262 against 494).
 static bool grouped_streams(int64_t rows, int K, int E, int dtype, bool w_in_4_bits) {
-  return K % 8 == 0 && rows <= (w_in_4_bits ? 64 + 16 * E : dtype == kDtypeBF16 ? 32 + 6 * E : 40 + 24 * E);
+  return K % 8 == 0 && rows <= (w_in_4_bits ? 64 + 16 * E : dtype == kDtypeBF16 ? 32 + 6 * E : 32 + 32 * E);
 }
 // What a call of a product needs beside its tensors.
 struct GroupedPlan {

@@ -15,10 +15,10 @@ def lib():
 
 @pytest.mark.parametrize("E", [1, 8, 64])
 def test_few_fp32_rows_are_streamed(lib, E):
-    """Up to 24 rows an expert and 40 more: all of them on one expert take at
+    """Up to 32 rows an expert and 32 more: all of them on one expert take at
     most about twice the tiles' time."""
     need = lambda rows, K: lib.mm_grouped_matmul_workspace_bytes(rows, K, 1024, E, L.MM_DTYPE_F32)  # noqa: E731
-    assert need(40 + 24 * E, 2048) == 0 and need(40 + 24 * E + 1, 2048) > 0
+    assert need(32 + 32 * E, 2048) == 0 and need(32 + 32 * E + 1, 2048) > 0
     # rows that do not start on 16 bytes: multiply-adds up to 4 rows an expert and 16 more
     assert need(16 + 4 * E, 2049) == 0 and need(16 + 4 * E + 1, 2049) > 0
 
