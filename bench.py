@@ -912,6 +912,25 @@ BLOCK_OPS_MORE = [
 ]
 
 
+def _products_more():
+    """Forms of the products by expert that perf/more_operators.py does not list."""
+    f = lambda name, op, T, K, N, E, k, dtype="bf16": dict(  # noqa: E731
+        name=name, op=op, T=T, K=K, N=N, E=E, k=k, align=1, drop=0.0, dtype=dtype)
+    return [
+        f("gmm_t4000_e8k2_f32", "gmm", 4000, 768, 2432, 8, 2, "f32"),
+        f("gmm_t60_e8k1_f32", "gmm", 60, 2048, 2048, 8, 1, "f32"),
+        f("gmm_bwd_t1000_e4k1_f32", "gmm_bwd", 1000, 768, 2432, 4, 1, "f32"),
+        f("gmm_bwd_t1_e8k2", "gmm_bwd", 1, 768, 4864, 8, 2),
+        f("gmm_bwd_t1_e8k2_f32", "gmm_bwd", 1, 768, 4864, 8, 2, "f32"),
+        f("mx4w_t4096_e8k2_gateup", "mx4w", 4096, 768, 4864, 8, 2),
+        f("mx4w_t16_k4096", "mx4w", 16, 4096, 4096, 1, 1),
+        f("mx4_mm_t16_k4096", "mx4_mm", 16, 4096, 4096, 1, 1),
+        f("mx4_mm_t300_k8192_n768", "mx4_mm", 300, 8192, 768, 1, 1),
+        dict(name="mx4_pack_r32768_c2432_f32", op="mx4_pack", R=32768, C=2432, dtype="f32"),
+        dict(name="mx4_pack_r8000_c4100", op="mx4_pack", R=8000, C=4100, dtype="bf16"),
+    ]
+
+
 def run_block_ops(args):
     """The operators around the experts' products and the products by expert at
     the cases of perf/operators.py and perf/more_operators.py and a few more,
@@ -940,7 +959,7 @@ def run_block_ops(args):
         return statistics.median(times)
 
     for ops, case in ([(operators, c) for c in operators.listed() + BLOCK_OPS_MORE] +
-                      [(more_operators, c) for c in more_operators.listed()]):
+                      [(more_operators, c) for c in more_operators.listed() + _products_more()]):
         bare = case.get("bare", False)
         # without a checkpoint: g, u and h, 2 bytes each
         nbytes = case["R"] * case["I"] * 6 if bare else ops.work(case)["bytes"]
