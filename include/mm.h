@@ -568,7 +568,9 @@ int mm_mx4_dequantize(const void* codes, const uint8_t* exps, int64_t R, int64_t
 
 /* mm_grouped_matmul with w in 4 bits (codes [E * N, 16 G], exps), for xs in
  * 4 bits (x: codes, x_exps) or in bf16 (x_exps NULL); ys is bf16:
- *   ys[r, n] = sum_k v(xs[r, k]) v(w[e, n, k]),  v() the values stood for. */
+ *   ys[r, n] = sum_k v(xs[r, k]) v(w[e, n, k]),  v() the values stood for
+ * (with xs in bf16 those that mm_mx4_dequantize gives in bf16: a weight of 2^128
+ * is an infinity there). */
 size_t mm_mx4_matmul_workspace_bytes(int64_t rows, int K, int N, int E, int x_in_4_bits);
 
 int mm_mx4_matmul(const void* x, const uint8_t* x_exps, const void* w_codes, const uint8_t* w_exps,

@@ -1199,8 +1199,8 @@ struct GroupedPlan {
 };
 // fp32 that is not streamed: a forward pass of few rows, whose width keeps them
 // from starting on 16 bytes, goes to the CUDA cores (grouped_simt.cu), all else
-// to the tensor cores: T = 1000, E = 4, K = 768, N = 2432 148 -> 50 us, 8000
-// rows, E = 8 634 -> 163; 64 rows, E = 8 equal.
+// to the tensor cores: T = 1000, E = 4, K = 768, N = 2432 148 -> 51 us, 8000
+// rows, E = 8 634 -> 168; 64 rows, E = 8 equal.
 static bool f32_on_tensor_cores(int64_t rows, int E, bool backward) {
   return (backward || rows > f32_few_rows(E)) && rows <= int64_t{1} << 29;       // three planes of rows are counted in 32 bits
 }

@@ -286,8 +286,8 @@ inline int64_t row_tiles256(const GroupTables& g) {
 // most half the pairs of SMs (512 rows, K = 2048, N = 4096: 14.9 -> 13.1 us; 200
 // rows, E = 8, K = 768, N = 1024: 9.5 -> 8.6, with 4-bit weights 12.9 -> 9.5).
 // Up to all the pairs they mostly lose what they gain in a second round (N =
-// 8192: 16.6 -> 22.1; fp32, 1000 rows, N = 2432: 50.5 -> 53.6; 400 rows, E = 4,
-// N = 2432: 10.3 -> 9.0).
+// 8192: 16.6 -> 22.1; fp32, 1000 rows, N = 2432: 50.5 -> 53.6), so that 400 rows,
+// E = 4, N = 2432, which would gain (10.3 -> 9.0), stay with 256.
 inline int gm_columns(int64_t row_tiles, int cols) {
   return cols <= 128 || 2 * row_tiles * ((cols + 255) / 256) <= num_sms() / 2 ? 128 : 256;
 }

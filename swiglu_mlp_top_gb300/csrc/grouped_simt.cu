@@ -5,7 +5,7 @@
 // too large for that, told by flags on the device without which the tile kernel
 // returns.  The tiles are bound by the
 // multiply-adds (T = 1000, E = 4, K = 768, N = 2432: 148 us, of which 52 at 72
-// Tflop/s; the tensor cores take 50).
+// Tflop/s; the tensor cores take 51).
 //
 //   forward   ys[r, n]  = sum_k xs[r, k] w[e, n, k]       A = xs, B = w[e], both with k contiguous
 //   dgrad     dxs[r, k] = sum_n dys[r, n] w[e, n, k]      A = dys, B = w[e] with its output index contiguous
