@@ -258,3 +258,23 @@ def test_fp32_products_use_every_part(counts, K, N, kind):
         else:
             x = one_each(x, 0, rows, gen)
         same(mm.grouped_matmul_backward(dy.cuda(), x.cuda(), None, gplan)[1], ref.matmul_backward(dy, x, torch.zeros_like(v), plan, zeros(K))[1][0])
+
+
+def test_two_streams_at_once():
+    """Calls that run at the same time, each with a workspace of its own."""
+    gen = torch.Generator().manual_seed(33)
+    made = [calls_with_scratch(gen) for _ in range(2)]
+    want = [{name: [t.clone() for t in tensors(call())] for name, (call, _) in calls.items()} for calls in made]
+    spaces = [mm.new_workspace(max(need for _, need in calls.values())) for calls in made]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in made]
+    got = [{}, {}]
+    for _ in range(5):
+        for name in made[0]:
+            for i, (calls, ws, stream) in enumerate(zip(made, spaces, streams)):
+                got[i][name] = tensors(calls[name][0](workspace=ws, stream=stream))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert mm.check_status(spaces[i]) == 0
+        for name, outs in want[i].items():
+            assert all(torch.equal(a, b) for a, b in zip(got[i][name], outs)), name
