@@ -510,9 +510,10 @@ int mm_swiglu_act_backward(const void* codes, const uint8_t* exps, const void* d
  * fp32 operands are multiplied on the tensor cores as three bf16 parts each,
  * which hold all 24 bits of every number (six of the nine products; the others
  * are below 2^-25).  Where operands hold an infinity, a NaN or a magnitude of
- * 2^103 or more in a row that counts, or sums reach 2^80, the operation (of few
- * rows: the results that it touches) is made on the CUDA cores instead, with
- * the same accuracy, in four to nine times the time.
+ * 2^103 or more in a row that counts, the call is made on the CUDA cores
+ * instead, and so is each of its results ys, dxs or dw of which a sum reaches
+ * 2^80 (of few rows in either case: the results that are touched); with fp32's
+ * accuracy, in four to nine times the time.
  * Outputs overlap neither inputs nor each other.  A device wait that exceeded
  * its time limit is recorded in the header of `status_ws` (nullable; a zeroed
  * workspace of >= 256 bytes) or, without one, of `workspace`, for
